@@ -11,6 +11,11 @@
  *                               in the same launch;
  *   pkv_decode_plan_*           a decode call validated once and launched (or
  *                               run as a whole serving step) many times;
+ *   pkv_paged_attention_chunk   attention of any number of new tokens per
+ *                               sequence over the cache (prompts, chunks of
+ *                               prompts, drafted tokens, an encoder's states);
+ *   pkv_qk_norm_rope[_and_cache] the norm of each query and key head and the
+ *                               position rotation, with the slot-mapped write;
  *   pkv_reshape_and_cache       the slot-mapped write of new tokens' K/V;
  *   pkv_copy_blocks             the whole-block copy behind copy-on-write;
  *   pkv_swap_blocks             block copies between device and page-locked
@@ -404,6 +409,88 @@ int pkv_paged_attention_decode_noalloc(void *out, const void *query,
                                        int32_t *dev_status, pkv_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Chunk attention                                                           */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * pkv_paged_attention_chunk
+ *
+ * Attention of several new tokens per sequence over the paged cache: a whole
+ * prompt, a chunk of a long prompt, drafted tokens to verify, single tokens,
+ * or any mixture of them in one call.  The new tokens' keys and values must
+ * be in the cache already (pkv_reshape_and_cache or
+ * pkv_qk_norm_rope_and_cache with the slots of pkv_append_tokens).
+ *
+ * Sequence s owns the query rows query_starts[s] .. query_starts[s+1]-1; let
+ * n be their number and L = context_lens[s].  Row i of them is position
+ * p = L - n + i of its sequence.  For every query head h, with
+ * kvh = h / (num_heads / num_kv_heads) and K[t], V[t] found through the block
+ * table as in pkv_paged_attention_decode:
+ *
+ *     out[row][h] = sum_t softmax_t(scale * q[row][h] . K[t][kvh]) * V[t][kvh]
+ *
+ * over the visible t: with causal != 0, t <= p, and with window > 0 also
+ * t > p - window; with causal == 0 every t < L, whatever n is (the cache then
+ * holds another sequence's states, for instance an encoder's, and window must
+ * be 0).  A row that sees no position (L == 0, or p < 0 where n > L) gives
+ * zeros.  Scores, softmax statistics and the weighted sum are held in fp32;
+ * the softmax weights are rounded to fp16 for the second product, and the
+ * result is rounded to fp16, to nearest even.
+ *
+ * What no row of a sequence sees is not read for the result: table entries
+ * past ceil(L / block_size), or of blocks that lie wholly before every
+ * row's window, may hold -1, and cache positions outside may hold anything.
+ * A position that some rows see and others do not does not reach the others,
+ * also where its value is infinite or NaN.
+ *
+ * Arguments (device pointers unless noted):
+ *   out          fp16 [num_tokens][num_heads][head_dim]         (written; must
+ *                not overlap any input)
+ *   query        fp16 [num_tokens][num_heads][head_dim]
+ *   key_cache, value_cache, block_tables, max_blocks_per_seq, scale,
+ *   dev_status, stream: as for pkv_paged_attention_decode
+ *   context_lens int32 [num_seqs]
+ *   query_starts int32 [num_seqs + 1], not decreasing, from 0 up to at most
+ *                num_tokens.  Rows before the first sequence's and behind the
+ *                last one's are left as they were; a sequence may have no rows.
+ *   num_tokens   rows of query and out (host value)
+ *   causal, window  the mask (host values), above
+ *   num_ctas     persistent grid size; 0 = one CTA per SM.  Any value >= 1
+ *                gives the same result within rounding.
+ *   workspace    device scratch of at least pkv_chunk_workspace_size(...)
+ *                bytes for the same (num_tokens, num_heads, num_kv_heads,
+ *                head_dim, num_ctas); 256-byte aligned.  It carries nothing
+ *                from call to call and needs no clearing, but must not be
+ *                used by another call that runs at the same time (two
+ *                captured graphs that share one must not overlap).
+ *
+ * Results are deterministic for a fixed grid.  Supported: head_dim in
+ * {64, 128}; block_size in {8, 16, 32, 64, 128}; num_heads / num_kv_heads
+ * from 1 to 16; 1 <= num_seqs <= 4096; num_blocks * num_kv_heads * block_size
+ * < 2^31; max_blocks_per_seq * block_size <= 2^30; num_ctas <= 4096.
+ * num_tokens == 0 or num_seqs == 0 launches nothing.
+ * A context longer than its table (clamped to it) or negative (taken as 0), a
+ * table entry outside [0, num_blocks) among those read (block 0 is read), and
+ * query_starts that decrease or leave [0, num_tokens] (clamped to the rows
+ * there are) set PKV_ERR_OUT_OF_RANGE.
+ */
+int pkv_paged_attention_chunk(void *out, const void *query,
+                              const void *key_cache, const void *value_cache,
+                              const int32_t *block_tables, int max_blocks_per_seq,
+                              const int32_t *context_lens, const int32_t *query_starts,
+                              int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
+                              int head_dim, int block_size, int num_blocks,
+                              float scale, int causal, int window, int num_ctas,
+                              void *workspace, size_t workspace_bytes,
+                              int32_t *dev_status, pkv_stream_t stream);
+
+/* Bytes of workspace pkv_paged_attention_chunk needs (host call; queries the
+ * current device's SM count when num_ctas == 0).  Returns 0 for unsupported
+ * shapes. */
+size_t pkv_chunk_workspace_size(int num_tokens, int num_heads, int num_kv_heads,
+                                int head_dim, int num_ctas);
+
+/* ------------------------------------------------------------------------ */
 /* Cache writes                                                              */
 /* ------------------------------------------------------------------------ */
 
@@ -431,6 +518,72 @@ int pkv_reshape_and_cache(const void *key, const void *value,
                           int num_kv_heads, int head_dim, int block_size,
                           int num_blocks, int32_t *dev_status,
                           pkv_stream_t stream);
+
+/*
+ * pkv_qk_norm_rope, pkv_qk_norm_rope_and_cache
+ *
+ * The step between a model's projections and its attention: an RMS norm of
+ * every query and key head and the position rotation, in one pass over the
+ * data.  For each token t and each head x of its queries (and keys):
+ *
+ *     y = x * weight / sqrt(mean(x^2) + eps)     where the weight is not NULL
+ *     y = x                                      where it is NULL
+ *
+ * then the first rot_dim elements of y are rotated by the position's angles
+ * in pairs (a, b) -> (a cos - b sin, b cos + a sin): pair i is elements i and
+ * i + rot_dim/2 (interleaved == 0) or 2i and 2i + 1 (interleaved != 0); the
+ * other elements stay.  Computed in fp32, rounded once to fp16.
+ *
+ * pkv_qk_norm_rope writes the queries and keys to query_out and key_out (for
+ * pkv_paged_attention_decode_append, which writes the cache itself).
+ * pkv_qk_norm_rope_and_cache writes the queries to query_out, and the keys
+ * and the (unchanged) values to their cache slots, as pkv_reshape_and_cache
+ * does: for pkv_paged_attention_chunk or pkv_paged_attention_decode.
+ *
+ *   query        fp16 [num_tokens][num_heads][head_dim], a token's heads
+ *                contiguous, tokens query_stride elements apart; key, value:
+ *                the same with num_kv_heads.  The strides are multiples of 8
+ *                and at least one token's elements, so the three may be views
+ *                of one projection's output.
+ *   query_out, key_out  written, with strides of their own; each may be the
+ *                tensor it is made from (same pointer and stride), but must
+ *                not overlap an input in any other way
+ *   positions    int64 [num_tokens] (device): rows of cos_sin
+ *   cos_sin      fp32 [max_positions][rot_dim] (device): rot_dim/2 cosines,
+ *                then rot_dim/2 sines; 16-byte aligned
+ *   rot_dim      multiple of 16, 0 <= rot_dim <= head_dim; 0: no rotation
+ *                (positions and cos_sin may then be NULL)
+ *   query_weight, key_weight  fp16 [head_dim] (device, nullable)
+ *   eps          >= 0 (host value)
+ *   key_cache, value_cache, slot_mapping  as for pkv_reshape_and_cache: a
+ *                negative slot writes no key or value (the query is computed)
+ *   dev_status   a position outside [0, max_positions) sets
+ *                PKV_ERR_OUT_OF_RANGE and nothing of that token is written; a
+ *                slot >= num_blocks * block_size sets it and the token's key
+ *                and value are not written.
+ * head_dim is a multiple of 8 up to 256.  num_tokens == 0 launches nothing.
+ */
+int pkv_qk_norm_rope(void *query_out, int64_t query_out_stride,
+                     void *key_out, int64_t key_out_stride,
+                     const void *query, int64_t query_stride,
+                     const void *key, int64_t key_stride,
+                     const int64_t *positions, const float *cos_sin, int max_positions,
+                     int rot_dim, int interleaved,
+                     const void *query_weight, const void *key_weight, float eps,
+                     int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                     int32_t *dev_status, pkv_stream_t stream);
+int pkv_qk_norm_rope_and_cache(void *query_out, int64_t query_out_stride,
+                               const void *query, int64_t query_stride,
+                               const void *key, int64_t key_stride,
+                               const void *value, int64_t value_stride,
+                               void *key_cache, void *value_cache,
+                               const int64_t *slot_mapping,
+                               const int64_t *positions, const float *cos_sin, int max_positions,
+                               int rot_dim, int interleaved,
+                               const void *query_weight, const void *key_weight, float eps,
+                               int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                               int block_size, int num_blocks,
+                               int32_t *dev_status, pkv_stream_t stream);
 
 /*
  * pkv_copy_blocks

@@ -12,6 +12,12 @@ Names mirror the C ABI without its ``pkv_`` prefix:
 
 * paged_attention_decode(out, query, key_cache, value_cache, block_tables,
   context_lens, scale, ...)
+* paged_attention_chunk(out, query, key_cache, value_cache, block_tables,
+  context_lens, query_starts, scale, ...): any number of new tokens per
+  sequence
+* qk_norm_rope(query_out, key_out, query, key, positions, cos_sin, ...) and
+  qk_norm_rope_and_cache(query_out, query, key, value, key_cache, value_cache,
+  slot_mapping, positions, cos_sin, ...)
 * reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, ...)
 * copy_blocks(key_cache, value_cache, block_pairs, ...)
 * swap_blocks(src_key, src_value, dst_key, dst_value, block_pairs, ...)
@@ -43,6 +49,7 @@ PKV_ERR_SWAPPED = 8
 
 # Every symbol include/pkv.h declares, with (restype, argtypes).
 _c_int, _c_size, _vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+_c_i64 = ctypes.c_int64
 _i32p = ctypes.POINTER(ctypes.c_int32)
 _i64p = ctypes.POINTER(ctypes.c_int64)
 _intp = ctypes.POINTER(ctypes.c_int)
@@ -64,6 +71,15 @@ SIGNATURES = {
                                                     _c_int, _c_int, _c_int, _c_int, ctypes.c_float, _c_int,
                                                     _vp, _vp]),
     "pkv_decode_default_ctas": (_c_int, [_c_int, _c_int, _c_int, _c_int]),
+    "pkv_paged_attention_chunk": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int,
+                                           _c_int, _c_int, _c_int, _c_int, ctypes.c_float, _c_int, _c_int, _c_int,
+                                           _vp, _c_size, _vp, _vp]),
+    "pkv_chunk_workspace_size": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "pkv_qk_norm_rope": (_c_int, [_vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _vp, _c_int, _c_int,
+                                  _c_int, _vp, _vp, ctypes.c_float, _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
+    "pkv_qk_norm_rope_and_cache": (_c_int, [_vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _vp, _vp,
+                                            _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, ctypes.c_float, _c_int,
+                                            _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
     "pkv_reshape_and_cache": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
                                        _vp, _vp]),
     "pkv_copy_blocks": (_c_int, [_vp, _vp, _vp, _c_int, _c_size, _c_int, _vp, _vp]),
@@ -394,6 +410,55 @@ def paged_attention_decode_shared(out, query, key_cache, value_cache, block_tabl
     return out
 
 
+def chunk_workspace_size(num_tokens, num_heads, num_kv_heads, head_dim, num_ctas=0):
+    return int(load().pkv_chunk_workspace_size(num_tokens, num_heads, num_kv_heads, head_dim, num_ctas))
+
+
+def new_chunk_workspace(num_tokens, num_heads, num_kv_heads, head_dim, num_ctas=0, device="cuda"):
+    """A device workspace of the size pkv_chunk_workspace_size asks for."""
+    import torch
+    n = chunk_workspace_size(num_tokens, num_heads, num_kv_heads, head_dim, num_ctas)
+    if n == 0:
+        raise PkvError(PKV_ERR_UNSUPPORTED, "chunk_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+@_traced
+def paged_attention_chunk(out, query, key_cache, value_cache, block_tables, context_lens, query_starts, scale,
+                          causal=True, window=0, num_ctas=0, workspace=None, status=None, stream=None):
+    """pkv_paged_attention_chunk on torch tensors (see include/pkv.h): the
+    rows query_starts[s] .. query_starts[s+1]-1 of query are the last tokens
+    of sequence s (with causal false, tokens that see its whole context).
+
+    out, query: fp16 [T][H][D]; key_cache, value_cache: fp16 [NB][Hkv][bs][D];
+    block_tables: int32 [N][MB]; context_lens: int32 [N]; query_starts: int32
+    [N + 1]; window: 0, or how many positions back a row sees (itself
+    included).  A workspace (new_chunk_workspace) is allocated when None.
+    """
+    import torch
+    _need_all((query, torch.float16, "query", 3), (out, torch.float16, "out", 3),
+              (key_cache, torch.float16, "key_cache", 4), (value_cache, torch.float16, "value_cache", 4),
+              (block_tables, torch.int32, "block_tables", 2), (context_lens, torch.int32, "context_lens", 1),
+              (query_starts, torch.int32, "query_starts", 1))
+    t, h, d = query.shape
+    nb, hkv, bs, d2 = key_cache.shape
+    n, mb = block_tables.shape
+    if out.shape != query.shape or d2 != d or value_cache.shape != key_cache.shape \
+            or context_lens.shape[0] != n or query_starts.shape[0] != n + 1:
+        raise ValueError("inconsistent shapes")
+    with _one_device((out, query, key_cache, value_cache, block_tables, context_lens, query_starts, workspace,
+                      status), stream):
+        if workspace is None and t and n:
+            workspace = new_chunk_workspace(t, h, hkv, d, num_ctas, query.device)
+        ws, ws_bytes = _workspace(workspace) if workspace is not None else (None, 0)
+        rc = load().pkv_paged_attention_chunk(
+            _ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables), mb, _ptr(context_lens),
+            _ptr(query_starts), t, n, h, hkv, d, bs, nb, float(scale), int(bool(causal)), int(window), int(num_ctas),
+            ws, ws_bytes, _status_ptr(status), _stream(stream))
+    _check(rc, "pkv_paged_attention_chunk")
+    return out
+
+
 class DecodePlan:
     """pkv_decode_plan_*: a decode call validated once and launched many
     times with the same tensors (their contents may change between launches).
@@ -559,6 +624,104 @@ def reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, status=N
                                           _ptr(slot_mapping), t, hkv, d, bs, nb, _status_ptr(status),
                                           _stream(stream))
     _check(rc, "pkv_reshape_and_cache")
+
+
+def _rows(t, name):
+    """The token stride of fp16 [T][heads][D]: each token's heads contiguous,
+    tokens any multiple of 8 elements apart (a view of a projection's output)."""
+    import torch
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name}: expected {torch.float16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected 3 dims, got {tuple(t.shape)}")
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    stride = t.stride(0) if n > 1 else h * d
+    if stride < h * d or stride % 8:
+        raise ValueError(f"{name}: tokens must be a multiple of 8 elements apart and must not overlap")
+    return stride
+
+
+def _on_gpu(*specs):
+    for t, name in specs:
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _rope_args(query, key, positions, cos_sin, query_weight, key_weight):
+    """The checks that both qk_norm_rope calls share; -> rot_dim."""
+    import torch
+    t, _, d = query.shape
+    rot = 0
+    if (positions is None) != (cos_sin is None):
+        raise ValueError("positions and cos_sin go together")
+    if positions is not None:
+        _need_all((positions, torch.int64, "positions", 1), (cos_sin, torch.float32, "cos_sin", 2))
+        rot = cos_sin.shape[1]
+        if positions.shape[0] != t:
+            raise ValueError("inconsistent shapes")
+    for w, name in ((query_weight, "query_weight"), (key_weight, "key_weight")):
+        if w is not None:
+            _need_all((w, torch.float16, name, 1))
+            if w.shape[0] != d:
+                raise ValueError("inconsistent shapes")
+    if key.shape[0] != t or key.shape[2] != d:
+        raise ValueError("inconsistent shapes")
+    return rot
+
+
+@_traced
+def qk_norm_rope(query_out, key_out, query, key, positions=None, cos_sin=None, query_weight=None, key_weight=None,
+                 eps=1e-6, interleaved=False, status=None, stream=None):
+    """pkv_qk_norm_rope (see include/pkv.h): RMS norm of each head of query
+    (fp16 [T][H][D]) and key (fp16 [T][Hkv][D]) where a weight (fp16 [D]) is
+    given, and the rotation by row positions[t] (int64 [T]) of cos_sin (fp32
+    [P][rot_dim]: the cosines, then the sines).  The four tensors may be
+    views whose tokens are strided; query_out may be query, key_out key."""
+    sq, sk, sqo, sko = _rows(query, "query"), _rows(key, "key"), _rows(query_out, "query_out"), \
+        _rows(key_out, "key_out")
+    _on_gpu((query, "query"), (key, "key"), (query_out, "query_out"), (key_out, "key_out"))
+    rot = _rope_args(query, key, positions, cos_sin, query_weight, key_weight)
+    t, h, d = query.shape
+    if query_out.shape != query.shape or key_out.shape != key.shape:
+        raise ValueError("inconsistent shapes")
+    with _one_device((query_out, key_out, query, key, positions, cos_sin, query_weight, key_weight, status), stream):
+        rc = load().pkv_qk_norm_rope(
+            _ptr(query_out), sqo, _ptr(key_out), sko, _ptr(query), sq, _ptr(key), sk, _ptr(positions), _ptr(cos_sin),
+            cos_sin.shape[0] if rot else 0, rot, int(bool(interleaved)), _ptr(query_weight), _ptr(key_weight),
+            float(eps), t, h, key.shape[1], d, _status_ptr(status), _stream(stream))
+    _check(rc, "pkv_qk_norm_rope")
+    return query_out, key_out
+
+
+@_traced
+def qk_norm_rope_and_cache(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions=None,
+                           cos_sin=None, query_weight=None, key_weight=None, eps=1e-6, interleaved=False,
+                           status=None, stream=None):
+    """pkv_qk_norm_rope_and_cache (see include/pkv.h): qk_norm_rope with the
+    keys and the values (unchanged) written to the slots slot_mapping (int64
+    [T]) of key_cache / value_cache (fp16 [NB][Hkv][bs][D])."""
+    import torch
+    sq, sk, sv, sqo = _rows(query, "query"), _rows(key, "key"), _rows(value, "value"), _rows(query_out, "query_out")
+    _on_gpu((query, "query"), (key, "key"), (value, "value"), (query_out, "query_out"))
+    rot = _rope_args(query, key, positions, cos_sin, query_weight, key_weight)
+    _need_all((key_cache, torch.float16, "key_cache", 4), (value_cache, torch.float16, "value_cache", 4),
+              (slot_mapping, torch.int64, "slot_mapping", 1))
+    t, h, d = query.shape
+    nb, hkv, bs, d2 = key_cache.shape
+    if query_out.shape != query.shape or value.shape != key.shape or key.shape[1] != hkv or d2 != d \
+            or value_cache.shape != key_cache.shape or slot_mapping.shape[0] != t:
+        raise ValueError("inconsistent shapes")
+    with _one_device((query_out, query, key, value, key_cache, value_cache, slot_mapping, positions, cos_sin,
+                      query_weight, key_weight, status), stream):
+        rc = load().pkv_qk_norm_rope_and_cache(
+            _ptr(query_out), sqo, _ptr(query), sq, _ptr(key), sk, _ptr(value), sv, _ptr(key_cache),
+            _ptr(value_cache), _ptr(slot_mapping), _ptr(positions), _ptr(cos_sin), cos_sin.shape[0] if rot else 0,
+            rot, int(bool(interleaved)), _ptr(query_weight), _ptr(key_weight), float(eps), t, h, hkv, d, bs, nb,
+            _status_ptr(status), _stream(stream))
+    _check(rc, "pkv_qk_norm_rope_and_cache")
+    return query_out
 
 
 @_traced
