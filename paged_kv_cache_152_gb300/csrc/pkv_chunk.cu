@@ -1,5 +1,5 @@
-// pkv_chunk.cu -- attention of each sequence's newest tokens over its paged
-// cache: host entry points and kernel.
+// pkv_chunk.cu -- host entry points of the chunk attention (the kernels are in
+// pkv_chunk_impl.cuh): argument checks, grid, workspace and tensor maps.
 #include <cuda_runtime.h>
 
 #include <math.h>
@@ -7,7 +7,7 @@
 #include <algorithm>
 
 #include "../../include/pkv.h"
-#include "pkv_device.cuh"
+#include "pkv_chunk_impl.cuh"
 #include "pkv_host.h"
 #include "pkv_launch.h"
 
@@ -18,99 +18,67 @@ constexpr int kMaxSeqs = 4096;
 constexpr int kMaxCtas = 4096;
 constexpr int kMaxGroup = 16;
 
-struct ChunkParams {
-    __half *out;
-    const __half *query;
-    const __half *key_cache;
-    const __half *value_cache;
-    const int32_t *block_tables;
-    const int32_t *context_lens;
-    const int32_t *query_starts;
-    int32_t *status;
-    int num_tokens;
-    int num_seqs;
-    int num_heads;
-    int num_kv_heads;
-    int max_blocks_per_seq;
-    int num_blocks;
-    int block_size;
-    int causal;
-    int window;
-    float scale_log2;
-};
-
-// One warp per (row, head): the softmax's running maximum and sum over the
-// visible positions, one key at a time.
-template <int D>
-__global__ void __launch_bounds__(128) chunk_rows_kernel(const __grid_constant__ ChunkParams p) {
-    grid_dependency_wait();
-    launch_dependents();
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x % 32;
-    const int64_t total = (int64_t)p.num_tokens * p.num_heads;
-    for (int64_t w = (int64_t)blockIdx.x * 4 + threadIdx.x / 32; w < total; w += (int64_t)gridDim.x * 4) {
-        const int row = (int)(w / p.num_heads), head = (int)(w - (int64_t)row * p.num_heads);
-        const int kvh = head / (p.num_heads / p.num_kv_heads);
-        int seq = -1, lo = 0, hi = 0;
-        for (int s = 0; s < p.num_seqs; ++s) {
-            int a = p.query_starts[s], b = p.query_starts[s + 1];
-            if (a < 0 || b < a || b > p.num_tokens) {
-                if (w == 0 && lane == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
-                a = min(max(a, 0), p.num_tokens);
-                b = min(max(b, a), p.num_tokens);
-            }
-            if (row >= a && row < b) {
-                seq = s;
-                lo = a;
-                hi = b;
-            }
-        }
-        if (seq < 0) continue;
-        int len = p.context_lens[seq];
-        if (len < 0 || len > p.max_blocks_per_seq * p.block_size) {
-            if (lane == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
-            len = min(max(len, 0), p.max_blocks_per_seq * p.block_size);
-        }
-        int t0 = 0, t1 = len;
-        if (p.causal) {
-            const int pos = len - (hi - lo) + (row - lo);
-            t1 = max(pos + 1, 0);
-            if (p.window) t0 = max(0, pos - p.window + 1);
-        }
-        float q[E], acc[E] = {};
-        const int64_t at = ((int64_t)row * p.num_heads + head) * D + lane * E;
-#pragma unroll
-        for (int k = 0; k < E; ++k) q[k] = __half2float(p.query[at + k]) * p.scale_log2;
-        float top = -INFINITY, sum = 0.f;
-        for (int t = t0; t < t1; ++t) {
-            int blk = p.block_tables[(int64_t)seq * p.max_blocks_per_seq + t / p.block_size];
-            if (blk < 0 || blk >= p.num_blocks) {
-                if (lane == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
-                blk = 0;
-            }
-            const int64_t kv = (((int64_t)blk * p.num_kv_heads + kvh) * p.block_size + t % p.block_size) * D + lane * E;
-            float dot = 0.f;
-#pragma unroll
-            for (int k = 0; k < E; ++k) dot = fmaf(q[k], __half2float(p.key_cache[kv + k]), dot);
-#pragma unroll
-            for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(kFullMask, dot, d);
-            const float next = fmaxf(top, dot);
-            const float base = next == -INFINITY ? 0.f : next;  // nothing but -inf (or NaN) yet
-            const float fade = exp2f(top - base);
-            const float weight = exp2f(dot - base);
-            sum = sum * fade + weight;
-#pragma unroll
-            for (int k = 0; k < E; ++k) acc[k] = acc[k] * fade + weight * __half2float(p.value_cache[kv + k]);
-            top = next;
-        }
-#pragma unroll
-        for (int k = 0; k < E; ++k) p.out[at + k] = __float2half_rn(t1 > t0 ? acc[k] / sum : 0.f);
-    }
-}
-
 bool shape_ok(int num_heads, int num_kv_heads, int head_dim) {
     return num_heads > 0 && num_kv_heads > 0 && num_heads % num_kv_heads == 0 &&
            num_heads / num_kv_heads <= kMaxGroup && (head_dim == 64 || head_dim == 128);
+}
+
+// Units of an item besides its positions: what a piece costs before its first
+// step (queries in, output out), in positions.
+constexpr int kOverhead = 256;
+// Items are cut at multiples of this many steps.
+constexpr int kQuantum = 2;
+
+// The workspace: parts' descriptions, their (maximum, sum), their outputs.
+struct ChunkWorkspace {
+    size_t ml, o, total;
+    int part_rows;
+    static ChunkWorkspace plan(int num_tokens, int group, int head_dim, int ctas) {
+        auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+        ChunkWorkspace w;
+        const int tile_tokens = kChunkRows / group;
+        w.part_rows = (int)std::min<int64_t>(2 * tile_tokens, num_tokens) * group;
+        w.ml = up(sizeof(ChunkPart) * 2 * (size_t)ctas);
+        w.o = w.ml + up(sizeof(float2) * 2 * (size_t)ctas * w.part_rows);
+        w.total = w.o + up(sizeof(float) * 2 * (size_t)ctas * w.part_rows * head_dim);
+        return w;
+    }
+};
+
+int default_ctas(int *ctas) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(ctas, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_CUDA;
+    }
+    return PKV_OK;
+}
+
+// The queries as a 3-D tensor [T][H][D], in boxes of 64 dims of one KV head's
+// query heads of one tile's tokens.
+int encode_query_map(CUtensorMap *map, const void *query, int num_tokens, int num_heads, int head_dim, int group) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return PKV_ERR_CUDA;
+    const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)num_heads, (cuuint64_t)num_tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)num_heads * head_dim * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(kChunkRows / group)};
+    const cuuint32_t elem_strides[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(query), dims, strides, box,
+                              elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
+}
+
+// The kernel hands registers from its four helper warps to its softmax warps;
+// that must add up to what it is launched with, or it would wait for good.
+bool registers_add_up(const void *fn) {
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, fn) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return a.numRegs == kChunkLaunchRegs;
 }
 
 }  // namespace
@@ -122,7 +90,8 @@ extern "C" size_t pkv_chunk_workspace_size(int num_tokens, int num_heads, int nu
                                            int num_ctas) {
     if (num_tokens < 0 || num_ctas < 0 || num_ctas > kMaxCtas || !shape_ok(num_heads, num_kv_heads, head_dim))
         return 0;
-    return 256;
+    if (num_ctas == 0 && default_ctas(&num_ctas) != PKV_OK) return 0;
+    return ChunkWorkspace::plan(num_tokens, num_heads / num_kv_heads, head_dim, num_ctas).total;
 }
 
 extern "C" int pkv_paged_attention_chunk(void *out, const void *query, const void *key_cache,
@@ -149,34 +118,66 @@ extern "C" int pkv_paged_attention_chunk(void *out, const void *query, const voi
     if (!shape_ok(num_heads, num_kv_heads, head_dim)) return PKV_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128)
         return PKV_ERR_UNSUPPORTED;
-    const size_t need = pkv_chunk_workspace_size(num_tokens, num_heads, num_kv_heads, head_dim, num_ctas);
-    if (need == 0) return PKV_ERR_CUDA;
-    if (workspace_bytes < need) return PKV_ERR_INVALID_ARG;
+    if (num_ctas == 0 && default_ctas(&num_ctas) != PKV_OK) return PKV_ERR_CUDA;
+    const int group = num_heads / num_kv_heads;
+    const ChunkWorkspace ws = ChunkWorkspace::plan(num_tokens, group, head_dim, num_ctas);
+    if (workspace_bytes < ws.total) return PKV_ERR_INVALID_ARG;
 
     ChunkParams p = {};
+    int rc = encode_query_map(&p.tmap_q, query, num_tokens, num_heads, head_dim, group);
+    if (rc == PKV_OK)
+        rc = encode_cache_map(&p.tmap_k, key_cache, num_blocks, num_kv_heads, block_size, head_dim, block_size, 1);
+    if (rc == PKV_OK)
+        rc = encode_cache_map(&p.tmap_v, value_cache, num_blocks, num_kv_heads, block_size, head_dim, block_size, 1);
+    if (rc != PKV_OK) return rc;
+    unsigned char *wsb = static_cast<unsigned char *>(workspace);
     p.out = static_cast<__half *>(out);
-    p.query = static_cast<const __half *>(query);
-    p.key_cache = static_cast<const __half *>(key_cache);
     p.value_cache = static_cast<const __half *>(value_cache);
     p.block_tables = block_tables;
     p.context_lens = context_lens;
     p.query_starts = query_starts;
+    p.parts = reinterpret_cast<ChunkPart *>(wsb);
+    p.part_ml = reinterpret_cast<float2 *>(wsb + ws.ml);
+    p.part_o = reinterpret_cast<float *>(wsb + ws.o);
     p.status = dev_status;
+    p.shape.tile_tokens = kChunkRows / group;
+    p.shape.num_kv_heads = num_kv_heads;
+    p.shape.causal = causal != 0;
+    p.shape.window = window;
+    p.shape.overhead = kOverhead;
+    p.shape.quantum = kQuantum;
     p.num_tokens = num_tokens;
     p.num_seqs = num_seqs;
     p.num_heads = num_heads;
-    p.num_kv_heads = num_kv_heads;
+    p.group = group;
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.num_blocks = num_blocks;
-    p.block_size = block_size;
-    p.causal = causal;
-    p.window = window;
+    p.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : 7;
+    p.part_rows = ws.part_rows;
     p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
+    p.wait_limit_ns = kWaitLimitNs;
+
+    const bool d64 = head_dim == 64;
+    const void *fn = d64 ? reinterpret_cast<const void *>(&chunk_kernel<64>)
+                         : reinterpret_cast<const void *>(&chunk_kernel<128>);
+    const size_t smem = d64 ? ChunkConfig<64>::kSmem : ChunkConfig<128>::kSmem;
+    static const bool good_regs = registers_add_up(reinterpret_cast<const void *>(&chunk_kernel<64>)) &&
+                                  registers_add_up(reinterpret_cast<const void *>(&chunk_kernel<128>));
+    if (!good_regs) return PKV_ERR_CUDA;
+    rc = ensure_smem_attr(fn, smem);
+    if (rc != PKV_OK) return rc;
     void *args[] = {&p};
-    const void *fn = head_dim == 64 ? reinterpret_cast<const void *>(&chunk_rows_kernel<64>)
-                                    : reinterpret_cast<const void *>(&chunk_rows_kernel<128>);
-    const int64_t blocks = std::min<int64_t>(((int64_t)num_tokens * num_heads + 3) / 4, 65536);
-    if (launch_pdl(fn, dim3((unsigned)blocks), dim3(128), 0, stream, args) != cudaSuccess) {
+    if (launch_pdl(fn, dim3((unsigned)num_ctas), dim3(kChunkThreads), smem, stream, args) != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_CUDA;
+    }
+    // No table is long enough for an item to be cut: nothing to join.
+    if ((int64_t)max_blocks_per_seq * block_size <= (int64_t)kQuantum * kChunkTile || num_ctas == 1) return PKV_OK;
+    fn = d64 ? reinterpret_cast<const void *>(&chunk_join_kernel<64>)
+             : reinterpret_cast<const void *>(&chunk_join_kernel<128>);
+    void *join_args[] = {&p, &num_ctas};
+    if (launch_pdl(fn, dim3(2u * (unsigned)num_ctas, (unsigned)(ws.part_rows + 15) / 16), dim3(128),
+                   sizeof(int) * (size_t)num_ctas, stream, join_args) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
     }

@@ -1,0 +1,1049 @@
+// pkv_chunk_impl.cuh -- the chunk attention kernel: attention of each
+// sequence's newest tokens over its paged cache, on the tensor cores.
+//
+// Mathematics.  Row by row, over steps of 128 cache positions: scores
+// S = Q K^T, a running maximum m and sum l, weights P = 2^(c (S - m)) with
+// c = scale * log2(e), O = O * 2^(c (m_old - m)) + P V, and out = O / l.  The
+// group of query heads that share a KV head are rows of one tile, so each step
+// of K and V serves all of them.
+//
+// One CTA per SM, 12 warps, walking its share of the work (pkv_chunk_schedule.h)
+// piece by piece:
+//   warps 0-3, 4-7  one softmax warpgroup per slot, a row per thread
+//   warp 8          issues the products (one thread)
+//   warp 9          walks the schedule and the block tables, issues the copies
+//   warps 10, 11    guard V where a step is not seen by every row (below)
+// A slot is a tile of 128 query rows with its own S and O in tensor memory
+// (P overlays S: all 512 columns are used at head_dim 128).  The two slots of a
+// piece are either two query tiles that share every step of K and V, or, where
+// the item has one tile, the same tile with alternate steps, joined at the end.
+// While one slot's softmax runs, the other's products do.
+//
+// What bounds it: with 256 rows a step is 4 * 256 * 128 * D operations for
+// 512 * D bytes, so long prompts are bound by the products and the exponentials
+// (a warpgroup's softmax of a step has to fit in the other slot's products);
+// with one token per sequence the tile is nearly empty, and a step's copy from
+// HBM takes longer than its products, so padding costs no time.
+//
+// V is read as an operand for every row of a tile, and 0 * NaN is NaN.  So in
+// steps that some row does not see whole, the guard warps clear the rows of V
+// that no row of the item sees (table ends, what precedes a window) and clear
+// single elements that are not finite; the epilogue adds the latter to the
+// rows that do see them (they decide those elements: finite + inf = inf).
+#ifndef PKV_CHUNK_IMPL_CUH
+#define PKV_CHUNK_IMPL_CUH
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pkv_chunk_schedule.h"
+#include "pkv_device.cuh"
+#include "pkv_tcgen05.cuh"
+
+namespace pkv {
+
+constexpr int kChunkThreads = 384;
+constexpr int kChunkRows = 128;   // rows of a query tile
+constexpr int kChunkPieces = 4;   // piece descriptors in flight
+// Registers per thread: 384 at launch x 168 = 64512 = 256 x 208 + 128 x 88.
+constexpr int kChunkLaunchRegs = 168;
+
+// One of at most two partial pieces a CTA writes, for the joining kernel.
+struct ChunkPart {
+    long long item;  // the item's first unit on the line: the same for all its pieces
+    int row0;        // first query row
+    int tokens;
+    int kv_head;
+    int flags;       // 1: valid, 2: the item's first steps, 4: its last steps
+};
+
+struct ChunkParams {
+    CUtensorMap tmap_q;  // [T][H][D] in boxes {64, group, tile_tokens}
+    CUtensorMap tmap_k;  // the caches in boxes of {64, block rows, 1}
+    CUtensorMap tmap_v;
+    __half *out;
+    const __half *value_cache;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    const int32_t *query_starts;
+    ChunkPart *parts;    // [2 * CTAs]
+    float2 *part_ml;     // [2 * CTAs][part_rows] (c * m, l)
+    float *part_o;       // [2 * CTAs][part_rows][D], not normalised
+    int32_t *status;
+    ChunkShape shape;
+    int num_tokens;
+    int num_seqs;
+    int num_heads;
+    int group;
+    int max_blocks_per_seq;
+    int num_blocks;
+    int block_shift;     // log2(block_size)
+    int part_rows;
+    float scale_log2;
+    uint64_t wait_limit_ns;
+};
+
+struct ChunkPiece {
+    int row0;            // first query row of the item
+    int tokens;          // its tokens
+    int kv_head;
+    int seq;
+    int pos0;            // position of its first token (negative: sees nothing)
+    int len;
+    int lo, hi;          // positions that some row sees
+    int all_lo, all_hi;  // positions that every row sees
+    int t0, t1;          // steps of this piece
+    int partial;         // the part it writes, or -1
+    int single;          // one query tile: the slots take alternate steps
+    int last;            // no piece: the end
+    int odd;             // a guard cleared an element that was not finite
+};
+
+template <int D>
+struct ChunkConfig {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kHalfBytes = kChunkTile * 128;
+    static constexpr int kTileBytes = kHalves * kHalfBytes;
+    static constexpr int kStages = D == 128 ? 5 : 10;  // 160 KB of K and V in flight
+    struct Control {
+        uint64_t full[kStages], empty[kStages], edge[kStages], guard[kStages];
+        uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], o_cross[2];
+        uint64_t x_full, x_empty, drain;
+        uint64_t piece_full[kChunkPieces], piece_empty[kChunkPieces];
+        ChunkPiece piece[kChunkPieces];
+        float2 ml[2][kChunkRows];
+        uint32_t tmem;
+        int abort;
+    };
+    static constexpr size_t kSmem = (size_t)(2 + kStages) * kTileBytes + sizeof(Control);
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+template <int R>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// A bounded wait of one thread: false once it has run out of time, or once
+// any thread of the CTA has (the abort flag); every role then leaves its loop.
+__device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, int *abort, int32_t *status,
+                                           uint64_t limit_ns) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+#pragma unroll 1
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*(volatile int *)abort) return false;
+        if (global_ns() - t0 > limit_ns) {
+            *(volatile int *)abort = 1;
+            report(status, PKV_ERR_DEVICE_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// The same for a whole warp, which leaves together.
+__device__ __forceinline__ bool chunk_wait_warp(uint32_t bar, uint32_t parity, int *abort, int32_t *status,
+                                                uint64_t limit_ns) {
+    return __all_sync(kFullMask, chunk_wait(bar, parity, abort, status, limit_ns));
+}
+
+__device__ __forceinline__ int chunk_clamp(int64_t x, int hi) { return (int)chunk_min64(chunk_max64(x, 0), hi); }
+
+// A sequence's rows and length, clamped to what there is.
+__device__ __forceinline__ ChunkSeq chunk_load_seq(const ChunkParams &p, int s, bool tell) {
+    ChunkSeq q;
+    const int a = __ldg(p.query_starts + s), b = __ldg(p.query_starts + s + 1), len = __ldg(p.context_lens + s);
+    const int most = p.max_blocks_per_seq << p.block_shift;
+    q.row0 = chunk_clamp(a, p.num_tokens);
+    q.n = chunk_clamp(b, p.num_tokens) - q.row0;
+    if (q.n < 0) q.n = 0;
+    q.len = chunk_clamp(len, most);
+    if (tell && (a != q.row0 || b != q.row0 + q.n || len != q.len)) report(p.status, PKV_ERR_OUT_OF_RANGE);
+    return q;
+}
+
+// The steps of a piece that a slot takes: first, first + stride, ... < end.
+__device__ __forceinline__ void chunk_slot_steps(const ChunkParams &p, const ChunkPiece &pc, int slot, int *first,
+                                                 int *end, int *stride) {
+    if (pc.single) {
+        *first = pc.t0 + slot;
+        *end = pc.t1;
+        *stride = 2;
+        if (*first > *end) *first = *end;
+        return;
+    }
+    *stride = 1;
+    const int a = slot * p.shape.tile_tokens, b = min(a + p.shape.tile_tokens, pc.tokens);
+    int lo = 0, hi = pc.len;
+    if (p.shape.causal) {
+        hi = chunk_clamp((int64_t)pc.pos0 + b, pc.len);
+        if (p.shape.window) lo = chunk_clamp((int64_t)pc.pos0 + a - p.shape.window + 1, hi);
+    }
+    *first = max(lo / kChunkTile, pc.t0);
+    *end = min((hi + kChunkTile - 1) / kChunkTile, pc.t1);
+    if (hi <= lo || *end < *first) *end = *first;
+}
+
+// Whether some row of the item does not see all of step t.
+__device__ __forceinline__ bool chunk_edge(const ChunkPiece &pc, int t) {
+    return t * kChunkTile < pc.all_lo || (t + 1) * kChunkTile > pc.all_hi;
+}
+
+// Whether a position of step t is seen by some rows of the item and not by others.
+__device__ __forceinline__ bool chunk_mixed(const ChunkPiece &pc, int t) {
+    return max(t * kChunkTile, pc.lo) < pc.all_lo || min((t + 1) * kChunkTile, pc.hi) > pc.all_hi;
+}
+
+// Ring positions of a piece's copies relative to its first: K0 K1 V0 K2 V1 ...
+__device__ __forceinline__ uint32_t chunk_k_at(int k) { return k == 0 ? 0u : 2u * k - 1u; }
+__device__ __forceinline__ uint32_t chunk_v_at(int k, int n) { return k < n - 1 ? 2u * k + 2u : 2u * n - 1u; }
+
+__device__ __forceinline__ int chunk_block(const ChunkParams &p, int seq, int logical) {
+    int blk = __ldg(p.block_tables + (int64_t)seq * p.max_blocks_per_seq + logical);
+    if (blk < 0 || blk >= p.num_blocks) {
+        report(p.status, PKV_ERR_OUT_OF_RANGE);
+        blk = 0;
+    }
+    return blk;
+}
+
+__device__ __forceinline__ bool odd_halves(uint32_t w) { return (((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u) != 0; }
+
+// Adds the elements of V that are not finite to the columns [c0, c0 + cols) of
+// a row already written: those of the mixed steps of the piece that the row
+// sees.  Rare, so plain loops.
+template <int D, typename T>
+__device__ __noinline__ void chunk_add_odd(const ChunkParams &p, const ChunkPiece &pc, int row_lo, int row_hi, T *row,
+                                           int c0, int cols) {
+    for (int t = pc.t0; t < pc.t1; ++t) {
+        if (!chunk_mixed(pc, t)) continue;
+        const int a = max(t * kChunkTile, row_lo), b = min((t + 1) * kChunkTile, row_hi);
+        for (int pos = a; pos < b; ++pos) {
+            const int64_t blk = chunk_block(p, pc.seq, pos >> p.block_shift);
+            const __half *v = p.value_cache + (((blk * p.shape.num_kv_heads + pc.kv_head) << p.block_shift) +
+                                               (pos & ((1 << p.block_shift) - 1))) * D;
+            for (int c = c0; c < c0 + cols; ++c) {
+                const __half h = v[c];
+                if ((__half_as_ushort(h) & 0x7c00) == 0x7c00) row[c] = (T)((float)row[c] + __half2float(h));
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// warp 9: the schedule and the copies
+
+template <int D>
+struct ChunkLoader {
+    using Cfg = ChunkConfig<D>;
+    const ChunkParams &p;
+    typename Cfg::Control &ctl;
+    uint32_t q_smem, ring_smem;
+    int lane;
+    uint32_t ring = 0;          // ring position of the next copy
+    uint32_t pieces = 0;
+    uint32_t q_uses[2] = {0, 0};
+    uint32_t edge_phase = 0, edge_used = 0;  // bit per stage
+    int parts = 0;
+
+    __device__ bool wait(uint64_t &bar, uint32_t parity) {
+        return chunk_wait_warp(smem_addr(&bar), parity, &ctl.abort, p.status, p.wait_limit_ns);
+    }
+
+    // This lane's block of step t (-1: none of its positions is seen).
+    __device__ int lookup(const ChunkPiece &pc, int t) {
+        const int b = (t * kChunkTile >> p.block_shift) + lane;
+        const bool mine = lane < (kChunkTile >> p.block_shift) && ((int64_t)b << p.block_shift) < pc.hi &&
+                          ((int64_t)(b + 1) << p.block_shift) > pc.lo;
+        return mine ? chunk_block(p, pc.seq, b) : -1;
+    }
+
+    // One tile into the next stage.  A tile that the guards go over first
+    // (edge) lands on a barrier of their own, and the products wait for them.
+    __device__ bool copy(const CUtensorMap *map, int blk, int kv_head, bool edge) {
+        const uint32_t st = ring % Cfg::kStages;
+        if (!wait(ctl.empty[st], (ring / Cfg::kStages & 1) ^ 1)) return false;
+        ++ring;
+        const uint32_t bar = smem_addr(edge ? &ctl.edge[st] : &ctl.full[st]);
+        const unsigned live = __ballot_sync(kFullMask, blk >= 0);
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar, __popc(live) * ((uint32_t)D * 2 << p.block_shift));
+            if (edge) mbar_arrive(smem_addr(&ctl.full[st]));
+        }
+        if (edge) {
+            edge_phase ^= 1u << st;
+            edge_used |= 1u << st;
+        }
+        __syncwarp();
+        if (blk >= 0) {
+            const uint32_t dst = ring_smem + st * Cfg::kTileBytes + ((uint32_t)lane << p.block_shift) * 128;
+            const int row = (int)(((int64_t)blk * p.shape.num_kv_heads + kv_head) << p.block_shift);
+#pragma unroll
+            for (int h = 0; h < Cfg::kHalves; ++h) tma_load_3d(dst + h * Cfg::kHalfBytes, map, 0, row, h, bar);
+        }
+        return true;
+    }
+
+    __device__ bool emit(const ChunkPiece &pc) {
+        const uint32_t slot = pieces % kChunkPieces;
+        if (!wait(ctl.piece_empty[slot], (pieces / kChunkPieces & 1) ^ 1)) return false;
+        ++pieces;
+        if (lane == 0) {
+            ctl.piece[slot] = pc;
+            mbar_arrive(smem_addr(&ctl.piece_full[slot]));
+        }
+        __syncwarp();
+        return true;
+    }
+
+    __device__ bool load(const ChunkPiece &pc) {
+        const int n = pc.t1 - pc.t0;
+        if (n == 0) return true;
+        for (int b = 0; b < (pc.single ? 1 : 2); ++b) {
+            if (!wait(ctl.q_empty[b], (q_uses[b] & 1) ^ 1)) return false;
+            ++q_uses[b];
+            if (lane == 0) {
+                const uint32_t bar = smem_addr(&ctl.q_full[b]);
+                mbar_arrive_expect_tx(bar, (uint32_t)p.shape.tile_tokens * p.group * D * 2);
+#pragma unroll
+                for (int h = 0; h < Cfg::kHalves; ++h)
+                    tma_load_3d(q_smem + b * Cfg::kTileBytes + h * Cfg::kHalfBytes, &p.tmap_q, h * 64,
+                                pc.kv_head * p.group, pc.row0 + b * p.shape.tile_tokens, bar);
+            }
+            __syncwarp();
+        }
+        int blk = lookup(pc, pc.t0);
+        if (!copy(&p.tmap_k, blk, pc.kv_head, false)) return false;
+        for (int t = pc.t0; t < pc.t1; ++t) {
+            const int next = t + 1 < pc.t1 ? lookup(pc, t + 1) : -1;
+            if (t + 1 < pc.t1 && !copy(&p.tmap_k, next, pc.kv_head, false)) return false;
+            if (!copy(&p.tmap_v, blk, pc.kv_head, chunk_edge(pc, t))) return false;
+            blk = next;
+        }
+        return true;
+    }
+
+    // The next sequence at or after s that has rows; num_seqs if none.
+    __device__ int next_seq(int s) {
+        while (s < p.num_seqs) {
+            const bool has = s + lane < p.num_seqs && chunk_load_seq(p, s + lane, false).n > 0;
+            const unsigned m = __ballot_sync(kFullMask, has);
+            if (m) return s + __ffs(m) - 1;
+            s += 32;
+        }
+        return p.num_seqs;
+    }
+
+    // The share [u, end) of the line; cum = units before sequence s.
+    __device__ bool walk(int s, int64_t cum, int64_t u, int64_t end) {
+        if (u >= end) return true;
+        const ChunkShape &c = p.shape;
+        ChunkSeq q = chunk_load_seq(p, s, false);
+        int head, item, items = chunk_items(c, q);
+        int64_t off;
+        chunk_find(c, q, u - cum, &head, &item, &off);
+        while (true) {
+            ChunkPiece pc;
+            const int w = 2 * c.tile_tokens;
+            int lo, hi;
+            chunk_item_range(c, q, item, &lo, &hi);
+            const int64_t cost = (int64_t)(hi - lo) + c.overhead;
+            const int64_t stop = chunk_min64(cost, off + (end - u));
+            const int steps = chunk_steps(lo, hi), first = lo / kChunkTile;
+            const int a = chunk_step_at(c, lo, hi, off), b = chunk_step_at(c, lo, hi, stop);
+            if (b > a || (steps == 0 && off == 0)) {
+                pc.row0 = q.row0 + item * w;
+                pc.tokens = min(w, q.n - item * w);
+                pc.kv_head = head;
+                pc.seq = s;
+                pc.pos0 = q.len - q.n + item * w;
+                pc.len = q.len;
+                pc.lo = lo;
+                pc.hi = hi;
+                pc.all_lo = 0;
+                pc.all_hi = q.len;
+                if (c.causal) {
+                    pc.all_hi = chunk_clamp((int64_t)pc.pos0 + 1, q.len);
+                    if (c.window) pc.all_lo = chunk_clamp((int64_t)pc.pos0 + pc.tokens - c.window, q.len);
+                }
+                pc.t0 = first + a;
+                pc.t1 = first + b;
+                pc.partial = -1;
+                pc.single = pc.tokens <= c.tile_tokens;
+                pc.last = 0;
+                pc.odd = 0;
+                if (b - a < steps) {
+                    pc.partial = parts;
+                    if (lane == 0) {
+                        ChunkPart part;
+                        part.item = u - off;
+                        part.row0 = pc.row0;
+                        part.tokens = pc.tokens;
+                        part.kv_head = head;
+                        part.flags = 1 | (a == 0 ? 2 : 0) | (b == steps ? 4 : 0);
+                        p.parts[2 * blockIdx.x + parts] = part;
+                    }
+                    ++parts;
+                }
+                if (!emit(pc) || !load(pc)) return false;
+            }
+            u += stop - off;
+            if (u >= end) return true;
+            off = 0;
+            if (++item == items) {
+                item = 0;
+                if (++head == c.num_kv_heads) {
+                    head = 0;
+                    s = next_seq(s + 1);
+                    if (s >= p.num_seqs) return true;
+                    q = chunk_load_seq(p, s, false);
+                    items = chunk_items(c, q);
+                }
+            }
+        }
+    }
+
+    __device__ void run(int s, int64_t cum, int64_t u, int64_t end) {
+        bool ok = walk(s, cum, u, end);
+        if (lane == 0)
+            for (int k = parts; k < 2; ++k) p.parts[2 * blockIdx.x + k].flags = 0;
+        if (ok) {
+            ChunkPiece pc = {};
+            pc.last = 1;
+            ok = emit(pc);
+        }
+        // every copy has landed and every product that reads it is complete
+        for (int i = 0; ok && i < Cfg::kStages; ++i, ++ring)
+            ok = wait(ctl.empty[ring % Cfg::kStages], (ring / Cfg::kStages & 1) ^ 1);
+        for (int b = 0; ok && b < 2; ++b) ok = wait(ctl.q_empty[b], (q_uses[b] & 1) ^ 1);
+        if (!ok) {  // gave up: only the copies in flight matter now
+            for (uint32_t i = 1; i <= (uint32_t)Cfg::kStages && i <= ring; ++i)
+                mbar_wait_bounded(smem_addr(&ctl.full[(ring - i) % Cfg::kStages]),
+                                  (ring - i) / Cfg::kStages & 1, p.wait_limit_ns / 8);
+            for (int st = 0; st < Cfg::kStages; ++st)
+                if (edge_used >> st & 1)
+                    mbar_wait_bounded(smem_addr(&ctl.edge[st]), (edge_phase >> st & 1) ^ 1, p.wait_limit_ns / 8);
+            for (int b = 0; b < 2; ++b)
+                if (q_uses[b])
+                    mbar_wait_bounded(smem_addr(&ctl.q_full[b]), (q_uses[b] - 1) & 1, p.wait_limit_ns / 8);
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
+// warp 8: the products (one thread)
+
+template <int D>
+struct ChunkProducts {
+    using Cfg = ChunkConfig<D>;
+    const ChunkParams &p;
+    typename Cfg::Control &ctl;
+    uint32_t q_smem, ring_smem, tmem;
+    uint32_t ring = 0;
+    uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0}, o_uses[2] = {0, 0}, merges = 0;
+    uint32_t guard_phase = 0;  // bit per stage
+
+    __device__ bool wait(uint64_t &bar, uint32_t parity) {
+        return chunk_wait(smem_addr(&bar), parity, &ctl.abort, p.status, p.wait_limit_ns);
+    }
+    __device__ uint32_t s_at(int slot) { return tmem + slot * kChunkTile; }
+    __device__ uint32_t o_at(int slot) { return tmem + 2 * kChunkTile + slot * D; }
+
+    __device__ bool scores(const ChunkPiece &pc, int slot, int t, bool release) {
+        const uint32_t at = ring + chunk_k_at(t - pc.t0), st = at % Cfg::kStages;
+        if (!wait(ctl.full[st], at / Cfg::kStages & 1)) return false;
+        tc_fence_after();
+        const uint64_t a = umma_desc(q_smem + (pc.single ? 0 : slot) * Cfg::kTileBytes, 16, 1024);
+        const uint64_t b = umma_desc(ring_smem + st * Cfg::kTileBytes, 16, 1024);
+        constexpr uint32_t idesc = umma_idesc_f16(128, kChunkTile, false);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            const uint32_t step = ((k / 4) * Cfg::kHalfBytes + (k % 4) * 32) >> 4;
+            umma_ss(s_at(slot), a + step, b + step, idesc, k > 0);
+        }
+        umma_commit(smem_addr(&ctl.s_full[slot]));
+        if (release) umma_commit(smem_addr(&ctl.empty[st]));
+        return true;
+    }
+
+    __device__ bool weighted(const ChunkPiece &pc, int slot, int t, bool first, bool last, bool check_guard,
+                             bool release) {
+        if (!wait(ctl.p_full[slot], p_uses[slot] & 1)) return false;
+        ++p_uses[slot];
+        const uint32_t at = ring + chunk_v_at(t - pc.t0, pc.t1 - pc.t0), st = at % Cfg::kStages;
+        if (!wait(ctl.full[st], at / Cfg::kStages & 1)) return false;
+        if (check_guard) {  // the first slot that takes an edge step waits for its guards
+            if (!wait(ctl.guard[st], guard_phase >> st & 1)) return false;
+            guard_phase ^= 1u << st;
+        }
+        if (first) {  // the previous piece's output has been read
+            if (!wait(ctl.o_free[slot], (o_uses[slot] & 1) ^ 1)) return false;
+            if (!wait(ctl.o_cross[slot], (merges & 1) ^ 1)) return false;
+            ++o_uses[slot];
+        }
+        tc_fence_after();
+        const uint64_t b = umma_desc(ring_smem + st * Cfg::kTileBytes, Cfg::kHalfBytes, 1024);
+        constexpr uint32_t idesc = umma_idesc_f16(128, D, true);
+#pragma unroll
+        for (int k = 0; k < kChunkTile / 16; ++k)
+            umma_ts(o_at(slot), s_at(slot) + k * 8, b + (k * 2048 >> 4), idesc, !(first && k == 0));
+        if (release) umma_commit(smem_addr(&ctl.empty[st]));
+        if (last) umma_commit(smem_addr(&ctl.o_full[slot]));
+        return true;
+    }
+
+    __device__ bool piece(const ChunkPiece &pc) {
+        const int n = pc.t1 - pc.t0;
+        if (n == 0) return true;
+        const int buffers = pc.single ? 1 : 2;
+        for (int b = 0; b < buffers; ++b) {
+            if (!wait(ctl.q_full[b], q_uses[b] & 1)) return false;
+            ++q_uses[b];
+        }
+        int first[2], end[2], stride[2];
+        for (int s = 0; s < 2; ++s) chunk_slot_steps(p, pc, s, &first[s], &end[s], &stride[s]);
+        auto takes = [&](int s, int t) {
+            return t >= first[s] && t < end[s] && (!pc.single || (t - pc.t0) % 2 == s);
+        };
+        int left = (end[0] - first[0] + stride[0] - 1) / stride[0] + (end[1] - first[1] + stride[1] - 1) / stride[1];
+        auto do_scores = [&](int s, int t) {
+            // the last slot that takes a step frees its K
+            if (!scores(pc, s, t, s == 1 || !takes(1, t))) return false;
+            if (--left == 0)
+                for (int b = 0; b < buffers; ++b) umma_commit(smem_addr(&ctl.q_empty[b]));
+            return true;
+        };
+        // Slot 0 always meets a step that both take before slot 1 (its window
+        // begins and ends no later), also where slot 1 starts a step later.
+        for (int s = 0; s < 2; ++s)
+            if (first[s] < end[s] && (pc.single || first[s] == pc.t0) && !do_scores(s, first[s])) return false;
+        for (int t = pc.t0; t < pc.t1; ++t) {
+            bool guard = chunk_edge(pc, t);
+            for (int s = 0; s < 2; ++s) {
+                if (!takes(s, t)) {
+                    if (!pc.single && first[s] < end[s] && t + 1 == first[s] && !do_scores(s, t + 1)) return false;
+                    continue;
+                }
+                const int next = t + stride[s];
+                if (!weighted(pc, s, t, t == first[s], next >= end[s], guard, s == 1 || !takes(1, t))) return false;
+                guard = false;
+                if (next < end[s] && !do_scores(s, next)) return false;
+            }
+        }
+        if (pc.single && n > 1) ++merges;
+        ring += 2 * n;
+        return true;
+    }
+
+    __device__ void run() {
+        for (uint32_t k = 0;; ++k) {
+            const uint32_t slot = k % kChunkPieces;
+            if (!wait(ctl.piece_full[slot], k / kChunkPieces & 1)) break;
+            const ChunkPiece &pc = ctl.piece[slot];
+            if (pc.last) break;
+            if (!piece(pc)) break;
+            mbar_arrive(smem_addr(&ctl.piece_empty[slot]));
+        }
+        umma_commit(smem_addr(&ctl.drain));
+        mbar_wait_bounded(smem_addr(&ctl.drain), 0, p.wait_limit_ns);
+    }
+};
+
+// ---------------------------------------------------------------------------
+// warps 10, 11: V in steps that not every row sees whole
+
+template <int D>
+__device__ void chunk_guard(const ChunkParams &p, typename ChunkConfig<D>::Control &ctl, uint32_t ring_smem, int half,
+                            int lane) {
+    using Cfg = ChunkConfig<D>;
+    uint32_t ring = 0, phase = 0;
+    for (uint32_t k = 0;; ++k) {
+        const uint32_t slot = k % kChunkPieces;
+        if (!chunk_wait_warp(smem_addr(&ctl.piece_full[slot]), k / kChunkPieces & 1, &ctl.abort, p.status,
+                             p.wait_limit_ns))
+            return;
+        ChunkPiece &pc = ctl.piece[slot];
+        if (pc.last) return;
+        const int n = pc.t1 - pc.t0;
+        for (int t = pc.t0; t < pc.t1; ++t) {
+            if (!chunk_edge(pc, t)) continue;
+            const uint32_t at = ring + chunk_v_at(t - pc.t0, n), st = at % Cfg::kStages;
+            if (!chunk_wait_warp(smem_addr(&ctl.edge[st]), phase >> st & 1, &ctl.abort, p.status, p.wait_limit_ns))
+                return;
+            phase ^= 1u << st;
+            const bool mixed = chunk_mixed(pc, t);
+            const int keep_lo = pc.lo - t * kChunkTile, keep_hi = pc.hi - t * kChunkTile;
+            bool odd = false;
+            // this warp's 64 rows, 4 rows of 128 bytes at a time
+            const uint32_t base = ring_smem + st * Cfg::kTileBytes + half * 64 * 128 + lane * 16;
+#pragma unroll
+            for (int h = 0; h < Cfg::kHalves; ++h) {
+#pragma unroll 4
+                for (int i = 0; i < 16; ++i) {
+                    const int row = half * 64 + i * 4 + lane / 8;
+                    const uint32_t a = base + h * Cfg::kHalfBytes + i * 512;
+                    if (row < keep_lo || row >= keep_hi) {
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+                    } else if (mixed) {
+                        uint32_t w[4];
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                     : "r"(a)
+                                     : "memory");
+                        if (odd_halves(w[0]) || odd_halves(w[1]) || odd_halves(w[2]) || odd_halves(w[3])) {
+                            odd = true;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                if ((w[j] & 0x7c00u) == 0x7c00u) w[j] &= 0xffff0000u;
+                                if ((w[j] & 0x7c000000u) == 0x7c000000u) w[j] &= 0x0000ffffu;
+                            }
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]),
+                                         "r"(w[2]), "r"(w[3])
+                                         : "memory");
+                        }
+                    }
+                }
+            }
+            if (odd) *(volatile int *)&pc.odd = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&ctl.guard[st]));
+        }
+        ring += 2 * n;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&ctl.piece_empty[slot]));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// warps 0-7: softmax and output
+
+template <int D>
+struct ChunkSoftmax {
+    using Cfg = ChunkConfig<D>;
+    const ChunkParams &p;
+    typename Cfg::Control &ctl;
+    uint32_t tmem;  // with this warp's lanes
+    int slot, row, lane;
+    uint32_t s_uses = 0, o_uses = 0, merges = 0;
+    float m, l;     // running maximum (of unscaled scores) and sum
+
+    __device__ bool wait(uint64_t &bar, uint32_t parity) {
+        return chunk_wait_warp(smem_addr(&bar), parity, &ctl.abort, p.status, p.wait_limit_ns);
+    }
+    __device__ void arrive(uint64_t &bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&bar));
+    }
+    __device__ uint32_t s_at() { return tmem + slot * kChunkTile; }
+    __device__ uint32_t o_at(int s) { return tmem + 2 * kChunkTile + s * D; }
+
+    // One step: scores -> weights, in place in tensor memory.
+    __device__ bool step(int col0, int row_lo, int row_hi, bool first) {
+        if (!wait(ctl.s_full[slot], s_uses & 1)) return false;
+        ++s_uses;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_at() + c * 32, s[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_pin32(s[c]);
+        const bool whole = row_lo <= col0 && col0 + kChunkTile <= row_hi;
+        if (!__all_sync(kFullMask, whole)) {
+            const int a = row_lo - col0;
+            const unsigned n = (unsigned)max(row_hi - max(row_lo, 0), 0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if ((unsigned)(c * 32 + i - a) >= n) s[c][i] = 0xff800000u;  // -inf
+        }
+        float top[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            top[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+            for (int i = 1; i < 32; ++i) top[c] = fmaxf(top[c], __uint_as_float(s[c][i]));
+        }
+        const float next = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m);
+        // The maximum moves only when it rises by more than a factor 2^8 of the
+        // weights (fp16 carries weights up to 2^15), so O is seldom rescaled.
+        const bool move = first ? true : (next - m) * p.scale_log2 > 8.f;
+        if (!first && __any_sync(kFullMask, move)) {
+            const float fade = move ? ex2((m - next) * p.scale_log2) : 1.f;
+            l *= fade;
+            const uint64_t fade2 = pack2(fade, fade);
+            // the scores' arrival means every earlier product is complete, O's last one among them
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(o_at(slot) + c * 32, o);
+                tmem_wait_ld();
+                tmem_pin32(o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float x, y;
+                    unpack2(mul2(pack2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), fade2), x, y);
+                    o[2 * i] = __float_as_uint(x);
+                    o[2 * i + 1] = __float_as_uint(y);
+                }
+                tmem_st32(o_at(slot) + c * 32, o);
+            }
+        }
+        if (move) m = next;
+        const float base = m == -INFINITY ? 0.f : -m * p.scale_log2;
+        const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), base2 = pack2(base, base);
+        uint64_t sum2 = pack2(0.f, 0.f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const uint32_t *x = &s[2 * h + i / 16][2 * (i % 16)];
+                float a, b;
+                unpack2(fma2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, base2), a, b);
+                a = ex2(a);
+                b = ex2(b);
+                sum2 = add2(sum2, pack2(a, b));
+                w[i] = pack_half2(a, b);  // the second product's operand type; l sums the unrounded weights
+            }
+            tmem_st32(s_at() + h * 32, w);
+        }
+        float x, y;
+        unpack2(sum2, x, y);
+        l += x + y;
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(ctl.p_full[slot]);
+        return true;
+    }
+
+    __device__ void store_out(__half *dst, const uint32_t (&o)[32], float inv) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(o[8 * i + j]) * inv;
+            reinterpret_cast<uint4 *>(dst)[i] = pack8(f);
+        }
+    }
+    __device__ void store_part(float *dst, const uint32_t (&o)[32]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    }
+
+    __device__ bool piece(const ChunkPiece &pc) {
+        int first, end, stride;
+        chunk_slot_steps(p, pc, slot, &first, &end, &stride);
+        const bool merge = pc.single && pc.t1 - pc.t0 > 1;
+        // this thread's row: a token of the item and a query head
+        const int token = row / p.group + (pc.single ? 0 : slot * p.shape.tile_tokens);
+        const int head = pc.kv_head * p.group + row % p.group;
+        const bool live = row < p.shape.tile_tokens * p.group && token < pc.tokens &&
+                          (slot == 0 || !pc.single || merge);
+        int row_lo = 0, row_hi = 0;
+        if (live) {
+            row_hi = pc.len;
+            if (p.shape.causal) {
+                const int64_t pos = (int64_t)pc.pos0 + token;
+                row_hi = chunk_clamp(pos + 1, pc.len);
+                if (p.shape.window) row_lo = chunk_clamp(pos - p.shape.window + 1, row_hi);
+            }
+        }
+        m = -INFINITY;
+        l = 0.f;
+        for (int t = first; t < end; t += stride)
+            if (!step(t * kChunkTile, row_lo, row_hi, t == first)) return false;
+
+        __half *out = p.out + ((int64_t)(pc.row0 + token) * p.num_heads + head) * D;
+        const int64_t part_row = (int64_t)(2 * blockIdx.x + pc.partial) * p.part_rows + token * p.group + row % p.group;
+        float *part = p.part_o + part_row * D;
+        const bool mine = first < end;
+        if (mine) {
+            if (!wait(ctl.o_full[slot], o_uses & 1)) return false;
+            ++o_uses;
+            tc_fence_after();
+        }
+        if (!merge) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            if (mine) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(o_at(slot) + c * 32, o);
+                    tmem_wait_ld();
+                    tmem_pin32(o);
+                    if (live) {
+                        if (pc.partial < 0)
+                            store_out(out + c * 32, o, inv);
+                        else
+                            store_part(part + c * 32, o);
+                    }
+                }
+                tc_fence_before();
+                arrive(ctl.o_free[slot]);
+            } else if (live && pc.partial < 0) {  // no step of the item is seen by this tile
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
+            }
+            if (live) {
+                if (pc.partial >= 0) p.part_ml[part_row] = make_float2(m * p.scale_log2, l);
+                if (pc.odd && mine) {
+                    if (pc.partial < 0)
+                        chunk_add_odd<D>(p, pc, row_lo, row_hi, out, 0, D);
+                    else
+                        chunk_add_odd<D>(p, pc, row_lo, row_hi, part, 0, D);
+                }
+            }
+            return true;
+        }
+        // One tile, alternate steps: join the slots.  Both warpgroups hold the
+        // same rows, and a warp reads the other slot's O in its own lanes; each
+        // writes half of the columns.
+        if (!wait(ctl.x_empty, (merges & 1) ^ 1)) return false;
+        ctl.ml[slot][row] = make_float2(m * p.scale_log2, l);
+        tc_fence_before();
+        arrive(ctl.x_full);  // this slot's O is complete, too
+        if (!wait(ctl.x_full, merges & 1)) return false;
+        tc_fence_after();
+        ++merges;
+        const float2 a = ctl.ml[0][row], b = ctl.ml[1][row];
+        arrive(ctl.x_empty);
+        const float top = fmaxf(a.x, b.x), base = top == -INFINITY ? 0.f : top;
+        const float fa = ex2(a.x - base), fb = ex2(b.x - base);
+        const float sum = fa * a.y + fb * b.y;
+        const float inv = pc.partial >= 0 ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+        const uint64_t fa2 = pack2(fa, fa), fb2 = pack2(fb, fb);
+        const int c0 = slot * (D / 2);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            uint32_t oa[32], ob[32];
+            tmem_ld32(o_at(0) + c0 + c * 32, oa);
+            tmem_ld32(o_at(1) + c0 + c * 32, ob);
+            tmem_wait_ld();
+            tmem_pin32(oa);
+            tmem_pin32(ob);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float x, y;
+                unpack2(fma2(pack2(__uint_as_float(oa[2 * i]), __uint_as_float(oa[2 * i + 1])), fa2,
+                             mul2(pack2(__uint_as_float(ob[2 * i]), __uint_as_float(ob[2 * i + 1])), fb2)), x, y);
+                oa[2 * i] = __float_as_uint(x);
+                oa[2 * i + 1] = __float_as_uint(y);
+            }
+            if (live) {
+                if (pc.partial < 0)
+                    store_out(out + c0 + c * 32, oa, inv);
+                else
+                    store_part(part + c0 + c * 32, oa);
+            }
+        }
+        tc_fence_before();
+        arrive(ctl.o_free[slot]);
+        arrive(ctl.o_cross[1 - slot]);
+        if (live) {
+            if (pc.partial >= 0 && slot == 0) p.part_ml[part_row] = make_float2(top, sum);
+            if (pc.odd) {
+                if (pc.partial < 0)
+                    chunk_add_odd<D>(p, pc, row_lo, row_hi, out, c0, D / 2);
+                else
+                    chunk_add_odd<D>(p, pc, row_lo, row_hi, part, c0, D / 2);
+            }
+        }
+        return true;
+    }
+
+    __device__ void run() {
+        for (uint32_t k = 0;; ++k) {
+            const uint32_t at = k % kChunkPieces;
+            if (!wait(ctl.piece_full[at], k / kChunkPieces & 1)) return;
+            const ChunkPiece &pc = ctl.piece[at];
+            if (pc.last || !piece(pc)) return;
+            arrive(ctl.piece_empty[at]);
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
+
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
+    using Cfg = ChunkConfig<D>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char *ring = smem + 2 * Cfg::kTileBytes;
+    typename Cfg::Control &ctl = *reinterpret_cast<typename Cfg::Control *>(ring + Cfg::kStages * Cfg::kTileBytes);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Cfg::kStages; ++i) {
+            mbar_init(smem_addr(&ctl.full[i]), 1);
+            mbar_init(smem_addr(&ctl.empty[i]), 1);
+            mbar_init(smem_addr(&ctl.edge[i]), 1);
+            mbar_init(smem_addr(&ctl.guard[i]), 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&ctl.q_full[i]), 1);
+            mbar_init(smem_addr(&ctl.q_empty[i]), 1);
+            mbar_init(smem_addr(&ctl.s_full[i]), 1);
+            mbar_init(smem_addr(&ctl.p_full[i]), 4);
+            mbar_init(smem_addr(&ctl.o_full[i]), 1);
+            mbar_init(smem_addr(&ctl.o_free[i]), 4);
+            mbar_init(smem_addr(&ctl.o_cross[i]), 4);
+        }
+        mbar_init(smem_addr(&ctl.x_full), 8);
+        mbar_init(smem_addr(&ctl.x_empty), 8);
+        mbar_init(smem_addr(&ctl.drain), 1);
+        for (int i = 0; i < kChunkPieces; ++i) {
+            mbar_init(smem_addr(&ctl.piece_full[i]), 1);
+            mbar_init(smem_addr(&ctl.piece_empty[i]), 11);  // 8 softmax warps, the products, 2 guards
+        }
+        ctl.abort = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&p.tmap_q);
+        prefetch_tensormap(&p.tmap_k);
+        prefetch_tensormap(&p.tmap_v);
+    }
+    if (warp == 8) tmem_alloc(smem_addr(&ctl.tmem), 512);
+    grid_dependency_wait();
+    launch_dependents();
+
+    // Where this CTA's share starts: the units of each thread's run of
+    // sequences, their running sum, and the run that holds the share's first
+    // unit (the ring's memory is free until the first copy).
+    int64_t *run_units = reinterpret_cast<int64_t *>(ring);
+    const int per = (p.num_seqs + kChunkThreads - 1) / kChunkThreads;
+    int64_t units = 0;
+    for (int s = threadIdx.x * per; s < min((int)(threadIdx.x + 1) * per, p.num_seqs); ++s)
+        units += chunk_seq_units(p.shape, chunk_load_seq(p, s, blockIdx.x == 0));
+    run_units[threadIdx.x] = units;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    if (warp >= 8) {
+        regs_down<88>();
+        if (warp == 9) {
+            // 12 runs per lane
+            int64_t mine = 0;
+            for (int i = 0; i < 12; ++i) mine += run_units[lane * 12 + i];
+            int64_t upto = mine;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t x = __shfl_up_sync(kFullMask, upto, d);
+                if (lane >= d) upto += x;
+            }
+            const int64_t total = __shfl_sync(kFullMask, upto, 31);
+            const int64_t u = chunk_share(total, gridDim.x, blockIdx.x);
+            const int64_t end = chunk_share(total, gridDim.x, blockIdx.x + 1);
+            int s = 0;
+            int64_t cum = 0;
+            if (u < end) {
+                const int who = __ffs(__ballot_sync(kFullMask, upto > u)) - 1;
+                cum = __shfl_sync(kFullMask, upto - mine, who);
+                int run = who * 12;
+                while (cum + run_units[run] <= u) cum += run_units[run++];
+                s = run * per;
+                while (true) {
+                    const int64_t x = chunk_seq_units(p.shape, chunk_load_seq(p, s, false));
+                    if (cum + x > u) break;
+                    cum += x;
+                    ++s;
+                }
+            }
+            __syncwarp();
+            fence_proxy_async_smem();  // the ring's memory was read and written by ordinary accesses
+            ChunkLoader<D> loader{p, ctl, smem_addr(smem), smem_addr(ring), lane};
+            loader.run(s, cum, u, end);
+        } else if (warp == 8) {
+            if (lane == 0) {
+                ChunkProducts<D> products{p, ctl, smem_addr(smem), smem_addr(ring), ctl.tmem};
+                products.run();
+            }
+            __syncwarp();
+        } else {
+            chunk_guard<D>(p, ctl, smem_addr(ring), warp - 10, lane);
+        }
+    } else {
+        regs_up<208>();
+        ChunkSoftmax<D> softmax{p, ctl, ctl.tmem + ((uint32_t)(warp % 4) << 21), warp / 4,
+                                (int)threadIdx.x % kChunkRows, lane};
+        softmax.run();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_free(ctl.tmem, 512);
+}
+
+// Joins the pieces of items cut between CTAs: a warp per row.  blockIdx.x
+// names a part; the CTA that holds an item's first steps does the item.
+template <int D>
+__global__ void __launch_bounds__(128) chunk_join_kernel(const __grid_constant__ ChunkParams p, int ctas) {
+    constexpr int kRowsPerBlock = 16;
+    constexpr int E = D / 32;
+    extern __shared__ int list[];  // the item's parts, in the order of its steps
+    grid_dependency_wait();
+    launch_dependents();
+    const ChunkPart part = p.parts[blockIdx.x];
+    if ((part.flags & 3) != 3) return;
+    const int rows = part.tokens * p.group;
+    if ((int)blockIdx.y * kRowsPerBlock >= rows) return;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // Later pieces are the first parts of the following CTAs (one whose share
+    // of the item held no step has none).
+    int count = 1;
+    if (threadIdx.x == 0) list[0] = blockIdx.x;
+    for (int c = blockIdx.x / 2 + 1; c < ctas; c += 32) {
+        ChunkPart next;
+        next.flags = 0;
+        next.item = -1;
+        if (c + lane < ctas) next = p.parts[2 * (c + lane)];
+        const bool hit = (next.flags & 1) && next.item == part.item;
+        const unsigned hits = __ballot_sync(kFullMask, hit);
+        if (warp == 0 && hit) list[count + __popc(hits & ((1u << lane) - 1u))] = 2 * (c + lane);
+        count += __popc(hits);
+        if (__any_sync(kFullMask, hit && (next.flags & 4))) break;
+    }
+    __syncthreads();
+    for (int r = blockIdx.y * kRowsPerBlock + warp; r < min(rows, ((int)blockIdx.y + 1) * kRowsPerBlock); r += 4) {
+        float top = -INFINITY;
+        for (int i = lane; i < count; i += 32) top = fmaxf(top, p.part_ml[(int64_t)list[i] * p.part_rows + r].x);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, d));
+        const float base = top == -INFINITY ? 0.f : top;
+        float sum = 0.f, acc[E] = {};
+        for (int i = 0; i < count; ++i) {
+            const int64_t at = (int64_t)list[i] * p.part_rows + r;
+            const float2 ml = p.part_ml[at];
+            if (ml.y == 0.f) continue;  // the row sees nothing of this piece, whose O may not be written
+            const float w = ex2(ml.x - base);
+            sum += w * ml.y;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += w * p.part_o[at * D + lane * E + e];
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int token = r / p.group, head = part.kv_head * p.group + r % p.group;
+        __half *out = p.out + ((int64_t)(part.row0 + token) * p.num_heads + head) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<__half2 *>(out + e) = __floats2half2_rn(acc[e] * inv, acc[e + 1] * inv);
+    }
+}
+
+}  // namespace pkv
+
+#endif  // PKV_CHUNK_IMPL_CUH

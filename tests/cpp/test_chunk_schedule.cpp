@@ -1,0 +1,157 @@
+// Host check of the chunk attention's work split: for many batches and grids,
+// every step of every item is in exactly one share, empty items are met once,
+// a share holds at most two partial pieces, the closed-form prefix equals the
+// sum, and bisection finds what a walk finds.
+#include <stdio.h>
+#include <stdlib.h>
+
+#include <map>
+#include <tuple>
+#include <vector>
+
+#include "pkv_chunk_schedule.h"
+
+using namespace pkv;
+
+#define CHECK(x)                                                       \
+    do {                                                               \
+        if (!(x)) {                                                    \
+            printf("FAILED %s at line %d\n", #x, __LINE__);            \
+            exit(1);                                                   \
+        }                                                              \
+    } while (0)
+
+static unsigned long long rng_state = 88172645463325252ull;
+static unsigned rnd(unsigned n) {
+    rng_state ^= rng_state << 13;
+    rng_state ^= rng_state >> 7;
+    rng_state ^= rng_state << 17;
+    return (unsigned)(rng_state >> 11) % n;
+}
+
+// A row's own visible range, from the definition.
+static void row_range(const ChunkShape &c, const ChunkSeq &s, int r, int *lo, int *hi) {
+    *lo = 0;
+    *hi = s.len;
+    if (!c.causal) return;
+    const int p = s.len - s.n + r;
+    *hi = p + 1 > 0 ? p + 1 : 0;
+    if (c.window && p - c.window + 1 > 0) *lo = p - c.window + 1;
+}
+
+static void check(const ChunkShape &c, const std::vector<ChunkSeq> &seqs, int shares) {
+    int64_t total = 0;
+    std::vector<int64_t> cum(1, 0);
+    for (const ChunkSeq &s : seqs) {
+        const int items = s.n > 0 ? chunk_items(c, s) : 0;
+        int64_t sum = 0;
+        for (int i = 0; i < items; ++i) {
+            CHECK(chunk_prefix(c, s, i) == sum);
+            int lo, hi, first = 1 << 30, last = 0;
+            chunk_item_range(c, s, i, &lo, &hi);
+            const int w = 2 * c.tile_tokens;
+            for (int r = i * w; r < (i + 1) * w && r < s.n; ++r) {
+                int a, b;
+                row_range(c, s, r, &a, &b);
+                if (b > a) {
+                    if (a < first) first = a;
+                    if (b > last) last = b;
+                }
+            }
+            if (last > 0)
+                CHECK(lo == first && hi == last);
+            else
+                CHECK(lo == hi);
+            CHECK(chunk_cost(c, s, i) == hi - lo + c.overhead);
+            sum += chunk_cost(c, s, i);
+        }
+        if (items) CHECK(chunk_prefix(c, s, items) == sum);
+        CHECK(chunk_seq_units(c, s) == sum * c.num_kv_heads);
+        total += sum * c.num_kv_heads;
+        cum.push_back(total);
+    }
+    std::map<std::tuple<int, int, int>, int> done;   // item -> steps so far, in order of the shares
+    std::map<std::tuple<int, int, int>, int> met;    // empty items
+    CHECK(chunk_share(total, shares, 0) == 0 && chunk_share(total, shares, shares) == total);
+    for (int k = 0; k < shares; ++k) {
+        int64_t u = chunk_share(total, shares, k);
+        const int64_t end = chunk_share(total, shares, k + 1);
+        CHECK(end >= u);
+        int partial = 0;
+        size_t s = 0;
+        while (s < seqs.size() && cum[s + 1] <= u) ++s;
+        if (u >= end) continue;
+        int head, item;
+        int64_t off;
+        chunk_find(c, seqs[s], u - cum[s], &head, &item, &off);
+        while (u < end) {
+            int lo, hi;
+            chunk_item_range(c, seqs[s], item, &lo, &hi);
+            const int64_t cost = chunk_cost(c, seqs[s], item);
+            CHECK(off >= 0 && off < cost);
+            const int64_t b = off + (end - u) < cost ? off + (end - u) : cost;
+            const int t0 = chunk_step_at(c, lo, hi, off), t1 = chunk_step_at(c, lo, hi, b);
+            const int steps = chunk_steps(lo, hi);
+            const auto key = std::make_tuple((int)s, head, item);
+            if (steps == 0 && off == 0) ++met[key];
+            if (t1 > t0) {
+                CHECK(done[key] == t0);
+                done[key] = t1;
+                if (t1 - t0 < steps) ++partial;
+            }
+            u += b - off;
+            off = 0;
+            if (++item == chunk_items(c, seqs[s])) {
+                item = 0;
+                if (++head == c.num_kv_heads) {
+                    head = 0;
+                    do ++s;
+                    while (s < seqs.size() && seqs[s].n == 0);
+                }
+            }
+        }
+        CHECK(partial <= 2);
+    }
+    for (size_t s = 0; s < seqs.size(); ++s)
+        for (int h = 0; h < c.num_kv_heads; ++h)
+            for (int i = 0; seqs[s].n > 0 && i < chunk_items(c, seqs[s]); ++i) {
+                int lo, hi;
+                chunk_item_range(c, seqs[s], i, &lo, &hi);
+                const auto key = std::make_tuple((int)s, h, i);
+                if (chunk_steps(lo, hi))
+                    CHECK(done[key] == chunk_steps(lo, hi));
+                else
+                    CHECK(met[key] == 1);
+            }
+}
+
+int main() {
+    for (int round = 0; round < 4000; ++round) {
+        ChunkShape c;
+        c.tile_tokens = 128 / (1 + (int)rnd(16));
+        c.num_kv_heads = 1 + (int)rnd(4);
+        c.causal = rnd(4) != 0;
+        c.window = c.causal && rnd(2) ? 1 + (int)rnd(rnd(2) ? 700 : 20) : 0;
+        c.overhead = 1 + (int)rnd(400);
+        c.quantum = 1 + (int)rnd(5);
+        std::vector<ChunkSeq> seqs;
+        const int n = 1 + (int)rnd(7);
+        int row = 0;
+        bool any = false;
+        for (int s = 0; s < n; ++s) {
+            ChunkSeq q;
+            q.row0 = row;
+            q.len = rnd(5) ? (int)rnd(rnd(2) ? 3000 : 140) : 0;
+            q.n = rnd(5) ? (int)rnd(rnd(3) ? 30 : 900) : 0;
+            if (rnd(4) && q.n > q.len) q.n = q.len;
+            row += q.n;
+            any = any || q.n > 0;
+            seqs.push_back(q);
+        }
+        if (!any) continue;
+        const int grids[] = {1, 2, 3, 17, 152, 601};
+        check(c, seqs, grids[rnd(6)]);
+    }
+    printf("chunk schedule ok\n");
+    return 0;
+}

@@ -2,6 +2,8 @@
 GPU: the binding's, and the library's own on fake pointers."""
 
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
@@ -83,6 +85,18 @@ def test_chunk_workspace_sizes(lib, no_gpu):
     assert size(100, 8, 2, 128, 4) > 0
     assert size(100, 8, 3, 128, 4) == size(100, 68, 4, 128, 4) == size(100, 8, 2, 96, 4) == 0
     assert size(-1, 8, 2, 128, 4) == size(100, 8, 2, 128, -1) == size(100, 8, 2, 128, 4097) == 0
+
+
+def test_chunk_schedule(tmp_path):
+    """The work split's host check (tests/cpp/test_chunk_schedule.cpp)."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = tmp_path / "test_chunk_schedule"
+    subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-Werror", "-fsanitize=undefined",
+                    "-fno-sanitize-recover=undefined", "-I", os.path.join(root, "paged_kv_cache_152_gb300", "csrc"),
+                    os.path.join(root, "tests", "cpp", "test_chunk_schedule.cpp"), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "chunk schedule ok" in r.stdout
 
 
 def rope_args(t=3, h=4, hkv=2, d=64, rot=64):

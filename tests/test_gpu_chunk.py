@@ -144,6 +144,15 @@ def test_sliding_windows(pkv, window, d, group):
     c.check(c.call(pkv))
 
 
+@pytest.mark.parametrize("group,window,d", [(8, 1000, 128), (8, 1024, 64), (5, 900, 128), (2, 1500, 128)])
+def test_windows_of_many_steps(pkv, group, window, d):
+    """Query tiles whose windows begin in different steps, over more steps than
+    are in flight at once."""
+    c = Case(27, group, 1, d, 32, [(260, 2300), (150, 1400), (90, 1700)], window=window).gpu()
+    c.check(c.call(pkv, num_ctas=3))
+    c.check(c.call(pkv))
+
+
 def test_rows_that_see_nothing(pkv):
     """No context, more new tokens than context, no new tokens."""
     c = Case(5, 4, 2, 128, 16, [(4, 0), (0, 0), (200, 30), (0, 50), (300, 20), (1, 0)], behind=5).gpu()
