@@ -259,6 +259,51 @@ def _status_ptr(status):
     return _ptr(status)
 
 
+def _checked_call(fn, what, specs, stream, args):
+    """One library call with little host work, for calls that take a few
+    microseconds on the GPU: the checks of _need_all and _one_device over
+    (tensor or None, dtype, name, ndim or None) specs, whose dtype None leaves
+    type and layout to the caller, then fn(*args, stream handle) with their
+    device current."""
+    import torch
+    for t, dtype, name, ndim in specs:
+        if t is None or dtype is None:
+            continue
+        if t.dtype is not dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if ndim is not None and t.dim() != ndim:
+            raise ValueError(f"{name}: expected {ndim} dims, got {tuple(t.shape)}")
+    index = None
+    for t, _, name, _ in specs:
+        if t is not None:
+            on = t.get_device()  # -1 on the host
+            if on != index:
+                if on < 0:
+                    raise ValueError(f"{name} must be a CUDA tensor")
+                if index is not None:
+                    raise ValueError("the device tensors of one call must all be on the same CUDA device")
+                index = on
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        if stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args(), handle)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args(), handle)
+    if rc != PKV_OK:
+        _check(rc, what)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
 def _workspace(ws):
     """A caller-given decode workspace: contiguous device memory (its size
     and alignment are checked by the library)."""
@@ -436,26 +481,32 @@ def paged_attention_chunk(out, query, key_cache, value_cache, block_tables, cont
     included).  A workspace (new_chunk_workspace) is allocated when None.
     """
     import torch
-    _need_all((query, torch.float16, "query", 3), (out, torch.float16, "out", 3),
-              (key_cache, torch.float16, "key_cache", 4), (value_cache, torch.float16, "value_cache", 4),
-              (block_tables, torch.int32, "block_tables", 2), (context_lens, torch.int32, "context_lens", 1),
-              (query_starts, torch.int32, "query_starts", 1))
-    t, h, d = query.shape
-    nb, hkv, bs, d2 = key_cache.shape
-    n, mb = block_tables.shape
-    if out.shape != query.shape or d2 != d or value_cache.shape != key_cache.shape \
-            or context_lens.shape[0] != n or query_starts.shape[0] != n + 1:
-        raise ValueError("inconsistent shapes")
-    with _one_device((out, query, key_cache, value_cache, block_tables, context_lens, query_starts, workspace,
-                      status), stream):
-        if workspace is None and t and n:
-            workspace = new_chunk_workspace(t, h, hkv, d, num_ctas, query.device)
-        ws, ws_bytes = _workspace(workspace) if workspace is not None else (None, 0)
-        rc = load().pkv_paged_attention_chunk(
-            _ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables), mb, _ptr(context_lens),
-            _ptr(query_starts), t, n, h, hkv, d, bs, nb, float(scale), int(bool(causal)), int(window), int(num_ctas),
-            ws, ws_bytes, _status_ptr(status), _stream(stream))
-    _check(rc, "pkv_paged_attention_chunk")
+    lib = load()
+
+    def args():
+        t, h, d = query.shape
+        nb, hkv, bs, d2 = key_cache.shape
+        n, mb = block_tables.shape
+        if out.shape != query.shape or d2 != d or value_cache.shape != key_cache.shape \
+                or context_lens.shape[0] != n or query_starts.shape[0] != n + 1:
+            raise ValueError("inconsistent shapes")
+        if status is not None and status.numel() < 1:
+            raise ValueError("status must hold at least one int32")
+        ws = workspace
+        if ws is None and t and n:
+            ws = new_chunk_workspace(t, h, hkv, d, num_ctas, query.device)
+        return (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                block_tables.data_ptr(), mb, context_lens.data_ptr(), query_starts.data_ptr(), t, n, h, hkv, d, bs,
+                nb, float(scale), 1 if causal else 0, int(window), int(num_ctas), _address(ws), 0 if ws is None else ws.nbytes,
+                _address(status))
+
+    f16, i32 = torch.float16, torch.int32
+    _checked_call(lib.pkv_paged_attention_chunk, "pkv_paged_attention_chunk",
+                  ((query, f16, "query", 3), (out, f16, "out", 3), (key_cache, f16, "key_cache", 4),
+                   (value_cache, f16, "value_cache", 4), (block_tables, i32, "block_tables", 2),
+                   (context_lens, i32, "context_lens", 1), (query_starts, i32, "query_starts", 1),
+                   (workspace, None if workspace is None else workspace.dtype, "workspace", None),
+                   (status, i32, "status", None)), stream, args)
     return out
 
 
@@ -630,45 +681,34 @@ def _rows(t, name):
     """The token stride of fp16 [T][heads][D]: each token's heads contiguous,
     tokens any multiple of 8 elements apart (a view of a projection's output)."""
     import torch
-    if t.dtype != torch.float16:
+    if t.dtype is not torch.float16:
         raise TypeError(f"{name}: expected {torch.float16}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name}: expected 3 dims, got {tuple(t.shape)}")
     n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    sn, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    stride = t.stride(0) if n > 1 else h * d
+    stride = sn if n > 1 else h * d
     if stride < h * d or stride % 8:
         raise ValueError(f"{name}: tokens must be a multiple of 8 elements apart and must not overlap")
     return stride
 
 
-def _on_gpu(*specs):
-    for t, name in specs:
-        if t.device.type != "cuda":
-            raise ValueError(f"{name} must be a CUDA tensor")
-
-
-def _rope_args(query, key, positions, cos_sin, query_weight, key_weight):
-    """The checks that both qk_norm_rope calls share; -> rot_dim."""
+def _rope_specs(t, d, positions, cos_sin, query_weight, key_weight, status):
+    """The checks of the tables that both qk_norm_rope calls share; -> specs."""
     import torch
-    t, _, d = query.shape
-    rot = 0
     if (positions is None) != (cos_sin is None):
         raise ValueError("positions and cos_sin go together")
-    if positions is not None:
-        _need_all((positions, torch.int64, "positions", 1), (cos_sin, torch.float32, "cos_sin", 2))
-        rot = cos_sin.shape[1]
-        if positions.shape[0] != t:
-            raise ValueError("inconsistent shapes")
-    for w, name in ((query_weight, "query_weight"), (key_weight, "key_weight")):
-        if w is not None:
-            _need_all((w, torch.float16, name, 1))
-            if w.shape[0] != d:
-                raise ValueError("inconsistent shapes")
-    if key.shape[0] != t or key.shape[2] != d:
-        raise ValueError("inconsistent shapes")
-    return rot
+    if positions is not None and positions.shape != (t,):
+        raise ValueError("positions: inconsistent shapes")
+    if query_weight is not None and query_weight.shape != (d,) or key_weight is not None and key_weight.shape != (d,):
+        raise ValueError("weights: inconsistent shapes")
+    if status is not None and status.numel() < 1:
+        raise ValueError("status must hold at least one int32")
+    return ((positions, torch.int64, "positions", 1), (cos_sin, torch.float32, "cos_sin", 2),
+            (query_weight, torch.float16, "query_weight", 1), (key_weight, torch.float16, "key_weight", 1),
+            (status, torch.int32, "status", None))
 
 
 @_traced
@@ -681,17 +721,20 @@ def qk_norm_rope(query_out, key_out, query, key, positions=None, cos_sin=None, q
     views whose tokens are strided; query_out may be query, key_out key."""
     sq, sk, sqo, sko = _rows(query, "query"), _rows(key, "key"), _rows(query_out, "query_out"), \
         _rows(key_out, "key_out")
-    _on_gpu((query, "query"), (key, "key"), (query_out, "query_out"), (key_out, "key_out"))
-    rot = _rope_args(query, key, positions, cos_sin, query_weight, key_weight)
     t, h, d = query.shape
-    if query_out.shape != query.shape or key_out.shape != key.shape:
+    if query_out.shape != query.shape or key_out.shape != key.shape or key.shape[0] != t or key.shape[2] != d:
         raise ValueError("inconsistent shapes")
-    with _one_device((query_out, key_out, query, key, positions, cos_sin, query_weight, key_weight, status), stream):
-        rc = load().pkv_qk_norm_rope(
-            _ptr(query_out), sqo, _ptr(key_out), sko, _ptr(query), sq, _ptr(key), sk, _ptr(positions), _ptr(cos_sin),
-            cos_sin.shape[0] if rot else 0, rot, int(bool(interleaved)), _ptr(query_weight), _ptr(key_weight),
-            float(eps), t, h, key.shape[1], d, _status_ptr(status), _stream(stream))
-    _check(rc, "pkv_qk_norm_rope")
+    specs = _rope_specs(t, d, positions, cos_sin, query_weight, key_weight, status)
+
+    def args():
+        reach, rot = cos_sin.shape if cos_sin is not None else (0, 0)
+        return (query_out.data_ptr(), sqo, key_out.data_ptr(), sko, query.data_ptr(), sq, key.data_ptr(), sk,
+                _address(positions), _address(cos_sin), reach, rot, 1 if interleaved else 0, _address(query_weight),
+                _address(key_weight), float(eps), t, h, key.shape[1], d, _address(status))
+
+    _checked_call(load().pkv_qk_norm_rope, "pkv_qk_norm_rope",
+                  ((query, None, "query", 3), (key, None, "key", 3), (query_out, None, "query_out", 3),
+                   (key_out, None, "key_out", 3)) + specs, stream, args)
     return query_out, key_out
 
 
@@ -704,23 +747,26 @@ def qk_norm_rope_and_cache(query_out, query, key, value, key_cache, value_cache,
     [T]) of key_cache / value_cache (fp16 [NB][Hkv][bs][D])."""
     import torch
     sq, sk, sv, sqo = _rows(query, "query"), _rows(key, "key"), _rows(value, "value"), _rows(query_out, "query_out")
-    _on_gpu((query, "query"), (key, "key"), (value, "value"), (query_out, "query_out"))
-    rot = _rope_args(query, key, positions, cos_sin, query_weight, key_weight)
-    _need_all((key_cache, torch.float16, "key_cache", 4), (value_cache, torch.float16, "value_cache", 4),
-              (slot_mapping, torch.int64, "slot_mapping", 1))
     t, h, d = query.shape
-    nb, hkv, bs, d2 = key_cache.shape
-    if query_out.shape != query.shape or value.shape != key.shape or key.shape[1] != hkv or d2 != d \
-            or value_cache.shape != key_cache.shape or slot_mapping.shape[0] != t:
-        raise ValueError("inconsistent shapes")
-    with _one_device((query_out, query, key, value, key_cache, value_cache, slot_mapping, positions, cos_sin,
-                      query_weight, key_weight, status), stream):
-        rc = load().pkv_qk_norm_rope_and_cache(
-            _ptr(query_out), sqo, _ptr(query), sq, _ptr(key), sk, _ptr(value), sv, _ptr(key_cache),
-            _ptr(value_cache), _ptr(slot_mapping), _ptr(positions), _ptr(cos_sin), cos_sin.shape[0] if rot else 0,
-            rot, int(bool(interleaved)), _ptr(query_weight), _ptr(key_weight), float(eps), t, h, hkv, d, bs, nb,
-            _status_ptr(status), _stream(stream))
-    _check(rc, "pkv_qk_norm_rope_and_cache")
+    specs = _rope_specs(t, d, positions, cos_sin, query_weight, key_weight, status)
+
+    def args():
+        nb, hkv, bs, d2 = key_cache.shape
+        if query_out.shape != query.shape or value.shape != key.shape or key.shape != (t, hkv, d) or d2 != d \
+                or value_cache.shape != key_cache.shape or slot_mapping.shape[0] != t:
+            raise ValueError("inconsistent shapes")
+        reach, rot = cos_sin.shape if cos_sin is not None else (0, 0)
+        return (query_out.data_ptr(), sqo, query.data_ptr(), sq, key.data_ptr(), sk, value.data_ptr(), sv,
+                key_cache.data_ptr(), value_cache.data_ptr(), slot_mapping.data_ptr(), _address(positions),
+                _address(cos_sin), reach, rot, 1 if interleaved else 0, _address(query_weight),
+                _address(key_weight), float(eps), t, h, hkv, d, bs, nb, _address(status))
+
+    f16 = torch.float16
+    _checked_call(load().pkv_qk_norm_rope_and_cache, "pkv_qk_norm_rope_and_cache",
+                  ((query, None, "query", 3), (key, None, "key", 3), (value, None, "value", 3),
+                   (query_out, None, "query_out", 3), (key_cache, f16, "key_cache", 4),
+                   (value_cache, f16, "value_cache", 4), (slot_mapping, torch.int64, "slot_mapping", 1)) + specs,
+                  stream, args)
     return query_out
 
 
