@@ -155,7 +155,7 @@ extern "C" int pkv_paged_attention_chunk(void *out, const void *query, const voi
     p.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : 7;
     p.part_rows = ws.part_rows;
     p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
-    p.wait_limit_ns = kWaitLimitNs;
+    p.wait_limit_ns = (uint32_t)kWaitLimitNs;
 
     const bool d64 = head_dim == 64;
     const void *fn = d64 ? reinterpret_cast<const void *>(&chunk_kernel<64>)

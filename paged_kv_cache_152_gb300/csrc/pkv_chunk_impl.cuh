@@ -10,7 +10,7 @@
 // One CTA per SM, 12 warps, walking its share of the work (pkv_chunk_schedule.h)
 // piece by piece:
 //   warps 0-3, 4-7  one softmax warpgroup per slot, a row per thread
-//   warp 8          issues the products (one thread)
+//   warp 8          issues the products
 //   warp 9          walks the schedule and the block tables, issues the copies
 //   warps 10, 11    guard V where a step is not seen by every row (below)
 // A slot is a tile of 128 query rows with its own S and O in tensor memory
@@ -82,7 +82,7 @@ struct ChunkParams {
     int block_shift;     // log2(block_size)
     int part_rows;
     float scale_log2;
-    uint64_t wait_limit_ns;
+    uint32_t wait_limit_ns;
 };
 
 struct ChunkPiece {
@@ -134,31 +134,25 @@ __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// A bounded wait of one thread: false once it has run out of time, or once
-// any thread of the CTA has (the abort flag); every role then leaves its loop.
-__device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, int *abort, int32_t *status,
-                                           uint64_t limit_ns) {
+// A bounded wait of a whole warp, which leaves together: false once it has run
+// out of time, or once any warp of the CTA has (the abort flag); every role
+// then leaves its loop, and the CTA reports the timeout at its end.  Kept
+// small, since it stands in many places: the roles' code has to share the
+// instruction cache.
+__device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, int *abort, uint32_t limit_ns) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint32_t t0 = (uint32_t)global_ns();
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-#pragma unroll 1
-    while (true) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*(volatile int *)abort) return false;
-        if (global_ns() - t0 > limit_ns) {
-            *(volatile int *)abort = 1;
-            report(status, PKV_ERR_DEVICE_TIMEOUT);
-            return false;
-        }
+        do {
+            ok = mbar_try_wait(bar, parity);
+            if (!ok && (uint32_t)global_ns() - t0 > limit_ns) *(volatile int *)abort = 1;
+        } while (!ok && !*(volatile int *)abort);
     }
+    return __all_sync(kFullMask, ok);
 }
 
-// The same for a whole warp, which leaves together.
-__device__ __forceinline__ bool chunk_wait_warp(uint32_t bar, uint32_t parity, int *abort, int32_t *status,
-                                                uint64_t limit_ns) {
-    return __all_sync(kFullMask, chunk_wait(bar, parity, abort, status, limit_ns));
-}
+__device__ __noinline__ void chunk_report_range(int32_t *status) { report(status, PKV_ERR_OUT_OF_RANGE); }
 
 __device__ __forceinline__ int chunk_clamp(int64_t x, int hi) { return (int)chunk_min64(chunk_max64(x, 0), hi); }
 
@@ -171,8 +165,18 @@ __device__ __forceinline__ ChunkSeq chunk_load_seq(const ChunkParams &p, int s, 
     q.n = chunk_clamp(b, p.num_tokens) - q.row0;
     if (q.n < 0) q.n = 0;
     q.len = chunk_clamp(len, most);
-    if (tell && (a != q.row0 || b != q.row0 + q.n || len != q.len)) report(p.status, PKV_ERR_OUT_OF_RANGE);
+    if (tell && (a != q.row0 || b != q.row0 + q.n || len != q.len)) chunk_report_range(p.status);
     return q;
+}
+
+// The schedule's closed forms, with their 64-bit divisions, once each.
+__device__ __noinline__ int64_t chunk_units(const ChunkParams &p, int s, bool tell, ChunkSeq *seq) {
+    *seq = chunk_load_seq(p, s, tell);
+    return chunk_seq_units(p.shape, *seq);
+}
+__device__ __noinline__ void chunk_locate(const ChunkParams &p, const ChunkSeq &s, int64_t x, int *kv_head, int *item,
+                                          int64_t *offset) {
+    chunk_find(p.shape, s, x, kv_head, item, offset);
 }
 
 // The steps of a piece that a slot takes: first, first + stride, ... < end.
@@ -214,13 +218,19 @@ __device__ __forceinline__ uint32_t chunk_v_at(int k, int n) { return k < n - 1 
 __device__ __forceinline__ int chunk_block(const ChunkParams &p, int seq, int logical) {
     int blk = __ldg(p.block_tables + (int64_t)seq * p.max_blocks_per_seq + logical);
     if (blk < 0 || blk >= p.num_blocks) {
-        report(p.status, PKV_ERR_OUT_OF_RANGE);
+        chunk_report_range(p.status);
         blk = 0;
     }
     return blk;
 }
 
 __device__ __forceinline__ bool odd_halves(uint32_t w) { return (((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u) != 0; }
+
+__device__ __forceinline__ uint32_t clear_odd(uint32_t w) {
+    if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u;
+    if ((w & 0x7c000000u) == 0x7c000000u) w &= 0x0000ffffu;
+    return w;
+}
 
 // Adds the elements of V that are not finite to the columns [c0, c0 + cols) of
 // a row already written: those of the mixed steps of the piece that the row
@@ -260,7 +270,7 @@ struct ChunkLoader {
     int parts = 0;
 
     __device__ bool wait(uint64_t &bar, uint32_t parity) {
-        return chunk_wait_warp(smem_addr(&bar), parity, &ctl.abort, p.status, p.wait_limit_ns);
+        return chunk_wait(smem_addr(&bar), parity, &ctl.abort, p.wait_limit_ns);
     }
 
     // This lane's block of step t (-1: none of its positions is seen).
@@ -325,13 +335,16 @@ struct ChunkLoader {
             }
             __syncwarp();
         }
-        int blk = lookup(pc, pc.t0);
-        if (!copy(&p.tmap_k, blk, pc.kv_head, false)) return false;
-        for (int t = pc.t0; t < pc.t1; ++t) {
-            const int next = t + 1 < pc.t1 ? lookup(pc, t + 1) : -1;
-            if (t + 1 < pc.t1 && !copy(&p.tmap_k, next, pc.kv_head, false)) return false;
-            if (!copy(&p.tmap_v, blk, pc.kv_head, chunk_edge(pc, t))) return false;
-            blk = next;
+        // The block table is read two steps ahead of the copies.
+        int now = lookup(pc, pc.t0), next = n > 1 ? lookup(pc, pc.t0 + 1) : -1;
+#pragma unroll 1
+        for (int t = pc.t0 - 1; t < pc.t1; ++t) {
+            const int ahead = t >= pc.t0 && t + 2 < pc.t1 ? lookup(pc, t + 2) : -1;
+            if (t + 1 < pc.t1 && !copy(&p.tmap_k, t < pc.t0 ? now : next, pc.kv_head, false)) return false;
+            if (t < pc.t0) continue;
+            if (!copy(&p.tmap_v, now, pc.kv_head, chunk_edge(pc, t))) return false;
+            now = next;
+            next = ahead;
         }
         return true;
     }
@@ -354,7 +367,7 @@ struct ChunkLoader {
         ChunkSeq q = chunk_load_seq(p, s, false);
         int head, item, items = chunk_items(c, q);
         int64_t off;
-        chunk_find(c, q, u - cum, &head, &item, &off);
+        chunk_locate(p, q, u - cum, &head, &item, &off);
         while (true) {
             ChunkPiece pc;
             const int w = 2 * c.tile_tokens;
@@ -444,7 +457,13 @@ struct ChunkLoader {
 };
 
 // ---------------------------------------------------------------------------
-// warp 8: the products (one thread)
+// warp 8: the products
+
+// A value that is the same in every lane, marked so for the compiler.
+template <typename T>
+__device__ __forceinline__ T uniform(T x) {
+    return __shfl_sync(kFullMask, x, 0);
+}
 
 template <int D>
 struct ChunkProducts {
@@ -452,110 +471,132 @@ struct ChunkProducts {
     const ChunkParams &p;
     typename Cfg::Control &ctl;
     uint32_t q_smem, ring_smem, tmem;
+    int lane;
     uint32_t ring = 0;
-    uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0}, o_uses[2] = {0, 0}, merges = 0;
-    uint32_t guard_phase = 0;  // bit per stage
+    uint32_t q_uses[2] = {0, 0}, p_uses = 0, o_uses = 0, merges = 0;  // p, o: a phase bit per slot
+    uint32_t guard_phase = 0;                                       // a bit per stage
 
     __device__ bool wait(uint64_t &bar, uint32_t parity) {
-        return chunk_wait(smem_addr(&bar), parity, &ctl.abort, p.status, p.wait_limit_ns);
+        return chunk_wait(smem_addr(&bar), parity, &ctl.abort, p.wait_limit_ns);
     }
     __device__ uint32_t s_at(int slot) { return tmem + slot * kChunkTile; }
     __device__ uint32_t o_at(int slot) { return tmem + 2 * kChunkTile + slot * D; }
 
-    __device__ bool scores(const ChunkPiece &pc, int slot, int t, bool release) {
-        const uint32_t at = ring + chunk_k_at(t - pc.t0), st = at % Cfg::kStages;
-        if (!wait(ctl.full[st], at / Cfg::kStages & 1)) return false;
-        tc_fence_after();
-        const uint64_t a = umma_desc(q_smem + (pc.single ? 0 : slot) * Cfg::kTileBytes, 16, 1024);
+    // S of a slot for step k of the piece, whose K is there.
+    __device__ void scores(uint32_t q_buffer, int slot, int k, bool release) {
+        const uint32_t st = uniform((ring + chunk_k_at(k)) % Cfg::kStages);
+        const uint64_t a = umma_desc(q_smem + q_buffer * Cfg::kTileBytes, 16, 1024);
         const uint64_t b = umma_desc(ring_smem + st * Cfg::kTileBytes, 16, 1024);
         constexpr uint32_t idesc = umma_idesc_f16(128, kChunkTile, false);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            const uint32_t step = ((k / 4) * Cfg::kHalfBytes + (k % 4) * 32) >> 4;
-            umma_ss(s_at(slot), a + step, b + step, idesc, k > 0);
+        for (int i = 0; i < D / 16; ++i) {
+            const uint32_t step = ((i / 4) * Cfg::kHalfBytes + (i % 4) * 32) >> 4;
+            umma_ss(s_at(slot), a + step, b + step, idesc, i > 0);
         }
         umma_commit(smem_addr(&ctl.s_full[slot]));
         if (release) umma_commit(smem_addr(&ctl.empty[st]));
-        return true;
     }
 
-    __device__ bool weighted(const ChunkPiece &pc, int slot, int t, bool first, bool last, bool check_guard,
-                             bool release) {
-        if (!wait(ctl.p_full[slot], p_uses[slot] & 1)) return false;
-        ++p_uses[slot];
-        const uint32_t at = ring + chunk_v_at(t - pc.t0, pc.t1 - pc.t0), st = at % Cfg::kStages;
-        if (!wait(ctl.full[st], at / Cfg::kStages & 1)) return false;
-        if (check_guard) {  // the first slot that takes an edge step waits for its guards
-            if (!wait(ctl.guard[st], guard_phase >> st & 1)) return false;
-            guard_phase ^= 1u << st;
-        }
-        if (first) {  // the previous piece's output has been read
-            if (!wait(ctl.o_free[slot], (o_uses[slot] & 1) ^ 1)) return false;
-            if (!wait(ctl.o_cross[slot], (merges & 1) ^ 1)) return false;
-            ++o_uses[slot];
-        }
-        tc_fence_after();
+    // O of a slot (+)= P V for step k of n, whose P and V are there.
+    __device__ void weighted(int slot, int k, int n, bool first, bool last, bool release) {
+        const uint32_t st = uniform((ring + chunk_v_at(k, n)) % Cfg::kStages);
         const uint64_t b = umma_desc(ring_smem + st * Cfg::kTileBytes, Cfg::kHalfBytes, 1024);
         constexpr uint32_t idesc = umma_idesc_f16(128, D, true);
 #pragma unroll
-        for (int k = 0; k < kChunkTile / 16; ++k)
-            umma_ts(o_at(slot), s_at(slot) + k * 8, b + (k * 2048 >> 4), idesc, !(first && k == 0));
+        for (int i = 0; i < kChunkTile / 16; ++i)
+            umma_ts(o_at(slot), s_at(slot) + i * 8, b + (i * 2048 >> 4), idesc, i > 0 || !first);
         if (release) umma_commit(smem_addr(&ctl.empty[st]));
         if (last) umma_commit(smem_addr(&ctl.o_full[slot]));
-        return true;
+    }
+
+    __device__ bool wait_k(int k) {
+        const uint32_t at = ring + chunk_k_at(k);
+        return wait(ctl.full[at % Cfg::kStages], at / Cfg::kStages & 1);
     }
 
     __device__ bool piece(const ChunkPiece &pc) {
-        const int n = pc.t1 - pc.t0;
+        const int t0 = uniform(pc.t0), n = uniform(pc.t1) - t0, single = uniform(pc.single);
         if (n == 0) return true;
-        const int buffers = pc.single ? 1 : 2;
+        const int buffers = single ? 1 : 2;
+        // steps of the piece that each slot takes, counted from its first
+        int first[2], end[2];
+        const int stride = single ? 2 : 1;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            int a, b, unused;
+            chunk_slot_steps(p, pc, s, &a, &b, &unused);
+            first[s] = uniform(a) - t0;
+            end[s] = uniform(b) - t0;
+        }
+        auto takes = [&](int s, int k) {
+            return k >= first[s] && k < end[s] && (!single || ((k - first[s]) & 1) == 0);
+        };
+        int left = (end[0] - first[0] + stride - 1) / stride + (end[1] - first[1] + stride - 1) / stride;
         for (int b = 0; b < buffers; ++b) {
             if (!wait(ctl.q_full[b], q_uses[b] & 1)) return false;
             ++q_uses[b];
         }
-        int first[2], end[2], stride[2];
-        for (int s = 0; s < 2; ++s) chunk_slot_steps(p, pc, s, &first[s], &end[s], &stride[s]);
-        auto takes = [&](int s, int t) {
-            return t >= first[s] && t < end[s] && (!pc.single || (t - pc.t0) % 2 == s);
-        };
-        int left = (end[0] - first[0] + stride[0] - 1) / stride[0] + (end[1] - first[1] + stride[1] - 1) / stride[1];
-        auto do_scores = [&](int s, int t) {
-            // the last slot that takes a step frees its K
-            if (!scores(pc, s, t, s == 1 || !takes(1, t))) return false;
-            if (--left == 0)
-                for (int b = 0; b < buffers; ++b) umma_commit(smem_addr(&ctl.q_empty[b]));
-            return true;
-        };
-        // Slot 0 always meets a step that both take before slot 1 (its window
-        // begins and ends no later), also where slot 1 starts a step later.
-        for (int s = 0; s < 2; ++s)
-            if (first[s] < end[s] && (pc.single || first[s] == pc.t0) && !do_scores(s, first[s])) return false;
-        for (int t = pc.t0; t < pc.t1; ++t) {
-            bool guard = chunk_edge(pc, t);
+        // Step by step and slot by slot: O of the step, then S of the slot's next
+        // step (k == -1: the slots' first S).  Slot 0 always meets a step that both
+        // take before slot 1 (its window begins and ends no later), also where
+        // slot 1 starts a step later.
+#pragma unroll 1
+        for (int k = -1; k < n; ++k) {
+            bool guard = k >= 0 && chunk_edge(pc, t0 + k);
+#pragma unroll 1
             for (int s = 0; s < 2; ++s) {
-                if (!takes(s, t)) {
-                    if (!pc.single && first[s] < end[s] && t + 1 == first[s] && !do_scores(s, t + 1)) return false;
-                    continue;
+                const int begin = s ? first[1] : first[0], stop = s ? end[1] : end[0];
+                const bool pv = k >= 0 && takes(s, k);
+                int next = k + (pv ? stride : 1);
+                bool more = next < stop;
+                if (!pv) {
+                    if (single) next = begin;
+                    more = begin < stop && (single ? k < 0 : next == begin);
                 }
-                const int next = t + stride[s];
-                if (!weighted(pc, s, t, t == first[s], next >= end[s], guard, s == 1 || !takes(1, t))) return false;
-                guard = false;
-                if (next < end[s] && !do_scores(s, next)) return false;
+                if (!pv && !more) continue;
+                // everything but P first, so that nothing stands between P and the products
+                if (more && !wait_k(next)) return false;
+                if (pv) {
+                    const uint32_t at = ring + chunk_v_at(k, n), st = at % Cfg::kStages;
+                    if (!wait(ctl.full[st], at / Cfg::kStages & 1)) return false;
+                    if (guard) {  // the first slot that takes an edge step waits for its guards
+                        if (!wait(ctl.guard[st], guard_phase >> st & 1)) return false;
+                        guard_phase ^= 1u << st;
+                        guard = false;
+                    }
+                    if (k == begin) {  // the previous piece's output has been read
+                        if (!wait(ctl.o_free[s], (o_uses >> s & 1) ^ 1)) return false;
+                        if (!wait(ctl.o_cross[s], (merges & 1) ^ 1)) return false;
+                        o_uses ^= 1u << s;
+                    }
+                    if (!wait(ctl.p_full[s], p_uses >> s & 1)) return false;
+                    p_uses ^= 1u << s;
+                    tc_fence_after();
+                    weighted(s, k, n, k == begin, !more, s == 1 || !takes(1, k));
+                }
+                if (more) {
+                    tc_fence_after();
+                    // the last slot that takes a step frees its K
+                    scores(single ? 0 : s, s, next, s == 1 || !takes(1, next));
+                    if (--left == 0)
+                        for (int b = 0; b < buffers; ++b) umma_commit(smem_addr(&ctl.q_empty[b]));
+                }
             }
         }
-        if (pc.single && n > 1) ++merges;
+        if (single && n > 1) ++merges;
         ring += 2 * n;
         return true;
     }
 
     __device__ void run() {
-        for (uint32_t k = 0;; ++k) {
-            const uint32_t slot = k % kChunkPieces;
-            if (!wait(ctl.piece_full[slot], k / kChunkPieces & 1)) break;
+        for (uint32_t i = 0;; ++i) {
+            const uint32_t slot = i % kChunkPieces;
+            if (!wait(ctl.piece_full[slot], i / kChunkPieces & 1)) break;
             const ChunkPiece &pc = ctl.piece[slot];
             if (pc.last) break;
             if (!piece(pc)) break;
-            mbar_arrive(smem_addr(&ctl.piece_empty[slot]));
+            if (lane == 0) mbar_arrive(smem_addr(&ctl.piece_empty[slot]));
+            __syncwarp();
         }
         umma_commit(smem_addr(&ctl.drain));
         mbar_wait_bounded(smem_addr(&ctl.drain), 0, p.wait_limit_ns);
@@ -566,63 +607,65 @@ struct ChunkProducts {
 // warps 10, 11: V in steps that not every row sees whole
 
 template <int D>
-__device__ void chunk_guard(const ChunkParams &p, typename ChunkConfig<D>::Control &ctl, uint32_t ring_smem, int half,
+__device__ void chunk_guard(const ChunkParams &p, typename ChunkConfig<D>::Control &ctl, unsigned char *ring, int half,
                             int lane) {
     using Cfg = ChunkConfig<D>;
-    uint32_t ring = 0, phase = 0;
+    uint32_t ring_at = 0, phase = 0;
     for (uint32_t k = 0;; ++k) {
         const uint32_t slot = k % kChunkPieces;
-        if (!chunk_wait_warp(smem_addr(&ctl.piece_full[slot]), k / kChunkPieces & 1, &ctl.abort, p.status,
-                             p.wait_limit_ns))
-            return;
+        if (!chunk_wait(smem_addr(&ctl.piece_full[slot]), k / kChunkPieces & 1, &ctl.abort, p.wait_limit_ns)) return;
         ChunkPiece &pc = ctl.piece[slot];
         if (pc.last) return;
         const int n = pc.t1 - pc.t0;
         for (int t = pc.t0; t < pc.t1; ++t) {
             if (!chunk_edge(pc, t)) continue;
-            const uint32_t at = ring + chunk_v_at(t - pc.t0, n), st = at % Cfg::kStages;
-            if (!chunk_wait_warp(smem_addr(&ctl.edge[st]), phase >> st & 1, &ctl.abort, p.status, p.wait_limit_ns))
-                return;
+            const uint32_t at = ring_at + chunk_v_at(t - pc.t0, n), st = at % Cfg::kStages;
+            if (!chunk_wait(smem_addr(&ctl.edge[st]), phase >> st & 1, &ctl.abort, p.wait_limit_ns)) return;
             phase ^= 1u << st;
-            const bool mixed = chunk_mixed(pc, t);
-            const int keep_lo = pc.lo - t * kChunkTile, keep_hi = pc.hi - t * kChunkTile;
+            // Rows of this step: [keep_lo, keep_hi) are seen by some row of the
+            // item, [all_lo, all_hi) by every one.
+            const int at0 = t * kChunkTile;
+            const int keep_lo = pc.lo - at0, keep_hi = pc.hi - at0, all_lo = pc.all_lo - at0, all_hi = pc.all_hi - at0;
             bool odd = false;
-            // this warp's 64 rows, 4 rows of 128 bytes at a time
-            const uint32_t base = ring_smem + st * Cfg::kTileBytes + half * 64 * 128 + lane * 16;
+            // this warp's 64 rows of 128 bytes, 4 at a time, 16 bytes per lane
+            unsigned char *base = ring + st * Cfg::kTileBytes + half * 64 * 128 + lane * 16;
+#pragma unroll 1
+            for (int i0 = 0; i0 < 16; i0 += 4) {
+                const int r0 = half * 64 + i0 * 4;
+                if (r0 >= keep_lo && r0 + 16 <= keep_hi && r0 >= all_lo && r0 + 16 <= all_hi) continue;
+                uint4 w[4][Cfg::kHalves];
+                bool look[4];
 #pragma unroll
-            for (int h = 0; h < Cfg::kHalves; ++h) {
-#pragma unroll 4
-                for (int i = 0; i < 16; ++i) {
-                    const int row = half * 64 + i * 4 + lane / 8;
-                    const uint32_t a = base + h * Cfg::kHalfBytes + i * 512;
-                    if (row < keep_lo || row >= keep_hi) {
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
-                    } else if (mixed) {
-                        uint32_t w[4];
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                     : "r"(a)
-                                     : "memory");
-                        if (odd_halves(w[0]) || odd_halves(w[1]) || odd_halves(w[2]) || odd_halves(w[3])) {
-                            odd = true;
+                for (int i = 0; i < 4; ++i) {
+                    const int row = r0 + i * 4 + lane / 8;
+                    const bool keep = row >= keep_lo && row < keep_hi;
+                    look[i] = keep && !(row >= all_lo && row < all_hi);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                if ((w[j] & 0x7c00u) == 0x7c00u) w[j] &= 0xffff0000u;
-                                if ((w[j] & 0x7c000000u) == 0x7c000000u) w[j] &= 0x0000ffffu;
-                            }
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]),
-                                         "r"(w[2]), "r"(w[3])
-                                         : "memory");
-                        }
+                    for (int h = 0; h < Cfg::kHalves; ++h) {
+                        uint4 *v = reinterpret_cast<uint4 *>(base + h * Cfg::kHalfBytes + (i0 + i) * 512);
+                        w[i][h] = make_uint4(0, 0, 0, 0);
+                        if (look[i]) w[i][h] = *v;
+                        if (!keep) *v = make_uint4(0, 0, 0, 0);
                     }
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int h = 0; h < Cfg::kHalves; ++h) {
+                        uint4 &x = w[i][h];
+                        if (odd_halves(x.x) | odd_halves(x.y) | odd_halves(x.z) | odd_halves(x.w)) {
+                            odd = true;
+                            x = make_uint4(clear_odd(x.x), clear_odd(x.y), clear_odd(x.z), clear_odd(x.w));
+                            *reinterpret_cast<uint4 *>(base + h * Cfg::kHalfBytes + (i0 + i) * 512) = x;
+                        }
+                    }
             }
             if (odd) *(volatile int *)&pc.odd = 1;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&ctl.guard[st]));
         }
-        ring += 2 * n;
+        ring_at += 2 * n;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&ctl.piece_empty[slot]));
     }
@@ -642,7 +685,7 @@ struct ChunkSoftmax {
     float m, l;     // running maximum (of unscaled scores) and sum
 
     __device__ bool wait(uint64_t &bar, uint32_t parity) {
-        return chunk_wait_warp(smem_addr(&bar), parity, &ctl.abort, p.status, p.wait_limit_ns);
+        return chunk_wait(smem_addr(&bar), parity, &ctl.abort, p.wait_limit_ns);
     }
     __device__ void arrive(uint64_t &bar) {
         __syncwarp();
@@ -662,10 +705,10 @@ struct ChunkSoftmax {
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_pin32(s[c]);
-        const bool whole = row_lo <= col0 && col0 + kChunkTile <= row_hi;
+        const bool whole = row_hi < 0 || (row_lo <= col0 && col0 + kChunkTile <= row_hi);
         if (!__all_sync(kFullMask, whole)) {
             const int a = row_lo - col0;
-            const unsigned n = (unsigned)max(row_hi - max(row_lo, 0), 0);
+            const unsigned n = (unsigned)max(row_hi - row_lo, 0);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -756,7 +799,7 @@ struct ChunkSoftmax {
         const int head = pc.kv_head * p.group + row % p.group;
         const bool live = row < p.shape.tile_tokens * p.group && token < pc.tokens &&
                           (slot == 0 || !pc.single || merge);
-        int row_lo = 0, row_hi = 0;
+        int row_lo = 0, row_hi = -1;  // a row of no token: whatever it computes stays in its lane
         if (live) {
             row_hi = pc.len;
             if (p.shape.causal) {
@@ -928,8 +971,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     int64_t *run_units = reinterpret_cast<int64_t *>(ring);
     const int per = (p.num_seqs + kChunkThreads - 1) / kChunkThreads;
     int64_t units = 0;
+    ChunkSeq seq;
     for (int s = threadIdx.x * per; s < min((int)(threadIdx.x + 1) * per, p.num_seqs); ++s)
-        units += chunk_seq_units(p.shape, chunk_load_seq(p, s, blockIdx.x == 0));
+        units += chunk_units(p, s, blockIdx.x == 0, &seq);
     run_units[threadIdx.x] = units;
     tc_fence_before();
     __syncthreads();
@@ -958,7 +1002,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                 while (cum + run_units[run] <= u) cum += run_units[run++];
                 s = run * per;
                 while (true) {
-                    const int64_t x = chunk_seq_units(p.shape, chunk_load_seq(p, s, false));
+                    const int64_t x = chunk_units(p, s, false, &seq);
                     if (cum + x > u) break;
                     cum += x;
                     ++s;
@@ -969,13 +1013,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             ChunkLoader<D> loader{p, ctl, smem_addr(smem), smem_addr(ring), lane};
             loader.run(s, cum, u, end);
         } else if (warp == 8) {
-            if (lane == 0) {
-                ChunkProducts<D> products{p, ctl, smem_addr(smem), smem_addr(ring), ctl.tmem};
-                products.run();
-            }
+            ChunkProducts<D> products{p, ctl, smem_addr(smem), smem_addr(ring), uniform(ctl.tmem), lane};
+            products.run();
             __syncwarp();
         } else {
-            chunk_guard<D>(p, ctl, smem_addr(ring), warp - 10, lane);
+            chunk_guard<D>(p, ctl, ring, warp - 10, lane);
         }
     } else {
         regs_up<208>();
@@ -987,6 +1029,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     if (warp == 8) tmem_free(ctl.tmem, 512);
+    if (threadIdx.x == 0 && ctl.abort) report(p.status, PKV_ERR_DEVICE_TIMEOUT);
 }
 
 // Joins the pieces of items cut between CTAs: a warp per row.  blockIdx.x
