@@ -10,9 +10,9 @@
 // One CTA per SM, 12 warps, walking its share of the work (pkv_chunk_schedule.h)
 // piece by piece:
 //   warps 0-3, 4-7  one softmax warpgroup per slot, a row per thread
-//   warp 8          issues the products
-//   warp 9          walks the schedule and the block tables, issues the copies
-//   warps 10, 11    guard V where a step is not seen by every row (below)
+//   warps 8, 9      issue the products of a slot each
+//   warp 10         walks the schedule and the block tables, issues the copies
+//   warp 11         guards V where a step is not seen by every row (below)
 // A slot is a tile of 128 query rows with its own S and O in tensor memory
 // (P overlays S: all 512 columns are used at head_dim 128).  The two slots of a
 // piece are either two query tiles that share every step of K and V, or, where
@@ -26,8 +26,8 @@
 // HBM takes longer than its products, so padding costs no time.
 //
 // V is read as an operand for every row of a tile, and 0 * NaN is NaN.  So in
-// steps that some row does not see whole, the guard warps clear the rows of V
-// that no row of the item sees (table ends, what precedes a window) and clear
+// steps that some row does not see whole, the guard warp clears the rows of V
+// that no row of the item sees (table ends, what precedes a window) and clears
 // single elements that are not finite; the epilogue adds the latter to the
 // rows that do see them (they decide those elements: finite + inf = inf).
 #ifndef PKV_CHUNK_IMPL_CUH
@@ -98,7 +98,7 @@ struct ChunkPiece {
     int partial;         // the part it writes, or -1
     int single;          // one query tile: the slots take alternate steps
     int last;            // no piece: the end
-    int odd;             // a guard cleared an element that was not finite
+    int odd;             // the guard cleared an element that was not finite
 };
 
 template <int D>
@@ -110,7 +110,7 @@ struct ChunkConfig {
     struct Control {
         uint64_t full[kStages], empty[kStages], edge[kStages], guard[kStages];
         uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], o_cross[2];
-        uint64_t x_full, x_empty, drain;
+        uint64_t x_full, x_empty, drain[2];
         uint64_t piece_full[kChunkPieces], piece_empty[kChunkPieces];
         ChunkPiece piece[kChunkPieces];
         float2 ml[2][kChunkRows];
@@ -140,16 +140,14 @@ __device__ __forceinline__ void regs_down() {
 // small, since it stands in many places: the roles' code has to share the
 // instruction cache.
 __device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, int *abort, uint32_t limit_ns) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok) {
-        const uint32_t t0 = (uint32_t)global_ns();
+    if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
+    const uint32_t t0 = (uint32_t)global_ns();
 #pragma unroll 1
-        do {
-            ok = mbar_try_wait(bar, parity);
-            if (!ok && (uint32_t)global_ns() - t0 > limit_ns) *(volatile int *)abort = 1;
-        } while (!ok && !*(volatile int *)abort);
+    while (true) {
+        if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
+        if ((uint32_t)global_ns() - t0 > limit_ns) *(volatile int *)abort = 1;
+        if (__any_sync(kFullMask, *(volatile int *)abort)) return false;
     }
-    return __all_sync(kFullMask, ok);
 }
 
 __device__ __noinline__ void chunk_report_range(int32_t *status) { report(status, PKV_ERR_OUT_OF_RANGE); }
@@ -254,7 +252,7 @@ __device__ __noinline__ void chunk_add_odd(const ChunkParams &p, const ChunkPiec
 }
 
 // ---------------------------------------------------------------------------
-// warp 9: the schedule and the copies
+// warp 10: the schedule and the copies
 
 template <int D>
 struct ChunkLoader {
@@ -281,8 +279,8 @@ struct ChunkLoader {
         return mine ? chunk_block(p, pc.seq, b) : -1;
     }
 
-    // One tile into the next stage.  A tile that the guards go over first
-    // (edge) lands on a barrier of their own, and the products wait for them.
+    // One tile into the next stage.  A tile that the guard goes over first
+    // (edge) lands on a barrier of its own, and the products wait for the guard.
     __device__ bool copy(const CUtensorMap *map, int blk, int kv_head, bool edge) {
         const uint32_t st = ring % Cfg::kStages;
         if (!wait(ctl.empty[st], (ring / Cfg::kStages & 1) ^ 1)) return false;
@@ -457,131 +455,109 @@ struct ChunkLoader {
 };
 
 // ---------------------------------------------------------------------------
-// warp 8: the products
+// warps 8, 9: the products of a slot each
 
-// A value that is the same in every lane, marked so for the compiler.
-template <typename T>
-__device__ __forceinline__ T uniform(T x) {
-    return __shfl_sync(kFullMask, x, 0);
-}
+// A value that is the same in every lane, put in a uniform register: a warp
+// reduction leaves it there, where a shuffle or a load would not.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(kFullMask, x); }
+__device__ __forceinline__ int uniform(int x) { return (int)uniform((uint32_t)x); }
 
 template <int D>
 struct ChunkProducts {
     using Cfg = ChunkConfig<D>;
     const ChunkParams &p;
     typename Cfg::Control &ctl;
-    uint32_t q_smem, ring_smem, tmem;
-    int lane;
-    uint32_t ring = 0;
-    uint32_t q_uses[2] = {0, 0}, p_uses = 0, o_uses = 0, merges = 0;  // p, o: a phase bit per slot
-    uint32_t guard_phase = 0;                                       // a bit per stage
+    uint32_t q_smem, ring_smem, s_tmem, o_tmem;
+    int slot;
+    uint32_t ring = 0;          // ring position of the piece's first copy
+    uint32_t q_uses[2] = {0, 0}, p_uses = 0, o_uses = 0, merges = 0;
+    uint32_t guard_phase = 0;   // a bit per stage
 
     __device__ bool wait(uint64_t &bar, uint32_t parity) {
         return chunk_wait(smem_addr(&bar), parity, &ctl.abort, p.wait_limit_ns);
     }
-    __device__ uint32_t s_at(int slot) { return tmem + slot * kChunkTile; }
-    __device__ uint32_t o_at(int slot) { return tmem + 2 * kChunkTile + slot * D; }
 
-    // S of a slot for step k of the piece, whose K is there.
-    __device__ void scores(uint32_t q_buffer, int slot, int k, bool release) {
-        const uint32_t st = uniform((ring + chunk_k_at(k)) % Cfg::kStages);
+    // S of the slot for step k of the piece, whose K is there.
+    __device__ void scores(uint32_t q_buffer, uint32_t st) {
         const uint64_t a = umma_desc(q_smem + q_buffer * Cfg::kTileBytes, 16, 1024);
         const uint64_t b = umma_desc(ring_smem + st * Cfg::kTileBytes, 16, 1024);
         constexpr uint32_t idesc = umma_idesc_f16(128, kChunkTile, false);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             const uint32_t step = ((i / 4) * Cfg::kHalfBytes + (i % 4) * 32) >> 4;
-            umma_ss(s_at(slot), a + step, b + step, idesc, i > 0);
+            umma_ss(s_tmem, a + step, b + step, idesc, i > 0);
         }
         umma_commit(smem_addr(&ctl.s_full[slot]));
-        if (release) umma_commit(smem_addr(&ctl.empty[st]));
     }
 
-    // O of a slot (+)= P V for step k of n, whose P and V are there.
-    __device__ void weighted(int slot, int k, int n, bool first, bool last, bool release) {
-        const uint32_t st = uniform((ring + chunk_v_at(k, n)) % Cfg::kStages);
+    // O of the slot (+)= P V, where P and V are there.
+    __device__ void weighted(uint32_t st, bool begins) {
         const uint64_t b = umma_desc(ring_smem + st * Cfg::kTileBytes, Cfg::kHalfBytes, 1024);
         constexpr uint32_t idesc = umma_idesc_f16(128, D, true);
 #pragma unroll
         for (int i = 0; i < kChunkTile / 16; ++i)
-            umma_ts(o_at(slot), s_at(slot) + i * 8, b + (i * 2048 >> 4), idesc, i > 0 || !first);
-        if (release) umma_commit(smem_addr(&ctl.empty[st]));
-        if (last) umma_commit(smem_addr(&ctl.o_full[slot]));
-    }
-
-    __device__ bool wait_k(int k) {
-        const uint32_t at = ring + chunk_k_at(k);
-        return wait(ctl.full[at % Cfg::kStages], at / Cfg::kStages & 1);
+            umma_ts(o_tmem, s_tmem + i * 8, b + (i * 2048 >> 4), idesc, i > 0 || !begins);
     }
 
     __device__ bool piece(const ChunkPiece &pc) {
         const int t0 = uniform(pc.t0), n = uniform(pc.t1) - t0, single = uniform(pc.single);
         if (n == 0) return true;
-        const int buffers = single ? 1 : 2;
-        // steps of the piece that each slot takes, counted from its first
-        int first[2], end[2];
-        const int stride = single ? 2 : 1;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            int a, b, unused;
-            chunk_slot_steps(p, pc, s, &a, &b, &unused);
-            first[s] = uniform(a) - t0;
-            end[s] = uniform(b) - t0;
-        }
-        auto takes = [&](int s, int k) {
-            return k >= first[s] && k < end[s] && (!single || ((k - first[s]) & 1) == 0);
-        };
-        int left = (end[0] - first[0] + stride - 1) / stride + (end[1] - first[1] + stride - 1) / stride;
-        for (int b = 0; b < buffers; ++b) {
-            if (!wait(ctl.q_full[b], q_uses[b] & 1)) return false;
-            ++q_uses[b];
-        }
-        // Step by step and slot by slot: O of the step, then S of the slot's next
-        // step (k == -1: the slots' first S).  Slot 0 always meets a step that both
-        // take before slot 1 (its window begins and ends no later), also where
-        // slot 1 starts a step later.
+        const int all_lo = uniform(pc.all_lo), all_hi = uniform(pc.all_hi);
+        int first, end, stride;
+        chunk_slot_steps(p, pc, slot, &first, &end, &stride);
+        first = uniform(first) - t0;
+        end = uniform(end) - t0;
+        stride = single ? 2 : 1;
+        auto takes = [&](int k) { return k >= first && k < end && (!single || ((k - first) & 1) == 0); };
+        const int last = first < end ? first + (end - 1 - first) / stride * stride : -1;
+        // Queries: a tile of its own each, or the first buffer for both.
+        const int buffer = single ? 0 : slot;
+        if (!wait(ctl.q_full[0], q_uses[0] & 1)) return false;
+        if (buffer == 1 && !wait(ctl.q_full[1], q_uses[1] & 1)) return false;
+        ++q_uses[0];
+        if (!single) ++q_uses[1];
+        if (slot == 1 && !single) umma_arrive(smem_addr(&ctl.q_empty[0]));
+        if (first >= end) umma_arrive(smem_addr(&ctl.q_empty[buffer]));
+        // Both warps go through all copies of the piece and each frees every
+        // stage, by a commit where it reads it and at once where it does not: O of
+        // step k, then S of step k + 1 (which overwrites P of the slot's last step).
 #pragma unroll 1
         for (int k = -1; k < n; ++k) {
-            bool guard = k >= 0 && chunk_edge(pc, t0 + k);
-#pragma unroll 1
-            for (int s = 0; s < 2; ++s) {
-                const int begin = s ? first[1] : first[0], stop = s ? end[1] : end[0];
-                const bool pv = k >= 0 && takes(s, k);
-                int next = k + (pv ? stride : 1);
-                bool more = next < stop;
-                if (!pv) {
-                    if (single) next = begin;
-                    more = begin < stop && (single ? k < 0 : next == begin);
-                }
-                if (!pv && !more) continue;
+            const uint32_t v_at = ring + chunk_v_at(k, n), v_st = v_at % Cfg::kStages;
+            const uint32_t k_at = ring + chunk_k_at(k + 1), k_st = k_at % Cfg::kStages;
+            const bool edge = k >= 0 && ((t0 + k) * kChunkTile < all_lo || (t0 + k + 1) * kChunkTile > all_hi);
+            if (k >= 0 && takes(k)) {
                 // everything but P first, so that nothing stands between P and the products
-                if (more && !wait_k(next)) return false;
-                if (pv) {
-                    const uint32_t at = ring + chunk_v_at(k, n), st = at % Cfg::kStages;
-                    if (!wait(ctl.full[st], at / Cfg::kStages & 1)) return false;
-                    if (guard) {  // the first slot that takes an edge step waits for its guards
-                        if (!wait(ctl.guard[st], guard_phase >> st & 1)) return false;
-                        guard_phase ^= 1u << st;
-                        guard = false;
-                    }
-                    if (k == begin) {  // the previous piece's output has been read
-                        if (!wait(ctl.o_free[s], (o_uses >> s & 1) ^ 1)) return false;
-                        if (!wait(ctl.o_cross[s], (merges & 1) ^ 1)) return false;
-                        o_uses ^= 1u << s;
-                    }
-                    if (!wait(ctl.p_full[s], p_uses >> s & 1)) return false;
-                    p_uses ^= 1u << s;
-                    tc_fence_after();
-                    weighted(s, k, n, k == begin, !more, s == 1 || !takes(1, k));
+                if (!wait(ctl.full[v_st], v_at / Cfg::kStages & 1)) return false;
+                if (edge && !wait(ctl.guard[v_st], guard_phase >> v_st & 1)) return false;
+                if (k == first) {  // the previous piece's output has been read
+                    if (!wait(ctl.o_free[slot], (o_uses & 1) ^ 1)) return false;
+                    if (!wait(ctl.o_cross[slot], (merges & 1) ^ 1)) return false;
+                    ++o_uses;
                 }
-                if (more) {
+                if (!wait(ctl.p_full[slot], p_uses & 1)) return false;
+                ++p_uses;
+                tc_fence_after();
+                weighted(v_st, k == first);
+                umma_commit(smem_addr(&ctl.empty[v_st]));
+                if (k == last) umma_commit(smem_addr(&ctl.o_full[slot]));
+            }
+            if (k + 1 < n) {
+                if (!wait(ctl.full[k_st], k_at / Cfg::kStages & 1)) return false;
+                if (takes(k + 1)) {
                     tc_fence_after();
-                    // the last slot that takes a step frees its K
-                    scores(single ? 0 : s, s, next, s == 1 || !takes(1, next));
-                    if (--left == 0)
-                        for (int b = 0; b < buffers; ++b) umma_commit(smem_addr(&ctl.q_empty[b]));
+                    scores(buffer, k_st);
+                    umma_commit(smem_addr(&ctl.empty[k_st]));
+                    if (k + 1 == last) umma_commit(smem_addr(&ctl.q_empty[buffer]));
+                } else {
+                    umma_arrive(smem_addr(&ctl.empty[k_st]));
                 }
             }
+            if (k >= 0 && !takes(k)) {
+                if (!wait(ctl.full[v_st], v_at / Cfg::kStages & 1)) return false;
+                umma_arrive(smem_addr(&ctl.empty[v_st]));
+            }
+            if (edge) guard_phase ^= 1u << v_st;
         }
         if (single && n > 1) ++merges;
         ring += 2 * n;
@@ -590,25 +566,23 @@ struct ChunkProducts {
 
     __device__ void run() {
         for (uint32_t i = 0;; ++i) {
-            const uint32_t slot = i % kChunkPieces;
-            if (!wait(ctl.piece_full[slot], i / kChunkPieces & 1)) break;
-            const ChunkPiece &pc = ctl.piece[slot];
-            if (pc.last) break;
+            const uint32_t at = i % kChunkPieces;
+            if (!wait(ctl.piece_full[at], i / kChunkPieces & 1)) break;
+            const ChunkPiece &pc = ctl.piece[at];
+            if (uniform(pc.last)) break;
             if (!piece(pc)) break;
-            if (lane == 0) mbar_arrive(smem_addr(&ctl.piece_empty[slot]));
-            __syncwarp();
+            umma_arrive(smem_addr(&ctl.piece_empty[at]));
         }
-        umma_commit(smem_addr(&ctl.drain));
-        mbar_wait_bounded(smem_addr(&ctl.drain), 0, p.wait_limit_ns);
+        umma_commit(smem_addr(&ctl.drain[slot]));
+        mbar_wait_bounded(smem_addr(&ctl.drain[slot]), 0, p.wait_limit_ns);
     }
 };
 
 // ---------------------------------------------------------------------------
-// warps 10, 11: V in steps that not every row sees whole
+// warp 11: V in steps that not every row sees whole
 
 template <int D>
-__device__ void chunk_guard(const ChunkParams &p, typename ChunkConfig<D>::Control &ctl, unsigned char *ring, int half,
-                            int lane) {
+__device__ void chunk_guard(const ChunkParams &p, typename ChunkConfig<D>::Control &ctl, unsigned char *ring, int lane) {
     using Cfg = ChunkConfig<D>;
     uint32_t ring_at = 0, phase = 0;
     for (uint32_t k = 0;; ++k) {
@@ -627,11 +601,11 @@ __device__ void chunk_guard(const ChunkParams &p, typename ChunkConfig<D>::Contr
             const int at0 = t * kChunkTile;
             const int keep_lo = pc.lo - at0, keep_hi = pc.hi - at0, all_lo = pc.all_lo - at0, all_hi = pc.all_hi - at0;
             bool odd = false;
-            // this warp's 64 rows of 128 bytes, 4 at a time, 16 bytes per lane
-            unsigned char *base = ring + st * Cfg::kTileBytes + half * 64 * 128 + lane * 16;
+            // rows of 128 bytes, 4 at a time, 16 bytes per lane
+            unsigned char *base = ring + st * Cfg::kTileBytes + lane * 16;
 #pragma unroll 1
-            for (int i0 = 0; i0 < 16; i0 += 4) {
-                const int r0 = half * 64 + i0 * 4;
+            for (int i0 = 0; i0 < 32; i0 += 4) {
+                const int r0 = i0 * 4;
                 if (r0 >= keep_lo && r0 + 16 <= keep_hi && r0 >= all_lo && r0 + 16 <= all_hi) continue;
                 uint4 w[4][Cfg::kHalves];
                 bool look[4];
@@ -935,25 +909,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     if (threadIdx.x == 0) {
         for (int i = 0; i < Cfg::kStages; ++i) {
             mbar_init(smem_addr(&ctl.full[i]), 1);
-            mbar_init(smem_addr(&ctl.empty[i]), 1);
+            mbar_init(smem_addr(&ctl.empty[i]), 2);  // both warps of products
             mbar_init(smem_addr(&ctl.edge[i]), 1);
-            mbar_init(smem_addr(&ctl.guard[i]), 2);
+            mbar_init(smem_addr(&ctl.guard[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&ctl.q_full[i]), 1);
-            mbar_init(smem_addr(&ctl.q_empty[i]), 1);
+            mbar_init(smem_addr(&ctl.q_empty[i]), i == 0 ? 2 : 1);  // the first buffer serves both slots of a lone tile
             mbar_init(smem_addr(&ctl.s_full[i]), 1);
             mbar_init(smem_addr(&ctl.p_full[i]), 4);
             mbar_init(smem_addr(&ctl.o_full[i]), 1);
             mbar_init(smem_addr(&ctl.o_free[i]), 4);
             mbar_init(smem_addr(&ctl.o_cross[i]), 4);
+            mbar_init(smem_addr(&ctl.drain[i]), 1);
         }
         mbar_init(smem_addr(&ctl.x_full), 8);
         mbar_init(smem_addr(&ctl.x_empty), 8);
-        mbar_init(smem_addr(&ctl.drain), 1);
         for (int i = 0; i < kChunkPieces; ++i) {
             mbar_init(smem_addr(&ctl.piece_full[i]), 1);
-            mbar_init(smem_addr(&ctl.piece_empty[i]), 11);  // 8 softmax warps, the products, 2 guards
+            mbar_init(smem_addr(&ctl.piece_empty[i]), 11);  // all but the loader
         }
         ctl.abort = 0;
         fence_barrier_init();
@@ -981,7 +955,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 
     if (warp >= 8) {
         regs_down<88>();
-        if (warp == 9) {
+        if (warp == 10) {
             // 12 runs per lane
             int64_t mine = 0;
             for (int i = 0; i < 12; ++i) mine += run_units[lane * 12 + i];
@@ -1012,12 +986,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             fence_proxy_async_smem();  // the ring's memory was read and written by ordinary accesses
             ChunkLoader<D> loader{p, ctl, smem_addr(smem), smem_addr(ring), lane};
             loader.run(s, cum, u, end);
-        } else if (warp == 8) {
-            ChunkProducts<D> products{p, ctl, smem_addr(smem), smem_addr(ring), uniform(ctl.tmem), lane};
-            products.run();
-            __syncwarp();
+        } else if (warp == 11) {
+            chunk_guard<D>(p, ctl, ring, lane);
         } else {
-            chunk_guard<D>(p, ctl, ring, warp - 10, lane);
+            const int slot = uniform(warp - 8);
+            const uint32_t tmem = uniform(ctl.tmem);
+            ChunkProducts<D> products{p, ctl, smem_addr(smem), smem_addr(ring), tmem + slot * kChunkTile,
+                                      tmem + 2 * kChunkTile + slot * D, slot};
+            products.run();
         }
     } else {
         regs_up<208>();
