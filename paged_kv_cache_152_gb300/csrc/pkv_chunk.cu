@@ -26,8 +26,8 @@ bool shape_ok(int num_heads, int num_kv_heads, int head_dim) {
 // Units of an item besides its positions: what a piece costs before its first
 // step (queries in, output out), in positions.
 constexpr int kOverhead = 256;
-// Items are cut at multiples of this many steps.
-constexpr int kQuantum = 2;
+// Items are cut at multiples of 2^this steps.
+constexpr int kQuantumShift = 1;
 
 // The workspace: parts' descriptions, their (maximum, sum), their outputs.
 struct ChunkWorkspace {
@@ -143,9 +143,9 @@ extern "C" int pkv_paged_attention_chunk(void *out, const void *query, const voi
     p.shape.tile_tokens = kChunkRows / group;
     p.shape.num_kv_heads = num_kv_heads;
     p.shape.causal = causal != 0;
-    p.shape.window = window;
+    p.shape.window = std::min(window, 1 << 30);  // no context is longer
     p.shape.overhead = kOverhead;
-    p.shape.quantum = kQuantum;
+    p.shape.quantum_shift = kQuantumShift;
     p.num_tokens = num_tokens;
     p.num_seqs = num_seqs;
     p.num_heads = num_heads;
@@ -172,7 +172,7 @@ extern "C" int pkv_paged_attention_chunk(void *out, const void *query, const voi
         return PKV_ERR_CUDA;
     }
     // No table is long enough for an item to be cut: nothing to join.
-    if ((int64_t)max_blocks_per_seq * block_size <= (int64_t)kQuantum * kChunkTile || num_ctas == 1) return PKV_OK;
+    if ((int64_t)max_blocks_per_seq * block_size <= ((int64_t)kChunkTile << kQuantumShift) || num_ctas == 1) return PKV_OK;
     fn = d64 ? reinterpret_cast<const void *>(&chunk_join_kernel<64>)
              : reinterpret_cast<const void *>(&chunk_join_kernel<128>);
     void *join_args[] = {&p, &num_ctas};

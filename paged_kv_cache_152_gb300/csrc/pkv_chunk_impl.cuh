@@ -95,8 +95,9 @@ struct ChunkPiece {
     int lo, hi;          // positions that some row sees
     int all_lo, all_hi;  // positions that every row sees
     int t0, t1;          // steps of this piece
+    int first[2], end[2];  // those a slot takes: first, first + stride, ... < end
     int partial;         // the part it writes, or -1
-    int single;          // one query tile: the slots take alternate steps
+    int single;          // one query tile: the slots take alternate steps (stride 2, else 1)
     int last;            // no piece: the end
     int odd;             // the guard cleared an element that was not finite
 };
@@ -139,8 +140,7 @@ __device__ __forceinline__ void regs_down() {
 // then leaves its loop, and the CTA reports the timeout at its end.  Kept
 // small, since it stands in many places: the roles' code has to share the
 // instruction cache.
-__device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, int *abort, uint32_t limit_ns) {
-    if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
+__device__ __forceinline__ bool chunk_wait_on(uint32_t bar, uint32_t parity, int *abort, uint32_t limit_ns) {
     const uint32_t t0 = (uint32_t)global_ns();
 #pragma unroll 1
     while (true) {
@@ -148,6 +148,11 @@ __device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, int *a
         if ((uint32_t)global_ns() - t0 > limit_ns) *(volatile int *)abort = 1;
         if (__any_sync(kFullMask, *(volatile int *)abort)) return false;
     }
+}
+
+__device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, int *abort, uint32_t limit_ns) {
+    if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
+    return chunk_wait_on(bar, parity, abort, limit_ns);
 }
 
 __device__ __noinline__ void chunk_report_range(int32_t *status) { report(status, PKV_ERR_OUT_OF_RANGE); }
@@ -172,31 +177,25 @@ __device__ __noinline__ int64_t chunk_units(const ChunkParams &p, int s, bool te
     *seq = chunk_load_seq(p, s, tell);
     return chunk_seq_units(p.shape, *seq);
 }
-__device__ __noinline__ void chunk_locate(const ChunkParams &p, const ChunkSeq &s, int64_t x, int *kv_head, int *item,
-                                          int64_t *offset) {
-    chunk_find(p.shape, s, x, kv_head, item, offset);
-}
-
-// The steps of a piece that a slot takes: first, first + stride, ... < end.
-__device__ __forceinline__ void chunk_slot_steps(const ChunkParams &p, const ChunkPiece &pc, int slot, int *first,
-                                                 int *end, int *stride) {
-    if (pc.single) {
-        *first = pc.t0 + slot;
-        *end = pc.t1;
-        *stride = 2;
-        if (*first > *end) *first = *end;
-        return;
-    }
-    *stride = 1;
-    const int a = slot * p.shape.tile_tokens, b = min(a + p.shape.tile_tokens, pc.tokens);
-    int lo = 0, hi = pc.len;
-    if (p.shape.causal) {
-        hi = chunk_clamp((int64_t)pc.pos0 + b, pc.len);
-        if (p.shape.window) lo = chunk_clamp((int64_t)pc.pos0 + a - p.shape.window + 1, hi);
-    }
-    *first = max(lo / kChunkTile, pc.t0);
-    *end = min((hi + kChunkTile - 1) / kChunkTile, pc.t1);
-    if (hi <= lo || *end < *first) *end = *first;
+// chunk_find by a whole warp: 32 candidates at a time.
+__device__ __noinline__ void chunk_locate(const ChunkParams &p, const ChunkSeq &s, int64_t x, int lane, int *kv_head,
+                                          int *item, int64_t *offset) {
+    const int items = chunk_items(p.shape, s);
+    const int64_t per_head = chunk_prefix(p.shape, s, items);
+    *kv_head = (int)(x / per_head);
+    x -= *kv_head * per_head;
+    int lo = 0, span = items;  // the item is in [lo, lo + span)
+    int64_t before = 0;
+    do {
+        const int step = (span + 31) / 32, i = lo + lane * step;
+        const int64_t at = i < items ? chunk_prefix(p.shape, s, i) : INT64_MAX;
+        const int who = 31 - __clz(__ballot_sync(kFullMask, lane * step < span && at <= x));
+        before = __shfl_sync(kFullMask, at, who);
+        lo += who * step;
+        span = min(step, items - lo);
+    } while (span > 1);
+    *item = lo;
+    *offset = x - before;
 }
 
 // Whether some row of the item does not see all of step t.
@@ -269,6 +268,14 @@ struct ChunkLoader {
 
     __device__ bool wait(uint64_t &bar, uint32_t parity) {
         return chunk_wait(smem_addr(&bar), parity, &ctl.abort, p.wait_limit_ns);
+    }
+
+    // The positions that row `token` of the item sees: [row_begin, row_end).
+    __device__ int row_end(const ChunkPiece &pc, int token) {
+        return p.shape.causal ? min(max(pc.pos0 + token + 1, 0), pc.len) : pc.len;
+    }
+    __device__ int row_begin(const ChunkPiece &pc, int token) {
+        return p.shape.window ? min(max(max(pc.pos0 + token, -1) - p.shape.window + 1, 0), pc.len) : 0;
     }
 
     // This lane's block of step t (-1: none of its positions is seen).
@@ -365,7 +372,7 @@ struct ChunkLoader {
         ChunkSeq q = chunk_load_seq(p, s, false);
         int head, item, items = chunk_items(c, q);
         int64_t off;
-        chunk_locate(p, q, u - cum, &head, &item, &off);
+        chunk_locate(p, q, u - cum, lane, &head, &item, &off);
         while (true) {
             ChunkPiece pc;
             const int w = 2 * c.tile_tokens;
@@ -387,8 +394,8 @@ struct ChunkLoader {
                 pc.all_lo = 0;
                 pc.all_hi = q.len;
                 if (c.causal) {
-                    pc.all_hi = chunk_clamp((int64_t)pc.pos0 + 1, q.len);
-                    if (c.window) pc.all_lo = chunk_clamp((int64_t)pc.pos0 + pc.tokens - c.window, q.len);
+                    pc.all_hi = row_end(pc, 0);
+                    if (c.window) pc.all_lo = row_begin(pc, pc.tokens - 1);
                 }
                 pc.t0 = first + a;
                 pc.t1 = first + b;
@@ -396,6 +403,19 @@ struct ChunkLoader {
                 pc.single = pc.tokens <= c.tile_tokens;
                 pc.last = 0;
                 pc.odd = 0;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (pc.single) {
+                        pc.first[k] = min(pc.t0 + k, pc.t1);
+                        pc.end[k] = pc.t1;
+                    } else {  // the steps that some row of the slot's tile sees
+                        const int r0 = k * c.tile_tokens, r1 = min(r0 + c.tile_tokens, pc.tokens) - 1;
+                        const int from = row_begin(pc, r0), to = row_end(pc, r1);
+                        pc.first[k] = max((int)((unsigned)from / kChunkTile), pc.t0);
+                        pc.end[k] = max(min((int)(((unsigned)to + kChunkTile - 1) / kChunkTile), pc.t1), pc.first[k]);
+                        if (to <= from) pc.end[k] = pc.first[k];
+                    }
+                }
                 if (b - a < steps) {
                     pc.partial = parts;
                     if (lane == 0) {
@@ -503,13 +523,9 @@ struct ChunkProducts {
         const int t0 = uniform(pc.t0), n = uniform(pc.t1) - t0, single = uniform(pc.single);
         if (n == 0) return true;
         const int all_lo = uniform(pc.all_lo), all_hi = uniform(pc.all_hi);
-        int first, end, stride;
-        chunk_slot_steps(p, pc, slot, &first, &end, &stride);
-        first = uniform(first) - t0;
-        end = uniform(end) - t0;
-        stride = single ? 2 : 1;
+        const int first = uniform(pc.first[slot]) - t0, end = uniform(pc.end[slot]) - t0, stride = single ? 2 : 1;
         auto takes = [&](int k) { return k >= first && k < end && (!single || ((k - first) & 1) == 0); };
-        const int last = first < end ? first + (end - 1 - first) / stride * stride : -1;
+        const int last = first < end ? (single ? end - 1 - (end - 1 - first & 1) : end - 1) : -1;
         // Queries: a tile of its own each, or the first buffer for both.
         const int buffer = single ? 0 : slot;
         if (!wait(ctl.q_full[0], q_uses[0] & 1)) return false;
@@ -669,26 +685,39 @@ struct ChunkSoftmax {
     __device__ uint32_t o_at(int s) { return tmem + 2 * kChunkTile + s * D; }
 
     // One step: scores -> weights, in place in tensor memory.
-    __device__ bool step(int col0, int row_lo, int row_hi, bool first) {
+    __device__ bool step(int col0, int row_lo, int row_hi, bool first, bool any) {
         if (!wait(ctl.s_full[slot], s_uses & 1)) return false;
         ++s_uses;
+        if (!any) {  // no row of this warp is one of the item's: their weights may be anything
+            arrive(ctl.p_full[slot]);
+            return true;
+        }
         tc_fence_after();
+        // Hidden positions become -inf in place first, where there are any: the
+        // common code then needs no mask.
+        const bool whole = row_hi < 0 || (row_lo <= col0 && col0 + kChunkTile <= row_hi);
+        if (!__all_sync(kFullMask, whole)) {
+            const unsigned n = (unsigned)max(row_hi - row_lo, 0);
+#pragma unroll 1
+            for (int c = 0; c < kChunkTile; c += 32) {
+                uint32_t x[32];
+                tmem_ld32(s_at() + c, x);
+                tmem_wait_ld();
+                tmem_pin32(x);
+                const int a = row_lo - col0 - c;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if ((unsigned)(i - a) >= n) x[i] = 0xff800000u;
+                tmem_st32(s_at() + c, x);
+            }
+            tmem_wait_st();
+        }
         uint32_t s[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_at() + c * 32, s[c]);
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_pin32(s[c]);
-        const bool whole = row_hi < 0 || (row_lo <= col0 && col0 + kChunkTile <= row_hi);
-        if (!__all_sync(kFullMask, whole)) {
-            const int a = row_lo - col0;
-            const unsigned n = (unsigned)max(row_hi - row_lo, 0);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if ((unsigned)(c * 32 + i - a) >= n) s[c][i] = 0xff800000u;  // -inf
-        }
         float top[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -705,7 +734,7 @@ struct ChunkSoftmax {
             l *= fade;
             const uint64_t fade2 = pack2(fade, fade);
             // the scores' arrival means every earlier product is complete, O's last one among them
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld32(o_at(slot) + c * 32, o);
@@ -765,8 +794,7 @@ struct ChunkSoftmax {
     }
 
     __device__ bool piece(const ChunkPiece &pc) {
-        int first, end, stride;
-        chunk_slot_steps(p, pc, slot, &first, &end, &stride);
+        const int first = pc.first[slot], end = pc.end[slot], stride = pc.single ? 2 : 1;
         const bool merge = pc.single && pc.t1 - pc.t0 > 1;
         // this thread's row: a token of the item and a query head
         const int token = row / p.group + (pc.single ? 0 : slot * p.shape.tile_tokens);
@@ -777,15 +805,17 @@ struct ChunkSoftmax {
         if (live) {
             row_hi = pc.len;
             if (p.shape.causal) {
-                const int64_t pos = (int64_t)pc.pos0 + token;
-                row_hi = chunk_clamp(pos + 1, pc.len);
-                if (p.shape.window) row_lo = chunk_clamp(pos - p.shape.window + 1, row_hi);
+                const int pos = max(pc.pos0 + token, -1);
+                row_hi = min(pos + 1, pc.len);
+                if (p.shape.window) row_lo = min(max(pos - p.shape.window + 1, 0), row_hi);
             }
         }
         m = -INFINITY;
         l = 0.f;
+        const bool any = __any_sync(kFullMask, live);
+#pragma unroll 1
         for (int t = first; t < end; t += stride)
-            if (!step(t * kChunkTile, row_lo, row_hi, t == first)) return false;
+            if (!step(t * kChunkTile, row_lo, row_hi, t == first, any)) return false;
 
         __half *out = p.out + ((int64_t)(pc.row0 + token) * p.num_heads + head) * D;
         const int64_t part_row = (int64_t)(2 * blockIdx.x + pc.partial) * p.part_rows + token * p.group + row % p.group;
@@ -799,8 +829,8 @@ struct ChunkSoftmax {
         if (!merge) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
             if (mine) {
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+                for (int c = 0; any && c < D / 32; ++c) {
                     uint32_t o[32];
                     tmem_ld32(o_at(slot) + c * 32, o);
                     tmem_wait_ld();
@@ -847,8 +877,8 @@ struct ChunkSoftmax {
         const float inv = pc.partial >= 0 ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
         const uint64_t fa2 = pack2(fa, fa), fb2 = pack2(fb, fb);
         const int c0 = slot * (D / 2);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
+#pragma unroll 1
+        for (int c = 0; any && c < D / 64; ++c) {
             uint32_t oa[32], ob[32];
             tmem_ld32(o_at(0) + c0 + c * 32, oa);
             tmem_ld32(o_at(1) + c0 + c * 32, ob);
@@ -975,7 +1005,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                 int run = who * 12;
                 while (cum + run_units[run] <= u) cum += run_units[run++];
                 s = run * per;
-                while (true) {
+                while (per > 1) {
                     const int64_t x = chunk_units(p, s, false, &seq);
                     if (cum + x > u) break;
                     cum += x;

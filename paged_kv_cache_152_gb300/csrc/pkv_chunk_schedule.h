@@ -38,7 +38,7 @@ struct ChunkShape {
     int causal;
     int window;        // 0: none
     int overhead;      // units of an item besides its positions, >= 1
-    int quantum;       // items are cut at multiples of this many steps
+    int quantum_shift; // items are cut at multiples of 2^this steps
 };
 
 struct ChunkSeq {
@@ -80,9 +80,9 @@ PKV_HD int64_t chunk_cost(const ChunkShape &c, const ChunkSeq &s, int64_t i) {
     return (int64_t)(hi - lo) + c.overhead;
 }
 
-// sum over k in [0, m) of max(a + k * w, 0)
+// sum over k in [0, m) of max(a + k * w, 0); a > -2^31, w <= 256
 PKV_HD int64_t chunk_ramp(int64_t a, int64_t w, int64_t m) {
-    const int64_t k0 = a >= 0 ? 0 : (-a + w - 1) / w;
+    const int64_t k0 = a >= 0 ? 0 : (int64_t)(((uint32_t)-a + (uint32_t)w - 1u) / (uint32_t)w);
     if (k0 >= m) return 0;
     const int64_t n = m - k0;
     return n * a + w * (n * (k0 + m - 1) / 2);
@@ -134,7 +134,7 @@ PKV_HD void chunk_find(const ChunkShape &c, const ChunkSeq &s, int64_t x, int *k
 }
 
 PKV_HD int chunk_steps(int lo, int hi) {
-    return hi > lo ? (hi + kChunkTile - 1) / kChunkTile - lo / kChunkTile : 0;
+    return hi > lo ? (int)(((unsigned)hi + kChunkTile - 1) / kChunkTile - (unsigned)lo / kChunkTile) : 0;
 }
 
 // How many of an item's steps lie before offset x of its units.  Not
@@ -145,9 +145,9 @@ PKV_HD int chunk_step_at(const ChunkShape &c, int lo, int hi, int64_t x) {
     if (x >= (int64_t)(hi - lo) + c.overhead) return steps;
     const int64_t y = x - c.overhead;
     if (y <= 0) return 0;
-    int t = (int)(y / kChunkTile) / c.quantum * c.quantum;
+    int t = (int)((unsigned)y / kChunkTile >> c.quantum_shift << c.quantum_shift);  // y < hi - lo
     if (t > steps) t = steps;
-    if (t > 0 && steps - t < c.quantum) t = steps;
+    if (t > 0 && steps - t < 1 << c.quantum_shift) t = steps;
     return t;
 }
 

@@ -133,7 +133,7 @@ int main() {
         c.causal = rnd(4) != 0;
         c.window = c.causal && rnd(2) ? 1 + (int)rnd(rnd(2) ? 700 : 20) : 0;
         c.overhead = 1 + (int)rnd(400);
-        c.quantum = 1 + (int)rnd(5);
+        c.quantum_shift = (int)rnd(4);
         std::vector<ChunkSeq> seqs;
         const int n = 1 + (int)rnd(7);
         int row = 0;
