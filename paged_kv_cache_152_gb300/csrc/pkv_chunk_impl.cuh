@@ -117,6 +117,7 @@ struct ChunkConfig {
         float2 ml[2][kChunkRows];
         uint32_t tmem;
         int abort;
+        int turn;  // the products' lock
     };
     static constexpr size_t kSmem = (size_t)(2 + kStages) * kTileBytes + sizeof(Control);
     static_assert(kSmem <= 232448, "shared memory");
@@ -488,13 +489,32 @@ struct ChunkProducts {
     const ChunkParams &p;
     typename Cfg::Control &ctl;
     uint32_t q_smem, ring_smem, s_tmem, o_tmem;
-    int slot;
+    int slot, lane;
     uint32_t ring = 0;          // ring position of the piece's first copy
     uint32_t q_uses[2] = {0, 0}, p_uses = 0, o_uses = 0, merges = 0;
     uint32_t guard_phase = 0;   // a bit per stage
 
     __device__ bool wait(uint64_t &bar, uint32_t parity) {
         return chunk_wait(smem_addr(&bar), parity, &ctl.abort, p.wait_limit_ns);
+    }
+
+    // The slots take turns at the tensor cores, a whole batch (O of a step, S of
+    // the next) at a time: run together, both slots would wait for both batches
+    // and then both do their softmax, with the tensor cores idle.
+    __device__ bool lock() {
+        const uint32_t t0 = (uint32_t)global_ns();
+#pragma unroll 1
+        while (true) {
+            int held = 1;
+            if (lane == 0) held = atomicExch(&ctl.turn, 1);
+            if (__any_sync(kFullMask, held == 0)) return true;
+            if ((uint32_t)global_ns() - t0 > p.wait_limit_ns) *(volatile int *)&ctl.abort = 1;
+            if (__any_sync(kFullMask, *(volatile int *)&ctl.abort)) return false;
+        }
+    }
+    __device__ void unlock() {
+        __syncwarp();
+        if (lane == 0) atomicExch(&ctl.turn, 0);
     }
 
     // S of the slot for step k of the piece, whose K is there.
@@ -542,8 +562,10 @@ struct ChunkProducts {
             const uint32_t v_at = ring + chunk_v_at(k, n), v_st = v_at % Cfg::kStages;
             const uint32_t k_at = ring + chunk_k_at(k + 1), k_st = k_at % Cfg::kStages;
             const bool edge = k >= 0 && ((t0 + k) * kChunkTile < all_lo || (t0 + k + 1) * kChunkTile > all_hi);
-            if (k >= 0 && takes(k)) {
-                // everything but P first, so that nothing stands between P and the products
+            // Everything but P first, so that nothing stands between P and the products.
+            const bool pv = k >= 0 && takes(k), qk = k + 1 < n && takes(k + 1);
+            if (k + 1 < n && !wait(ctl.full[k_st], k_at / Cfg::kStages & 1)) return false;
+            if (pv) {
                 if (!wait(ctl.full[v_st], v_at / Cfg::kStages & 1)) return false;
                 if (edge && !wait(ctl.guard[v_st], guard_phase >> v_st & 1)) return false;
                 if (k == first) {  // the previous piece's output has been read
@@ -553,22 +575,23 @@ struct ChunkProducts {
                 }
                 if (!wait(ctl.p_full[slot], p_uses & 1)) return false;
                 ++p_uses;
-                tc_fence_after();
-                weighted(v_st, k == first);
-                umma_commit(smem_addr(&ctl.empty[v_st]));
-                if (k == last) umma_commit(smem_addr(&ctl.o_full[slot]));
             }
-            if (k + 1 < n) {
-                if (!wait(ctl.full[k_st], k_at / Cfg::kStages & 1)) return false;
-                if (takes(k + 1)) {
-                    tc_fence_after();
+            if (pv || qk) {
+                if (!lock()) return false;
+                tc_fence_after();
+                if (pv) {
+                    weighted(v_st, k == first);
+                    umma_commit(smem_addr(&ctl.empty[v_st]));
+                    if (k == last) umma_commit(smem_addr(&ctl.o_full[slot]));
+                }
+                if (qk) {
                     scores(buffer, k_st);
                     umma_commit(smem_addr(&ctl.empty[k_st]));
                     if (k + 1 == last) umma_commit(smem_addr(&ctl.q_empty[buffer]));
-                } else {
-                    umma_arrive(smem_addr(&ctl.empty[k_st]));
                 }
+                unlock();
             }
+            if (k + 1 < n && !qk) umma_arrive(smem_addr(&ctl.empty[k_st]));
             if (k >= 0 && !takes(k)) {
                 if (!wait(ctl.full[v_st], v_at / Cfg::kStages & 1)) return false;
                 umma_arrive(smem_addr(&ctl.empty[v_st]));
@@ -597,6 +620,56 @@ struct ChunkProducts {
 // ---------------------------------------------------------------------------
 // warp 11: V in steps that not every row sees whole
 
+// Rows [a, b) of a tile, 4 rows of 128 bytes at a time, 16 bytes per lane.
+template <int D>
+__device__ __forceinline__ void guard_clear(unsigned char *tile, int a, int b, int lane) {
+#pragma unroll 1
+    for (int row = a + lane / 8; row < b; row += 4)
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+            *reinterpret_cast<uint4 *>(tile + h * ChunkConfig<D>::kHalfBytes + row * 128 + lane % 8 * 16) =
+                make_uint4(0, 0, 0, 0);
+}
+
+// Whether rows [a, b) hold an element that is not finite; those are cleared.
+// The magnitudes' maximum, which passes NaN on, finds them at an instruction
+// per two elements (rows past the end look at the last one again).
+template <int D>
+__device__ __forceinline__ bool guard_find(unsigned char *tile, int a, int b, int lane) {
+    if (a >= b) return false;
+    constexpr int kRows = D == 128 ? 4 : 8;  // 8 loads in flight
+    __half2 most[4] = {};
+#pragma unroll 1
+    for (int r0 = a + lane / 8; r0 < b; r0 += 4 * kRows) {
+        uint4 w[kRows][D / 64];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+                w[i][h] = *reinterpret_cast<const uint4 *>(tile + h * ChunkConfig<D>::kHalfBytes +
+                                                           min(r0 + 4 * i, b - 1) * 128 + lane % 8 * 16);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+                const __half2 *x = reinterpret_cast<const __half2 *>(&w[i][h]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) most[j] = __hmax2_nan(most[j], __habs2(x[j]));
+            }
+    }
+    const __half2 all = __hmax2_nan(__hmax2_nan(most[0], most[1]), __hmax2_nan(most[2], most[3]));
+    if (!__any_sync(kFullMask, odd_halves(*reinterpret_cast<const uint32_t *>(&all)))) return false;
+#pragma unroll 1
+    for (int row = a + lane / 8; row < b; row += 4)
+#pragma unroll 1
+        for (int h = 0; h < D / 64; ++h) {
+            uint4 *v = reinterpret_cast<uint4 *>(tile + h * ChunkConfig<D>::kHalfBytes + row * 128 + lane % 8 * 16);
+            const uint4 x = *v;
+            *v = make_uint4(clear_odd(x.x), clear_odd(x.y), clear_odd(x.z), clear_odd(x.w));
+        }
+    return true;
+}
+
 template <int D>
 __device__ void chunk_guard(const ChunkParams &p, typename ChunkConfig<D>::Control &ctl, unsigned char *ring, int lane) {
     using Cfg = ChunkConfig<D>;
@@ -616,40 +689,12 @@ __device__ void chunk_guard(const ChunkParams &p, typename ChunkConfig<D>::Contr
             // item, [all_lo, all_hi) by every one.
             const int at0 = t * kChunkTile;
             const int keep_lo = pc.lo - at0, keep_hi = pc.hi - at0, all_lo = pc.all_lo - at0, all_hi = pc.all_hi - at0;
-            bool odd = false;
-            // rows of 128 bytes, 4 at a time, 16 bytes per lane
-            unsigned char *base = ring + st * Cfg::kTileBytes + lane * 16;
-#pragma unroll 1
-            for (int i0 = 0; i0 < 32; i0 += 4) {
-                const int r0 = i0 * 4;
-                if (r0 >= keep_lo && r0 + 16 <= keep_hi && r0 >= all_lo && r0 + 16 <= all_hi) continue;
-                uint4 w[4][Cfg::kHalves];
-                bool look[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = r0 + i * 4 + lane / 8;
-                    const bool keep = row >= keep_lo && row < keep_hi;
-                    look[i] = keep && !(row >= all_lo && row < all_hi);
-#pragma unroll
-                    for (int h = 0; h < Cfg::kHalves; ++h) {
-                        uint4 *v = reinterpret_cast<uint4 *>(base + h * Cfg::kHalfBytes + (i0 + i) * 512);
-                        w[i][h] = make_uint4(0, 0, 0, 0);
-                        if (look[i]) w[i][h] = *v;
-                        if (!keep) *v = make_uint4(0, 0, 0, 0);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int h = 0; h < Cfg::kHalves; ++h) {
-                        uint4 &x = w[i][h];
-                        if (odd_halves(x.x) | odd_halves(x.y) | odd_halves(x.z) | odd_halves(x.w)) {
-                            odd = true;
-                            x = make_uint4(clear_odd(x.x), clear_odd(x.y), clear_odd(x.z), clear_odd(x.w));
-                            *reinterpret_cast<uint4 *>(base + h * Cfg::kHalfBytes + (i0 + i) * 512) = x;
-                        }
-                    }
-            }
+            unsigned char *tile = ring + st * Cfg::kTileBytes;
+            guard_clear<D>(tile, 0, min(keep_lo, kChunkTile), lane);
+            guard_clear<D>(tile, max(keep_hi, 0), kChunkTile, lane);
+            const int from = max(keep_lo, 0), to = min(keep_hi, kChunkTile);
+            bool odd = guard_find<D>(tile, from, min(all_lo, to), lane);
+            odd |= guard_find<D>(tile, max(max(all_hi, from), min(all_lo, to)), to, lane);
             if (odd) *(volatile int *)&pc.odd = 1;
             fence_proxy_async_smem();
             __syncwarp();
@@ -960,6 +1005,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             mbar_init(smem_addr(&ctl.piece_empty[i]), 11);  // all but the loader
         }
         ctl.abort = 0;
+        ctl.turn = 0;
         fence_barrier_init();
         prefetch_tensormap(&p.tmap_q);
         prefetch_tensormap(&p.tmap_k);
@@ -1022,7 +1068,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             const int slot = uniform(warp - 8);
             const uint32_t tmem = uniform(ctl.tmem);
             ChunkProducts<D> products{p, ctl, smem_addr(smem), smem_addr(ring), tmem + slot * kChunkTile,
-                                      tmem + 2 * kChunkTile + slot * D, slot};
+                                      tmem + 2 * kChunkTile + slot * D, slot, lane};
             products.run();
         }
     } else {
