@@ -46,6 +46,7 @@ namespace pkv {
 
 constexpr int kChunkThreads = 384;
 constexpr int kChunkRows = 128;   // rows of a query tile
+constexpr float kMostRise = 14.f;  // log2 of the largest weight
 constexpr int kChunkPieces = 4;   // piece descriptors in flight
 // Registers per thread: 384 at launch x 168 = 64512 = 256 x 208 + 128 x 88.
 constexpr int kChunkLaunchRegs = 168;
@@ -486,11 +487,24 @@ __device__ __forceinline__ int uniform(int x) { return (int)uniform((uint32_t)x)
 template <int D>
 struct ChunkProducts {
     using Cfg = ChunkConfig<D>;
+    // A place in the ring: its stage and the parity of that stage's use.
+    struct Place {
+        uint32_t st, phase;
+        __device__ void move(uint32_t by) {
+            st += by;
+            if (st >= Cfg::kStages) {
+                st -= Cfg::kStages;
+                phase ^= 1;
+            }
+        }
+    };
+
     const ChunkParams &p;
     typename Cfg::Control &ctl;
-    uint32_t q_smem, ring_smem, s_tmem, o_tmem;
+    uint32_t q_low, k_low, v_low;  // operand descriptors of the first buffers
+    uint32_t s_tmem, o_tmem;
     int slot, lane;
-    uint32_t ring = 0;          // ring position of the piece's first copy
+    Place ring = {0, 0};        // of the piece's first copy
     uint32_t q_uses[2] = {0, 0}, p_uses = 0, o_uses = 0, merges = 0;
     uint32_t guard_phase = 0;   // a bit per stage
 
@@ -501,13 +515,17 @@ struct ChunkProducts {
     // The slots take turns at the tensor cores, a whole batch (O of a step, S of
     // the next) at a time: run together, both slots would wait for both batches
     // and then both do their softmax, with the tensor cores idle.
+    __device__ bool take() {
+        int held = 1;
+        if (lane == 0) held = atomicExch(&ctl.turn, 1);
+        return __any_sync(kFullMask, held == 0);
+    }
     __device__ bool lock() {
+        if (take()) return true;
         const uint32_t t0 = (uint32_t)global_ns();
 #pragma unroll 1
         while (true) {
-            int held = 1;
-            if (lane == 0) held = atomicExch(&ctl.turn, 1);
-            if (__any_sync(kFullMask, held == 0)) return true;
+            if (take()) return true;
             if ((uint32_t)global_ns() - t0 > p.wait_limit_ns) *(volatile int *)&ctl.abort = 1;
             if (__any_sync(kFullMask, *(volatile int *)&ctl.abort)) return false;
         }
@@ -517,26 +535,15 @@ struct ChunkProducts {
         if (lane == 0) atomicExch(&ctl.turn, 0);
     }
 
-    // S of the slot for step k of the piece, whose K is there.
+    // S of the slot, whose K is there.
     __device__ void scores(uint32_t q_buffer, uint32_t st) {
-        const uint64_t a = umma_desc(q_smem + q_buffer * Cfg::kTileBytes, 16, 1024);
-        const uint64_t b = umma_desc(ring_smem + st * Cfg::kTileBytes, 16, 1024);
-        constexpr uint32_t idesc = umma_idesc_f16(128, kChunkTile, false);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            const uint32_t step = ((i / 4) * Cfg::kHalfBytes + (i % 4) * 32) >> 4;
-            umma_ss(s_tmem, a + step, b + step, idesc, i > 0);
-        }
-        umma_commit(smem_addr(&ctl.s_full[slot]));
+        umma_scores<D>(s_tmem, q_low + q_buffer * (Cfg::kTileBytes >> 4), k_low + st * (Cfg::kTileBytes >> 4),
+                       umma_idesc_f16(128, kChunkTile, false));
     }
 
     // O of the slot (+)= P V, where P and V are there.
     __device__ void weighted(uint32_t st, bool begins) {
-        const uint64_t b = umma_desc(ring_smem + st * Cfg::kTileBytes, Cfg::kHalfBytes, 1024);
-        constexpr uint32_t idesc = umma_idesc_f16(128, D, true);
-#pragma unroll
-        for (int i = 0; i < kChunkTile / 16; ++i)
-            umma_ts(o_tmem, s_tmem + i * 8, b + (i * 2048 >> 4), idesc, i > 0 || !begins);
+        umma_weighted(o_tmem, s_tmem, v_low + st * (Cfg::kTileBytes >> 4), umma_idesc_f16(128, D, true), !begins);
     }
 
     __device__ bool piece(const ChunkPiece &pc) {
@@ -557,16 +564,17 @@ struct ChunkProducts {
         // Both warps go through all copies of the piece and each frees every
         // stage, by a commit where it reads it and at once where it does not: O of
         // step k, then S of step k + 1 (which overwrites P of the slot's last step).
+        // Places: K of step k + 1 and V of step k (K0 K1 V0 K2 V1 ... from `ring` on).
+        Place kp = ring, vp = ring;
 #pragma unroll 1
         for (int k = -1; k < n; ++k) {
-            const uint32_t v_at = ring + chunk_v_at(k, n), v_st = v_at % Cfg::kStages;
-            const uint32_t k_at = ring + chunk_k_at(k + 1), k_st = k_at % Cfg::kStages;
+            const uint32_t k_st = kp.st, v_st = vp.st;
             const bool edge = k >= 0 && ((t0 + k) * kChunkTile < all_lo || (t0 + k + 1) * kChunkTile > all_hi);
             // Everything but P first, so that nothing stands between P and the products.
             const bool pv = k >= 0 && takes(k), qk = k + 1 < n && takes(k + 1);
-            if (k + 1 < n && !wait(ctl.full[k_st], k_at / Cfg::kStages & 1)) return false;
+            if (k + 1 < n && !wait(ctl.full[k_st], kp.phase)) return false;
             if (pv) {
-                if (!wait(ctl.full[v_st], v_at / Cfg::kStages & 1)) return false;
+                if (!wait(ctl.full[v_st], vp.phase)) return false;
                 if (edge && !wait(ctl.guard[v_st], guard_phase >> v_st & 1)) return false;
                 if (k == first) {  // the previous piece's output has been read
                     if (!wait(ctl.o_free[slot], (o_uses & 1) ^ 1)) return false;
@@ -579,27 +587,27 @@ struct ChunkProducts {
             if (pv || qk) {
                 if (!lock()) return false;
                 tc_fence_after();
-                if (pv) {
-                    weighted(v_st, k == first);
-                    umma_commit(smem_addr(&ctl.empty[v_st]));
-                    if (k == last) umma_commit(smem_addr(&ctl.o_full[slot]));
-                }
-                if (qk) {
-                    scores(buffer, k_st);
-                    umma_commit(smem_addr(&ctl.empty[k_st]));
-                    if (k + 1 == last) umma_commit(smem_addr(&ctl.q_empty[buffer]));
-                }
+                if (pv) weighted(v_st, k == first);
+                if (qk) scores(buffer, k_st);
+                // what a softmax waits for first
+                if (qk) umma_commit(smem_addr(&ctl.s_full[slot]));
+                if (pv && k == last) umma_commit(smem_addr(&ctl.o_full[slot]));
                 unlock();
+                if (pv) umma_commit(smem_addr(&ctl.empty[v_st]));
+                if (qk) umma_commit(smem_addr(&ctl.empty[k_st]));
+                if (qk && k + 1 == last) umma_commit(smem_addr(&ctl.q_empty[buffer]));
             }
             if (k + 1 < n && !qk) umma_arrive(smem_addr(&ctl.empty[k_st]));
             if (k >= 0 && !takes(k)) {
-                if (!wait(ctl.full[v_st], v_at / Cfg::kStages & 1)) return false;
+                if (!wait(ctl.full[v_st], vp.phase)) return false;
                 umma_arrive(smem_addr(&ctl.empty[v_st]));
             }
             if (edge) guard_phase ^= 1u << v_st;
+            kp.move(k < 0 ? 1 : 2);
+            vp.move(k + 2 >= n ? 1 : 2);
         }
         if (single && n > 1) ++merges;
-        ring += 2 * n;
+        ring = vp;
         return true;
     }
 
@@ -717,7 +725,7 @@ struct ChunkSoftmax {
     uint32_t tmem;  // with this warp's lanes
     int slot, row, lane;
     uint32_t s_uses = 0, o_uses = 0, merges = 0;
-    float m, l;     // running maximum (of unscaled scores) and sum
+    float m, l;     // what the weights are relative to (an unscaled score) and their sum
 
     __device__ bool wait(uint64_t &bar, uint32_t parity) {
         return chunk_wait(smem_addr(&bar), parity, &ctl.abort, p.wait_limit_ns);
@@ -726,6 +734,8 @@ struct ChunkSoftmax {
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&bar));
     }
+    // The maximum that a row's sum is relative to; none where it saw nothing.
+    __device__ float top() { return l == 0.f ? -INFINITY : m * p.scale_log2; }
     __device__ uint32_t s_at() { return tmem + slot * kChunkTile; }
     __device__ uint32_t o_at(int s) { return tmem + 2 * kChunkTile + s * D; }
 
@@ -757,66 +767,71 @@ struct ChunkSoftmax {
             }
             tmem_wait_st();
         }
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_at() + c * 32, s[c]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_pin32(s[c]);
-        float top[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            top[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-            for (int i = 1; i < 32; ++i) top[c] = fmaxf(top[c], __uint_as_float(s[c][i]));
-        }
-        const float next = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m);
-        // The maximum moves only when it rises by more than a factor 2^8 of the
-        // weights (fp16 carries weights up to 2^15), so O is seldom rescaled.
-        const bool move = first ? true : (next - m) * p.scale_log2 > 8.f;
-        if (!first && __any_sync(kFullMask, move)) {
-            const float fade = move ? ex2((m - next) * p.scale_log2) : 1.f;
-            l *= fade;
-            const uint64_t fade2 = pack2(fade, fade);
-            // the scores' arrival means every earlier product is complete, O's last one among them
+        // The weights are computed with the maximum as it stands while the step's own
+        // is found, so that neither waits for the other.  The maximum moves, and the
+        // step is done over, only when it rises by more than a factor 2^14 of the
+        // weights (fp16 carries them up to 2^15); a piece's first step guesses 0 and
+        // is done over unless the maximum lies in [0, 14], so that the largest
+        // weight of a row is never below 1.
+        uint32_t w[2][32];
+        float sum;
+        const float sc = p.scale_log2;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(o_at(slot) + c * 32, o);
-                tmem_wait_ld();
-                tmem_pin32(o);
+        for (bool again = false;; again = true) {
+            const float base = m == -INFINITY ? 0.f : -m * sc;
+            const uint64_t scale2 = pack2(sc, sc), base2 = pack2(base, base);
+            uint64_t sum2[2] = {};
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            uint32_t s[4][32];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float x, y;
-                    unpack2(mul2(pack2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), fade2), x, y);
-                    o[2 * i] = __float_as_uint(x);
-                    o[2 * i + 1] = __float_as_uint(y);
-                }
-                tmem_st32(o_at(slot) + c * 32, o);
-            }
-        }
-        if (move) m = next;
-        const float base = m == -INFINITY ? 0.f : -m * p.scale_log2;
-        const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), base2 = pack2(base, base);
-        uint64_t sum2 = pack2(0.f, 0.f);
+            for (int c = 0; c < 4; ++c) tmem_ld32(s_at() + c * 32, s[c]);
+            tmem_wait_ld();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t w[32];
+            for (int c = 0; c < 4; ++c) tmem_pin32(s[c]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const uint32_t *x = &s[2 * h + i / 16][2 * (i % 16)];
+            for (int i = 0; i < 64; ++i) {
+                const float x = __uint_as_float(s[i / 16][2 * (i % 16)]), y = __uint_as_float(s[i / 16][2 * (i % 16) + 1]);
+                top[i % 4] = fmaxf(top[i % 4], fmaxf(x, y));
                 float a, b;
-                unpack2(fma2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, base2), a, b);
+                unpack2(fma2(pack2(x, y), scale2, base2), a, b);
                 a = ex2(a);
                 b = ex2(b);
-                sum2 = add2(sum2, pack2(a, b));
-                w[i] = pack_half2(a, b);  // the second product's operand type; l sums the unrounded weights
+                sum2[i % 2] = add2(sum2[i % 2], pack2(a, b));
+                w[i / 32][i % 32] = pack_half2(a, b);  // the second product's operand type; the sum has the unrounded weights
             }
-            tmem_st32(s_at() + h * 32, w);
+            float x, y;
+            unpack2(add2(sum2[0], sum2[1]), x, y);
+            sum = x + y;
+            if (again) break;
+            const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), rise = (high - m) * sc;
+            const bool move = row_hi >= 0 && (first ? !(rise >= 0.f && rise <= kMostRise) : rise > kMostRise);
+            if (!__any_sync(kFullMask, move)) break;
+            const float next = first ? high : fmaxf(high, m);
+            if (!first) {
+                const float fade = move ? ex2((m - next) * sc) : 1.f;
+                l *= fade;
+                const uint64_t fade2 = pack2(fade, fade);
+                // the scores' arrival means every earlier product is complete, O's last one among them
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(o_at(slot) + c * 32, o);
+                    tmem_wait_ld();
+                    tmem_pin32(o);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        unpack2(mul2(pack2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), fade2), x, y);
+                        o[2 * i] = __float_as_uint(x);
+                        o[2 * i + 1] = __float_as_uint(y);
+                    }
+                    tmem_st32(o_at(slot) + c * 32, o);
+                }
+            }
+            if (move) m = next;
         }
-        float x, y;
-        unpack2(sum2, x, y);
-        l += x + y;
+        l += sum;
+        tmem_st32(s_at(), w[0]);
+        tmem_st32(s_at() + 32, w[1]);
         tmem_wait_st();
         tc_fence_before();
         arrive(ctl.p_full[slot]);
@@ -855,7 +870,7 @@ struct ChunkSoftmax {
                 if (p.shape.window) row_lo = min(max(pos - p.shape.window + 1, 0), row_hi);
             }
         }
-        m = -INFINITY;
+        m = 0.f;
         l = 0.f;
         const bool any = __any_sync(kFullMask, live);
 #pragma unroll 1
@@ -894,7 +909,7 @@ struct ChunkSoftmax {
                 for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
             }
             if (live) {
-                if (pc.partial >= 0) p.part_ml[part_row] = make_float2(m * p.scale_log2, l);
+                if (pc.partial >= 0) p.part_ml[part_row] = make_float2(top(), l);
                 if (pc.odd && mine) {
                     if (pc.partial < 0)
                         chunk_add_odd<D>(p, pc, row_lo, row_hi, out, 0, D);
@@ -908,7 +923,7 @@ struct ChunkSoftmax {
         // same rows, and a warp reads the other slot's O in its own lanes; each
         // writes half of the columns.
         if (!wait(ctl.x_empty, (merges & 1) ^ 1)) return false;
-        ctl.ml[slot][row] = make_float2(m * p.scale_log2, l);
+        ctl.ml[slot][row] = make_float2(top(), l);
         tc_fence_before();
         arrive(ctl.x_full);  // this slot's O is complete, too
         if (!wait(ctl.x_full, merges & 1)) return false;
@@ -916,7 +931,7 @@ struct ChunkSoftmax {
         ++merges;
         const float2 a = ctl.ml[0][row], b = ctl.ml[1][row];
         arrive(ctl.x_empty);
-        const float top = fmaxf(a.x, b.x), base = top == -INFINITY ? 0.f : top;
+        const float high = fmaxf(a.x, b.x), base = high == -INFINITY ? 0.f : high;
         const float fa = ex2(a.x - base), fb = ex2(b.x - base);
         const float sum = fa * a.y + fb * b.y;
         const float inv = pc.partial >= 0 ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
@@ -949,7 +964,7 @@ struct ChunkSoftmax {
         arrive(ctl.o_free[slot]);
         arrive(ctl.o_cross[1 - slot]);
         if (live) {
-            if (pc.partial >= 0 && slot == 0) p.part_ml[part_row] = make_float2(top, sum);
+            if (pc.partial >= 0 && slot == 0) p.part_ml[part_row] = make_float2(high, sum);
             if (pc.odd) {
                 if (pc.partial < 0)
                     chunk_add_odd<D>(p, pc, row_lo, row_hi, out, c0, D / 2);
@@ -1067,7 +1082,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         } else {
             const int slot = uniform(warp - 8);
             const uint32_t tmem = uniform(ctl.tmem);
-            ChunkProducts<D> products{p, ctl, smem_addr(smem), smem_addr(ring), tmem + slot * kChunkTile,
+            const uint32_t q = uniform(smem_addr(smem)), kv = uniform(smem_addr(ring));
+            ChunkProducts<D> products{p, ctl, umma_desc_low(q, 16), umma_desc_low(kv, 16),
+                                      umma_desc_low(kv, Cfg::kHalfBytes), tmem + slot * kChunkTile,
                                       tmem + 2 * kChunkTile + slot * D, slot, lane};
             products.run();
         }

@@ -20,13 +20,13 @@ __device__ __forceinline__ void tmem_free(uint32_t taddr, uint32_t columns) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(columns) : "memory");
 }
 
-// Shared-memory matrix descriptor of a 128-byte-swizzled tile: start address,
-// leading and stride byte offsets in units of 16 bytes, version 1 (bit 46),
-// swizzle mode 2 (bits 61-63).
-__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t leading_bytes, uint32_t stride_bytes) {
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(leading_bytes >> 4) << 16 |
-           (uint64_t)(stride_bytes >> 4) << 32 | UINT64_C(1) << 46 | UINT64_C(2) << 61;
+// Shared-memory matrix descriptor of a 128-byte-swizzled tile, its halves: the
+// start address and the leading byte offset in units of 16 bytes (low), the
+// stride byte offset, version 1 (bit 46) and swizzle mode 2 (bits 61-63) (high).
+__device__ __forceinline__ uint32_t umma_desc_low(uint32_t addr, uint32_t leading_bytes) {
+    return (addr & 0x3ffffu) >> 4 | (leading_bytes >> 4) << 16;
 }
+__host__ __device__ constexpr uint32_t umma_desc_high(uint32_t stride_bytes) { return stride_bytes >> 4 | 1u << 14 | 2u << 29; }
 
 // Instruction descriptor of kind::f16 with fp16 operands and fp32
 // accumulators: bit 4 the accumulator type, bit 16 set where B is stored with
@@ -35,28 +35,51 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(int m, int n, bool b_n_maj
     return 1u << 4 | (b_n_major ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (uint32_t)(m / 16) << 24;
 }
 
-// The products are issued by one thread, but called by a whole converged warp
-// with the same arguments: the descriptors then stay in uniform registers,
-// which the instruction reads (from inside a one-lane branch each product cost
-// 70 to 120 cycles to issue, more than it takes to compute).  The elected lane
-// is the same every time.
+// The products are issued by one elected lane, but called by a whole converged
+// warp with the same arguments, a chain of them in one statement: the
+// descriptors can then stay in uniform registers, which the instruction reads,
+// and the election is made once (from inside a one-lane branch each product
+// cost 70 to 120 cycles to issue, more than it takes to compute).
 
-// D (tensor memory) = A (shared) . B (shared) (+ D).
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
+#define PKV_MMA_HEAD                                                                                    \
+    "{\n\t.reg .pred p, e;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\telect.sync _|e, 0xffffffff;\n\t" \
+    "setp.ne.u32 p, %4, 0;\n\t"
+// One product of the chain at offsets XA, XB of the operands' low words; the first adds to D only if asked.
+#define PKV_MMA_SS(XA, XB, P)                                                              \
+    "add.u32 x, %1, " XA ";\n\tadd.u32 y, %2, " XB ";\n\t"                                \
+    "mov.b64 a, {x, %5};\n\tmov.b64 b, {y, %5};\n\t"                                     \
+    "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, " P ";\n\t"
+#define PKV_MMA_TS(XA, XB, P)                                                              \
+    "add.u32 x, %1, " XA ";\n\tadd.u32 y, %2, " XB ";\n\tmov.b64 b, {y, %5};\n\t"       \
+    "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, " P ";\n\t"
+
+// S (tensor memory) = Q (shared) . K^T (shared) over D = 64 or 128 dims, 16 at a
+// time: 32 bytes apart inside a half of 64 dims, halves 16 KB apart.
+template <int D>
+__device__ __forceinline__ void umma_scores(uint32_t s, uint32_t q, uint32_t k, uint32_t idesc) {
+    constexpr uint32_t high = umma_desc_high(1024);
+    if (D == 64)
+        asm volatile(PKV_MMA_HEAD PKV_MMA_SS("0", "0", "p") "setp.eq.u32 p, 0, 0;\n\t" PKV_MMA_SS("2", "2", "p")
+                         PKV_MMA_SS("4", "4", "p") PKV_MMA_SS("6", "6", "p") "}" ::"r"(s),
+                     "r"(q), "r"(k), "r"(idesc), "r"(0), "r"(high)
+                     : "memory");
+    else
+        asm volatile(PKV_MMA_HEAD PKV_MMA_SS("0", "0", "p") "setp.eq.u32 p, 0, 0;\n\t" PKV_MMA_SS("2", "2", "p")
+                         PKV_MMA_SS("4", "4", "p") PKV_MMA_SS("6", "6", "p") PKV_MMA_SS("1024", "1024", "p")
+                             PKV_MMA_SS("1026", "1026", "p") PKV_MMA_SS("1028", "1028", "p")
+                                 PKV_MMA_SS("1030", "1030", "p") "}" ::"r"(s),
+                     "r"(q), "r"(k), "r"(idesc), "r"(0), "r"(high)
+                     : "memory");
 }
 
-// D (tensor memory) = A (tensor memory) . B (shared) (+ D).
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
+// O (tensor memory) = P (tensor memory) . V (shared) (+ O) over 128 rows of V,
+// 16 at a time: 8 columns of P (fp16 pairs), 2048 bytes of V.
+__device__ __forceinline__ void umma_weighted(uint32_t o, uint32_t p, uint32_t v, uint32_t idesc, bool add) {
+    asm volatile(PKV_MMA_HEAD PKV_MMA_TS("0", "0", "p") "setp.eq.u32 p, 0, 0;\n\t" PKV_MMA_TS("8", "128", "p")
+                     PKV_MMA_TS("16", "256", "p") PKV_MMA_TS("24", "384", "p") PKV_MMA_TS("32", "512", "p")
+                         PKV_MMA_TS("40", "640", "p") PKV_MMA_TS("48", "768", "p") PKV_MMA_TS("56", "896", "p") "}" ::"r"(o),
+                 "r"(p), "r"(v), "r"(idesc), "r"((uint32_t)add), "r"(umma_desc_high(1024))
+                 : "memory");
 }
 
 // One arrival on the barrier once every product the elected lane has issued so
