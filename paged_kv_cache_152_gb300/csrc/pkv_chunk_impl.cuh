@@ -118,7 +118,7 @@ struct ChunkConfig {
         float2 ml[2][kChunkRows];
         uint32_t tmem;
         int abort;
-        int turn;  // the products' lock
+        uint32_t issued[2];  // batches of products, by slot
     };
     static constexpr size_t kSmem = (size_t)(2 + kStages) * kTileBytes + sizeof(Control);
     static_assert(kSmem <= 232448, "shared memory");
@@ -507,6 +507,7 @@ struct ChunkProducts {
     Place ring = {0, 0};        // of the piece's first copy
     uint32_t q_uses[2] = {0, 0}, p_uses = 0, o_uses = 0, merges = 0;
     uint32_t guard_phase = 0;   // a bit per stage
+    uint32_t mine = 0, theirs = 0;  // batches issued so far, by this slot and (up to the piece) by the other
 
     __device__ bool wait(uint64_t &bar, uint32_t parity) {
         return chunk_wait(smem_addr(&bar), parity, &ctl.abort, p.wait_limit_ns);
@@ -514,25 +515,18 @@ struct ChunkProducts {
 
     // The slots take turns at the tensor cores, a whole batch (O of a step, S of
     // the next) at a time: run together, both slots would wait for both batches
-    // and then both do their softmax, with the tensor cores idle.
-    __device__ bool take() {
-        int held = 1;
-        if (lane == 0) held = atomicExch(&ctl.turn, 1);
-        return __any_sync(kFullMask, held == 0);
-    }
-    __device__ bool lock() {
-        if (take()) return true;
+    // and then both do their softmax, with the tensor cores idle.  A slot waits
+    // until the other has issued so many batches in all.
+    __device__ bool turn(uint32_t batches) {
+        volatile uint32_t *issued = &ctl.issued[1 - slot];
+        if ((int)(*issued - batches) >= 0) return true;
         const uint32_t t0 = (uint32_t)global_ns();
 #pragma unroll 1
         while (true) {
-            if (take()) return true;
+            if (__all_sync(kFullMask, (int)(*issued - batches) >= 0)) return true;
             if ((uint32_t)global_ns() - t0 > p.wait_limit_ns) *(volatile int *)&ctl.abort = 1;
             if (__any_sync(kFullMask, *(volatile int *)&ctl.abort)) return false;
         }
-    }
-    __device__ void unlock() {
-        __syncwarp();
-        if (lane == 0) atomicExch(&ctl.turn, 0);
     }
 
     // S of the slot, whose K is there.
@@ -552,6 +546,10 @@ struct ChunkProducts {
         const int all_lo = uniform(pc.all_lo), all_hi = uniform(pc.all_hi);
         const int first = uniform(pc.first[slot]) - t0, end = uniform(pc.end[slot]) - t0, stride = single ? 2 : 1;
         auto takes = [&](int k) { return k >= first && k < end && (!single || ((k - first) & 1) == 0); };
+        const int other_first = uniform(pc.first[1 - slot]) - t0, other_end = uniform(pc.end[1 - slot]) - t0;
+        // The other slot's batches in this piece: S of its first step, then one per step.
+        const uint32_t other = other_first < other_end ? (other_end - other_first + stride - 1) / stride + 1 : 0;
+        uint32_t batch = 0;
         const int last = first < end ? (single ? end - 1 - (end - 1 - first & 1) : end - 1) : -1;
         // Queries: a tile of its own each, or the first buffer for both.
         const int buffer = single ? 0 : slot;
@@ -585,14 +583,17 @@ struct ChunkProducts {
                 ++p_uses;
             }
             if (pv || qk) {
-                if (!lock()) return false;
+                // slot 0's first batch, slot 1's first, slot 0's second ...
+                if (!turn(theirs + min(batch + slot, other))) return false;
+                ++batch;
                 tc_fence_after();
                 if (pv) weighted(v_st, k == first);
                 if (qk) scores(buffer, k_st);
                 // what a softmax waits for first
                 if (qk) umma_commit(smem_addr(&ctl.s_full[slot]));
                 if (pv && k == last) umma_commit(smem_addr(&ctl.o_full[slot]));
-                unlock();
+                ++mine;
+                if (lane == 0) *(volatile uint32_t *)&ctl.issued[slot] = mine;
                 if (pv) umma_commit(smem_addr(&ctl.empty[v_st]));
                 if (qk) umma_commit(smem_addr(&ctl.empty[k_st]));
                 if (qk && k + 1 == last) umma_commit(smem_addr(&ctl.q_empty[buffer]));
@@ -608,6 +609,7 @@ struct ChunkProducts {
         }
         if (single && n > 1) ++merges;
         ring = vp;
+        theirs += other;
         return true;
     }
 
@@ -1020,7 +1022,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             mbar_init(smem_addr(&ctl.piece_empty[i]), 11);  // all but the loader
         }
         ctl.abort = 0;
-        ctl.turn = 0;
+        ctl.issued[0] = ctl.issued[1] = 0;
         fence_barrier_init();
         prefetch_tensormap(&p.tmap_q);
         prefetch_tensormap(&p.tmap_k);
