@@ -23,6 +23,8 @@ bool shape_ok(int num_heads, int num_kv_heads, int head_dim) {
            num_heads / num_kv_heads <= kMaxGroup && (head_dim == 64 || head_dim == 128);
 }
 
+// Tries of a bounded device wait: one that fails takes 1.3 us (a suspended mbarrier try), so a second and more.
+constexpr uint32_t kWaitTries = 1u << 20;
 // Units of an item besides its positions: what a piece costs before its first
 // step (queries in, output out), in positions.
 constexpr int kOverhead = 256;
@@ -155,7 +157,7 @@ extern "C" int pkv_paged_attention_chunk(void *out, const void *query, const voi
     p.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : 7;
     p.part_rows = ws.part_rows;
     p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
-    p.wait_limit_ns = (uint32_t)kWaitLimitNs;
+    p.wait_tries = kWaitTries;
 
     const bool d64 = head_dim == 64;
     const void *fn = d64 ? reinterpret_cast<const void *>(&chunk_kernel<64>)

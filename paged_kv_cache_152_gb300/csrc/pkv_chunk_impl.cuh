@@ -36,6 +36,7 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "pkv_chunk_schedule.h"
@@ -83,7 +84,7 @@ struct ChunkParams {
     int block_shift;     // log2(block_size)
     int part_rows;
     float scale_log2;
-    uint32_t wait_limit_ns;
+    uint32_t wait_tries;
 };
 
 struct ChunkPiece {
@@ -102,6 +103,9 @@ struct ChunkPiece {
     int last;            // no piece: the end
     int odd;             // the guard cleared an element that was not finite
 };
+
+// Shared-memory address of a member of the control block at shared address `ctl_at`.
+#define PKV_CTL(member) (ctl_at + (uint32_t)offsetof(Control, member))
 
 template <int D>
 struct ChunkConfig {
@@ -137,24 +141,26 @@ __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// A bounded wait of a whole warp, which leaves together: false once it has run
-// out of time, or once any warp of the CTA has (the abort flag); every role
+// A bounded wait of a whole warp, which leaves together: false once it has
+// tried too often, or once any warp of the CTA has (the abort flag); every role
 // then leaves its loop, and the CTA reports the timeout at its end.  Kept
 // small, since it stands in many places: the roles' code has to share the
-// instruction cache.
-__device__ __forceinline__ bool chunk_wait_on(uint32_t bar, uint32_t parity, int *abort, uint32_t limit_ns) {
-    const uint32_t t0 = (uint32_t)global_ns();
+// instruction cache.  Addresses are those of shared memory.
+__device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t limit) {
 #pragma unroll 1
-    while (true) {
-        if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
-        if ((uint32_t)global_ns() - t0 > limit_ns) *(volatile int *)abort = 1;
-        if (__any_sync(kFullMask, *(volatile int *)abort)) return false;
+    for (uint32_t i = 0; !__all_sync(kFullMask, mbar_try_wait(bar, parity)); ++i) {
+        uint32_t gone;
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(gone) : "r"(abort) : "memory");
+        if (gone || i >= limit) {
+            asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1) : "memory");
+            return false;
+        }
     }
+    return true;
 }
 
-__device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, int *abort, uint32_t limit_ns) {
-    if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
-    return chunk_wait_on(bar, parity, abort, limit_ns);
+__device__ __noinline__ void chunk_drain(uint32_t bar, uint32_t parity) {
+    mbar_wait_bounded(bar, parity, kWaitLimitNs / 8);
 }
 
 __device__ __noinline__ void chunk_report_range(int32_t *status) { report(status, PKV_ERR_OUT_OF_RANGE); }
@@ -184,8 +190,15 @@ __device__ __noinline__ void chunk_locate(const ChunkParams &p, const ChunkSeq &
                                           int *item, int64_t *offset) {
     const int items = chunk_items(p.shape, s);
     const int64_t per_head = chunk_prefix(p.shape, s, items);
-    *kv_head = (int)(x / per_head);
-    x -= *kv_head * per_head;
+    int head = -1;  // the last one that begins at or before x
+    unsigned hits;
+    do {
+        const int h = head + 1 + lane;
+        hits = __ballot_sync(kFullMask, h < p.shape.num_kv_heads && h * per_head <= x);
+        head += __popc(hits);
+    } while (hits == kFullMask);
+    *kv_head = head;
+    x -= head * per_head;
     int lo = 0, span = items;  // the item is in [lo, lo + span)
     int64_t before = 0;
     do {
@@ -258,8 +271,10 @@ __device__ __noinline__ void chunk_add_odd(const ChunkParams &p, const ChunkPiec
 template <int D>
 struct ChunkLoader {
     using Cfg = ChunkConfig<D>;
+    using Control = typename Cfg::Control;
     const ChunkParams &p;
-    typename Cfg::Control &ctl;
+    Control &ctl;
+    uint32_t ctl_at;  // its shared-memory address
     uint32_t q_smem, ring_smem;
     int lane;
     uint32_t ring = 0;          // ring position of the next copy
@@ -268,9 +283,7 @@ struct ChunkLoader {
     uint32_t edge_phase = 0, edge_used = 0;  // bit per stage
     int parts = 0;
 
-    __device__ bool wait(uint64_t &bar, uint32_t parity) {
-        return chunk_wait(smem_addr(&bar), parity, &ctl.abort, p.wait_limit_ns);
-    }
+    __device__ bool wait(uint32_t bar, uint32_t parity) { return chunk_wait(bar, parity, PKV_CTL(abort), p.wait_tries); }
 
     // The positions that row `token` of the item sees: [row_begin, row_end).
     __device__ int row_end(const ChunkPiece &pc, int token) {
@@ -292,13 +305,13 @@ struct ChunkLoader {
     // (edge) lands on a barrier of its own, and the products wait for the guard.
     __device__ bool copy(const CUtensorMap *map, int blk, int kv_head, bool edge) {
         const uint32_t st = ring % Cfg::kStages;
-        if (!wait(ctl.empty[st], (ring / Cfg::kStages & 1) ^ 1)) return false;
+        if (!wait(PKV_CTL(empty) + 8 * st, (ring / Cfg::kStages & 1) ^ 1)) return false;
         ++ring;
-        const uint32_t bar = smem_addr(edge ? &ctl.edge[st] : &ctl.full[st]);
+        const uint32_t bar = (edge ? PKV_CTL(edge) : PKV_CTL(full)) + 8 * st;
         const unsigned live = __ballot_sync(kFullMask, blk >= 0);
         if (lane == 0) {
             mbar_arrive_expect_tx(bar, __popc(live) * ((uint32_t)D * 2 << p.block_shift));
-            if (edge) mbar_arrive(smem_addr(&ctl.full[st]));
+            if (edge) mbar_arrive(PKV_CTL(full) + 8 * st);
         }
         if (edge) {
             edge_phase ^= 1u << st;
@@ -316,11 +329,11 @@ struct ChunkLoader {
 
     __device__ bool emit(const ChunkPiece &pc) {
         const uint32_t slot = pieces % kChunkPieces;
-        if (!wait(ctl.piece_empty[slot], (pieces / kChunkPieces & 1) ^ 1)) return false;
+        if (!wait(PKV_CTL(piece_empty) + 8 * slot, (pieces / kChunkPieces & 1) ^ 1)) return false;
         ++pieces;
         if (lane == 0) {
             ctl.piece[slot] = pc;
-            mbar_arrive(smem_addr(&ctl.piece_full[slot]));
+            mbar_arrive(PKV_CTL(piece_full) + 8 * slot);
         }
         __syncwarp();
         return true;
@@ -330,10 +343,10 @@ struct ChunkLoader {
         const int n = pc.t1 - pc.t0;
         if (n == 0) return true;
         for (int b = 0; b < (pc.single ? 1 : 2); ++b) {
-            if (!wait(ctl.q_empty[b], (q_uses[b] & 1) ^ 1)) return false;
+            if (!wait(PKV_CTL(q_empty) + 8 * b, (q_uses[b] & 1) ^ 1)) return false;
             ++q_uses[b];
             if (lane == 0) {
-                const uint32_t bar = smem_addr(&ctl.q_full[b]);
+                const uint32_t bar = PKV_CTL(q_full) + 8 * b;
                 mbar_arrive_expect_tx(bar, (uint32_t)p.shape.tile_tokens * p.group * D * 2);
 #pragma unroll
                 for (int h = 0; h < Cfg::kHalves; ++h)
@@ -460,18 +473,15 @@ struct ChunkLoader {
         }
         // every copy has landed and every product that reads it is complete
         for (int i = 0; ok && i < Cfg::kStages; ++i, ++ring)
-            ok = wait(ctl.empty[ring % Cfg::kStages], (ring / Cfg::kStages & 1) ^ 1);
-        for (int b = 0; ok && b < 2; ++b) ok = wait(ctl.q_empty[b], (q_uses[b] & 1) ^ 1);
+            ok = wait(PKV_CTL(empty) + 8 * (ring % Cfg::kStages), (ring / Cfg::kStages & 1) ^ 1);
+        for (int b = 0; ok && b < 2; ++b) ok = wait(PKV_CTL(q_empty) + 8 * b, (q_uses[b] & 1) ^ 1);
         if (!ok) {  // gave up: only the copies in flight matter now
             for (uint32_t i = 1; i <= (uint32_t)Cfg::kStages && i <= ring; ++i)
-                mbar_wait_bounded(smem_addr(&ctl.full[(ring - i) % Cfg::kStages]),
-                                  (ring - i) / Cfg::kStages & 1, p.wait_limit_ns / 8);
+                chunk_drain(PKV_CTL(full) + 8 * ((ring - i) % Cfg::kStages), (ring - i) / Cfg::kStages & 1);
             for (int st = 0; st < Cfg::kStages; ++st)
-                if (edge_used >> st & 1)
-                    mbar_wait_bounded(smem_addr(&ctl.edge[st]), (edge_phase >> st & 1) ^ 1, p.wait_limit_ns / 8);
+                if (edge_used >> st & 1) chunk_drain(PKV_CTL(edge) + 8 * st, (edge_phase >> st & 1) ^ 1);
             for (int b = 0; b < 2; ++b)
-                if (q_uses[b])
-                    mbar_wait_bounded(smem_addr(&ctl.q_full[b]), (q_uses[b] - 1) & 1, p.wait_limit_ns / 8);
+                if (q_uses[b]) chunk_drain(PKV_CTL(q_full) + 8 * b, (q_uses[b] - 1) & 1);
         }
     }
 };
@@ -487,6 +497,7 @@ __device__ __forceinline__ int uniform(int x) { return (int)uniform((uint32_t)x)
 template <int D>
 struct ChunkProducts {
     using Cfg = ChunkConfig<D>;
+    using Control = typename Cfg::Control;
     // A place in the ring: its stage and the parity of that stage's use.
     struct Place {
         uint32_t st, phase;
@@ -500,7 +511,8 @@ struct ChunkProducts {
     };
 
     const ChunkParams &p;
-    typename Cfg::Control &ctl;
+    Control &ctl;
+    uint32_t ctl_at;  // its shared-memory address
     uint32_t q_low, k_low, v_low;  // operand descriptors of the first buffers
     uint32_t s_tmem, o_tmem;
     int slot, lane;
@@ -509,9 +521,7 @@ struct ChunkProducts {
     uint32_t guard_phase = 0;   // a bit per stage
     uint32_t mine = 0, theirs = 0;  // batches issued so far, by this slot and (up to the piece) by the other
 
-    __device__ bool wait(uint64_t &bar, uint32_t parity) {
-        return chunk_wait(smem_addr(&bar), parity, &ctl.abort, p.wait_limit_ns);
-    }
+    __device__ bool wait(uint32_t bar, uint32_t parity) { return chunk_wait(bar, parity, PKV_CTL(abort), p.wait_tries); }
 
     // The slots take turns at the tensor cores, a whole batch (O of a step, S of
     // the next) at a time: run together, both slots would wait for both batches
@@ -519,14 +529,15 @@ struct ChunkProducts {
     // until the other has issued so many batches in all.
     __device__ bool turn(uint32_t batches) {
         volatile uint32_t *issued = &ctl.issued[1 - slot];
-        if ((int)(*issued - batches) >= 0) return true;
-        const uint32_t t0 = (uint32_t)global_ns();
+        volatile int *abort = &ctl.abort;
 #pragma unroll 1
-        while (true) {
-            if (__all_sync(kFullMask, (int)(*issued - batches) >= 0)) return true;
-            if ((uint32_t)global_ns() - t0 > p.wait_limit_ns) *(volatile int *)&ctl.abort = 1;
-            if (__any_sync(kFullMask, *(volatile int *)&ctl.abort)) return false;
+        for (uint32_t i = 0; !__all_sync(kFullMask, (int)(*issued - batches) >= 0); ++i) {
+            if (*abort || i >= p.wait_tries) {
+                *abort = 1;
+                return false;
+            }
         }
+        return true;
     }
 
     // S of the slot, whose K is there.
@@ -553,12 +564,12 @@ struct ChunkProducts {
         const int last = first < end ? (single ? end - 1 - (end - 1 - first & 1) : end - 1) : -1;
         // Queries: a tile of its own each, or the first buffer for both.
         const int buffer = single ? 0 : slot;
-        if (!wait(ctl.q_full[0], q_uses[0] & 1)) return false;
-        if (buffer == 1 && !wait(ctl.q_full[1], q_uses[1] & 1)) return false;
+        if (!wait(PKV_CTL(q_full) + 8 * 0, q_uses[0] & 1)) return false;
+        if (buffer == 1 && !wait(PKV_CTL(q_full) + 8 * 1, q_uses[1] & 1)) return false;
         ++q_uses[0];
         if (!single) ++q_uses[1];
-        if (slot == 1 && !single) umma_arrive(smem_addr(&ctl.q_empty[0]));
-        if (first >= end) umma_arrive(smem_addr(&ctl.q_empty[buffer]));
+        if (slot == 1 && !single) umma_arrive(PKV_CTL(q_empty) + 8 * 0);
+        if (first >= end) umma_arrive(PKV_CTL(q_empty) + 8 * buffer);
         // Both warps go through all copies of the piece and each frees every
         // stage, by a commit where it reads it and at once where it does not: O of
         // step k, then S of step k + 1 (which overwrites P of the slot's last step).
@@ -570,16 +581,16 @@ struct ChunkProducts {
             const bool edge = k >= 0 && ((t0 + k) * kChunkTile < all_lo || (t0 + k + 1) * kChunkTile > all_hi);
             // Everything but P first, so that nothing stands between P and the products.
             const bool pv = k >= 0 && takes(k), qk = k + 1 < n && takes(k + 1);
-            if (k + 1 < n && !wait(ctl.full[k_st], kp.phase)) return false;
+            if (k + 1 < n && !wait(PKV_CTL(full) + 8 * k_st, kp.phase)) return false;
             if (pv) {
-                if (!wait(ctl.full[v_st], vp.phase)) return false;
-                if (edge && !wait(ctl.guard[v_st], guard_phase >> v_st & 1)) return false;
+                if (!wait(PKV_CTL(full) + 8 * v_st, vp.phase)) return false;
+                if (edge && !wait(PKV_CTL(guard) + 8 * v_st, guard_phase >> v_st & 1)) return false;
                 if (k == first) {  // the previous piece's output has been read
-                    if (!wait(ctl.o_free[slot], (o_uses & 1) ^ 1)) return false;
-                    if (!wait(ctl.o_cross[slot], (merges & 1) ^ 1)) return false;
+                    if (!wait(PKV_CTL(o_free) + 8 * slot, (o_uses & 1) ^ 1)) return false;
+                    if (!wait(PKV_CTL(o_cross) + 8 * slot, (merges & 1) ^ 1)) return false;
                     ++o_uses;
                 }
-                if (!wait(ctl.p_full[slot], p_uses & 1)) return false;
+                if (!wait(PKV_CTL(p_full) + 8 * slot, p_uses & 1)) return false;
                 ++p_uses;
             }
             if (pv || qk) {
@@ -590,18 +601,18 @@ struct ChunkProducts {
                 if (pv) weighted(v_st, k == first);
                 if (qk) scores(buffer, k_st);
                 // what a softmax waits for first
-                if (qk) umma_commit(smem_addr(&ctl.s_full[slot]));
-                if (pv && k == last) umma_commit(smem_addr(&ctl.o_full[slot]));
+                if (qk) umma_commit(PKV_CTL(s_full) + 8 * slot);
+                if (pv && k == last) umma_commit(PKV_CTL(o_full) + 8 * slot);
                 ++mine;
                 if (lane == 0) *(volatile uint32_t *)&ctl.issued[slot] = mine;
-                if (pv) umma_commit(smem_addr(&ctl.empty[v_st]));
-                if (qk) umma_commit(smem_addr(&ctl.empty[k_st]));
-                if (qk && k + 1 == last) umma_commit(smem_addr(&ctl.q_empty[buffer]));
+                if (pv) umma_commit(PKV_CTL(empty) + 8 * v_st);
+                if (qk) umma_commit(PKV_CTL(empty) + 8 * k_st);
+                if (qk && k + 1 == last) umma_commit(PKV_CTL(q_empty) + 8 * buffer);
             }
-            if (k + 1 < n && !qk) umma_arrive(smem_addr(&ctl.empty[k_st]));
+            if (k + 1 < n && !qk) umma_arrive(PKV_CTL(empty) + 8 * k_st);
             if (k >= 0 && !takes(k)) {
-                if (!wait(ctl.full[v_st], vp.phase)) return false;
-                umma_arrive(smem_addr(&ctl.empty[v_st]));
+                if (!wait(PKV_CTL(full) + 8 * v_st, vp.phase)) return false;
+                umma_arrive(PKV_CTL(empty) + 8 * v_st);
             }
             if (edge) guard_phase ^= 1u << v_st;
             kp.move(k < 0 ? 1 : 2);
@@ -614,16 +625,18 @@ struct ChunkProducts {
     }
 
     __device__ void run() {
-        for (uint32_t i = 0;; ++i) {
+        bool ok = wait(PKV_CTL(p_full) + 8 * slot, 0);  // the softmax's dry step is over
+        ++p_uses;
+        for (uint32_t i = 0; ok; ++i) {
             const uint32_t at = i % kChunkPieces;
-            if (!wait(ctl.piece_full[at], i / kChunkPieces & 1)) break;
+            if (!wait(PKV_CTL(piece_full) + 8 * at, i / kChunkPieces & 1)) break;
             const ChunkPiece &pc = ctl.piece[at];
             if (uniform(pc.last)) break;
             if (!piece(pc)) break;
-            umma_arrive(smem_addr(&ctl.piece_empty[at]));
+            umma_arrive(PKV_CTL(piece_empty) + 8 * at);
         }
-        umma_commit(smem_addr(&ctl.drain[slot]));
-        mbar_wait_bounded(smem_addr(&ctl.drain[slot]), 0, p.wait_limit_ns);
+        umma_commit(PKV_CTL(drain) + 8 * slot);
+        chunk_drain(PKV_CTL(drain) + 8 * slot, 0);
     }
 };
 
@@ -681,19 +694,21 @@ __device__ __forceinline__ bool guard_find(unsigned char *tile, int a, int b, in
 }
 
 template <int D>
-__device__ void chunk_guard(const ChunkParams &p, typename ChunkConfig<D>::Control &ctl, unsigned char *ring, int lane) {
+__device__ void chunk_guard(const ChunkParams &p, typename ChunkConfig<D>::Control &ctl, uint32_t ctl_at,
+                            unsigned char *ring, int lane) {
     using Cfg = ChunkConfig<D>;
+    using Control = typename Cfg::Control;
     uint32_t ring_at = 0, phase = 0;
     for (uint32_t k = 0;; ++k) {
         const uint32_t slot = k % kChunkPieces;
-        if (!chunk_wait(smem_addr(&ctl.piece_full[slot]), k / kChunkPieces & 1, &ctl.abort, p.wait_limit_ns)) return;
+        if (!chunk_wait(PKV_CTL(piece_full) + 8 * slot, k / kChunkPieces & 1, PKV_CTL(abort), p.wait_tries)) return;
         ChunkPiece &pc = ctl.piece[slot];
         if (pc.last) return;
         const int n = pc.t1 - pc.t0;
         for (int t = pc.t0; t < pc.t1; ++t) {
             if (!chunk_edge(pc, t)) continue;
             const uint32_t at = ring_at + chunk_v_at(t - pc.t0, n), st = at % Cfg::kStages;
-            if (!chunk_wait(smem_addr(&ctl.edge[st]), phase >> st & 1, &ctl.abort, p.wait_limit_ns)) return;
+            if (!chunk_wait(PKV_CTL(edge) + 8 * st, phase >> st & 1, PKV_CTL(abort), p.wait_tries)) return;
             phase ^= 1u << st;
             // Rows of this step: [keep_lo, keep_hi) are seen by some row of the
             // item, [all_lo, all_hi) by every one.
@@ -708,11 +723,11 @@ __device__ void chunk_guard(const ChunkParams &p, typename ChunkConfig<D>::Contr
             if (odd) *(volatile int *)&pc.odd = 1;
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&ctl.guard[st]));
+            if (lane == 0) mbar_arrive(PKV_CTL(guard) + 8 * st);
         }
         ring_at += 2 * n;
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&ctl.piece_empty[slot]));
+        if (lane == 0) mbar_arrive(PKV_CTL(piece_empty) + 8 * slot);
     }
 }
 
@@ -722,19 +737,19 @@ __device__ void chunk_guard(const ChunkParams &p, typename ChunkConfig<D>::Contr
 template <int D>
 struct ChunkSoftmax {
     using Cfg = ChunkConfig<D>;
+    using Control = typename Cfg::Control;
     const ChunkParams &p;
-    typename Cfg::Control &ctl;
+    Control &ctl;
+    uint32_t ctl_at;  // its shared-memory address
     uint32_t tmem;  // with this warp's lanes
     int slot, row, lane;
     uint32_t s_uses = 0, o_uses = 0, merges = 0;
     float m, l;     // what the weights are relative to (an unscaled score) and their sum
 
-    __device__ bool wait(uint64_t &bar, uint32_t parity) {
-        return chunk_wait(smem_addr(&bar), parity, &ctl.abort, p.wait_limit_ns);
-    }
-    __device__ void arrive(uint64_t &bar) {
+    __device__ bool wait(uint32_t bar, uint32_t parity) { return chunk_wait(bar, parity, PKV_CTL(abort), p.wait_tries); }
+    __device__ void arrive(uint32_t bar) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&bar));
+        if (lane == 0) mbar_arrive(bar);
     }
     // The maximum that a row's sum is relative to; none where it saw nothing.
     __device__ float top() { return l == 0.f ? -INFINITY : m * p.scale_log2; }
@@ -742,11 +757,14 @@ struct ChunkSoftmax {
     __device__ uint32_t o_at(int s) { return tmem + 2 * kChunkTile + s * D; }
 
     // One step: scores -> weights, in place in tensor memory.
-    __device__ bool step(int col0, int row_lo, int row_hi, bool first, bool any) {
-        if (!wait(ctl.s_full[slot], s_uses & 1)) return false;
-        ++s_uses;
+    // A dry step works on whatever is there and waits for nothing.
+    __device__ bool step(int col0, int row_lo, int row_hi, bool first, bool any, bool dry) {
+        if (!dry) {
+            if (!wait(PKV_CTL(s_full) + 8 * slot, s_uses & 1)) return false;
+            ++s_uses;
+        }
         if (!any) {  // no row of this warp is one of the item's: their weights may be anything
-            arrive(ctl.p_full[slot]);
+            arrive(PKV_CTL(p_full) + 8 * slot);
             return true;
         }
         tc_fence_after();
@@ -836,7 +854,7 @@ struct ChunkSoftmax {
         tmem_st32(s_at() + 32, w[1]);
         tmem_wait_st();
         tc_fence_before();
-        arrive(ctl.p_full[slot]);
+        arrive(PKV_CTL(p_full) + 8 * slot);
         return true;
     }
 
@@ -855,8 +873,11 @@ struct ChunkSoftmax {
             reinterpret_cast<uint4 *>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
     }
 
-    __device__ bool piece(const ChunkPiece &pc) {
-        const int first = pc.first[slot], end = pc.end[slot], stride = pc.single ? 2 : 1;
+    // The dry piece is one dry step: run while the schedule is being found, it
+    // brings the step's code, too long to be fetched while a score waits, into
+    // the instruction cache.
+    __device__ bool piece(const ChunkPiece &pc, bool dry) {
+        const int first = dry ? 0 : pc.first[slot], end = dry ? 1 : pc.end[slot], stride = pc.single ? 2 : 1;
         const bool merge = pc.single && pc.t1 - pc.t0 > 1;
         // this thread's row: a token of the item and a query head
         const int token = row / p.group + (pc.single ? 0 : slot * p.shape.tile_tokens);
@@ -872,19 +893,21 @@ struct ChunkSoftmax {
                 if (p.shape.window) row_lo = min(max(pos - p.shape.window + 1, 0), row_hi);
             }
         }
+        if (dry) row_lo = 0, row_hi = 1;  // with the mask
         m = 0.f;
         l = 0.f;
-        const bool any = __any_sync(kFullMask, live);
+        const bool any = dry || __any_sync(kFullMask, live);
 #pragma unroll 1
         for (int t = first; t < end; t += stride)
-            if (!step(t * kChunkTile, row_lo, row_hi, t == first, any)) return false;
+            if (!step(t * kChunkTile, row_lo, row_hi, t == first, any, dry)) return false;
+        if (dry) return true;
 
         __half *out = p.out + ((int64_t)(pc.row0 + token) * p.num_heads + head) * D;
         const int64_t part_row = (int64_t)(2 * blockIdx.x + pc.partial) * p.part_rows + token * p.group + row % p.group;
         float *part = p.part_o + part_row * D;
         const bool mine = first < end;
         if (mine) {
-            if (!wait(ctl.o_full[slot], o_uses & 1)) return false;
+            if (!wait(PKV_CTL(o_full) + 8 * slot, o_uses & 1)) return false;
             ++o_uses;
             tc_fence_after();
         }
@@ -905,7 +928,7 @@ struct ChunkSoftmax {
                     }
                 }
                 tc_fence_before();
-                arrive(ctl.o_free[slot]);
+                arrive(PKV_CTL(o_free) + 8 * slot);
             } else if (live && pc.partial < 0) {  // no step of the item is seen by this tile
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
@@ -924,15 +947,15 @@ struct ChunkSoftmax {
         // One tile, alternate steps: join the slots.  Both warpgroups hold the
         // same rows, and a warp reads the other slot's O in its own lanes; each
         // writes half of the columns.
-        if (!wait(ctl.x_empty, (merges & 1) ^ 1)) return false;
+        if (!wait(PKV_CTL(x_empty), (merges & 1) ^ 1)) return false;
         ctl.ml[slot][row] = make_float2(top(), l);
         tc_fence_before();
-        arrive(ctl.x_full);  // this slot's O is complete, too
-        if (!wait(ctl.x_full, merges & 1)) return false;
+        arrive(PKV_CTL(x_full));  // this slot's O is complete, too
+        if (!wait(PKV_CTL(x_full), merges & 1)) return false;
         tc_fence_after();
         ++merges;
         const float2 a = ctl.ml[0][row], b = ctl.ml[1][row];
-        arrive(ctl.x_empty);
+        arrive(PKV_CTL(x_empty));
         const float high = fmaxf(a.x, b.x), base = high == -INFINITY ? 0.f : high;
         const float fa = ex2(a.x - base), fb = ex2(b.x - base);
         const float sum = fa * a.y + fb * b.y;
@@ -963,8 +986,8 @@ struct ChunkSoftmax {
             }
         }
         tc_fence_before();
-        arrive(ctl.o_free[slot]);
-        arrive(ctl.o_cross[1 - slot]);
+        arrive(PKV_CTL(o_free) + 8 * slot);
+        arrive(PKV_CTL(o_cross) + 8 * (1 - slot));
         if (live) {
             if (pc.partial >= 0 && slot == 0) p.part_ml[part_row] = make_float2(high, sum);
             if (pc.odd) {
@@ -978,12 +1001,15 @@ struct ChunkSoftmax {
     }
 
     __device__ void run() {
-        for (uint32_t k = 0;; ++k) {
-            const uint32_t at = k % kChunkPieces;
-            if (!wait(ctl.piece_full[at], k / kChunkPieces & 1)) return;
+#pragma unroll 1
+        for (int k = -1;; ++k) {
+            const bool dry = k < 0;
+            const uint32_t at = dry ? 0 : k % kChunkPieces;
+            if (!dry && !wait(PKV_CTL(piece_full) + 8 * at, k / kChunkPieces & 1)) return;
             const ChunkPiece &pc = ctl.piece[at];
-            if (pc.last || !piece(pc)) return;
-            arrive(ctl.piece_empty[at]);
+            if (!dry && pc.last) return;
+            if (!piece(pc, dry)) return;
+            if (!dry) arrive(PKV_CTL(piece_empty) + 8 * at);
         }
     }
 };
@@ -996,6 +1022,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *ring = smem + 2 * Cfg::kTileBytes;
     typename Cfg::Control &ctl = *reinterpret_cast<typename Cfg::Control *>(ring + Cfg::kStages * Cfg::kTileBytes);
+    const uint32_t ctl_at = smem_addr(&ctl);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
     if (threadIdx.x == 0) {
@@ -1077,22 +1104,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             }
             __syncwarp();
             fence_proxy_async_smem();  // the ring's memory was read and written by ordinary accesses
-            ChunkLoader<D> loader{p, ctl, smem_addr(smem), smem_addr(ring), lane};
+            ChunkLoader<D> loader{p, ctl, ctl_at, smem_addr(smem), smem_addr(ring), lane};
             loader.run(s, cum, u, end);
         } else if (warp == 11) {
-            chunk_guard<D>(p, ctl, ring, lane);
+            chunk_guard<D>(p, ctl, ctl_at, ring, lane);
         } else {
             const int slot = uniform(warp - 8);
             const uint32_t tmem = uniform(ctl.tmem);
             const uint32_t q = uniform(smem_addr(smem)), kv = uniform(smem_addr(ring));
-            ChunkProducts<D> products{p, ctl, umma_desc_low(q, 16), umma_desc_low(kv, 16),
+            ChunkProducts<D> products{p, ctl, ctl_at, umma_desc_low(q, 16), umma_desc_low(kv, 16),
                                       umma_desc_low(kv, Cfg::kHalfBytes), tmem + slot * kChunkTile,
                                       tmem + 2 * kChunkTile + slot * D, slot, lane};
             products.run();
         }
     } else {
         regs_up<208>();
-        ChunkSoftmax<D> softmax{p, ctl, ctl.tmem + ((uint32_t)(warp % 4) << 21), warp / 4,
+        ChunkSoftmax<D> softmax{p, ctl, ctl_at, ctl.tmem + ((uint32_t)(warp % 4) << 21), warp / 4,
                                 (int)threadIdx.x % kChunkRows, lane};
         softmax.run();
     }
