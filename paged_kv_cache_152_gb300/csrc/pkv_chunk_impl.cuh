@@ -100,6 +100,7 @@ struct ChunkPiece {
     int first[2], end[2];  // those a slot takes: first, first + stride, ... < end
     int partial;         // the part it writes, or -1
     int single;          // one query tile: the slots take alternate steps (stride 2, else 1)
+    int q_buffer;        // of a lone tile's queries (two tiles take both buffers)
     int last;            // no piece: the end
     int odd;             // the guard cleared an element that was not finite
 };
@@ -279,9 +280,9 @@ struct ChunkLoader {
     int lane;
     uint32_t ring = 0;          // ring position of the next copy
     uint32_t pieces = 0;
-    uint32_t q_uses[2] = {0, 0};
+    uint32_t q_uses = 0, q_used = 0;         // a bit per buffer: phase, ever used
     uint32_t edge_phase = 0, edge_used = 0;  // bit per stage
-    int parts = 0;
+    int parts = 0, next_buffer = 0;
 
     __device__ bool wait(uint32_t bar, uint32_t parity) { return chunk_wait(bar, parity, PKV_CTL(abort), p.wait_tries); }
 
@@ -339,22 +340,29 @@ struct ChunkLoader {
         return true;
     }
 
-    __device__ bool load(const ChunkPiece &pc) {
-        const int n = pc.t1 - pc.t0;
-        if (n == 0) return true;
-        for (int b = 0; b < (pc.single ? 1 : 2); ++b) {
-            if (!wait(PKV_CTL(q_empty) + 8 * b, (q_uses[b] & 1) ^ 1)) return false;
-            ++q_uses[b];
+    __device__ bool load_queries(const ChunkPiece &pc) {
+#pragma unroll 1
+        for (int i = 0; i < (pc.single ? 1 : 2); ++i) {
+            const int b = pc.single ? pc.q_buffer : i;
+            if (!wait(PKV_CTL(q_empty) + 8 * b, (q_uses >> b & 1) ^ 1)) return false;
+            q_uses ^= 1u << b;
+            q_used |= 1u << b;
             if (lane == 0) {
                 const uint32_t bar = PKV_CTL(q_full) + 8 * b;
                 mbar_arrive_expect_tx(bar, (uint32_t)p.shape.tile_tokens * p.group * D * 2);
 #pragma unroll
                 for (int h = 0; h < Cfg::kHalves; ++h)
                     tma_load_3d(q_smem + b * Cfg::kTileBytes + h * Cfg::kHalfBytes, &p.tmap_q, h * 64,
-                                pc.kv_head * p.group, pc.row0 + b * p.shape.tile_tokens, bar);
+                                pc.kv_head * p.group, pc.row0 + i * p.shape.tile_tokens, bar);
             }
             __syncwarp();
         }
+        return true;
+    }
+
+    __device__ bool load(const ChunkPiece &pc) {
+        const int n = pc.t1 - pc.t0;
+        if (n == 0) return true;
         // The block table is read two steps ahead of the copies.
         int now = lookup(pc, pc.t0), next = n > 1 ? lookup(pc, pc.t0 + 1) : -1;
 #pragma unroll 1
@@ -362,6 +370,9 @@ struct ChunkLoader {
             const int ahead = t >= pc.t0 && t + 2 < pc.t1 ? lookup(pc, t + 2) : -1;
             if (t + 1 < pc.t1 && !copy(&p.tmap_k, t < pc.t0 ? now : next, pc.kv_head, false)) return false;
             if (t < pc.t0) continue;
+            // The queries only now: their buffer is free when the previous piece's
+            // last scores are done, and the first K can be on their way before.
+            if (t == pc.t0 && !load_queries(pc)) return false;
             if (!copy(&p.tmap_v, now, pc.kv_head, chunk_edge(pc, t))) return false;
             now = next;
             next = ahead;
@@ -417,6 +428,8 @@ struct ChunkLoader {
                 pc.partial = -1;
                 pc.single = pc.tokens <= c.tile_tokens;
                 pc.last = 0;
+                pc.q_buffer = next_buffer;  // the one that the last lone tile did not take
+                next_buffer ^= 1;
                 pc.odd = 0;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -474,14 +487,14 @@ struct ChunkLoader {
         // every copy has landed and every product that reads it is complete
         for (int i = 0; ok && i < Cfg::kStages; ++i, ++ring)
             ok = wait(PKV_CTL(empty) + 8 * (ring % Cfg::kStages), (ring / Cfg::kStages & 1) ^ 1);
-        for (int b = 0; ok && b < 2; ++b) ok = wait(PKV_CTL(q_empty) + 8 * b, (q_uses[b] & 1) ^ 1);
+        for (int b = 0; ok && b < 2; ++b) ok = wait(PKV_CTL(q_empty) + 8 * b, (q_uses >> b & 1) ^ 1);
         if (!ok) {  // gave up: only the copies in flight matter now
             for (uint32_t i = 1; i <= (uint32_t)Cfg::kStages && i <= ring; ++i)
                 chunk_drain(PKV_CTL(full) + 8 * ((ring - i) % Cfg::kStages), (ring - i) / Cfg::kStages & 1);
             for (int st = 0; st < Cfg::kStages; ++st)
                 if (edge_used >> st & 1) chunk_drain(PKV_CTL(edge) + 8 * st, (edge_phase >> st & 1) ^ 1);
             for (int b = 0; b < 2; ++b)
-                if (q_uses[b]) chunk_drain(PKV_CTL(q_full) + 8 * b, (q_uses[b] - 1) & 1);
+                if (q_used >> b & 1) chunk_drain(PKV_CTL(q_full) + 8 * b, (q_uses >> b & 1) ^ 1);
         }
     }
 };
@@ -517,7 +530,7 @@ struct ChunkProducts {
     uint32_t s_tmem, o_tmem;
     int slot, lane;
     Place ring = {0, 0};        // of the piece's first copy
-    uint32_t q_uses[2] = {0, 0}, p_uses = 0, o_uses = 0, merges = 0;
+    uint32_t q_uses = 0, p_uses = 0, o_uses = 0, merges = 0;  // q: a bit per buffer
     uint32_t guard_phase = 0;   // a bit per stage
     uint32_t mine = 0, theirs = 0;  // batches issued so far, by this slot and (up to the piece) by the other
 
@@ -562,14 +575,16 @@ struct ChunkProducts {
         const uint32_t other = other_first < other_end ? (other_end - other_first + stride - 1) / stride + 1 : 0;
         uint32_t batch = 0;
         const int last = first < end ? (single ? end - 1 - (end - 1 - first & 1) : end - 1) : -1;
-        // Queries: a tile of its own each, or the first buffer for both.
-        const int buffer = single ? 0 : slot;
-        if (!wait(PKV_CTL(q_full) + 8 * 0, q_uses[0] & 1)) return false;
-        if (buffer == 1 && !wait(PKV_CTL(q_full) + 8 * 1, q_uses[1] & 1)) return false;
-        ++q_uses[0];
-        if (!single) ++q_uses[1];
-        if (slot == 1 && !single) umma_arrive(PKV_CTL(q_empty) + 8 * 0);
-        if (first >= end) umma_arrive(PKV_CTL(q_empty) + 8 * buffer);
+        // Queries: a tile of its own each, or one tile for both.  Both warps see every
+        // use of a buffer and free it, by a commit behind their last S or at once.
+        const int lone = uniform(pc.q_buffer), buffer = single ? lone : slot;
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) {
+            if (single && b != lone) continue;
+            if (!wait(PKV_CTL(q_full) + 8 * b, q_uses >> b & 1)) return false;
+            q_uses ^= 1u << b;
+            if (b != buffer || first >= end) umma_arrive(PKV_CTL(q_empty) + 8 * b);
+        }
         // Both warps go through all copies of the piece and each frees every
         // stage, by a commit where it reads it and at once where it does not: O of
         // step k, then S of step k + 1 (which overwrites P of the slot's last step).
@@ -1034,7 +1049,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&ctl.q_full[i]), 1);
-            mbar_init(smem_addr(&ctl.q_empty[i]), i == 0 ? 2 : 1);  // the first buffer serves both slots of a lone tile
+            mbar_init(smem_addr(&ctl.q_empty[i]), 2);
             mbar_init(smem_addr(&ctl.s_full[i]), 1);
             mbar_init(smem_addr(&ctl.p_full[i]), 4);
             mbar_init(smem_addr(&ctl.o_full[i]), 1);
