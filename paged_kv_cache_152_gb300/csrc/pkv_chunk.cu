@@ -148,6 +148,7 @@ extern "C" int pkv_paged_attention_chunk(void *out, const void *query, const voi
     p.shape.window = std::min(window, 1 << 30);  // no context is longer
     p.shape.overhead = kOverhead;
     p.shape.quantum_shift = kQuantumShift;
+    p.fits_32 = chunk_fits_32(p.shape, num_tokens, num_seqs, (int64_t)max_blocks_per_seq * block_size);
     p.num_tokens = num_tokens;
     p.num_seqs = num_seqs;
     p.num_heads = num_heads;

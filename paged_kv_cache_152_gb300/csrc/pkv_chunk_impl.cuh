@@ -83,6 +83,7 @@ struct ChunkParams {
     int num_blocks;
     int block_shift;     // log2(block_size)
     int part_rows;
+    int fits_32;         // the schedule's line (chunk_fits_32)
     float scale_log2;
     uint32_t wait_tries;
 };
@@ -181,16 +182,20 @@ __device__ __forceinline__ ChunkSeq chunk_load_seq(const ChunkParams &p, int s, 
     return q;
 }
 
-// The schedule's closed forms, with their 64-bit divisions, once each.
-__device__ __noinline__ int64_t chunk_units(const ChunkParams &p, int s, bool tell, ChunkSeq *seq) {
-    *seq = chunk_load_seq(p, s, tell);
-    return chunk_seq_units(p.shape, *seq);
+// The schedule's closed forms, out of line: I = int32_t where the line fits it.
+template <typename I>
+__device__ __noinline__ int64_t chunk_units(const ChunkParams &p, const ChunkSeq &s) {
+    return chunk_seq_units<I>(p.shape, s);
 }
-// chunk_find by a whole warp: 32 candidates at a time.
-__device__ __noinline__ void chunk_locate(const ChunkParams &p, const ChunkSeq &s, int64_t x, int lane, int *kv_head,
-                                          int *item, int64_t *offset) {
+
+// The item of a sequence that holds unit x of its units, and x's offset in it,
+// by a whole warp: 32 candidates at a time.
+template <typename I>
+__device__ __noinline__ void chunk_locate(const ChunkParams &p, const ChunkSeq &s, int64_t unit, int lane, int *kv_head,
+                                          int *item, int *offset) {
     const int items = chunk_items(p.shape, s);
-    const int64_t per_head = chunk_prefix(p.shape, s, items);
+    const I per_head = chunk_prefix<I>(p.shape, s, items);
+    I x = (I)unit;
     int head = -1;  // the last one that begins at or before x
     unsigned hits;
     do {
@@ -201,17 +206,17 @@ __device__ __noinline__ void chunk_locate(const ChunkParams &p, const ChunkSeq &
     *kv_head = head;
     x -= head * per_head;
     int lo = 0, span = items;  // the item is in [lo, lo + span)
-    int64_t before = 0;
-    do {
+    I before = 0;
+    while (span > 1) {
         const int step = (span + 31) / 32, i = lo + lane * step;
-        const int64_t at = i < items ? chunk_prefix(p.shape, s, i) : INT64_MAX;
+        const I at = lane * step < span ? chunk_prefix<I>(p.shape, s, i) : 0;
         const int who = 31 - __clz(__ballot_sync(kFullMask, lane * step < span && at <= x));
         before = __shfl_sync(kFullMask, at, who);
         lo += who * step;
-        span = min(step, items - lo);
-    } while (span > 1);
+        span = min(step, span - who * step);
+    }
     *item = lo;
-    *offset = x - before;
+    *offset = (int)(x - before);
 }
 
 // Whether some row of the item does not see all of step t.
@@ -363,6 +368,7 @@ struct ChunkLoader {
     __device__ bool load(const ChunkPiece &pc) {
         const int n = pc.t1 - pc.t0;
         if (n == 0) return true;
+        if (pieces == 1 && !load_queries(pc)) return false;
         // The block table is read two steps ahead of the copies.
         int now = lookup(pc, pc.t0), next = n > 1 ? lookup(pc, pc.t0 + 1) : -1;
 #pragma unroll 1
@@ -370,9 +376,10 @@ struct ChunkLoader {
             const int ahead = t >= pc.t0 && t + 2 < pc.t1 ? lookup(pc, t + 2) : -1;
             if (t + 1 < pc.t1 && !copy(&p.tmap_k, t < pc.t0 ? now : next, pc.kv_head, false)) return false;
             if (t < pc.t0) continue;
-            // The queries only now: their buffer is free when the previous piece's
-            // last scores are done, and the first K can be on their way before.
-            if (t == pc.t0 && !load_queries(pc)) return false;
+            // The queries only now, but for the first piece: their buffer is free when
+            // the previous piece's last scores are done, and the first K can be on
+            // their way before.
+            if (t == pc.t0 && pieces > 1 && !load_queries(pc)) return false;
             if (!copy(&p.tmap_v, now, pc.kv_head, chunk_edge(pc, t))) return false;
             now = next;
             next = ahead;
@@ -396,16 +403,18 @@ struct ChunkLoader {
         if (u >= end) return true;
         const ChunkShape &c = p.shape;
         ChunkSeq q = chunk_load_seq(p, s, false);
-        int head, item, items = chunk_items(c, q);
-        int64_t off;
-        chunk_locate(p, q, u - cum, lane, &head, &item, &off);
+        int head, item, off, items = chunk_items(c, q);
+        if (p.fits_32)
+            chunk_locate<int32_t>(p, q, u - cum, lane, &head, &item, &off);
+        else
+            chunk_locate<int64_t>(p, q, u - cum, lane, &head, &item, &off);
         while (true) {
             ChunkPiece pc;
             const int w = 2 * c.tile_tokens;
             int lo, hi;
             chunk_item_range(c, q, item, &lo, &hi);
-            const int64_t cost = (int64_t)(hi - lo) + c.overhead;
-            const int64_t stop = chunk_min64(cost, off + (end - u));
+            const int cost = hi - lo + c.overhead;
+            const int stop = end - u < cost - off ? off + (int)(end - u) : cost;
             const int steps = chunk_steps(lo, hi), first = lo / kChunkTile;
             const int a = chunk_step_at(c, lo, hi, off), b = chunk_step_at(c, lo, hi, stop);
             if (b > a || (steps == 0 && off == 0)) {
@@ -640,13 +649,15 @@ struct ChunkProducts {
     }
 
     __device__ void run() {
-        bool ok = wait(PKV_CTL(p_full) + 8 * slot, 0);  // the softmax's dry step is over
-        ++p_uses;
-        for (uint32_t i = 0; ok; ++i) {
+        for (uint32_t i = 0;; ++i) {
             const uint32_t at = i % kChunkPieces;
             if (!wait(PKV_CTL(piece_full) + 8 * at, i / kChunkPieces & 1)) break;
             const ChunkPiece &pc = ctl.piece[at];
             if (uniform(pc.last)) break;
+            if (i == 0) {  // the softmax's dry step is over
+                if (!wait(PKV_CTL(p_full) + 8 * slot, 0)) break;
+                ++p_uses;
+            }
             if (!piece(pc)) break;
             umma_arrive(PKV_CTL(piece_empty) + 8 * at);
         }
@@ -888,8 +899,8 @@ struct ChunkSoftmax {
             reinterpret_cast<uint4 *>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
     }
 
-    // The dry piece is one dry step: run while the schedule is being found, it
-    // brings the step's code, too long to be fetched while a score waits, into
+    // The dry piece is one dry step: run while the first copies are on their way,
+    // it brings the step's code, too long to be fetched while a score waits, into
     // the instruction cache.
     __device__ bool piece(const ChunkPiece &pc, bool dry) {
         const int first = dry ? 0 : pc.first[slot], end = dry ? 1 : pc.end[slot], stride = pc.single ? 2 : 1;
@@ -1020,9 +1031,9 @@ struct ChunkSoftmax {
         for (int k = -1;; ++k) {
             const bool dry = k < 0;
             const uint32_t at = dry ? 0 : k % kChunkPieces;
-            if (!dry && !wait(PKV_CTL(piece_full) + 8 * at, k / kChunkPieces & 1)) return;
+            if (!wait(PKV_CTL(piece_full) + 8 * at, dry ? 0 : k / kChunkPieces & 1)) return;
             const ChunkPiece &pc = ctl.piece[at];
-            if (!dry && pc.last) return;
+            if (pc.last) return;
             if (!piece(pc, dry)) return;
             if (!dry) arrive(PKV_CTL(piece_empty) + 8 * at);
         }
@@ -1080,9 +1091,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     int64_t *run_units = reinterpret_cast<int64_t *>(ring);
     const int per = (p.num_seqs + kChunkThreads - 1) / kChunkThreads;
     int64_t units = 0;
-    ChunkSeq seq;
-    for (int s = threadIdx.x * per; s < min((int)(threadIdx.x + 1) * per, p.num_seqs); ++s)
-        units += chunk_units(p, s, blockIdx.x == 0, &seq);
+    for (int s = threadIdx.x * per; s < min((int)(threadIdx.x + 1) * per, p.num_seqs); ++s) {
+        const ChunkSeq seq = chunk_load_seq(p, s, blockIdx.x == 0);
+        units += p.fits_32 ? chunk_units<int32_t>(p, seq) : chunk_units<int64_t>(p, seq);
+    }
     run_units[threadIdx.x] = units;
     tc_fence_before();
     __syncthreads();
@@ -1111,7 +1123,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                 while (cum + run_units[run] <= u) cum += run_units[run++];
                 s = run * per;
                 while (per > 1) {
-                    const int64_t x = chunk_units(p, s, false, &seq);
+                    const ChunkSeq seq = chunk_load_seq(p, s, false);
+                    const int64_t x = p.fits_32 ? chunk_units<int32_t>(p, seq) : chunk_units<int64_t>(p, seq);
                     if (cum + x > u) break;
                     cum += x;
                     ++s;

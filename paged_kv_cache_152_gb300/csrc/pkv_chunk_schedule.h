@@ -55,82 +55,82 @@ PKV_HD int chunk_items(const ChunkShape &c, const ChunkSeq &s) {
     return (int)(((int64_t)s.n + w - 1) / w);
 }
 
-// The positions that some of rows [r0, r1) of a sequence see.
-PKV_HD void chunk_range(const ChunkShape &c, const ChunkSeq &s, int64_t r0, int64_t r1, int *lo, int *hi) {
-    if (!c.causal) {
-        *lo = 0;
-        *hi = s.len;
-        return;
-    }
-    const int64_t base = (int64_t)s.len - s.n;
-    const int64_t h = chunk_min64(chunk_max64(base + r1, 0), s.len);
-    const int64_t l = c.window ? chunk_max64(base + r0 - c.window + 1, 0) : 0;
-    *hi = (int)h;
-    *lo = (int)chunk_min64(l, h);
-}
+// The positions that some row of item i sees.
+PKV_HD int chunk_min(int a, int b) { return a < b ? a : b; }
+PKV_HD int chunk_max(int a, int b) { return a > b ? a : b; }
 
 PKV_HD void chunk_item_range(const ChunkShape &c, const ChunkSeq &s, int64_t i, int *lo, int *hi) {
-    const int64_t w = 2 * (int64_t)c.tile_tokens;
-    chunk_range(c, s, i * w, chunk_min64((i + 1) * w, s.n), lo, hi);
+    *lo = 0;
+    *hi = s.len;
+    if (!c.causal) return;
+    const int w = 2 * c.tile_tokens, r0 = (int)(i * w);          // below s.n
+    const int r1 = s.n - r0 < w ? s.n : r0 + w;
+    const int base = s.len - s.n;                                 // above -2^31
+    *hi = chunk_min(chunk_max(base + r1, 0), s.len);
+    if (c.window) *lo = chunk_min(chunk_max(chunk_max(base + r0, -1) - c.window + 1, 0), *hi);
 }
 
-PKV_HD int64_t chunk_cost(const ChunkShape &c, const ChunkSeq &s, int64_t i) {
+// Units of item i (below 2^31: no context is longer than 2^30).
+PKV_HD int chunk_cost(const ChunkShape &c, const ChunkSeq &s, int64_t i) {
     int lo, hi;
     chunk_item_range(c, s, i, &lo, &hi);
-    return (int64_t)(hi - lo) + c.overhead;
+    return hi - lo + c.overhead;
 }
 
 // sum over k in [0, m) of max(a + k * w, 0); a > -2^31, w <= 256
-PKV_HD int64_t chunk_ramp(int64_t a, int64_t w, int64_t m) {
-    const int64_t k0 = a >= 0 ? 0 : (int64_t)(((uint32_t)-a + (uint32_t)w - 1u) / (uint32_t)w);
+template <typename I>
+PKV_HD I chunk_ramp(I a, int w, I m) {
+    const I k0 = a >= 0 ? 0 : (I)(((uint32_t)-a + (uint32_t)w - 1u) / (uint32_t)w);
     if (k0 >= m) return 0;
-    const int64_t n = m - k0;
+    const I n = m - k0;
     return n * a + w * (n * (k0 + m - 1) / 2);
 }
 
 // Units of a sequence's first i items of one KV head, 0 <= i <= chunk_items.
-PKV_HD int64_t chunk_prefix(const ChunkShape &c, const ChunkSeq &s, int64_t i) {
-    const int64_t items = chunk_items(c, s);
+// I is int32_t where chunk_fits_32 (the usual case, and a third of the
+// instructions), else int64_t.
+template <typename I>
+PKV_HD I chunk_prefix(const ChunkShape &c, const ChunkSeq &s, I i) {
+    const I items = chunk_items(c, s);
     if (i == 0) return 0;
-    if (!c.causal) return i * ((int64_t)s.len + c.overhead);
-    const int64_t w = 2 * (int64_t)c.tile_tokens, base = (int64_t)s.len - s.n;
-    const int64_t m = i < items ? i : items - 1;  // items that end at a whole tile pair
-    int64_t sum = m * c.overhead + chunk_ramp(base + w, w, m);
-    if (c.window) sum -= chunk_ramp(base - c.window + 1, w, m);
+    if (!c.causal) return i * ((I)s.len + c.overhead);
+    const int w = 2 * c.tile_tokens;
+    const I base = (I)s.len - s.n;
+    const I m = i < items ? i : items - 1;  // items that end at a whole tile pair
+    I sum = m * c.overhead + chunk_ramp<I>(base + w, w, m);
+    if (c.window) sum -= chunk_ramp<I>(base - c.window + 1, w, m);
     if (i == items) sum += chunk_cost(c, s, items - 1);
     return sum;
 }
 
+template <typename I>
 PKV_HD int64_t chunk_seq_units(const ChunkShape &c, const ChunkSeq &s) {
     if (s.n <= 0) return 0;
-    const int64_t per_head = chunk_prefix(c, s, chunk_items(c, s));
-    return per_head > kChunkMaxSeqUnits / c.num_kv_heads ? kChunkMaxSeqUnits : per_head * c.num_kv_heads;
+    const I per_head = chunk_prefix<I>(c, s, chunk_items(c, s));
+    if (sizeof(I) == 4) return per_head * c.num_kv_heads;
+    return per_head > kChunkMaxSeqUnits / c.num_kv_heads ? kChunkMaxSeqUnits : (int64_t)per_head * c.num_kv_heads;
+}
+
+// Whether a line of num_tokens rows and num_seqs sequences, none longer than
+// longest, is surely so short (2^29 units) that nothing the closed form computes
+// on the way leaves 32 bits either.
+PKV_HD bool chunk_fits_32(const ChunkShape &c, int num_tokens, int num_seqs, int64_t longest) {
+    const int64_t items = num_tokens / (2 * c.tile_tokens) + (int64_t)num_seqs;
+    const int64_t each = longest + c.overhead;
+    return num_tokens < (1 << 29) && c.window <= (1 << 30) && items < (INT64_C(1) << 29) / each / c.num_kv_heads;
 }
 
 // Where share k of `shares` starts on a line of `total` units.
 PKV_HD int64_t chunk_share(int64_t total, int shares, int k) {
-    const int64_t q = total / shares, r = total % shares;
-    return q * k + (k < r ? k : r);
-}
-
-// The item of a sequence that holds unit x (0 <= x < its units) and the offset
-// of x in it.
-PKV_HD void chunk_find(const ChunkShape &c, const ChunkSeq &s, int64_t x, int *kv_head, int *item, int64_t *offset) {
-    const int items = chunk_items(c, s);
-    const int64_t per_head = chunk_prefix(c, s, items);
-    const int64_t h = x / per_head;
-    x -= h * per_head;
-    int a = 0, b = items - 1;  // the largest a with prefix(a) <= x
-    while (a < b) {
-        const int mid = (int)(((int64_t)a + b + 1) / 2);
-        if (chunk_prefix(c, s, mid) <= x)
-            a = mid;
-        else
-            b = mid - 1;
+    int64_t q, r;
+    if (total >> 32 == 0) {
+        q = (uint32_t)total / (uint32_t)shares;
+        r = (uint32_t)total % (uint32_t)shares;
+    } else {
+        q = total / shares;
+        r = total % shares;
     }
-    *kv_head = (int)h;
-    *item = a;
-    *offset = x - chunk_prefix(c, s, a);
+    return q * k + (k < r ? k : r);
 }
 
 PKV_HD int chunk_steps(int lo, int hi) {
@@ -140,10 +140,10 @@ PKV_HD int chunk_steps(int lo, int hi) {
 // How many of an item's steps lie before offset x of its units.  Not
 // decreasing in x, 0 at 0 and all of them at the item's cost, so the pieces
 // [step_at(a), step_at(b)) of consecutive offsets partition the steps.
-PKV_HD int chunk_step_at(const ChunkShape &c, int lo, int hi, int64_t x) {
+PKV_HD int chunk_step_at(const ChunkShape &c, int lo, int hi, int x) {
     const int steps = chunk_steps(lo, hi);
-    if (x >= (int64_t)(hi - lo) + c.overhead) return steps;
-    const int64_t y = x - c.overhead;
+    if (x >= hi - lo + c.overhead) return steps;
+    const int y = x - c.overhead;
     if (y <= 0) return 0;
     int t = (int)((unsigned)y / kChunkTile >> c.quantum_shift << c.quantum_shift);  // y < hi - lo
     if (t > steps) t = steps;

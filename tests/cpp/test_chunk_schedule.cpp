@@ -39,6 +39,19 @@ static void row_range(const ChunkShape &c, const ChunkSeq &s, int r, int *lo, in
     if (c.window && p - c.window + 1 > 0) *lo = p - c.window + 1;
 }
 
+// The item of a sequence that holds unit x (0 <= x < its units) and the offset of x in it.
+template <typename I>
+static void find(const ChunkShape &c, const ChunkSeq &s, int64_t x, int *head, int *item, int64_t *offset) {
+    const I per_head = chunk_prefix<I>(c, s, chunk_items(c, s));
+    *head = (int)(x / per_head);
+    x -= (int64_t)*head * per_head;
+    int i = 0;
+    while (i + 1 < chunk_items(c, s) && chunk_prefix<I>(c, s, i + 1) <= x) ++i;
+    *item = i;
+    *offset = x - chunk_prefix<I>(c, s, i);
+}
+
+template <typename I>
 static void check(const ChunkShape &c, const std::vector<ChunkSeq> &seqs, int shares) {
     int64_t total = 0;
     std::vector<int64_t> cum(1, 0);
@@ -46,7 +59,7 @@ static void check(const ChunkShape &c, const std::vector<ChunkSeq> &seqs, int sh
         const int items = s.n > 0 ? chunk_items(c, s) : 0;
         int64_t sum = 0;
         for (int i = 0; i < items; ++i) {
-            CHECK(chunk_prefix(c, s, i) == sum);
+            CHECK(chunk_prefix<I>(c, s, i) == sum);
             int lo, hi, first = 1 << 30, last = 0;
             chunk_item_range(c, s, i, &lo, &hi);
             const int w = 2 * c.tile_tokens;
@@ -65,8 +78,8 @@ static void check(const ChunkShape &c, const std::vector<ChunkSeq> &seqs, int sh
             CHECK(chunk_cost(c, s, i) == hi - lo + c.overhead);
             sum += chunk_cost(c, s, i);
         }
-        if (items) CHECK(chunk_prefix(c, s, items) == sum);
-        CHECK(chunk_seq_units(c, s) == sum * c.num_kv_heads);
+        if (items) CHECK(chunk_prefix<I>(c, s, items) == sum);
+        CHECK(chunk_seq_units<I>(c, s) == sum * c.num_kv_heads);
         total += sum * c.num_kv_heads;
         cum.push_back(total);
     }
@@ -83,7 +96,7 @@ static void check(const ChunkShape &c, const std::vector<ChunkSeq> &seqs, int sh
         if (u >= end) continue;
         int head, item;
         int64_t off;
-        chunk_find(c, seqs[s], u - cum[s], &head, &item, &off);
+        find<I>(c, seqs[s], u - cum[s], &head, &item, &off);
         while (u < end) {
             int lo, hi;
             chunk_item_range(c, seqs[s], item, &lo, &hi);
@@ -150,7 +163,24 @@ int main() {
         }
         if (!any) continue;
         const int grids[] = {1, 2, 3, 17, 152, 601};
-        check(c, seqs, grids[rnd(6)]);
+        const int grid = grids[rnd(6)];
+        int longest = 0;
+        for (const ChunkSeq &q : seqs) longest = q.len > longest ? q.len : longest;
+        CHECK(chunk_fits_32(c, row, n, longest));
+        check<int64_t>(c, seqs, grid);
+        check<int32_t>(c, seqs, grid);
+    }
+    // Lines that do not fit 32 bits: the closed form against a sum over items.
+    for (int round = 0; round < 200; ++round) {
+        ChunkShape c = {16 + (int)rnd(112), 1 + (int)rnd(16), 1, rnd(2) ? 1 + (int)rnd(1 << 30) : 0, 256, 1};
+        ChunkSeq s = {0, 1 + (int)rnd(1 << 22), 1 + (int)rnd(1 << 30)};
+        CHECK(!chunk_fits_32(c, 1 << 30, 1, s.len));
+        int64_t sum = 0;
+        for (int i = 0; i < chunk_items(c, s); ++i) sum += chunk_cost(c, s, i);
+        CHECK(chunk_prefix<int64_t>(c, s, chunk_items(c, s)) == sum);
+        CHECK(chunk_seq_units<int64_t>(c, s) == sum * c.num_kv_heads);
+        CHECK(chunk_share(sum, 152, 152) == sum);
+        if (chunk_fits_32(c, s.n, 1, s.len)) CHECK(chunk_prefix<int32_t>(c, s, chunk_items(c, s)) == sum);
     }
     printf("chunk schedule ok\n");
     return 0;
