@@ -259,45 +259,59 @@ def _status_ptr(status):
     return _ptr(status)
 
 
-def _checked_call(fn, what, specs, stream, args):
-    """One library call with little host work, for calls that take a few
-    microseconds on the GPU: the checks of _need_all and _one_device over
-    (tensor or None, dtype, name, ndim or None) specs, whose dtype None leaves
-    type and layout to the caller, then fn(*args, stream handle) with their
-    device current."""
-    import torch
+def _checked(specs):
+    """The checks of _need_all and _one_device, with little host work for calls
+    that take a few microseconds on the GPU, over (tensor, dtype, name, ndim)
+    specs; -> their device's index.  A dtype of None leaves type and layout to
+    the caller."""
+    index = specs[0][0].get_device()
+    for t, dtype, _, ndim in specs:
+        if t.get_device() != index or (dtype is not None and (t.dtype is not dtype or t.dim() != ndim or
+                                                              not t.is_contiguous())):
+            break
+    else:
+        if index >= 0:
+            return index
     for t, dtype, name, ndim in specs:
-        if t is None or dtype is None:
-            continue
-        if t.dtype is not dtype:
-            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if ndim is not None and t.dim() != ndim:
-            raise ValueError(f"{name}: expected {ndim} dims, got {tuple(t.shape)}")
-    index = None
+        if dtype is not None:
+            _need(t, dtype, name, ndim, device=False)
     for t, _, name, _ in specs:
-        if t is not None:
-            on = t.get_device()  # -1 on the host
-            if on != index:
-                if on < 0:
-                    raise ValueError(f"{name} must be a CUDA tensor")
-                if index is not None:
-                    raise ValueError("the device tensors of one call must all be on the same CUDA device")
-                index = on
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    raise ValueError("the device tensors of one call must all be on the same CUDA device")
+
+
+def _launch(fn, what, index, stream, args):
+    """fn(*args, stream handle) with device `index` current."""
+    import torch
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
     else:
-        if stream.device.index != index:
-            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
         handle = stream.cuda_stream
     if torch._C._cuda_getDevice() == index:
-        rc = fn(*args(), handle)
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(index):
-            rc = fn(*args(), handle)
+            rc = fn(*args, handle)
     if rc != PKV_OK:
         _check(rc, what)
+
+
+def _status_address(status, index):
+    if status is None:
+        return None
+    if _checked(((status, _torch().int32, "status", status.dim()),)) != index:
+        raise ValueError("the device tensors of one call must all be on the same CUDA device")
+    if status.numel() < 1:
+        raise ValueError("status must hold at least one int32")
+    return status.data_ptr()
+
+
+def _torch():
+    import torch
+    return torch
 
 
 def _address(t):
@@ -459,12 +473,22 @@ def chunk_workspace_size(num_tokens, num_heads, num_kv_heads, head_dim, num_ctas
     return int(load().pkv_chunk_workspace_size(num_tokens, num_heads, num_kv_heads, head_dim, num_ctas))
 
 
+@functools.lru_cache(maxsize=4096)
+def _chunk_workspace(num_tokens, num_heads, num_kv_heads, head_dim, num_ctas, index):
+    """chunk_workspace_size on device `index`, whose SM count it goes by."""
+    with _device_guard(index):
+        n = chunk_workspace_size(num_tokens, num_heads, num_kv_heads, head_dim, num_ctas)
+    if n == 0:
+        raise PkvError(PKV_ERR_UNSUPPORTED, "chunk_workspace_size")
+    return n
+
+
 def new_chunk_workspace(num_tokens, num_heads, num_kv_heads, head_dim, num_ctas=0, device="cuda"):
     """A device workspace of the size pkv_chunk_workspace_size asks for."""
     import torch
-    n = chunk_workspace_size(num_tokens, num_heads, num_kv_heads, head_dim, num_ctas)
-    if n == 0:
-        raise PkvError(PKV_ERR_UNSUPPORTED, "chunk_workspace_size")
+    device = torch.device(device)
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    n = _chunk_workspace(num_tokens, num_heads, num_kv_heads, head_dim, num_ctas, index)
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
@@ -481,32 +505,29 @@ def paged_attention_chunk(out, query, key_cache, value_cache, block_tables, cont
     included).  A workspace (new_chunk_workspace) is allocated when None.
     """
     import torch
-    lib = load()
-
-    def args():
-        t, h, d = query.shape
-        nb, hkv, bs, d2 = key_cache.shape
-        n, mb = block_tables.shape
-        if out.shape != query.shape or d2 != d or value_cache.shape != key_cache.shape \
-                or context_lens.shape[0] != n or query_starts.shape[0] != n + 1:
-            raise ValueError("inconsistent shapes")
-        if status is not None and status.numel() < 1:
-            raise ValueError("status must hold at least one int32")
-        ws = workspace
-        if ws is None and t and n:
-            ws = new_chunk_workspace(t, h, hkv, d, num_ctas, query.device)
-        return (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
-                block_tables.data_ptr(), mb, context_lens.data_ptr(), query_starts.data_ptr(), t, n, h, hkv, d, bs,
-                nb, float(scale), 1 if causal else 0, int(window), int(num_ctas), _address(ws), 0 if ws is None else ws.nbytes,
-                _address(status))
-
     f16, i32 = torch.float16, torch.int32
-    _checked_call(lib.pkv_paged_attention_chunk, "pkv_paged_attention_chunk",
-                  ((query, f16, "query", 3), (out, f16, "out", 3), (key_cache, f16, "key_cache", 4),
-                   (value_cache, f16, "value_cache", 4), (block_tables, i32, "block_tables", 2),
-                   (context_lens, i32, "context_lens", 1), (query_starts, i32, "query_starts", 1),
-                   (workspace, None if workspace is None else workspace.dtype, "workspace", None),
-                   (status, i32, "status", None)), stream, args)
+    index = _checked(((query, f16, "query", 3), (out, f16, "out", 3), (key_cache, f16, "key_cache", 4),
+                      (value_cache, f16, "value_cache", 4), (block_tables, i32, "block_tables", 2),
+                      (context_lens, i32, "context_lens", 1), (query_starts, i32, "query_starts", 1)))
+    t, h, d = query.shape
+    nb, hkv, bs, d2 = key_cache.shape
+    n, mb = block_tables.shape
+    if out.shape != query.shape or d2 != d or value_cache.shape != key_cache.shape \
+            or context_lens.shape[0] != n or query_starts.shape[0] != n + 1:
+        raise ValueError("inconsistent shapes")
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if _checked(((workspace, workspace.dtype, "workspace", workspace.dim()),)) != index:
+            raise ValueError("the device tensors of one call must all be on the same CUDA device")
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    elif t and n:
+        ws_bytes = _chunk_workspace(t, h, hkv, d, num_ctas, index)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=query.device)
+        ws = workspace.data_ptr()
+    _launch(load().pkv_paged_attention_chunk, "pkv_paged_attention_chunk", index, stream,
+            (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
+             mb, context_lens.data_ptr(), query_starts.data_ptr(), t, n, h, hkv, d, bs, nb, float(scale),
+             1 if causal else 0, int(window), int(num_ctas), ws, ws_bytes, _status_address(status, index)))
     return out
 
 
@@ -677,38 +698,44 @@ def reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, status=N
     _check(rc, "pkv_reshape_and_cache")
 
 
-def _rows(t, name):
+def _rows(t, name, f16):
     """The token stride of fp16 [T][heads][D]: each token's heads contiguous,
     tokens any multiple of 8 elements apart (a view of a projection's output)."""
-    import torch
-    if t.dtype is not torch.float16:
-        raise TypeError(f"{name}: expected {torch.float16}, got {t.dtype}")
+    if t.dtype is not f16:
+        raise TypeError(f"{name}: expected {f16}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name}: expected 3 dims, got {tuple(t.shape)}")
     n, h, d = t.shape
-    sn, sh, sd = t.stride()
-    if (d > 1 and sd != 1) or (h > 1 and sh != d):
+    stride, sh, sd = t.stride()
+    if sd == 1 and sh == d and n > 1 and stride >= h * d and stride % 8 == 0:
+        return stride
+    if n < 2:
+        stride = h * d
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    stride = sn if n > 1 else h * d
     if stride < h * d or stride % 8:
         raise ValueError(f"{name}: tokens must be a multiple of 8 elements apart and must not overlap")
     return stride
 
 
-def _rope_specs(t, d, positions, cos_sin, query_weight, key_weight, status):
-    """The checks of the tables that both qk_norm_rope calls share; -> specs."""
+def _rope_tables(t, d, positions, cos_sin, query_weight, key_weight):
+    """The checks of the tables that both qk_norm_rope calls share; -> specs of
+    those given, rows and width of cos_sin."""
     import torch
-    if (positions is None) != (cos_sin is None):
+    specs, reach, rot = (), 0, 0
+    if positions is not None and cos_sin is not None:
+        specs = ((positions, torch.int64, "positions", 1), (cos_sin, torch.float32, "cos_sin", 2))
+        if positions.dim() != 1 or cos_sin.dim() != 2 or positions.shape[0] != t:
+            raise ValueError("positions, cos_sin: inconsistent shapes")
+        reach, rot = cos_sin.shape
+    elif positions is not None or cos_sin is not None:
         raise ValueError("positions and cos_sin go together")
-    if positions is not None and positions.shape != (t,):
-        raise ValueError("positions: inconsistent shapes")
-    if query_weight is not None and query_weight.shape != (d,) or key_weight is not None and key_weight.shape != (d,):
-        raise ValueError("weights: inconsistent shapes")
-    if status is not None and status.numel() < 1:
-        raise ValueError("status must hold at least one int32")
-    return ((positions, torch.int64, "positions", 1), (cos_sin, torch.float32, "cos_sin", 2),
-            (query_weight, torch.float16, "query_weight", 1), (key_weight, torch.float16, "key_weight", 1),
-            (status, torch.int32, "status", None))
+    for w, name in ((query_weight, "query_weight"), (key_weight, "key_weight")):
+        if w is not None:
+            if w.dim() != 1 or w.shape[0] != d:
+                raise ValueError(f"{name}: inconsistent shapes")
+            specs += ((w, torch.float16, name, 1),)
+    return specs, reach, rot
 
 
 @_traced
@@ -719,22 +746,20 @@ def qk_norm_rope(query_out, key_out, query, key, positions=None, cos_sin=None, q
     given, and the rotation by row positions[t] (int64 [T]) of cos_sin (fp32
     [P][rot_dim]: the cosines, then the sines).  The four tensors may be
     views whose tokens are strided; query_out may be query, key_out key."""
-    sq, sk, sqo, sko = _rows(query, "query"), _rows(key, "key"), _rows(query_out, "query_out"), \
-        _rows(key_out, "key_out")
+    import torch
+    f16 = torch.float16
+    sq, sk, sqo, sko = _rows(query, "query", f16), _rows(key, "key", f16), _rows(query_out, "query_out", f16), \
+        _rows(key_out, "key_out", f16)
     t, h, d = query.shape
     if query_out.shape != query.shape or key_out.shape != key.shape or key.shape[0] != t or key.shape[2] != d:
         raise ValueError("inconsistent shapes")
-    specs = _rope_specs(t, d, positions, cos_sin, query_weight, key_weight, status)
-
-    def args():
-        reach, rot = cos_sin.shape if cos_sin is not None else (0, 0)
-        return (query_out.data_ptr(), sqo, key_out.data_ptr(), sko, query.data_ptr(), sq, key.data_ptr(), sk,
-                _address(positions), _address(cos_sin), reach, rot, 1 if interleaved else 0, _address(query_weight),
-                _address(key_weight), float(eps), t, h, key.shape[1], d, _address(status))
-
-    _checked_call(load().pkv_qk_norm_rope, "pkv_qk_norm_rope",
-                  ((query, None, "query", 3), (key, None, "key", 3), (query_out, None, "query_out", 3),
-                   (key_out, None, "key_out", 3)) + specs, stream, args)
+    specs, reach, rot = _rope_tables(t, d, positions, cos_sin, query_weight, key_weight)
+    index = _checked(((query, None, "query", 3), (key, None, "key", 3), (query_out, None, "query_out", 3),
+                      (key_out, None, "key_out", 3)) + specs)
+    _launch(load().pkv_qk_norm_rope, "pkv_qk_norm_rope", index, stream,
+            (query_out.data_ptr(), sqo, key_out.data_ptr(), sko, query.data_ptr(), sq, key.data_ptr(), sk,
+             _address(positions), _address(cos_sin), reach, rot, 1 if interleaved else 0, _address(query_weight),
+             _address(key_weight), float(eps), t, h, key.shape[1], d, _status_address(status, index)))
     return query_out, key_out
 
 
@@ -746,27 +771,23 @@ def qk_norm_rope_and_cache(query_out, query, key, value, key_cache, value_cache,
     keys and the values (unchanged) written to the slots slot_mapping (int64
     [T]) of key_cache / value_cache (fp16 [NB][Hkv][bs][D])."""
     import torch
-    sq, sk, sv, sqo = _rows(query, "query"), _rows(key, "key"), _rows(value, "value"), _rows(query_out, "query_out")
-    t, h, d = query.shape
-    specs = _rope_specs(t, d, positions, cos_sin, query_weight, key_weight, status)
-
-    def args():
-        nb, hkv, bs, d2 = key_cache.shape
-        if query_out.shape != query.shape or value.shape != key.shape or key.shape != (t, hkv, d) or d2 != d \
-                or value_cache.shape != key_cache.shape or slot_mapping.shape[0] != t:
-            raise ValueError("inconsistent shapes")
-        reach, rot = cos_sin.shape if cos_sin is not None else (0, 0)
-        return (query_out.data_ptr(), sqo, query.data_ptr(), sq, key.data_ptr(), sk, value.data_ptr(), sv,
-                key_cache.data_ptr(), value_cache.data_ptr(), slot_mapping.data_ptr(), _address(positions),
-                _address(cos_sin), reach, rot, 1 if interleaved else 0, _address(query_weight),
-                _address(key_weight), float(eps), t, h, hkv, d, bs, nb, _address(status))
-
     f16 = torch.float16
-    _checked_call(load().pkv_qk_norm_rope_and_cache, "pkv_qk_norm_rope_and_cache",
-                  ((query, None, "query", 3), (key, None, "key", 3), (value, None, "value", 3),
-                   (query_out, None, "query_out", 3), (key_cache, f16, "key_cache", 4),
-                   (value_cache, f16, "value_cache", 4), (slot_mapping, torch.int64, "slot_mapping", 1)) + specs,
-                  stream, args)
+    sq, sk, sv, sqo = _rows(query, "query", f16), _rows(key, "key", f16), _rows(value, "value", f16), \
+        _rows(query_out, "query_out", f16)
+    t, h, d = query.shape
+    specs, reach, rot = _rope_tables(t, d, positions, cos_sin, query_weight, key_weight)
+    index = _checked(((query, None, "query", 3), (key, None, "key", 3), (value, None, "value", 3),
+                      (query_out, None, "query_out", 3), (key_cache, f16, "key_cache", 4),
+                      (value_cache, f16, "value_cache", 4), (slot_mapping, torch.int64, "slot_mapping", 1)) + specs)
+    nb, hkv, bs, d2 = key_cache.shape
+    if query_out.shape != query.shape or value.shape != key.shape or key.shape != (t, hkv, d) or d2 != d \
+            or value_cache.shape != key_cache.shape or slot_mapping.shape[0] != t:
+        raise ValueError("inconsistent shapes")
+    _launch(load().pkv_qk_norm_rope_and_cache, "pkv_qk_norm_rope_and_cache", index, stream,
+            (query_out.data_ptr(), sqo, query.data_ptr(), sq, key.data_ptr(), sk, value.data_ptr(), sv,
+             key_cache.data_ptr(), value_cache.data_ptr(), slot_mapping.data_ptr(), _address(positions),
+             _address(cos_sin), reach, rot, 1 if interleaved else 0, _address(query_weight), _address(key_weight),
+             float(eps), t, h, hkv, d, bs, nb, _status_address(status, index)))
     return query_out
 
 
