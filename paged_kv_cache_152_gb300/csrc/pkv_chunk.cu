@@ -31,17 +31,18 @@ constexpr int kOverhead = 256;
 // Items are cut at multiples of 2^this steps.
 constexpr int kQuantumShift = 1;
 
-// The workspace: parts' descriptions, their (maximum, sum), their outputs.
+// The workspace: records of the items cut between CTAs, the parts' (maximum,
+// sum) and outputs.
 struct ChunkWorkspace {
     size_t ml, o, total;
     int part_rows;
     static ChunkWorkspace plan(int num_tokens, int group, int head_dim, int ctas) {
         auto up = [](size_t x) { return (x + 255) / 256 * 256; };
         ChunkWorkspace w;
-        const int tile_tokens = kChunkRows / group;
-        w.part_rows = (int)std::min<int64_t>(2 * tile_tokens, num_tokens) * group;
-        w.ml = up(sizeof(ChunkPart) * 2 * (size_t)ctas);
-        w.o = w.ml + up(sizeof(float2) * 2 * (size_t)ctas * w.part_rows);
+        // one tile's rows, or two tiles'
+        w.part_rows = num_tokens <= kChunkRows / group ? num_tokens * group : 2 * kChunkRows;
+        w.ml = up(sizeof(ChunkPart) * (size_t)ctas);
+        w.o = w.ml + up(sizeof(float2) * 2 * (size_t)ctas * 2 * kChunkRows);
         w.total = w.o + up(sizeof(float) * 2 * (size_t)ctas * w.part_rows * head_dim);
         return w;
     }
@@ -178,9 +179,8 @@ extern "C" int pkv_paged_attention_chunk(void *out, const void *query, const voi
     if ((int64_t)max_blocks_per_seq * block_size <= ((int64_t)kChunkTile << kQuantumShift) || num_ctas == 1) return PKV_OK;
     fn = d64 ? reinterpret_cast<const void *>(&chunk_join_kernel<64>)
              : reinterpret_cast<const void *>(&chunk_join_kernel<128>);
-    void *join_args[] = {&p, &num_ctas};
-    if (launch_pdl(fn, dim3(2u * (unsigned)num_ctas, (unsigned)(ws.part_rows + 15) / 16), dim3(128),
-                   sizeof(int) * (size_t)num_ctas, stream, join_args) != cudaSuccess) {
+    if (launch_pdl(fn, dim3((unsigned)num_ctas, (unsigned)(ws.part_rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0,
+                   stream, args) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
     }

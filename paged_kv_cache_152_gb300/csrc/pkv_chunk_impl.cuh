@@ -52,13 +52,16 @@ constexpr int kChunkPieces = 4;   // piece descriptors in flight
 // Registers per thread: 384 at launch x 168 = 64512 = 256 x 208 + 128 x 88.
 constexpr int kChunkLaunchRegs = 168;
 
-// One of at most two partial pieces a CTA writes, for the joining kernel.
+// The part of an item that a CTA begins and others end, for the joining kernel.
 struct ChunkPart {
-    long long item;  // the item's first unit on the line: the same for all its pieces
-    int row0;        // first query row
+    long long start;     // the item's first unit
+    ChunkShares shares;  // the cut of the line
+    int valid;
+    int row0;            // first query row
     int tokens;
     int kv_head;
-    int flags;       // 1: valid, 2: the item's first steps, 4: its last steps
+    int lo, hi;          // positions that some row sees
+    int cta1;            // the last CTA that holds it
 };
 
 struct ChunkParams {
@@ -70,9 +73,11 @@ struct ChunkParams {
     const int32_t *block_tables;
     const int32_t *context_lens;
     const int32_t *query_starts;
-    ChunkPart *parts;    // [2 * CTAs]
-    float2 *part_ml;     // [2 * CTAs][part_rows] (c * m, l)
-    float *part_o;       // [2 * CTAs][part_rows][D], not normalised
+    // A CTA's parts of items that it shares with others: part 2 * CTA + 1 of the
+    // item that it begins, 2 * CTA of the one that it does not (chunk_part).
+    ChunkPart *parts;      // [CTAs] of the first kind
+    float2 *part_ml;       // [2 * CTAs][2 slots][128 rows] (c * m, l)
+    float *part_o;         // [2 * CTAs][part_rows][D], not normalised
     int32_t *status;
     ChunkShape shape;
     int num_tokens;
@@ -99,7 +104,8 @@ struct ChunkPiece {
     int all_lo, all_hi;  // positions that every row sees
     int t0, t1;          // steps of this piece
     int first[2], end[2];  // those a slot takes: first, first + stride, ... < end
-    int partial;         // the part it writes, or -1
+    int partial;         // some of the item's steps, not all
+    int part;            // then this CTA's part of it
     int single;          // one query tile: the slots take alternate steps (stride 2, else 1)
     int q_buffer;        // of a lone tile's queries (two tiles take both buffers)
     int last;            // no piece: the end
@@ -287,7 +293,9 @@ struct ChunkLoader {
     uint32_t pieces = 0;
     uint32_t q_uses = 0, q_used = 0;         // a bit per buffer: phase, ever used
     uint32_t edge_phase = 0, edge_used = 0;  // bit per stage
-    int parts = 0, next_buffer = 0;
+    int next_buffer = 0;
+    bool begun = false;  // an item that others end
+    ChunkShares shares;
 
     __device__ bool wait(uint32_t bar, uint32_t parity) { return chunk_wait(bar, parity, PKV_CTL(abort), p.wait_tries); }
 
@@ -434,7 +442,6 @@ struct ChunkLoader {
                 }
                 pc.t0 = first + a;
                 pc.t1 = first + b;
-                pc.partial = -1;
                 pc.single = pc.tokens <= c.tile_tokens;
                 pc.last = 0;
                 pc.q_buffer = next_buffer;  // the one that the last lone tile did not take
@@ -453,18 +460,23 @@ struct ChunkLoader {
                         if (to <= from) pc.end[k] = pc.first[k];
                     }
                 }
-                if (b - a < steps) {
-                    pc.partial = parts;
+                pc.partial = b - a < steps;
+                if (pc.partial) pc.part = 2 * blockIdx.x + (a == 0 ? 1 : 0);
+                if (pc.partial && a == 0) {
+                    begun = true;
                     if (lane == 0) {
                         ChunkPart part;
-                        part.item = u - off;
+                        part.start = u - off;
+                        part.shares = shares;
+                        part.valid = 1;
                         part.row0 = pc.row0;
                         part.tokens = pc.tokens;
                         part.kv_head = head;
-                        part.flags = 1 | (a == 0 ? 2 : 0) | (b == steps ? 4 : 0);
-                        p.parts[2 * blockIdx.x + parts] = part;
+                        part.lo = lo;
+                        part.hi = hi;
+                        part.cta1 = chunk_share_of(shares, part.start + cost - 1);
+                        p.parts[blockIdx.x] = part;
                     }
-                    ++parts;
                 }
                 if (!emit(pc) || !load(pc)) return false;
             }
@@ -486,8 +498,7 @@ struct ChunkLoader {
 
     __device__ void run(int s, int64_t cum, int64_t u, int64_t end) {
         bool ok = walk(s, cum, u, end);
-        if (lane == 0)
-            for (int k = parts; k < 2; ++k) p.parts[2 * blockIdx.x + k].flags = 0;
+        if (lane == 0 && !begun) p.parts[blockIdx.x].valid = 0;
         if (ok) {
             ChunkPiece pc = {};
             pc.last = 1;
@@ -642,7 +653,8 @@ struct ChunkProducts {
             kp.move(k < 0 ? 1 : 2);
             vp.move(k + 2 >= n ? 1 : 2);
         }
-        if (single && n > 1) ++merges;
+        // the other softmax warpgroup reads this slot's output, too
+        if (single && (n > 1 || (slot == 0 && uniform(pc.partial)))) ++merges;
         ring = vp;
         theirs += other;
         return true;
@@ -904,7 +916,7 @@ struct ChunkSoftmax {
     // the instruction cache.
     __device__ bool piece(const ChunkPiece &pc, bool dry) {
         const int first = dry ? 0 : pc.first[slot], end = dry ? 1 : pc.end[slot], stride = pc.single ? 2 : 1;
-        const bool merge = pc.single && pc.t1 - pc.t0 > 1;
+        const bool both = pc.single && pc.t1 - pc.t0 > 1, merge = both || (pc.single && pc.partial);
         // this thread's row: a token of the item and a query head
         const int token = row / p.group + (pc.single ? 0 : slot * p.shape.tile_tokens);
         const int head = pc.kv_head * p.group + row % p.group;
@@ -929,8 +941,8 @@ struct ChunkSoftmax {
         if (dry) return true;
 
         __half *out = p.out + ((int64_t)(pc.row0 + token) * p.num_heads + head) * D;
-        const int64_t part_row = (int64_t)(2 * blockIdx.x + pc.partial) * p.part_rows + token * p.group + row % p.group;
-        float *part = p.part_o + part_row * D;
+        float *part = p.part_o + ((int64_t)pc.part * p.part_rows + (pc.single ? row : slot * kChunkRows + row)) * D;
+        float2 *part_ml = p.part_ml + ((int64_t)pc.part * 2 + slot) * kChunkRows + row;
         const bool mine = first < end;
         if (mine) {
             if (!wait(PKV_CTL(o_full) + 8 * slot, o_uses & 1)) return false;
@@ -947,7 +959,7 @@ struct ChunkSoftmax {
                     tmem_wait_ld();
                     tmem_pin32(o);
                     if (live) {
-                        if (pc.partial < 0)
+                        if (!pc.partial)
                             store_out(out + c * 32, o, inv);
                         else
                             store_part(part + c * 32, o);
@@ -955,14 +967,14 @@ struct ChunkSoftmax {
                 }
                 tc_fence_before();
                 arrive(PKV_CTL(o_free) + 8 * slot);
-            } else if (live && pc.partial < 0) {  // no step of the item is seen by this tile
+            } else if (live && !pc.partial) {  // no step of the item is seen by this tile
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
             }
             if (live) {
-                if (pc.partial >= 0) p.part_ml[part_row] = make_float2(top(), l);
+                if (pc.partial) *part_ml = make_float2(top(), l);
                 if (pc.odd && mine) {
-                    if (pc.partial < 0)
+                    if (!pc.partial)
                         chunk_add_odd<D>(p, pc, row_lo, row_hi, out, 0, D);
                     else
                         chunk_add_odd<D>(p, pc, row_lo, row_hi, part, 0, D);
@@ -985,14 +997,14 @@ struct ChunkSoftmax {
         const float high = fmaxf(a.x, b.x), base = high == -INFINITY ? 0.f : high;
         const float fa = ex2(a.x - base), fb = ex2(b.x - base);
         const float sum = fa * a.y + fb * b.y;
-        const float inv = pc.partial >= 0 ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+        const float inv = pc.partial ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
         const uint64_t fa2 = pack2(fa, fa), fb2 = pack2(fb, fb);
         const int c0 = slot * (D / 2);
 #pragma unroll 1
         for (int c = 0; any && c < D / 64; ++c) {
             uint32_t oa[32], ob[32];
             tmem_ld32(o_at(0) + c0 + c * 32, oa);
-            tmem_ld32(o_at(1) + c0 + c * 32, ob);
+            tmem_ld32(o_at(both ? 1 : 0) + c0 + c * 32, ob);  // (once more with the weight 0 where there is one slot)
             tmem_wait_ld();
             tmem_pin32(oa);
             tmem_pin32(ob);
@@ -1005,19 +1017,19 @@ struct ChunkSoftmax {
                 oa[2 * i + 1] = __float_as_uint(y);
             }
             if (live) {
-                if (pc.partial < 0)
+                if (!pc.partial)
                     store_out(out + c0 + c * 32, oa, inv);
                 else
                     store_part(part + c0 + c * 32, oa);
             }
         }
         tc_fence_before();
-        arrive(PKV_CTL(o_free) + 8 * slot);
-        arrive(PKV_CTL(o_cross) + 8 * (1 - slot));
+        if (mine) arrive(PKV_CTL(o_free) + 8 * slot);
+        if (both || slot == 1) arrive(PKV_CTL(o_cross) + 8 * (1 - slot));
         if (live) {
-            if (pc.partial >= 0 && slot == 0) p.part_ml[part_row] = make_float2(high, sum);
+            if (pc.partial) *part_ml = make_float2(high, sum);
             if (pc.odd) {
-                if (pc.partial < 0)
+                if (!pc.partial)
                     chunk_add_odd<D>(p, pc, row_lo, row_hi, out, c0, D / 2);
                 else
                     chunk_add_odd<D>(p, pc, row_lo, row_hi, part, c0, D / 2);
@@ -1112,8 +1124,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                 if (lane >= d) upto += x;
             }
             const int64_t total = __shfl_sync(kFullMask, upto, 31);
-            const int64_t u = chunk_share(total, gridDim.x, blockIdx.x);
-            const int64_t end = chunk_share(total, gridDim.x, blockIdx.x + 1);
+            const ChunkShares shares = chunk_shares(total, gridDim.x);
+            const int64_t u = chunk_share(shares, blockIdx.x), end = chunk_share(shares, blockIdx.x + 1);
             int s = 0;
             int64_t cum = 0;
             if (u < end) {
@@ -1133,6 +1145,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             __syncwarp();
             fence_proxy_async_smem();  // the ring's memory was read and written by ordinary accesses
             ChunkLoader<D> loader{p, ctl, ctl_at, smem_addr(smem), smem_addr(ring), lane};
+            loader.shares = shares;
             loader.run(s, cum, u, end);
         } else if (warp == 11) {
             chunk_guard<D>(p, ctl, ctl_at, ring, lane);
@@ -1158,58 +1171,122 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     if (threadIdx.x == 0 && ctl.abort) report(p.status, PKV_ERR_DEVICE_TIMEOUT);
 }
 
-// Joins the pieces of items cut between CTAs: a warp per row.  blockIdx.x
-// names a part; the CTA that holds an item's first steps does the item.
+// Joins the parts of items cut between CTAs.  blockIdx.x is the CTA that began
+// an item, blockIdx.y 32 of its tiles' rows, four per warp.  Bound by latency:
+// the record, then the parts' weights and (of the first two, the usual number)
+// outputs together.  The parts are taken in the order of the item's steps.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 32;
+
 template <int D>
-__global__ void __launch_bounds__(128) chunk_join_kernel(const __grid_constant__ ChunkParams p, int ctas) {
-    constexpr int kRowsPerBlock = 16;
-    constexpr int E = D / 32;
-    extern __shared__ int list[];  // the item's parts, in the order of its steps
+__global__ void __launch_bounds__(kJoinThreads, 3) chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+    constexpr int R = kJoinRows / (kJoinThreads / 32);
+    constexpr int E = D / 32;  // columns per lane, in a row
     grid_dependency_wait();
     launch_dependents();
-    const ChunkPart part = p.parts[blockIdx.x];
-    if ((part.flags & 3) != 3) return;
-    const int rows = part.tokens * p.group;
-    if ((int)blockIdx.y * kRowsPerBlock >= rows) return;
+    const ChunkPart item = p.parts[blockIdx.x];
+    if (!item.valid) return;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    // Later pieces are the first parts of the following CTAs (one whose share
-    // of the item held no step has none).
-    int count = 1;
-    if (threadIdx.x == 0) list[0] = blockIdx.x;
-    for (int c = blockIdx.x / 2 + 1; c < ctas; c += 32) {
-        ChunkPart next;
-        next.flags = 0;
-        next.item = -1;
-        if (c + lane < ctas) next = p.parts[2 * (c + lane)];
-        const bool hit = (next.flags & 1) && next.item == part.item;
-        const unsigned hits = __ballot_sync(kFullMask, hit);
-        if (warp == 0 && hit) list[count + __popc(hits & ((1u << lane) - 1u))] = 2 * (c + lane);
-        count += __popc(hits);
-        if (__any_sync(kFullMask, hit && (next.flags & 4))) break;
-    }
-    __syncthreads();
-    for (int r = blockIdx.y * kRowsPerBlock + warp; r < min(rows, ((int)blockIdx.y + 1) * kRowsPerBlock); r += 4) {
-        float top = -INFINITY;
-        for (int i = lane; i < count; i += 32) top = fmaxf(top, p.part_ml[(int64_t)list[i] * p.part_rows + r].x);
+    // The tile and this warp's rows of it.
+    const int at = blockIdx.y * kJoinRows + warp * R, slot = at / kChunkRows, row0 = at % kChunkRows;
+    const int token0 = slot * p.shape.tile_tokens;
+    const int rows = min(p.shape.tile_tokens, item.tokens - token0) * p.group;
+    if (row0 >= rows) return;
+    const int last = min(R, rows - row0) - 1;  // rows past the end repeat the last one
+
+    float top[R], sum[R], acc[R][E] = {};
 #pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, d));
-        const float base = top == -INFINITY ? 0.f : top;
-        float sum = 0.f, acc[E] = {};
-        for (int i = 0; i < count; ++i) {
-            const int64_t at = (int64_t)list[i] * p.part_rows + r;
-            const float2 ml = p.part_ml[at];
-            if (ml.y == 0.f) continue;  // the row sees nothing of this piece, whose O may not be written
-            const float w = ex2(ml.x - base);
-            sum += w * ml.y;
+    for (int r = 0; r < R; ++r) top[r] = -INFINITY, sum[r] = 0.f;
+    // Parts 32 CTAs at a time: where there are more, once for the maximum first.
+    const bool few = item.cta1 - (int)blockIdx.x < 32;
+#pragma unroll 1
+    for (int pass = few ? 1 : 0; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int cta = blockIdx.x; cta <= item.cta1; cta += 32) {
+            int a = 0, b = 0;
+            if (cta + lane <= item.cta1)
+                chunk_part(p.shape, item.shares, cta + lane, item.start, item.lo, item.hi, &a, &b);
+            const int part = 2 * (cta + lane) + (a == 0 ? 1 : 0);
+            unsigned has = __ballot_sync(kFullMask, b > a);
+            float2 ml[R];
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += w * p.part_o[at * D + lane * E + e];
+            for (int r = 0; r < R; ++r) {
+                ml[r] = make_float2(-INFINITY, 0.f);
+                if (b > a) ml[r] = p.part_ml[((int64_t)part * 2 + slot) * kChunkRows + row0 + min(r, last)];
+            }
+            auto load = [&](int i, float (&v)[R][E]) {
+                const float *o = p.part_o + ((int64_t)__shfl_sync(kFullMask, part, i) * p.part_rows + at) * D + lane * E;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) {
+                        const float2 x = *reinterpret_cast<const float2 *>(o + min(r, last) * D + e);
+                        v[r][e] = x.x;
+                        v[r][e + 1] = x.y;
+                    }
+            };
+            float v0[R][E], v1[R][E];
+            int i0 = 0, i1 = 0;
+            if (pass && has) {
+                i0 = __ffs(has) - 1;
+                has &= has - 1;
+                i1 = has ? __ffs(has) - 1 : i0;
+                load(i0, v0);
+                load(i1, v1);
+            }
+            if (few || pass == 0) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float t = ml[r].x;
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) t = fmaxf(t, __shfl_xor_sync(kFullMask, t, d));
+                    top[r] = fmaxf(top[r], t);
+                }
+                if (pass == 0) continue;
+            }
+            unsigned seen[R];  // parts whose output counts: a row that sees nothing of a part may have none written
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                seen[r] = __ballot_sync(kFullMask, ml[r].y != 0.f);
+                ml[r].x = ex2(ml[r].x - (top[r] == -INFINITY ? 0.f : top[r]));
+                float t = ml[r].y == 0.f ? 0.f : ml[r].x * ml[r].y;
+#pragma unroll
+                for (int d = 16; d; d >>= 1) t += __shfl_xor_sync(kFullMask, t, d);
+                sum[r] += t;
+            }
+            auto add = [&](int i, const float (&v)[R][E]) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float w = __shfl_sync(kFullMask, ml[r].x, i);
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (seen[r] >> i & 1) acc[r][e] = fmaf(w, v[r][e], acc[r][e]);
+                }
+            };
+            add(i0, v0);
+            if (has) {
+                add(i1, v1);
+                has &= has - 1;
+            }
+#pragma unroll 1
+            while (has) {
+                const int i = __ffs(has) - 1;
+                has &= has - 1;
+                load(i, v0);
+                add(i, v0);
+            }
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int token = r / p.group, head = part.kv_head * p.group + r % p.group;
-        __half *out = p.out + ((int64_t)(part.row0 + token) * p.num_heads + head) * D + lane * E;
+    }
 #pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<__half2 *>(out + e) = __floats2half2_rn(acc[e] * inv, acc[e + 1] * inv);
+    for (int r = 0; r < R; ++r) {
+        const int row = row0 + r;
+        const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
+        const int token = token0 + row / p.group, head = item.kv_head * p.group + row % p.group;
+        __half *out = p.out + ((int64_t)(item.row0 + token) * p.num_heads + head) * D + lane * E;
+        if (r <= last)
+#pragma unroll
+            for (int e = 0; e < E; e += 2)
+                *reinterpret_cast<__half2 *>(out + e) = __floats2half2_rn(acc[r][e] * inv, acc[r][e + 1] * inv);
     }
 }
 

@@ -120,17 +120,34 @@ PKV_HD bool chunk_fits_32(const ChunkShape &c, int num_tokens, int num_seqs, int
     return num_tokens < (1 << 29) && c.window <= (1 << 30) && items < (INT64_C(1) << 29) / each / c.num_kv_heads;
 }
 
-// Where share k of `shares` starts on a line of `total` units.
-PKV_HD int64_t chunk_share(int64_t total, int shares, int k) {
-    int64_t q, r;
+// A line of `total` units cut into `shares` equal shares: the first r of them
+// have q + 1 units, the others q.
+struct ChunkShares {
+    int64_t q;
+    int r;
+};
+
+PKV_HD ChunkShares chunk_shares(int64_t total, int shares) {
+    ChunkShares s;
     if (total >> 32 == 0) {
-        q = (uint32_t)total / (uint32_t)shares;
-        r = (uint32_t)total % (uint32_t)shares;
+        s.q = (uint32_t)total / (uint32_t)shares;
+        s.r = (int)((uint32_t)total % (uint32_t)shares);
     } else {
-        q = total / shares;
-        r = total % shares;
+        s.q = total / shares;
+        s.r = (int)(total % shares);
     }
-    return q * k + (k < r ? k : r);
+    return s;
+}
+
+// Where share k starts.
+PKV_HD int64_t chunk_share(const ChunkShares &s, int k) { return s.q * k + (k < s.r ? k : s.r); }
+
+// The share that holds unit x.
+PKV_HD int chunk_share_of(const ChunkShares &s, int64_t x) {
+    const int64_t longer = (s.q + 1) * s.r;
+    if (s.q >> 31 == 0 && x >> 32 == 0)
+        return x < longer ? (int)((uint32_t)x / (uint32_t)(s.q + 1)) : s.r + (int)((uint32_t)(x - longer) / (uint32_t)s.q);
+    return x < longer ? (int)(x / (s.q + 1)) : s.r + (int)((x - longer) / s.q);
 }
 
 PKV_HD int chunk_steps(int lo, int hi) {
@@ -149,6 +166,17 @@ PKV_HD int chunk_step_at(const ChunkShape &c, int lo, int hi, int x) {
     if (t > steps) t = steps;
     if (t > 0 && steps - t < 1 << c.quantum_shift) t = steps;
     return t;
+}
+
+// The steps [*a, *b) that share k has of the item [lo, hi) which starts at unit
+// `start`.  Where they are some but not all, they are the share's part
+// (*a == 0) of that item: a share has at most one part that begins an item and
+// one that does not.
+PKV_HD void chunk_part(const ChunkShape &c, const ChunkShares &s, int k, int64_t start, int lo, int hi, int *a, int *b) {
+    const int64_t from = chunk_share(s, k) - start, to = chunk_share(s, k + 1) - start;
+    const int cost = hi - lo + c.overhead;
+    *a = chunk_step_at(c, lo, hi, (int)chunk_min64(chunk_max64(from, 0), cost));
+    *b = chunk_step_at(c, lo, hi, (int)chunk_min64(chunk_max64(to, 0), cost));
 }
 
 }  // namespace pkv

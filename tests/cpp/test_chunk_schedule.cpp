@@ -85,12 +85,13 @@ static void check(const ChunkShape &c, const std::vector<ChunkSeq> &seqs, int sh
     }
     std::map<std::tuple<int, int, int>, int> done;   // item -> steps so far, in order of the shares
     std::map<std::tuple<int, int, int>, int> met;    // empty items
-    CHECK(chunk_share(total, shares, 0) == 0 && chunk_share(total, shares, shares) == total);
+    const ChunkShares cut = chunk_shares(total, shares);
+    CHECK(chunk_share(cut, 0) == 0 && chunk_share(cut, shares) == total);
     for (int k = 0; k < shares; ++k) {
-        int64_t u = chunk_share(total, shares, k);
-        const int64_t end = chunk_share(total, shares, k + 1);
+        int64_t u = chunk_share(cut, k);
+        const int64_t end = chunk_share(cut, k + 1);
         CHECK(end >= u);
-        int partial = 0;
+        int partial[2] = {0, 0};
         size_t s = 0;
         while (s < seqs.size() && cum[s + 1] <= u) ++s;
         if (u >= end) continue;
@@ -107,10 +108,23 @@ static void check(const ChunkShape &c, const std::vector<ChunkSeq> &seqs, int sh
             const int steps = chunk_steps(lo, hi);
             const auto key = std::make_tuple((int)s, head, item);
             if (steps == 0 && off == 0) ++met[key];
+            // the item's parts as any share finds them
+            const int64_t start = u - off;
+            const int from = chunk_share_of(cut, start), to = chunk_share_of(cut, start + cost - 1);
+            CHECK(from <= k && k <= to && chunk_share(cut, from) <= start && start < chunk_share(cut, from + 1));
+            int at = 0;
+            for (int j = from; j <= to; ++j) {
+                int a, b;
+                chunk_part(c, cut, j, start, lo, hi, &a, &b);
+                CHECK(a == at && b >= a);
+                if (j == k) CHECK(a == t0 && b == t1);
+                at = b;
+            }
+            CHECK(at == steps);
             if (t1 > t0) {
                 CHECK(done[key] == t0);
                 done[key] = t1;
-                if (t1 - t0 < steps) ++partial;
+                if (t1 - t0 < steps) ++partial[t0 == 0];
             }
             u += b - off;
             off = 0;
@@ -123,7 +137,7 @@ static void check(const ChunkShape &c, const std::vector<ChunkSeq> &seqs, int sh
                 }
             }
         }
-        CHECK(partial <= 2);
+        CHECK(partial[0] <= 1 && partial[1] <= 1);
     }
     for (size_t s = 0; s < seqs.size(); ++s)
         for (int h = 0; h < c.num_kv_heads; ++h)
@@ -179,7 +193,10 @@ int main() {
         for (int i = 0; i < chunk_items(c, s); ++i) sum += chunk_cost(c, s, i);
         CHECK(chunk_prefix<int64_t>(c, s, chunk_items(c, s)) == sum);
         CHECK(chunk_seq_units<int64_t>(c, s) == sum * c.num_kv_heads);
-        CHECK(chunk_share(sum, 152, 152) == sum);
+        const ChunkShares cut = chunk_shares(sum, 152);
+        CHECK(chunk_share(cut, 152) == sum);
+        for (int k = 0; k < 152; ++k)
+            CHECK(chunk_share_of(cut, chunk_share(cut, k)) == k && chunk_share_of(cut, chunk_share(cut, k + 1) - 1) == k);
         if (chunk_fits_32(c, s.n, 1, s.len)) CHECK(chunk_prefix<int32_t>(c, s, chunk_items(c, s)) == sum);
     }
     printf("chunk schedule ok\n");
