@@ -666,10 +666,6 @@ struct ChunkProducts {
             if (!wait(PKV_CTL(piece_full) + 8 * at, i / kChunkPieces & 1)) break;
             const ChunkPiece &pc = ctl.piece[at];
             if (uniform(pc.last)) break;
-            if (i == 0) {  // the softmax's dry step is over
-                if (!wait(PKV_CTL(p_full) + 8 * slot, 0)) break;
-                ++p_uses;
-            }
             if (!piece(pc)) break;
             umma_arrive(PKV_CTL(piece_empty) + 8 * at);
         }
@@ -795,8 +791,10 @@ struct ChunkSoftmax {
     __device__ uint32_t o_at(int s) { return tmem + 2 * kChunkTile + s * D; }
 
     // One step: scores -> weights, in place in tensor memory.
-    // A dry step works on whatever is there and waits for nothing.
+    // A dry step works on whatever the output's columns hold, waits for nothing and
+    // tells nobody.
     __device__ bool step(int col0, int row_lo, int row_hi, bool first, bool any, bool dry) {
+        const uint32_t s_cols = dry ? o_at(slot) : s_at();
         if (!dry) {
             if (!wait(PKV_CTL(s_full) + 8 * slot, s_uses & 1)) return false;
             ++s_uses;
@@ -814,14 +812,14 @@ struct ChunkSoftmax {
 #pragma unroll 1
             for (int c = 0; c < kChunkTile; c += 32) {
                 uint32_t x[32];
-                tmem_ld32(s_at() + c, x);
+                tmem_ld32(s_cols + c, x);
                 tmem_wait_ld();
                 tmem_pin32(x);
                 const int a = row_lo - col0 - c;
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     if ((unsigned)(i - a) >= n) x[i] = 0xff800000u;
-                tmem_st32(s_at() + c, x);
+                tmem_st32(s_cols + c, x);
             }
             tmem_wait_st();
         }
@@ -842,7 +840,7 @@ struct ChunkSoftmax {
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             uint32_t s[4][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(s_at() + c * 32, s[c]);
+            for (int c = 0; c < 4; ++c) tmem_ld32(s_cols + c * 32, s[c]);
             tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_pin32(s[c]);
@@ -888,11 +886,11 @@ struct ChunkSoftmax {
             if (move) m = next;
         }
         l += sum;
-        tmem_st32(s_at(), w[0]);
-        tmem_st32(s_at() + 32, w[1]);
+        tmem_st32(s_cols, w[0]);
+        tmem_st32(s_cols + 32, w[1]);
         tmem_wait_st();
         tc_fence_before();
-        arrive(PKV_CTL(p_full) + 8 * slot);
+        if (!dry) arrive(PKV_CTL(p_full) + 8 * slot);
         return true;
     }
 
