@@ -188,41 +188,44 @@ __device__ __forceinline__ ChunkSeq chunk_load_seq(const ChunkParams &p, int s, 
     return q;
 }
 
-// The schedule's closed forms, out of line: I = int32_t where the line fits it.
+// The schedule's closed forms, out of line, their arguments in registers (a
+// reference to the parameters would be read through the caches, cold): I =
+// int32_t where the line fits it.
 template <typename I>
-__device__ __noinline__ int64_t chunk_units(const ChunkParams &p, const ChunkSeq &s) {
-    return chunk_seq_units<I>(p.shape, s);
+__device__ __noinline__ int64_t chunk_units(ChunkShape c, ChunkSeq s) {
+    return chunk_seq_units<I>(c, s);
 }
 
 // The item of a sequence that holds unit x of its units, and x's offset in it,
 // by a whole warp: 32 candidates at a time.
+struct ChunkPlace {
+    int kv_head, item, offset;
+};
+
 template <typename I>
-__device__ __noinline__ void chunk_locate(const ChunkParams &p, const ChunkSeq &s, int64_t unit, int lane, int *kv_head,
-                                          int *item, int *offset) {
-    const int items = chunk_items(p.shape, s);
-    const I per_head = chunk_prefix<I>(p.shape, s, items);
+__device__ __noinline__ ChunkPlace chunk_locate(ChunkShape c, ChunkSeq s, int64_t unit, int lane) {
+    const int items = chunk_items(c, s);
+    const I per_head = chunk_prefix<I>(c, s, items);
     I x = (I)unit;
     int head = -1;  // the last one that begins at or before x
     unsigned hits;
     do {
         const int h = head + 1 + lane;
-        hits = __ballot_sync(kFullMask, h < p.shape.num_kv_heads && h * per_head <= x);
+        hits = __ballot_sync(kFullMask, h < c.num_kv_heads && h * per_head <= x);
         head += __popc(hits);
     } while (hits == kFullMask);
-    *kv_head = head;
     x -= head * per_head;
     int lo = 0, span = items;  // the item is in [lo, lo + span)
     I before = 0;
     while (span > 1) {
         const int step = (span + 31) / 32, i = lo + lane * step;
-        const I at = lane * step < span ? chunk_prefix<I>(p.shape, s, i) : 0;
+        const I at = lane * step < span ? chunk_prefix<I>(c, s, i) : 0;
         const int who = 31 - __clz(__ballot_sync(kFullMask, lane * step < span && at <= x));
         before = __shfl_sync(kFullMask, at, who);
         lo += who * step;
         span = min(step, span - who * step);
     }
-    *item = lo;
-    *offset = (int)(x - before);
+    return ChunkPlace{head, lo, (int)(x - before)};
 }
 
 // Whether some row of the item does not see all of step t.
@@ -376,9 +379,9 @@ struct ChunkLoader {
     __device__ bool load(const ChunkPiece &pc) {
         const int n = pc.t1 - pc.t0;
         if (n == 0) return true;
-        if (pieces == 1 && !load_queries(pc)) return false;
         // The block table is read two steps ahead of the copies.
         int now = lookup(pc, pc.t0), next = n > 1 ? lookup(pc, pc.t0 + 1) : -1;
+        if (pieces == 1 && !load_queries(pc)) return false;
 #pragma unroll 1
         for (int t = pc.t0 - 1; t < pc.t1; ++t) {
             const int ahead = t >= pc.t0 && t + 2 < pc.t1 ? lookup(pc, t + 2) : -1;
@@ -411,11 +414,8 @@ struct ChunkLoader {
         if (u >= end) return true;
         const ChunkShape &c = p.shape;
         ChunkSeq q = chunk_load_seq(p, s, false);
-        int head, item, off, items = chunk_items(c, q);
-        if (p.fits_32)
-            chunk_locate<int32_t>(p, q, u - cum, lane, &head, &item, &off);
-        else
-            chunk_locate<int64_t>(p, q, u - cum, lane, &head, &item, &off);
+        const ChunkPlace at = p.fits_32 ? chunk_locate<int32_t>(c, q, u - cum, lane) : chunk_locate<int64_t>(c, q, u - cum, lane);
+        int head = at.kv_head, item = at.item, off = at.offset, items = chunk_items(c, q);
         while (true) {
             ChunkPiece pc;
             const int w = 2 * c.tile_tokens;
@@ -1103,7 +1103,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     int64_t units = 0;
     for (int s = threadIdx.x * per; s < min((int)(threadIdx.x + 1) * per, p.num_seqs); ++s) {
         const ChunkSeq seq = chunk_load_seq(p, s, blockIdx.x == 0);
-        units += p.fits_32 ? chunk_units<int32_t>(p, seq) : chunk_units<int64_t>(p, seq);
+        units += p.fits_32 ? chunk_units<int32_t>(p.shape, seq) : chunk_units<int64_t>(p.shape, seq);
     }
     run_units[threadIdx.x] = units;
     tc_fence_before();
@@ -1129,12 +1129,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             if (u < end) {
                 const int who = __ffs(__ballot_sync(kFullMask, upto > u)) - 1;
                 cum = __shfl_sync(kFullMask, upto - mine, who);
-                int run = who * 12;
-                while (cum + run_units[run] <= u) cum += run_units[run++];
-                s = run * per;
+                // the same among that lane's 12 runs
+                const int64_t own = lane < 12 ? run_units[who * 12 + lane] : 0;
+                int64_t up = own;
+                for (int d = 1; d < 12; d <<= 1) {
+                    const int64_t x = __shfl_up_sync(kFullMask, up, d);
+                    if (lane >= d) up += x;
+                }
+                const int run = __ffs(__ballot_sync(kFullMask, cum + up > u)) - 1;
+                cum += __shfl_sync(kFullMask, up - own, run);
+                s = (who * 12 + run) * per;
                 while (per > 1) {
                     const ChunkSeq seq = chunk_load_seq(p, s, false);
-                    const int64_t x = p.fits_32 ? chunk_units<int32_t>(p, seq) : chunk_units<int64_t>(p, seq);
+                    const int64_t x = p.fits_32 ? chunk_units<int32_t>(p.shape, seq) : chunk_units<int64_t>(p.shape, seq);
                     if (cum + x > u) break;
                     cum += x;
                     ++s;

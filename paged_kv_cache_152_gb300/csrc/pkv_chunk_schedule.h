@@ -51,8 +51,8 @@ PKV_HD int64_t chunk_max64(int64_t a, int64_t b) { return a > b ? a : b; }
 PKV_HD int64_t chunk_min64(int64_t a, int64_t b) { return a < b ? a : b; }
 
 PKV_HD int chunk_items(const ChunkShape &c, const ChunkSeq &s) {
-    const int w = 2 * c.tile_tokens;
-    return (int)(((int64_t)s.n + w - 1) / w);
+    const unsigned w = 2u * c.tile_tokens;
+    return (int)((s.n + w - 1) / w);
 }
 
 // The positions that some row of item i sees.
