@@ -28,8 +28,6 @@ constexpr uint32_t kWaitTries = 1u << 20;
 // Units of an item besides its positions: what a piece costs before its first
 // step (queries in, output out), in positions.
 constexpr int kOverhead = 256;
-// Items are cut at multiples of 2^this steps.
-constexpr int kQuantumShift = 1;
 
 // The workspace: records of the items cut between CTAs, the parts' (maximum,
 // sum) and outputs.
@@ -148,7 +146,7 @@ extern "C" int pkv_paged_attention_chunk(void *out, const void *query, const voi
     p.shape.causal = causal != 0;
     p.shape.window = std::min(window, 1 << 30);  // no context is longer
     p.shape.overhead = kOverhead;
-    p.shape.quantum_shift = kQuantumShift;
+    p.shape.quantum_shift = 0;  // the kernel goes by the share
     p.fits_32 = chunk_fits_32(p.shape, num_tokens, num_seqs, (int64_t)max_blocks_per_seq * block_size);
     p.num_tokens = num_tokens;
     p.num_seqs = num_seqs;
@@ -176,7 +174,7 @@ extern "C" int pkv_paged_attention_chunk(void *out, const void *query, const voi
         return PKV_ERR_CUDA;
     }
     // No table is long enough for an item to be cut: nothing to join.
-    if ((int64_t)max_blocks_per_seq * block_size <= ((int64_t)kChunkTile << kQuantumShift) || num_ctas == 1) return PKV_OK;
+    if ((int64_t)max_blocks_per_seq * block_size <= kChunkTile || num_ctas == 1) return PKV_OK;
     fn = d64 ? reinterpret_cast<const void *>(&chunk_join_kernel<64>)
              : reinterpret_cast<const void *>(&chunk_join_kernel<128>);
     if (launch_pdl(fn, dim3((unsigned)num_ctas, (unsigned)(ws.part_rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0,

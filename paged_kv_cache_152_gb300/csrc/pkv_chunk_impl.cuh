@@ -412,7 +412,8 @@ struct ChunkLoader {
     // The share [u, end) of the line; cum = units before sequence s.
     __device__ bool walk(int s, int64_t cum, int64_t u, int64_t end) {
         if (u >= end) return true;
-        const ChunkShape &c = p.shape;
+        ChunkShape c = p.shape;
+        c.quantum_shift = chunk_quantum_shift(shares);
         ChunkSeq q = chunk_load_seq(p, s, false);
         const ChunkPlace at = p.fits_32 ? chunk_locate<int32_t>(c, q, u - cum, lane) : chunk_locate<int64_t>(c, q, u - cum, lane);
         int head = at.kv_head, item = at.item, off = at.offset, items = chunk_items(c, q);
@@ -653,8 +654,7 @@ struct ChunkProducts {
             kp.move(k < 0 ? 1 : 2);
             vp.move(k + 2 >= n ? 1 : 2);
         }
-        // the other softmax warpgroup reads this slot's output, too
-        if (single && (n > 1 || (slot == 0 && uniform(pc.partial)))) ++merges;
+        if (single && n > 1) ++merges;  // the other softmax warpgroup reads this slot's output, too
         ring = vp;
         theirs += other;
         return true;
@@ -914,7 +914,7 @@ struct ChunkSoftmax {
     // the instruction cache.
     __device__ bool piece(const ChunkPiece &pc, bool dry) {
         const int first = dry ? 0 : pc.first[slot], end = dry ? 1 : pc.end[slot], stride = pc.single ? 2 : 1;
-        const bool both = pc.single && pc.t1 - pc.t0 > 1, merge = both || (pc.single && pc.partial);
+        const bool merge = pc.single && pc.t1 - pc.t0 > 1;
         // this thread's row: a token of the item and a query head
         const int token = row / p.group + (pc.single ? 0 : slot * p.shape.tile_tokens);
         const int head = pc.kv_head * p.group + row % p.group;
@@ -1002,7 +1002,7 @@ struct ChunkSoftmax {
         for (int c = 0; any && c < D / 64; ++c) {
             uint32_t oa[32], ob[32];
             tmem_ld32(o_at(0) + c0 + c * 32, oa);
-            tmem_ld32(o_at(both ? 1 : 0) + c0 + c * 32, ob);  // (once more with the weight 0 where there is one slot)
+            tmem_ld32(o_at(1) + c0 + c * 32, ob);
             tmem_wait_ld();
             tmem_pin32(oa);
             tmem_pin32(ob);
@@ -1022,8 +1022,8 @@ struct ChunkSoftmax {
             }
         }
         tc_fence_before();
-        if (mine) arrive(PKV_CTL(o_free) + 8 * slot);
-        if (both || slot == 1) arrive(PKV_CTL(o_cross) + 8 * (1 - slot));
+        arrive(PKV_CTL(o_free) + 8 * slot);
+        arrive(PKV_CTL(o_cross) + 8 * (1 - slot));
         if (live) {
             if (pc.partial) *part_ml = make_float2(high, sum);
             if (pc.odd) {
@@ -1191,6 +1191,8 @@ __global__ void __launch_bounds__(kJoinThreads, 3) chunk_join_kernel(const __gri
     launch_dependents();
     const ChunkPart item = p.parts[blockIdx.x];
     if (!item.valid) return;
+    ChunkShape shape = p.shape;
+    shape.quantum_shift = chunk_quantum_shift(item.shares);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     // The tile and this warp's rows of it.
     const int at = blockIdx.y * kJoinRows + warp * R, slot = at / kChunkRows, row0 = at % kChunkRows;
@@ -1210,7 +1212,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) chunk_join_kernel(const __gri
         for (int cta = blockIdx.x; cta <= item.cta1; cta += 32) {
             int a = 0, b = 0;
             if (cta + lane <= item.cta1)
-                chunk_part(p.shape, item.shares, cta + lane, item.start, item.lo, item.hi, &a, &b);
+                chunk_part(shape, item.shares, cta + lane, item.start, item.lo, item.hi, &a, &b);
             const int part = 2 * (cta + lane) + (a == 0 ? 1 : 0);
             unsigned has = __ballot_sync(kFullMask, b > a);
             float2 ml[R];

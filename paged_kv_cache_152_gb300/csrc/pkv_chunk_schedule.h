@@ -142,6 +142,17 @@ PKV_HD ChunkShares chunk_shares(int64_t total, int shares) {
 // Where share k starts.
 PKV_HD int64_t chunk_share(const ChunkShares &s, int k) { return s.q * k + (k < s.r ? k : s.r); }
 
+// Where items may be cut: at multiples of 2^this steps, a sixteenth of a share
+// or less (up to 8 steps).  A cut off the even share costs less than the pieces
+// of a short item: 64 sequences of 5 new tokens over 50 to 900 take 126.8 us with
+// cuts at every second step and 117.4 at every fourth (77 steps a share), but
+// 8 x 12 heads of 1500 positions 39.8 and 42.3 (13 steps a share), 38.7 at every
+// step.
+PKV_HD int chunk_quantum_shift(const ChunkShares &s) {
+    const int64_t sixteenth = s.q / (16 * kChunkTile);
+    return sixteenth >= 8 ? 3 : sixteenth >= 4 ? 2 : sixteenth >= 2 ? 1 : 0;
+}
+
 // The share that holds unit x.
 PKV_HD int chunk_share_of(const ChunkShares &s, int64_t x) {
     const int64_t longer = (s.q + 1) * s.r;
