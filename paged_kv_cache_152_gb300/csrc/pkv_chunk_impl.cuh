@@ -636,11 +636,11 @@ struct ChunkProducts {
                 tc_fence_after();
                 if (pv) weighted(v_st, k == first);
                 if (qk) scores(buffer, k_st);
+                ++mine;  // (a commit waits for its place behind the products)
+                if (lane == 0) *(volatile uint32_t *)&ctl.issued[slot] = mine;
                 // what a softmax waits for first
                 if (qk) umma_commit(PKV_CTL(s_full) + 8 * slot);
                 if (pv && k == last) umma_commit(PKV_CTL(o_full) + 8 * slot);
-                ++mine;
-                if (lane == 0) *(volatile uint32_t *)&ctl.issued[slot] = mine;
                 if (pv) umma_commit(PKV_CTL(empty) + 8 * v_st);
                 if (qk) umma_commit(PKV_CTL(empty) + 8 * k_st);
                 if (qk && k + 1 == last) umma_commit(PKV_CTL(q_empty) + 8 * buffer);
@@ -894,19 +894,19 @@ struct ChunkSoftmax {
         return true;
     }
 
+    // Rows go out a thread each, in whole sectors: a store's lanes are on 32
+    // different lines, so its cost goes by their number.
     __device__ void store_out(__half *dst, const uint32_t (&o)[32], float inv) {
+        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float f[8];
+        for (int i = 0; i < 16; ++i)
+            w[i] = pack_half2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(o[8 * i + j]) * inv;
-            reinterpret_cast<uint4 *>(dst)[i] = pack8(f);
-        }
+        for (int i = 0; i < 2; ++i) store_32(dst + 16 * i, w + 8 * i);
     }
     __device__ void store_part(float *dst, const uint32_t (&o)[32]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        for (int i = 0; i < 4; ++i) store_32(dst + 8 * i, o + 8 * i);
     }
 
     // The dry piece is one dry step: run while the first copies are on their way,
