@@ -791,14 +791,9 @@ struct ChunkSoftmax {
     __device__ uint32_t o_at(int s) { return tmem + 2 * kChunkTile + s * D; }
 
     // One step: scores -> weights, in place in tensor memory.
-    // A dry step works on whatever the output's columns hold, waits for nothing and
-    // tells nobody.
-    __device__ bool step(int col0, int row_lo, int row_hi, bool first, bool any, bool dry) {
-        const uint32_t s_cols = dry ? o_at(slot) : s_at();
-        if (!dry) {
-            if (!wait(PKV_CTL(s_full) + 8 * slot, s_uses & 1)) return false;
-            ++s_uses;
-        }
+    __device__ bool step(int col0, int row_lo, int row_hi, bool first, bool any) {
+        if (!wait(PKV_CTL(s_full) + 8 * slot, s_uses & 1)) return false;
+        ++s_uses;
         if (!any) {  // no row of this warp is one of the item's: their weights may be anything
             arrive(PKV_CTL(p_full) + 8 * slot);
             return true;
@@ -812,14 +807,14 @@ struct ChunkSoftmax {
 #pragma unroll 1
             for (int c = 0; c < kChunkTile; c += 32) {
                 uint32_t x[32];
-                tmem_ld32(s_cols + c, x);
+                tmem_ld32(s_at() + c, x);
                 tmem_wait_ld();
                 tmem_pin32(x);
                 const int a = row_lo - col0 - c;
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     if ((unsigned)(i - a) >= n) x[i] = 0xff800000u;
-                tmem_st32(s_cols + c, x);
+                tmem_st32(s_at() + c, x);
             }
             tmem_wait_st();
         }
@@ -840,7 +835,7 @@ struct ChunkSoftmax {
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             uint32_t s[4][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(s_cols + c * 32, s[c]);
+            for (int c = 0; c < 4; ++c) tmem_ld32(s_at() + c * 32, s[c]);
             tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_pin32(s[c]);
@@ -886,11 +881,11 @@ struct ChunkSoftmax {
             if (move) m = next;
         }
         l += sum;
-        tmem_st32(s_cols, w[0]);
-        tmem_st32(s_cols + 32, w[1]);
+        tmem_st32(s_at(), w[0]);
+        tmem_st32(s_at() + 32, w[1]);
         tmem_wait_st();
         tc_fence_before();
-        if (!dry) arrive(PKV_CTL(p_full) + 8 * slot);
+        arrive(PKV_CTL(p_full) + 8 * slot);
         return true;
     }
 
@@ -909,11 +904,8 @@ struct ChunkSoftmax {
         for (int i = 0; i < 4; ++i) store_32(dst + 8 * i, o + 8 * i);
     }
 
-    // The dry piece is one dry step: run while the first copies are on their way,
-    // it brings the step's code, too long to be fetched while a score waits, into
-    // the instruction cache.
-    __device__ bool piece(const ChunkPiece &pc, bool dry) {
-        const int first = dry ? 0 : pc.first[slot], end = dry ? 1 : pc.end[slot], stride = pc.single ? 2 : 1;
+    __device__ bool piece(const ChunkPiece &pc) {
+        const int first = pc.first[slot], end = pc.end[slot], stride = pc.single ? 2 : 1;
         const bool merge = pc.single && pc.t1 - pc.t0 > 1;
         // this thread's row: a token of the item and a query head
         const int token = row / p.group + (pc.single ? 0 : slot * p.shape.tile_tokens);
@@ -929,14 +921,12 @@ struct ChunkSoftmax {
                 if (p.shape.window) row_lo = min(max(pos - p.shape.window + 1, 0), row_hi);
             }
         }
-        if (dry) row_lo = 0, row_hi = 1;  // with the mask
         m = 0.f;
         l = 0.f;
-        const bool any = dry || __any_sync(kFullMask, live);
+        const bool any = __any_sync(kFullMask, live);
 #pragma unroll 1
         for (int t = first; t < end; t += stride)
-            if (!step(t * kChunkTile, row_lo, row_hi, t == first, any, dry)) return false;
-        if (dry) return true;
+            if (!step(t * kChunkTile, row_lo, row_hi, t == first, any)) return false;
 
         __half *out = p.out + ((int64_t)(pc.row0 + token) * p.num_heads + head) * D;
         float *part = p.part_o + ((int64_t)pc.part * p.part_rows + (pc.single ? row : slot * kChunkRows + row)) * D;
@@ -1037,15 +1027,12 @@ struct ChunkSoftmax {
     }
 
     __device__ void run() {
-#pragma unroll 1
-        for (int k = -1;; ++k) {
-            const bool dry = k < 0;
-            const uint32_t at = dry ? 0 : k % kChunkPieces;
-            if (!wait(PKV_CTL(piece_full) + 8 * at, dry ? 0 : k / kChunkPieces & 1)) return;
+        for (uint32_t k = 0;; ++k) {
+            const uint32_t at = k % kChunkPieces;
+            if (!wait(PKV_CTL(piece_full) + 8 * at, k / kChunkPieces & 1)) return;
             const ChunkPiece &pc = ctl.piece[at];
-            if (pc.last) return;
-            if (!piece(pc, dry)) return;
-            if (!dry) arrive(PKV_CTL(piece_empty) + 8 * at);
+            if (pc.last || !piece(pc)) return;
+            arrive(PKV_CTL(piece_empty) + 8 * at);
         }
     }
 };
