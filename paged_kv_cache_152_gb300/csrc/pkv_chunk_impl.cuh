@@ -890,12 +890,19 @@ struct ChunkSoftmax {
     }
 
     // Rows go out a thread each, in whole sectors: a store's lanes are on 32
-    // different lines, so its cost goes by their number.
+    // different lines, so its cost goes by their number.  An output that is
+    // aligned to 16 bytes only takes twice as many.
     __device__ void store_out(__half *dst, const uint32_t (&o)[32], float inv) {
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             w[i] = pack_half2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+        if (reinterpret_cast<uintptr_t>(dst) & 16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) store_32(dst + 16 * i, w + 8 * i);
     }

@@ -379,6 +379,30 @@ def test_blocks_far_into_a_large_pool(pkv):
     c.check(c.call(pkv))
 
 
+def _shifted(t, bytes):
+    """The same tensor at an address `bytes` past a 256-byte boundary."""
+    n = bytes // t.element_size()
+    room = torch.empty(t.numel() + n, dtype=t.dtype, device=t.device)
+    view = room[n:].view(t.shape)
+    view.copy_(t)
+    assert view.data_ptr() % 256 == bytes
+    return view
+
+
+@pytest.mark.parametrize("h,hkv,d", [(4, 2, 64), (8, 1, 128)])
+def test_addresses_of_the_least_alignment(pkv, h, hkv, d):
+    """16 bytes past a boundary: every tensor, for items of one tile and of
+    two, whole ones and ones in parts, and rows that see nothing."""
+    c = Case(27, h, hkv, d, 16, [(3, 40), (140, 900), (1, 2000), (200, 150), (300, 300)]).gpu()
+    expect = c.oracle()
+    for k in ("q", "kc", "vc"):
+        c.t[k] = _shifted(c.t[k], 16)
+    for k in ("tables", "lens", "starts"):
+        c.t[k] = _shifted(c.t[k], 4)
+    for num_ctas in (0, 3):
+        c.check(c.call(pkv, out=_shifted(c.out, 16), num_ctas=num_ctas), expect)
+
+
 def _refuses(pkv, c, code, rows=None, **changes):
     old = dict(c.t)
     c.t.update(changes)
