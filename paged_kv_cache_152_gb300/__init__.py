@@ -502,7 +502,8 @@ def paged_attention_chunk(out, query, key_cache, value_cache, block_tables, cont
     out, query: fp16 [T][H][D]; key_cache, value_cache: fp16 [NB][Hkv][bs][D];
     block_tables: int32 [N][MB]; context_lens: int32 [N]; query_starts: int32
     [N + 1]; window: 0, or how many positions back a row sees (itself
-    included).  A workspace (new_chunk_workspace) is allocated when None.
+    included).  A workspace (new_chunk_workspace) is allocated when None, on
+    the call's stream.
     """
     import torch
     f16, i32 = torch.float16, torch.int32
@@ -522,7 +523,9 @@ def paged_attention_chunk(out, query, key_cache, value_cache, block_tables, cont
         ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
     elif t and n:
         ws_bytes = _chunk_workspace(t, h, hkv, d, num_ctas, index)
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=query.device)
+        # Of the stream that uses it: freed on return, it then goes to that stream's later work only.
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=query.device)
         ws = workspace.data_ptr()
     _launch(load().pkv_paged_attention_chunk, "pkv_paged_attention_chunk", index, stream,
             (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),

@@ -361,6 +361,29 @@ def test_two_calls_at_once(pkv):
         c.check(c.out, e)
 
 
+def test_own_workspace_stays_with_its_stream(pkv, monkeypatch):
+    """The workspace a call allocates is not handed to the current stream's
+    work while a call on another stream may still use it."""
+    c = Case(28, 8, 2, 128, 16, [(1, 2000), (100, 400)]).gpu()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    taken, empty = [], torch.empty
+
+    def spy(*args, **kw):
+        taken.append(empty(*args, **kw))
+        return taken[-1]
+
+    monkeypatch.setattr(torch, "empty", spy)
+    c.call(pkv, stream=side)
+    monkeypatch.undo()
+    assert len(taken) == 1
+    size, address = taken[0].numel(), taken.pop().data_ptr()
+    later = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert all(x.data_ptr() != address for x in later)
+    side.synchronize()
+    c.check(c.out)
+
+
 def test_blocks_far_into_a_large_pool(pkv):
     """Element offsets past 2^32 in each cache (8.6 GB, only the used blocks written)."""
     hkv, bs, d = 8, 16, 128
