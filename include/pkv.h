@@ -432,10 +432,11 @@ int pkv_paged_attention_decode_noalloc(void *out, const void *query,
  * over the visible t: with causal != 0, t <= p, and with window > 0 also
  * t > p - window; with causal == 0 every t < L, whatever n is (the cache then
  * holds another sequence's states, for instance an encoder's, and window must
- * be 0).  A row that sees no position (L == 0, or p < 0 where n > L) gives
- * zeros.  Scores, softmax statistics and the weighted sum are held in fp32;
- * the softmax weights are rounded to fp16 for the second product, and the
- * result is rounded to fp16, to nearest even.
+ * be 0).  A row that sees no position (L == 0, or p < 0 where n > L), or none
+ * whose score is above minus infinity, gives zeros.  Scores, softmax
+ * statistics and the weighted sum are held in fp32; the softmax weights are
+ * rounded to fp16 for the second product, and the result is rounded to fp16,
+ * to nearest even.
  *
  * What no row of a sequence sees is not read for the result: table entries
  * past ceil(L / block_size), or of blocks that lie wholly before every
