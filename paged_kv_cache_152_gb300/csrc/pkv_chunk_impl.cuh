@@ -123,7 +123,7 @@ struct ChunkConfig {
     static constexpr int kStages = D == 128 ? 5 : 10;  // 160 KB of K and V in flight
     struct Control {
         uint64_t full[kStages], empty[kStages], edge[kStages], guard[kStages];
-        uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], o_cross[2];
+        uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], o_free[2], o_cross[2];
         uint64_t x_full, x_empty, drain[2];
         uint64_t piece_full[kChunkPieces], piece_empty[kChunkPieces];
         ChunkPiece piece[kChunkPieces];
@@ -580,9 +580,17 @@ struct ChunkProducts {
                        umma_idesc_f16(128, kChunkTile, false));
     }
 
-    // O of the slot (+)= P V, where P and V are there.
-    __device__ void weighted(uint32_t st, bool begins) {
-        umma_weighted(o_tmem, s_tmem, v_low + st * (Cfg::kTileBytes >> 4), umma_idesc_f16(128, D, true), !begins);
+    // O of the slot (+)= P V, in halves of the step's positions, each as soon as its weights are there.
+    __device__ bool weighted(uint32_t st, bool begins) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            if (!wait(PKV_CTL(p_full) + 8 * (2 * slot + h), p_uses & 1)) return false;
+            tc_fence_after();
+            umma_weighted(o_tmem, s_tmem + 32 * h, v_low + st * (Cfg::kTileBytes >> 4) + 512 * h,
+                          umma_idesc_f16(128, D, true), !begins || h);
+        }
+        ++p_uses;
+        return true;
     }
 
     __device__ bool piece(const ChunkPiece &pc) {
@@ -626,15 +634,13 @@ struct ChunkProducts {
                     if (!wait(PKV_CTL(o_cross) + 8 * slot, (merges & 1) ^ 1)) return false;
                     ++o_uses;
                 }
-                if (!wait(PKV_CTL(p_full) + 8 * slot, p_uses & 1)) return false;
-                ++p_uses;
             }
             if (pv || qk) {
                 // slot 0's first batch, slot 1's first, slot 0's second ...
                 if (!turn(theirs + min(batch + slot, other))) return false;
                 ++batch;
+                if (pv && !weighted(v_st, k == first)) return false;
                 tc_fence_after();
-                if (pv) weighted(v_st, k == first);
                 if (qk) scores(buffer, k_st);
                 ++mine;  // (a commit waits for its place behind the products)
                 if (lane == 0) *(volatile uint32_t *)&ctl.issued[slot] = mine;
@@ -795,7 +801,8 @@ struct ChunkSoftmax {
         if (!wait(PKV_CTL(s_full) + 8 * slot, s_uses & 1)) return false;
         ++s_uses;
         if (!any) {  // no row of this warp is one of the item's: their weights may be anything
-            arrive(PKV_CTL(p_full) + 8 * slot);
+            arrive(PKV_CTL(p_full) + 16 * slot);
+            arrive(PKV_CTL(p_full) + 16 * slot + 8);
             return true;
         }
         tc_fence_after();
@@ -818,48 +825,28 @@ struct ChunkSoftmax {
             }
             tmem_wait_st();
         }
-        // The weights are computed with the maximum as it stands while the step's own
-        // is found, so that neither waits for the other.  The maximum moves, and the
-        // step is done over, only when it rises by more than a factor 2^14 of the
-        // weights (fp16 carries them up to 2^15); a piece's first step guesses 0 and
-        // is done over unless the maximum lies in [0, 14], so that the largest
-        // weight of a row is never below 1.
-        uint32_t w[2][32];
-        float sum;
         const float sc = p.scale_log2;
-#pragma unroll 1
-        for (bool again = false;; again = true) {
-            const float base = m == -INFINITY ? 0.f : -m * sc;
-            const uint64_t scale2 = pack2(sc, sc), base2 = pack2(base, base);
-            uint64_t sum2[2] = {};
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            uint32_t s[4][32];
+        uint32_t s[4][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(s_at() + c * 32, s[c]);
-            tmem_wait_ld();
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_at() + c * 32, s[c]);
+        tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_pin32(s[c]);
+        for (int c = 0; c < 4; ++c) tmem_pin32(s[c]);
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
-                const float x = __uint_as_float(s[i / 16][2 * (i % 16)]), y = __uint_as_float(s[i / 16][2 * (i % 16) + 1]);
-                top[i % 4] = fmaxf(top[i % 4], fmaxf(x, y));
-                float a, b;
-                unpack2(fma2(pack2(x, y), scale2, base2), a, b);
-                a = ex2(a);
-                b = ex2(b);
-                sum2[i % 2] = add2(sum2[i % 2], pack2(a, b));
-                w[i / 32][i % 32] = pack_half2(a, b);  // the second product's operand type; the sum has the unrounded weights
-            }
-            float x, y;
-            unpack2(add2(sum2[0], sum2[1]), x, y);
-            sum = x + y;
-            if (again) break;
-            const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), rise = (high - m) * sc;
-            const bool move = row_hi >= 0 && (first ? !(rise >= 0.f && rise <= kMostRise) : rise > kMostRise);
-            if (!__any_sync(kFullMask, move)) break;
-            const float next = first ? high : fmaxf(high, m);
-            if (!first) {
-                const float fade = move ? ex2((m - next) * sc) : 1.f;
+        for (int i = 0; i < 64; ++i)
+            top[i % 4] = fmaxf(top[i % 4], fmaxf(__uint_as_float(s[i / 16][2 * (i % 16)]),
+                                                 __uint_as_float(s[i / 16][2 * (i % 16) + 1])));
+        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        // What the weights are relative to moves only when the maximum rises by more
+        // than a factor 2^14 of the weights (fp16 carries them up to 2^15).
+        if (first) {
+            if (row_hi >= 0) m = high;
+        } else {
+            const bool move = row_hi >= 0 && (high - m) * sc > kMostRise;
+            if (__any_sync(kFullMask, move)) {
+                const float next = fmaxf(high, m), fade = move ? ex2((m - next) * sc) : 1.f;
+                if (move) m = next;
                 l *= fade;
                 const uint64_t fade2 = pack2(fade, fade);
                 // the scores' arrival means every earlier product is complete, O's last one among them
@@ -871,6 +858,7 @@ struct ChunkSoftmax {
                     tmem_pin32(o);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
+                        float x, y;
                         unpack2(mul2(pack2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), fade2), x, y);
                         o[2 * i] = __float_as_uint(x);
                         o[2 * i + 1] = __float_as_uint(y);
@@ -878,14 +866,31 @@ struct ChunkSoftmax {
                     tmem_st32(o_at(slot) + c * 32, o);
                 }
             }
-            if (move) m = next;
         }
-        l += sum;
-        tmem_st32(s_at(), w[0]);
-        tmem_st32(s_at() + 32, w[1]);
-        tmem_wait_st();
-        tc_fence_before();
-        arrive(PKV_CTL(p_full) + 8 * slot);
+        const float base = m == -INFINITY ? 0.f : -m * sc;
+        const uint64_t scale2 = pack2(sc, sc), base2 = pack2(base, base);
+        uint64_t sum2[2] = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const uint32_t *x = &s[2 * h + i / 16][2 * (i % 16)];
+                float a, b;
+                unpack2(fma2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, base2), a, b);
+                a = ex2(a);
+                b = ex2(b);
+                sum2[i % 2] = add2(sum2[i % 2], pack2(a, b));
+                w[i] = pack_half2(a, b);  // the second product's operand type; the sum has the unrounded weights
+            }
+            tmem_st32(s_at() + 32 * h, w);
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(PKV_CTL(p_full) + 16 * slot + 8 * h);
+        }
+        float x, y;
+        unpack2(add2(sum2[0], sum2[1]), x, y);
+        l += x + y;
         return true;
     }
 
@@ -1066,7 +1071,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             mbar_init(smem_addr(&ctl.q_full[i]), 1);
             mbar_init(smem_addr(&ctl.q_empty[i]), 2);
             mbar_init(smem_addr(&ctl.s_full[i]), 1);
-            mbar_init(smem_addr(&ctl.p_full[i]), 4);
+            mbar_init(smem_addr(&ctl.p_full[i][0]), 4);
+            mbar_init(smem_addr(&ctl.p_full[i][1]), 4);
             mbar_init(smem_addr(&ctl.o_full[i]), 1);
             mbar_init(smem_addr(&ctl.o_free[i]), 4);
             mbar_init(smem_addr(&ctl.o_cross[i]), 4);

@@ -72,12 +72,11 @@ __device__ __forceinline__ void umma_scores(uint32_t s, uint32_t q, uint32_t k, 
                      : "memory");
 }
 
-// O (tensor memory) = P (tensor memory) . V (shared) (+ O) over 128 rows of V,
+// O (tensor memory) = P (tensor memory) . V (shared) (+ O) over 64 rows of V,
 // 16 at a time: 8 columns of P (fp16 pairs), 2048 bytes of V.
 __device__ __forceinline__ void umma_weighted(uint32_t o, uint32_t p, uint32_t v, uint32_t idesc, bool add) {
     asm volatile(PKV_MMA_HEAD PKV_MMA_TS("0", "0", "p") "setp.eq.u32 p, 0, 0;\n\t" PKV_MMA_TS("8", "128", "p")
-                     PKV_MMA_TS("16", "256", "p") PKV_MMA_TS("24", "384", "p") PKV_MMA_TS("32", "512", "p")
-                         PKV_MMA_TS("40", "640", "p") PKV_MMA_TS("48", "768", "p") PKV_MMA_TS("56", "896", "p") "}" ::"r"(o),
+                     PKV_MMA_TS("16", "256", "p") PKV_MMA_TS("24", "384", "p") "}" ::"r"(o),
                  "r"(p), "r"(v), "r"(idesc), "r"((uint32_t)add), "r"(umma_desc_high(1024))
                  : "memory");
 }
