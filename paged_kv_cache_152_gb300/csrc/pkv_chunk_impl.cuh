@@ -239,7 +239,6 @@ __device__ __forceinline__ bool chunk_mixed(const ChunkPiece &pc, int t) {
 }
 
 // Ring positions of a piece's copies relative to its first: K0 K1 V0 K2 V1 ...
-__device__ __forceinline__ uint32_t chunk_k_at(int k) { return k == 0 ? 0u : 2u * k - 1u; }
 __device__ __forceinline__ uint32_t chunk_v_at(int k, int n) { return k < n - 1 ? 2u * k + 2u : 2u * n - 1u; }
 
 __device__ __forceinline__ int chunk_block(const ChunkParams &p, int seq, int logical) {

@@ -191,13 +191,6 @@ __device__ __forceinline__ float2 unpack_half2(uint32_t v) {
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// One 32-byte store of eight 32-bit words; dst 32-byte aligned.
-__device__ __forceinline__ void store_32(void *dst, const uint32_t *w) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-
 // 8 fp16 values packed in 16 bytes -> 8 floats.
 __device__ __forceinline__ void unpack8(const uint4 &raw, float (&f)[8]) {
     const __half2 *h = reinterpret_cast<const __half2 *>(&raw);

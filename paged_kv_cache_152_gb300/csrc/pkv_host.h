@@ -1,5 +1,6 @@
-// pkv_host.h -- host helpers of the attention entry points: the dynamic
-// shared-memory limit and the tensor maps.
+// pkv_host.h -- host helpers of the chunk attention's entry point: the dynamic
+// shared-memory limit and the tensor maps.  (The decode's are its own, in
+// pkv_decode.cu: its sources stay as they were measured.)
 #ifndef PKV_HOST_H
 #define PKV_HOST_H
 
@@ -71,7 +72,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // promotion: a box is one contiguous run of whole 128-byte lines already,
 // and widening the requests measured ~1% slower (7b 96.1 against 94.8 us).
 inline int encode_cache_map(CUtensorMap *map, const void *cache, int num_blocks, int num_kv_heads, int block_size,
-                     int head_dim, int box_rows, int box_halves) {
+                            int head_dim, int box_rows, int box_halves) {
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode) return PKV_ERR_CUDA;
     const cuuint64_t dims[3] = {64, (cuuint64_t)num_blocks * num_kv_heads * block_size,
