@@ -510,11 +510,11 @@ def paged_attention_chunk(out, query, key_cache, value_cache, block_tables, cont
     index = _checked(((query, f16, "query", 3), (out, f16, "out", 3), (key_cache, f16, "key_cache", 4),
                       (value_cache, f16, "value_cache", 4), (block_tables, i32, "block_tables", 2),
                       (context_lens, i32, "context_lens", 1), (query_starts, i32, "query_starts", 1)))
-    t, h, d = query.shape
-    nb, hkv, bs, d2 = key_cache.shape
+    t, h, d = rows = query.shape
+    nb, hkv, bs, d2 = pool = key_cache.shape
     n, mb = block_tables.shape
-    if out.shape != query.shape or d2 != d or value_cache.shape != key_cache.shape \
-            or context_lens.shape[0] != n or query_starts.shape[0] != n + 1:
+    if out.shape != rows or d2 != d or value_cache.shape != pool or context_lens.shape != (n,) \
+            or query_starts.shape != (n + 1,):
         raise ValueError("inconsistent shapes")
     ws, ws_bytes = None, 0
     if workspace is not None:
@@ -704,14 +704,15 @@ def reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, status=N
 def _rows(t, name, f16):
     """The token stride of fp16 [T][heads][D]: each token's heads contiguous,
     tokens any multiple of 8 elements apart (a view of a projection's output)."""
+    shape = t.shape
     if t.dtype is not f16:
         raise TypeError(f"{name}: expected {f16}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name}: expected 3 dims, got {tuple(t.shape)}")
-    n, h, d = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name}: expected 3 dims, got {tuple(shape)}")
+    n, h, d = shape
+    if t.is_contiguous() and h * d % 8 == 0:
+        return h * d
     stride, sh, sd = t.stride()
-    if sd == 1 and sh == d and n > 1 and stride >= h * d and stride % 8 == 0:
-        return stride
     if n < 2:
         stride = h * d
     if (sd != 1 and d > 1) or (sh != d and h > 1):
@@ -728,14 +729,15 @@ def _rope_tables(t, d, positions, cos_sin, query_weight, key_weight):
     specs, reach, rot = (), 0, 0
     if positions is not None and cos_sin is not None:
         specs = ((positions, torch.int64, "positions", 1), (cos_sin, torch.float32, "cos_sin", 2))
-        if positions.dim() != 1 or cos_sin.dim() != 2 or positions.shape[0] != t:
+        table = cos_sin.shape
+        if positions.shape != (t,) or len(table) != 2:
             raise ValueError("positions, cos_sin: inconsistent shapes")
-        reach, rot = cos_sin.shape
+        reach, rot = table
     elif positions is not None or cos_sin is not None:
         raise ValueError("positions and cos_sin go together")
     for w, name in ((query_weight, "query_weight"), (key_weight, "key_weight")):
         if w is not None:
-            if w.dim() != 1 or w.shape[0] != d:
+            if w.shape != (d,):
                 raise ValueError(f"{name}: inconsistent shapes")
             specs += ((w, torch.float16, name, 1),)
     return specs, reach, rot
@@ -753,8 +755,9 @@ def qk_norm_rope(query_out, key_out, query, key, positions=None, cos_sin=None, q
     f16 = torch.float16
     sq, sk, sqo, sko = _rows(query, "query", f16), _rows(key, "key", f16), _rows(query_out, "query_out", f16), \
         _rows(key_out, "key_out", f16)
-    t, h, d = query.shape
-    if query_out.shape != query.shape or key_out.shape != key.shape or key.shape[0] != t or key.shape[2] != d:
+    t, h, d = rows = query.shape
+    tk, hkv, dk = key_rows = key.shape
+    if query_out.shape != rows or key_out.shape != key_rows or tk != t or dk != d:
         raise ValueError("inconsistent shapes")
     specs, reach, rot = _rope_tables(t, d, positions, cos_sin, query_weight, key_weight)
     index = _checked(((query, None, "query", 3), (key, None, "key", 3), (query_out, None, "query_out", 3),
@@ -762,7 +765,7 @@ def qk_norm_rope(query_out, key_out, query, key, positions=None, cos_sin=None, q
     _launch(load().pkv_qk_norm_rope, "pkv_qk_norm_rope", index, stream,
             (query_out.data_ptr(), sqo, key_out.data_ptr(), sko, query.data_ptr(), sq, key.data_ptr(), sk,
              _address(positions), _address(cos_sin), reach, rot, 1 if interleaved else 0, _address(query_weight),
-             _address(key_weight), float(eps), t, h, key.shape[1], d, _status_address(status, index)))
+             _address(key_weight), float(eps), t, h, hkv, d, _status_address(status, index)))
     return query_out, key_out
 
 
@@ -777,14 +780,15 @@ def qk_norm_rope_and_cache(query_out, query, key, value, key_cache, value_cache,
     f16 = torch.float16
     sq, sk, sv, sqo = _rows(query, "query", f16), _rows(key, "key", f16), _rows(value, "value", f16), \
         _rows(query_out, "query_out", f16)
-    t, h, d = query.shape
+    t, h, d = rows = query.shape
+    key_rows = key.shape
     specs, reach, rot = _rope_tables(t, d, positions, cos_sin, query_weight, key_weight)
     index = _checked(((query, None, "query", 3), (key, None, "key", 3), (value, None, "value", 3),
                       (query_out, None, "query_out", 3), (key_cache, f16, "key_cache", 4),
                       (value_cache, f16, "value_cache", 4), (slot_mapping, torch.int64, "slot_mapping", 1)) + specs)
-    nb, hkv, bs, d2 = key_cache.shape
-    if query_out.shape != query.shape or value.shape != key.shape or key.shape != (t, hkv, d) or d2 != d \
-            or value_cache.shape != key_cache.shape or slot_mapping.shape[0] != t:
+    nb, hkv, bs, d2 = pool = key_cache.shape
+    if query_out.shape != rows or value.shape != key_rows or key_rows != (t, hkv, d) or d2 != d \
+            or value_cache.shape != pool or slot_mapping.shape != (t,):
         raise ValueError("inconsistent shapes")
     _launch(load().pkv_qk_norm_rope_and_cache, "pkv_qk_norm_rope_and_cache", index, stream,
             (query_out.data_ptr(), sqo, query.data_ptr(), sq, key.data_ptr(), sk, value.data_ptr(), sv,
