@@ -610,8 +610,11 @@ struct ChunkProducts {
         const int first = uniform(pc.first[slot]) - t0, end = uniform(pc.end[slot]) - t0, stride = single ? 2 : 1;
         auto takes = [&](int k) { return k >= first && k < end && (!single || ((k - first) & 1) == 0); };
         const int other_first = uniform(pc.first[1 - slot]) - t0, other_end = uniform(pc.end[1 - slot]) - t0;
-        // The other slot's batches in this piece: S of its first step, then one per step.
-        const uint32_t other = other_first < other_end ? (other_end - other_first + stride - 1) / stride + 1 : 0;
+        // The other slot's batches in this piece: S of its first step, then one per
+        // step; with alternate steps S and O of each by themselves, out of turn (its
+        // O would wait for this slot's P).
+        const uint32_t other_steps = other_first < other_end ? (other_end - other_first + stride - 1) / stride : 0;
+        const uint32_t other = single ? 2 * other_steps : other_steps ? other_steps + 1 : 0;
         uint32_t batch = 0;
         const int last = first < end ? (single ? end - 1 - (end - 1 - first & 1) : end - 1) : -1;
         // Queries: a tile of its own each, or one tile for both.  Both warps see every
@@ -647,7 +650,7 @@ struct ChunkProducts {
             }
             if (pv || qk) {
                 // slot 0's first batch, slot 1's first, slot 0's second ...
-                if (!turn(theirs + min(batch + slot, other))) return false;
+                if (!single && !turn(theirs + min(batch + slot, other))) return false;
                 ++batch;
                 if (pv && !weighted(v_st, k == first)) return false;
                 tc_fence_after();
