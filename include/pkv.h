@@ -435,8 +435,9 @@ int pkv_paged_attention_decode_noalloc(void *out, const void *query,
  * be 0).  A row that sees no position (L == 0, or p < 0 where n > L), or none
  * whose score is above minus infinity, gives zeros.  Scores, softmax
  * statistics and the weighted sum are held in fp32; the softmax weights are
- * rounded to fp16 for the second product, and the result is rounded to fp16,
- * to nearest even.
+ * rounded to fp16 for the second product (11 significant bits down to 2^-23 of
+ * the row's largest weight, steps of 2^-33 of it below), and the result is
+ * rounded to fp16, to nearest even.
  *
  * What no row of a sequence sees is not read for the result: table entries
  * past ceil(L / block_size), or of blocks that lie wholly before every

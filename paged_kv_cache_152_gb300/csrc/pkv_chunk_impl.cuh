@@ -2,7 +2,7 @@
 // sequence's newest tokens over its paged cache, on the tensor cores.
 //
 // Mathematics.  Row by row, over steps of 128 cache positions: scores
-// S = Q K^T, a running maximum m and sum l, weights P = 2^(c (S - m)) with
+// S = Q K^T, a running maximum m and sum l, weights P = 2^(c (S - m) + 9) with
 // c = scale * log2(e), O = O * 2^(c (m_old - m)) + P V, and out = O / l.  The
 // group of query heads that share a KV head are rows of one tile, so each step
 // of K and V serves all of them.
@@ -58,7 +58,12 @@ namespace pkv {
 
 constexpr int kChunkThreads = 384;
 constexpr int kChunkRows = 128;   // rows of a query tile
-constexpr float kMostRise = 14.f;  // log2 of the largest weight
+// Weights are 2^(c (S - m) + kWeightLift), held as fp16 for the second product:
+// a row's largest is 2^9 to 2^14, so that one is lost only below 2^-34 of it.  At
+// 1 a long context's small weights would be lost from 2^-25 on but counted in the
+// sum: 131072 positions at e^-17.5 of one are 3.3e-3 of the row.
+constexpr float kWeightLift = 9.f;
+constexpr float kMostRise = 5.f;  // log2 of how far the maximum may rise above m before O is rescaled
 constexpr int kChunkPieces = 4;   // piece descriptors in flight
 // Registers per thread: 384 at launch x 168 = 64512 = 256 x 208 + 128 x 88.
 constexpr int kChunkLaunchRegs = 168;
@@ -87,7 +92,7 @@ struct ChunkParams {
     // A CTA's parts of items that it shares with others: part 2 * CTA + 1 of the
     // item that it begins, 2 * CTA of the one that it does not (chunk_part).
     ChunkPart *parts;      // [CTAs] of the first kind
-    float2 *part_ml;       // [2 * CTAs][2 slots][128 rows] (c * m, l)
+    float2 *part_ml;       // [2 * CTAs][2 slots][128 rows] (top(), l)
     float *part_o;         // [2 * CTAs][part_rows][D], not normalised
     int32_t *status;
     ChunkShape shape;
@@ -804,8 +809,8 @@ struct ChunkSoftmax {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     }
-    // The maximum that a row's sum is relative to; none where it saw nothing.
-    __device__ float top() { return l == 0.f ? -INFINITY : m * p.scale_log2; }
+    // The exponent that a row's sum and output are relative to; none where it saw nothing.
+    __device__ float top() { return l == 0.f ? -INFINITY : fmaf(m, p.scale_log2, -kWeightLift); }
     __device__ uint32_t s_at() { return tmem + slot * kChunkTile; }
     __device__ uint32_t o_at(int s) { return tmem + 2 * kChunkTile + s * D; }
 
@@ -855,7 +860,7 @@ struct ChunkSoftmax {
                                                  __uint_as_float(s[i / 16][2 * (i % 16) + 1])));
         const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         // What the weights are relative to moves only when the maximum rises by more
-        // than a factor 2^14 of the weights (fp16 carries them up to 2^15).
+        // than a factor 2^kMostRise of the weights (fp16 carries them up to 2^15).
         if (first) {
             if (row_hi >= 0) m = high;
         } else {
@@ -883,7 +888,7 @@ struct ChunkSoftmax {
                 }
             }
         }
-        const float base = m == -INFINITY ? 0.f : -m * sc;
+        const float base = m == -INFINITY ? 0.f : fmaf(-m, sc, kWeightLift);  // -top()
         const uint64_t scale2 = pack2(sc, sc), base2 = pack2(base, base);
         uint64_t sum2[2] = {};
 #pragma unroll
