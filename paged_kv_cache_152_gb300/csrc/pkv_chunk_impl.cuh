@@ -59,11 +59,16 @@ namespace pkv {
 constexpr int kChunkThreads = 384;
 constexpr int kChunkRows = 128;   // rows of a query tile
 // Weights are 2^(c (S - m) + kWeightLift), held as fp16 for the second product:
-// a row's largest is 2^9 to 2^14, so that one is lost only below 2^-34 of it.  At
+// a row's largest is 2^9 to 2^15.5, so that one is lost only below 2^-34 of it.  At
 // 1 a long context's small weights would be lost from 2^-25 on but counted in the
 // sum: 131072 positions at e^-17.5 of one are 3.3e-3 of the row.
 constexpr float kWeightLift = 9.f;
-constexpr float kMostRise = 5.f;  // log2 of how far the maximum may rise above m before O is rescaled
+// log2 of how far the maximum may rise above m before O is rescaled.  Less lift and
+// more room to rise saves rescaling where a tile's first step shows a few
+// positions: 2 x 1000 to 4001 tokens with a window of 1024 take 78.0 us with 9 and
+// 6.5, 77.5 with 8 and 7.5, 76.6 with 6 and 9.5; the others are level.
+constexpr float kMostRise = 6.5f;
+constexpr float kFarScore = 1048576.f;  // 2^20: an exponent in fp32 is off by up to 2^-4 from here on
 constexpr int kChunkPieces = 4;   // piece descriptors in flight
 // Registers per thread: 384 at launch x 168 = 64512 = 256 x 208 + 128 x 88.
 constexpr int kChunkLaunchRegs = 168;
@@ -792,6 +797,35 @@ __device__ void chunk_guard(const ChunkParams &p, typename ChunkConfig<D>::Contr
 // ---------------------------------------------------------------------------
 // warps 0-7: softmax and output
 
+// The weights of a step, in place, and their sum, where exponents are so large
+// that c S - c m rounded on the way would leave fp16's range (or the maximum's
+// own weight at 0): the maximum is taken off the scores first, which is exact
+// next to it.  Rare, so out of line; the weights of positions [0, 64) overwrite
+// scores already read.
+__device__ __noinline__ float chunk_far_weights(uint32_t s_at, float m, float sc) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        uint32_t x[2][32], w[32];
+        tmem_ld32(s_at + 64 * h, x[0]);
+        tmem_ld32(s_at + 64 * h + 32, x[1]);
+        tmem_wait_ld();
+        tmem_pin32(x[0]);
+        tmem_pin32(x[1]);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const uint32_t *y = &x[i / 16][2 * (i % 16)];
+            const float a = ex2(fmaf(__uint_as_float(y[0]) - m, sc, kWeightLift));
+            const float b = ex2(fmaf(__uint_as_float(y[1]) - m, sc, kWeightLift));
+            sum += a + b;
+            w[i] = pack_half2(a, b);
+        }
+        tmem_st32(s_at + 32 * h, w);
+        tmem_wait_st();
+    }
+    return sum;
+}
+
 template <int D>
 struct ChunkSoftmax {
     using Cfg = ChunkConfig<D>;
@@ -803,6 +837,7 @@ struct ChunkSoftmax {
     int slot, row, lane;
     uint32_t s_uses = 0, o_uses = 0, merges = 0;
     float m, l;     // what the weights are relative to (an unscaled score) and their sum
+    bool far;       // some row of the warp has an m whose exponent fp32 holds too coarsely
 
     __device__ bool wait(uint32_t bar, uint32_t parity) { return chunk_wait(bar, parity, PKV_CTL(abort), p.wait_tries); }
     __device__ void arrive(uint32_t bar) {
@@ -811,6 +846,7 @@ struct ChunkSoftmax {
     }
     // The exponent that a row's sum and output are relative to; none where it saw nothing.
     __device__ float top() { return l == 0.f ? -INFINITY : fmaf(m, p.scale_log2, -kWeightLift); }
+    __device__ bool look_far() { return __any_sync(kFullMask, fabsf(m * p.scale_log2) >= kFarScore && m != -INFINITY); }
     __device__ uint32_t s_at() { return tmem + slot * kChunkTile; }
     __device__ uint32_t o_at(int s) { return tmem + 2 * kChunkTile + s * D; }
 
@@ -860,15 +896,17 @@ struct ChunkSoftmax {
                                                  __uint_as_float(s[i / 16][2 * (i % 16) + 1])));
         const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         // What the weights are relative to moves only when the maximum rises by more
-        // than a factor 2^kMostRise of the weights (fp16 carries them up to 2^15).
+        // than a factor 2^kMostRise of the weights (fp16 carries them up to 65504).
         if (first) {
             if (row_hi >= 0) m = high;
+            far = look_far();
         } else {
             const bool move = row_hi >= 0 && (high - m) * sc > kMostRise;
             if (__any_sync(kFullMask, move)) {
                 const float next = fmaxf(high, m), fade = move ? ex2((m - next) * sc) : 1.f;
                 if (move) m = next;
                 l *= fade;
+                far = look_far();
                 const uint64_t fade2 = pack2(fade, fade);
                 // the scores' arrival means every earlier product is complete, O's last one among them
 #pragma unroll 1
@@ -889,6 +927,13 @@ struct ChunkSoftmax {
             }
         }
         const float base = m == -INFINITY ? 0.f : fmaf(-m, sc, kWeightLift);  // -top()
+        if (far) {
+            l += chunk_far_weights(s_at(), m == -INFINITY ? 0.f : m, sc);
+            tc_fence_before();
+            arrive(PKV_CTL(p_full) + 16 * slot);
+            arrive(PKV_CTL(p_full) + 16 * slot + 8);
+            return true;
+        }
         const uint64_t scale2 = pack2(sc, sc), base2 = pack2(base, base);
         uint64_t sum2[2] = {};
 #pragma unroll

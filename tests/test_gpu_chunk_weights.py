@@ -1,5 +1,6 @@
 """GPU checks of the chunk attention's softmax weights where one position
-outweighs the others: long contexts whose small weights add up.
+outweighs the others: long contexts whose small weights add up, and scores of
+any size that fp16 inputs reach.
 
 The inputs are such that the result follows from a closed form in fp64: keys
 of two kinds, so every row has two different scores.
@@ -102,3 +103,35 @@ def test_one_position_above_a_long_context(pkv, length, n, num_ctas, d):
         length * 2.0 ** -34 * 1.25
     over = np.abs(got - ref) / tol
     assert over.max() <= 1.0, over.max()
+
+
+@pytest.mark.parametrize("a,b", [(1.0, 1.0), (30.0, 1000.0), (1000.0, 1000.0), (65504.0, 1000.0), (65504.0, 65504.0)])
+@pytest.mark.parametrize("length,n,num_ctas", [(1, 1, 0), (300, 130, 0), (300, 200, 2), (1000, 1, 0), (1000, 1, 1),
+                                               (700, 3, 1)])
+def test_scores_of_any_size(pkv, a, b, length, n, num_ctas):
+    """All keys the same but one: its rows return that position's value (or,
+    for small scores, the mean that the scores give), the others the plain
+    mean, however large the scores are.
+
+    Tolerance: as above; equal scores are equal in fp32 too, and the two
+    differ by 0.6 (one term; exponent's rounding 2^-20, twice) or by more
+    than 1e5, where the smaller weights are zero in any arithmetic."""
+    d, scale = 128, 0.3
+    rng = np.random.default_rng(length + n)
+    at = max(0, length - n // 2 - 1)
+    one = b == 1.0
+    q = torch.zeros(n, 2, d, dtype=torch.float16, device="cuda")
+    keys = torch.zeros(length, d, dtype=torch.float16, device="cuda")
+    width = 1 if one else d
+    q[..., :width] = a
+    keys[:, :width] = -b
+    keys[at, :width] = b
+    score = 2 * float(np.float32(scale)) * a * b * width
+    values = rng.standard_normal((length, d)).astype(np.float16)
+    got = run(pkv, q, keys, torch.from_numpy(values).cuda(), scale, num_ctas, bs=16)
+    values = values.astype(np.float64)
+    ref, spread = two_kinds(values, values[at], at, n, score)
+    tol = 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + (2.0 ** -11 + 2.0 ** -14 + 2.0 ** -18) * spread + length * 2.0 ** -34 * 5.5
+    for h in range(2):
+        over = np.abs(got[:, h] - ref) / tol
+        assert over.max() <= 1.0, over.max()
