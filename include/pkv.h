@@ -869,6 +869,34 @@ int pkv_alloc_load(const void *buf, size_t bytes, pkv_alloc_t **out);
 int pkv_selftest_wait_timeout(int32_t *dev_status, uint64_t limit_ns,
                               pkv_stream_t stream);
 
+/*
+ * The chunk attention's bounded waits.
+ *
+ * pkv_selftest_chunk_waits launches one CTA that waits, with the kernel's own
+ * limits, for a barrier that nothing completes (one warp) and for a counter
+ * that nothing advances (another).  It writes how long each took to give up,
+ * in nanoseconds, to elapsed_ns[0] and [1] (device) and
+ * PKV_ERR_DEVICE_TIMEOUT to dev_status, and returns normally after two
+ * seconds or so.
+ *
+ * pkv_selftest_chunk_give_up is pkv_paged_attention_chunk with waits that give
+ * up after wait_tries failed tries (0 to 2^19, a try takes one to
+ * four microseconds): with a few of them the kernel gives up in mid-work, leaves
+ * out unspecified, writes PKV_ERR_DEVICE_TIMEOUT to dev_status and returns
+ * normally.
+ */
+int pkv_selftest_chunk_waits(int32_t *dev_status, uint64_t *elapsed_ns,
+                             pkv_stream_t stream);
+int pkv_selftest_chunk_give_up(void *out, const void *query,
+                               const void *key_cache, const void *value_cache,
+                               const int32_t *block_tables, int max_blocks_per_seq,
+                               const int32_t *context_lens, const int32_t *query_starts,
+                               int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
+                               int head_dim, int block_size, int num_blocks,
+                               float scale, int causal, int window, int num_ctas,
+                               void *workspace, size_t workspace_bytes,
+                               int32_t *dev_status, pkv_stream_t stream, int wait_tries);
+
 #ifdef __cplusplus
 }
 #endif

@@ -107,6 +107,10 @@ SIGNATURES = {
     "pkv_num_free": (_c_int, [_vp, _intp]),
     "pkv_free_list": (_c_int, [_vp, _i32p, _c_int, _intp]),
     "pkv_selftest_wait_timeout": (_c_int, [_vp, ctypes.c_uint64, _vp]),
+    "pkv_selftest_chunk_waits": (_c_int, [_vp, _vp, _vp]),
+    "pkv_selftest_chunk_give_up": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int,
+                                            _c_int, _c_int, _c_int, _c_int, ctypes.c_float, _c_int, _c_int, _c_int,
+                                            _vp, _c_size, _vp, _vp, _c_int]),
     "pkv_swap_blocks": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_size, _c_int, _c_int, _vp, _vp]),
     "pkv_swap_blocks_layers": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _c_size, _c_int, _c_int,
                                         _vp, _vp]),
@@ -933,6 +937,22 @@ def selftest_wait_timeout(status, limit_ns, stream=None):
     with _one_device((status,), stream):
         rc = load().pkv_selftest_wait_timeout(_status_ptr(status), int(limit_ns), _stream(stream))
     _check(rc, "pkv_selftest_wait_timeout")
+
+
+@_traced
+def selftest_chunk_waits(status, elapsed_ns, stream=None):
+    """pkv_selftest_chunk_waits: the chunk attention's bounded waits give up;
+    elapsed_ns (int64 [2], CUDA) takes how long each took, status (int32 CUDA
+    tensor) PKV_ERR_DEVICE_TIMEOUT."""
+    import torch
+    if status is None:
+        raise ValueError("status is required")
+    _need(elapsed_ns, torch.int64, "elapsed_ns", 1)
+    if elapsed_ns.numel() < 2:
+        raise ValueError("elapsed_ns must hold two int64")
+    with _one_device((status, elapsed_ns), stream):
+        rc = load().pkv_selftest_chunk_waits(_status_ptr(status), _ptr(elapsed_ns), _stream(stream))
+    _check(rc, "pkv_selftest_chunk_waits")
 
 
 # ---------------------------------------------------------------------------

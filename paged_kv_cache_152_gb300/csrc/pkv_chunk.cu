@@ -23,8 +23,10 @@ bool shape_ok(int num_heads, int num_kv_heads, int head_dim) {
            num_heads / num_kv_heads <= kMaxGroup && (head_dim == 64 || head_dim == 128);
 }
 
-// Tries of a bounded device wait: one that fails takes 1.3 us (a suspended mbarrier try), so a second and more.
-constexpr uint32_t kWaitTries = 1u << 20;
+// Tries of a bounded device wait.  One that fails takes 1.3 to 3.8 us (a suspended
+// mbarrier try; kSpinsPerTry looks at a counter, 69 ns each, 3.3 us), so about two
+// seconds.
+constexpr uint32_t kWaitTries = 1u << 19;
 // Units of an item besides its positions: what a piece costs before its first
 // step (queries in, output out), in positions.  With 128, 192, 256, 320, 384 of
 // them: 64 x 5 tokens over 50 to 900 take 129, 110, 113, 114, 118 us, 28 single
@@ -85,26 +87,12 @@ bool registers_add_up(const void *fn) {
     return a.numRegs == kChunkLaunchRegs;
 }
 
-}  // namespace
-}  // namespace pkv
-
-using namespace pkv;
-
-extern "C" size_t pkv_chunk_workspace_size(int num_tokens, int num_heads, int num_kv_heads, int head_dim,
-                                           int num_ctas) {
-    if (num_tokens < 0 || num_ctas < 0 || num_ctas > kMaxCtas || !shape_ok(num_heads, num_kv_heads, head_dim))
-        return 0;
-    if (num_ctas == 0 && default_ctas(&num_ctas) != PKV_OK) return 0;
-    return ChunkWorkspace::plan(num_tokens, num_heads / num_kv_heads, head_dim, num_ctas).total;
-}
-
-extern "C" int pkv_paged_attention_chunk(void *out, const void *query, const void *key_cache,
-                                         const void *value_cache, const int32_t *block_tables,
-                                         int max_blocks_per_seq, const int32_t *context_lens,
-                                         const int32_t *query_starts, int num_tokens, int num_seqs, int num_heads,
-                                         int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
-                                         int causal, int window, int num_ctas, void *workspace,
-                                         size_t workspace_bytes, int32_t *dev_status, pkv_stream_t stream) {
+// A call whose waits give up after wait_tries tries.
+int call(void *out, const void *query, const void *key_cache, const void *value_cache, const int32_t *block_tables,
+         int max_blocks_per_seq, const int32_t *context_lens, const int32_t *query_starts, int num_tokens,
+         int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+         int causal, int window, int num_ctas, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+         pkv_stream_t stream, uint32_t wait_tries) {
     if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
     if (num_tokens < 0 || num_seqs < 0 || num_seqs > kMaxSeqs || max_blocks_per_seq < 1 || num_blocks < 1 ||
         num_ctas < 0 || num_ctas > kMaxCtas || block_size < 1)
@@ -160,7 +148,7 @@ extern "C" int pkv_paged_attention_chunk(void *out, const void *query, const voi
     p.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : 7;
     p.part_rows = ws.part_rows;
     p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
-    p.wait_tries = kWaitTries;
+    p.wait_tries = wait_tries;
 
     const bool d64 = head_dim == 64;
     const void *fn = d64 ? reinterpret_cast<const void *>(&chunk_kernel<64>)
@@ -186,4 +174,49 @@ extern "C" int pkv_paged_attention_chunk(void *out, const void *query, const voi
         return PKV_ERR_CUDA;
     }
     return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" size_t pkv_chunk_workspace_size(int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                           int num_ctas) {
+    if (num_tokens < 0 || num_ctas < 0 || num_ctas > kMaxCtas || !shape_ok(num_heads, num_kv_heads, head_dim))
+        return 0;
+    if (num_ctas == 0 && default_ctas(&num_ctas) != PKV_OK) return 0;
+    return ChunkWorkspace::plan(num_tokens, num_heads / num_kv_heads, head_dim, num_ctas).total;
+}
+
+extern "C" int pkv_paged_attention_chunk(void *out, const void *query, const void *key_cache,
+                                         const void *value_cache, const int32_t *block_tables,
+                                         int max_blocks_per_seq, const int32_t *context_lens,
+                                         const int32_t *query_starts, int num_tokens, int num_seqs, int num_heads,
+                                         int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                         float scale, int causal, int window, int num_ctas, void *workspace,
+                                         size_t workspace_bytes, int32_t *dev_status, pkv_stream_t stream) {
+    return call(out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens, query_starts,
+                num_tokens, num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, causal, window,
+                num_ctas, workspace, workspace_bytes, dev_status, stream, kWaitTries);
+}
+
+extern "C" int pkv_selftest_chunk_give_up(void *out, const void *query, const void *key_cache,
+                                          const void *value_cache, const int32_t *block_tables,
+                                          int max_blocks_per_seq, const int32_t *context_lens,
+                                          const int32_t *query_starts, int num_tokens, int num_seqs, int num_heads,
+                                          int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                          float scale, int causal, int window, int num_ctas, void *workspace,
+                                          size_t workspace_bytes, int32_t *dev_status, pkv_stream_t stream,
+                                          int wait_tries) {
+    if (wait_tries < 0 || (uint32_t)wait_tries > kWaitTries) return PKV_ERR_INVALID_ARG;
+    return call(out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens, query_starts,
+                num_tokens, num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, causal, window,
+                num_ctas, workspace, workspace_bytes, dev_status, stream, (uint32_t)wait_tries);
+}
+
+extern "C" int pkv_selftest_chunk_waits(int32_t *dev_status, uint64_t *elapsed_ns, pkv_stream_t stream) {
+    if (!dev_status || !elapsed_ns) return PKV_ERR_INVALID_ARG;
+    chunk_waits_selftest_kernel<<<1, 64, 0, reinterpret_cast<cudaStream_t>(stream)>>>(dev_status, elapsed_ns, kWaitTries);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

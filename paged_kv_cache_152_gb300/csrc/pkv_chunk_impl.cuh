@@ -188,6 +188,24 @@ __device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, uint32
     return true;
 }
 
+// A bounded wait for a counter in shared memory, the same otherwise.  A try is
+// two loads and a vote, far less than a suspended one: kSpinsPerTry of them count
+// as one.
+constexpr uint32_t kSpinsPerTry = 48;
+__device__ __forceinline__ bool chunk_wait_count(uint32_t counter, uint32_t value, uint32_t abort, uint32_t limit) {
+#pragma unroll 1
+    for (uint32_t i = 0;; ++i) {
+        uint32_t x, gone;
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(x) : "r"(counter) : "memory");
+        if (__all_sync(kFullMask, (int)(x - value) >= 0)) return true;
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(gone) : "r"(abort) : "memory");
+        if (gone || i >= limit * kSpinsPerTry) {
+            asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1) : "memory");
+            return false;
+        }
+    }
+}
+
 __device__ __noinline__ void chunk_drain(uint32_t bar, uint32_t parity) {
     mbar_wait_bounded(bar, parity, kWaitLimitNs / 8);
 }
@@ -582,16 +600,7 @@ struct ChunkProducts {
     // and then both do their softmax, with the tensor cores idle.  A slot waits
     // until the other has issued so many batches in all.
     __device__ bool turn(uint32_t batches) {
-        volatile uint32_t *issued = &ctl.issued[1 - slot];
-        volatile int *abort = &ctl.abort;
-#pragma unroll 1
-        for (uint32_t i = 0; !__all_sync(kFullMask, (int)(*issued - batches) >= 0); ++i) {
-            if (*abort || i >= p.wait_tries) {
-                *abort = 1;
-                return false;
-            }
-        }
-        return true;
+        return chunk_wait_count(PKV_CTL(issued) + 4 * (1 - slot), batches, PKV_CTL(abort), p.wait_tries);
     }
 
     // S of the slot, whose K is there.
@@ -1240,6 +1249,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     tc_fence_after();
     if (warp == 8) tmem_free(ctl.tmem, 512);
     if (threadIdx.x == 0 && ctl.abort) report(p.status, PKV_ERR_DEVICE_TIMEOUT);
+}
+
+// The two waits on what never comes, a warp each, and how long each takes to give up.
+__global__ void __launch_bounds__(64) chunk_waits_selftest_kernel(int32_t *status, uint64_t *elapsed_ns, uint32_t tries) {
+    __shared__ uint64_t bar;
+    __shared__ uint32_t counter, abort[2];
+    const int warp = threadIdx.x / 32;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_addr(&bar), 1);
+        counter = abort[0] = abort[1] = 0;
+    }
+    __syncthreads();
+    const uint64_t t0 = global_ns();
+    const bool came = warp == 0 ? chunk_wait(smem_addr(&bar), 0, smem_addr(&abort[0]), tries)
+                                : chunk_wait_count(smem_addr(&counter), 1, smem_addr(&abort[1]), tries);
+    if (threadIdx.x % 32 == 0) {
+        elapsed_ns[warp] = global_ns() - t0;
+        if (!came && abort[warp]) report(status, PKV_ERR_DEVICE_TIMEOUT);
+    }
 }
 
 // Joins the parts of items cut between CTAs.  blockIdx.x is the CTA that began
