@@ -534,7 +534,8 @@ def paged_attention_chunk(out, query, key_cache, value_cache, block_tables, cont
     _launch(load().pkv_paged_attention_chunk, "pkv_paged_attention_chunk", index, stream,
             (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
              mb, context_lens.data_ptr(), query_starts.data_ptr(), t, n, h, hkv, d, bs, nb, float(scale),
-             1 if causal else 0, int(window), int(num_ctas), ws, ws_bytes, _status_address(status, index)))
+             1 if causal else 0, max(-1, min(int(window), 0x7fffffff)), int(num_ctas), ws, ws_bytes,
+             _status_address(status, index)))
     return out
 
 
