@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "../../include/pkv.h"
 #include "pkv_chunk_impl.cuh"
@@ -154,9 +155,13 @@ int call(void *out, const void *query, const void *key_cache, const void *value_
     const void *fn = d64 ? reinterpret_cast<const void *>(&chunk_kernel<64>)
                          : reinterpret_cast<const void *>(&chunk_kernel<128>);
     const size_t smem = d64 ? ChunkConfig<64>::kSmem : ChunkConfig<128>::kSmem;
-    static const bool good_regs = registers_add_up(reinterpret_cast<const void *>(&chunk_kernel<64>)) &&
-                                  registers_add_up(reinterpret_cast<const void *>(&chunk_kernel<128>));
-    if (!good_regs) return PKV_ERR_CUDA;
+    static std::atomic<bool> good_regs{false};  // only a good answer is kept: a query may fail once
+    if (!good_regs) {
+        if (!registers_add_up(reinterpret_cast<const void *>(&chunk_kernel<64>)) ||
+            !registers_add_up(reinterpret_cast<const void *>(&chunk_kernel<128>)))
+            return PKV_ERR_CUDA;
+        good_regs = true;
+    }
     rc = ensure_smem_attr(fn, smem);
     if (rc != PKV_OK) return rc;
     void *args[] = {&p};
