@@ -77,7 +77,7 @@ UNIT = "GB/s"
 FALLBACK_HBM_GBS = 6800.0
 FLUSH_BYTES = 256 << 20  # read between flushed repetitions: twice the 129 MB L2
 KERNEL_SOURCES = ["pkv_decode_impl.cuh", "pkv_decode_inst.cuh", "pkv_decode.cu", "pkv_device.cuh",
-                  "pkv_schedule.h", "pkv_decode_params.h"]
+                  "pkv_host.h", "pkv_schedule.h", "pkv_decode_params.h"]
 
 WORKLOAD_TEXT = {
     "7b": "7B-class decode, one layer: batch 64, 32 query heads = 32 KV heads, head_dim 128, fp16, "

@@ -23,6 +23,7 @@
 
 #include "../../include/pkv.h"
 #include "pkv_device.cuh"
+#include "pkv_host.h"
 #include "pkv_launch.h"
 #include "pkv_tcgen05.cuh"
 
@@ -223,7 +224,6 @@ const void *rope_kernel(bool many, bool interleaved) {
                 : reinterpret_cast<const void *>(&qk_norm_rope_kernel<LANES, 1, false>);
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool good_stride(int64_t stride, int64_t least) { return stride >= least && stride % 8 == 0; }
 
 // The checks that both calls share, and the launch.
