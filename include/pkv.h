@@ -555,7 +555,7 @@ int pkv_reshape_and_cache(const void *key, const void *value,
  *                then rot_dim/2 sines; 16-byte aligned
  *   rot_dim      multiple of 16, 0 <= rot_dim <= head_dim; 0: no rotation
  *                (positions and cos_sin may then be NULL)
- *   query_weight, key_weight  fp16 [head_dim] (device, nullable)
+ *   query_weight, key_weight  fp16 [head_dim] (device, nullable; 16-byte aligned)
  *   eps          >= 0 (host value)
  *   key_cache, value_cache, slot_mapping  as for pkv_reshape_and_cache: a
  *                negative slot writes no key or value (the query is computed)

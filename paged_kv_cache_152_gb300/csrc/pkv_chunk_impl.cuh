@@ -23,18 +23,20 @@
 // 512 * D bytes, so long prompts are bound by the products and the softmax: a
 // slot's step is its products, 1024 cycles at the tensor cores' rate, then its
 // softmax, somewhat longer with the hand-overs, under the other slot's products
-// (the tensor cores are busy 73% of the time).  With one token per sequence the
+// (1024 tokens of 16384, groups of 4: the tensor cores are busy 73% of the time).
+// At head_dim 64 the products are half of that and a step takes as long: the chain
+// through one slot's S is what counts.  With one token per sequence the
 // tile is nearly empty, and a step's copy from HBM takes longer than its
 // products, so padding costs no time.
 //
 // Measured on one GB300 (head_dim 128):
 //   32 heads, a prompt of 4096 tokens           138 us, 1000 TFLOP/s
-//   32 heads in groups of 4, 2048 new of 32768  667 us, 1600 TFLOP/s; in a row
-//                                               770 us, 1380 (power: 1500 MHz)
-//   8 single tokens over 8000 to 32768, groups of 4   121 us, 6070 GB/s
+//   32 heads in groups of 4, 2048 new of 32768  763 to 790 us, 1350 to 1400
+//                                               TFLOP/s (power: 1500 MHz)
+//   8 single tokens over 8000 to 32768, groups of 4   120 us, 6110 GB/s
 //   64 x 5 tokens over 50 to 900, 32 heads      113 us, 4350 GB/s
 // A call's fixed parts: 6 us until the first scores (launch, schedule, table,
-// first copy), 4 us of last pieces, up to 11 us of the joining kernel.
+// first copy), 4 us of last pieces, 5 to 13 us of the joining kernel.
 //
 // V is read as an operand for every row of a tile, and 0 * NaN is NaN.  So in
 // steps that some row does not see whole, the guard warp clears the rows of V
@@ -905,7 +907,8 @@ struct ChunkSoftmax {
                                                  __uint_as_float(s[i / 16][2 * (i % 16) + 1])));
         const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         // What the weights are relative to moves only when the maximum rises by more
-        // than a factor 2^kMostRise of the weights (fp16 carries them up to 65504).
+        // than a factor 2^kMostRise of the weights (fp16 carries them up to 65504), a
+        // published refinement of the running maximum.
         if (first) {
             if (row_hi >= 0) m = high;
             far = look_far();
@@ -1274,9 +1277,12 @@ __global__ void __launch_bounds__(64) chunk_waits_selftest_kernel(int32_t *statu
 // an item, blockIdx.y 32 of its tiles' rows, four per warp.  Bound by latency:
 // the record, then the parts' weights and (of the first two, the usual number)
 // outputs together.  The parts are taken in the order of the item's steps.  In
-// calls one behind the other it costs up to 11 us a call (a prompt of 4096
-// tokens 147 us instead of 136); joined inside chunk_kernel by the part that
-// arrives last, the same prompt took 158 to 173.
+// calls one behind the other a prompt of 4096 tokens takes 137.6 us with this kernel
+// and would take 124.0 without it, a window of 1024 77.7 and 64.8, 8 x 12 heads of
+// 1500 positions 35.0 and 27.6, 8 single tokens over 8000 to 32768 120.1 and 115.0.
+// (Joined inside chunk_kernel by the part that arrives last, an earlier form of
+// it took longer than with this one: 158 us against 147.)  At head_dim 128 three
+// CTAs per SM leave 80 registers, and 28 bytes are spilled.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 32;
 
