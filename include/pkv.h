@@ -17,6 +17,12 @@
  *   pkv_qk_norm_rope[_and_cache] the norm of each query and key head and the
  *                               position rotation, with the slot-mapped write;
  *   pkv_reshape_and_cache       the slot-mapped write of new tokens' K/V;
+ *   pkv_reshape_and_cache_q8, pkv_paged_attention_decode_q8
+ *                               the write and the decode of a cache held in 8
+ *                               bits with a scale per block and KV head;
+ *   pkv_block_key_bounds, pkv_select_blocks, pkv_paged_attention_decode_selected
+ *                               decode over the blocks whose keys can score
+ *                               highest;
  *   pkv_copy_blocks             the whole-block copy behind copy-on-write;
  *   pkv_swap_blocks             block copies between device and page-locked
  *                               host pools (swap out / in);
@@ -690,6 +696,229 @@ int pkv_swap_blocks_layers(const void *const *src_keys, const void *const *src_v
  * distinct, no destination also a source.  PKV_OK or PKV_ERR_INVALID_ARG. */
 int pkv_validate_block_pairs(const int64_t *host_pairs, int num_pairs,
                              int num_blocks);
+
+/* ------------------------------------------------------------------------ */
+/* The 8-bit cache                                                           */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Element type of a cache.  An 8-bit cache has the layout of the fp16 one with
+ * one byte per element, and for each of key_cache and value_cache an fp32 scale
+ * per (block, KV head): num_blocks rows of num_kv_heads, scale_stride floats
+ * apart.  An element is its code times the scale of its block and head.  int8 codes are -127 .. 127; e4m3
+ * codes (four significant bits, up to 448; the format without infinities).
+ * A pool's blocks and their scales are copied and swapped like any other:
+ * pkv_copy_blocks and pkv_swap_blocks with block_bytes = num_kv_heads *
+ * block_size * head_dim for the codes and 4 * scale_stride for the scales (a
+ * multiple of 16 for that: scale_stride a multiple of 4).
+ */
+typedef enum pkv_cache_type {
+    PKV_CACHE_F16 = 0,
+    PKV_CACHE_INT8 = 1,
+    PKV_CACHE_E4M3 = 2
+} pkv_cache_type;
+
+/*
+ * pkv_reshape_and_cache_q8
+ *
+ * The write of new tokens into an 8-bit cache: each sequence's newest tokens go
+ * to their positions through its block table (the slots of pkv_append_tokens).
+ * Sequence s owns the rows query_starts[s] .. query_starts[s+1]-1 of key and
+ * value; with n of them and L = context_lens[s] (new tokens counted), row i is
+ * position L - n + i.  query_starts NULL: one row per sequence (num_tokens ==
+ * num_seqs), sequences with L == 0 have none.
+ *
+ * A block and head's scale is a / M, rounded to fp32: a the largest magnitude
+ * of what the block holds for that head, an fp16 value, and M = 127 (int8) or
+ * 448 (e4m3).  For each block that gets new tokens, a0 = 0 if its first position
+ * is among them, else a0 = the scale times M, rounded to fp16 (which gives back
+ * the a that the scale was made from), and a = max(a0, largest finite |x| of its
+ * new rows).  The new rows become the codes nearest to M x / a (ties to even);
+ * where a > a0, the block's earlier rows are rounded again, to the codes nearest
+ * to code * a0 / a.  Every code is that of the exact quotient.  Infinite elements
+ * become the largest code; NaN becomes 0 in int8 and stays NaN in e4m3.  Rows of
+ * the block behind the new ones are not written.
+ *
+ *   key, value    fp16 [num_tokens][num_kv_heads][head_dim] (device), a token's
+ *                 heads contiguous, tokens key_stride / value_stride elements
+ *                 apart (multiples of 8, at least one token's elements)
+ *   key_cache, value_cache   codes [num_blocks][num_kv_heads][block_size]
+ *                 [head_dim] (device, written)
+ *   key_scale, value_scale   fp32 [num_blocks] rows of num_kv_heads (device,
+ *                 written), scale_stride >= num_kv_heads floats apart
+ *   block_tables, max_blocks_per_seq   as for pkv_paged_attention_decode
+ *   context_lens  int32 [num_seqs]
+ *   query_starts  int32 [num_seqs + 1] (nullable), not decreasing, from 0 up to
+ *                 at most num_tokens; rows outside are not looked at
+ *   cache_type    PKV_CACHE_INT8 or PKV_CACHE_E4M3
+ * head_dim in {64, 128}, block_size in {8, 16, 32, 64, 128}, num_seqs <= 4096,
+ * num_blocks * num_kv_heads * block_size <= 2^31, max_blocks_per_seq *
+ * block_size <= 2^30.  num_tokens == 0 or num_seqs == 0 launches nothing.
+ * A context that is negative or longer than its table, more new tokens than
+ * context (the tokens before position 0 and past the table are not written), a
+ * table entry of a block to write outside [0, num_blocks) (not written), and
+ * query_starts that decrease or leave [0, num_tokens] (what is written is then
+ * unspecified) set PKV_ERR_OUT_OF_RANGE.  Two sequences that write one block
+ * race (the block manager's copy-on-write never lets them).
+ */
+int pkv_reshape_and_cache_q8(const void *key, int64_t key_stride,
+                             const void *value, int64_t value_stride,
+                             void *key_cache, void *value_cache,
+                             float *key_scale, float *value_scale, int scale_stride,
+                             const int32_t *block_tables, int max_blocks_per_seq,
+                             const int32_t *context_lens, const int32_t *query_starts,
+                             int num_tokens, int num_seqs, int num_kv_heads,
+                             int head_dim, int block_size, int num_blocks, int cache_type,
+                             int32_t *dev_status, pkv_stream_t stream);
+
+/*
+ * pkv_paged_attention_decode_q8
+ *
+ * pkv_paged_attention_decode over an 8-bit cache: out[s][h] = sum_t
+ * softmax_t(scale * q[s][h] . K[t][kvh]) * V[t][kvh] with K and V the codes
+ * times their scales.  The products take the codes as they are (exact in fp16)
+ * and accumulate in fp32; softmax statistics and outputs are held in fp32; the
+ * weights, with the value's scale in them, are rounded to fp16 for the second
+ * product (11 significant bits down to 2^-29 of the row's largest); one rounding
+ * to fp16 at the end.  A context of 0 gives zeros.  A row with a score that is
+ * not finite is unspecified.
+ *
+ * With block lists (selected not NULL) the sum runs over the listed blocks'
+ * positions below context_lens[s] only, a list for each sequence and KV head:
+ *   selected      int32 [num_seqs][num_kv_heads][max_selected]: logical blocks of
+ *                 the sequence, in any order.  A block listed twice counts twice.
+ *   num_selected  int32 [num_seqs][num_kv_heads]: entries that count, at most
+ *                 max_selected and the context's blocks.  No entry: zeros.
+ * selected and num_selected go together (both NULL: every block).
+ *
+ *   key_scale, value_scale, scale_stride  as for pkv_reshape_and_cache_q8; a
+ *                 scale is 0 or between 2^-40 and 2^40
+ *   cache_type    PKV_CACHE_INT8 or PKV_CACHE_E4M3
+ *   num_ctas      persistent grid size; 0 = one CTA per SM.  Any value gives the
+ *                 same result within rounding; deterministic for a fixed grid.
+ *   workspace     at least pkv_decode_team_workspace_size(...) bytes for the same
+ *                 (num_heads, num_kv_heads, head_dim, num_ctas); 256-byte
+ *                 aligned.  It carries nothing from call to call and needs no
+ *                 clearing, but must not be used by another call that runs at
+ *                 the same time.
+ * Other arguments as for pkv_paged_attention_decode.  Supported: head_dim in
+ * {64, 128}; block_size in {8, 16, 32, 64, 128}; num_heads / num_kv_heads from 1
+ * to 16; num_kv_heads <= 2^16; num_seqs <= 4096; num_ctas <= 4096; num_blocks *
+ * num_kv_heads * block_size <= 2^31; max_blocks_per_seq * block_size <= 2^30.
+ * A context that is negative (taken as 0) or longer than its table (clamped), a
+ * table entry outside [0, num_blocks) among those read (block 0 is read), a
+ * listed block outside the context (left out) and num_selected out of its range
+ * (clamped) set PKV_ERR_OUT_OF_RANGE.
+ */
+int pkv_paged_attention_decode_q8(void *out, const void *query,
+                                  const void *key_cache, const void *value_cache,
+                                  const float *key_scale, const float *value_scale, int scale_stride,
+                                  const int32_t *block_tables, int max_blocks_per_seq,
+                                  const int32_t *context_lens,
+                                  const int32_t *selected, const int32_t *num_selected, int max_selected,
+                                  int num_seqs, int num_heads, int num_kv_heads,
+                                  int head_dim, int block_size, int num_blocks, int cache_type,
+                                  float scale, int num_ctas,
+                                  void *workspace, size_t workspace_bytes,
+                                  int32_t *dev_status, pkv_stream_t stream);
+
+/* Bytes of workspace pkv_paged_attention_decode_q8 and
+ * pkv_paged_attention_decode_selected need (host call; queries the current
+ * device's SM count when num_ctas == 0).  Returns 0 for unsupported shapes. */
+size_t pkv_decode_team_workspace_size(int num_heads, int num_kv_heads, int head_dim, int num_ctas);
+
+/* ------------------------------------------------------------------------ */
+/* Decode over selected blocks                                               */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * pkv_paged_attention_decode_selected: the decode over block lists (as for
+ * pkv_paged_attention_decode_q8, selected and num_selected required) of an fp16
+ * cache.
+ */
+int pkv_paged_attention_decode_selected(void *out, const void *query,
+                                        const void *key_cache, const void *value_cache,
+                                        const int32_t *block_tables, int max_blocks_per_seq,
+                                        const int32_t *context_lens,
+                                        const int32_t *selected, const int32_t *num_selected,
+                                        int max_selected,
+                                        int num_seqs, int num_heads, int num_kv_heads,
+                                        int head_dim, int block_size, int num_blocks,
+                                        float scale, int num_ctas,
+                                        void *workspace, size_t workspace_bytes,
+                                        int32_t *dev_status, pkv_stream_t stream);
+
+/*
+ * pkv_block_key_bounds
+ *
+ * The largest and the smallest key, channel by channel, of each block that
+ * holds new tokens, over the block's positions below the context length (all of
+ * them are read from the cache again, so nothing depends on what the bounds held
+ * before).  To be called after the write of the new tokens, with the same
+ * tables, lengths and query_starts.  A channel with a NaN has NaN for both.
+ *
+ *   key_bounds  fp16 [num_blocks][num_kv_heads][2][head_dim] (device, written):
+ *               the largest, then the smallest; of an 8-bit cache the codes'
+ *               times the scale, rounded to fp16
+ *   key_scale, scale_stride  8-bit caches only (else NULL, any)
+ *   cache_type  PKV_CACHE_F16, PKV_CACHE_INT8 or PKV_CACHE_E4M3
+ * Other arguments, shapes and errors as for pkv_reshape_and_cache_q8.  A block
+ * that two sequences share may be given by both (they write the same bounds if
+ * both see all of it).
+ */
+int pkv_block_key_bounds(void *key_bounds, const void *key_cache, const float *key_scale, int scale_stride,
+                         const int32_t *block_tables, int max_blocks_per_seq,
+                         const int32_t *context_lens, const int32_t *query_starts,
+                         int num_tokens, int num_seqs, int num_kv_heads,
+                         int head_dim, int block_size, int num_blocks, int cache_type,
+                         int32_t *dev_status, pkv_stream_t stream);
+
+/*
+ * pkv_select_blocks
+ *
+ * For each sequence s and KV head, the blocks whose keys can score highest for
+ * the single-token query.  Block b's score is the largest, over the KV head's
+ * query heads h, of
+ *
+ *     sum_i max(q[s][h][i], 0) * hi[b][i] + min(q[s][h][i], 0) * lo[b][i]
+ *
+ * with hi and lo the block's key bounds: no key of the block has a larger
+ * product with the query.  Of the context's B = ceil(L / block_size) blocks,
+ * min(B, max_selected) are kept: the first first_blocks and the last
+ * last_blocks, and of the others those with the largest scores, of equal ones
+ * the lowest index.  A score that is not finite counts as the largest.  The
+ * choice is that of the scores in 64 bits.
+ *
+ *   selected      int32 [num_seqs][num_kv_heads][max_selected] (device, written):
+ *                 the kept blocks' logical indices in ascending order, then -1
+ *   num_selected  int32 [num_seqs][num_kv_heads] (device, written)
+ *   query         fp16 [num_seqs][num_heads][head_dim]
+ *   key_bounds    as pkv_block_key_bounds writes it
+ *   max_selected >= 1, first_blocks >= 0, last_blocks >= 0 (host values),
+ *                 first_blocks + last_blocks <= max_selected
+ *   workspace     at least pkv_select_workspace_size(num_seqs, num_kv_heads,
+ *                 max_blocks_per_seq) bytes; 256-byte aligned; as for
+ *                 pkv_paged_attention_decode_q8
+ * Supported: head_dim in {64, 128}; block_size in {8, 16, 32, 64, 128};
+ * num_heads / num_kv_heads from 1 to 16; num_kv_heads <= 65535; num_seqs <= 4096;
+ * sizes as for pkv_paged_attention_decode_q8.  A context that is negative (taken
+ * as 0) or longer than its table (clamped) and a table entry outside
+ * [0, num_blocks) among those read (block 0's bounds are taken) set
+ * PKV_ERR_OUT_OF_RANGE.
+ */
+int pkv_select_blocks(int32_t *selected, int32_t *num_selected,
+                      const void *query, const void *key_bounds,
+                      const int32_t *block_tables, int max_blocks_per_seq,
+                      const int32_t *context_lens,
+                      int num_seqs, int num_heads, int num_kv_heads,
+                      int head_dim, int block_size, int num_blocks,
+                      int max_selected, int first_blocks, int last_blocks,
+                      void *workspace, size_t workspace_bytes,
+                      int32_t *dev_status, pkv_stream_t stream);
+
+/* Bytes of workspace pkv_select_blocks needs.  Returns 0 for sizes out of
+ * range. */
+size_t pkv_select_workspace_size(int num_seqs, int num_kv_heads, int max_blocks_per_seq);
 
 /* ------------------------------------------------------------------------ */
 /* Block manager (host)                                                      */

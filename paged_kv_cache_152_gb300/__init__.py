@@ -19,6 +19,16 @@ Names mirror the C ABI without its ``pkv_`` prefix:
   qk_norm_rope_and_cache(query_out, query, key, value, key_cache, value_cache,
   slot_mapping, positions, cos_sin, ...)
 * reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, ...)
+* reshape_and_cache_q8(key, value, key_cache, value_cache, key_scale,
+  value_scale, block_tables, context_lens, ...) and paged_attention_decode_q8(
+  out, query, key_cache, value_cache, key_scale, value_scale, block_tables,
+  context_lens, scale, ...): the cache in 8 bits (torch.int8 or
+  torch.float8_e4m3fn)
+* block_key_bounds(key_bounds, key_cache, block_tables, context_lens, ...),
+  select_blocks(selected, num_selected, query, key_bounds, block_tables,
+  context_lens, block_size, ...) and paged_attention_decode_selected(out, query,
+  key_cache, value_cache, block_tables, context_lens, selected, num_selected,
+  scale, ...): decode over the blocks that matter
 * copy_blocks(key_cache, value_cache, block_pairs, ...)
 * swap_blocks(src_key, src_value, dst_key, dst_value, block_pairs, ...)
 * DecodePlan: pkv_decode_plan_* (validate once, launch every step)
@@ -46,6 +56,9 @@ PKV_ERR_OUT_OF_RANGE = 5
 PKV_ERR_NOT_FOUND = 6
 PKV_ERR_UNSUPPORTED = 7
 PKV_ERR_SWAPPED = 8
+PKV_CACHE_F16 = 0
+PKV_CACHE_INT8 = 1
+PKV_CACHE_E4M3 = 2
 
 # Every symbol include/pkv.h declares, with (restype, argtypes).
 _c_int, _c_size, _vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
@@ -82,6 +95,20 @@ SIGNATURES = {
                                             _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
     "pkv_reshape_and_cache": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
                                        _vp, _vp]),
+    "pkv_reshape_and_cache_q8": (_c_int, [_vp, _c_i64, _vp, _c_i64, _vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _vp, _vp, _c_int,
+                                          _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
+    "pkv_paged_attention_decode_q8": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _vp, _vp, _vp, _c_int, _c_int,
+                                               _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, ctypes.c_float, _c_int,
+                                               _vp, _c_size, _vp, _vp]),
+    "pkv_paged_attention_decode_selected": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _vp, _c_int, _c_int,
+                                                     _c_int, _c_int, _c_int, _c_int, _c_int, ctypes.c_float, _c_int,
+                                                     _vp, _c_size, _vp, _vp]),
+    "pkv_decode_team_workspace_size": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "pkv_block_key_bounds": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                      _c_int, _c_int, _vp, _vp]),
+    "pkv_select_blocks": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                   _c_int, _c_int, _c_int, _vp, _c_size, _vp, _vp]),
+    "pkv_select_workspace_size": (_c_size, [_c_int, _c_int, _c_int]),
     "pkv_copy_blocks": (_c_int, [_vp, _vp, _vp, _c_int, _c_size, _c_int, _vp, _vp]),
     "pkv_validate_block_pairs": (_c_int, [_i64p, _c_int, _c_int]),
     "pkv_reshape_and_cache_layers": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _c_int, _c_int, _c_int,
@@ -803,12 +830,305 @@ def qk_norm_rope_and_cache(query_out, query, key, value, key_cache, value_cache,
     return query_out
 
 
+def decode_team_workspace_size(num_heads, num_kv_heads, head_dim, num_ctas=0):
+    return int(load().pkv_decode_team_workspace_size(num_heads, num_kv_heads, head_dim, num_ctas))
+
+
+def select_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq):
+    return int(load().pkv_select_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq))
+
+
+@functools.lru_cache(maxsize=4096)
+def _team_workspace(num_heads, num_kv_heads, head_dim, num_ctas, index):
+    """decode_team_workspace_size on device `index`, whose SM count it goes by."""
+    with _device_guard(index):
+        n = decode_team_workspace_size(num_heads, num_kv_heads, head_dim, num_ctas)
+    if n == 0:
+        raise PkvError(PKV_ERR_UNSUPPORTED, "decode_team_workspace_size")
+    return n
+
+
+@functools.lru_cache(maxsize=4096)
+def _select_workspace(num_seqs, num_kv_heads, max_blocks_per_seq):
+    n = select_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq)
+    if n == 0:
+        raise PkvError(PKV_ERR_UNSUPPORTED, "select_workspace_size")
+    return n
+
+
+def new_team_workspace(num_heads, num_kv_heads, head_dim, num_ctas=0, device="cuda"):
+    """A device workspace of the size pkv_decode_team_workspace_size asks for."""
+    import torch
+    device = torch.device(device)
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    return torch.empty(_team_workspace(num_heads, num_kv_heads, head_dim, num_ctas, index), dtype=torch.uint8,
+                       device=device)
+
+
+def new_select_workspace(num_seqs, num_kv_heads, max_blocks_per_seq, device="cuda"):
+    """A device workspace of the size pkv_select_workspace_size asks for."""
+    import torch
+    return torch.empty(_select_workspace(num_seqs, num_kv_heads, max_blocks_per_seq), dtype=torch.uint8,
+                       device=device)
+
+
+def _scratch(workspace, size, index, device, stream):
+    """(tensor, address, bytes) of the caller's workspace, or of a new one of
+    `size` bytes.  A new one belongs to the stream that uses it: freed on return,
+    it then goes to that stream's later work only."""
+    if workspace is None:
+        import torch
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    elif _checked(((workspace, workspace.dtype, "workspace", workspace.dim()),)) != index:
+        raise ValueError("the device tensors of one call must all be on the same CUDA device")
+    return workspace, workspace.data_ptr(), workspace.nbytes
+
+
+def _cache_type(t, name, f16=False):
+    """The PKV_CACHE_* of an 8-bit cache (f16: or of an fp16 one)."""
+    torch = _torch()
+    if t.dtype is torch.int8:
+        return PKV_CACHE_INT8
+    if t.dtype is torch.float8_e4m3fn:
+        return PKV_CACHE_E4M3
+    if f16 and t.dtype is torch.float16:
+        return PKV_CACHE_F16
+    raise TypeError(f"{name}: expected {'torch.float16, ' if f16 else ''}torch.int8 or torch.float8_e4m3fn, "
+                    f"got {t.dtype}")
+
+
+def _scale_spec(t, name):
+    """The spec of an 8-bit cache's scales, fp32 [NB][Hkv], which may be the first
+    columns of wider rows."""
+    if t.dtype is not _torch().float32:
+        raise TypeError(f"{name}: expected torch.float32, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected 2 dims, got {tuple(t.shape)}")
+    return (t, None, name, 2)
+
+
+def _scale_stride(nb, hkv, *scales):
+    """Floats between the rows of one cache's scales."""
+    for t in scales:
+        if t.shape != (nb, hkv):
+            raise ValueError("key_scale, value_scale: inconsistent shapes")
+        if hkv > 1 and t.stride(1) != 1:
+            raise ValueError("key_scale, value_scale: a block's scales must be contiguous")
+    if nb < 2:
+        return hkv
+    stride = scales[0].stride(0)
+    if stride < hkv or stride > 0x7fffffff or scales[-1].stride(0) != stride:
+        raise ValueError("key_scale, value_scale: rows must be equally far apart in both and must not overlap")
+    return stride
+
+
+@_traced
+def reshape_and_cache_q8(key, value, key_cache, value_cache, key_scale, value_scale, block_tables, context_lens,
+                         query_starts=None, status=None, stream=None):
+    """pkv_reshape_and_cache_q8 on torch tensors (see include/pkv.h): each
+    sequence's newest tokens into an 8-bit cache, through its block table.
+
+    key, value: fp16 [T][Hkv][D], tokens any multiple of 8 elements apart (views
+    of a projection's output); key_cache, value_cache: int8 or float8_e4m3fn
+    [NB][Hkv][bs][D]; key_scale, value_scale: fp32 [NB][Hkv], or the first
+    columns of wider rows (copy_blocks and swap_blocks move rows of a multiple of
+    4); block_tables: int32 [N][MB]; context_lens: int32 [N]; query_starts: int32 [N + 1], or None:
+    one token of each sequence (T == N)."""
+    torch = _torch()
+    f16, i32 = torch.float16, torch.int32
+    sk, sv = _rows(key, "key", f16), _rows(value, "value", f16)
+    kind = _cache_type(key_cache, "key_cache")
+    specs = ((key, None, "key", 3), (value, None, "value", 3), (key_cache, key_cache.dtype, "key_cache", 4),
+             (value_cache, key_cache.dtype, "value_cache", 4), _scale_spec(key_scale, "key_scale"),
+             _scale_spec(value_scale, "value_scale"), (block_tables, i32, "block_tables", 2),
+             (context_lens, i32, "context_lens", 1))
+    if query_starts is not None:
+        specs += ((query_starts, i32, "query_starts", 1),)
+    index = _checked(specs)
+    t, hkv, d = rows = key.shape
+    nb, hkv2, bs, d2 = pool = key_cache.shape
+    n, mb = block_tables.shape
+    scale_stride = _scale_stride(nb, hkv2, key_scale, value_scale)
+    if value.shape != rows or hkv2 != hkv or d2 != d or value_cache.shape != pool or context_lens.shape != (n,) \
+            or (t != n if query_starts is None else query_starts.shape != (n + 1,)):
+        raise ValueError("inconsistent shapes")
+    _launch(load().pkv_reshape_and_cache_q8, "pkv_reshape_and_cache_q8", index, stream,
+            (key.data_ptr(), sk, value.data_ptr(), sv, key_cache.data_ptr(), value_cache.data_ptr(),
+             key_scale.data_ptr(), value_scale.data_ptr(), scale_stride, block_tables.data_ptr(), mb,
+             context_lens.data_ptr(), _address(query_starts), t, n, hkv, d, bs, nb, kind, _status_address(status, index)))
+
+
+@_traced
+def paged_attention_decode_q8(out, query, key_cache, value_cache, key_scale, value_scale, block_tables, context_lens,
+                              scale, selected=None, num_selected=None, num_ctas=0, workspace=None, status=None,
+                              stream=None):
+    """pkv_paged_attention_decode_q8 on torch tensors (see include/pkv.h).
+
+    out, query: fp16 [N][H][D]; key_cache, value_cache: int8 or float8_e4m3fn
+    [NB][Hkv][bs][D]; key_scale, value_scale: fp32 [NB][Hkv] (as for
+    reshape_and_cache_q8); block_tables: int32 [N][MB]; context_lens: int32 [N]; selected: int32 [N][Hkv][K] and
+    num_selected: int32 [N][Hkv], or None: every block.  A workspace
+    (new_team_workspace) is allocated when None, on the call's stream."""
+    torch = _torch()
+    f16, i32 = torch.float16, torch.int32
+    kind = _cache_type(key_cache, "key_cache")
+    specs = ((query, f16, "query", 3), (out, f16, "out", 3), (key_cache, key_cache.dtype, "key_cache", 4),
+             (value_cache, key_cache.dtype, "value_cache", 4), _scale_spec(key_scale, "key_scale"),
+             _scale_spec(value_scale, "value_scale"), (block_tables, i32, "block_tables", 2),
+             (context_lens, i32, "context_lens", 1))
+    if (selected is None) != (num_selected is None):
+        raise ValueError("selected and num_selected go together")
+    if selected is not None:
+        specs += ((selected, i32, "selected", 3), (num_selected, i32, "num_selected", 2))
+    index = _checked(specs)
+    n, h, d = rows = query.shape
+    nb, hkv, bs, d2 = pool = key_cache.shape
+    scale_stride = _scale_stride(nb, hkv, key_scale, value_scale)
+    if out.shape != rows or d2 != d or value_cache.shape != pool or block_tables.shape[0] != n \
+            or context_lens.shape != (n,):
+        raise ValueError("inconsistent shapes")
+    keep = 0
+    if selected is not None:
+        keep = selected.shape[2]
+        if selected.shape != (n, hkv, keep) or num_selected.shape != (n, hkv):
+            raise ValueError("inconsistent shapes")
+    if n == 0:
+        return out
+    size = _team_workspace(h, hkv, d, num_ctas, index) if workspace is None else 0
+    workspace, ws, ws_bytes = _scratch(workspace, size, index, query.device, stream)
+    _launch(load().pkv_paged_attention_decode_q8, "pkv_paged_attention_decode_q8", index, stream,
+            (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), key_scale.data_ptr(),
+             value_scale.data_ptr(), scale_stride, block_tables.data_ptr(), block_tables.shape[1],
+             context_lens.data_ptr(), _address(selected), _address(num_selected), keep, n, h, hkv, d, bs, nb, kind, float(scale),
+             int(num_ctas), ws, ws_bytes, _status_address(status, index)))
+    return out
+
+
+@_traced
+def paged_attention_decode_selected(out, query, key_cache, value_cache, block_tables, context_lens, selected,
+                                    num_selected, scale, num_ctas=0, workspace=None, status=None, stream=None):
+    """pkv_paged_attention_decode_selected on torch tensors (see include/pkv.h):
+    the decode over listed blocks of an fp16 cache.
+
+    out, query: fp16 [N][H][D]; key_cache, value_cache: fp16 [NB][Hkv][bs][D];
+    block_tables: int32 [N][MB]; context_lens: int32 [N]; selected: int32
+    [N][Hkv][K]; num_selected: int32 [N][Hkv].  A workspace (new_team_workspace)
+    is allocated when None, on the call's stream."""
+    torch = _torch()
+    f16, i32 = torch.float16, torch.int32
+    index = _checked(((query, f16, "query", 3), (out, f16, "out", 3), (key_cache, f16, "key_cache", 4),
+                      (value_cache, f16, "value_cache", 4), (block_tables, i32, "block_tables", 2),
+                      (context_lens, i32, "context_lens", 1), (selected, i32, "selected", 3),
+                      (num_selected, i32, "num_selected", 2)))
+    n, h, d = rows = query.shape
+    nb, hkv, bs, d2 = pool = key_cache.shape
+    keep = selected.shape[2]
+    if out.shape != rows or d2 != d or value_cache.shape != pool or block_tables.shape[0] != n \
+            or context_lens.shape != (n,) or selected.shape != (n, hkv, keep) or num_selected.shape != (n, hkv):
+        raise ValueError("inconsistent shapes")
+    if n == 0:
+        return out
+    size = _team_workspace(h, hkv, d, num_ctas, index) if workspace is None else 0
+    workspace, ws, ws_bytes = _scratch(workspace, size, index, query.device, stream)
+    _launch(load().pkv_paged_attention_decode_selected, "pkv_paged_attention_decode_selected", index, stream,
+            (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
+             block_tables.shape[1], context_lens.data_ptr(), selected.data_ptr(), num_selected.data_ptr(), keep, n, h,
+             hkv, d, bs, nb, float(scale), int(num_ctas), ws, ws_bytes, _status_address(status, index)))
+    return out
+
+
+@_traced
+def block_key_bounds(key_bounds, key_cache, block_tables, context_lens, query_starts=None, num_tokens=None,
+                     key_scale=None, status=None, stream=None):
+    """pkv_block_key_bounds on torch tensors (see include/pkv.h): the bounds of
+    the blocks that hold the newest tokens, after their write.
+
+    key_bounds: fp16 [NB][Hkv][2][D]; key_cache: fp16, int8 or float8_e4m3fn
+    [NB][Hkv][bs][D]; block_tables: int32 [N][MB]; context_lens: int32 [N];
+    query_starts: int32 [N + 1] with num_tokens (its last value, or the rows it
+    indexes), or None: one token of each sequence; key_scale: fp32 [NB][Hkv],
+    with an 8-bit cache."""
+    torch = _torch()
+    i32 = torch.int32
+    kind = _cache_type(key_cache, "key_cache", f16=True)
+    if (kind != PKV_CACHE_F16) != (key_scale is not None):
+        raise ValueError("key_scale goes with an 8-bit cache")
+    if (query_starts is None) != (num_tokens is None):
+        raise ValueError("query_starts and num_tokens go together")
+    specs = ((key_bounds, torch.float16, "key_bounds", 4), (key_cache, key_cache.dtype, "key_cache", 4),
+             (block_tables, i32, "block_tables", 2), (context_lens, i32, "context_lens", 1))
+    if query_starts is not None:
+        specs += ((query_starts, i32, "query_starts", 1),)
+    if key_scale is not None:
+        specs += (_scale_spec(key_scale, "key_scale"),)
+    index = _checked(specs)
+    nb, hkv, bs, d = key_cache.shape
+    n, mb = block_tables.shape
+    if key_bounds.shape != (nb, hkv, 2, d) or context_lens.shape != (n,) \
+            or (query_starts is not None and query_starts.shape != (n + 1,)):
+        raise ValueError("inconsistent shapes")
+    scale_stride = 0 if key_scale is None else _scale_stride(nb, hkv, key_scale)
+    _launch(load().pkv_block_key_bounds, "pkv_block_key_bounds", index, stream,
+            (key_bounds.data_ptr(), key_cache.data_ptr(), _address(key_scale), scale_stride, block_tables.data_ptr(),
+             mb, context_lens.data_ptr(), _address(query_starts), n if num_tokens is None else int(num_tokens), n, hkv, d,
+             bs, nb, kind, _status_address(status, index)))
+    return key_bounds
+
+
+@_traced
+def select_blocks(selected, num_selected, query, key_bounds, block_tables, context_lens, block_size, first_blocks=1,
+                  last_blocks=2, workspace=None, status=None, stream=None):
+    """pkv_select_blocks on torch tensors (see include/pkv.h): for each sequence
+    and KV head the K blocks whose keys can score highest, the first first_blocks
+    and the last last_blocks among them.
+
+    selected: int32 [N][Hkv][K] and num_selected: int32 [N][Hkv] (written); query:
+    fp16 [N][H][D]; key_bounds: fp16 [NB][Hkv][2][D]; block_tables: int32 [N][MB];
+    context_lens: int32 [N].  A workspace (new_select_workspace) is allocated when
+    None, on the call's stream.  -> selected, num_selected"""
+    torch = _torch()
+    f16, i32 = torch.float16, torch.int32
+    index = _checked(((query, f16, "query", 3), (key_bounds, f16, "key_bounds", 4),
+                      (block_tables, i32, "block_tables", 2), (context_lens, i32, "context_lens", 1),
+                      (selected, i32, "selected", 3), (num_selected, i32, "num_selected", 2)))
+    n, h, d = query.shape
+    nb, hkv, two, d2 = key_bounds.shape
+    mb = block_tables.shape[1]
+    if two != 2 or d2 != d or selected.shape[:2] != (n, hkv) or num_selected.shape != (n, hkv) \
+            or block_tables.shape[0] != n or context_lens.shape != (n,):
+        raise ValueError("inconsistent shapes")
+    if n == 0:
+        return selected, num_selected
+    size = _select_workspace(n, hkv, mb) if workspace is None else 0
+    workspace, ws, ws_bytes = _scratch(workspace, size, index, query.device, stream)
+    _launch(load().pkv_select_blocks, "pkv_select_blocks", index, stream,
+            (selected.data_ptr(), num_selected.data_ptr(), query.data_ptr(), key_bounds.data_ptr(),
+             block_tables.data_ptr(), mb, context_lens.data_ptr(), n, h, hkv, d, int(block_size), nb,
+             selected.shape[2], int(first_blocks), int(last_blocks), ws, ws_bytes, _status_address(status, index)))
+    return selected, num_selected
+
+
+def _block_pool(t):
+    """(element type, rank) that a pool of blocks like t has: a cache's, or an
+    8-bit cache's scales'."""
+    torch = _torch()
+    if t.dtype is torch.float32:
+        return t.dtype, 2
+    return (t.dtype if t.dtype in (torch.int8, torch.float8_e4m3fn) else torch.float16), 4
+
+
 @_traced
 def copy_blocks(key_cache, value_cache, block_pairs, status=None, stream=None):
-    """pkv_copy_blocks: block_pairs int64 [n][2] (src, dst) on the device."""
+    """pkv_copy_blocks: block_pairs int64 [n][2] (src, dst) on the device.  The
+    pools are caches (fp16, int8 or float8_e4m3fn [NB][Hkv][bs][D]) or an 8-bit
+    cache's scales (fp32 [NB][a multiple of 4])."""
     import torch
-    _need_all((key_cache, torch.float16, "key_cache", 4), (value_cache, torch.float16, "value_cache", 4),
+    kind, ndim = _block_pool(key_cache)
+    _need_all((key_cache, kind, "key_cache", ndim), (value_cache, kind, "value_cache", ndim),
               (block_pairs, torch.int64, "block_pairs", 2))
+    if ndim == 2 and value_cache.shape != key_cache.shape:
+        raise ValueError("inconsistent shapes")
     nb = key_cache.shape[0]
     block_bytes = key_cache[0].numel() * key_cache.element_size()
     with _one_device((key_cache, value_cache, block_pairs, status), stream):
@@ -854,8 +1174,11 @@ def copy_blocks_layers(key_caches, value_caches, block_pairs, status=None, strea
     n = len(key_caches)
     if len(value_caches) != n or n == 0:
         raise ValueError("one key_cache and value_cache per layer")
+    kind, ndim = _block_pool(key_caches[0])
     for t in list(key_caches) + list(value_caches):
-        _need(t, torch.float16, "cache", 4)
+        _need(t, kind, "cache", ndim)
+        if ndim == 2 and t.shape != key_caches[0].shape:
+            raise ValueError("every layer's pool must have the same shape")
     _need(block_pairs, torch.int64, "block_pairs", 2)
     nb = key_caches[0].shape[0]
     block_bytes = key_caches[0][0].numel() * key_caches[0].element_size()
@@ -867,12 +1190,18 @@ def copy_blocks_layers(key_caches, value_caches, block_pairs, status=None, strea
 
 
 def _pool(t, name):
-    """A swap pool: fp16 [NB][Hkv][bs][D], contiguous, on the GPU or in
-    page-locked host memory (the library checks the pointer as well)."""
-    torch = _need(t, __import__("torch").float16, name, 4, device=False)
+    """A swap pool: a cache [NB][Hkv][bs][D] or an 8-bit cache's scales (fp32
+    [NB][a multiple of 4]), contiguous, on the GPU or in page-locked host memory
+    (the library checks the pointer as well)."""
+    torch = _need(t, _block_pool(t)[0], name, _block_pool(t)[1], device=False)
     if t.device.type == "cpu" and not t.is_pinned():
         raise ValueError(f"{name}: a host pool must be page-locked (pin_memory)")
     return torch
+
+
+def _same_type(pools):
+    if any(t.dtype is not pools[0].dtype for t in pools):
+        raise TypeError("the pools of one call must all have the same element type")
 
 
 @_traced
@@ -883,6 +1212,7 @@ def swap_blocks(src_key, src_value, dst_key, dst_value, block_pairs, status=None
     torch = _pool(src_key, "src_key")
     for t, name in ((src_value, "src_value"), (dst_key, "dst_key"), (dst_value, "dst_value")):
         _pool(t, name)
+    _same_type((src_key, src_value, dst_key, dst_value))
     if tuple(src_key.shape[1:]) != tuple(dst_key.shape[1:]) or src_key.shape != src_value.shape \
             or dst_key.shape != dst_value.shape:
         raise ValueError("source and destination pools must have the same block shape")
@@ -910,6 +1240,7 @@ def swap_blocks_layers(src_keys, src_values, dst_keys, dst_values, block_pairs, 
         _pool(t, "destination pool")
         if tuple(t.shape) != tuple(dst_keys[0].shape):
             raise ValueError("every layer's destination pool must have the same shape")
+    _same_type(list(src_keys) + list(src_values) + list(dst_keys) + list(dst_values))
     if tuple(src_keys[0].shape[1:]) != tuple(dst_keys[0].shape[1:]):
         raise ValueError("source and destination pools must have the same block shape")
     _need(block_pairs, torch.int64, "block_pairs", 2)

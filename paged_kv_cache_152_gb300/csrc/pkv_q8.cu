@@ -1,0 +1,374 @@
+// pkv_q8.cu -- the write of new tokens into a cache of 8-bit codes.
+//
+// A (block, KV head) tile holds codes of one scale a / M: a the largest magnitude
+// of the tile's rows so far (an fp16 value), M = 127 (int8) or 448 (e4m3).  A row
+// x becomes rn(M x / a).  Where new rows raise a from a0, the rows before them are
+// rounded again, rn(code a0 / a); a0 comes back exactly from the scale, as the
+// fp16 value next to M times it.  M x and code a0 are exact in fp32, so each code
+// is the exact quotient's, ties to even: a quotient that is no tie differs from
+// one by 2^-20 of itself or more (the numerators are integers below 2^22), and
+// fp32's division is off by 2^-24.
+//
+// Bound by HBM for prompts (2 bytes read and 1 written per element), by latency
+// for single tokens.  A tile belongs to block_size * D / 64 threads, which hold
+// its new rows in registers, 64 elements each, between the maximum and the codes.
+#include <cuda_runtime.h>
+
+#include "../../include/pkv.h"
+#include "pkv_device.cuh"
+#include "pkv_host.h"
+#include "pkv_launch.h"
+#include "pkv_touched.cuh"
+
+namespace pkv {
+namespace {
+
+struct WriteParams {
+    TouchedParams t;
+    const __half *rows[2];   // keys, values: a token's heads contiguous
+    int64_t stride[2];       // elements between tokens
+    unsigned char *cache[2];
+    float *scale[2];
+    int64_t tiles;
+    int num_kv_heads;
+    int scale_stride;
+};
+
+template <bool E4M3>
+struct Codes {
+    static constexpr float kTop = E4M3 ? 448.f : 127.f;
+    // Eight values in units of the scale -> codes.  NaN: 0 in int8, NaN in e4m3.
+    __device__ static uint2 pack(const float (&y)[8]) {
+        uint32_t r[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (E4M3) {
+                asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
+                    "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n\t}"
+                    : "=r"(r[k])
+                    : "f"(y[4 * k]), "f"(y[4 * k + 1]), "f"(y[4 * k + 2]), "f"(y[4 * k + 3]));
+            } else {
+                int v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = min(max(__float2int_rn(y[4 * k + e]), -127), 127);
+                r[k] = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410);
+            }
+        }
+        return make_uint2(r[0], r[1]);
+    }
+    __device__ static void unpack(uint2 c, float (&y)[8]) {
+        const uint32_t r[2] = {c.x, c.y};
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (E4M3) {
+                uint32_t lo, hi;
+                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+                    "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+                    : "=r"(lo), "=r"(hi)
+                    : "r"(r[k]));
+                const float2 a = unpack_half2(lo), b = unpack_half2(hi);
+                y[4 * k] = a.x, y[4 * k + 1] = a.y, y[4 * k + 2] = b.x, y[4 * k + 3] = b.y;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[4 * k + e] = (float)(signed char)(r[k] >> (8 * e));
+            }
+    }
+};
+
+// The largest finite magnitude of two packed fp16 values, as their bits.
+__device__ __forceinline__ uint32_t finite_bits(uint32_t v) {
+    const uint32_t m = v & 0x7fff7fffu;
+    return m & __vcmpltu2(m, 0x7c007c00u);
+}
+
+constexpr int kThreads = 256;
+constexpr int kVecs = 8;  // vectors of 8 elements per thread
+
+// TILE threads per tile.
+template <bool E4M3, int D, int TILE>
+__global__ void __launch_bounds__(kThreads) write_q8_kernel(const __grid_constant__ WriteParams p) {
+    constexpr int kPerRow = D / 8, kTiles = kThreads / TILE;
+    constexpr float kTop = Codes<E4M3>::kTop;
+    __shared__ uint32_t tops[kThreads / 32];
+    grid_dependency_wait();
+    launch_dependents();
+    const int in = threadIdx.x % TILE;
+    const int64_t tile = (int64_t)blockIdx.x * kTiles + threadIdx.x / TILE;
+    // tiles of one block side by side: its heads' keys, then its heads' values
+    const int64_t unit = tile / (2 * p.num_kv_heads);
+    const int rest = (int)(tile - unit * 2 * p.num_kv_heads);
+    const int which = rest >= p.num_kv_heads, head = rest - which * p.num_kv_heads;
+    TouchedBlock b = {-1, 0, 0, 0};
+    if (tile < p.tiles) b = touched_block(p.t, unit, in == 0 && rest == 0);
+    const int64_t at = (int64_t)b.phys * p.num_kv_heads + head;
+    float *scale = p.scale[which] + (int64_t)b.phys * p.scale_stride + head;
+    uint2 *codes = reinterpret_cast<uint2 *>(p.cache[which]) + (at << p.t.block_shift) * kPerRow;
+    const __half *src = p.rows[which] + (b.token - b.lo) * p.stride[which] + (int64_t)head * D;
+
+    uint4 x[kVecs];
+    uint32_t top = 0;
+    float before = 0.f;
+    if (b.phys >= 0) {
+        if (b.lo > 0) before = *scale;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int v = i * TILE + in, r = v / kPerRow;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (r >= b.lo && r < b.hi)
+                x[i] = *reinterpret_cast<const uint4 *>(src + r * p.stride[which] + v % kPerRow * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(finite_bits(x[i].x), finite_bits(x[i].y)),
+                                         __vmaxu2(finite_bits(x[i].z), finite_bits(x[i].w))));
+        top = max(top & 0xffffu, top >> 16);
+    }
+#pragma unroll
+    for (int d = (TILE < 32 ? TILE : 32) / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(kFullMask, top, d));
+    if (TILE > 32) {
+        constexpr int kW = TILE < 32 ? 1 : TILE / 32;
+        if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = top;
+        __syncthreads();  // also: every thread has read the scale
+        const int w0 = threadIdx.x / TILE * kW;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) top = max(top, tops[w0 + w]);
+    } else {
+        __syncwarp();
+    }
+    if (b.phys < 0) return;
+
+    // a0: what the scale stands for; a scale that is no finite one counts as 0
+    float a0 = __half2float(__float2half_rn(before * kTop));
+    if (!(a0 > 0.f)) a0 = 0.f;
+    a0 = fminf(a0, 65504.f);
+    const float a = fmaxf(a0, __half2float(__ushort_as_half((unsigned short)top)));
+    const bool grown = b.lo > 0 && a > a0;
+    if (in == 0 && (b.lo == 0 || grown)) *scale = a / kTop;
+    const float by = a > 0.f ? a : 1.f;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const int v = i * TILE + in, r = v / kPerRow;
+        const bool fresh = r >= b.lo && r < b.hi;
+        if (!fresh && !(grown && r < b.lo)) continue;
+        float y[8];
+        if (fresh) {
+            unpack8(x[i], y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = y[e] * kTop / by;
+        } else {
+            Codes<E4M3>::unpack(codes[v], y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = y[e] * a0 / by;
+        }
+        codes[v] = Codes<E4M3>::pack(y);
+    }
+}
+
+template <bool E4M3, int D>
+const void *write_kernel(int tile) {
+    switch (tile) {
+        case 8: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, 8>);
+        case 16: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, 16>);
+        case 32: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, 32>);
+        case 64: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, 64>);
+        case 128: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, 128>);
+        default: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, 256>);
+    }
+}
+
+// ---- the key bounds ----
+
+struct BoundsParams {
+    TouchedParams t;
+    const unsigned char *cache;
+    const float *scale;
+    __half *bounds;
+    int64_t tiles;
+    int num_kv_heads;
+    int scale_stride;
+};
+
+// A warp per (block, KV head): lanes take 8 channels each of 4 (head_dim 64) or 2
+// rows at a time.  Bound by HBM: the block's rows are read once.
+template <int TYPE, int D>
+__global__ void __launch_bounds__(kThreads) key_bounds_kernel(const __grid_constant__ BoundsParams p) {
+    constexpr int kPerRow = D / 8, kRows = 32 / kPerRow, kAhead = 8;
+    grid_dependency_wait();
+    launch_dependents();
+    const int lane = threadIdx.x % 32, row = lane / kPerRow, col = lane % kPerRow;
+    const int64_t tile = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    if (tile >= p.tiles) return;
+    const int64_t unit = tile / p.num_kv_heads;
+    const int head = (int)(tile - unit * p.num_kv_heads);
+    const TouchedBlock b = touched_block(p.t, unit, lane == 0 && head == 0);
+    if (b.phys < 0) return;
+    const int64_t at = (int64_t)b.phys * p.num_kv_heads + head;
+    const int64_t first = (at << p.t.block_shift) * kPerRow + col;
+    __half2 hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        hi[k] = __halves2half2(__ushort_as_half(0xfc00), __ushort_as_half(0xfc00));
+        lo[k] = __hneg2(hi[k]);
+    }
+    for (int r0 = row; r0 < b.hi; r0 += kRows * kAhead) {
+        uint4 x[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = r0 + i * kRows;
+            if (r < b.hi) {
+                if (TYPE == PKV_CACHE_F16) {
+                    x[i] = reinterpret_cast<const uint4 *>(p.cache)[first + (int64_t)r * kPerRow];
+                } else {
+                    const uint2 c = reinterpret_cast<const uint2 *>(p.cache)[first + (int64_t)r * kPerRow];
+                    float y[8];
+                    Codes<TYPE == PKV_CACHE_E4M3>::unpack(c, y);
+                    x[i] = pack8(y);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (r0 + i * kRows < b.hi) {
+                const __half2 *h = reinterpret_cast<const __half2 *>(&x[i]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    hi[k] = __hmax2_nan(hi[k], h[k]);
+                    lo[k] = __hmin2_nan(lo[k], h[k]);
+                }
+            }
+    }
+#pragma unroll
+    for (int d = kPerRow; d < 32; d <<= 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            hi[k] = __hmax2_nan(hi[k], __shfl_xor_sync(kFullMask, hi[k], d));
+            lo[k] = __hmin2_nan(lo[k], __shfl_xor_sync(kFullMask, lo[k], d));
+        }
+    if (row < 2) {  // one row of lanes writes the maxima, the next the minima
+        uint4 y;
+        __half2 *h = reinterpret_cast<__half2 *>(&y);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = row ? lo[k] : hi[k];
+        if (TYPE != PKV_CACHE_F16) {
+            const float s = p.scale[(int64_t)b.phys * p.scale_stride + head];
+            float f[8];
+            unpack8(y, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] *= s;
+            y = pack8(f);
+        }
+        reinterpret_cast<uint4 *>(p.bounds)[(at * 2 + row) * kPerRow + col] = y;
+    }
+}
+
+template <int D>
+const void *bounds_kernel(int type) {
+    return type == PKV_CACHE_F16    ? reinterpret_cast<const void *>(&key_bounds_kernel<PKV_CACHE_F16, D>)
+           : type == PKV_CACHE_INT8 ? reinterpret_cast<const void *>(&key_bounds_kernel<PKV_CACHE_INT8, D>)
+                                    : reinterpret_cast<const void *>(&key_bounds_kernel<PKV_CACHE_E4M3, D>);
+}
+
+bool good_block_size(int bs) { return bs == 8 || bs == 16 || bs == 32 || bs == 64 || bs == 128; }
+
+// What both calls check of the sequences; PKV_OK fills t.
+int sequences(TouchedParams &t, const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+              const int32_t *query_starts, int num_tokens, int num_seqs, int num_kv_heads, int head_dim,
+              int block_size, int num_blocks, int32_t *dev_status) {
+    if (num_tokens < 0 || num_seqs < 0 || num_seqs > 4096 || max_blocks_per_seq < 1 || num_blocks < 1 ||
+        num_kv_heads < 1 || num_kv_heads > (1 << 16) || block_size < 1 || head_dim < 1)
+        return PKV_ERR_INVALID_ARG;
+    if (!block_tables || !context_lens || (!query_starts && num_tokens != num_seqs)) return PKV_ERR_INVALID_ARG;
+    if ((int64_t)max_blocks_per_seq * block_size > (1 << 30)) return PKV_ERR_INVALID_ARG;
+    if ((int64_t)num_blocks * num_kv_heads > (INT64_C(1) << 31) / block_size) return PKV_ERR_INVALID_ARG;
+    if ((head_dim != 64 && head_dim != 128) || !good_block_size(block_size)) return PKV_ERR_UNSUPPORTED;
+    t.block_tables = block_tables;
+    t.context_lens = context_lens;
+    t.query_starts = query_starts;
+    t.status = dev_status;
+    t.num_tokens = num_tokens;
+    t.num_seqs = num_seqs;
+    t.max_blocks_per_seq = max_blocks_per_seq;
+    t.num_blocks = num_blocks;
+    t.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : 7;
+    return PKV_OK;
+}
+
+int launch(const void *fn, int64_t blocks, void **args, pkv_stream_t stream) {
+    if (blocks > INT32_MAX) return PKV_ERR_INVALID_ARG;
+    if (launch_pdl(fn, dim3((unsigned)blocks), dim3(kThreads), 0, stream, args) != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_CUDA;
+    }
+    return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" int pkv_reshape_and_cache_q8(const void *key, int64_t key_stride, const void *value, int64_t value_stride,
+                                        void *key_cache, void *value_cache, float *key_scale, float *value_scale,
+                                        int scale_stride, const int32_t *block_tables, int max_blocks_per_seq,
+                                        const int32_t *context_lens, const int32_t *query_starts, int num_tokens,
+                                        int num_seqs, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                        int cache_type, int32_t *dev_status, pkv_stream_t stream) {
+    if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
+    if (cache_type != PKV_CACHE_INT8 && cache_type != PKV_CACHE_E4M3) return PKV_ERR_INVALID_ARG;
+    if (!key || !value || !key_cache || !value_cache || !key_scale || !value_scale) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(key) || !aligned16(value) || !aligned16(key_cache) || !aligned16(value_cache))
+        return PKV_ERR_INVALID_ARG;
+    WriteParams p = {};
+    const int rc = sequences(p.t, block_tables, max_blocks_per_seq, context_lens, query_starts, num_tokens, num_seqs,
+                             num_kv_heads, head_dim, block_size, num_blocks, dev_status);
+    if (rc != PKV_OK) return rc;
+    const int64_t row = (int64_t)num_kv_heads * head_dim;
+    if (key_stride < row || key_stride % 8 || value_stride < row || value_stride % 8 ||
+        scale_stride < num_kv_heads)
+        return PKV_ERR_INVALID_ARG;
+    p.rows[0] = static_cast<const __half *>(key);
+    p.rows[1] = static_cast<const __half *>(value);
+    p.stride[0] = key_stride;
+    p.stride[1] = value_stride;
+    p.cache[0] = static_cast<unsigned char *>(key_cache);
+    p.cache[1] = static_cast<unsigned char *>(value_cache);
+    p.scale[0] = key_scale;
+    p.scale[1] = value_scale;
+    p.scale_stride = scale_stride;
+    p.num_kv_heads = num_kv_heads;
+    p.tiles = touched_units(num_tokens, num_seqs, p.t.block_shift, query_starts != nullptr) * 2 * num_kv_heads;
+    const int tile = block_size * head_dim / 64;
+    const bool e4m3 = cache_type == PKV_CACHE_E4M3;
+    const void *fn = head_dim == 64 ? (e4m3 ? write_kernel<true, 64>(tile) : write_kernel<false, 64>(tile))
+                                    : (e4m3 ? write_kernel<true, 128>(tile) : write_kernel<false, 128>(tile));
+    void *args[] = {&p};
+    const int64_t per = kThreads / tile;
+    return launch(fn, (p.tiles + per - 1) / per, args, stream);
+}
+
+extern "C" int pkv_block_key_bounds(void *key_bounds, const void *key_cache, const float *key_scale,
+                                    int scale_stride, const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                                    const int32_t *query_starts, int num_tokens, int num_seqs, int num_kv_heads,
+                                    int head_dim, int block_size, int num_blocks, int cache_type,
+                                    int32_t *dev_status, pkv_stream_t stream) {
+    if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
+    if (cache_type != PKV_CACHE_F16 && cache_type != PKV_CACHE_INT8 && cache_type != PKV_CACHE_E4M3)
+        return PKV_ERR_INVALID_ARG;
+    if (!key_bounds || !key_cache || (cache_type != PKV_CACHE_F16 && (!key_scale || scale_stride < num_kv_heads)))
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned16(key_bounds) || !aligned16(key_cache)) return PKV_ERR_INVALID_ARG;
+    BoundsParams p = {};
+    const int rc = sequences(p.t, block_tables, max_blocks_per_seq, context_lens, query_starts, num_tokens, num_seqs,
+                             num_kv_heads, head_dim, block_size, num_blocks, dev_status);
+    if (rc != PKV_OK) return rc;
+    p.cache = static_cast<const unsigned char *>(key_cache);
+    p.scale = key_scale;
+    p.scale_stride = scale_stride;
+    p.bounds = static_cast<__half *>(key_bounds);
+    p.num_kv_heads = num_kv_heads;
+    p.tiles = touched_units(num_tokens, num_seqs, p.t.block_shift, query_starts != nullptr) * num_kv_heads;
+    void *args[] = {&p};
+    constexpr int64_t per = kThreads / 32;
+    return launch(head_dim == 64 ? bounds_kernel<64>(cache_type) : bounds_kernel<128>(cache_type),
+                  (p.tiles + per - 1) / per, args, stream);
+}

@@ -1,0 +1,619 @@
+// pkv_team_impl.cuh -- the team decode: single-token attention over a cache of
+// 8-bit codes with a scale per (block, KV head), or over listed blocks.
+//
+// For each (sequence, KV head) and query head h of its group, over the rows t
+// (all of the context, or those of the listed blocks):
+//
+//     x_t = c k_b (q_h . K_t),   out = sum_t e^{x_t} v_b V_t / sum_t e^{x_t}
+//
+// with K, V the codes (exact in fp16), k_b, v_b the scales of t's block (1 for
+// an fp16 cache) and c the softmax scale.  With y_t = x_t + ln v_b and m the
+// running maximum of y, the weights w_t = e^{x_t - m} v_b are at most 1 whatever
+// the scales, and the sum runs over e^{x_t - m}: one exponential per score.
+//
+// Bound by HBM: a row is read once for all query heads of its group.  8-bit rows
+// halve the bytes, so the work per byte doubles: the split and the layout are
+// chosen for few instructions per row.
+//  * All 8 warps of a CTA work on one segment's piece, each on every eighth
+//    step of 16 or 32 rows, with a ring of its own (cp.async, two to four steps
+//    in flight, 128 KB per SM) that runs on into the next pieces; the warps meet
+//    once per piece, in shared memory.
+//  * mma.sync m16n8k16 with the rows on M and the heads on N for the scores
+//    (8 heads fill N; a 16-row tile takes D/16 instructions), and the dims on M
+//    and the heads on N for the output, transposed: the codes come from shared
+//    memory by ldmatrix (.trans for V) as pairs of bytes, whose dims are taken
+//    in the order that the fragments want them (queries and outputs follow it),
+//    so that widening to fp16 is all that is done to them.  The weights turn
+//    from the scores' layout to the product's by movmatrix.
+//  * Weights are stored as fp16 after a factor of 2^15: 11 significant bits down
+//    to 2^-29 of the largest.
+//  * A piece that is a whole segment is divided and written by the CTA; one that
+//    a CTA boundary cuts leaves (maximum, sum, output) in the workspace for the
+//    joining kernel, which runs behind it with its launch hidden.
+#ifndef PKV_TEAM_IMPL_CUH
+#define PKV_TEAM_IMPL_CUH
+
+#include <math_constants.h>
+
+#include "pkv_device.cuh"
+#include "pkv_team_params.h"
+#include "pkv_team_schedule.h"
+
+namespace pkv {
+
+enum TeamKind { kTeamF16, kTeamInt8, kTeamE4m3 };
+
+template <int KIND, int D>
+struct TeamConfig {
+    static constexpr bool kWide = KIND == kTeamF16;
+    static constexpr int kRowBytes = D * (kWide ? 2 : 1);
+    static constexpr int kRows = kRowBytes == 64 ? 32 : 16;  // of a step
+    static constexpr int kTiles = kRows / 16;
+    static constexpr int kGroups = kRows / 8;                // a group of 8 rows lies in one block
+    static constexpr int kUnits = kRowBytes / 16;            // 16-byte units of a row
+    static constexpr int kTileBytes = kRows * kRowBytes;
+    static constexpr int kStages = 16384 / (2 * kTileBytes); // 16 KB per warp in flight
+    static constexpr int kCopies = kRows * kUnits / 32;      // of a lane, per cache and step
+    static constexpr int kPitch = D + 8;                     // floats between heads of a warp's output
+    // [warps][stages][K, V tiles] [warps][stages][groups] float4 (scales, rows)
+    // [warps][8 heads][pitch] floats, [warps][8 heads] (maximum, sum), then by sequence: cum, context
+    static constexpr size_t kMeta = (size_t)kTeamWarps * kStages * 2 * kTileBytes;
+    static constexpr size_t kRed = kMeta + (size_t)kTeamWarps * kStages * kGroups * 16;
+    static constexpr size_t kMl = kRed + (size_t)kTeamWarps * 8 * kPitch * 4;
+    static constexpr size_t kCum = kMl + (size_t)kTeamWarps * 8 * 8;
+    static constexpr size_t kFixed = kCum + 8 + 16;          // + the last cum, alignment
+};
+
+// Steps that a CTA boundary moves at most to spare a cut, and the least a CTA takes.
+constexpr int kTeamSnap = 8;
+constexpr int kTeamLeast = 8;
+
+// Byte of 16-byte unit u of row r in a tile whose rows are RB bytes: eight
+// consecutive rows' unit u lie in eight different 16-byte columns of the banks.
+template <int RB>
+__device__ __forceinline__ int team_swizzle(int r, int u) {
+    if (RB == 64) return r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
+    return r * RB + ((u ^ (r & 7)) << 4);
+}
+
+// Four codes in a register -> the fp16 pairs (b0, b1), (b2, b3), or with PAIRED
+// (b0, b2), (b1, b3).  int8: u = code + 128 in the low bits of 1024 + u.
+template <int KIND, bool PAIRED>
+__device__ __forceinline__ void team_widen(uint32_t codes, uint32_t &lo, uint32_t &hi) {
+    if (KIND == kTeamInt8) {
+        const uint32_t u = codes ^ 0x80808080u;
+        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+        const uint32_t a = __byte_perm(u, 0x64646464u, PAIRED ? 0x4240 : 0x4140);
+        const uint32_t b = __byte_perm(u, 0x64646464u, PAIRED ? 0x4341 : 0x4342);
+        const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
+        const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
+        lo = *reinterpret_cast<const uint32_t *>(&x);
+        hi = *reinterpret_cast<const uint32_t *>(&y);
+    } else {
+        const uint32_t c = PAIRED ? __byte_perm(codes, 0, 0x3120) : codes;
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(c));
+    }
+}
+
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_4_or_zero(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// 2^x for x <= 15 or so; 2^-inf = 0.
+__device__ __forceinline__ float team_exp2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+constexpr float kTeamPlace = 15.f;  // weights are stored times 2^15
+
+// A warp's attention state: lane (g, t) = (lane / 4, lane % 4) has heads 2t and
+// 2t + 1 of each tile of eight: m their maximum (the same on all g), l the sum
+// over the rows that this lane has seen, o[i] the output of the fragment's dims.
+template <int D, int NT>
+struct TeamState {
+    float m[NT][2], l[NT][2];
+    float o[NT][D / 16][4];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m[n][0] = m[n][1] = -CUDART_INF_F;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+        }
+    }
+};
+
+// The dim of o[i][2 * second + ...] of lane row g.
+template <int KIND>
+__device__ __forceinline__ int team_dim(int i, int g, int second) {
+    return KIND == kTeamF16 ? 16 * i + g + 8 * second : 16 * i + 2 * g + second;
+}
+
+// One step: tiles at kt, vt (shared addresses), meta[group] = (key scale, value
+// scale, live rows).
+template <int KIND, int D, int NT>
+__device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt, const float4 *meta,
+                                          const uint32_t (&q)[NT][D / 16][2], float scale_log2, TeamState<D, NT> &st,
+                                          int lane) {
+    using C = TeamConfig<KIND, D>;
+    constexpr int RB = C::kRowBytes;
+    const int g = lane >> 2;
+    const int row16 = (lane & 7) + ((lane >> 3) & 1) * 8, second = lane >> 4;  // ldmatrix: this lane's row and unit
+
+    float s[C::kTiles][NT][4];
+#pragma unroll
+    for (int r = 0; r < C::kTiles; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[r][n][0] = s[r][n][1] = s[r][n][2] = s[r][n][3] = 0.f;
+#pragma unroll
+    for (int u = 0; u < C::kUnits; u += 2)
+#pragma unroll
+        for (int r = 0; r < C::kTiles; ++r) {
+            uint32_t x0, x1, x2, x3;  // rows 0-7, rows 8-15 of unit u, the same of unit u + 1
+            ldsm_x4(kt + team_swizzle<RB>(r * 16 + row16, u + second), x0, x1, x2, x3);
+            if constexpr (C::kWide) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_16816(s[r][n], x0, x1, x2, x3, q[n][u / 2][0], q[n][u / 2][1]);
+            } else {
+                uint32_t a0, a1, a2, a3;
+                team_widen<KIND, false>(x0, a0, a2);
+                team_widen<KIND, false>(x1, a1, a3);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_16816(s[r][n], a0, a1, a2, a3, q[n][u][0], q[n][u][1]);
+                team_widen<KIND, false>(x2, a0, a2);
+                team_widen<KIND, false>(x3, a1, a3);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_16816(s[r][n], a0, a1, a2, a3, q[n][u + 1][0], q[n][u + 1][1]);
+            }
+        }
+
+    // scores in log2 units; x: for the sum, x + lv: with the value's scale
+    float lv[C::kGroups], vs[C::kGroups];
+    float top[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -CUDART_INF_F;
+#pragma unroll
+    for (int r = 0; r < C::kTiles; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = 2 * r + h;
+            const float4 info = meta[j];
+            const bool live = g < __float_as_int(info.z);
+            const float f = C::kWide ? scale_log2 : scale_log2 * info.x;
+            vs[j] = C::kWide ? 1.f : info.y;
+            // the logarithm only places the weights: bounded, so that a scale of zero does not
+            lv[j] = C::kWide ? 0.f : fminf(fmaxf(__log2f(info.y), -40.f), 40.f);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float &x = s[r][n][2 * h + e];
+                    x = live ? x * f : -CUDART_INF_F;
+                    top[n][e] = fmaxf(top[n][e], x + lv[j]);
+                }
+        }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top[n][e] = fmaxf(top[n][e], __shfl_xor_sync(kFullMask, top[n][e], d));
+
+    bool moved = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) moved |= top[n][e] > st.m[n][e];
+    if (__any_sync(kFullMask, moved)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float to = fmaxf(top[n][e], st.m[n][e]);
+                f[e] = to == -CUDART_INF_F ? 1.f : team_exp2(st.m[n][e] - to);
+                st.m[n][e] = to;
+                st.l[n][e] *= f[e];
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                st.o[n][i][0] *= f[0];
+                st.o[n][i][1] *= f[1];
+                st.o[n][i][2] *= f[0];
+                st.o[n][i][3] *= f[1];
+            }
+        }
+    }
+    uint32_t w[C::kGroups][NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        float ref[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) ref[e] = (st.m[n][e] == -CUDART_INF_F ? 0.f : st.m[n][e]) - kTeamPlace;
+#pragma unroll
+        for (int r = 0; r < C::kTiles; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float p0 = team_exp2(s[r][n][2 * h] - ref[0]), p1 = team_exp2(s[r][n][2 * h + 1] - ref[1]);
+                st.l[n][0] += p0;
+                st.l[n][1] += p1;
+                w[2 * r + h][n] = transpose_8x8(pack_half2(p0 * vs[2 * r + h], p1 * vs[2 * r + h]));
+            }
+    }
+
+#pragma unroll
+    for (int r = 0; r < C::kTiles; ++r)
+#pragma unroll
+        for (int u = 0; u < C::kUnits; u += 2) {
+            uint32_t x0, x1, x2, x3;
+            ldsm_x4_trans(vt + team_swizzle<RB>(r * 16 + row16, u + second), x0, x1, x2, x3);
+            if constexpr (C::kWide) {  // x0, x1: rows 0-7 and 8-15 of dims 0-7; x2, x3: of dims 8-15
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_16816(st.o[n][u / 2], x0, x2, x1, x3, w[2 * r][n], w[2 * r + 1][n]);
+            } else {
+                uint32_t a0, a1, a2, a3;
+                team_widen<KIND, true>(x0, a0, a1);
+                team_widen<KIND, true>(x1, a2, a3);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_16816(st.o[n][u], a0, a1, a2, a3, w[2 * r][n], w[2 * r + 1][n]);
+                team_widen<KIND, true>(x2, a0, a1);
+                team_widen<KIND, true>(x3, a2, a3);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma_16816(st.o[n][u + 1], a0, a1, a2, a3, w[2 * r][n], w[2 * r + 1][n]);
+            }
+        }
+}
+
+// A walk over a CTA's share, every kTeamWarps-th step of it.
+struct TeamCursor {
+    int64_t g, c, n;
+    int s, kvh;
+    __device__ __forceinline__ void begin(const int64_t *cum, int num_seqs, int heads, int64_t at, int64_t end) {
+        g = at;
+        if (at >= end) return;
+        const TeamPos p = team_locate(cum, num_seqs, heads, at);
+        s = p.s, kvh = p.kvh, c = p.c, n = p.n;
+    }
+    __device__ __forceinline__ void next(const int64_t *cum, int heads, int64_t end) {
+        g += kTeamWarps;
+        if (g >= end) return;
+        c += kTeamWarps;
+#pragma unroll 1
+        while (c >= n) {  // there is a later segment: g is before the end
+            c -= n;
+            if (++kvh == heads) {
+                kvh = 0;
+                do ++s; while (cum[s + 1] == cum[s]);
+                n = cum[s + 1] - cum[s];
+            }
+        }
+    }
+};
+
+template <int KIND, int D, int NT>
+__global__ void __launch_bounds__(kTeamThreads, 1) team_kernel(const __grid_constant__ TeamParams p) {
+    using C = TeamConfig<KIND, D>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    float *red = reinterpret_cast<float *>(smem + C::kRed);
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::kMl);
+    int64_t *cum = reinterpret_cast<int64_t *>(smem + C::kCum);
+    int *lens = reinterpret_cast<int *>(cum + p.num_seqs + 1);
+    __shared__ int64_t warp_sum[kTeamWarps], share[2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int heads = p.num_kv_heads, bs = 1 << p.block_shift;
+
+    grid_dependency_wait();
+    launch_dependents();
+
+    // Contexts, and the prefix sums of the sequences' steps.
+    {
+        const int64_t reach = (int64_t)p.max_blocks_per_seq << p.block_shift;
+        const int per = (p.num_seqs + kTeamThreads - 1) / kTeamThreads;
+        const int first = tid * per;
+        int64_t mine = 0;
+        bool bad = false;
+        for (int i = 0; i < per; ++i) {
+            const int s = first + i;
+            if (s >= p.num_seqs) break;
+            int len = __ldg(p.context_lens + s);
+            bad |= len < 0 || len > reach;
+            len = len < 0 ? 0 : len > reach ? (int)reach : len;
+            lens[s] = len;
+            mine += team_steps(team_rows(len, p.block_shift, p.selected ? p.max_selected : -1), C::kRows);
+        }
+        if (bad && blockIdx.x == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
+        int64_t sum = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t x = __shfl_up_sync(kFullMask, sum, d);
+            if (lane >= d) sum += x;
+        }
+        if (lane == 31) warp_sum[warp] = sum;
+        __syncthreads();
+        int64_t at = sum - mine;
+        for (int w = 0; w < warp; ++w) at += warp_sum[w];
+        for (int i = 0; i < per; ++i) {
+            const int s = first + i;
+            if (s >= p.num_seqs) break;
+            cum[s] = at;
+            at += team_steps(team_rows(lens[s], p.block_shift, p.selected ? p.max_selected : -1), C::kRows);
+        }
+        if (tid == kTeamThreads - 1) cum[p.num_seqs] = at;
+        __syncthreads();
+    }
+    const int64_t T = cum[p.num_seqs] * heads;
+    const int64_t ctas = team_ctas(T, gridDim.x, kTeamLeast);
+    if (tid < 2) share[tid] = (int64_t)blockIdx.x + tid <= ctas ? team_start(cum, p.num_seqs, heads, blockIdx.x + tid, ctas, kTeamSnap) : T;
+    // Rows of sequences without a position.
+    for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x)
+        if (cum[s + 1] == cum[s])
+            for (int i = tid; i < p.num_heads * D / 8; i += kTeamThreads)
+                reinterpret_cast<uint4 *>(p.out + (int64_t)s * p.num_heads * D)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    const int64_t a = share[0], b = share[1];
+    int2 cut = make_int2(-1, -1);
+
+    // ---- the ring ----
+    const uint32_t ring = smem_addr(smem) + warp * C::kStages * 2 * C::kTileBytes;
+    float4 *meta = reinterpret_cast<float4 *>(smem + C::kMeta) + warp * C::kStages * C::kGroups;
+    TeamCursor ahead;  // the next step to issue
+    ahead.begin(cum, p.num_seqs, heads, a + warp, b);
+    // lane j < kGroups: physical block and live rows of group j of that step
+    int phys = 0, rows = 0;
+    auto look_up = [&]() {
+        rows = 0;
+        if (lane < C::kGroups && ahead.g < b) {
+            const int64_t v = ahead.c * C::kRows + lane * 8;  // row of the segment
+            int64_t block = v >> p.block_shift;
+            const int len = lens[ahead.s];
+            bool bad = false, there = true;
+            if (p.selected) {
+                const int64_t seg = (int64_t)ahead.s * heads + ahead.kvh;
+                const int blocks = (len + bs - 1) >> p.block_shift;
+                const int most = min(blocks, p.max_selected);
+                int count = __ldg(p.num_selected + seg);
+                bad = (count < 0 || count > most) && ahead.c == 0 && lane == 0;
+                count = min(count, most);
+                there = block < count;
+                if (there) {
+                    block = __ldg(p.selected + seg * p.max_selected + block);
+                    if (block < 0 || block >= blocks) bad = true, there = false;
+                }
+            }
+            if (there) {
+                const int64_t pos = (block << p.block_shift) + (v & (bs - 1));
+                rows = (int)max((int64_t)0, min((int64_t)8, len - pos));
+                if (rows > 0) {
+                    phys = __ldg(p.block_tables + (int64_t)ahead.s * p.max_blocks_per_seq + block);
+                    if (phys < 0 || phys >= p.num_blocks) bad = true, phys = 0;
+                }
+            }
+            if (bad) report(p.status, PKV_ERR_OUT_OF_RANGE);
+        }
+    };
+    auto issue = [&](int stage) {
+        if (ahead.g < b) {
+            const uint32_t kt = ring + stage * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
+            const int off0 = (int)(ahead.c * C::kRows) & (bs - 1);
+#pragma unroll
+            for (int i = 0; i < C::kCopies; ++i) {
+                const int idx = i * 32 + lane, r = idx / C::kUnits, u = idx % C::kUnits;
+                const int block = __shfl_sync(kFullMask, phys, r >> 3);
+                const bool live = (r & 7) < __shfl_sync(kFullMask, rows, r >> 3);
+                const int64_t at = ((((int64_t)block * heads + ahead.kvh) << p.block_shift) + ((off0 + r) & (bs - 1))) *
+                                       C::kRowBytes + u * 16;
+                const int64_t from = live ? at : 0;
+                cp_async_16_or_zero(kt + team_swizzle<C::kRowBytes>(r, u),
+                                    static_cast<const unsigned char *>(p.key_cache) + from, live);
+                cp_async_16_or_zero(vt + team_swizzle<C::kRowBytes>(r, u),
+                                    static_cast<const unsigned char *>(p.value_cache) + from, live);
+            }
+            if (lane < C::kGroups) {
+                float4 *m = meta + stage * C::kGroups + lane;
+                m->z = __int_as_float(rows);
+                if (!C::kWide) {
+                    const int64_t at = rows > 0 ? (int64_t)phys * p.scale_stride + ahead.kvh : 0;
+                    cp_async_4_or_zero(smem_addr(&m->x), p.key_scale + at, rows > 0);
+                    cp_async_4_or_zero(smem_addr(&m->y), p.value_scale + at, rows > 0);
+                }
+            }
+            ahead.next(cum, heads, b);
+            look_up();
+        }
+        cp_async_commit();
+    };
+    look_up();
+    for (int i = 0; i < C::kStages; ++i) issue(i);
+
+    // ---- pieces ----
+    const int g = lane >> 2, t = lane & 3;
+    TeamState<D, NT> st;
+    uint32_t q[NT][D / 16][2];
+    int stage = 0;
+    int64_t mine = a + warp;  // this warp's next step
+    TeamPos at = {};
+    if (a < b) at = team_locate(cum, p.num_seqs, heads, a);
+    for (int64_t begin = a; begin < b;) {
+        const int64_t seg0 = begin - at.c, seg1 = seg0 + at.n;
+        const int64_t end = seg1 < b ? seg1 : b;
+        const bool whole = seg0 >= a && seg1 <= b;
+        const __half *rows_q = p.query + ((int64_t)at.s * p.num_heads + (int64_t)at.kvh * p.group) * D;
+        if (mine < end) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int h = n * 8 + g;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    // fp16: dims 2t, 2t + 1 and 8 further; codes: dims 4t to 4t + 3
+                    const __half *src = rows_q + h * D + 16 * k + (C::kWide ? 2 * t : 4 * t);
+                    q[n][k][0] = h < p.group ? __ldg(reinterpret_cast<const uint32_t *>(src)) : 0u;
+                    q[n][k][1] = h < p.group ? __ldg(reinterpret_cast<const uint32_t *>(src + (C::kWide ? 8 : 2))) : 0u;
+                }
+            }
+        }
+        st.clear();
+        for (; mine < end; mine += kTeamWarps) {
+            cp_async_wait<C::kStages - 1>();
+            __syncwarp();
+            const uint32_t kt = ring + stage * 2 * C::kTileBytes;
+            team_step<KIND, D, NT>(kt, kt + C::kTileBytes, meta + stage * C::kGroups, q, p.scale_log2, st, lane);
+            __syncwarp();
+            issue(stage);
+            if (++stage == C::kStages) stage = 0;
+        }
+
+        // ---- the warps' outputs, eight heads at a time ----
+        const int slot = seg0 < a ? 0 : 1;
+        if (!whole) (slot ? cut.y : cut.x) = (int)((int64_t)at.s * heads + at.kvh);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int live = min(8, p.group - n * 8);
+            if (NT > 1 && live <= 0) break;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l = st.l[n][e];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(kFullMask, l, d);
+                const int h = 2 * t + e;
+                if (h < live) {
+                    if (g == 0) ml[warp * 8 + h] = make_float2(st.m[n][e], l);
+                    float *dst = red + (warp * 8 + h) * C::kPitch;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        dst[team_dim<KIND>(i, g, 0)] = st.o[n][i][e];
+                        dst[team_dim<KIND>(i, g, 1)] = st.o[n][i][2 + e];
+                    }
+                }
+            }
+            __syncthreads();
+            for (int i = tid; i < live * (D / 2); i += kTeamThreads) {
+                const int h = i / (D / 2), d = i % (D / 2) * 2;
+                float top = -CUDART_INF_F, l = 0.f;
+#pragma unroll
+                for (int w = 0; w < kTeamWarps; ++w) top = fmaxf(top, ml[w * 8 + h].x);
+                const float ref = top == -CUDART_INF_F ? 0.f : top;
+                float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kTeamWarps; ++w) {
+                    const float2 x = ml[w * 8 + h];
+                    const float f = team_exp2(x.x - ref);
+                    const float2 y = *reinterpret_cast<const float2 *>(red + (w * 8 + h) * C::kPitch + d);
+                    l = fmaf(x.y, f, l);
+                    o.x = fmaf(y.x, f, o.x);
+                    o.y = fmaf(y.y, f, o.y);
+                }
+                const int head = n * 8 + h;
+                if (whole) {
+                    const float inv = l == 0.f ? 0.f : 1.f / l;  // no row: zeros
+                    const int64_t row = (int64_t)at.s * p.num_heads + (int64_t)at.kvh * p.group + head;
+                    *reinterpret_cast<__half2 *>(p.out + row * D + d) = __floats2half2_rn(o.x * inv, o.y * inv);
+                } else {
+                    const int64_t part = ((int64_t)blockIdx.x * 2 + slot) * p.group + head;
+                    if (d == 0) p.part_ml[part] = make_float2(top, l);
+                    *reinterpret_cast<float2 *>(p.part_o + part * D + d) = o;
+                }
+            }
+            __syncthreads();
+        }
+        begin = end;
+        at.c = 0;
+        if (begin < b && ++at.kvh == heads) {
+            at.kvh = 0;
+            do ++at.s; while (cum[at.s + 1] == cum[at.s]);
+            at.n = cum[at.s + 1] - cum[at.s];
+        }
+    }
+    if (tid == 0) p.cut[blockIdx.x] = cut;
+}
+
+// Joins the parts of segments that CTA boundaries cut: block (c, h) takes head h
+// of the segment whose first part is CTA c's last piece.
+constexpr int kTeamJoinThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kTeamJoinThreads) team_join_kernel(const __grid_constant__ TeamParams p) {
+    constexpr int kWarps = kTeamJoinThreads / 32, kPer = D / 32;
+    __shared__ float2 ml[kWarps];
+    __shared__ float out[kWarps][D];
+    grid_dependency_wait();
+    launch_dependents();
+    const int c = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int seg = p.cut[c].y;
+    if (seg < 0) return;
+    int parts = 1;  // CTA c's, then the CTAs whose first piece is the same segment's
+    for (int first = c + 1; first < (int)gridDim.x; first += kTeamJoinThreads) {
+        const int i = first + (int)threadIdx.x;
+        const int more = __syncthreads_count(i < (int)gridDim.x && p.cut[i].x == seg);
+        parts += more;
+        if (more < kTeamJoinThreads) break;
+    }
+    float top = -CUDART_INF_F, l = 0.f, o[kPer] = {};
+    for (int i = warp; i < parts; i += kWarps) {
+        const int64_t part = ((int64_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * p.group + h;
+        const float2 x = p.part_ml[part];
+        float y[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) y[k] = p.part_o[part * D + k * 32 + lane];
+        const float to = fmaxf(top, x.x), ref = to == -CUDART_INF_F ? 0.f : to;
+        const float f = team_exp2(top - ref), fx = team_exp2(x.x - ref);
+        top = to;
+        l = l * f + x.y * fx;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) o[k] = o[k] * f + y[k] * fx;
+    }
+    if (lane == 0) ml[warp] = make_float2(top, l);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) out[warp][k * 32 + lane] = o[k];
+    __syncthreads();
+    if (threadIdx.x < D) {
+        float all = -CUDART_INF_F, sum = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) all = fmaxf(all, ml[w].x);
+        const float ref = all == -CUDART_INF_F ? 0.f : all;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = team_exp2(ml[w].x - ref);
+            sum = fmaf(ml[w].y, f, sum);
+            y = fmaf(out[w][threadIdx.x], f, y);
+        }
+        const int s = seg / p.num_kv_heads, kvh = seg % p.num_kv_heads;
+        const int64_t row = (int64_t)s * p.num_heads + (int64_t)kvh * p.group + h;
+        p.out[row * D + threadIdx.x] = __float2half_rn(sum == 0.f ? 0.f : y / sum);
+    }
+}
+
+template <int KIND, int D>
+TeamKernel team_kernel_info(int group) {
+    using C = TeamConfig<KIND, D>;
+    TeamKernel k;
+    k.fn = group <= 8 ? reinterpret_cast<const void *>(&team_kernel<KIND, D, 1>)
+                      : reinterpret_cast<const void *>(&team_kernel<KIND, D, 2>);
+    k.smem_fixed = C::kFixed;
+    k.step_rows = C::kRows;
+    return k;
+}
+
+}  // namespace pkv
+
+#endif  // PKV_TEAM_IMPL_CUH
