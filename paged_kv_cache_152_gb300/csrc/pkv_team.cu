@@ -21,10 +21,13 @@ bool shape_ok(int num_heads, int num_kv_heads, int head_dim) {
            num_heads / num_kv_heads <= kTeamMaxGroup && (head_dim == 64 || head_dim == 128);
 }
 
-int default_ctas(int *ctas) {
+// Shared memory that two CTAs of an SM can have each (the SM's 228 KB less 1 KB each).
+constexpr size_t kSmemOfTwo = 113 * 1024 - 256;
+
+int multiprocessors(int *n) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(ctas, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
     }
@@ -55,8 +58,15 @@ int decode(void *out, const void *query, const void *key_cache, const void *valu
     if (!shape_ok(num_heads, num_kv_heads, head_dim)) return PKV_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128)
         return PKV_ERR_UNSUPPORTED;
-    if (num_ctas == 0 && default_ctas(&num_ctas) != PKV_OK) return PKV_ERR_CUDA;
     const int group = num_heads / num_kv_heads;
+    const TeamKernel k = cache_type == PKV_CACHE_F16    ? team_kernel_f16(head_dim, group)
+                         : cache_type == PKV_CACHE_INT8 ? team_kernel_int8(head_dim, group)
+                                                        : team_kernel_e4m3(head_dim, group);
+    const size_t smem = k.smem_fixed + 8 * (size_t)num_seqs;
+    if (num_ctas == 0) {
+        if (multiprocessors(&num_ctas) != PKV_OK) return PKV_ERR_CUDA;
+        if (k.ctas_per_sm == 2 && smem <= kSmemOfTwo) num_ctas *= 2;
+    }
     const TeamWorkspace ws = TeamWorkspace::plan(num_ctas, group, head_dim);
     if (workspace_bytes < ws.total) return PKV_ERR_INVALID_ARG;
 
@@ -87,10 +97,6 @@ int decode(void *out, const void *query, const void *key_cache, const void *valu
     p.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : 7;
     p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
 
-    const TeamKernel k = cache_type == PKV_CACHE_F16    ? team_kernel_f16(head_dim, group)
-                         : cache_type == PKV_CACHE_INT8 ? team_kernel_int8(head_dim, group)
-                                                        : team_kernel_e4m3(head_dim, group);
-    const size_t smem = k.smem_fixed + 12 * (size_t)num_seqs;
     const int rc = ensure_smem_attr(k.fn, smem);
     if (rc != PKV_OK) return rc;
     void *args[] = {&p};
@@ -116,7 +122,10 @@ using namespace pkv;
 
 extern "C" size_t pkv_decode_team_workspace_size(int num_heads, int num_kv_heads, int head_dim, int num_ctas) {
     if (num_ctas < 0 || num_ctas > kMaxCtas || !shape_ok(num_heads, num_kv_heads, head_dim)) return 0;
-    if (num_ctas == 0 && default_ctas(&num_ctas) != PKV_OK) return 0;
+    if (num_ctas == 0) {
+        if (multiprocessors(&num_ctas) != PKV_OK) return 0;
+        num_ctas *= 2;  // the most that the default is
+    }
     return TeamWorkspace::plan(num_ctas, num_heads / num_kv_heads, head_dim).total;
 }
 

@@ -43,7 +43,7 @@ namespace pkv {
 
 enum TeamKind { kTeamF16, kTeamInt8, kTeamE4m3 };
 
-template <int KIND, int D>
+template <int KIND, int D, int NT>
 struct TeamConfig {
     static constexpr bool kWide = KIND == kTeamF16;
     static constexpr int kRowBytes = D * (kWide ? 2 : 1);
@@ -52,16 +52,15 @@ struct TeamConfig {
     static constexpr int kGroups = kRows / 8;                // a group of 8 rows lies in one block
     static constexpr int kUnits = kRowBytes / 16;            // 16-byte units of a row
     static constexpr int kTileBytes = kRows * kRowBytes;
-    static constexpr int kStages = 16384 / (2 * kTileBytes); // 16 KB per warp in flight
-    static constexpr int kCopies = kRows * kUnits / 32;      // of a lane, per cache and step
+    static constexpr int kCtas = NT == 1 && kTileBytes <= 2048 ? 2 : 1;  // per SM
+    static constexpr int kStages = 16384 / kCtas / (2 * kTileBytes);     // 128 KB per SM in flight
+    static constexpr int kGroupCopies = kUnits / 4;          // of a lane, per cache and group
     static constexpr int kPitch = D + 8;                     // floats between heads of a warp's output
     // [warps][stages][K, V tiles] [warps][stages][groups] float4 (scales, rows)
-    // [warps][8 heads][pitch] floats, [warps][8 heads] (maximum, sum), then by sequence: cum, context
+    // [warps][8 heads] (maximum, sum), then by sequence: cum, then [warps][heads][pitch] floats
     static constexpr size_t kMeta = (size_t)kTeamWarps * kStages * 2 * kTileBytes;
-    static constexpr size_t kRed = kMeta + (size_t)kTeamWarps * kStages * kGroups * 16;
-    static constexpr size_t kMl = kRed + (size_t)kTeamWarps * 8 * kPitch * 4;
-    static constexpr size_t kCum = kMl + (size_t)kTeamWarps * 8 * 8;
-    static constexpr size_t kFixed = kCum + 8 + 16;          // + the last cum, alignment
+    static constexpr size_t kMl = kMeta + (size_t)kTeamWarps * kStages * kGroups * 16;
+    static constexpr size_t kRed = kMl + (size_t)kTeamWarps * 8 * 8;
 };
 
 // Steps that a CTA boundary moves at most to spare a cut, and the least a CTA takes.
@@ -155,7 +154,7 @@ template <int KIND, int D, int NT>
 __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt, const float4 *meta,
                                           const uint32_t (&q)[NT][D / 16][2], float scale_log2, TeamState<D, NT> &st,
                                           int lane) {
-    using C = TeamConfig<KIND, D>;
+    using C = TeamConfig<KIND, D, NT>;
     constexpr int RB = C::kRowBytes;
     const int g = lane >> 2;
     const int row16 = (lane & 7) + ((lane >> 3) & 1) * 8, second = lane >> 4;  // ldmatrix: this lane's row and unit
@@ -285,64 +284,48 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt, const float4
         }
 }
 
-// A walk over a CTA's share, every kTeamWarps-th step of it.
-struct TeamCursor {
-    int64_t g, c, n;
-    int s, kvh;
-    __device__ __forceinline__ void begin(const int64_t *cum, int num_seqs, int heads, int64_t at, int64_t end) {
-        g = at;
-        if (at >= end) return;
-        const TeamPos p = team_locate(cum, num_seqs, heads, at);
-        s = p.s, kvh = p.kvh, c = p.c, n = p.n;
-    }
-    __device__ __forceinline__ void next(const int64_t *cum, int heads, int64_t end) {
-        g += kTeamWarps;
-        if (g >= end) return;
-        c += kTeamWarps;
-#pragma unroll 1
-        while (c >= n) {  // there is a later segment: g is before the end
-            c -= n;
-            if (++kvh == heads) {
-                kvh = 0;
-                do ++s; while (cum[s + 1] == cum[s]);
-                n = cum[s + 1] - cum[s];
-            }
-        }
-    }
+// Up to 32 steps of a warp (every kTeamWarps-th of the CTA's share) in one
+// segment: lane j looks up the block table's entry j of theirs, all at once and a
+// batch ahead of their use.
+struct TeamBatch {
+    int64_t g;      // the first step
+    int s, kvh;     // its segment
+    int c, n;       // the step in the segment, the segment's steps
+    int count;      // steps of the batch, 0: none
+    int phys;       // lane j: physical block of entry j
+    int rows;       //         and its rows in use
 };
 
 template <int KIND, int D, int NT>
-__global__ void __launch_bounds__(kTeamThreads, 1) team_kernel(const __grid_constant__ TeamParams p) {
-    using C = TeamConfig<KIND, D>;
+__global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
+    team_kernel(const __grid_constant__ TeamParams p) {
+    using C = TeamConfig<KIND, D, NT>;
     extern __shared__ __align__(128) unsigned char smem[];
-    float *red = reinterpret_cast<float *>(smem + C::kRed);
     float2 *ml = reinterpret_cast<float2 *>(smem + C::kMl);
-    int64_t *cum = reinterpret_cast<int64_t *>(smem + C::kCum);
-    int *lens = reinterpret_cast<int *>(cum + p.num_seqs + 1);
+    const int red_heads = min(8, p.group);
+    float *red = reinterpret_cast<float *>(smem + C::kRed);
+    int64_t *cum = reinterpret_cast<int64_t *>(red + kTeamWarps * red_heads * C::kPitch);
     __shared__ int64_t warp_sum[kTeamWarps], share[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int heads = p.num_kv_heads, bs = 1 << p.block_shift;
+    const int64_t reach = (int64_t)p.max_blocks_per_seq << p.block_shift;
+    auto context = [&](int s) {
+        const int len = __ldg(p.context_lens + s);
+        return len < 0 ? 0 : len > reach ? (int)reach : len;
+    };
+    auto steps_of = [&](int s) {
+        return team_steps(team_rows(context(s), p.block_shift, p.selected ? p.max_selected : -1), C::kRows);
+    };
 
     grid_dependency_wait();
     launch_dependents();
 
-    // Contexts, and the prefix sums of the sequences' steps.
+    // The prefix sums of the sequences' steps.
     {
-        const int64_t reach = (int64_t)p.max_blocks_per_seq << p.block_shift;
         const int per = (p.num_seqs + kTeamThreads - 1) / kTeamThreads;
-        const int first = tid * per;
+        const int first = min(tid * per, p.num_seqs), end = min(first + per, p.num_seqs);
         int64_t mine = 0;
-        bool bad = false;
-        for (int i = 0; i < per; ++i) {
-            const int s = first + i;
-            if (s >= p.num_seqs) break;
-            int len = __ldg(p.context_lens + s);
-            bad |= len < 0 || len > reach;
-            len = len < 0 ? 0 : len > reach ? (int)reach : len;
-            lens[s] = len;
-            mine += team_steps(team_rows(len, p.block_shift, p.selected ? p.max_selected : -1), C::kRows);
-        }
-        if (bad && blockIdx.x == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
+        for (int s = first; s < end; ++s) mine += steps_of(s);
         int64_t sum = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -353,23 +336,26 @@ __global__ void __launch_bounds__(kTeamThreads, 1) team_kernel(const __grid_cons
         __syncthreads();
         int64_t at = sum - mine;
         for (int w = 0; w < warp; ++w) at += warp_sum[w];
-        for (int i = 0; i < per; ++i) {
-            const int s = first + i;
-            if (s >= p.num_seqs) break;
+        for (int s = first; s < end; ++s) {
             cum[s] = at;
-            at += team_steps(team_rows(lens[s], p.block_shift, p.selected ? p.max_selected : -1), C::kRows);
+            at += steps_of(s);
         }
         if (tid == kTeamThreads - 1) cum[p.num_seqs] = at;
         __syncthreads();
     }
     const int64_t T = cum[p.num_seqs] * heads;
     const int64_t ctas = team_ctas(T, gridDim.x, kTeamLeast);
-    if (tid < 2) share[tid] = (int64_t)blockIdx.x + tid <= ctas ? team_start(cum, p.num_seqs, heads, blockIdx.x + tid, ctas, kTeamSnap) : T;
-    // Rows of sequences without a position.
-    for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x)
-        if (cum[s + 1] == cum[s])
+    if (tid < 2)
+        share[tid] = (int64_t)blockIdx.x + tid <= ctas
+                         ? team_start(cum, p.num_seqs, heads, blockIdx.x + tid, ctas, kTeamSnap)
+                         : T;
+    for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
+        const int len = __ldg(p.context_lens + s);
+        if ((len < 0 || len > reach) && tid == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
+        if (cum[s + 1] == cum[s])  // no position: zeros
             for (int i = tid; i < p.num_heads * D / 8; i += kTeamThreads)
                 reinterpret_cast<uint4 *>(p.out + (int64_t)s * p.num_heads * D)[i] = make_uint4(0, 0, 0, 0);
+    }
     __syncthreads();
     const int64_t a = share[0], b = share[1];
     int2 cut = make_int2(-1, -1);
@@ -377,101 +363,141 @@ __global__ void __launch_bounds__(kTeamThreads, 1) team_kernel(const __grid_cons
     // ---- the ring ----
     const uint32_t ring = smem_addr(smem) + warp * C::kStages * 2 * C::kTileBytes;
     float4 *meta = reinterpret_cast<float4 *>(smem + C::kMeta) + warp * C::kStages * C::kGroups;
-    TeamCursor ahead;  // the next step to issue
-    ahead.begin(cum, p.num_seqs, heads, a + warp, b);
-    // lane j < kGroups: physical block and live rows of group j of that step
-    int phys = 0, rows = 0;
-    auto look_up = [&]() {
-        rows = 0;
-        if (lane < C::kGroups && ahead.g < b) {
-            const int64_t v = ahead.c * C::kRows + lane * 8;  // row of the segment
-            int64_t block = v >> p.block_shift;
-            const int len = lens[ahead.s];
-            bool bad = false, there = true;
-            if (p.selected) {
-                const int64_t seg = (int64_t)ahead.s * heads + ahead.kvh;
-                const int blocks = (len + bs - 1) >> p.block_shift;
-                const int most = min(blocks, p.max_selected);
-                int count = __ldg(p.num_selected + seg);
-                bad = (count < 0 || count > most) && ahead.c == 0 && lane == 0;
-                count = min(count, most);
-                there = block < count;
-                if (there) {
-                    block = __ldg(p.selected + seg * p.max_selected + block);
-                    if (block < 0 || block >= blocks) bad = true, there = false;
-                }
-            }
+    // a step's rows lie in `entries` blocks, 2^span_shift rows in each
+    const int span_shift = min(p.block_shift, C::kRows == 32 ? 5 : 4);
+    const int entries = C::kRows >> span_shift;
+    const int room = 32 / entries;  // steps of a batch
+    // The entries of the batch that begins at (s, kvh, c).
+    auto look_up = [&](TeamBatch &x) {
+        x.rows = x.phys = 0;
+        const int64_t left = (b - x.g + kTeamWarps - 1) / kTeamWarps;  // this warp's steps to the share's end
+        x.count = (int)min(left, (int64_t)min(room, (x.n - x.c + kTeamWarps - 1) / kTeamWarps));
+        if (lane >= x.count * entries) return;
+        const int64_t v = (int64_t)(x.c + lane / entries * kTeamWarps) * C::kRows + (lane % entries << span_shift);
+        int64_t block = v >> p.block_shift;
+        const int len = context(x.s);
+        bool bad = false, there = true;
+        if (p.selected) {
+            const int64_t seg = (int64_t)x.s * heads + x.kvh;
+            const int blocks = (len + bs - 1) >> p.block_shift;
+            const int most = min(blocks, p.max_selected);
+            int count = __ldg(p.num_selected + seg);
+            bad = (count < 0 || count > most) && v == 0;
+            count = min(count, most);
+            there = block < count;
             if (there) {
-                const int64_t pos = (block << p.block_shift) + (v & (bs - 1));
-                rows = (int)max((int64_t)0, min((int64_t)8, len - pos));
-                if (rows > 0) {
-                    phys = __ldg(p.block_tables + (int64_t)ahead.s * p.max_blocks_per_seq + block);
-                    if (phys < 0 || phys >= p.num_blocks) bad = true, phys = 0;
-                }
+                block = __ldg(p.selected + seg * p.max_selected + block);
+                if (block < 0 || block >= blocks) bad = true, there = false;
             }
-            if (bad) report(p.status, PKV_ERR_OUT_OF_RANGE);
         }
+        if (there) {
+            const int64_t pos = (block << p.block_shift) + (v & (bs - 1));
+            x.rows = (int)max((int64_t)0, min((int64_t)1 << span_shift, len - pos));
+            if (x.rows > 0) x.phys = __ldg(p.block_tables + (int64_t)x.s * p.max_blocks_per_seq + block);
+        }
+        if (bad) report(p.status, PKV_ERR_OUT_OF_RANGE);
     };
-    auto issue = [&](int stage) {
-        if (ahead.g < b) {
-            const uint32_t kt = ring + stage * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
-            const int off0 = (int)(ahead.c * C::kRows) & (bs - 1);
-#pragma unroll
-            for (int i = 0; i < C::kCopies; ++i) {
-                const int idx = i * 32 + lane, r = idx / C::kUnits, u = idx % C::kUnits;
-                const int block = __shfl_sync(kFullMask, phys, r >> 3);
-                const bool live = (r & 7) < __shfl_sync(kFullMask, rows, r >> 3);
-                const int64_t at = ((((int64_t)block * heads + ahead.kvh) << p.block_shift) + ((off0 + r) & (bs - 1))) *
-                                       C::kRowBytes + u * 16;
-                const int64_t from = live ? at : 0;
-                cp_async_16_or_zero(kt + team_swizzle<C::kRowBytes>(r, u),
-                                    static_cast<const unsigned char *>(p.key_cache) + from, live);
-                cp_async_16_or_zero(vt + team_swizzle<C::kRowBytes>(r, u),
-                                    static_cast<const unsigned char *>(p.value_cache) + from, live);
+    // The batch after x.
+    auto follow = [&](const TeamBatch &x, TeamBatch &y) {
+        y = x;
+        y.g += (int64_t)x.count * kTeamWarps;
+        y.count = 0;
+        if (y.g >= b) return;
+        y.c += x.count * kTeamWarps;
+#pragma unroll 1
+        while (y.c >= y.n) {  // there is a later segment: y.g is before the end
+            y.c -= y.n;
+            if (++y.kvh == heads) {
+                y.kvh = 0;
+                do ++y.s; while (cum[y.s + 1] == cum[y.s]);
+                y.n = (int)(cum[y.s + 1] - cum[y.s]);
             }
-            if (lane < C::kGroups) {
-                float4 *m = meta + stage * C::kGroups + lane;
-                m->z = __int_as_float(rows);
-                if (!C::kWide) {
-                    const int64_t at = rows > 0 ? (int64_t)phys * p.scale_stride + ahead.kvh : 0;
-                    cp_async_4_or_zero(smem_addr(&m->x), p.key_scale + at, rows > 0);
-                    cp_async_4_or_zero(smem_addr(&m->y), p.value_scale + at, rows > 0);
+        }
+        look_up(y);
+    };
+    TeamBatch now, then;
+    now.count = then.count = 0;
+    int k = 0;  // the next step to issue in `now`
+    now.g = a + warp;
+    if (now.g < b) {
+        const TeamPos at = team_locate(cum, p.num_seqs, heads, now.g);
+        now.s = at.s, now.kvh = at.kvh, now.c = (int)at.c, now.n = (int)at.n;
+        look_up(now);
+        follow(now, then);
+    }
+    const unsigned char *kc = static_cast<const unsigned char *>(p.key_cache) + lane * 16;
+    const unsigned char *vc = static_cast<const unsigned char *>(p.value_cache) + lane * 16;
+    auto issue = [&](int stage) {
+        if (now.count > 0) {
+            const uint32_t kt = ring + stage * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
+            if (k == 0 && now.rows > 0 && (now.phys < 0 || now.phys >= p.num_blocks)) {
+                report(p.status, PKV_ERR_OUT_OF_RANGE);
+                now.phys = 0;
+            }
+            const int off0 = (now.c + k * kTeamWarps) * C::kRows & (bs - 1);
+#pragma unroll
+            for (int j = 0; j < C::kGroups; ++j) {
+                const int entry = k * entries + (j * 8 >> span_shift), in = j * 8 & ((1 << span_shift) - 1);
+                const int block = __shfl_sync(kFullMask, now.phys, entry);
+                const int rows = __shfl_sync(kFullMask, now.rows, entry) - in;
+                const int64_t at = ((((int64_t)block * heads + now.kvh) << p.block_shift) + (off0 & ~((1 << span_shift) - 1)) + in) *
+                                   C::kRowBytes;
+#pragma unroll
+                for (int i = 0; i < C::kGroupCopies; ++i) {
+                    const int idx = i * 32 + lane, r = idx / C::kUnits, u = idx % C::kUnits;
+                    const uint32_t to = team_swizzle<C::kRowBytes>(j * 8 + r, u);
+                    cp_async_16_or_zero(kt + to, kc + at + i * 512, r < rows);
+                    cp_async_16_or_zero(vt + to, vc + at + i * 512, r < rows);
+                }
+                if (lane == j) {
+                    float4 *m = meta + stage * C::kGroups + j;
+                    m->z = __int_as_float(rows);
+                    if (!C::kWide) {
+                        const int64_t of = (int64_t)block * p.scale_stride + now.kvh;
+                        cp_async_4_or_zero(smem_addr(&m->x), p.key_scale + of, rows > 0);
+                        cp_async_4_or_zero(smem_addr(&m->y), p.value_scale + of, rows > 0);
+                    }
                 }
             }
-            ahead.next(cum, heads, b);
-            look_up();
+            if (++k == now.count) {
+                k = 0;
+                now = then;
+                if (now.count > 0) follow(now, then);
+            }
         }
         cp_async_commit();
     };
-    look_up();
     for (int i = 0; i < C::kStages; ++i) issue(i);
 
     // ---- pieces ----
     const int g = lane >> 2, t = lane & 3;
     TeamState<D, NT> st;
     uint32_t q[NT][D / 16][2];
+    auto load_q = [&](int s, int kvh) {
+        const __half *rows_q = p.query + ((int64_t)s * p.num_heads + (int64_t)kvh * p.group) * D;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int h = n * 8 + g;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                // fp16: dims 2t, 2t + 1 and 8 further; codes: dims 4t to 4t + 3
+                const __half *src = rows_q + h * D + 16 * i + (C::kWide ? 2 * t : 4 * t);
+                q[n][i][0] = h < p.group ? __ldg(reinterpret_cast<const uint32_t *>(src)) : 0u;
+                q[n][i][1] = h < p.group ? __ldg(reinterpret_cast<const uint32_t *>(src + (C::kWide ? 8 : 2))) : 0u;
+            }
+        }
+    };
     int stage = 0;
     int64_t mine = a + warp;  // this warp's next step
     TeamPos at = {};
-    if (a < b) at = team_locate(cum, p.num_seqs, heads, a);
+    if (a < b) {
+        at = team_locate(cum, p.num_seqs, heads, a);
+        load_q(at.s, at.kvh);
+    }
     for (int64_t begin = a; begin < b;) {
         const int64_t seg0 = begin - at.c, seg1 = seg0 + at.n;
         const int64_t end = seg1 < b ? seg1 : b;
         const bool whole = seg0 >= a && seg1 <= b;
-        const __half *rows_q = p.query + ((int64_t)at.s * p.num_heads + (int64_t)at.kvh * p.group) * D;
-        if (mine < end) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int h = n * 8 + g;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    // fp16: dims 2t, 2t + 1 and 8 further; codes: dims 4t to 4t + 3
-                    const __half *src = rows_q + h * D + 16 * k + (C::kWide ? 2 * t : 4 * t);
-                    q[n][k][0] = h < p.group ? __ldg(reinterpret_cast<const uint32_t *>(src)) : 0u;
-                    q[n][k][1] = h < p.group ? __ldg(reinterpret_cast<const uint32_t *>(src + (C::kWide ? 8 : 2))) : 0u;
-                }
-            }
-        }
         st.clear();
         for (; mine < end; mine += kTeamWarps) {
             cp_async_wait<C::kStages - 1>();
@@ -482,10 +508,20 @@ __global__ void __launch_bounds__(kTeamThreads, 1) team_kernel(const __grid_cons
             issue(stage);
             if (++stage == C::kStages) stage = 0;
         }
+        const TeamPos here = at;
+        at.c = 0;
+        if (end < b) {  // the next piece's queries come while this one's outputs meet
+            if (++at.kvh == heads) {
+                at.kvh = 0;
+                do ++at.s; while (cum[at.s + 1] == cum[at.s]);
+                at.n = cum[at.s + 1] - cum[at.s];
+            }
+            load_q(at.s, at.kvh);
+        }
 
         // ---- the warps' outputs, eight heads at a time ----
         const int slot = seg0 < a ? 0 : 1;
-        if (!whole) (slot ? cut.y : cut.x) = (int)((int64_t)at.s * heads + at.kvh);
+        if (!whole) (slot ? cut.y : cut.x) = (int)((int64_t)here.s * heads + here.kvh);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int live = min(8, p.group - n * 8);
@@ -498,7 +534,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) team_kernel(const __grid_cons
                 const int h = 2 * t + e;
                 if (h < live) {
                     if (g == 0) ml[warp * 8 + h] = make_float2(st.m[n][e], l);
-                    float *dst = red + (warp * 8 + h) * C::kPitch;
+                    float *dst = red + (warp * red_heads + h) * C::kPitch;
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
                         dst[team_dim<KIND>(i, g, 0)] = st.o[n][i][e];
@@ -518,7 +554,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) team_kernel(const __grid_cons
                 for (int w = 0; w < kTeamWarps; ++w) {
                     const float2 x = ml[w * 8 + h];
                     const float f = team_exp2(x.x - ref);
-                    const float2 y = *reinterpret_cast<const float2 *>(red + (w * 8 + h) * C::kPitch + d);
+                    const float2 y = *reinterpret_cast<const float2 *>(red + (w * red_heads + h) * C::kPitch + d);
                     l = fmaf(x.y, f, l);
                     o.x = fmaf(y.x, f, o.x);
                     o.y = fmaf(y.y, f, o.y);
@@ -526,7 +562,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) team_kernel(const __grid_cons
                 const int head = n * 8 + h;
                 if (whole) {
                     const float inv = l == 0.f ? 0.f : 1.f / l;  // no row: zeros
-                    const int64_t row = (int64_t)at.s * p.num_heads + (int64_t)at.kvh * p.group + head;
+                    const int64_t row = (int64_t)here.s * p.num_heads + (int64_t)here.kvh * p.group + head;
                     *reinterpret_cast<__half2 *>(p.out + row * D + d) = __floats2half2_rn(o.x * inv, o.y * inv);
                 } else {
                     const int64_t part = ((int64_t)blockIdx.x * 2 + slot) * p.group + head;
@@ -537,12 +573,6 @@ __global__ void __launch_bounds__(kTeamThreads, 1) team_kernel(const __grid_cons
             __syncthreads();
         }
         begin = end;
-        at.c = 0;
-        if (begin < b && ++at.kvh == heads) {
-            at.kvh = 0;
-            do ++at.s; while (cum[at.s + 1] == cum[at.s]);
-            at.n = cum[at.s + 1] - cum[at.s];
-        }
     }
     if (tid == 0) p.cut[blockIdx.x] = cut;
 }
@@ -603,15 +633,19 @@ __global__ void __launch_bounds__(kTeamJoinThreads) team_join_kernel(const __gri
     }
 }
 
+template <int KIND, int D, int NT>
+TeamKernel team_kernel_info_of(int group) {
+    using C = TeamConfig<KIND, D, NT>;
+    TeamKernel k;
+    k.fn = reinterpret_cast<const void *>(&team_kernel<KIND, D, NT>);
+    k.smem_fixed = C::kRed + (size_t)kTeamWarps * (group < 8 ? group : 8) * C::kPitch * 4 + 8;
+    k.ctas_per_sm = C::kCtas;
+    return k;
+}
+
 template <int KIND, int D>
 TeamKernel team_kernel_info(int group) {
-    using C = TeamConfig<KIND, D>;
-    TeamKernel k;
-    k.fn = group <= 8 ? reinterpret_cast<const void *>(&team_kernel<KIND, D, 1>)
-                      : reinterpret_cast<const void *>(&team_kernel<KIND, D, 2>);
-    k.smem_fixed = C::kFixed;
-    k.step_rows = C::kRows;
-    return k;
+    return group <= 8 ? team_kernel_info_of<KIND, D, 1>(group) : team_kernel_info_of<KIND, D, 2>(group);
 }
 
 }  // namespace pkv

@@ -55,8 +55,8 @@ struct TeamWorkspace {
 // One compiled kernel.
 struct TeamKernel {
     const void *fn;
-    size_t smem_fixed;    // dynamic shared memory without the per-sequence arrays (12 bytes each)
-    int step_rows;
+    size_t smem_fixed;    // dynamic shared memory without the prefix sums (8 bytes per sequence)
+    int ctas_per_sm;
 };
 
 // pkv_team_{f16,int8,e4m3}.cu; head_dim 64 or 128, group 1 to 16.
