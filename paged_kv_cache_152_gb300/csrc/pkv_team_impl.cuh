@@ -63,10 +63,6 @@ struct TeamConfig {
     static constexpr size_t kRed = kMl + (size_t)kTeamWarps * 8 * 8;
 };
 
-// Steps that a CTA boundary moves at most to spare a cut, and the least a CTA takes.
-constexpr int kTeamSnap = 8;
-constexpr int kTeamLeast = 8;
-
 // Byte of 16-byte unit u of row r in a tile whose rows are RB bytes: eight
 // consecutive rows' unit u lie in eight different 16-byte columns of the banks.
 template <int RB>
@@ -76,18 +72,15 @@ __device__ __forceinline__ int team_swizzle(int r, int u) {
 }
 
 // Four codes in a register -> the fp16 pairs (b0, b1), (b2, b3), or with PAIRED
-// (b0, b2), (b1, b3).  int8: u = code + 128 in the low bits of 1024 + u.
+// (b0, b2), (b1, b3).  An int8 code comes as (code + 128) 2^-24: the byte code ^
+// 0x80 in the low bits of an fp16 below the normal range, which the products take
+// as it is; kTeamBias is what they have too much, kTeamUnit what undoes the 2^-24.
 template <int KIND, bool PAIRED>
 __device__ __forceinline__ void team_widen(uint32_t codes, uint32_t &lo, uint32_t &hi) {
     if (KIND == kTeamInt8) {
         const uint32_t u = codes ^ 0x80808080u;
-        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
-        const uint32_t a = __byte_perm(u, 0x64646464u, PAIRED ? 0x4240 : 0x4140);
-        const uint32_t b = __byte_perm(u, 0x64646464u, PAIRED ? 0x4341 : 0x4342);
-        const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
-        const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
-        lo = *reinterpret_cast<const uint32_t *>(&x);
-        hi = *reinterpret_cast<const uint32_t *>(&y);
+        lo = __byte_perm(u, 0, PAIRED ? 0x4240 : 0x4140);
+        hi = __byte_perm(u, 0, PAIRED ? 0x4341 : 0x4342);
     } else {
         const uint32_t c = PAIRED ? __byte_perm(codes, 0, 0x3120) : codes;
         asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
@@ -96,6 +89,9 @@ __device__ __forceinline__ void team_widen(uint32_t codes, uint32_t &lo, uint32_
             : "r"(c));
     }
 }
+constexpr uint32_t kTeamBias = 0x00800080u;  // two fp16 values 128 2^-24
+template <int KIND>
+__device__ __forceinline__ constexpr float team_unit() { return KIND == kTeamInt8 ? 16777216.f : 1.f; }
 
 __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -131,11 +127,13 @@ template <int D, int NT>
 struct TeamState {
     float m[NT][2], l[NT][2];
     float o[NT][D / 16][4];
+    float z[NT][4];  // int8: the biases' share of the output, the same for every dim
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             m[n][0] = m[n][1] = -CUDART_INF_F;
             l[n][0] = l[n][1] = 0.f;
+            z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
         }
@@ -152,8 +150,8 @@ __device__ __forceinline__ int team_dim(int i, int g, int second) {
 // scale, live rows).
 template <int KIND, int D, int NT>
 __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt, const float4 *meta,
-                                          const uint32_t (&q)[NT][D / 16][2], float scale_log2, TeamState<D, NT> &st,
-                                          int lane) {
+                                          const uint32_t (&q)[NT][D / 16][2], const float (&bias)[NT][2],
+                                          float scale_log2, TeamState<D, NT> &st, int lane) {
     using C = TeamConfig<KIND, D, NT>;
     constexpr int RB = C::kRowBytes;
     const int g = lane >> 2;
@@ -163,7 +161,9 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt, const float4
 #pragma unroll
     for (int r = 0; r < C::kTiles; ++r)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) s[r][n][0] = s[r][n][1] = s[r][n][2] = s[r][n][3] = 0.f;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[r][n][e] = KIND == kTeamInt8 ? -bias[n][e & 1] : 0.f;
 #pragma unroll
     for (int u = 0; u < C::kUnits; u += 2)
 #pragma unroll
@@ -198,7 +198,7 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt, const float4
             const int j = 2 * r + h;
             const float4 info = meta[j];
             const bool live = g < __float_as_int(info.z);
-            const float f = C::kWide ? scale_log2 : scale_log2 * info.x;
+            const float f = C::kWide ? scale_log2 : scale_log2 * team_unit<KIND>() * info.x;
             vs[j] = C::kWide ? 1.f : info.y;
             // the logarithm only places the weights: bounded, so that a scale of zero does not
             lv[j] = C::kWide ? 0.f : fminf(fmaxf(__log2f(info.y), -40.f), 40.f);
@@ -241,6 +241,7 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt, const float4
                 st.o[n][i][2] *= f[0];
                 st.o[n][i][3] *= f[1];
             }
+            if (KIND == kTeamInt8) st.z[n][0] *= f[0], st.z[n][1] *= f[1];
         }
     }
     uint32_t w[C::kGroups][NT];
@@ -260,6 +261,13 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt, const float4
             }
     }
 
+    if (KIND == kTeamInt8) {
+#pragma unroll
+        for (int r = 0; r < C::kTiles; ++r)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                mma_16816(st.z[n], kTeamBias, kTeamBias, kTeamBias, kTeamBias, w[2 * r][n], w[2 * r + 1][n]);
+    }
 #pragma unroll
     for (int r = 0; r < C::kTiles; ++r)
 #pragma unroll
@@ -284,13 +292,12 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt, const float4
         }
 }
 
-// Up to 32 steps of a warp (every kTeamWarps-th of the CTA's share) in one
-// segment: lane j looks up the block table's entry j of theirs, all at once and a
-// batch ahead of their use.
+// Up to 32 steps of a warp (every kTeamWarps-th of a piece's) in one segment: lane
+// j looks up the block table's entry j of theirs, all at once and a batch ahead of
+// their use.
 struct TeamBatch {
-    int64_t g;      // the first step
-    int s, kvh;     // its segment
-    int c, n;       // the step in the segment, the segment's steps
+    int seg, s;     // the segment and its sequence
+    int c, end;     // the first step, the end of the piece
     int count;      // steps of the batch, 0: none
     int phys;       // lane j: physical block of entry j
     int rows;       //         and its rows in use
@@ -305,7 +312,8 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
     const int red_heads = min(8, p.group);
     float *red = reinterpret_cast<float *>(smem + C::kRed);
     int64_t *cum = reinterpret_cast<int64_t *>(red + kTeamWarps * red_heads * C::kPitch);
-    __shared__ int64_t warp_sum[kTeamWarps], share[2];
+    __shared__ int64_t warp_sum[kTeamWarps];
+    __shared__ TeamPlace share[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int heads = p.num_kv_heads, bs = 1 << p.block_shift;
     const int64_t reach = (int64_t)p.max_blocks_per_seq << p.block_shift;
@@ -325,7 +333,7 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
         const int per = (p.num_seqs + kTeamThreads - 1) / kTeamThreads;
         const int first = min(tid * per, p.num_seqs), end = min(first + per, p.num_seqs);
         int64_t mine = 0;
-        for (int s = first; s < end; ++s) mine += steps_of(s);
+        for (int s = first; s < end; ++s) mine += team_units(steps_of(s));
         int64_t sum = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -338,17 +346,14 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
         for (int w = 0; w < warp; ++w) at += warp_sum[w];
         for (int s = first; s < end; ++s) {
             cum[s] = at;
-            at += steps_of(s);
+            at += team_units(steps_of(s));
         }
         if (tid == kTeamThreads - 1) cum[p.num_seqs] = at;
         __syncthreads();
     }
     const int64_t T = cum[p.num_seqs] * heads;
-    const int64_t ctas = team_ctas(T, gridDim.x, kTeamLeast);
-    if (tid < 2)
-        share[tid] = (int64_t)blockIdx.x + tid <= ctas
-                         ? team_start(cum, p.num_seqs, heads, blockIdx.x + tid, ctas, kTeamSnap)
-                         : T;
+    const int64_t ctas = team_ctas(T, gridDim.x);
+    if (tid < 2) share[tid] = team_start(cum, p.num_seqs, heads, min((int64_t)blockIdx.x + tid, ctas), ctas);
     for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
         const int len = __ldg(p.context_lens + s);
         if ((len < 0 || len > reach) && tid == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
@@ -357,7 +362,11 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
                 reinterpret_cast<uint4 *>(p.out + (int64_t)s * p.num_heads * D)[i] = make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
-    const int64_t a = share[0], b = share[1];
+    // The share: segments from.seg, from step from.step on, to to.seg, before to.step.
+    const TeamPlace from = share[0], to = share[1];
+    auto more = [&](int seg) { return seg < to.seg || (seg == to.seg && to.step > 0); };
+    auto piece_end = [&](int seg, int s) { return seg < to.seg ? team_steps_of(cum, s) : to.step; };
+    const bool any = more(from.seg) && !(from.seg == to.seg && from.step >= to.step);
     int2 cut = make_int2(-1, -1);
 
     // ---- the ring ----
@@ -367,18 +376,17 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
     const int span_shift = min(p.block_shift, C::kRows == 32 ? 5 : 4);
     const int entries = C::kRows >> span_shift;
     const int room = 32 / entries;  // steps of a batch
-    // The entries of the batch that begins at (s, kvh, c).
+    // The entries of the batch that begins at step c of the piece.
     auto look_up = [&](TeamBatch &x) {
         x.rows = x.phys = 0;
-        const int64_t left = (b - x.g + kTeamWarps - 1) / kTeamWarps;  // this warp's steps to the share's end
-        x.count = (int)min(left, (int64_t)min(room, (x.n - x.c + kTeamWarps - 1) / kTeamWarps));
+        x.count = min(room, (x.end - x.c + kTeamWarps - 1) / kTeamWarps);
         if (lane >= x.count * entries) return;
         const int64_t v = (int64_t)(x.c + lane / entries * kTeamWarps) * C::kRows + (lane % entries << span_shift);
         int64_t block = v >> p.block_shift;
         const int len = context(x.s);
         bool bad = false, there = true;
         if (p.selected) {
-            const int64_t seg = (int64_t)x.s * heads + x.kvh;
+            const int64_t seg = x.seg;
             const int blocks = (len + bs - 1) >> p.block_shift;
             const int most = min(blocks, p.max_selected);
             int count = __ldg(p.num_selected + seg);
@@ -397,33 +405,28 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
         }
         if (bad) report(p.status, PKV_ERR_OUT_OF_RANGE);
     };
-    // The batch after x.
+    // The next batch: the piece's, or the next piece's in which this warp has a step.
     auto follow = [&](const TeamBatch &x, TeamBatch &y) {
         y = x;
-        y.g += (int64_t)x.count * kTeamWarps;
-        y.count = 0;
-        if (y.g >= b) return;
         y.c += x.count * kTeamWarps;
+        y.count = 0;
 #pragma unroll 1
-        while (y.c >= y.n) {  // there is a later segment: y.g is before the end
-            y.c -= y.n;
-            if (++y.kvh == heads) {
-                y.kvh = 0;
-                do ++y.s; while (cum[y.s + 1] == cum[y.s]);
-                y.n = (int)(cum[y.s + 1] - cum[y.s]);
-            }
+        while (y.c >= y.end) {
+            y.seg = team_next(cum, p.num_seqs, heads, y.seg, y.s);
+            if (!more(y.seg)) return;
+            y.c = warp;
+            y.end = piece_end(y.seg, y.s);
         }
         look_up(y);
     };
     TeamBatch now, then;
     now.count = then.count = 0;
     int k = 0;  // the next step to issue in `now`
-    now.g = a + warp;
-    if (now.g < b) {
-        const TeamPos at = team_locate(cum, p.num_seqs, heads, now.g);
-        now.s = at.s, now.kvh = at.kvh, now.c = (int)at.c, now.n = (int)at.n;
-        look_up(now);
-        follow(now, then);
+    const int first_s = any ? from.seg / heads : 0;
+    if (any) {
+        then.seg = from.seg, then.s = first_s, then.c = from.step + warp, then.end = piece_end(from.seg, first_s);
+        follow(then, now);
+        if (now.count > 0) follow(now, then);
     }
     const unsigned char *kc = static_cast<const unsigned char *>(p.key_cache) + lane * 16;
     const unsigned char *vc = static_cast<const unsigned char *>(p.value_cache) + lane * 16;
@@ -435,12 +438,13 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
                 now.phys = 0;
             }
             const int off0 = (now.c + k * kTeamWarps) * C::kRows & (bs - 1);
+            const int kvh = now.seg - now.s * heads;
 #pragma unroll
             for (int j = 0; j < C::kGroups; ++j) {
                 const int entry = k * entries + (j * 8 >> span_shift), in = j * 8 & ((1 << span_shift) - 1);
                 const int block = __shfl_sync(kFullMask, now.phys, entry);
                 const int rows = __shfl_sync(kFullMask, now.rows, entry) - in;
-                const int64_t at = ((((int64_t)block * heads + now.kvh) << p.block_shift) + (off0 & ~((1 << span_shift) - 1)) + in) *
+                const int64_t at = ((((int64_t)block * heads + kvh) << p.block_shift) + (off0 & ~((1 << span_shift) - 1)) + in) *
                                    C::kRowBytes;
 #pragma unroll
                 for (int i = 0; i < C::kGroupCopies; ++i) {
@@ -453,7 +457,7 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
                     float4 *m = meta + stage * C::kGroups + j;
                     m->z = __int_as_float(rows);
                     if (!C::kWide) {
-                        const int64_t of = (int64_t)block * p.scale_stride + now.kvh;
+                        const int64_t of = (int64_t)block * p.scale_stride + kvh;
                         cp_async_4_or_zero(smem_addr(&m->x), p.key_scale + of, rows > 0);
                         cp_async_4_or_zero(smem_addr(&m->y), p.value_scale + of, rows > 0);
                     }
@@ -473,8 +477,9 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
     const int g = lane >> 2, t = lane & 3;
     TeamState<D, NT> st;
     uint32_t q[NT][D / 16][2];
-    auto load_q = [&](int s, int kvh) {
-        const __half *rows_q = p.query + ((int64_t)s * p.num_heads + (int64_t)kvh * p.group) * D;
+    float bias[NT][2];
+    auto load_q = [&](int seg) {
+        const __half *rows_q = p.query + (int64_t)seg * p.group * D;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int h = n * 8 + g;
@@ -488,40 +493,41 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
         }
     };
     int stage = 0;
-    int64_t mine = a + warp;  // this warp's next step
-    TeamPos at = {};
-    if (a < b) {
-        at = team_locate(cum, p.num_seqs, heads, a);
-        load_q(at.s, at.kvh);
-    }
-    for (int64_t begin = a; begin < b;) {
-        const int64_t seg0 = begin - at.c, seg1 = seg0 + at.n;
-        const int64_t end = seg1 < b ? seg1 : b;
-        const bool whole = seg0 >= a && seg1 <= b;
+    int seg = from.seg, s = first_s, lo = from.step;
+    bool on = any;
+    if (on) load_q(seg);
+    while (on) {
+        const int end = piece_end(seg, s), n_steps = team_steps_of(cum, s);
+        if (KIND == kTeamInt8) {  // what the biases add to each head's scores
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    mma_16816(x, kTeamBias, kTeamBias, kTeamBias, kTeamBias, q[n][i][0], q[n][i][1]);
+                bias[n][0] = x[0], bias[n][1] = x[1];
+            }
+        }
         st.clear();
-        for (; mine < end; mine += kTeamWarps) {
+        for (int c = lo + warp; c < end; c += kTeamWarps) {
             cp_async_wait<C::kStages - 1>();
             __syncwarp();
             const uint32_t kt = ring + stage * 2 * C::kTileBytes;
-            team_step<KIND, D, NT>(kt, kt + C::kTileBytes, meta + stage * C::kGroups, q, p.scale_log2, st, lane);
+            team_step<KIND, D, NT>(kt, kt + C::kTileBytes, meta + stage * C::kGroups, q, bias, p.scale_log2, st, lane);
             __syncwarp();
             issue(stage);
             if (++stage == C::kStages) stage = 0;
         }
-        const TeamPos here = at;
-        at.c = 0;
-        if (end < b) {  // the next piece's queries come while this one's outputs meet
-            if (++at.kvh == heads) {
-                at.kvh = 0;
-                do ++at.s; while (cum[at.s + 1] == cum[at.s]);
-                at.n = cum[at.s + 1] - cum[at.s];
-            }
-            load_q(at.s, at.kvh);
-        }
+        const int here = seg;
+        const bool whole = lo == 0 && end == n_steps;
+        const int slot = lo > 0 ? 0 : 1;
+        seg = team_next(cum, p.num_seqs, heads, seg, s);
+        lo = 0;
+        on = more(seg);
+        if (on) load_q(seg);  // the next piece's queries come while this one's outputs meet
 
         // ---- the warps' outputs, eight heads at a time ----
-        const int slot = seg0 < a ? 0 : 1;
-        if (!whole) (slot ? cut.y : cut.x) = (int)((int64_t)here.s * heads + here.kvh);
+        if (!whole) (slot ? cut.y : cut.x) = here;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int live = min(8, p.group - n * 8);
@@ -537,8 +543,9 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
                     float *dst = red + (warp * red_heads + h) * C::kPitch;
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
-                        dst[team_dim<KIND>(i, g, 0)] = st.o[n][i][e];
-                        dst[team_dim<KIND>(i, g, 1)] = st.o[n][i][2 + e];
+                        const float z = KIND == kTeamInt8 ? st.z[n][e] : 0.f;
+                        dst[team_dim<KIND>(i, g, 0)] = (st.o[n][i][e] - z) * team_unit<KIND>();
+                        dst[team_dim<KIND>(i, g, 1)] = (st.o[n][i][2 + e] - z) * team_unit<KIND>();
                     }
                 }
             }
@@ -562,7 +569,7 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
                 const int head = n * 8 + h;
                 if (whole) {
                     const float inv = l == 0.f ? 0.f : 1.f / l;  // no row: zeros
-                    const int64_t row = (int64_t)here.s * p.num_heads + (int64_t)here.kvh * p.group + head;
+                    const int64_t row = (int64_t)here * p.group + head;
                     *reinterpret_cast<__half2 *>(p.out + row * D + d) = __floats2half2_rn(o.x * inv, o.y * inv);
                 } else {
                     const int64_t part = ((int64_t)blockIdx.x * 2 + slot) * p.group + head;
@@ -572,7 +579,6 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
             }
             __syncthreads();
         }
-        begin = end;
     }
     if (tid == 0) p.cut[blockIdx.x] = cut;
 }
@@ -627,8 +633,7 @@ __global__ void __launch_bounds__(kTeamJoinThreads) team_join_kernel(const __gri
             sum = fmaf(ml[w].y, f, sum);
             y = fmaf(out[w][threadIdx.x], f, y);
         }
-        const int s = seg / p.num_kv_heads, kvh = seg % p.num_kv_heads;
-        const int64_t row = (int64_t)s * p.num_heads + (int64_t)kvh * p.group + h;
+        const int64_t row = (int64_t)seg * p.group + h;
         p.out[row * D + threadIdx.x] = __float2half_rn(sum == 0.f ? 0.f : y / sum);
     }
 }

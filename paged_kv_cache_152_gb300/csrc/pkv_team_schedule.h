@@ -3,16 +3,18 @@
 // (tests/cpp/test_team_schedule.cpp) runs the same code.
 //
 // A segment is one (sequence, KV head).  Its rows -- the context's, or with a
-// block list the listed blocks' -- are cut into steps of a few rows; steps are
-// numbered sequence-major, then KV head, then position:
+// block list the listed blocks' -- are cut into steps of a few rows.  A segment
+// of n > 0 steps costs n + kTeamPiece units: what a piece costs besides its steps
+// (queries in, the warps' outputs joined and written) is that of so many steps.
+// Units are numbered sequence-major, then KV head, then position:
 //
-//   g = cum[s] * heads + kvh * n(s) + c,   n(s) = cum[s + 1] - cum[s],
-//   T = cum[N] * heads.
+//   cum[s + 1] = cum[s] + (n(s) > 0 ? n(s) + kTeamPiece : 0),   T = cum[N] * heads,
 //
-// The T steps are divided among C CTAs in order.  CTA c's nominal start c T / C
-// moves to a segment boundary that lies within `snap` steps, so that a short
-// segment is not cut for the sake of a few steps.  A CTA's share is walked by
-// all its warps together, one segment's part (a piece) after the other.
+// and divided among C CTAs in order.  CTA c's nominal start c T / C falls into a
+// segment, and moves to the segment's start or end where that is at most
+// kTeamSnap steps away, so that a short segment is not cut for a few steps.  A
+// CTA's share is walked by all its warps together, one segment's part (a piece)
+// after the other.
 #ifndef PKV_TEAM_SCHEDULE_H
 #define PKV_TEAM_SCHEDULE_H
 
@@ -22,8 +24,15 @@
 
 namespace pkv {
 
+#ifndef PKV_TEAM_PIECE
+#define PKV_TEAM_PIECE 8
+#endif
+constexpr int kTeamPiece = PKV_TEAM_PIECE;
+constexpr int kTeamSnap = 8;
+constexpr int kTeamLeast = 16;  // units that a CTA gets at the least
+
 // Steps of a sequence of `rows` rows.
-PKV_HD int64_t team_steps(int64_t rows, int step_rows) { return rows <= 0 ? 0 : (rows + step_rows - 1) / step_rows; }
+PKV_HD int team_steps(int64_t rows, int step_rows) { return rows <= 0 ? 0 : (int)((rows + step_rows - 1) / step_rows); }
 
 // Rows of a sequence: the context, or at most `listed` blocks of it (a listed
 // block counts as a whole one, the context's last may be anywhere in the list).
@@ -33,51 +42,63 @@ PKV_HD int64_t team_rows(int64_t context, int block_shift, int64_t listed) {
     return (blocks < listed ? blocks : listed) << block_shift;
 }
 
-// CTAs that get a share: each of them at least `least` steps.
-PKV_HD int64_t team_ctas(int64_t T, int64_t grid, int64_t least) {
-    const int64_t c = T / least;
+PKV_HD int64_t team_units(int steps) { return steps > 0 ? (int64_t)steps + kTeamPiece : 0; }
+
+// CTAs that get a share.
+PKV_HD int64_t team_ctas(int64_t T, int64_t grid) {
+    const int64_t c = T / kTeamLeast;
     return c < 1 ? 1 : c < grid ? c : grid;
 }
 
-struct TeamPos {
-    int s;      // sequence
-    int kvh;    // KV head
-    int64_t c;  // step in the segment
-    int64_t n;  // the segment's steps
+// A place between two steps: segment s * heads + kvh, before its step `step`
+// (0 <= step < n); behind the last segment: num_seqs * heads, 0.
+struct TeamPlace {
+    int seg;
+    int step;
 };
 
-// Where step g (0 <= g < T) lies.
-PKV_HD TeamPos team_locate(const int64_t *cum, int num_seqs, int heads, int64_t g) {
-    const int64_t row = div_nonneg(g, heads);  // cum[s] <= row < cum[s + 1]
-    int lo = 0, hi = num_seqs;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cum[mid] <= row) lo = mid; else hi = mid;
-    }
-    TeamPos p;
-    p.s = lo;
-    p.n = cum[lo + 1] - cum[lo];
-    const int64_t off = g - cum[lo] * heads;
-    p.kvh = (int)div_nonneg(off, p.n);
-    p.c = off - p.kvh * p.n;
-    return p;
+// Steps of a segment of sequence s.
+PKV_HD int team_steps_of(const int64_t *cum, int s) {
+    const int64_t units = cum[s + 1] - cum[s];
+    return units > 0 ? (int)(units - kTeamPiece) : 0;
 }
 
-// First step of CTA c's share, 0 <= c <= C.  Never decreasing in c: of two
-// nominal starts between the same two boundaries the later one is nearer to the
-// right and farther from the left.  A share may be empty only where two starts
-// moved to the same boundary, so the CTAs that share a segment are consecutive.
-PKV_HD int64_t team_start(const int64_t *cum, int num_seqs, int heads, int64_t c, int64_t C, int64_t snap) {
+// The next segment with steps, `seg` being in sequence s (s moves along).
+PKV_HD int team_next(const int64_t *cum, int num_seqs, int heads, int seg, int &s) {
+    if (++seg < (s + 1) * heads) return seg;
+    do ++s; while (s < num_seqs && cum[s + 1] == cum[s]);
+    return s * heads;
+}
+
+// Where CTA c's share begins, 0 <= c <= C.  Never decreasing in c: of two nominal
+// starts between the same two boundaries the later one is nearer to the right
+// and farther from the left.  Two starts are equal only at a boundary, so the
+// CTAs that share a segment are consecutive.
+PKV_HD TeamPlace team_start(const int64_t *cum, int num_seqs, int heads, int64_t c, int64_t C) {
     const int64_t T = cum[num_seqs] * heads;
     const int64_t share = div_nonneg(T, C);  // c T / C without a product past 64 bits
     const int64_t at = c * share + div_nonneg(c * (T - share * C), C);
-    if (at <= 0 || at >= T) return at <= 0 ? 0 : T;
-    const TeamPos p = team_locate(cum, num_seqs, heads, at);
-    const int64_t most = div_nonneg(T, 2 * C + 1);
-    if (snap > most) snap = most;
-    const int64_t left = p.c, right = p.n - p.c;
-    if (left <= right) return left <= snap ? at - left : at;
-    return right <= snap ? at + right : at;
+    if (at >= T) return TeamPlace{num_seqs * heads, 0};
+    const int64_t row = div_nonneg(at, heads);  // cum[s] <= row < cum[s + 1]
+    int s = 0, hi = num_seqs;
+    while (hi - s > 1) {
+        const int mid = (s + hi) >> 1;
+        if (cum[mid] <= row) s = mid; else hi = mid;
+    }
+    const int64_t units = cum[s + 1] - cum[s];
+    const int64_t off = at - cum[s] * heads;
+    const int kvh = (int)div_nonneg(off, units);
+    const int n = (int)(units - kTeamPiece);
+    const int64_t unit = off - kvh * units;
+    const int step = unit < kTeamPiece ? 0 : (int)(unit - kTeamPiece);
+    TeamPlace p = {s * heads + kvh, step};
+    if (step <= n - step) {
+        if (step <= kTeamSnap) p.step = 0;
+    } else if (n - step <= kTeamSnap) {
+        p.seg = team_next(cum, num_seqs, heads, p.seg, s);
+        p.step = 0;
+    }
+    return p;
 }
 
 }  // namespace pkv
