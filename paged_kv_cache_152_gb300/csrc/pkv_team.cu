@@ -4,6 +4,8 @@
 
 #include <math.h>
 
+#include <algorithm>
+
 #include "../../include/pkv.h"
 #include "pkv_host.h"
 #include "pkv_launch.h"
@@ -21,8 +23,8 @@ bool shape_ok(int num_heads, int num_kv_heads, int head_dim) {
            num_heads / num_kv_heads <= kTeamMaxGroup && (head_dim == 64 || head_dim == 128);
 }
 
-// Shared memory that two CTAs of an SM can have each (the SM's 228 KB less 1 KB each).
-constexpr size_t kSmemOfTwo = 113 * 1024 - 256;
+// Shared memory of an SM, and what a CTA takes of it besides its dynamic part.
+constexpr size_t kSmemOfSm = 228 * 1024, kSmemOfCta = 1024 + 256;
 
 int multiprocessors(int *n) {
     int dev = 0;
@@ -65,7 +67,7 @@ int decode(void *out, const void *query, const void *key_cache, const void *valu
     const size_t smem = k.smem_fixed + 8 * (size_t)num_seqs;
     if (num_ctas == 0) {
         if (multiprocessors(&num_ctas) != PKV_OK) return PKV_ERR_CUDA;
-        if (k.ctas_per_sm == 2 && smem <= kSmemOfTwo) num_ctas *= 2;
+        num_ctas *= std::max(1, std::min(k.ctas_per_sm, (int)(kSmemOfSm / (smem + kSmemOfCta))));
     }
     const TeamWorkspace ws = TeamWorkspace::plan(num_ctas, group, head_dim);
     if (workspace_bytes < ws.total) return PKV_ERR_INVALID_ARG;
@@ -124,7 +126,7 @@ extern "C" size_t pkv_decode_team_workspace_size(int num_heads, int num_kv_heads
     if (num_ctas < 0 || num_ctas > kMaxCtas || !shape_ok(num_heads, num_kv_heads, head_dim)) return 0;
     if (num_ctas == 0) {
         if (multiprocessors(&num_ctas) != PKV_OK) return 0;
-        num_ctas *= 2;  // the most that the default is
+        num_ctas *= 4;  // the most that the default is
     }
     return TeamWorkspace::plan(num_ctas, num_heads / num_kv_heads, head_dim).total;
 }

@@ -14,7 +14,7 @@
 // Bound by HBM: a row is read once for all query heads of its group.  8-bit rows
 // halve the bytes, so the work per byte doubles: the split and the layout are
 // chosen for few instructions per row.
-//  * All 8 warps of a CTA work on one segment's piece, each on every eighth
+//  * The 4 warps of a CTA work on one segment's piece, each on every fourth
 //    step of 16 or 32 rows, with a ring of its own (cp.async, two to four steps
 //    in flight, 128 KB per SM) that runs on into the next pieces; the warps meet
 //    once per piece, in shared memory.
@@ -43,6 +43,14 @@ namespace pkv {
 
 enum TeamKind { kTeamF16, kTeamInt8, kTeamE4m3 };
 
+// What goes with a step's tiles: the key and value scales of its groups, and the
+// groups' rows in use.
+template <int GROUPS>
+struct alignas(16) TeamMeta {
+    float2 scale[GROUPS];
+    int rows[GROUPS];
+};
+
 template <int KIND, int D, int NT>
 struct TeamConfig {
     static constexpr bool kWide = KIND == kTeamF16;
@@ -52,15 +60,15 @@ struct TeamConfig {
     static constexpr int kGroups = kRows / 8;                // a group of 8 rows lies in one block
     static constexpr int kUnits = kRowBytes / 16;            // 16-byte units of a row
     static constexpr int kTileBytes = kRows * kRowBytes;
-    static constexpr int kCtas = NT == 1 && kTileBytes <= 2048 ? 2 : 1;  // per SM
-    static constexpr int kStages = 16384 / kCtas / (2 * kTileBytes);     // 128 KB per SM in flight
+    static constexpr int kCtas = (NT == 1 && kTileBytes <= 2048 ? 16 : 8) / kTeamWarps;     // per SM
+    static constexpr int kStages = 131072 / (kCtas * kTeamWarps) / (2 * kTileBytes);  // 128 KB per SM in flight
     static constexpr int kGroupCopies = kUnits / 4;          // of a lane, per cache and group
     static constexpr int kPitch = D + 8;                     // floats between heads of a warp's output
-    // [warps][stages][K, V tiles] [warps][stages][groups] float4 (scales, rows)
-    // [warps][8 heads] (maximum, sum), then by sequence: cum, then [warps][heads][pitch] floats
+    // [warps][stages][K, V tiles] [warps][stages] TeamMeta
+    // [warps][8 heads] (maximum, sum, bias), [warps][heads][pitch] floats, then by sequence: cum
     static constexpr size_t kMeta = (size_t)kTeamWarps * kStages * 2 * kTileBytes;
-    static constexpr size_t kMl = kMeta + (size_t)kTeamWarps * kStages * kGroups * 16;
-    static constexpr size_t kRed = kMl + (size_t)kTeamWarps * 8 * 8;
+    static constexpr size_t kMl = kMeta + (size_t)kTeamWarps * kStages * sizeof(TeamMeta<kGroups>);
+    static constexpr size_t kRed = kMl + (size_t)kTeamWarps * 8 * 16;
 };
 
 // Byte of 16-byte unit u of row r in a tile whose rows are RB bytes: eight
@@ -95,6 +103,9 @@ __device__ __forceinline__ constexpr float team_unit() { return KIND == kTeamInt
 
 __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_16_of(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_4_or_zero(uint32_t dst, const void *src, bool live) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
@@ -140,22 +151,21 @@ struct TeamState {
     }
 };
 
-// The dim of o[i][2 * second + ...] of lane row g.
-template <int KIND>
-__device__ __forceinline__ int team_dim(int i, int g, int second) {
-    return KIND == kTeamF16 ? 16 * i + g + 8 * second : 16 * i + 2 * g + second;
-}
-
-// One step: tiles at kt, vt (shared addresses), meta[group] = (key scale, value
-// scale, live rows).
+// One step: tiles at kt, vt (shared addresses).
 template <int KIND, int D, int NT>
-__device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt, const float4 *meta,
+__device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt,
+                                          const TeamMeta<TeamConfig<KIND, D, NT>::kGroups> &meta,
                                           const uint32_t (&q)[NT][D / 16][2], const float (&bias)[NT][2],
-                                          float scale_log2, TeamState<D, NT> &st, int lane) {
+                                          float scale_log2, int group, TeamState<D, NT> &st, int lane) {
     using C = TeamConfig<KIND, D, NT>;
     constexpr int RB = C::kRowBytes;
     const int g = lane >> 2;
-    const int row16 = (lane & 7) + ((lane >> 3) & 1) * 8, second = lane >> 4;  // ldmatrix: this lane's row and unit
+    // ldmatrix: this lane's row and which of two units; a pair's two lie 16 bytes
+    // apart but for the swizzle, so unit u's place is unit 0's with u's bits flipped
+    const int row16 = (lane & 7) + ((lane >> 3) & 1) * 8;
+    uint32_t place[C::kUnits / 2];
+#pragma unroll
+    for (int u = 0; u < C::kUnits; u += 2) place[u / 2] = team_swizzle<RB>(row16, u + (lane >> 4));
 
     float s[C::kTiles][NT][4];
 #pragma unroll
@@ -169,7 +179,7 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt, const float4
 #pragma unroll
         for (int r = 0; r < C::kTiles; ++r) {
             uint32_t x0, x1, x2, x3;  // rows 0-7, rows 8-15 of unit u, the same of unit u + 1
-            ldsm_x4(kt + team_swizzle<RB>(r * 16 + row16, u + second), x0, x1, x2, x3);
+            ldsm_x4(kt + place[u / 2] + r * 16 * RB, x0, x1, x2, x3);
             if constexpr (C::kWide) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) mma_16816(s[r][n], x0, x1, x2, x3, q[n][u / 2][0], q[n][u / 2][1]);
@@ -196,12 +206,12 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt, const float4
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int j = 2 * r + h;
-            const float4 info = meta[j];
-            const bool live = g < __float_as_int(info.z);
-            const float f = C::kWide ? scale_log2 : scale_log2 * team_unit<KIND>() * info.x;
-            vs[j] = C::kWide ? 1.f : info.y;
+            const bool live = g < meta.rows[j];
+            const float2 scale = C::kWide ? make_float2(1.f, 1.f) : meta.scale[j];
+            const float f = C::kWide ? scale_log2 : scale_log2 * scale.x;
+            vs[j] = scale.y;
             // the logarithm only places the weights: bounded, so that a scale of zero does not
-            lv[j] = C::kWide ? 0.f : fminf(fmaxf(__log2f(info.y), -40.f), 40.f);
+            lv[j] = C::kWide ? 0.f : fminf(fmaxf(__log2f(scale.y), -40.f), 40.f);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -218,30 +228,31 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt, const float4
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top[n][e] = fmaxf(top[n][e], __shfl_xor_sync(kFullMask, top[n][e], d));
 
+    // (heads past the group, whose queries are zeros, and states that are empty
+    // still need no rescaling)
     bool moved = false;
+    float f[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) moved |= top[n][e] > st.m[n][e];
+        for (int e = 0; e < 2; ++e) {
+            const float was = st.m[n][e], to = fmaxf(top[n][e], was);
+            f[n][e] = team_exp2(was - (to == -CUDART_INF_F ? 0.f : to));
+            moved |= to > was && was != -CUDART_INF_F && n * 8 + 2 * (lane & 3) + e < group;
+            st.m[n][e] = to;
+            st.l[n][e] *= f[n][e];
+        }
     if (__any_sync(kFullMask, moved)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float f[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float to = fmaxf(top[n][e], st.m[n][e]);
-                f[e] = to == -CUDART_INF_F ? 1.f : team_exp2(st.m[n][e] - to);
-                st.m[n][e] = to;
-                st.l[n][e] *= f[e];
-            }
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-                st.o[n][i][0] *= f[0];
-                st.o[n][i][1] *= f[1];
-                st.o[n][i][2] *= f[0];
-                st.o[n][i][3] *= f[1];
+                st.o[n][i][0] *= f[n][0];
+                st.o[n][i][1] *= f[n][1];
+                st.o[n][i][2] *= f[n][0];
+                st.o[n][i][3] *= f[n][1];
             }
-            if (KIND == kTeamInt8) st.z[n][0] *= f[0], st.z[n][1] *= f[1];
+            if (KIND == kTeamInt8) st.z[n][0] *= f[n][0], st.z[n][1] *= f[n][1];
         }
     }
     uint32_t w[C::kGroups][NT];
@@ -273,7 +284,7 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt, const float4
 #pragma unroll
         for (int u = 0; u < C::kUnits; u += 2) {
             uint32_t x0, x1, x2, x3;
-            ldsm_x4_trans(vt + team_swizzle<RB>(r * 16 + row16, u + second), x0, x1, x2, x3);
+            ldsm_x4_trans(vt + place[u / 2] + r * 16 * RB, x0, x1, x2, x3);
             if constexpr (C::kWide) {  // x0, x1: rows 0-7 and 8-15 of dims 0-7; x2, x3: of dims 8-15
 #pragma unroll
                 for (int n = 0; n < NT; ++n) mma_16816(st.o[n][u / 2], x0, x2, x1, x3, w[2 * r][n], w[2 * r + 1][n]);
@@ -300,7 +311,8 @@ struct TeamBatch {
     int c, end;     // the first step, the end of the piece
     int count;      // steps of the batch, 0: none
     int phys;       // lane j: physical block of entry j
-    int rows;       //         and its rows in use
+    int rows;       //         its rows in use
+    int64_t at;     //         where they are in the caches, in bytes (fixed when the batch's turn comes)
 };
 
 template <int KIND, int D, int NT>
@@ -308,7 +320,7 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
     team_kernel(const __grid_constant__ TeamParams p) {
     using C = TeamConfig<KIND, D, NT>;
     extern __shared__ __align__(128) unsigned char smem[];
-    float2 *ml = reinterpret_cast<float2 *>(smem + C::kMl);
+    float4 *ml = reinterpret_cast<float4 *>(smem + C::kMl);
     const int red_heads = min(8, p.group);
     float *red = reinterpret_cast<float *>(smem + C::kRed);
     int64_t *cum = reinterpret_cast<int64_t *>(red + kTeamWarps * red_heads * C::kPitch);
@@ -371,7 +383,7 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
 
     // ---- the ring ----
     const uint32_t ring = smem_addr(smem) + warp * C::kStages * 2 * C::kTileBytes;
-    float4 *meta = reinterpret_cast<float4 *>(smem + C::kMeta) + warp * C::kStages * C::kGroups;
+    TeamMeta<C::kGroups> *meta = reinterpret_cast<TeamMeta<C::kGroups> *>(smem + C::kMeta) + warp * C::kStages;
     // a step's rows lie in `entries` blocks, 2^span_shift rows in each
     const int span_shift = min(p.block_shift, C::kRows == 32 ? 5 : 4);
     const int entries = C::kRows >> span_shift;
@@ -419,6 +431,15 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
         }
         look_up(y);
     };
+    // A batch's turn: its table entries, loaded a batch ago, are looked at.
+    auto settle = [&](TeamBatch &x) {
+        if (x.rows > 0 && (x.phys < 0 || x.phys >= p.num_blocks)) {
+            report(p.status, PKV_ERR_OUT_OF_RANGE);
+            x.phys = 0;
+        }
+        const int row = (x.c + lane / entries * kTeamWarps) * C::kRows + (lane % entries << span_shift);
+        x.at = ((((int64_t)x.phys * heads + (x.seg - x.s * heads)) << p.block_shift) + (row & (bs - 1))) * C::kRowBytes;
+    };
     TeamBatch now, then;
     now.count = then.count = 0;
     int k = 0;  // the next step to issue in `now`
@@ -426,47 +447,78 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
     if (any) {
         then.seg = from.seg, then.s = first_s, then.c = from.step + warp, then.end = piece_end(from.seg, first_s);
         follow(then, now);
-        if (now.count > 0) follow(now, then);
+        if (now.count > 0) {
+            follow(now, then);
+            settle(now);
+        }
     }
     const unsigned char *kc = static_cast<const unsigned char *>(p.key_cache) + lane * 16;
     const unsigned char *vc = static_cast<const unsigned char *>(p.value_cache) + lane * 16;
+    // lanes 2 j, 2 j + 1: the key and the value scale of group j
+    const float *sc = lane & 1 ? p.value_scale : p.key_scale;
+    uint32_t places[C::kGroupCopies];
+#pragma unroll
+    for (int i = 0; i < C::kGroupCopies; ++i)
+        places[i] = team_swizzle<C::kRowBytes>((i * 32 + lane) / C::kUnits, (i * 32 + lane) % C::kUnits);
     auto issue = [&](int stage) {
         if (now.count > 0) {
-            const uint32_t kt = ring + stage * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
-            if (k == 0 && now.rows > 0 && (now.phys < 0 || now.phys >= p.num_blocks)) {
-                report(p.status, PKV_ERR_OUT_OF_RANGE);
-                now.phys = 0;
-            }
-            const int off0 = (now.c + k * kTeamWarps) * C::kRows & (bs - 1);
-            const int kvh = now.seg - now.s * heads;
+            const uint32_t kt = ring + stage * 2 * C::kTileBytes;
+            if (entries == 1) {  // one block
+                const int64_t at = __shfl_sync(kFullMask, now.at, k);
+                const int rows = __shfl_sync(kFullMask, now.rows, k);
+                const unsigned char *ks = kc + at, *vs = vc + at;
+                if (rows == C::kRows) {
 #pragma unroll
-            for (int j = 0; j < C::kGroups; ++j) {
-                const int entry = k * entries + (j * 8 >> span_shift), in = j * 8 & ((1 << span_shift) - 1);
-                const int block = __shfl_sync(kFullMask, now.phys, entry);
-                const int rows = __shfl_sync(kFullMask, now.rows, entry) - in;
-                const int64_t at = ((((int64_t)block * heads + kvh) << p.block_shift) + (off0 & ~((1 << span_shift) - 1)) + in) *
-                                   C::kRowBytes;
+                    for (int j = 0; j < C::kGroups; ++j)
 #pragma unroll
-                for (int i = 0; i < C::kGroupCopies; ++i) {
-                    const int idx = i * 32 + lane, r = idx / C::kUnits, u = idx % C::kUnits;
-                    const uint32_t to = team_swizzle<C::kRowBytes>(j * 8 + r, u);
-                    cp_async_16_or_zero(kt + to, kc + at + i * 512, r < rows);
-                    cp_async_16_or_zero(vt + to, vc + at + i * 512, r < rows);
+                        for (int i = 0; i < C::kGroupCopies; ++i) {
+                            const int off = (j * C::kGroupCopies + i) * 512;
+                            cp_async_16_of(kt + places[i] + j * 8 * C::kRowBytes, ks + off);
+                            cp_async_16_of(kt + places[i] + j * 8 * C::kRowBytes + C::kTileBytes, vs + off);
+                        }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < C::kGroups; ++j)
+#pragma unroll
+                        for (int i = 0; i < C::kGroupCopies; ++i) {
+                            const bool live = j * 8 + (i * 32 + lane) / C::kUnits < rows;
+                            const int off = live ? (j * C::kGroupCopies + i) * 512 : 0;
+                            cp_async_16_or_zero(kt + places[i] + j * 8 * C::kRowBytes, ks + off, live);
+                            cp_async_16_or_zero(kt + places[i] + j * 8 * C::kRowBytes + C::kTileBytes, vs + off, live);
+                        }
                 }
-                if (lane == j) {
-                    float4 *m = meta + stage * C::kGroups + j;
-                    m->z = __int_as_float(rows);
-                    if (!C::kWide) {
-                        const int64_t of = (int64_t)block * p.scale_stride + kvh;
-                        cp_async_4_or_zero(smem_addr(&m->x), p.key_scale + of, rows > 0);
-                        cp_async_4_or_zero(smem_addr(&m->y), p.value_scale + of, rows > 0);
+            } else {
+#pragma unroll
+                for (int j = 0; j < C::kGroups; ++j) {
+                    const int entry = k * entries + (j * 8 >> span_shift), in = j * 8 & ((1 << span_shift) - 1);
+                    const int64_t at = __shfl_sync(kFullMask, now.at, entry) + in * C::kRowBytes;
+                    const int rows = __shfl_sync(kFullMask, now.rows, entry) - in;
+#pragma unroll
+                    for (int i = 0; i < C::kGroupCopies; ++i) {
+                        const bool live = (i * 32 + lane) / C::kUnits < rows;
+                        const int64_t off = live ? at + i * 512 : 0;
+                        cp_async_16_or_zero(kt + places[i] + j * 8 * C::kRowBytes, kc + off, live);
+                        cp_async_16_or_zero(kt + places[i] + j * 8 * C::kRowBytes + C::kTileBytes, vc + off, live);
                     }
                 }
+            }
+            const int entry = k * entries + ((lane >> 1) * 8 >> span_shift);
+            const int rows = __shfl_sync(kFullMask, now.rows, entry) - ((lane >> 1) * 8 & ((1 << span_shift) - 1));
+            const int block = C::kWide ? 0 : __shfl_sync(kFullMask, now.phys, entry);
+            if (lane < 2 * C::kGroups) {
+                TeamMeta<C::kGroups> &m = meta[stage];
+                m.rows[lane >> 1] = rows;
+                if (!C::kWide)
+                    cp_async_4_or_zero(smem_addr(m.scale) + lane * 4,
+                                       sc + (int64_t)block * p.scale_stride + (now.seg - now.s * heads), rows > 0);
             }
             if (++k == now.count) {
                 k = 0;
                 now = then;
-                if (now.count > 0) follow(now, then);
+                if (now.count > 0) {
+                    follow(now, then);
+                    settle(now);
+                }
             }
         }
         cp_async_commit();
@@ -483,15 +535,25 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int h = n * 8 + g;
+            const bool live = h < p.group;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 // fp16: dims 2t, 2t + 1 and 8 further; codes: dims 4t to 4t + 3
                 const __half *src = rows_q + h * D + 16 * i + (C::kWide ? 2 * t : 4 * t);
-                q[n][i][0] = h < p.group ? __ldg(reinterpret_cast<const uint32_t *>(src)) : 0u;
-                q[n][i][1] = h < p.group ? __ldg(reinterpret_cast<const uint32_t *>(src + (C::kWide ? 8 : 2))) : 0u;
+                uint2 x = make_uint2(0u, 0u);
+                if (live) {
+                    if (C::kWide) {
+                        x.x = __ldg(reinterpret_cast<const uint32_t *>(src));
+                        x.y = __ldg(reinterpret_cast<const uint32_t *>(src + 8));
+                    } else {
+                        x = __ldg(reinterpret_cast<const uint2 *>(src));
+                    }
+                }
+                q[n][i][0] = x.x, q[n][i][1] = x.y;
             }
         }
     };
+    const float factor = p.scale_log2 * team_unit<KIND>();
     int stage = 0;
     int seg = from.seg, s = first_s, lo = from.step;
     bool on = any;
@@ -513,7 +575,7 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
             cp_async_wait<C::kStages - 1>();
             __syncwarp();
             const uint32_t kt = ring + stage * 2 * C::kTileBytes;
-            team_step<KIND, D, NT>(kt, kt + C::kTileBytes, meta + stage * C::kGroups, q, bias, p.scale_log2, st, lane);
+            team_step<KIND, D, NT>(kt, kt + C::kTileBytes, meta[stage], q, bias, factor, p.group, st, lane);
             __syncwarp();
             issue(stage);
             if (++stage == C::kStages) stage = 0;
@@ -539,33 +601,39 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
                 for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(kFullMask, l, d);
                 const int h = 2 * t + e;
                 if (h < live) {
-                    if (g == 0) ml[warp * 8 + h] = make_float2(st.m[n][e], l);
+                    if (g == 0) ml[warp * 8 + h] = make_float4(st.m[n][e], l, KIND == kTeamInt8 ? st.z[n][e] : 0.f, 0.f);
                     float *dst = red + (warp * red_heads + h) * C::kPitch;
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
-                        const float z = KIND == kTeamInt8 ? st.z[n][e] : 0.f;
-                        dst[team_dim<KIND>(i, g, 0)] = (st.o[n][i][e] - z) * team_unit<KIND>();
-                        dst[team_dim<KIND>(i, g, 1)] = (st.o[n][i][2 + e] - z) * team_unit<KIND>();
+                        if (C::kWide) {
+                            dst[16 * i + g] = st.o[n][i][e];
+                            dst[16 * i + g + 8] = st.o[n][i][2 + e];
+                        } else {
+                            *reinterpret_cast<float2 *>(dst + 16 * i + 2 * g) = make_float2(st.o[n][i][e], st.o[n][i][2 + e]);
+                        }
                     }
                 }
             }
             __syncthreads();
             for (int i = tid; i < live * (D / 2); i += kTeamThreads) {
                 const int h = i / (D / 2), d = i % (D / 2) * 2;
-                float top = -CUDART_INF_F, l = 0.f;
+                float top = -CUDART_INF_F, l = 0.f, z = 0.f;
 #pragma unroll
                 for (int w = 0; w < kTeamWarps; ++w) top = fmaxf(top, ml[w * 8 + h].x);
                 const float ref = top == -CUDART_INF_F ? 0.f : top;
                 float2 o = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < kTeamWarps; ++w) {
-                    const float2 x = ml[w * 8 + h];
+                    const float4 x = ml[w * 8 + h];
                     const float f = team_exp2(x.x - ref);
                     const float2 y = *reinterpret_cast<const float2 *>(red + (w * red_heads + h) * C::kPitch + d);
                     l = fmaf(x.y, f, l);
+                    z = fmaf(x.z, f, z);
                     o.x = fmaf(y.x, f, o.x);
                     o.y = fmaf(y.y, f, o.y);
                 }
+                o.x = (o.x - z) * team_unit<KIND>();
+                o.y = (o.y - z) * team_unit<KIND>();
                 const int head = n * 8 + h;
                 if (whole) {
                     const float inv = l == 0.f ? 0.f : 1.f / l;  // no row: zeros

@@ -8,7 +8,10 @@
 
 namespace pkv {
 
-constexpr int kTeamWarps = 8;
+#ifndef PKV_TEAM_WARPS
+#define PKV_TEAM_WARPS 8
+#endif
+constexpr int kTeamWarps = PKV_TEAM_WARPS;
 constexpr int kTeamThreads = kTeamWarps * 32;
 constexpr int kTeamMaxGroup = 16;
 

@@ -25,7 +25,7 @@
 namespace pkv {
 
 #ifndef PKV_TEAM_PIECE
-#define PKV_TEAM_PIECE 8
+#define PKV_TEAM_PIECE 16
 #endif
 constexpr int kTeamPiece = PKV_TEAM_PIECE;
 constexpr int kTeamSnap = 8;

@@ -53,8 +53,8 @@ static void check_split(const std::vector<int> &steps, int heads, int64_t grid, 
                 const int hi = seg < end.seg ? steps[s] : end.step;
                 CHECK(seg == next_seg && lo == next_step && lo < hi);
                 std::vector<char> seen(hi - lo, 0);
-                for (int w = 0; w < 8; ++w)
-                    for (int x = lo + w; x < hi; x += 8) seen[x - lo]++;
+                for (int w = 0; w < 4; ++w)
+                    for (int x = lo + w; x < hi; x += 4) seen[x - lo]++;
                 for (char x : seen) CHECK(x == 1);
                 units += hi - lo + kTeamPiece;
                 next_step = hi;

@@ -20,7 +20,7 @@ Tolerance of the decode, per output element, with the codes and scales as given:
   factors' sum off again, so their terms' magnitudes count |code| + 256;
 * sums in fp32, at most 2^-22 of the magnitudes' sum per step (an instruction
   adds 16 products, each cut at 2^-23 or finer of the largest): a step of 16 rows
-  for each of 8 warps, and two dozen joins.
+  for each of 4 warps, and two dozen joins.
 """
 
 import numpy as np
@@ -45,7 +45,7 @@ def pkv():
     return m
 
 
-def bound(ref, spread, reach, count, top, d, warps=8, reach8=0.0, spread8=0.0):
+def bound(ref, spread, reach, count, top, d, warps=4, reach8=0.0, spread8=0.0):
     """reach8, spread8: what int8's 256 steps of the scale add to the terms' magnitudes in the scores and in the sums."""
     score = (2 * d * (reach + reach8) + 12 * 1.45 * reach) * 2.0 ** -24 + 2.0 ** -18
     sums = (count / 16 / warps + 24) * 2.0 ** -22
@@ -160,7 +160,7 @@ class Case:
         k, v = (np.nan_to_num(x) * s[:, :, None, None] for x, s in zip(self.pools, self.scales))
         return Q.decode(self.q, k, v, self.tables, self.lens, self.scale, self.lists)
 
-    def check(self, out, expect=None, status=0, warps=8):
+    def check(self, out, expect=None, status=0, warps=4):
         torch.cuda.synchronize()
         assert int(self.status.item()) == status
         ref, spread, reach, count, top = expect or self.oracle()
