@@ -102,11 +102,13 @@ int decode(void *out, const void *query, const void *key_cache, const void *valu
     const int rc = ensure_smem_attr(k.fn, smem);
     if (rc != PKV_OK) return rc;
     void *args[] = {&p};
-    if (launch_pdl(k.fn, dim3((unsigned)num_ctas), dim3(kTeamThreads), smem, stream, args) != cudaSuccess) {
+    if (launch_pdl(k.fn, dim3((unsigned)num_ctas), dim3((unsigned)k.threads), smem, stream, args) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
     }
-    if (num_ctas == 1) return PKV_OK;  // nothing is cut
+    // No segment is long enough to be cut: nothing to join.
+    const int64_t most = team_rows((int64_t)max_blocks_per_seq * block_size, p.block_shift, selected ? max_selected : -1);
+    if (num_ctas == 1 || team_steps(most, k.step_rows) <= 2 * kTeamSnap) return PKV_OK;
     const void *join = head_dim == 64 ? reinterpret_cast<const void *>(&team_join_kernel<64>)
                                       : reinterpret_cast<const void *>(&team_join_kernel<128>);
     if (launch_pdl(join, dim3((unsigned)num_ctas, (unsigned)group), dim3(kTeamJoinThreads), 0, stream, args) !=
@@ -126,7 +128,7 @@ extern "C" size_t pkv_decode_team_workspace_size(int num_heads, int num_kv_heads
     if (num_ctas < 0 || num_ctas > kMaxCtas || !shape_ok(num_heads, num_kv_heads, head_dim)) return 0;
     if (num_ctas == 0) {
         if (multiprocessors(&num_ctas) != PKV_OK) return 0;
-        num_ctas *= 4;  // the most that the default is
+        num_ctas *= 2;  // the most that the default is
     }
     return TeamWorkspace::plan(num_ctas, num_heads / num_kv_heads, head_dim).total;
 }

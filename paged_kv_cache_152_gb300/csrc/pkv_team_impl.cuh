@@ -55,20 +55,24 @@ template <int KIND, int D, int NT>
 struct TeamConfig {
     static constexpr bool kWide = KIND == kTeamF16;
     static constexpr int kRowBytes = D * (kWide ? 2 : 1);
-    static constexpr int kRows = kRowBytes == 64 ? 32 : 16;  // of a step
+    static constexpr int kRows = kRowBytes <= 128 ? 32 : 16;  // of a step
     static constexpr int kTiles = kRows / 16;
     static constexpr int kGroups = kRows / 8;                // a group of 8 rows lies in one block
     static constexpr int kUnits = kRowBytes / 16;            // 16-byte units of a row
     static constexpr int kTileBytes = kRows * kRowBytes;
-    static constexpr int kCtas = (NT == 1 && kTileBytes <= 2048 ? 16 : 8) / kTeamWarps;     // per SM
-    static constexpr int kStages = 131072 / (kCtas * kTeamWarps) / (2 * kTileBytes);  // 128 KB per SM in flight
+    static constexpr int kWarps = kWide ? 8 : 4;             // of a CTA
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kCtas = 8 / kWarps;                 // per SM
+    static constexpr int kStages = 16384 / (2 * kTileBytes); // 16 KB per warp in flight, 128 KB per SM
     static constexpr int kGroupCopies = kUnits / 4;          // of a lane, per cache and group
     static constexpr int kPitch = D + 8;                     // floats between heads of a warp's output
     // [warps][stages][K, V tiles] [warps][stages] TeamMeta
-    // [warps][8 heads] (maximum, sum, bias), [warps][heads][pitch] floats, then by sequence: cum
-    static constexpr size_t kMeta = (size_t)kTeamWarps * kStages * 2 * kTileBytes;
-    static constexpr size_t kMl = kMeta + (size_t)kTeamWarps * kStages * sizeof(TeamMeta<kGroups>);
-    static constexpr size_t kRed = kMl + (size_t)kTeamWarps * 8 * 16;
+    // [warps][8 rows] (maximum, sum, bias), [warps][8 rows][pitch] floats (a row is a head of
+    // one of the pieces in hold), then by sequence: cum
+    static constexpr size_t kMeta = (size_t)kWarps * kStages * 2 * kTileBytes;
+    static constexpr size_t kMl = kMeta + (size_t)kWarps * kStages * sizeof(TeamMeta<kGroups>);
+    static constexpr size_t kRed = kMl + (size_t)kWarps * 8 * 16;
+    static constexpr size_t kCum = kRed + (size_t)kWarps * 8 * kPitch * 4;
 };
 
 // Byte of 16-byte unit u of row r in a tile whose rows are RB bytes: eight
@@ -303,12 +307,14 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt,
         }
 }
 
-// Up to 32 steps of a warp (every kTeamWarps-th of a piece's) in one segment: lane
+// Up to 32 steps of a warp (every kWarps-th of a piece's) in one segment: lane
 // j looks up the block table's entry j of theirs, all at once and a batch ahead of
 // their use.
 struct TeamBatch {
     int seg, s;     // the segment and its sequence
-    int c, end;     // the first step, the end of the piece
+    int c;          // the first step
+    int lo, end;    // the piece
+    int rot;        // the warp that takes the piece's first step
     int count;      // steps of the batch, 0: none
     int phys;       // lane j: physical block of entry j
     int rows;       //         its rows in use
@@ -316,15 +322,15 @@ struct TeamBatch {
 };
 
 template <int KIND, int D, int NT>
-__global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
+__global__ void __launch_bounds__(TeamConfig<KIND, D, NT>::kThreads, TeamConfig<KIND, D, NT>::kCtas)
     team_kernel(const __grid_constant__ TeamParams p) {
     using C = TeamConfig<KIND, D, NT>;
     extern __shared__ __align__(128) unsigned char smem[];
     float4 *ml = reinterpret_cast<float4 *>(smem + C::kMl);
-    const int red_heads = min(8, p.group);
     float *red = reinterpret_cast<float *>(smem + C::kRed);
-    int64_t *cum = reinterpret_cast<int64_t *>(red + kTeamWarps * red_heads * C::kPitch);
-    __shared__ int64_t warp_sum[kTeamWarps];
+    int64_t *cum = reinterpret_cast<int64_t *>(smem + C::kCum);
+    __shared__ int64_t warp_sum[C::kWarps];
+    __shared__ int4 held[8];  // a piece: segment, the warp of its first step, its warps, 0 / 1 / 2: part 0 / part 1 / whole
     __shared__ TeamPlace share[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int heads = p.num_kv_heads, bs = 1 << p.block_shift;
@@ -342,7 +348,7 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
 
     // The prefix sums of the sequences' steps.
     {
-        const int per = (p.num_seqs + kTeamThreads - 1) / kTeamThreads;
+        const int per = (p.num_seqs + C::kThreads - 1) / C::kThreads;
         const int first = min(tid * per, p.num_seqs), end = min(first + per, p.num_seqs);
         int64_t mine = 0;
         for (int s = first; s < end; ++s) mine += team_units(steps_of(s));
@@ -360,7 +366,7 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
             cum[s] = at;
             at += team_units(steps_of(s));
         }
-        if (tid == kTeamThreads - 1) cum[p.num_seqs] = at;
+        if (tid == C::kThreads - 1) cum[p.num_seqs] = at;
         __syncthreads();
     }
     const int64_t T = cum[p.num_seqs] * heads;
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
         const int len = __ldg(p.context_lens + s);
         if ((len < 0 || len > reach) && tid == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
         if (cum[s + 1] == cum[s])  // no position: zeros
-            for (int i = tid; i < p.num_heads * D / 8; i += kTeamThreads)
+            for (int i = tid; i < p.num_heads * D / 8; i += C::kThreads)
                 reinterpret_cast<uint4 *>(p.out + (int64_t)s * p.num_heads * D)[i] = make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
@@ -391,9 +397,9 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
     // The entries of the batch that begins at step c of the piece.
     auto look_up = [&](TeamBatch &x) {
         x.rows = x.phys = 0;
-        x.count = min(room, (x.end - x.c + kTeamWarps - 1) / kTeamWarps);
+        x.count = min(room, (x.end - x.c + C::kWarps - 1) / C::kWarps);
         if (lane >= x.count * entries) return;
-        const int64_t v = (int64_t)(x.c + lane / entries * kTeamWarps) * C::kRows + (lane % entries << span_shift);
+        const int64_t v = (int64_t)(x.c + lane / entries * C::kWarps) * C::kRows + (lane % entries << span_shift);
         int64_t block = v >> p.block_shift;
         const int len = context(x.s);
         bool bad = false, there = true;
@@ -420,13 +426,15 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
     // The next batch: the piece's, or the next piece's in which this warp has a step.
     auto follow = [&](const TeamBatch &x, TeamBatch &y) {
         y = x;
-        y.c += x.count * kTeamWarps;
+        y.c += x.count * C::kWarps;
         y.count = 0;
 #pragma unroll 1
         while (y.c >= y.end) {
             y.seg = team_next(cum, p.num_seqs, heads, y.seg, y.s);
             if (!more(y.seg)) return;
-            y.c = warp;
+            y.rot = (y.rot + y.end - y.lo) % C::kWarps;
+            y.lo = 0;
+            y.c = (warp - y.rot) & (C::kWarps - 1);
             y.end = piece_end(y.seg, y.s);
         }
         look_up(y);
@@ -437,7 +445,7 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
             report(p.status, PKV_ERR_OUT_OF_RANGE);
             x.phys = 0;
         }
-        const int row = (x.c + lane / entries * kTeamWarps) * C::kRows + (lane % entries << span_shift);
+        const int row = (x.c + lane / entries * C::kWarps) * C::kRows + (lane % entries << span_shift);
         x.at = ((((int64_t)x.phys * heads + (x.seg - x.s * heads)) << p.block_shift) + (row & (bs - 1))) * C::kRowBytes;
     };
     TeamBatch now, then;
@@ -445,7 +453,8 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
     int k = 0;  // the next step to issue in `now`
     const int first_s = any ? from.seg / heads : 0;
     if (any) {
-        then.seg = from.seg, then.s = first_s, then.c = from.step + warp, then.end = piece_end(from.seg, first_s);
+        then.seg = from.seg, then.s = first_s, then.rot = 0;
+        then.lo = from.step, then.c = from.step + warp, then.end = piece_end(from.seg, first_s);
         follow(then, now);
         if (now.count > 0) {
             follow(now, then);
@@ -525,11 +534,13 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
     };
     for (int i = 0; i < C::kStages; ++i) issue(i);
 
-    // ---- pieces ----
+    // ---- pieces, some in hold: their outputs stay apart until a barrier for all ----
     const int g = lane >> 2, t = lane & 3;
     TeamState<D, NT> st;
     uint32_t q[NT][D / 16][2];
     float bias[NT][2];
+    const float factor = p.scale_log2 * team_unit<KIND>();
+    const int red_heads = min(8, p.group), hold = 8 / red_heads;
     auto load_q = [&](int seg) {
         const __half *rows_q = p.query + (int64_t)seg * p.group * D;
 #pragma unroll
@@ -553,100 +564,123 @@ __global__ void __launch_bounds__(kTeamThreads, TeamConfig<KIND, D, NT>::kCtas)
             }
         }
     };
-    const float factor = p.scale_log2 * team_unit<KIND>();
+    // Dims d and d + 1 of a row of the outputs that a piece's warps hold: to the output, or to the workspace.
+    auto join = [&](int row, int head, int d, const int4 &piece) {
+        float top = -CUDART_INF_F, l = 0.f, z = 0.f;
+        float4 x[C::kWarps];
+#pragma unroll
+        for (int w = 0; w < C::kWarps; ++w) {
+            x[w] = make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
+            if (((w - piece.y) & (C::kWarps - 1)) < piece.z) x[w] = ml[w * 8 + row];
+            top = fmaxf(top, x[w].x);
+        }
+        const float ref = top == -CUDART_INF_F ? 0.f : top;
+        float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < C::kWarps; ++w) {
+            if (((w - piece.y) & (C::kWarps - 1)) >= piece.z) continue;
+            const float f = team_exp2(x[w].x - ref);
+            const float2 y = *reinterpret_cast<const float2 *>(red + (w * 8 + row) * C::kPitch + d);
+            l = fmaf(x[w].y, f, l);
+            z = fmaf(x[w].z, f, z);
+            o.x = fmaf(y.x, f, o.x);
+            o.y = fmaf(y.y, f, o.y);
+        }
+        o.x = (o.x - z) * team_unit<KIND>();
+        o.y = (o.y - z) * team_unit<KIND>();
+        if (piece.w == 2) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // no row: zeros
+            *reinterpret_cast<__half2 *>(p.out + ((int64_t)piece.x * p.group + head) * D + d) =
+                __floats2half2_rn(o.x * inv, o.y * inv);
+        } else {
+            const int64_t part = ((int64_t)blockIdx.x * 2 + piece.w) * p.group + head;
+            if (d == 0) p.part_ml[part] = make_float2(top, l);
+            *reinterpret_cast<float2 *>(p.part_o + part * D + d) = o;
+        }
+    };
+
     int stage = 0;
-    int seg = from.seg, s = first_s, lo = from.step;
+    int seg = from.seg, s = first_s, lo = from.step, rot = 0;
     bool on = any;
     if (on) load_q(seg);
     while (on) {
-        const int end = piece_end(seg, s), n_steps = team_steps_of(cum, s);
-        if (KIND == kTeamInt8) {  // what the biases add to each head's scores
+        int pieces = 0;
+        for (; pieces < hold && on; ++pieces) {
+            const int j = pieces, end = piece_end(seg, s), live_warps = min(C::kWarps, end - lo);
+            const bool whole = lo == 0 && end == team_steps_of(cum, s);
+            const int mine = (warp - rot) & (C::kWarps - 1);
+            if (!whole) (lo > 0 ? cut.x : cut.y) = seg;
+            if (tid == 0) held[j] = make_int4(seg, rot, live_warps, whole ? 2 : lo > 0 ? 0 : 1);
+            if (mine < live_warps) {
+                if (KIND == kTeamInt8) {  // what the biases add to each head's scores
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i)
+                            mma_16816(x, kTeamBias, kTeamBias, kTeamBias, kTeamBias, q[n][i][0], q[n][i][1]);
+                        bias[n][0] = x[0], bias[n][1] = x[1];
+                    }
+                }
+                st.clear();
+                for (int c = lo + mine; c < end; c += C::kWarps) {
+                    cp_async_wait<C::kStages - 1>();
+                    __syncwarp();
+                    const uint32_t kt = ring + stage * 2 * C::kTileBytes;
+                    team_step<KIND, D, NT>(kt, kt + C::kTileBytes, meta[stage], q, bias, factor, p.group, st, lane);
+                    __syncwarp();
+                    issue(stage);
+                    if (++stage == C::kStages) stage = 0;
+                }
+            }
+            rot = (rot + end - lo) % C::kWarps;
+            seg = team_next(cum, p.num_seqs, heads, seg, s);
+            lo = 0;
+            on = more(seg);
+            if (on) load_q(seg);  // the next piece's queries come while this one's outputs go
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                const int live = min(8, p.group - n * 8);
+                if (mine < live_warps) {
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    mma_16816(x, kTeamBias, kTeamBias, kTeamBias, kTeamBias, q[n][i][0], q[n][i][1]);
-                bias[n][0] = x[0], bias[n][1] = x[1];
-            }
-        }
-        st.clear();
-        for (int c = lo + warp; c < end; c += kTeamWarps) {
-            cp_async_wait<C::kStages - 1>();
-            __syncwarp();
-            const uint32_t kt = ring + stage * 2 * C::kTileBytes;
-            team_step<KIND, D, NT>(kt, kt + C::kTileBytes, meta[stage], q, bias, factor, p.group, st, lane);
-            __syncwarp();
-            issue(stage);
-            if (++stage == C::kStages) stage = 0;
-        }
-        const int here = seg;
-        const bool whole = lo == 0 && end == n_steps;
-        const int slot = lo > 0 ? 0 : 1;
-        seg = team_next(cum, p.num_seqs, heads, seg, s);
-        lo = 0;
-        on = more(seg);
-        if (on) load_q(seg);  // the next piece's queries come while this one's outputs meet
-
-        // ---- the warps' outputs, eight heads at a time ----
-        if (!whole) (slot ? cut.y : cut.x) = here;
+                    for (int e = 0; e < 2; ++e) {
+                        float l = st.l[n][e];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int live = min(8, p.group - n * 8);
-            if (NT > 1 && live <= 0) break;
+                        for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(kFullMask, l, d);
+                        const int h = 2 * t + e;
+                        if (h < live) {
+                            const int at = warp * 8 + j * red_heads + h;
+                            if (g == 0) ml[at] = make_float4(st.m[n][e], l, KIND == kTeamInt8 ? st.z[n][e] : 0.f, 0.f);
+                            float *dst = red + at * C::kPitch;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float l = st.l[n][e];
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(kFullMask, l, d);
-                const int h = 2 * t + e;
-                if (h < live) {
-                    if (g == 0) ml[warp * 8 + h] = make_float4(st.m[n][e], l, KIND == kTeamInt8 ? st.z[n][e] : 0.f, 0.f);
-                    float *dst = red + (warp * red_heads + h) * C::kPitch;
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        if (C::kWide) {
-                            dst[16 * i + g] = st.o[n][i][e];
-                            dst[16 * i + g + 8] = st.o[n][i][2 + e];
-                        } else {
-                            *reinterpret_cast<float2 *>(dst + 16 * i + 2 * g) = make_float2(st.o[n][i][e], st.o[n][i][2 + e]);
+                            for (int i = 0; i < D / 16; ++i) {
+                                if (C::kWide) {
+                                    dst[16 * i + g] = st.o[n][i][e];
+                                    dst[16 * i + g + 8] = st.o[n][i][2 + e];
+                                } else {
+                                    *reinterpret_cast<float2 *>(dst + 16 * i + 2 * g) =
+                                        make_float2(st.o[n][i][e], st.o[n][i][2 + e]);
+                                }
+                            }
                         }
                     }
                 }
-            }
-            __syncthreads();
-            for (int i = tid; i < live * (D / 2); i += kTeamThreads) {
-                const int h = i / (D / 2), d = i % (D / 2) * 2;
-                float top = -CUDART_INF_F, l = 0.f, z = 0.f;
-#pragma unroll
-                for (int w = 0; w < kTeamWarps; ++w) top = fmaxf(top, ml[w * 8 + h].x);
-                const float ref = top == -CUDART_INF_F ? 0.f : top;
-                float2 o = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < kTeamWarps; ++w) {
-                    const float4 x = ml[w * 8 + h];
-                    const float f = team_exp2(x.x - ref);
-                    const float2 y = *reinterpret_cast<const float2 *>(red + (w * red_heads + h) * C::kPitch + d);
-                    l = fmaf(x.y, f, l);
-                    z = fmaf(x.z, f, z);
-                    o.x = fmaf(y.x, f, o.x);
-                    o.y = fmaf(y.y, f, o.y);
-                }
-                o.x = (o.x - z) * team_unit<KIND>();
-                o.y = (o.y - z) * team_unit<KIND>();
-                const int head = n * 8 + h;
-                if (whole) {
-                    const float inv = l == 0.f ? 0.f : 1.f / l;  // no row: zeros
-                    const int64_t row = (int64_t)here * p.group + head;
-                    *reinterpret_cast<__half2 *>(p.out + row * D + d) = __floats2half2_rn(o.x * inv, o.y * inv);
-                } else {
-                    const int64_t part = ((int64_t)blockIdx.x * 2 + slot) * p.group + head;
-                    if (d == 0) p.part_ml[part] = make_float2(top, l);
-                    *reinterpret_cast<float2 *>(p.part_o + part * D + d) = o;
+                if (NT > 1) {  // a piece at a time, eight heads at a time
+                    __syncthreads();
+                    for (int i = tid; i < live * (D / 2); i += C::kThreads)
+                        join(i / (D / 2), n * 8 + i / (D / 2), i % (D / 2) * 2, held[0]);
+                    if (n + 1 < NT) __syncthreads();
                 }
             }
-            __syncthreads();
         }
+        if (NT == 1) {
+            __syncthreads();
+            for (int i = tid; i < pieces * red_heads * (D / 2); i += C::kThreads) {
+                const int row = i / (D / 2), j = row / red_heads;
+                join(row, row - j * red_heads, i % (D / 2) * 2, held[j]);
+            }
+        }
+        __syncthreads();
     }
     if (tid == 0) p.cut[blockIdx.x] = cut;
 }
@@ -707,18 +741,20 @@ __global__ void __launch_bounds__(kTeamJoinThreads) team_join_kernel(const __gri
 }
 
 template <int KIND, int D, int NT>
-TeamKernel team_kernel_info_of(int group) {
+TeamKernel team_kernel_info_of() {
     using C = TeamConfig<KIND, D, NT>;
     TeamKernel k;
     k.fn = reinterpret_cast<const void *>(&team_kernel<KIND, D, NT>);
-    k.smem_fixed = C::kRed + (size_t)kTeamWarps * (group < 8 ? group : 8) * C::kPitch * 4 + 8;
+    k.smem_fixed = C::kCum + 8;
+    k.threads = C::kThreads;
     k.ctas_per_sm = C::kCtas;
+    k.step_rows = C::kRows;
     return k;
 }
 
 template <int KIND, int D>
 TeamKernel team_kernel_info(int group) {
-    return group <= 8 ? team_kernel_info_of<KIND, D, 1>(group) : team_kernel_info_of<KIND, D, 2>(group);
+    return group <= 8 ? team_kernel_info_of<KIND, D, 1>() : team_kernel_info_of<KIND, D, 2>();
 }
 
 }  // namespace pkv

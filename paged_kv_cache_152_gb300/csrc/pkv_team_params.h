@@ -8,11 +8,6 @@
 
 namespace pkv {
 
-#ifndef PKV_TEAM_WARPS
-#define PKV_TEAM_WARPS 8
-#endif
-constexpr int kTeamWarps = PKV_TEAM_WARPS;
-constexpr int kTeamThreads = kTeamWarps * 32;
 constexpr int kTeamMaxGroup = 16;
 
 struct TeamParams {
@@ -59,7 +54,9 @@ struct TeamWorkspace {
 struct TeamKernel {
     const void *fn;
     size_t smem_fixed;    // dynamic shared memory without the prefix sums (8 bytes per sequence)
+    int threads;
     int ctas_per_sm;
+    int step_rows;
 };
 
 // pkv_team_{f16,int8,e4m3}.cu; head_dim 64 or 128, group 1 to 16.

@@ -25,11 +25,18 @@
 namespace pkv {
 
 #ifndef PKV_TEAM_PIECE
-#define PKV_TEAM_PIECE 16
+#define PKV_TEAM_PIECE 4
 #endif
 constexpr int kTeamPiece = PKV_TEAM_PIECE;
-constexpr int kTeamSnap = 8;
-constexpr int kTeamLeast = 16;  // units that a CTA gets at the least
+
+#ifndef PKV_TEAM_LEAST
+#define PKV_TEAM_LEAST 6
+#endif
+#ifndef PKV_TEAM_SNAP
+#define PKV_TEAM_SNAP 8
+#endif
+constexpr int kTeamSnap = PKV_TEAM_SNAP;
+constexpr int kTeamLeast = PKV_TEAM_LEAST;  // units that a CTA gets at the least
 
 // Steps of a sequence of `rows` rows.
 PKV_HD int team_steps(int64_t rows, int step_rows) { return rows <= 0 ? 0 : (int)((rows + step_rows - 1) / step_rows); }
