@@ -343,6 +343,22 @@ __global__ void __launch_bounds__(TeamConfig<KIND, D, NT>::kThreads, TeamConfig<
         return team_steps(team_rows(context(s), p.block_shift, p.selected ? p.max_selected : -1), C::kRows);
     };
 
+    // While the kernel before still runs nothing is read, but what will be read one after the other is asked into
+    // L2 (which its writes go through): contexts, tables, lists and queries, up to 1 MB of each.
+    {
+        const int first = blockIdx.x * C::kThreads + tid, step = gridDim.x * C::kThreads;
+        auto ask = [&](const void *at, int64_t bytes) {
+            const int lines = (int)(min(bytes, (int64_t)1 << 20) + 127 >> 7);
+            for (int i = first; i < lines; i += step) prefetch_l2(static_cast<const char *>(at) + (int64_t)i * 128);
+        };
+        ask(p.context_lens, (int64_t)p.num_seqs * 4);
+        ask(p.block_tables, (int64_t)p.num_seqs * p.max_blocks_per_seq * 4);
+        if (p.selected) {
+            ask(p.num_selected, (int64_t)p.num_seqs * heads * 4);
+            ask(p.selected, (int64_t)p.num_seqs * heads * p.max_selected * 4);
+        }
+        ask(p.query, (int64_t)p.num_seqs * p.num_heads * D * 2);
+    }
     grid_dependency_wait();
     launch_dependents();
 
@@ -372,13 +388,6 @@ __global__ void __launch_bounds__(TeamConfig<KIND, D, NT>::kThreads, TeamConfig<
     const int64_t T = cum[p.num_seqs] * heads;
     const int64_t ctas = team_ctas(T, gridDim.x);
     if (tid < 2) share[tid] = team_start(cum, p.num_seqs, heads, min((int64_t)blockIdx.x + tid, ctas), ctas);
-    for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
-        const int len = __ldg(p.context_lens + s);
-        if ((len < 0 || len > reach) && tid == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
-        if (cum[s + 1] == cum[s])  // no position: zeros
-            for (int i = tid; i < p.num_heads * D / 8; i += C::kThreads)
-                reinterpret_cast<uint4 *>(p.out + (int64_t)s * p.num_heads * D)[i] = make_uint4(0, 0, 0, 0);
-    }
     __syncthreads();
     // The share: segments from.seg, from step from.step on, to to.seg, before to.step.
     const TeamPlace from = share[0], to = share[1];
@@ -408,11 +417,13 @@ __global__ void __launch_bounds__(TeamConfig<KIND, D, NT>::kThreads, TeamConfig<
             const int blocks = (len + bs - 1) >> p.block_shift;
             const int most = min(blocks, p.max_selected);
             int count = __ldg(p.num_selected + seg);
+            // (a row past max_selected is that of a step past the list)
+            const int listed = __ldg(p.selected + seg * p.max_selected + min(block, (int64_t)p.max_selected - 1));
             bad = (count < 0 || count > most) && v == 0;
             count = min(count, most);
             there = block < count;
             if (there) {
-                block = __ldg(p.selected + seg * p.max_selected + block);
+                block = listed;
                 if (block < 0 || block >= blocks) bad = true, there = false;
             }
         }
@@ -533,6 +544,14 @@ __global__ void __launch_bounds__(TeamConfig<KIND, D, NT>::kThreads, TeamConfig<
         cp_async_commit();
     };
     for (int i = 0; i < C::kStages; ++i) issue(i);
+
+    for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
+        const int len = __ldg(p.context_lens + s);
+        if ((len < 0 || len > reach) && tid == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
+        if (cum[s + 1] == cum[s])  // no position: zeros
+            for (int i = tid; i < p.num_heads * D / 8; i += C::kThreads)
+                reinterpret_cast<uint4 *>(p.out + (int64_t)s * p.num_heads * D)[i] = make_uint4(0, 0, 0, 0);
+    }
 
     // ---- pieces, some in hold: their outputs stay apart until a barrier for all ----
     const int g = lane >> 2, t = lane & 3;
@@ -697,22 +716,33 @@ __global__ void __launch_bounds__(kTeamJoinThreads) team_join_kernel(const __gri
     grid_dependency_wait();
     launch_dependents();
     const int c = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // A warp's part i: CTA c's last piece, then the first pieces of the CTAs behind it.
+    float2 x;
+    float y[kPer];
+    auto load = [&](int i) {
+        const int64_t part = ((int64_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * p.group + h;
+        x = p.part_ml[part];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) y[k] = p.part_o[part * D + k * 32 + lane];
+    };
+    // The first ones are loaded along with what tells whether they are any.
+    const bool in = c + warp < (int)gridDim.x;
+    if (in) load(warp);
     const int seg = p.cut[c].y;
+    int i = c + 1 + (int)threadIdx.x;
+    int more = i < (int)gridDim.x ? p.cut[i].x : -1;
     if (seg < 0) return;
-    int parts = 1;  // CTA c's, then the CTAs whose first piece is the same segment's
-    for (int first = c + 1; first < (int)gridDim.x; first += kTeamJoinThreads) {
-        const int i = first + (int)threadIdx.x;
-        const int more = __syncthreads_count(i < (int)gridDim.x && p.cut[i].x == seg);
-        parts += more;
-        if (more < kTeamJoinThreads) break;
+    int parts = 1;
+    while (true) {
+        const int n = __syncthreads_count(more == seg);
+        parts += n;
+        if (n < kTeamJoinThreads) break;
+        i += kTeamJoinThreads;
+        more = i < (int)gridDim.x ? p.cut[i].x : -1;
     }
     float top = -CUDART_INF_F, l = 0.f, o[kPer] = {};
     for (int i = warp; i < parts; i += kWarps) {
-        const int64_t part = ((int64_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * p.group + h;
-        const float2 x = p.part_ml[part];
-        float y[kPer];
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) y[k] = p.part_o[part * D + k * 32 + lane];
+        if (i != warp) load(i);
         const float to = fmaxf(top, x.x), ref = to == -CUDART_INF_F ? 0.f : to;
         const float f = team_exp2(top - ref), fx = team_exp2(x.x - ref);
         top = to;
