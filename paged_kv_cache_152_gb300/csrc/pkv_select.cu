@@ -37,8 +37,9 @@ constexpr int kTileBlocks = 16;                 // of a warp's product
 constexpr int kCtaBlocks = kWarps * kTileBlocks;
 // A product of 2 D terms in the tensor cores: an instruction adds 16 products to
 // the sum, each cut at 2^-23 of the largest or finer, so 17 x 2^-23 of the terms'
-// magnitudes, and at most 16 instructions follow one another: 2^-14.9.
-constexpr float kScoreError = 6.103515625e-5f;  // 2^-14
+// magnitudes, and at most 8 instructions follow one another in each of two sums,
+// which are added at the end: 2^-15.9 of the magnitudes of both, and 2^-24.
+constexpr float kScoreError = 2.2e-5f;  // 2^-15.5
 constexpr float kNoNumber = FLT_MAX;            // the score of a block whose product is not finite
 
 struct SelectParams {
@@ -153,48 +154,7 @@ __global__ void __launch_bounds__(kThreads) select_score_kernel(const __grid_con
     if (lane == 0) p.reach[(seg * p.row + b0) / kTileBlocks] = reach;
 }
 
-// ---- a CTA's sums, maxima and places ----
-
-__device__ __forceinline__ int cta_sum(int v, int *scratch) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kFullMask, v, d);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int sum = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += scratch[w];
-    return sum;
-}
-
-__device__ __forceinline__ float cta_max(float v, float *scratch) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, d));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float top = scratch[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, scratch[w]);
-    return top;
-}
-
-// Threads with a true flag before this one, and how many there are.
-__device__ __forceinline__ int cta_place(bool flag, int *scratch, int *total) {
-    const unsigned mask = __ballot_sync(kFullMask, flag);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __syncthreads();
-    if (lane == 0) scratch[warp] = __popc(mask);
-    __syncthreads();
-    int before = 0, sum = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += scratch[w];
-        sum += scratch[w];
-    }
-    *total = sum;
-    return before + __popc(mask & ((1u << lane) - 1));
-}
+// ---- the blocks kept ----
 
 // Keys in the order of the values.
 __device__ __forceinline__ uint32_t order32(float v) {
@@ -209,9 +169,34 @@ __device__ __forceinline__ uint64_t order64(double v) {
     return b ^ ((b >> 63) ? ~0ull : 1ull << 63);
 }
 
-constexpr int kBins = 1024;
-constexpr int kList = 256;     // candidates ranked in one step
-constexpr int kCached = 8192;  // scores kept in shared memory
+constexpr int kKeepThreads = 128;
+constexpr int kKeepWarps = kKeepThreads / 32;
+constexpr int kList = 128;  // candidates ranked in one step
+
+struct KeepScratch {
+    int sums[2][kKeepWarps][4];  // two sets in turn, so that a sum takes one barrier
+    int list[kList];
+    double list64[kList];
+    int keep[kList];
+    int list_n;
+};
+
+// Sums over the CTA of four counts, the same on all threads; `turn` alternates.
+__device__ __forceinline__ int4 cta_sums(int4 v, KeepScratch &sh, int &turn) {
+    v.x = __reduce_add_sync(kFullMask, v.x);
+    v.y = __reduce_add_sync(kFullMask, v.y);
+    v.z = __reduce_add_sync(kFullMask, v.z);
+    if ((threadIdx.x & 31) == 0) *reinterpret_cast<int4 *>(sh.sums[turn][threadIdx.x >> 5]) = v;
+    __syncthreads();
+    int4 sum = make_int4(0, 0, 0, 0);
+#pragma unroll
+    for (int w = 0; w < kKeepWarps; ++w) {
+        const int4 x = *reinterpret_cast<const int4 *>(sh.sums[turn][w]);
+        sum.x += x.x, sum.y += x.y, sum.z += x.z;
+    }
+    turn ^= 1;
+    return sum;
+}
 
 // The block's score in 64 bits, by a warp (the same on all lanes).
 template <int D>
@@ -226,9 +211,10 @@ __device__ double exact_score(const SelectParams &p, int s, int kvh, int64_t blo
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
             const int i = k * 32 + lane;
-            const double v = __half2float(q[i]);
-            sum += fmax(v, 0.0) * (double)__half2float(hi[i]) + fmin(v, 0.0) * (double)__half2float(hi[D + i]);
-            if (v != v) sum = CUDART_NAN;
+            const float v = __half2float(q[i]);
+            // one of the two products is zero (or not a number, with a bound that is not finite): in fp32 each is exact
+            const float a = fmaxf(v, 0.f) * __half2float(hi[i]), b = fminf(v, 0.f) * __half2float(hi[D + i]);
+            sum += (double)(v == v ? a + b : CUDART_NAN_F);
         }
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
@@ -237,16 +223,100 @@ __device__ double exact_score(const SelectParams &p, int s, int kvh, int64_t blo
     return best;
 }
 
-// A CTA per (sequence, KV head).
+// Twice the error bound of a row's fp32 scores, partly: the largest |bound| of this thread's tiles and the largest
+// sum of |q| of this warp's heads.
 template <int D>
-__global__ void __launch_bounds__(kThreads) select_keep_kernel(const __grid_constant__ SelectParams p) {
-    __shared__ float cached[kCached];
-    __shared__ int bins[kBins];
-    __shared__ int scratch[kWarps];
-    __shared__ float scratch_f[kWarps];
-    __shared__ int list[kList];
-    __shared__ double list64[kList];
-    __shared__ int list_n, edge[2];
+__device__ __forceinline__ float2 keep_bound(const SelectParams &p, int s, int kvh, int64_t seg, int count) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float size = 0.f, norm = 0.f;
+    for (int i = tid; i < (count + kTileBlocks - 1) / kTileBlocks; i += kKeepThreads)
+        size = fmaxf(size, p.reach[seg * p.row / kTileBlocks + i]);
+    for (int h = warp; h < p.group; h += kKeepWarps) {
+        const __half2 *q = reinterpret_cast<const __half2 *>(
+            p.query + ((int64_t)s * p.num_heads + (int64_t)kvh * p.group + h) * D);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            const float2 v = __half22float2(q[i * 32 + lane]);
+            sum += fminf(fabsf(v.x), 65504.f) + fminf(fabsf(v.y), 65504.f);
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
+        norm = fmaxf(norm, sum);
+    }
+    return make_float2(size, norm);
+}
+
+// Any number of blocks, and any number of them alike: the scores stay in global memory.  Marks what is kept of the
+// border by infinities and returns the score above which (`all_near`: from which on) blocks are kept.
+template <int D>
+__device__ float keep_slowly(const SelectParams &p, KeepScratch &sh, int &turn, int s, int kvh, int64_t seg, int m0, int m,
+                             int need, float twice, bool *all_near) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float *score = p.score + seg * p.row + m0;
+    uint32_t top = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t trial = top | 1u << bit;
+        int n = 0;
+        for (int i = tid; i < m; i += kKeepThreads) n += order32(score[i]) >= trial;
+        if (cta_sums(make_int4(n, 0, 0, 0), sh, turn).x >= need) top = trial;
+    }
+    const float last = unorder32(top);
+    auto close = [&](float v) { return v <= last + twice && v >= last - twice; };
+    int above = 0, near = 0;
+    for (int i = tid; i < m; i += kKeepThreads) {
+        above += score[i] > last + twice;
+        near += close(score[i]);
+    }
+    const int4 sums = cta_sums(make_int4(above, near, 0, 0), sh, turn);
+    const int want = need - sums.x;
+    *all_near = want == sums.y;
+    if (*all_near) return last - twice;
+    double *exact = p.score64 + seg * p.row;
+    for (int64_t i = warp; i < m; i += kKeepWarps)
+        if (close(score[i])) {
+            const double e = exact_score<D>(p, s, kvh, m0 + i, lane);
+            if (lane == 0) exact[i] = e;
+        }
+    __syncthreads();
+    uint64_t key = 0;
+    for (int bit = 63; bit >= 0; --bit) {
+        const uint64_t trial = key | 1ull << bit;
+        int n = 0;
+        for (int i = tid; i < m; i += kKeepThreads)
+            if (close(score[i])) n += order64(exact[i]) >= trial;
+        if (cta_sums(make_int4(n, 0, 0, 0), sh, turn).x >= want) key = trial;
+    }
+    int more = 0;  // above the border's value; the first of its equals fill up
+    for (int i = tid; i < m; i += kKeepThreads)
+        if (close(score[i])) more += order64(exact[i]) > key;
+    int ties = want - cta_sums(make_int4(more, 0, 0, 0), sh, turn).x;
+    for (int base = 0; base < m; base += kKeepThreads) {
+        const int i = base + tid;
+        const bool mine = i < m && close(score[i]);
+        const uint64_t e = mine ? order64(exact[i]) : 0;
+        const unsigned mask = __ballot_sync(kFullMask, mine && e == key);
+        if (lane == 0) sh.sums[turn][warp][0] = __popc(mask);
+        __syncthreads();
+        int place = __popc(mask & ((1u << lane) - 1)), total = 0;
+        for (int w = 0; w < kKeepWarps; ++w) {
+            if (w < warp) place += sh.sums[turn][w][0];
+            total += sh.sums[turn][w][0];
+        }
+        turn ^= 1;
+        if (mine) score[i] = e > key || (e == key && place < ties) ? CUDART_INF_F : -CUDART_INF_F;
+        ties -= min(ties, total);
+    }
+    __syncthreads();
+    return last + twice;
+}
+
+// A CTA per (sequence, KV head).  Thread t holds the scores t, t + 128, ... of up to VALUES * 128 blocks (VALUES 0:
+// any number, in global memory); the need-th largest is found two bits of its key at a time.
+template <int D, int VALUES>
+__global__ void __launch_bounds__(kKeepThreads) select_keep_kernel(const __grid_constant__ SelectParams p) {
+    __shared__ __align__(16) KeepScratch sh;
+    __shared__ int4 places[VALUES < 1 ? 1 : VALUES];
     grid_dependency_wait();
     launch_dependents();
     const int s = blockIdx.y, kvh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -257,189 +327,166 @@ __global__ void __launch_bounds__(kThreads) select_keep_kernel(const __grid_cons
     const int kept = min(count, p.max_selected);
     if (tid == 0) p.num_selected[seg] = kept;
     if (count <= p.max_selected) {
-        for (int i = tid; i < p.max_selected; i += kThreads) out[i] = i < count ? i : -1;
+        for (int i = tid; i < p.max_selected; i += kKeepThreads) out[i] = i < count ? i : -1;
         return;
     }
     // Always kept: the first and the last; `need` of the m blocks between.
     const int m0 = p.first_blocks, m = count - p.first_blocks - p.last_blocks;
     const int need = kept - p.first_blocks - p.last_blocks;
-    float *score = p.score + seg * p.row + m0;
-    if (m <= kCached) {
-        for (int i = tid; i < m; i += kThreads) cached[i] = score[i];
-        score = cached;
-    }
-    // ---- E: the error bound of this row's scores ----
-    float size = 0.f, norm = 0.f;
-    for (int i = tid; i < (count + kTileBlocks - 1) / kTileBlocks; i += kThreads)
-        size = fmaxf(size, p.reach[seg * p.row / kTileBlocks + i]);
-    for (int h = warp; h < p.group; h += kWarps) {
-        const __half *q = p.query + ((int64_t)s * p.num_heads + (int64_t)kvh * p.group + h) * D;
-        float sum = 0.f;
-        for (int i = lane; i < D; i += 32) sum += fminf(fabsf(__half2float(q[i])), 65504.f);
+    for (int i = tid; i < m0; i += kKeepThreads) out[i] = i;
+    for (int i = tid; i < p.last_blocks; i += kKeepThreads) out[kept - p.last_blocks + i] = count - p.last_blocks + i;
+    if (need == 0) return;
+    int turn = 0;
+    if (tid == 0) sh.list_n = 0;
+
+    float v[VALUES < 1 ? 1 : VALUES];
 #pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
-        norm = fmaxf(norm, sum);
+    for (int j = 0; j < VALUES; ++j) {
+        const int i = j * kKeepThreads + tid;
+        v[j] = i < m ? p.score[seg * p.row + m0 + i] : -CUDART_INF_F;  // not finite: none
     }
-    size = cta_max(size, scratch_f);
-    norm = cta_max(norm, scratch_f);
+    // the row's error bound, and the keys' leading bits that are all alike
+    uint32_t high = 0, low = 0xffffffffu;
+#pragma unroll
+    for (int j = 0; j < VALUES; ++j)
+        if (j * kKeepThreads + tid < m) {
+            high = max(high, order32(v[j]));
+            low = min(low, order32(v[j]));
+        }
+    {
+        const float2 part = keep_bound<D>(p, s, kvh, seg, count);
+        const int4 mine = make_int4((int)__reduce_max_sync(kFullMask, __float_as_uint(part.x)), __float_as_int(part.y),
+                                    (int)__reduce_max_sync(kFullMask, high), (int)__reduce_min_sync(kFullMask, low));
+        if (lane == 0) *reinterpret_cast<int4 *>(sh.sums[turn][warp]) = mine;
+    }
+    __syncthreads();
+    float size = 0.f, norm = 0.f;
+#pragma unroll
+    for (int w = 0; w < kKeepWarps; ++w) {
+        const int4 x = *reinterpret_cast<const int4 *>(sh.sums[turn][w]);
+        size = fmaxf(size, __int_as_float(x.x));
+        norm = fmaxf(norm, __int_as_float(x.y));
+        high = max(high, (uint32_t)x.z);
+        low = min(low, (uint32_t)x.w);
+    }
+    turn ^= 1;
     const float twice = 2.f * kScoreError * size * norm;
 
-    // ---- the need-th largest fp32 score ----
-    float last = CUDART_INF_F;
     bool all_near = false;
-    if (need > 0) {
-        // A histogram over the finite scores' range finds its bin.
-        float top = -CUDART_INF_F, low = -CUDART_INF_F;  // low: of the negated scores
-        for (int i = tid; i < m; i += kThreads) {
-            const float v = score[i];
-            low = fmaxf(low, -v);
-            if (v < kNoNumber) top = fmaxf(top, v);
-        }
-        top = cta_max(top, scratch_f);
-        low = -cta_max(low, scratch_f);
-        const float per = top > low ? (float)(kBins - 2) / (top - low) : 0.f;
-        for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
-        if (tid == 0) list_n = 0;
-        __syncthreads();
-        auto bin_of = [&](float v) { return v < kNoNumber ? min((int)((v - low) * per), kBins - 2) : kBins - 1; };
-        for (int i = tid; i < m; i += kThreads) atomicAdd(bins + bin_of(score[i]), 1);
-        __syncthreads();
-        if (warp == 0) {  // from the top: the bin in which the count passes `need`
-            int above = 0;
-            for (int base = kBins - 32; base >= 0; base -= 32) {
-                const int n = bins[base + 31 - lane];
-                int sum = n;
+    float bar;  // what is above it is kept (all_near: from it on)
+    if constexpr (VALUES > 0) {
+        // ---- the need-th largest key ----
+        const int same = __clz(high ^ low) & ~1;  // leading bits, an even number (32: all)
+        uint32_t key = same == 0 ? 0 : high & ~(uint32_t)((1ull << (32 - same)) - 1);
+        for (int bit = 30 - same; bit >= 0; bit -= 2) {
+            const uint32_t one = key + (1u << bit), two = key + (2u << bit), three = key + (3u << bit);
+            int4 n = make_int4(0, 0, 0, 0);
 #pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int v = __shfl_up_sync(kFullMask, sum, d);
-                    if (lane >= d) sum += v;
-                }
-                const unsigned hit = __ballot_sync(kFullMask, above + sum >= need);
-                if (hit) {
-                    const int l = __ffs(hit) - 1;
-                    if (lane == l) edge[0] = base + 31 - l, edge[1] = above + sum - n;
-                    break;
-                }
-                above += __shfl_sync(kFullMask, sum, 31);
+            for (int j = 0; j < VALUES; ++j) {
+                const uint32_t k = order32(v[j]);
+                n.x += k >= one;
+                n.y += k >= two;
+                n.z += k >= three;
             }
+            n = cta_sums(n, sh, turn);
+            key = n.z >= need ? three : n.y >= need ? two : n.x >= need ? one : key;
+        }
+        const float last = unorder32(key);
+        // ---- the blocks about the border ----
+        int4 n = make_int4(0, 0, 0, 0);
+        uint32_t close = 0;
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j) {
+            n.x += v[j] > last + twice;
+            if (v[j] <= last + twice && v[j] >= last - twice) close |= 1u << j;
+        }
+        const int closes = __popc(close);
+        n.y = closes;
+        n = cta_sums(n, sh, turn);
+        const int want = need - n.x;
+        all_near = want == n.y;
+        bar = all_near ? last - twice : last + twice;
+        if (!all_near && n.y <= kList) {
+            const int at = closes ? atomicAdd(&sh.list_n, closes) : 0;
+            int k = at;
+#pragma unroll
+            for (int j = 0; j < VALUES; ++j)
+                if (close >> j & 1) sh.list[k++] = j * kKeepThreads + tid;
+            __syncthreads();
+            for (int i = warp; i < n.y; i += kKeepWarps) {
+                const double e = exact_score<D>(p, s, kvh, m0 + sh.list[i], lane);
+                if (lane == 0) sh.list64[i] = e;
+            }
+            __syncthreads();
+            if (tid < n.y) {
+                const int mine = sh.list[tid];
+                const double e = sh.list64[tid];
+                int before = 0;
+                for (int j = 0; j < n.y; ++j)
+                    before += sh.list64[j] > e || (sh.list64[j] == e && sh.list[j] < mine);
+                sh.keep[tid] = before < want;
+            }
+            __syncthreads();
+            k = at;
+#pragma unroll
+            for (int j = 0; j < VALUES; ++j)
+                if (close >> j & 1) v[j] = sh.keep[k++] ? CUDART_INF_F : -CUDART_INF_F;
+        } else if (!all_near) {
+            bar = keep_slowly<D>(p, sh, turn, s, kvh, seg, m0, m, need, twice, &all_near);
+#pragma unroll
+            for (int j = 0; j < VALUES; ++j) {
+                const int i = j * kKeepThreads + tid;
+                if (i < m) v[j] = p.score[seg * p.row + m0 + i];
+            }
+        }
+        // ---- the list, in ascending order ----
+        uint32_t chosen = 0;
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j) {
+            const bool keep = all_near ? v[j] >= bar : v[j] > bar;
+            const unsigned mask = __ballot_sync(kFullMask, keep);
+            if (lane == 0) reinterpret_cast<int *>(places + j)[warp] = __popc(mask);
+            if (keep) chosen |= 1u << j;
         }
         __syncthreads();
-        const int bin = edge[0], rank = need - edge[1], inside = bins[bin];  // the rank-th of the bin, from 1
-        if (inside <= kList) {
-            for (int i = tid; i < m; i += kThreads)
-                if (bin_of(score[i]) == bin) list[atomicAdd(&list_n, 1)] = i;
-            __syncthreads();
-            if (tid < inside) {
-                const float v = score[list[tid]];
-                int above = 0, same = 0;
-                for (int j = 0; j < inside; ++j) {
-                    const float u = score[list[j]];
-                    above += u > v;
-                    same += u == v;
-                }
-                if (above < rank && rank <= above + same) scratch_f[0] = v;  // equal values write the same
-            }
-            __syncthreads();
-            last = scratch_f[0];
-            __syncthreads();
-        } else {  // many alike: its bits one by one
-            uint32_t key = 0;
-            for (int bit = 31; bit >= 0; --bit) {
-                const uint32_t trial = key | 1u << bit;
-                int n = 0;
-                for (int i = tid; i < m; i += kThreads) n += order32(score[i]) >= trial;
-                if (cta_sum(n, scratch) >= need) key = trial;
-            }
-            last = unorder32(key);
+        int base = m0;
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j) {
+            const int4 x = places[j];
+            const unsigned mask = __ballot_sync(kFullMask, chosen >> j & 1);
+            const int at = base + (warp > 0 ? x.x : 0) + (warp > 1 ? x.y : 0) + (warp > 2 ? x.z : 0) +
+                           __popc(mask & ((1u << lane) - 1));
+            if (chosen >> j & 1) out[at] = m0 + j * kKeepThreads + tid;
+            base += x.x + x.y + x.z + x.w;
         }
+    } else {
+        bar = keep_slowly<D>(p, sh, turn, s, kvh, seg, m0, m, need, twice, &all_near);
+        int base = m0;
+        for (int first = 0; first < m; first += kKeepThreads) {
+            const int i = first + tid;
+            const float x = i < m ? p.score[seg * p.row + m0 + i] : -CUDART_INF_F;
+            const bool keep = all_near ? x >= bar : x > bar;
+            const unsigned mask = __ballot_sync(kFullMask, keep);
+            if (lane == 0) sh.sums[turn][warp][0] = __popc(mask);
+            __syncthreads();
+            int at = base + __popc(mask & ((1u << lane) - 1));
+            for (int w = 0; w < kKeepWarps; ++w) {
+                if (w < warp) at += sh.sums[turn][w][0];
+                base += sh.sums[turn][w][0];
+            }
+            turn ^= 1;
+            if (keep) out[at] = m0 + i;
+        }
+    }
+}
 
-        // ---- the blocks about the border ----
-        int above = 0, near = 0;
-        if (tid == 0) list_n = 0;
-        for (int i = tid; i < m; i += kThreads) {
-            const float v = score[i];
-            above += v > last + twice;
-            near += v <= last + twice && v >= last - twice;
-        }
-        above = cta_sum(above, scratch);
-        near = cta_sum(near, scratch);
-        const int want = need - above;  // of the `near` ones
-        if (want < near) {
-            if (near <= kList) {
-                for (int i = tid; i < m; i += kThreads) {
-                    const float v = score[i];
-                    if (v <= last + twice && v >= last - twice) list[atomicAdd(&list_n, 1)] = i;
-                }
-                __syncthreads();
-                for (int i = warp; i < near; i += kWarps) {
-                    const double v = exact_score<D>(p, s, kvh, m0 + list[i], lane);
-                    if (lane == 0) list64[i] = v;
-                }
-                __syncthreads();
-                int mine = -1, before = 0;
-                if (tid < near) {
-                    mine = list[tid];
-                    const double v = list64[tid];
-                    for (int j = 0; j < near; ++j)
-                        before += list64[j] > v || (list64[j] == v && list[j] < mine);
-                }
-                __syncthreads();
-                if (mine >= 0) score[mine] = before < want ? CUDART_INF_F : -CUDART_INF_F;
-            } else {
-                double *exact = p.score64 + seg * p.row;
-                for (int64_t i = warp; i < m; i += kWarps) {
-                    const float v = score[i];
-                    if (v <= last + twice && v >= last - twice) {
-                        const double e = exact_score<D>(p, s, kvh, m0 + i, lane);
-                        if (lane == 0) exact[i] = e;
-                    }
-                }
-                __syncthreads();
-                uint64_t key = 0;
-                for (int bit = 63; bit >= 0; --bit) {
-                    const uint64_t trial = key | 1ull << bit;
-                    int n = 0;
-                    for (int i = tid; i < m; i += kThreads) {
-                        const float v = score[i];
-                        if (v <= last + twice && v >= last - twice) n += order64(exact[i]) >= trial;
-                    }
-                    if (cta_sum(n, scratch) >= want) key = trial;
-                }
-                int more = 0;  // above the border's value; the first of its equals fill up
-                for (int i = tid; i < m; i += kThreads) {
-                    const float v = score[i];
-                    if (v <= last + twice && v >= last - twice) more += order64(exact[i]) > key;
-                }
-                int ties = want - cta_sum(more, scratch);
-                for (int base = 0; base < m; base += kThreads) {
-                    const int i = base + tid;
-                    const float v = i < m ? score[i] : 0.f;
-                    const bool close = i < m && v <= last + twice && v >= last - twice;
-                    const uint64_t e = close ? order64(exact[i]) : 0;
-                    int total;
-                    const int place = cta_place(close && e == key, scratch, &total);
-                    if (close) score[i] = e > key || (e == key && place < ties) ? CUDART_INF_F : -CUDART_INF_F;
-                    ties -= min(ties, total);
-                }
-            }
-            __syncthreads();
-        }
-        all_near = want == near;
-    }
-    // ---- the list, in ascending order ----
-    // (where not all of the border's blocks are kept, infinities mark which are)
-    const float bar = all_near ? last - twice : last + twice;
-    int at = m0;
-    for (int i = tid; i < m0; i += kThreads) out[i] = i;
-    for (int base = 0; base < m; base += kThreads) {
-        const int i = base + tid;
-        const bool keep = i < m && (all_near ? score[i] >= bar : score[i] > bar);
-        int total;
-        const int place = cta_place(keep, scratch, &total);
-        if (keep) out[at + place] = m0 + i;
-        at += total;
-    }
-    for (int i = tid; i < p.last_blocks; i += kThreads) out[kept - p.last_blocks + i] = count - p.last_blocks + i;
+template <int D>
+const void *keep_kernel(int max_blocks) {
+    return max_blocks <= 4 * kKeepThreads    ? reinterpret_cast<const void *>(&select_keep_kernel<D, 4>)
+           : max_blocks <= 8 * kKeepThreads  ? reinterpret_cast<const void *>(&select_keep_kernel<D, 8>)
+           : max_blocks <= 16 * kKeepThreads ? reinterpret_cast<const void *>(&select_keep_kernel<D, 16>)
+           : max_blocks <= 32 * kKeepThreads ? reinterpret_cast<const void *>(&select_keep_kernel<D, 32>)
+                                             : reinterpret_cast<const void *>(&select_keep_kernel<D, 0>);
 }
 
 // Workspace carve-up (byte offsets).  It carries nothing from call to call.
@@ -532,9 +579,8 @@ extern "C" int pkv_select_blocks(int32_t *selected, int32_t *num_selected, const
         cudaGetLastError();
         return PKV_ERR_CUDA;
     }
-    fn = d64 ? reinterpret_cast<const void *>(&select_keep_kernel<64>)
-             : reinterpret_cast<const void *>(&select_keep_kernel<128>);
-    if (launch_pdl(fn, dim3((unsigned)num_kv_heads, (unsigned)num_seqs), dim3(kThreads), 0, stream, args) !=
+    fn = d64 ? keep_kernel<64>(max_blocks_per_seq) : keep_kernel<128>(max_blocks_per_seq);
+    if (launch_pdl(fn, dim3((unsigned)num_kv_heads, (unsigned)num_seqs), dim3(kKeepThreads), 0, stream, args) !=
         cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
