@@ -9,13 +9,17 @@
 // lo) with (max(q, 0), min(q, 0)), on the tensor cores.  A block's score is the
 // largest over its KV head's query heads.
 //
-// First kernel: the scores in fp32, bound by HBM (4 D bytes per block and head are
-// read once, straight into the fragments: the products' inner index is taken in
-// the order that 16-byte loads bring it).  Second kernel, a CTA per (sequence, KV
-// head): the blocks kept.  fp32 scores are off by E or less (below), so blocks
-// more than 2 E above the last kept score are kept and those more than 2 E below
-// it are not; the few between are scored again in 64 bits and ranked, ties to the
-// lowest index, so that the choice does not hang on the order of a sum.
+// The scores are fp32 sums, bound by HBM (4 D bytes per block and head are read
+// once, straight into the fragments: the products' inner index is taken in the
+// order that 16-byte loads bring it) where there is much of them, and by latency
+// where there is little: so one kernel does both parts, a cluster of CTAs per
+// (sequence, KV head), and the scores never leave shared memory.  (Contexts of more
+// than 4096 blocks take two kernels, with the scores in global memory.)
+//
+// The choice: fp32 scores are off by E or less (below), so blocks more than 2 E
+// above the last kept score are kept and those more than 2 E below it are not; the
+// few between are scored again with twice the digits and ranked, ties to the lowest
+// index, so that the choice does not hang on the order of a sum.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
@@ -32,9 +36,7 @@ namespace {
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxGroup = 16;
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kTileBlocks = 16;                 // of a warp's product
-constexpr int kCtaBlocks = kWarps * kTileBlocks;
 // A product of 2 D terms in the tensor cores: an instruction adds 16 products to
 // the sum, each cut at 2^-23 of the largest or finer, so 17 x 2^-23 of the terms'
 // magnitudes, and at most 8 instructions follow one another in each of two sums,
@@ -72,29 +74,48 @@ __device__ __forceinline__ int select_blocks_of(const SelectParams &p, int s, bo
     return (len + (1 << p.block_shift) - 1) >> p.block_shift;
 }
 
+// The fragments of a KV head's queries: 16 bytes of head n * 8 + g at each of the
+// places that a lane's loads of a block's bounds cover, with max(q, 0) for the
+// first half of the loads, which are hi, and min(q, 0) for the others.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) select_score_kernel(const __grid_constant__ SelectParams p) {
-    constexpr int kLoads = 4 * D / 64;  // 64 bytes of a row per load of four lanes
-    grid_dependency_wait();
-    launch_dependents();
-    const int s = blockIdx.z, kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, t = lane & 3;
-    bool bad;
-    const int count = select_blocks_of(p, s, &bad);
-    if (bad && blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
-    const int64_t b0 = (int64_t)blockIdx.x * kCtaBlocks + warp * kTileBlocks;
-    if (b0 >= count || count <= p.max_selected) return;
+struct SelectQueries {
+    static constexpr int kLoads = 4 * D / 64;  // 64 bytes of a row per load of four lanes
+    uint4 q[NT][kLoads];
 
+    __device__ __forceinline__ void load(const SelectParams &p, int64_t seg, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+        const __half *rows = p.query + seg * p.group * D;
+        const __half2 zero = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < kLoads / 2; ++i) {
+                uint4 raw = make_uint4(0, 0, 0, 0);
+                if (n * 8 + g < p.group)
+                    raw = __ldg(reinterpret_cast<const uint4 *>(rows + (n * 8 + g) * D + (i * 4 + t) * 8));
+                q[n][i] = q[n][i + kLoads / 2] = raw;
+                __half2 *up = reinterpret_cast<__half2 *>(&q[n][i]);
+                __half2 *down = reinterpret_cast<__half2 *>(&q[n][i + kLoads / 2]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    up[k] = __hmax2_nan(up[k], zero);
+                    down[k] = __hmin2_nan(down[k], zero);
+                }
+            }
+    }
+};
+
+// Scores 16 blocks, by a warp: best[r] is that of row g + 8 r (on all four lanes of the row), reach the largest finite
+// |bound| (on all lanes).  phys: this lane's rows' physical blocks.
+template <int D, int NT>
+__device__ __forceinline__ void score_tile(const SelectParams &p, const SelectQueries<D, NT> &queries, const int (&phys)[2],
+                                           int kvh, int lane, float (&best)[2], float &reach) {
+    constexpr int kLoads = SelectQueries<D, NT>::kLoads;
+    const int t = lane & 3;
     uint4 x[2][kLoads];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        const int64_t block = min(b0 + g + 8 * r, (int64_t)count - 1);  // a row past the end repeats the last
-        int phys = __ldg(p.block_tables + (int64_t)s * p.max_blocks_per_seq + block);
-        if (phys < 0 || phys >= p.num_blocks) {
-            if (t == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
-            phys = 0;
-        }
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + ((int64_t)phys * p.num_kv_heads + kvh) * 2 * D);
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + ((int64_t)phys[r] * p.num_kv_heads + kvh) * 2 * D);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) x[r][i] = __ldg(src + i * 4 + t);
     }
@@ -103,25 +124,16 @@ __global__ void __launch_bounds__(kThreads) select_score_kernel(const __grid_con
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) acc[n][c][0] = acc[n][c][1] = acc[n][c][2] = acc[n][c][3] = 0.f;
-    const __half *q = p.query + ((int64_t)s * p.num_heads + (int64_t)kvh * p.group) * D;
-    const __half2 zero = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        // the first half of the loads are hi, for max(q, 0), the others lo, for min(q, 0)
-        const int dim = (i * 4 + t) * 8 - (i < kLoads / 2 ? 0 : D);
+    for (int i = 0; i < kLoads; ++i)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (n * 8 + g < p.group) raw = __ldg(reinterpret_cast<const uint4 *>(q + (n * 8 + g) * D + dim));
-            __half2 *h = reinterpret_cast<__half2 *>(&raw);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) h[k] = i < kLoads / 2 ? __hmax2_nan(h[k], zero) : __hmin2_nan(h[k], zero);
-            mma_16816(acc[n][0], x[0][i].x, x[1][i].x, x[0][i].y, x[1][i].y, raw.x, raw.y);
-            mma_16816(acc[n][1], x[0][i].z, x[1][i].z, x[0][i].w, x[1][i].w, raw.z, raw.w);
+            const uint4 q = queries.q[n][i];
+            mma_16816(acc[n][0], x[0][i].x, x[1][i].x, x[0][i].y, x[1][i].y, q.x, q.y);
+            mma_16816(acc[n][1], x[0][i].z, x[1][i].z, x[0][i].w, x[1][i].w, q.z, q.w);
         }
-    }
-    // rows g and g + 8: the largest over the heads 2t, 2t + 1 (+ 8), then over t
-    float best[2] = {-CUDART_INF_F, -CUDART_INF_F};
+    // the largest over the heads 2t, 2t + 1 (+ 8), then over t
+    best[0] = best[1] = -CUDART_INF_F;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -134,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) select_score_kernel(const __grid_con
     for (int d = 1; d < 4; d <<= 1)
 #pragma unroll
         for (int r = 0; r < 2; ++r) best[r] = fmaxf(best[r], __shfl_xor_sync(kFullMask, best[r], d));
-    __half2 top = zero;
+    __half2 top = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -143,11 +155,38 @@ __global__ void __launch_bounds__(kThreads) select_score_kernel(const __grid_con
 #pragma unroll
             for (int k = 0; k < 4; ++k) top = __hmax2(top, __habs2(h[k]));  // a NaN gives way
         }
-    float reach = fminf(fmaxf(__low2float(top), __high2float(top)), 65504.f);
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) reach = fmaxf(reach, __shfl_xor_sync(kFullMask, reach, d));
+    const float most = fminf(fmaxf(__low2float(top), __high2float(top)), 65504.f);
+    reach = __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(most)));
+}
+
+// The physical block of block `block` (past the end: the last one's).
+__device__ __forceinline__ int select_phys(const SelectParams &p, int s, int64_t block, int count, bool first) {
+    int phys = __ldg(p.block_tables + (int64_t)s * p.max_blocks_per_seq + min(block, (int64_t)count - 1));
+    if (phys < 0 || phys >= p.num_blocks) {
+        if (first) report(p.status, PKV_ERR_OUT_OF_RANGE);
+        phys = 0;
+    }
+    return phys;
+}
+
+// Contexts of more blocks than the fused kernel holds: scores to global memory.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads) select_score_kernel(const __grid_constant__ SelectParams p) {
+    grid_dependency_wait();
+    launch_dependents();
+    const int s = blockIdx.z, kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
     const int64_t seg = (int64_t)s * p.num_kv_heads + kvh;
-    if (t == 0)
+    bool bad;
+    const int count = select_blocks_of(p, s, &bad);
+    if (bad && blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
+    const int64_t b0 = ((int64_t)blockIdx.x * (kThreads / 32) + warp) * kTileBlocks;
+    if (b0 >= count || count <= p.max_selected) return;
+    const int phys[2] = {select_phys(p, s, b0 + g, count, (lane & 3) == 0), select_phys(p, s, b0 + g + 8, count, (lane & 3) == 0)};
+    SelectQueries<D, NT> queries;
+    queries.load(p, seg, lane);
+    float best[2], reach;
+    score_tile<D, NT>(p, queries, phys, kvh, lane, best, reach);
+    if ((lane & 3) == 0)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
             if (b0 + g + 8 * r < count) p.score[seg * p.row + b0 + g + 8 * r] = best[r];
@@ -198,27 +237,46 @@ __device__ __forceinline__ int4 cta_sums(int4 v, KeepScratch &sh, int &turn) {
     return sum;
 }
 
-// The block's score in 64 bits, by a warp (the same on all lanes).
+// sum + low + x, with what rounding takes from the sum added to `low` (Knuth's two-sum).
+__device__ __forceinline__ void add_exactly(float &sum, float &low, float x) {
+    const float to = __fadd_rn(sum, x), part = __fsub_rn(to, sum);
+    low += __fadd_rn(__fsub_rn(sum, __fsub_rn(to, part)), __fsub_rn(x, part));
+    sum = to;
+}
+
+// The block's score as a sum of two fp32 values, off by 2^-44 of its terms' magnitudes at most, in 64 bits (the GPU has
+// few fp64 units); by a warp, lane 0's counts.
 template <int D>
 __device__ double exact_score(const SelectParams &p, int s, int kvh, int64_t block, int lane) {
     int phys = __ldg(p.block_tables + (int64_t)s * p.max_blocks_per_seq + block);
     if (phys < 0 || phys >= p.num_blocks) phys = 0;
     const __half *hi = p.bounds + ((int64_t)phys * p.num_kv_heads + kvh) * 2 * D;
     double best = -CUDART_INF;
+    float bounds[2][D / 32];
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+        bounds[0][k] = __half2float(hi[k * 32 + lane]);
+        bounds[1][k] = __half2float(hi[D + k * 32 + lane]);
+    }
+#pragma unroll 4
     for (int h = 0; h < p.group; ++h) {
         const __half *q = p.query + ((int64_t)s * p.num_heads + (int64_t)kvh * p.group + h) * D;
-        double sum = 0;
+        float sum = 0.f, low = 0.f;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
-            const int i = k * 32 + lane;
-            const float v = __half2float(q[i]);
-            // one of the two products is zero (or not a number, with a bound that is not finite): in fp32 each is exact
-            const float a = fmaxf(v, 0.f) * __half2float(hi[i]), b = fminf(v, 0.f) * __half2float(hi[D + i]);
-            sum += (double)(v == v ? a + b : CUDART_NAN_F);
+            const float v = __half2float(q[k * 32 + lane]);
+            // one of the two products is zero (or not a number, with a bound that is not finite); fp32 holds them exactly
+            const float a = fmaxf(v, 0.f) * bounds[0][k], b = fminf(v, 0.f) * bounds[1][k];
+            add_exactly(sum, low, v == v ? a + b : CUDART_NAN_F);
         }
 #pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
-        best = fmax(best, fabs(sum) < CUDART_INF ? sum : CUDART_INF);
+        for (int d = 16; d; d >>= 1) {
+            const float other = __shfl_xor_sync(kFullMask, sum, d), other_low = __shfl_xor_sync(kFullMask, low, d);
+            add_exactly(sum, low, other);
+            low += other_low;
+        }
+        const double e = (double)sum + (double)low;
+        best = fmax(best, fabs(e) < CUDART_INF ? e : CUDART_INF);
     }
     return best;
 }
@@ -226,11 +284,11 @@ __device__ double exact_score(const SelectParams &p, int s, int kvh, int64_t blo
 // Twice the error bound of a row's fp32 scores, partly: the largest |bound| of this thread's tiles and the largest
 // sum of |q| of this warp's heads.
 template <int D>
-__device__ __forceinline__ float2 keep_bound(const SelectParams &p, int s, int kvh, int64_t seg, int count) {
+__device__ __forceinline__ float2 keep_bound(const SelectParams &p, int s, int kvh, const float *reach, int count) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     float size = 0.f, norm = 0.f;
     for (int i = tid; i < (count + kTileBlocks - 1) / kTileBlocks; i += kKeepThreads)
-        size = fmaxf(size, p.reach[seg * p.row / kTileBlocks + i]);
+        size = fmaxf(size, reach[i]);
     for (int h = warp; h < p.group; h += kKeepWarps) {
         const __half2 *q = reinterpret_cast<const __half2 *>(
             p.query + ((int64_t)s * p.num_heads + (int64_t)kvh * p.group + h) * D);
@@ -311,25 +369,16 @@ __device__ float keep_slowly(const SelectParams &p, KeepScratch &sh, int &turn, 
     return last + twice;
 }
 
-// A CTA per (sequence, KV head).  Thread t holds the scores t, t + 128, ... of up to VALUES * 128 blocks (VALUES 0:
-// any number, in global memory); the need-th largest is found two bits of its key at a time.
+// A CTA keeps the blocks of one (sequence, KV head) of more than max_selected.  score, reach: its blocks' scores and its
+// tiles' reach; thread t holds the scores t, t + 128, ... of up to VALUES * 128 blocks (VALUES 0: any number, in global
+// memory).  The need-th largest is found two bits of its key at a time.
 template <int D, int VALUES>
-__global__ void __launch_bounds__(kKeepThreads) select_keep_kernel(const __grid_constant__ SelectParams p) {
-    __shared__ __align__(16) KeepScratch sh;
-    __shared__ int4 places[VALUES < 1 ? 1 : VALUES];
-    grid_dependency_wait();
-    launch_dependents();
-    const int s = blockIdx.y, kvh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+__device__ __forceinline__ void keep_blocks(const SelectParams &p, KeepScratch &sh, int4 *places, int s, int kvh, int count,
+                                            const float *score, const float *reach) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t seg = (int64_t)s * p.num_kv_heads + kvh;
     int32_t *out = p.selected + seg * p.max_selected;
-    bool bad;
-    const int count = select_blocks_of(p, s, &bad);
-    const int kept = min(count, p.max_selected);
-    if (tid == 0) p.num_selected[seg] = kept;
-    if (count <= p.max_selected) {
-        for (int i = tid; i < p.max_selected; i += kKeepThreads) out[i] = i < count ? i : -1;
-        return;
-    }
+    const int kept = p.max_selected;
     // Always kept: the first and the last; `need` of the m blocks between.
     const int m0 = p.first_blocks, m = count - p.first_blocks - p.last_blocks;
     const int need = kept - p.first_blocks - p.last_blocks;
@@ -343,7 +392,7 @@ __global__ void __launch_bounds__(kKeepThreads) select_keep_kernel(const __grid_
 #pragma unroll
     for (int j = 0; j < VALUES; ++j) {
         const int i = j * kKeepThreads + tid;
-        v[j] = i < m ? p.score[seg * p.row + m0 + i] : -CUDART_INF_F;  // not finite: none
+        v[j] = i < m ? score[m0 + i] : -CUDART_INF_F;
     }
     // the row's error bound, and the keys' leading bits that are all alike
     uint32_t high = 0, low = 0xffffffffu;
@@ -354,7 +403,7 @@ __global__ void __launch_bounds__(kKeepThreads) select_keep_kernel(const __grid_
             low = min(low, order32(v[j]));
         }
     {
-        const float2 part = keep_bound<D>(p, s, kvh, seg, count);
+        const float2 part = keep_bound<D>(p, s, kvh, reach, count);
         const int4 mine = make_int4((int)__reduce_max_sync(kFullMask, __float_as_uint(part.x)), __float_as_int(part.y),
                                     (int)__reduce_max_sync(kFullMask, high), (int)__reduce_min_sync(kFullMask, low));
         if (lane == 0) *reinterpret_cast<int4 *>(sh.sums[turn][warp]) = mine;
@@ -432,6 +481,12 @@ __global__ void __launch_bounds__(kKeepThreads) select_keep_kernel(const __grid_
             for (int j = 0; j < VALUES; ++j)
                 if (close >> j & 1) v[j] = sh.keep[k++] ? CUDART_INF_F : -CUDART_INF_F;
         } else if (!all_near) {
+#pragma unroll
+            for (int j = 0; j < VALUES; ++j) {
+                const int i = j * kKeepThreads + tid;
+                if (i < m) p.score[seg * p.row + m0 + i] = v[j];
+            }
+            __syncthreads();
             bar = keep_slowly<D>(p, sh, turn, s, kvh, seg, m0, m, need, twice, &all_near);
 #pragma unroll
             for (int j = 0; j < VALUES; ++j) {
@@ -480,13 +535,142 @@ __global__ void __launch_bounds__(kKeepThreads) select_keep_kernel(const __grid_
     }
 }
 
+// A sequence of at most max_selected blocks keeps all of them.
+__device__ __forceinline__ void keep_all(const SelectParams &p, int64_t seg, int count) {
+    for (int i = threadIdx.x; i < p.max_selected; i += kKeepThreads)
+        p.selected[seg * p.max_selected + i] = i < count ? i : -1;
+    if (threadIdx.x == 0) p.num_selected[seg] = count;
+}
+
 template <int D>
-const void *keep_kernel(int max_blocks) {
-    return max_blocks <= 4 * kKeepThreads    ? reinterpret_cast<const void *>(&select_keep_kernel<D, 4>)
-           : max_blocks <= 8 * kKeepThreads  ? reinterpret_cast<const void *>(&select_keep_kernel<D, 8>)
-           : max_blocks <= 16 * kKeepThreads ? reinterpret_cast<const void *>(&select_keep_kernel<D, 16>)
-           : max_blocks <= 32 * kKeepThreads ? reinterpret_cast<const void *>(&select_keep_kernel<D, 32>)
-                                             : reinterpret_cast<const void *>(&select_keep_kernel<D, 0>);
+__global__ void __launch_bounds__(kKeepThreads) select_keep_kernel(const __grid_constant__ SelectParams p) {
+    __shared__ __align__(16) KeepScratch sh;
+    grid_dependency_wait();
+    launch_dependents();
+    const int s = blockIdx.y, kvh = blockIdx.x;
+    const int64_t seg = (int64_t)s * p.num_kv_heads + kvh;
+    bool bad;
+    const int count = select_blocks_of(p, s, &bad);
+    if (count <= p.max_selected) {
+        keep_all(p, seg, count);
+        return;
+    }
+    if (threadIdx.x == 0) p.num_selected[seg] = p.max_selected;
+    keep_blocks<D, 0>(p, sh, nullptr, s, kvh, count, p.score + seg * p.row, p.reach + seg * p.row / kTileBlocks);
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Stores to the shared memory of the cluster's CTA 0.
+__device__ __forceinline__ void store_first(const float *at, float v) {
+    uint32_t to;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(smem_addr(at)));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
+}
+
+// A cluster of CTAs per (sequence, KV head) of up to VALUES * 128 blocks: its warps score 16 blocks in turn, the scores
+// meet in the first CTA's shared memory, which keeps the blocks.
+template <int D, int NT, int VALUES>
+__global__ void __launch_bounds__(kKeepThreads) select_fused_kernel(const __grid_constant__ SelectParams p) {
+    __shared__ __align__(16) KeepScratch sh;
+    __shared__ int4 places[VALUES];
+    __shared__ float scores[VALUES * kKeepThreads], reaches[VALUES * kKeepThreads / kTileBlocks];
+    uint32_t rank, ctas;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+    const int s = blockIdx.z, kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
+    const int64_t seg = (int64_t)s * p.num_kv_heads + kvh;
+    // asked into L2 while the kernel before still runs (nothing is read): the context, the table's row, the queries
+    if (rank == 0) {
+        if (threadIdx.x == 0) prefetch_l2(p.context_lens + s);
+        const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
+        if (kvh == 0)
+            for (int i = threadIdx.x * 32; i < p.max_blocks_per_seq; i += kKeepThreads * 32) prefetch_l2(row + i);
+        for (int i = threadIdx.x * 64; i < p.group * D; i += kKeepThreads * 64) prefetch_l2(p.query + seg * p.group * D + i);
+    }
+    grid_dependency_wait();
+    launch_dependents();
+    bool bad;
+    const int count = select_blocks_of(p, s, &bad);
+    if (bad && rank == 0 && kvh == 0 && threadIdx.x == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
+    if (count <= p.max_selected) {  // for all CTAs of the cluster
+        if (rank == 0) keep_all(p, seg, count);
+        return;
+    }
+    cluster_arrive();  // this CTA runs: its shared memory may be written
+    const int tiles = (count + kTileBlocks - 1) / kTileBlocks, step = (int)ctas * kKeepWarps;
+    int tile = (int)rank * kKeepWarps + warp;
+    int phys[2] = {0, 0};
+    const bool first = (lane & 3) == 0;
+    if (tile < tiles) {
+        phys[0] = select_phys(p, s, tile * kTileBlocks + g, count, first);
+        phys[1] = select_phys(p, s, tile * kTileBlocks + g + 8, count, first);
+    }
+    SelectQueries<D, NT> queries;
+    queries.load(p, seg, lane);
+    cluster_wait();
+    for (; tile < tiles; tile += step) {
+        float best[2], reach;
+        score_tile<D, NT>(p, queries, phys, kvh, lane, best, reach);
+        const int b0 = tile * kTileBlocks;
+        if (tile + step < tiles) {
+            phys[0] = select_phys(p, s, b0 + step * kTileBlocks + g, count, first);
+            phys[1] = select_phys(p, s, b0 + step * kTileBlocks + g + 8, count, first);
+        }
+        if (first)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                if (b0 + g + 8 * r < count) store_first(scores + b0 + g + 8 * r, best[r]);
+        if (lane == 0) store_first(reaches + tile, reach);
+    }
+    __syncwarp();
+    cluster_arrive();
+    if (rank != 0) {  // (a CTA waits for its barrier before it ends)
+        cluster_wait();
+        return;
+    }
+    cluster_wait();
+    if (threadIdx.x == 0) p.num_selected[seg] = p.max_selected;
+    keep_blocks<D, VALUES>(p, sh, places, s, kvh, count, scores, reaches);
+}
+
+// The fused kernel for up to max_blocks blocks a sequence, or NULL.
+constexpr int kFusedBlocks = 32 * kKeepThreads;
+template <int D, int NT>
+const void *fused_kernel(int max_blocks) {
+    return max_blocks <= 4 * kKeepThreads    ? reinterpret_cast<const void *>(&select_fused_kernel<D, NT, 4>)
+           : max_blocks <= 8 * kKeepThreads  ? reinterpret_cast<const void *>(&select_fused_kernel<D, NT, 8>)
+           : max_blocks <= 16 * kKeepThreads ? reinterpret_cast<const void *>(&select_fused_kernel<D, NT, 16>)
+           : max_blocks <= kFusedBlocks      ? reinterpret_cast<const void *>(&select_fused_kernel<D, NT, 32>)
+                                             : nullptr;
+}
+
+constexpr int kSelectFill = 608;
+// CTAs of a cluster: at most 8, a tile per warp, and fewer with more segments than fill the GPU, which then take more
+// tiles each.  Measured with up to 304, 608, 1216, 2500 and 5000 CTAs in all: 64 sequences x 8 heads of up to 1024 blocks
+// 42, 42, 45, 46 and 56 us, 32 x 8 32, 26, 29, 32 and 32, 16 x 8 21, 19, 22, 22 and 22.
+int cluster_ctas(int max_blocks, int64_t segments) {
+    const int tiles = (max_blocks + kTileBlocks - 1) / kTileBlocks;
+    int ctas = 8;
+    while (ctas > 1 && (tiles <= ctas / 2 * kKeepWarps || segments * ctas > kSelectFill)) ctas /= 2;
+    return ctas;
+}
+
+cudaError_t launch_cluster(const void *fn, dim3 grid, int ctas, pkv_stream_t stream, void **args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kKeepThreads);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 // Workspace carve-up (byte offsets).  It carries nothing from call to call.
@@ -569,17 +753,28 @@ extern "C" int pkv_select_blocks(int32_t *selected, int32_t *num_selected, const
 
     void *args[] = {&p};
     const bool d64 = head_dim == 64, wide = p.group > 8;
+    const void *fused = d64 ? (wide ? fused_kernel<64, 2>(max_blocks_per_seq) : fused_kernel<64, 1>(max_blocks_per_seq))
+                            : (wide ? fused_kernel<128, 2>(max_blocks_per_seq) : fused_kernel<128, 1>(max_blocks_per_seq));
+    if (fused) {
+        const int ctas = cluster_ctas(max_blocks_per_seq, (int64_t)num_seqs * num_kv_heads);
+        if (launch_cluster(fused, dim3((unsigned)ctas, (unsigned)num_kv_heads, (unsigned)num_seqs), ctas, stream, args) !=
+            cudaSuccess) {
+            cudaGetLastError();
+            return PKV_ERR_CUDA;
+        }
+        return PKV_OK;
+    }
     const void *fn = d64 ? (wide ? reinterpret_cast<const void *>(&select_score_kernel<64, 2>)
                                  : reinterpret_cast<const void *>(&select_score_kernel<64, 1>))
                          : (wide ? reinterpret_cast<const void *>(&select_score_kernel<128, 2>)
                                  : reinterpret_cast<const void *>(&select_score_kernel<128, 1>));
-    const unsigned tiles = (unsigned)((max_blocks_per_seq + kCtaBlocks - 1) / kCtaBlocks);
-    if (launch_pdl(fn, dim3(tiles, (unsigned)num_kv_heads, (unsigned)num_seqs), dim3(kThreads), 0, stream, args) !=
-        cudaSuccess) {
+    constexpr int per = kThreads / 32 * kTileBlocks;
+    if (launch_pdl(fn, dim3((unsigned)((max_blocks_per_seq + per - 1) / per), (unsigned)num_kv_heads, (unsigned)num_seqs),
+                   dim3(kThreads), 0, stream, args) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
     }
-    fn = d64 ? keep_kernel<64>(max_blocks_per_seq) : keep_kernel<128>(max_blocks_per_seq);
+    fn = d64 ? reinterpret_cast<const void *>(&select_keep_kernel<64>) : reinterpret_cast<const void *>(&select_keep_kernel<128>);
     if (launch_pdl(fn, dim3((unsigned)num_kv_heads, (unsigned)num_seqs), dim3(kKeepThreads), 0, stream, args) !=
         cudaSuccess) {
         cudaGetLastError();
