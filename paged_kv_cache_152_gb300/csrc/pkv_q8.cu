@@ -34,27 +34,45 @@ struct WriteParams {
     int scale_stride;
 };
 
+// y to 20 significant bits, nearest (Veltkamp's splitting).
+__device__ __forceinline__ float to_20_bits(float y) {
+    const float c = __fmul_rn(y, 17.f);
+    return __fsub_rn(c, __fsub_rn(c, y));
+}
+
 template <bool E4M3>
 struct Codes {
     static constexpr float kTop = E4M3 ? 448.f : 127.f;
-    // Eight values in units of the scale -> codes.  NaN: 0 in int8, NaN in e4m3.
+    // Eight quotients in units of the scale, each within 2^-22 of itself -> codes.
     __device__ static uint2 pack(const float (&y)[8]) {
         uint32_t r[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
+            float z[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = to_20_bits(y[4 * k + e]);
             if (E4M3) {
                 asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
                     "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n\t}"
                     : "=r"(r[k])
-                    : "f"(y[4 * k]), "f"(y[4 * k + 1]), "f"(y[4 * k + 2]), "f"(y[4 * k + 3]));
-            } else {
-                int v[4];
+                    : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
+            } else {  // 1.5 2^23 + z: the nearest integer to z is in the low bits
+                uint32_t v[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = min(max(__float2int_rn(y[4 * k + e]), -127), 127);
+                for (int e = 0; e < 4; ++e) v[e] = __float_as_uint(__fadd_rn(z[e], 12582912.f));
                 r[k] = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410);
             }
         }
         return make_uint2(r[0], r[1]);
+    }
+    // The same of elements x that may be no numbers.  Infinite ones: the largest code.  NaN: 0 in int8, NaN in e4m3.
+    __device__ static uint2 pack_any(float (&y)[8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (y[e] != y[e] && !E4M3) y[e] = 0.f;
+            if (fabsf(y[e]) > kTop) y[e] = copysignf(kTop, y[e]);
+        }
+        return pack(y);
     }
     __device__ static void unpack(uint2 c, float (&y)[8]) {
         const uint32_t r[2] = {c.x, c.y};
@@ -90,6 +108,7 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(const __grid_constan
     constexpr int kPerRow = D / 8, kTiles = kThreads / TILE;
     constexpr float kTop = Codes<E4M3>::kTop;
     __shared__ uint32_t tops[kThreads / 32];
+    touched_ask(p.t);
     grid_dependency_wait();
     launch_dependents();
     const int in = threadIdx.x % TILE;
@@ -106,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(const __grid_constan
     const __half *src = p.rows[which] + (b.token - b.lo) * p.stride[which] + (int64_t)head * D;
 
     uint4 x[kVecs];
-    uint32_t top = 0;
+    uint32_t top = 0, all = 0;  // largest finite magnitudes, all bits of the magnitudes
     float before = 0.f;
     if (b.phys >= 0) {
         if (b.lo > 0) before = *scale;
@@ -118,9 +137,18 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(const __grid_constan
                 x[i] = *reinterpret_cast<const uint4 *>(src + r * p.stride[which] + v % kPerRow * 8);
         }
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(finite_bits(x[i].x), finite_bits(x[i].y)),
-                                         __vmaxu2(finite_bits(x[i].z), finite_bits(x[i].w))));
+        for (int i = 0; i < kVecs; ++i) {
+            const uint32_t m[4] = {x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu, x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu};
+            all = __vmaxu2(all, __vmaxu2(__vmaxu2(m[0], m[1]), __vmaxu2(m[2], m[3])));
+        }
+        top = all;
+        if (__vcmpgtu2(all, 0x7bff7bffu)) {  // not all are finite
+            top = 0;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(finite_bits(x[i].x), finite_bits(x[i].y)),
+                                             __vmaxu2(finite_bits(x[i].z), finite_bits(x[i].w))));
+        }
         top = max(top & 0xffffu, top >> 16);
     }
 #pragma unroll
@@ -144,7 +172,8 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(const __grid_constan
     const float a = fmaxf(a0, __half2float(__ushort_as_half((unsigned short)top)));
     const bool grown = b.lo > 0 && a > a0;
     if (in == 0 && (b.lo == 0 || grown)) *scale = a / kTop;
-    const float by = a > 0.f ? a : 1.f;
+    const float by = a > 0.f ? kTop / a : kTop, again = a > 0.f ? a0 / a : 0.f;
+    const bool odd = __vcmpgtu2(all, 0x7bff7bffu) != 0;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         const int v = i * TILE + in, r = v / kPerRow;
@@ -154,13 +183,13 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(const __grid_constan
         if (fresh) {
             unpack8(x[i], y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = y[e] * kTop / by;
+            for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(y[e], by);
         } else {
             Codes<E4M3>::unpack(codes[v], y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = y[e] * a0 / by;
+            for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(y[e], again);
         }
-        codes[v] = Codes<E4M3>::pack(y);
+        codes[v] = odd && fresh ? Codes<E4M3>::pack_any(y) : Codes<E4M3>::pack(y);
     }
 }
 
@@ -193,6 +222,7 @@ struct BoundsParams {
 template <int TYPE, int D>
 __global__ void __launch_bounds__(kThreads) key_bounds_kernel(const __grid_constant__ BoundsParams p) {
     constexpr int kPerRow = D / 8, kRows = 32 / kPerRow, kAhead = 8;
+    touched_ask(p.t);
     grid_dependency_wait();
     launch_dependents();
     const int lane = threadIdx.x % 32, row = lane / kPerRow, col = lane % kPerRow;

@@ -40,6 +40,17 @@ __device__ __forceinline__ int touched_start(const TouchedParams &p, int s) {
     return min(max(__ldg(p.query_starts + s), 0), p.num_tokens);
 }
 
+// Asks into L2, while the kernel before still runs (nothing is read), what the blocks are found by.
+__device__ __forceinline__ void touched_ask(const TouchedParams &p) {
+    const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    auto ask = [&](const void *at, int64_t bytes) {
+        if (first * 128 < bytes) prefetch_l2(static_cast<const char *>(at) + first * 128);
+    };
+    ask(p.context_lens, (int64_t)p.num_seqs * 4);
+    if (p.query_starts) ask(p.query_starts, ((int64_t)p.num_seqs + 1) * 4);
+    ask(p.block_tables, (int64_t)p.num_seqs * p.max_blocks_per_seq * 4);
+}
+
 // Block number u.  `first`: one thread per number, which reports what is wrong.
 __device__ __forceinline__ TouchedBlock touched_block(const TouchedParams &p, int64_t u, bool first) {
     TouchedBlock t = {-1, 0, 0, 0};
@@ -47,10 +58,20 @@ __device__ __forceinline__ TouchedBlock touched_block(const TouchedParams &p, in
     int64_t j = 0;
     bool bad = false;
     if (p.query_starts) {
-        int lo = 0, hi = p.num_seqs;  // the last s whose first number is not past u
+        // the last s whose first number is not past u: seven of them looked at at a time
+        int lo = 0, hi = p.num_seqs;
         while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if ((touched_start(p, mid) >> p.block_shift) + 2 * (int64_t)mid <= u) lo = mid; else hi = mid;
+            const int step = (hi - lo + 7) >> 3;
+            int first[7], n = 0;
+#pragma unroll
+            for (int k = 0; k < 7; ++k) first[k] = touched_start(p, min(lo + (k + 1) * step, p.num_seqs - 1));
+#pragma unroll
+            for (int k = 0; k < 7; ++k) {
+                const int at = lo + (k + 1) * step;
+                n += at < hi && (first[k] >> p.block_shift) + 2 * (int64_t)at <= u;
+            }
+            lo += n * step;
+            hi = min(hi, lo + step);
         }
         s = lo;
         start = touched_start(p, s);
