@@ -18,6 +18,8 @@
 #include "pkv_device.cuh"
 #include "pkv_host.h"
 #include "pkv_launch.h"
+#include "pkv_schedule.h"
+#include "pkv_tcgen05.cuh"
 #include "pkv_touched.cuh"
 
 namespace pkv {
@@ -34,43 +36,51 @@ struct WriteParams {
     int scale_stride;
 };
 
-// y to 20 significant bits, nearest (Veltkamp's splitting).
-__device__ __forceinline__ float to_20_bits(float y) {
-    const float c = __fmul_rn(y, 17.f);
-    return __fsub_rn(c, __fsub_rn(c, y));
+// Two values to 20 significant bits each, nearest (Veltkamp's splitting).
+__device__ __forceinline__ uint64_t to_20_bits(uint64_t y) {
+    const uint64_t minus = pack2(-1.f, -1.f), c = mul2(y, pack2(17.f, 17.f));
+    return fma2(fma2(y, minus, c), minus, c);  // c - (c - y), each rounded once
 }
 
 template <bool E4M3>
 struct Codes {
     static constexpr float kTop = E4M3 ? 448.f : 127.f;
-    // Eight quotients in units of the scale, each within 2^-22 of itself -> codes.
-    __device__ static uint2 pack(const float (&y)[8]) {
+    // Eight quotients in units of the scale, in pairs, each within 2^-22 of itself -> codes.
+    __device__ static uint2 pack(const uint64_t (&y)[4]) {
         uint32_t r[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             float z[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] = to_20_bits(y[4 * k + e]);
-            if (E4M3) {
+            uint64_t a = to_20_bits(y[2 * k]), b = to_20_bits(y[2 * k + 1]);
+            if (!E4M3) {  // 1.5 2^23 + z: the nearest integer to z is in the low bits
+                const uint64_t place = pack2(12582912.f, 12582912.f);
+                a = add2(a, place), b = add2(b, place);
+            }
+            unpack2(a, z[0], z[1]);
+            unpack2(b, z[2], z[3]);
+            if (E4M3)
                 asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
                     "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n\t}"
                     : "=r"(r[k])
                     : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
-            } else {  // 1.5 2^23 + z: the nearest integer to z is in the low bits
-                uint32_t v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = __float_as_uint(__fadd_rn(z[e], 12582912.f));
-                r[k] = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410);
-            }
+            else
+                r[k] = __byte_perm(__byte_perm(__float_as_uint(z[0]), __float_as_uint(z[1]), 0x0040),
+                                   __byte_perm(__float_as_uint(z[2]), __float_as_uint(z[3]), 0x0040), 0x5410);
         }
         return make_uint2(r[0], r[1]);
     }
-    // The same of elements x that may be no numbers.  Infinite ones: the largest code.  NaN: 0 in int8, NaN in e4m3.
-    __device__ static uint2 pack_any(float (&y)[8]) {
+    // The same of quotients that may be no numbers.  Infinite ones: the largest code.  NaN: 0 in int8, NaN in e4m3.
+    __device__ static uint2 pack_any(uint64_t (&y)[4]) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (y[e] != y[e] && !E4M3) y[e] = 0.f;
-            if (fabsf(y[e]) > kTop) y[e] = copysignf(kTop, y[e]);
+        for (int k = 0; k < 4; ++k) {
+            float z[2];
+            unpack2(y[k], z[0], z[1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (z[e] != z[e] && !E4M3) z[e] = 0.f;
+                if (fabsf(z[e]) > kTop) z[e] = copysignf(kTop, z[e]);
+            }
+            y[k] = pack2(z[0], z[1]);
         }
         return pack(y);
     }
@@ -114,7 +124,7 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(const __grid_constan
     const int in = threadIdx.x % TILE;
     const int64_t tile = (int64_t)blockIdx.x * kTiles + threadIdx.x / TILE;
     // tiles of one block side by side: its heads' keys, then its heads' values
-    const int64_t unit = tile / (2 * p.num_kv_heads);
+    const int64_t unit = div_nonneg(tile, 2 * p.num_kv_heads);
     const int rest = (int)(tile - unit * 2 * p.num_kv_heads);
     const int which = rest >= p.num_kv_heads, head = rest - which * p.num_kv_heads;
     TouchedBlock b = {-1, 0, 0, 0};
@@ -124,6 +134,11 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(const __grid_constan
     uint2 *codes = reinterpret_cast<uint2 *>(p.cache[which]) + (at << p.t.block_shift) * kPerRow;
     const __half *src = p.rows[which] + (b.token - b.lo) * p.stride[which] + (int64_t)head * D;
 
+    // thread `in` has vector in % kPerRow of the rows in / kPerRow + i kStep (a tile's vectors side by side)
+    constexpr int kStep = TILE / kPerRow;
+    static_assert(TILE % kPerRow == 0, "whole rows");
+    const int64_t stride = p.stride[which];
+    const __half *at_row = src + in / kPerRow * stride + in % kPerRow * 8;
     uint4 x[kVecs];
     uint32_t top = 0, all = 0;  // largest finite magnitudes, all bits of the magnitudes
     float before = 0.f;
@@ -131,10 +146,10 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(const __grid_constan
         if (b.lo > 0) before = *scale;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            const int v = i * TILE + in, r = v / kPerRow;
+            const int r = (i * TILE + in) / kPerRow;
             x[i] = make_uint4(0, 0, 0, 0);
-            if (r >= b.lo && r < b.hi)
-                x[i] = *reinterpret_cast<const uint4 *>(src + r * p.stride[which] + v % kPerRow * 8);
+            if (r >= b.lo && r < b.hi) x[i] = *reinterpret_cast<const uint4 *>(at_row);
+            at_row += kStep * stride;
         }
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
@@ -179,29 +194,33 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(const __grid_constan
         const int v = i * TILE + in, r = v / kPerRow;
         const bool fresh = r >= b.lo && r < b.hi;
         if (!fresh && !(grown && r < b.lo)) continue;
-        float y[8];
+        uint64_t y[4];
         if (fresh) {
-            unpack8(x[i], y);
+            const uint32_t h[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(y[e], by);
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = unpack_half2(h[k]);
+                y[k] = mul2(pack2(f.x, f.y), pack2(by, by));
+            }
         } else {
-            Codes<E4M3>::unpack(codes[v], y);
+            float f[8];
+            Codes<E4M3>::unpack(codes[v], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(y[e], again);
+            for (int k = 0; k < 4; ++k) y[k] = mul2(pack2(f[2 * k], f[2 * k + 1]), pack2(again, again));
         }
         codes[v] = odd && fresh ? Codes<E4M3>::pack_any(y) : Codes<E4M3>::pack(y);
     }
 }
 
+// block_size * D / 64 threads per tile: D / 8 at block size 8, to 16 times as many at 128.
 template <bool E4M3, int D>
-const void *write_kernel(int tile) {
-    switch (tile) {
-        case 8: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, 8>);
-        case 16: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, 16>);
-        case 32: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, 32>);
-        case 64: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, 64>);
-        case 128: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, 128>);
-        default: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, 256>);
+const void *write_kernel(int block_size) {
+    switch (block_size) {
+        case 8: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, D / 8>);
+        case 16: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, D / 4>);
+        case 32: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, D / 2>);
+        case 64: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, D>);
+        default: return reinterpret_cast<const void *>(&write_q8_kernel<E4M3, D, 2 * D>);
     }
 }
 
@@ -228,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) key_bounds_kernel(const __grid_const
     const int lane = threadIdx.x % 32, row = lane / kPerRow, col = lane % kPerRow;
     const int64_t tile = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
     if (tile >= p.tiles) return;
-    const int64_t unit = tile / p.num_kv_heads;
+    const int64_t unit = div_nonneg(tile, p.num_kv_heads);
     const int head = (int)(tile - unit * p.num_kv_heads);
     const TouchedBlock b = touched_block(p.t, unit, lane == 0 && head == 0);
     if (b.phys < 0) return;
@@ -369,8 +388,8 @@ extern "C" int pkv_reshape_and_cache_q8(const void *key, int64_t key_stride, con
     p.tiles = touched_units(num_tokens, num_seqs, p.t.block_shift, query_starts != nullptr) * 2 * num_kv_heads;
     const int tile = block_size * head_dim / 64;
     const bool e4m3 = cache_type == PKV_CACHE_E4M3;
-    const void *fn = head_dim == 64 ? (e4m3 ? write_kernel<true, 64>(tile) : write_kernel<false, 64>(tile))
-                                    : (e4m3 ? write_kernel<true, 128>(tile) : write_kernel<false, 128>(tile));
+    const void *fn = head_dim == 64 ? (e4m3 ? write_kernel<true, 64>(block_size) : write_kernel<false, 64>(block_size))
+                                    : (e4m3 ? write_kernel<true, 128>(block_size) : write_kernel<false, 128>(block_size));
     void *args[] = {&p};
     const int64_t per = kThreads / tile;
     return launch(fn, (p.tiles + per - 1) / per, args, stream);
