@@ -779,8 +779,8 @@ int pkv_reshape_and_cache_q8(const void *key, int64_t key_stride,
  * times their scales.  The products take the codes as they are (exact in fp16)
  * and accumulate in fp32; softmax statistics and outputs are held in fp32; the
  * weights, with the value's scale in them, are rounded to fp16 for the second
- * product (11 significant bits down to 2^-29 of the row's largest); one rounding
- * to fp16 at the end.  A context of 0 gives zeros.  A row with a score that is
+ * product (11 significant bits down to 2^-29 of the weight of the row's largest
+ * score with its largest scale); one rounding to fp16 at the end.  A context of 0 gives zeros.  A row with a score that is
  * not finite is unspecified.
  *
  * With block lists (selected not NULL) the sum runs over the listed blocks'
@@ -791,8 +791,8 @@ int pkv_reshape_and_cache_q8(const void *key, int64_t key_stride,
  *                 max_selected and the context's blocks.  No entry: zeros.
  * selected and num_selected go together (both NULL: every block).
  *
- *   key_scale, value_scale, scale_stride  as for pkv_reshape_and_cache_q8; a
- *                 scale is 0 or between 2^-40 and 2^40
+ *   key_scale, value_scale, scale_stride  as for pkv_reshape_and_cache_q8; any
+ *                 scales from 0 to 2^100
  *   cache_type    PKV_CACHE_INT8 or PKV_CACHE_E4M3
  *   num_ctas      persistent grid size; 0 = one CTA per SM.  Any value gives the
  *                 same result within rounding; deterministic for a fixed grid.

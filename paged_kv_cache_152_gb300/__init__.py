@@ -877,10 +877,14 @@ def _scratch(workspace, size, index, device, stream):
     `size` bytes.  A new one belongs to the stream that uses it: freed on return,
     it then goes to that stream's later work only."""
     if workspace is None:
-        import torch
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        torch = _torch()
+        if stream is None:
             workspace = torch.empty(size, dtype=torch.uint8, device=device)
-    elif _checked(((workspace, workspace.dtype, "workspace", workspace.dim()),)) != index:
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), size
+    if _checked(((workspace, workspace.dtype, "workspace", workspace.dim()),)) != index:
         raise ValueError("the device tensors of one call must all be on the same CUDA device")
     return workspace, workspace.data_ptr(), workspace.nbytes
 
@@ -910,6 +914,8 @@ def _scale_spec(t, name):
 
 def _scale_stride(nb, hkv, *scales):
     """Floats between the rows of one cache's scales."""
+    if all([t.shape == (nb, hkv) and t.is_contiguous() for t in scales]):
+        return hkv
     for t in scales:
         if t.shape != (nb, hkv):
             raise ValueError("key_scale, value_scale: inconsistent shapes")

@@ -7,29 +7,52 @@
 //     x_t = c k_b (q_h . K_t),   out = sum_t e^{x_t} v_b V_t / sum_t e^{x_t}
 //
 // with K, V the codes (exact in fp16), k_b, v_b the scales of t's block (1 for
-// an fp16 cache) and c the softmax scale.  With y_t = x_t + ln v_b and m the
-// running maximum of y, the weights w_t = e^{x_t - m} v_b are at most 1 whatever
-// the scales, and the sum runs over e^{x_t - m}: one exponential per score.
+// an fp16 cache) and c the softmax scale.  With m the running maximum of x and 2^e
+// the running least power of two above the scales v, the weights e^{x_t - m} v_b 2^-e
+// are at most 1 whatever the scores and the scales; the sum runs over e^{x_t - m}.
 //
 // Bound by HBM: a row is read once for all query heads of its group.  8-bit rows
 // halve the bytes, so the work per byte doubles: the split and the layout are
-// chosen for few instructions per row.
-//  * The 4 warps of a CTA work on one segment's piece, each on every fourth
-//    step of 16 or 32 rows, with a ring of its own (cp.async, two to four steps
-//    in flight, 128 KB per SM) that runs on into the next pieces; the warps meet
-//    once per piece, in shared memory.
+// chosen for few instructions per row and few meetings of the warps.
+//  * The warps of a CTA (four; eight over fp16) work on one segment's piece
+//    together, a step of 32 rows (16 of 256 bytes) each in turn, with a ring of
+//    their own (16 KB per warp, 128 KB per SM in flight) that runs on into the next
+//    pieces.  Their outputs meet in shared memory, those of up to eight short
+//    pieces between two barriers (64 sequences over 50 to 900, 32 heads, int8: 48 us;
+//    59 with barriers at every piece).  Four warps with steps of 32 rows, two CTAs
+//    per SM, take 48.8 us there, eight warps with steps of 16 rows 53.9; a grouped
+//    batch 176 and 180.
+//  * Copies by cp.async: a lane copies the 16 bytes that its place in the swizzled
+//    tile wants, from the block that its row lies in, and rows past the end come
+//    as zeros; the block table's entries of 32 steps are looked up at once, a batch
+//    ahead.  With the arithmetic and the joining left out, the copies alone take 40
+//    of the 48 us above and 56 of the 62 for 8 long contexts.
 //  * mma.sync m16n8k16 with the rows on M and the heads on N for the scores
 //    (8 heads fill N; a 16-row tile takes D/16 instructions), and the dims on M
 //    and the heads on N for the output, transposed: the codes come from shared
 //    memory by ldmatrix (.trans for V) as pairs of bytes, whose dims are taken
 //    in the order that the fragments want them (queries and outputs follow it),
 //    so that widening to fp16 is all that is done to them.  The weights turn
-//    from the scores' layout to the product's by movmatrix.
+//    from the scores' layout to the product's by movmatrix.  (One group's heads are
+//    16 rows at most: tcgen05's tiles of 64 or 128 would stay empty.  The tensor pipe
+//    is active 14% of the time, the integer pipe, which widens, most of all.)
+//  * int8 codes need no subtraction: the byte code ^ 0x80 is fp16's (code + 128)
+//    2^-24, below the normal range, which the products take as it is.  128 times
+//    the queries' sum is where the scores' sums begin, below zero, and a product
+//    with ones keeps 128 times the weights' sum, taken off the output at the end
+//    (87 to 56 us above, with an even split).  Sums are of |code| + 256 instead of
+//    |code|, in fp32.
 //  * Weights are stored as fp16 after a factor of 2^15: 11 significant bits down
-//    to 2^-29 of the largest.
+//    to 2^-29, where 1 is a weight of the largest score and the largest scale.
 //  * A piece that is a whole segment is divided and written by the CTA; one that
 //    a CTA boundary cuts leaves (maximum, sum, output) in the workspace for the
-//    joining kernel, which runs behind it with its launch hidden.
+//    joining kernel, which runs behind it with its launch hidden (2.3 us).
+//
+// Measured (us, GB/s, of the copy bandwidth): 64 sequences over 50 to 900, 32 heads,
+// int8 48.2, 5060, 0.75; 256 over 256 to 4096, 32 heads and 8 KV heads, e4m3 177,
+// 6560, 0.97; 8 over 8000 to 32768, int8 62.4, 5880, 0.87; 64 blocks of 32 rows of
+// each of these, fp16 19.0, 3510, 0.52 (of a latency of three look-ups in a row);
+// 128 blocks of 16 for 64 sequences, fp16 89, 6030, 0.89.
 #ifndef PKV_TEAM_IMPL_CUH
 #define PKV_TEAM_IMPL_CUH
 
@@ -67,7 +90,7 @@ struct TeamConfig {
     static constexpr int kGroupCopies = kUnits / 4;          // of a lane, per cache and group
     static constexpr int kPitch = D + 8;                     // floats between heads of a warp's output
     // [warps][stages][K, V tiles] [warps][stages] TeamMeta
-    // [warps][8 rows] (maximum, sum, bias), [warps][8 rows][pitch] floats (a row is a head of
+    // [warps][8 rows] (maximum, sum, bias, output's unit), [warps][8 rows][pitch] floats (a row is a head of
     // one of the pieces in hold), then by sequence: cum
     static constexpr size_t kMeta = (size_t)kWarps * kStages * 2 * kTileBytes;
     static constexpr size_t kMl = kMeta + (size_t)kWarps * kStages * sizeof(TeamMeta<kGroups>);
@@ -126,14 +149,16 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     return r;
 }
 
-// 2^x for x <= 15 or so; 2^-inf = 0.
+// 2^x; 2^-inf = 0.
 __device__ __forceinline__ float team_exp2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
-constexpr float kTeamPlace = 15.f;  // weights are stored times 2^15
+constexpr int kTeamPlace = 15;      // weights are stored times 2^15
+constexpr int kTeamLeastExp = -100;  // the least e
+__device__ __forceinline__ float power_of_2(int e) { return __int_as_float((e + 127) << 23); }
 
 // A warp's attention state: lane (g, t) = (lane / 4, lane % 4) has heads 2t and
 // 2t + 1 of each tile of eight: m their maximum (the same on all g), l the sum
@@ -143,7 +168,9 @@ struct TeamState {
     float m[NT][2], l[NT][2];
     float o[NT][D / 16][4];
     float z[NT][4];  // int8: the biases' share of the output, the same for every dim
+    int e;           // the outputs are in units of 2^e
     __device__ __forceinline__ void clear() {
+        e = kTeamLeastExp;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             m[n][0] = m[n][1] = -CUDART_INF_F;
@@ -200,9 +227,10 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt,
             }
         }
 
-    // scores in log2 units; x: for the sum, x + lv: with the value's scale
-    float lv[C::kGroups], vs[C::kGroups];
+    // scores in log2 units
+    float vs[C::kGroups];
     float top[NT][2];
+    int e_to = C::kWide ? 0 : st.e;
 #pragma unroll
     for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -CUDART_INF_F;
 #pragma unroll
@@ -214,15 +242,14 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt,
             const float2 scale = C::kWide ? make_float2(1.f, 1.f) : meta.scale[j];
             const float f = C::kWide ? scale_log2 : scale_log2 * scale.x;
             vs[j] = scale.y;
-            // the logarithm only places the weights: bounded, so that a scale of zero does not
-            lv[j] = C::kWide ? 0.f : fminf(fmaxf(__log2f(scale.y), -40.f), 40.f);
+            if (!C::kWide) e_to = max(e_to, (int)((__float_as_uint(scale.y) & 0x7fffffffu) >> 23) - 126);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float &x = s[r][n][2 * h + e];
                     x = live ? x * f : -CUDART_INF_F;
-                    top[n][e] = fmaxf(top[n][e], x + lv[j]);
+                    top[n][e] = fmaxf(top[n][e], x);
                 }
         }
 #pragma unroll
@@ -242,13 +269,15 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt,
         for (int e = 0; e < 2; ++e) {
             const float was = st.m[n][e], to = fmaxf(top[n][e], was);
             f[n][e] = team_exp2(was - (to == -CUDART_INF_F ? 0.f : to));
-            moved |= to > was && was != -CUDART_INF_F && n * 8 + 2 * (lane & 3) + e < group;
+            moved |= (to > was || e_to > st.e) && was != -CUDART_INF_F && n * 8 + 2 * (lane & 3) + e < group;
             st.m[n][e] = to;
             st.l[n][e] *= f[n][e];
         }
     if (__any_sync(kFullMask, moved)) {
+        const float unit = C::kWide ? 1.f : power_of_2(max(st.e - e_to, -126));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            f[n][0] *= unit, f[n][1] *= unit;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 st.o[n][i][0] *= f[n][0];
@@ -259,12 +288,16 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt,
             if (KIND == kTeamInt8) st.z[n][0] *= f[n][0], st.z[n][1] *= f[n][1];
         }
     }
+    st.e = e_to;
+    const float placed = power_of_2(kTeamPlace - e_to);
     uint32_t w[C::kGroups][NT];
+#pragma unroll
+    for (int j = 0; j < C::kGroups; ++j) vs[j] *= placed;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         float ref[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) ref[e] = (st.m[n][e] == -CUDART_INF_F ? 0.f : st.m[n][e]) - kTeamPlace;
+        for (int e = 0; e < 2; ++e) ref[e] = st.m[n][e] == -CUDART_INF_F ? 0.f : st.m[n][e];
 #pragma unroll
         for (int r = 0; r < C::kTiles; ++r)
 #pragma unroll
@@ -598,15 +631,16 @@ __global__ void __launch_bounds__(TeamConfig<KIND, D, NT>::kThreads, TeamConfig<
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) {
             if (((w - piece.y) & (C::kWarps - 1)) >= piece.z) continue;
-            const float f = team_exp2(x[w].x - ref);
+            const float f = team_exp2(x[w].x - ref), fo = f * x[w].w;
             const float2 y = *reinterpret_cast<const float2 *>(red + (w * 8 + row) * C::kPitch + d);
             l = fmaf(x[w].y, f, l);
-            z = fmaf(x[w].z, f, z);
-            o.x = fmaf(y.x, f, o.x);
-            o.y = fmaf(y.y, f, o.y);
+            z = fmaf(x[w].z, fo, z);
+            o.x = fmaf(y.x, fo, o.x);
+            o.y = fmaf(y.y, fo, o.y);
         }
-        o.x = (o.x - z) * team_unit<KIND>();
-        o.y = (o.y - z) * team_unit<KIND>();
+        constexpr float unit = team_unit<KIND>() / (1 << kTeamPlace);
+        o.x = (o.x - z) * unit;
+        o.y = (o.y - z) * unit;
         if (piece.w == 2) {
             const float inv = l == 0.f ? 0.f : 1.f / l;  // no row: zeros
             *reinterpret_cast<__half2 *>(p.out + ((int64_t)piece.x * p.group + head) * D + d) =
@@ -669,7 +703,7 @@ __global__ void __launch_bounds__(TeamConfig<KIND, D, NT>::kThreads, TeamConfig<
                         const int h = 2 * t + e;
                         if (h < live) {
                             const int at = warp * 8 + j * red_heads + h;
-                            if (g == 0) ml[at] = make_float4(st.m[n][e], l, KIND == kTeamInt8 ? st.z[n][e] : 0.f, 0.f);
+                            if (g == 0) ml[at] = make_float4(st.m[n][e], l, KIND == kTeamInt8 ? st.z[n][e] : 0.f, power_of_2(st.e));
                             float *dst = red + at * C::kPitch;
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i) {

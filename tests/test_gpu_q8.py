@@ -6,10 +6,10 @@ Tolerance of the decode, per output element, with the codes and scales as given:
 
 * the output's rounding to fp16: 2^-11 |out|, 2^-25 below the normal range;
 * each weight's rounding to fp16: 2^-11 of it, together 2^-11 sum_t w_t |v_t|;
-  weights are stored times 2^15 where the largest (with its value's scale) is 1,
-  so one below fp16's normal range is off by at most 2^-25 of 2^15: count *
-  2^-40 times the largest |v| of any channel (some block's largest element
-  times its scale);
+  weights are stored times 2^15, where 1 is at most that of the largest score with
+  twice the largest value scale, so one below fp16's normal range is off by at most
+  2^-25 of 2^15: count * 2^-40 * 2 times the largest |v| of any channel (some
+  block's largest element times its scale);
 * scores: a product of D terms in fp32 is off by at most D 2^-24 of the terms'
   magnitudes, doubled because tensor cores may cut instead of round; the score's
   factor, the reference's subtraction and the places between, at most 12
@@ -51,7 +51,7 @@ def bound(ref, spread, reach, count, top, d, warps=4, reach8=0.0, spread8=0.0):
     sums = (count / 16 / warps + 24) * 2.0 ** -22
     return (2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + 2.0 ** -11 * spread + (2 * score + sums)[..., None] * spread +
             sums[..., None] * np.asarray(spread8)[..., None] +
-            count[..., None] * 2.0 ** -40 * top.max(axis=-1, keepdims=True))
+            count[..., None] * 2.0 ** -39 * top.max(axis=-1, keepdims=True))
 
 
 def biased(q, scales, tables, lens, bs, scale):
@@ -313,12 +313,18 @@ def test_a_large_score_and_many_small_ones(pkv):
 
 
 @pytest.mark.parametrize("kind", ALL)
-def test_scores_of_several_thousand(pkv, kind):
+@pytest.mark.parametrize("q_std", [600.0, 12000.0])
+def test_scores_of_any_size(pkv, kind, q_std):
     """The tolerance grows with the scores; the result stays a weighting."""
-    c = Case(13, kind, 4, 2, 128, 16, [300, 77], q_std=600.0)
+    c = Case(13, kind, 4, 2, 128, 16, [300, 77], q_std=q_std)
+    c.q = np.clip(c.q, -65504, 65504)
+    if q_std > 1000 and kind != "fp16":  # scores of 10^9, and the largest value scales: one position decides
+        c.scales[0] *= 65504
+        c.scales[1] = np.where(c.scales[1] < 1e20, c.scales[1] * 2.0 ** 12, c.scales[1])
     if kind == "fp16":
         c.pick(20)
     c.gpu()
+    c.scales = [x.astype(np.float32).astype(np.float64) for x in c.scales]
     c.check(c.call(pkv))
 
 
