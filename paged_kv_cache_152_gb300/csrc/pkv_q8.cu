@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(const __grid_constan
     }
     if (b.phys < 0) return;
 
-    // a0: what the scale stands for; a scale that is no finite one counts as 0
+    // a0: what the scale stands for; one that is negative or no number counts as 0
     float a0 = __half2float(__float2half_rn(before * kTop));
     if (!(a0 > 0.f)) a0 = 0.f;
     a0 = fminf(a0, 65504.f);

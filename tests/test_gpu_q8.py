@@ -206,6 +206,24 @@ def test_grids(pkv, grid, kind):
     assert torch.equal(first.view(torch.int16), again.view(torch.int16))
 
 
+@pytest.mark.parametrize("kind", ALL)
+@pytest.mark.parametrize("h,hkv", [(3, 3), (4, 2), (9, 3), (8, 2), (10, 2), (24, 2)])
+@pytest.mark.parametrize("grid", [1, 3, 11, 0])
+def test_many_short_pieces(pkv, grid, h, hkv, kind):
+    """Pieces of one to a few steps, some between two long ones, of every number
+    of heads that goes between two barriers; cut or not."""
+    rng = np.random.default_rng(h)
+    lens = [int(x) for x in rng.integers(0, 70, 37)] + [700, 1, 33, 0, 0, 900] + [int(x) for x in rng.integers(0, 200, 20)]
+    c = Case(30, kind, h, hkv, 128, 16, lens)
+    if kind == "fp16":
+        c.pick(50, "any")
+    c.gpu()
+    expect = c.oracle()
+    for _ in range(2):
+        c.out.fill_(-77)
+        c.check(c.call(pkv, num_ctas=grid), expect)
+
+
 @pytest.mark.parametrize("kind,d", [("int8", 128), ("e4m3", 64)])
 def test_one_long_context(pkv, kind, d):
     c = Case(4, kind, 8, 1, d, 64, [20011, 3]).gpu()
@@ -383,6 +401,35 @@ def test_streams_graphs_and_workspaces(pkv):
     c.t["q"].copy_(torch.from_numpy(c.q))
     graphs[0].replay()
     c.check(c.out)
+
+
+def test_two_streams_at_once(pkv):
+    """Calls that run at the same time, each with a workspace of its own."""
+    cases = [Case(31, "int8", 8, 2, 128, 16, [3000, 40, 2000]).gpu(), Case(32, "e4m3", 4, 4, 64, 16, [2500, 1, 900]).gpu(),
+             Case(33, "fp16", 8, 1, 128, 32, [4000, 77]).pick(60).gpu()]
+    expect = [c.oracle() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for c, s in zip(cases, streams):
+            c.call(pkv, stream=s)
+    for c, e in zip(cases, expect):
+        c.check(c.out, e)
+
+
+def test_the_same_bits_every_time(pkv):
+    """500 launches on one workspace, two shapes in turn."""
+    a, b = Case(34, "int8", 8, 2, 128, 16, [1500, 3, 0, 800]).gpu(), Case(35, "fp16", 12, 4, 64, 8, [900, 60]).pick(40).gpu()
+    ws = pkv.new_team_workspace(8, 2, 128)  # the larger of the two
+    first = [x.call(pkv, workspace=ws).clone() for x in (a, b)]
+    for x, f in zip((a, b), first):
+        x.check(f)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(500):
+        for x, f in zip((a, b), first):
+            x.out.fill_(-77)
+            differ += (x.call(pkv, workspace=ws).view(torch.int16) != f.view(torch.int16)).sum()
+    assert int(differ.item()) == 0
 
 
 def test_shapes_that_do_not_fit(pkv):
@@ -619,3 +666,52 @@ def test_write_in_a_graph(pkv):
         w.t["v"].copy_(torch.from_numpy(w.rows[1]))
         graph.replay()
         w.check()
+
+
+@pytest.mark.parametrize("kind", EIGHT)
+def test_pools_are_copied_and_swapped(pkv, kind):
+    """copy_blocks and swap_blocks, one layer and several, on codes and scales."""
+    rng = np.random.default_rng(40)
+    nb, hkv, bs, d = 12, 3, 8, 64
+    codes = [torch.from_numpy(rng.integers(0, 127, (nb, hkv, bs, d)).astype(np.int8)).view(DTYPE[kind]).cuda()
+             for _ in range(4)]
+    scales = [torch.from_numpy(rng.standard_normal((nb, 4)).astype(np.float32)).cuda() for _ in range(4)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pairs = torch.tensor([[2, 7], [11, 0], [3, 4]], device="cuda")
+
+    def moved(pools, src=None):
+        out = []
+        for i, p in enumerate(pools):
+            q, s = p.cpu().view(torch.uint8).clone(), (src[i] if src else p).cpu().view(torch.uint8)
+            for a, b in pairs.tolist():
+                q[b] = s[a]
+            out.append(q)
+        return out
+
+    def same(pools, expect):
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        assert all(torch.equal(p.cpu().view(torch.uint8), e) for p, e in zip(pools, expect))
+
+    for group in (codes, scales):
+        expect = moved(group[:2])
+        pkv.copy_blocks(group[0], group[1], pairs, status=status)
+        same(group[:2], expect)
+        expect = moved(group)
+        pkv.copy_blocks_layers(group[0::2], group[1::2], pairs, status=status)
+        same(group, expect)
+        host = [torch.empty_like(x, device="cpu").fill_(0).pin_memory() for x in group]
+        expect = moved(host, group)
+        pkv.swap_blocks(group[0], group[1], host[0], host[1], pairs, status=status)
+        pkv.swap_blocks_layers(group[2:3], group[3:4], host[2:3], host[3:4], pairs, status=status)
+        same(host, expect)
+        expect = moved(group, host)
+        pkv.swap_blocks_layers(host[0::2], host[1::2], group[0::2], group[1::2], pairs, status=status)
+        same(group, expect)
+    with pytest.raises(TypeError):
+        pkv.copy_blocks(codes[0], codes[1].view(torch.uint8).half(), pairs)
+    with pytest.raises((TypeError, ValueError)):
+        pkv.swap_blocks(codes[0], codes[1], scales[0].cpu().pin_memory(), scales[1].cpu().pin_memory(), pairs)
+    odd = torch.zeros(nb, 3, device="cuda")
+    with pytest.raises(pkv.PkvError):
+        pkv.copy_blocks(odd, odd.clone(), pairs)
