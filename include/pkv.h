@@ -777,11 +777,12 @@ int pkv_reshape_and_cache_q8(const void *key, int64_t key_stride,
  * pkv_paged_attention_decode over an 8-bit cache: out[s][h] = sum_t
  * softmax_t(scale * q[s][h] . K[t][kvh]) * V[t][kvh] with K and V the codes
  * times their scales.  The products take the codes as they are (exact in fp16)
- * and accumulate in fp32; softmax statistics and outputs are held in fp32; the
- * weights, with the value's scale in them, are rounded to fp16 for the second
- * product (11 significant bits down to 2^-29 of the weight of the row's largest
- * score with its largest scale); one rounding to fp16 at the end.  A context of 0 gives zeros.  A row with a score that is
- * not finite is unspecified.
+ * and accumulate in fp32; softmax statistics and outputs are held in fp32; a
+ * weight, with the value's scale in it, goes into the second product as two fp16
+ * terms (22 significant bits down to 2^-18 of the weight of the row's largest
+ * score with its largest scale, steps of 2^-39 of that below); one rounding to
+ * fp16 at the end.  A context of 0 gives zeros.  A row with a score that is not
+ * finite is unspecified.
  *
  * With block lists (selected not NULL) the sum runs over the listed blocks'
  * positions below context_lens[s] only, a list for each sequence and KV head:

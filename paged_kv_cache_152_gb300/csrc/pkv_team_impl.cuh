@@ -18,15 +18,15 @@
 //    together, a step of 32 rows (16 of 256 bytes) each in turn, with a ring of
 //    their own (16 KB per warp, 128 KB per SM in flight) that runs on into the next
 //    pieces.  Their outputs meet in shared memory, those of up to eight short
-//    pieces between two barriers (64 sequences over 50 to 900, 32 heads, int8: 48 us;
-//    59 with barriers at every piece).  Four warps with steps of 32 rows, two CTAs
-//    per SM, take 48.8 us there, eight warps with steps of 16 rows 53.9; a grouped
-//    batch 176 and 180.
+//    pieces between two barriers (64 sequences over 50 to 900, 32 heads, int8, "chats":
+//    48.3 us, 59.4 with barriers at every piece).  Four warps with steps of 32 rows,
+//    two CTAs per SM, took 48.8 us there, eight warps with steps of 16 rows 53.9; a
+//    grouped batch 176 and 180.
 //  * Copies by cp.async: a lane copies the 16 bytes that its place in the swizzled
 //    tile wants, from the block that its row lies in, and rows past the end come
 //    as zeros; the block table's entries of 32 steps are looked up at once, a batch
-//    ahead.  With the arithmetic and the joining left out, the copies alone take 40
-//    of the 48 us above and 56 of the 62 for 8 long contexts.
+//    ahead.  With the arithmetic and the joining left out, the copies alone take 39.8
+//    us of the chats' and 56.0 of the 62 for 8 long contexts.
 //  * mma.sync m16n8k16 with the rows on M and the heads on N for the scores
 //    (8 heads fill N; a 16-row tile takes D/16 instructions), and the dims on M
 //    and the heads on N for the output, transposed: the codes come from shared
@@ -36,23 +36,26 @@
 //    from the scores' layout to the product's by movmatrix.  (One group's heads are
 //    16 rows at most: tcgen05's tiles of 64 or 128 would stay empty.  The tensor pipe
 //    is active 14% of the time, the integer pipe, which widens, most of all.)
-//  * int8 codes need no subtraction: the byte code ^ 0x80 is fp16's (code + 128)
-//    2^-24, below the normal range, which the products take as it is.  128 times
-//    the queries' sum is where the scores' sums begin, below zero, and a product
-//    with ones keeps 128 times the weights' sum, taken off the output at the end
-//    (87 to 56 us above, with an even split).  Sums are of |code| + 256 instead of
-//    |code|, in fp32.
-//  * Weights are stored as fp16 after a factor of 2^15: 11 significant bits down
-//    to 2^-29, where 1 is a weight of the largest score and the largest scale.
+//  * int8 codes widen to fp16 below the normal range: the byte code ^ 0x80 is fp16's
+//    (code + 128) 2^-24, which the products take as it is.  The keys keep the 128
+//    (128 times the queries' sum is where the scores' sums begin, below zero, and the
+//    sums are of |code| + 256 instead of |code|, in fp32); off the values it is
+//    subtracted, exactly: their sums run over the whole context, and a mean of many
+//    values is small beside 128 (with a product for it instead, the outputs of
+//    contexts of 20000 had 2.5 times the error).
+//  * A weight goes into its product as two fp16 terms, after a factor of 2^15: 22
+//    significant bits down to 2^-18, 11 down to 2^-29, where 1 is a weight of the
+//    largest score and the largest scale.  (One term: 1.4 times the error of an output
+//    rounded once, and the chats 48.0 instead of 49.8 us, the others level.)
 //  * A piece that is a whole segment is divided and written by the CTA; one that
 //    a CTA boundary cuts leaves (maximum, sum, output) in the workspace for the
 //    joining kernel, which runs behind it with its launch hidden (2.3 us).
 //
 // Measured (us, GB/s, of the copy bandwidth): 64 sequences over 50 to 900, 32 heads,
-// int8 48.2, 5060, 0.75; 256 over 256 to 4096, 32 heads and 8 KV heads, e4m3 177,
-// 6560, 0.97; 8 over 8000 to 32768, int8 62.4, 5880, 0.87; 64 blocks of 32 rows of
-// each of these, fp16 19.0, 3510, 0.52 (of a latency of three look-ups in a row);
-// 128 blocks of 16 for 64 sequences, fp16 89, 6030, 0.89.
+// int8 49.8, 4890, 0.72; 256 over 256 to 4096, 32 heads and 8 KV heads, e4m3 178,
+// 6520, 0.96; 8 over 8000 to 32768, int8 62.9, 5830, 0.86; 64 blocks of 32 rows of
+// each of these, fp16 19.1, 3490, 0.51 (of a latency of three look-ups in a row);
+// 128 blocks of 16 for 64 sequences, fp16 90, 5960, 0.88.
 #ifndef PKV_TEAM_IMPL_CUH
 #define PKV_TEAM_IMPL_CUH
 
@@ -90,7 +93,7 @@ struct TeamConfig {
     static constexpr int kGroupCopies = kUnits / 4;          // of a lane, per cache and group
     static constexpr int kPitch = D + 8;                     // floats between heads of a warp's output
     // [warps][stages][K, V tiles] [warps][stages] TeamMeta
-    // [warps][8 rows] (maximum, sum, bias, output's unit), [warps][8 rows][pitch] floats (a row is a head of
+    // [warps][8 rows] (maximum, sum, output's unit), [warps][8 rows][pitch] floats (a row is a head of
     // one of the pieces in hold), then by sequence: cum
     static constexpr size_t kMeta = (size_t)kWarps * kStages * 2 * kTileBytes;
     static constexpr size_t kMl = kMeta + (size_t)kWarps * kStages * sizeof(TeamMeta<kGroups>);
@@ -109,13 +112,22 @@ __device__ __forceinline__ int team_swizzle(int r, int u) {
 // Four codes in a register -> the fp16 pairs (b0, b1), (b2, b3), or with PAIRED
 // (b0, b2), (b1, b3).  An int8 code comes as (code + 128) 2^-24: the byte code ^
 // 0x80 in the low bits of an fp16 below the normal range, which the products take
-// as it is; kTeamBias is what they have too much, kTeamUnit what undoes the 2^-24.
+// as it is (PAIRED, the values: without the 128); team_unit undoes the 2^-24.
+constexpr uint32_t kTeamBias = 0x00800080u;  // two fp16 values 128 2^-24
 template <int KIND, bool PAIRED>
 __device__ __forceinline__ void team_widen(uint32_t codes, uint32_t &lo, uint32_t &hi) {
     if (KIND == kTeamInt8) {
         const uint32_t u = codes ^ 0x80808080u;
         lo = __byte_perm(u, 0, PAIRED ? 0x4240 : 0x4140);
         hi = __byte_perm(u, 0, PAIRED ? 0x4341 : 0x4342);
+        if (PAIRED) {
+            const uint32_t bias = kTeamBias;
+            const __half2 b = *reinterpret_cast<const __half2 *>(&bias);
+            const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&lo), b);
+            const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&hi), b);
+            lo = *reinterpret_cast<const uint32_t *>(&x);
+            hi = *reinterpret_cast<const uint32_t *>(&y);
+        }
     } else {
         const uint32_t c = PAIRED ? __byte_perm(codes, 0, 0x3120) : codes;
         asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
@@ -124,7 +136,6 @@ __device__ __forceinline__ void team_widen(uint32_t codes, uint32_t &lo, uint32_
             : "r"(c));
     }
 }
-constexpr uint32_t kTeamBias = 0x00800080u;  // two fp16 values 128 2^-24
 template <int KIND>
 __device__ __forceinline__ constexpr float team_unit() { return KIND == kTeamInt8 ? 16777216.f : 1.f; }
 
@@ -167,7 +178,6 @@ template <int D, int NT>
 struct TeamState {
     float m[NT][2], l[NT][2];
     float o[NT][D / 16][4];
-    float z[NT][4];  // int8: the biases' share of the output, the same for every dim
     int e;           // the outputs are in units of 2^e
     __device__ __forceinline__ void clear() {
         e = kTeamLeastExp;
@@ -175,7 +185,6 @@ struct TeamState {
         for (int n = 0; n < NT; ++n) {
             m[n][0] = m[n][1] = -CUDART_INF_F;
             l[n][0] = l[n][1] = 0.f;
-            z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
         }
@@ -285,12 +294,11 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt,
                 st.o[n][i][2] *= f[n][0];
                 st.o[n][i][3] *= f[n][1];
             }
-            if (KIND == kTeamInt8) st.z[n][0] *= f[n][0], st.z[n][1] *= f[n][1];
         }
     }
     st.e = e_to;
     const float placed = power_of_2(kTeamPlace - e_to);
-    uint32_t w[C::kGroups][NT];
+    uint32_t w[C::kGroups][NT][2];  // a weight as two fp16 terms
 #pragma unroll
     for (int j = 0; j < C::kGroups; ++j) vs[j] *= placed;
 #pragma unroll
@@ -305,17 +313,14 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt,
                 const float p0 = team_exp2(s[r][n][2 * h] - ref[0]), p1 = team_exp2(s[r][n][2 * h + 1] - ref[1]);
                 st.l[n][0] += p0;
                 st.l[n][1] += p1;
-                w[2 * r + h][n] = transpose_8x8(pack_half2(p0 * vs[2 * r + h], p1 * vs[2 * r + h]));
+                const float w0 = p0 * vs[2 * r + h], w1 = p1 * vs[2 * r + h];
+                const uint32_t hi = pack_half2(w0, w1);
+                const float2 back = unpack_half2(hi);
+                w[2 * r + h][n][0] = transpose_8x8(hi);
+                w[2 * r + h][n][1] = transpose_8x8(pack_half2(w0 - back.x, w1 - back.y));
             }
     }
 
-    if (KIND == kTeamInt8) {
-#pragma unroll
-        for (int r = 0; r < C::kTiles; ++r)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                mma_16816(st.z[n], kTeamBias, kTeamBias, kTeamBias, kTeamBias, w[2 * r][n], w[2 * r + 1][n]);
-    }
 #pragma unroll
     for (int r = 0; r < C::kTiles; ++r)
 #pragma unroll
@@ -324,18 +329,26 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt,
             ldsm_x4_trans(vt + place[u / 2] + r * 16 * RB, x0, x1, x2, x3);
             if constexpr (C::kWide) {  // x0, x1: rows 0-7 and 8-15 of dims 0-7; x2, x3: of dims 8-15
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_16816(st.o[n][u / 2], x0, x2, x1, x3, w[2 * r][n], w[2 * r + 1][n]);
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        mma_16816(st.o[n][u / 2], x0, x2, x1, x3, w[2 * r][n][e], w[2 * r + 1][n][e]);
             } else {
                 uint32_t a0, a1, a2, a3;
                 team_widen<KIND, true>(x0, a0, a1);
                 team_widen<KIND, true>(x1, a2, a3);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_16816(st.o[n][u], a0, a1, a2, a3, w[2 * r][n], w[2 * r + 1][n]);
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        mma_16816(st.o[n][u], a0, a1, a2, a3, w[2 * r][n][e], w[2 * r + 1][n][e]);
                 team_widen<KIND, true>(x2, a0, a1);
                 team_widen<KIND, true>(x3, a2, a3);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    mma_16816(st.o[n][u + 1], a0, a1, a2, a3, w[2 * r][n], w[2 * r + 1][n]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        mma_16816(st.o[n][u + 1], a0, a1, a2, a3, w[2 * r][n][e], w[2 * r + 1][n][e]);
             }
         }
 }
@@ -618,7 +631,7 @@ __global__ void __launch_bounds__(TeamConfig<KIND, D, NT>::kThreads, TeamConfig<
     };
     // Dims d and d + 1 of a row of the outputs that a piece's warps hold: to the output, or to the workspace.
     auto join = [&](int row, int head, int d, const int4 &piece) {
-        float top = -CUDART_INF_F, l = 0.f, z = 0.f;
+        float top = -CUDART_INF_F, l = 0.f;
         float4 x[C::kWarps];
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) {
@@ -631,16 +644,15 @@ __global__ void __launch_bounds__(TeamConfig<KIND, D, NT>::kThreads, TeamConfig<
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) {
             if (((w - piece.y) & (C::kWarps - 1)) >= piece.z) continue;
-            const float f = team_exp2(x[w].x - ref), fo = f * x[w].w;
+            const float f = team_exp2(x[w].x - ref), fo = f * x[w].z;
             const float2 y = *reinterpret_cast<const float2 *>(red + (w * 8 + row) * C::kPitch + d);
             l = fmaf(x[w].y, f, l);
-            z = fmaf(x[w].z, fo, z);
             o.x = fmaf(y.x, fo, o.x);
             o.y = fmaf(y.y, fo, o.y);
         }
         constexpr float unit = team_unit<KIND>() / (1 << kTeamPlace);
-        o.x = (o.x - z) * unit;
-        o.y = (o.y - z) * unit;
+        o.x *= unit;
+        o.y *= unit;
         if (piece.w == 2) {
             const float inv = l == 0.f ? 0.f : 1.f / l;  // no row: zeros
             *reinterpret_cast<__half2 *>(p.out + ((int64_t)piece.x * p.group + head) * D + d) =
@@ -703,7 +715,7 @@ __global__ void __launch_bounds__(TeamConfig<KIND, D, NT>::kThreads, TeamConfig<
                         const int h = 2 * t + e;
                         if (h < live) {
                             const int at = warp * 8 + j * red_heads + h;
-                            if (g == 0) ml[at] = make_float4(st.m[n][e], l, KIND == kTeamInt8 ? st.z[n][e] : 0.f, power_of_2(st.e));
+                            if (g == 0) ml[at] = make_float4(st.m[n][e], l, power_of_2(st.e), 0.f);
                             float *dst = red + at * C::kPitch;
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i) {

@@ -5,19 +5,19 @@ too) within the roundings it makes.
 Tolerance of the decode, per output element, with the codes and scales as given:
 
 * the output's rounding to fp16: 2^-11 |out|, 2^-25 below the normal range;
-* each weight's rounding to fp16: 2^-11 of it, together 2^-11 sum_t w_t |v_t|;
-  weights are stored times 2^15, where 1 is at most that of the largest score with
-  twice the largest value scale, so one below fp16's normal range is off by at most
-  2^-25 of 2^15: count * 2^-40 * 2 times the largest |v| of any channel (some
-  block's largest element times its scale);
+* each weight's rounding to two fp16 terms: 2^-22 of it, together 2^-22 sum_t w_t
+  |v_t|; weights are stored times 2^15, where 1 is at most that of the largest score
+  with twice the largest value scale, so where the second term is below fp16's
+  normal range it is off by at most 2^-25 of 2^15: count * 2^-40 * 2 times the
+  largest |v| of any channel (some block's largest element times its scale);
 * scores: a product of D terms in fp32 is off by at most D 2^-24 of the terms'
   magnitudes, doubled because tensor cores may cut instead of round; the score's
   factor, the reference's subtraction and the places between, at most 12
   roundings of numbers up to 1.45 of the score's size (log2 units); ex2 and the
   factors of a maximum that rises, 2^-22 each, at most 16 of them: 2^-18.  A
   score off by x moves a weight by e^x, in the numerator and the sum.  The
-  products may hold an int8 code as code + 128 and take 128 times the other
-  factors' sum off again, so their terms' magnitudes count |code| + 256;
+  products hold an int8 code as code + 128, and 128 times the queries' sum is
+  taken off, so their terms' magnitudes count |code| + 256;
 * sums in fp32, at most 2^-22 of the magnitudes' sum per step (an instruction
   adds 16 products, each cut at 2^-23 or finer of the largest): a step of 16 rows
   for each of 4 warps, and two dozen joins.
@@ -45,27 +45,24 @@ def pkv():
     return m
 
 
-def bound(ref, spread, reach, count, top, d, warps=4, reach8=0.0, spread8=0.0):
-    """reach8, spread8: what int8's 256 steps of the scale add to the terms' magnitudes in the scores and in the sums."""
+def bound(ref, spread, reach, count, top, d, warps=4, reach8=0.0):
+    """reach8: what int8's 256 steps of the scale add to the terms' magnitudes in the scores."""
     score = (2 * d * (reach + reach8) + 12 * 1.45 * reach) * 2.0 ** -24 + 2.0 ** -18
     sums = (count / 16 / warps + 24) * 2.0 ** -22
-    return (2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + 2.0 ** -11 * spread + (2 * score + sums)[..., None] * spread +
-            sums[..., None] * np.asarray(spread8)[..., None] +
+    return (2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + 2.0 ** -22 * spread + (2 * score + sums)[..., None] * spread +
             count[..., None] * 2.0 ** -39 * top.max(axis=-1, keepdims=True))
 
 
-def biased(q, scales, tables, lens, bs, scale):
-    """(reach8, spread8) [N][H] of an int8 cache with these scales."""
-    hkv = scales[0].shape[1]
-    group = q.shape[1] // hkv
-    reach, spread = np.zeros(q.shape[:2]), np.zeros(q.shape[:2])
+def biased(q, scale, tables, lens, bs, softmax_scale):
+    """reach8 [N][H] of an int8 cache with these key scales."""
+    group = q.shape[1] // scale.shape[1]
+    reach = np.zeros(q.shape[:2])
     for s in range(len(lens)):
         blocks = tables[s][:-(-int(lens[s]) // bs)]
         if len(blocks):
-            ks, vs = (np.repeat(x[blocks].max(axis=0), group) for x in scales)
-            reach[s] = scale * 256 * ks * np.abs(q[s].astype(np.float64)).sum(axis=1)
-            spread[s] = 256 * vs
-    return reach, spread
+            largest = np.repeat(scale[blocks].max(axis=0), group)
+            reach[s] = softmax_scale * 256 * largest * np.abs(q[s].astype(np.float64)).sum(axis=1)
+    return reach
 
 
 def to_gpu(codes, kind):
@@ -166,8 +163,10 @@ class Case:
         ref, spread, reach, count, top = expect or self.oracle()
         got = out.float().cpu().numpy().astype(np.float64)
         assert np.isfinite(got).all()
-        more = biased(self.q, self.scales, self.tables, self.lens, self.bs, self.scale) if self.kind == "int8" else ()
-        over = np.abs(got - ref) / bound(ref, spread, reach, count, top, self.d, warps, *more)
+        more = 0.0
+        if self.kind == "int8":
+            more = biased(self.q, self.scales[0], self.tables, self.lens, self.bs, self.scale)
+        over = np.abs(got - ref) / bound(ref, spread, reach, count, top, self.d, warps, more)
         assert over.max() <= 1.0, (over.max(), np.unravel_index(over.argmax(), over.shape))
 
 

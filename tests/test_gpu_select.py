@@ -307,5 +307,5 @@ def test_the_path_step_by_step(pkv, kind):
         lists = [[ref[s, k, :count[s, k]].tolist() for k in range(hkv)] for s in range(len(seqs))]
         expect, spread, reach, seen, top = Q.decode(q, values[0], values[1], tables, ln, 0.125, lists)
         got = out.double().cpu().numpy()
-        more = G.biased(q, o_scales, tables, ln, bs, 0.125) if kind == "int8" else ()
-        assert (np.abs(got - expect) <= G.bound(expect, spread, reach, seen, top, d, 4, *more)).all()
+        more = G.biased(q, o_scales[0], tables, ln, bs, 0.125) if kind == "int8" else 0.0
+        assert (np.abs(got - expect) <= G.bound(expect, spread, reach, seen, top, d, 4, more)).all()
