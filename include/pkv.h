@@ -705,8 +705,9 @@ int pkv_validate_block_pairs(const int64_t *host_pairs, int num_pairs,
  * Element type of a cache.  An 8-bit cache has the layout of the fp16 one with
  * one byte per element, and for each of key_cache and value_cache an fp32 scale
  * per (block, KV head): num_blocks rows of num_kv_heads, scale_stride floats
- * apart.  An element is its code times the scale of its block and head.  int8 codes are -127 .. 127; e4m3
- * codes (four significant bits, up to 448; the format without infinities).
+ * apart.  An element is its code times the scale of its block and head.  Codes
+ * are int8, -127 .. 127, or e4m3 (four significant bits, up to 448; the format
+ * without infinities).
  * A pool's blocks and their scales are copied and swapped like any other:
  * pkv_copy_blocks and pkv_swap_blocks with block_bytes = num_kv_heads *
  * block_size * head_dim for the codes and 4 * scale_stride for the scales (a
@@ -795,7 +796,7 @@ int pkv_reshape_and_cache_q8(const void *key, int64_t key_stride,
  *   key_scale, value_scale, scale_stride  as for pkv_reshape_and_cache_q8; any
  *                 scales from 0 to 2^100
  *   cache_type    PKV_CACHE_INT8 or PKV_CACHE_E4M3
- *   num_ctas      persistent grid size; 0 = one CTA per SM.  Any value gives the
+ *   num_ctas      grid size; 0 = as many as run at once.  Any value gives the
  *                 same result within rounding; deterministic for a fixed grid.
  *   workspace     at least pkv_decode_team_workspace_size(...) bytes for the same
  *                 (num_heads, num_kv_heads, head_dim, num_ctas); 256-byte
@@ -887,8 +888,10 @@ int pkv_block_key_bounds(void *key_bounds, const void *key_cache, const float *k
  * product with the query.  Of the context's B = ceil(L / block_size) blocks,
  * min(B, max_selected) are kept: the first first_blocks and the last
  * last_blocks, and of the others those with the largest scores, of equal ones
- * the lowest index.  A score that is not finite counts as the largest.  The
- * choice is that of the scores in 64 bits.
+ * the lowest index.  A score that is not finite counts as the largest.  Scores
+ * that fp32 sums cannot tell apart are summed again with twice the digits, off
+ * by 2^-44 of their terms' magnitudes at most, before they are compared: what
+ * is kept does not depend on the order of a sum.
  *
  *   selected      int32 [num_seqs][num_kv_heads][max_selected] (device, written):
  *                 the kept blocks' logical indices in ascending order, then -1

@@ -939,8 +939,8 @@ def reshape_and_cache_q8(key, value, key_cache, value_cache, key_scale, value_sc
     of a projection's output); key_cache, value_cache: int8 or float8_e4m3fn
     [NB][Hkv][bs][D]; key_scale, value_scale: fp32 [NB][Hkv], or the first
     columns of wider rows (copy_blocks and swap_blocks move rows of a multiple of
-    4); block_tables: int32 [N][MB]; context_lens: int32 [N]; query_starts: int32 [N + 1], or None:
-    one token of each sequence (T == N)."""
+    4); block_tables: int32 [N][MB]; context_lens: int32 [N]; query_starts: int32
+    [N + 1], or None: one token of each sequence (T == N)."""
     torch = _torch()
     f16, i32 = torch.float16, torch.int32
     sk, sv = _rows(key, "key", f16), _rows(value, "value", f16)
@@ -973,9 +973,10 @@ def paged_attention_decode_q8(out, query, key_cache, value_cache, key_scale, val
 
     out, query: fp16 [N][H][D]; key_cache, value_cache: int8 or float8_e4m3fn
     [NB][Hkv][bs][D]; key_scale, value_scale: fp32 [NB][Hkv] (as for
-    reshape_and_cache_q8); block_tables: int32 [N][MB]; context_lens: int32 [N]; selected: int32 [N][Hkv][K] and
-    num_selected: int32 [N][Hkv], or None: every block.  A workspace
-    (new_team_workspace) is allocated when None, on the call's stream."""
+    reshape_and_cache_q8); block_tables: int32 [N][MB]; context_lens: int32 [N];
+    selected: int32 [N][Hkv][K] and num_selected: int32 [N][Hkv], or None: every
+    block.  A workspace (new_team_workspace) is allocated when None, on the call's
+    stream."""
     torch = _torch()
     f16, i32 = torch.float16, torch.int32
     kind = _cache_type(key_cache, "key_cache")

@@ -62,15 +62,15 @@ __device__ __forceinline__ TouchedBlock touched_block(const TouchedParams &p, in
         int lo = 0, hi = p.num_seqs;
         while (hi - lo > 1) {
             const int step = (hi - lo + 7) >> 3;
-            int first[7], n = 0;
+            int begin[7], before = 0;
 #pragma unroll
-            for (int k = 0; k < 7; ++k) first[k] = touched_start(p, min(lo + (k + 1) * step, p.num_seqs - 1));
+            for (int k = 0; k < 7; ++k) begin[k] = touched_start(p, min(lo + (k + 1) * step, p.num_seqs - 1));
 #pragma unroll
             for (int k = 0; k < 7; ++k) {
                 const int at = lo + (k + 1) * step;
-                n += at < hi && (first[k] >> p.block_shift) + 2 * (int64_t)at <= u;
+                before += at < hi && (begin[k] >> p.block_shift) + 2 * (int64_t)at <= u;
             }
-            lo += n * step;
+            lo += before * step;
             hi = min(hi, lo + step);
         }
         s = lo;
