@@ -24,6 +24,9 @@ upcast exactly.  Modules:
                        copies.
 * ``block_manager`` -- the block manager (free list, reference counts,
                        on-demand append, fork, copy-on-write, release).
+* ``q8``            -- the cache in 8 bits: the write's codes and scales, the
+                       decode over them or over listed blocks, the blocks' key
+                       bounds and the choice of blocks.
 * ``accounting``    -- block counts, slot waste and KV bytes per token.
 
 Every function is pinned by ``tests/test_oracle_*.py`` to values the pages
