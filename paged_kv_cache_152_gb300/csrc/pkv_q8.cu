@@ -16,11 +16,11 @@
 // (packed fp32 arithmetic), the blocks found from query_starts by a search in
 // eighths.
 //
-// Measured: four prompts of 1000 to 4001 tokens, 8 heads of 128, 16.1 us, 3680 GB/s,
-// 0.54 of the copy bandwidth (with fp32 divisions for the codes and a search in
+// Measured: four prompts of 1000 to 4001 tokens, 8 heads of 128, 15.7 us, 3780 GB/s,
+// 0.56 of the copy bandwidth (with fp32 divisions for the codes and a search in
 // halves 25.1).  Not HBM but instructions bound it: 66% of the issue slots, of which
 // the conversions from fp16 and to the codes are the slowest.  64 single tokens of
-// 8 heads 4.5 us, three dependent look-ups behind a launch.
+// 8 heads 4.4 us, three dependent look-ups behind a launch.
 #include <cuda_runtime.h>
 
 #include "../../include/pkv.h"
@@ -118,15 +118,18 @@ __device__ __forceinline__ uint32_t finite_bits(uint32_t v) {
     return m & __vcmpltu2(m, 0x7c007c00u);
 }
 
-constexpr int kThreads = 256;
 constexpr int kVecs = 8;  // vectors of 8 elements per thread
+// Threads of a CTA, 64, 128 and 256: four prompts 15.7, 15.7 and 16.2 us, 64 single tokens 4.4, 4.4 and 4.6.
+constexpr int kLeastWriteThreads = 128;
+template <int TILE>
+constexpr int kWriteThreads = TILE > kLeastWriteThreads ? TILE : kLeastWriteThreads;
 
 // TILE threads per tile.
 template <bool E4M3, int D, int TILE>
-__global__ void __launch_bounds__(kThreads) write_q8_kernel(const __grid_constant__ WriteParams p) {
-    constexpr int kPerRow = D / 8, kTiles = kThreads / TILE;
+__global__ void __launch_bounds__(kWriteThreads<TILE>) write_q8_kernel(const __grid_constant__ WriteParams p) {
+    constexpr int kPerRow = D / 8, kTiles = kWriteThreads<TILE> / TILE;
     constexpr float kTop = Codes<E4M3>::kTop;
-    __shared__ uint32_t tops[kThreads / 32];
+    __shared__ uint32_t tops[kWriteThreads<TILE> / 32];
     touched_ask(p.t);
     grid_dependency_wait();
     launch_dependents();
@@ -249,16 +252,19 @@ struct BoundsParams {
 // rows at a time, eight loads ahead.  Nothing meets in shared memory: what the lanes
 // of one channel have is joined by shuffles.  Bound by HBM for prompts, whose blocks'
 // rows are read once, and its latency: those of two prompts of 8000 and 16384 tokens,
-// 8 heads of 128, fp16, 12.0 us, 4400 GB/s, 0.65 of the copy bandwidth; the last
-// blocks of 64 sequences 4.1 us.
+// 8 heads of 128, fp16, 11.5 us, 4590 GB/s, 0.68 of the copy bandwidth; the last
+// blocks of 64 sequences 3.7 us.
+// Threads of a CTA, 32, 64, 128 and 256: prompts 11.4, 11.5, 11.9 and 12.1 us, single tokens 3.7, 3.7, 3.9 and 4.1.
+constexpr int kBoundsThreads = 64;
+
 template <int TYPE, int D>
-__global__ void __launch_bounds__(kThreads) key_bounds_kernel(const __grid_constant__ BoundsParams p) {
+__global__ void __launch_bounds__(kBoundsThreads) key_bounds_kernel(const __grid_constant__ BoundsParams p) {
     constexpr int kPerRow = D / 8, kRows = 32 / kPerRow, kAhead = 8;
     touched_ask(p.t);
     grid_dependency_wait();
     launch_dependents();
     const int lane = threadIdx.x % 32, row = lane / kPerRow, col = lane % kPerRow;
-    const int64_t tile = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    const int64_t tile = (int64_t)blockIdx.x * (kBoundsThreads / 32) + threadIdx.x / 32;
     if (tile >= p.tiles) return;
     const int64_t unit = div_nonneg(tile, p.num_kv_heads);
     const int head = (int)(tile - unit * p.num_kv_heads);
@@ -355,9 +361,9 @@ int sequences(TouchedParams &t, const int32_t *block_tables, int max_blocks_per_
     return PKV_OK;
 }
 
-int launch(const void *fn, int64_t blocks, void **args, pkv_stream_t stream) {
+int launch(const void *fn, int64_t blocks, int threads, void **args, pkv_stream_t stream) {
     if (blocks > INT32_MAX) return PKV_ERR_INVALID_ARG;
-    if (launch_pdl(fn, dim3((unsigned)blocks), dim3(kThreads), 0, stream, args) != cudaSuccess) {
+    if (launch_pdl(fn, dim3((unsigned)blocks), dim3((unsigned)threads), 0, stream, args) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
     }
@@ -404,8 +410,8 @@ extern "C" int pkv_reshape_and_cache_q8(const void *key, int64_t key_stride, con
     const void *fn = head_dim == 64 ? (e4m3 ? write_kernel<true, 64>(block_size) : write_kernel<false, 64>(block_size))
                                     : (e4m3 ? write_kernel<true, 128>(block_size) : write_kernel<false, 128>(block_size));
     void *args[] = {&p};
-    const int64_t per = kThreads / tile;
-    return launch(fn, (p.tiles + per - 1) / per, args, stream);
+    const int threads = tile > kLeastWriteThreads ? tile : kLeastWriteThreads, per = threads / tile;
+    return launch(fn, (p.tiles + per - 1) / per, threads, args, stream);
 }
 
 extern "C" int pkv_block_key_bounds(void *key_bounds, const void *key_cache, const float *key_scale,
@@ -430,7 +436,7 @@ extern "C" int pkv_block_key_bounds(void *key_bounds, const void *key_cache, con
     p.num_kv_heads = num_kv_heads;
     p.tiles = touched_units(num_tokens, num_seqs, p.t.block_shift, query_starts != nullptr) * num_kv_heads;
     void *args[] = {&p};
-    constexpr int64_t per = kThreads / 32;
+    constexpr int64_t per = kBoundsThreads / 32;
     return launch(head_dim == 64 ? bounds_kernel<64>(cache_type) : bounds_kernel<128>(cache_type),
-                  (p.tiles + per - 1) / per, args, stream);
+                  (p.tiles + per - 1) / per, kBoundsThreads, args, stream);
 }
