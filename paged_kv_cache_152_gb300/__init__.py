@@ -872,21 +872,27 @@ def new_select_workspace(num_seqs, num_kv_heads, max_blocks_per_seq, device="cud
                        device=device)
 
 
-def _scratch(workspace, size, index, device, stream):
-    """(tensor, address, bytes) of the caller's workspace, or of a new one of
-    `size` bytes.  A new one belongs to the stream that uses it: freed on return,
-    it then goes to that stream's later work only."""
-    if workspace is None:
-        torch = _torch()
-        if stream is None:
-            workspace = torch.empty(size, dtype=torch.uint8, device=device)
-        else:
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(size, dtype=torch.uint8, device=device)
-        return workspace, workspace.data_ptr(), size
-    if _checked(((workspace, workspace.dtype, "workspace", workspace.dim()),)) != index:
-        raise ValueError("the device tensors of one call must all be on the same CUDA device")
-    return workspace, workspace.data_ptr(), workspace.nbytes
+def _launch_scratch(fn, what, index, stream, args, workspace, size, status):
+    """_launch of a call that ends in workspace, workspace_bytes, dev_status: the
+    caller's workspace, or `size` bytes of torch's allocator.  Those belong to the
+    stream that uses them: freed after the launch, they go to that stream's later
+    work only.  (Raw bytes: beside a launch, a tensor costs 3 us more host time.)"""
+    status = _status_address(status, index)
+    if workspace is not None:
+        if _checked(((workspace, workspace.dtype, "workspace", workspace.dim()),)) != index:
+            raise ValueError("the device tensors of one call must all be on the same CUDA device")
+        _launch(fn, what, index, stream, args + (workspace.data_ptr(), workspace.nbytes, status))
+        return
+    raw = _torch()._C
+
+    def with_bytes(*args):
+        address = raw._cuda_cudaCachingAllocator_raw_alloc(size, args[-1])
+        try:
+            return fn(*args[:-1], address, size, status, args[-1])
+        finally:
+            raw._cuda_cudaCachingAllocator_raw_delete(address)
+
+    _launch(with_bytes, what, index, stream, args)
 
 
 def _cache_type(t, name, f16=False):
@@ -1003,12 +1009,11 @@ def paged_attention_decode_q8(out, query, key_cache, value_cache, key_scale, val
     if n == 0:
         return out
     size = _team_workspace(h, hkv, d, num_ctas, index) if workspace is None else 0
-    workspace, ws, ws_bytes = _scratch(workspace, size, index, query.device, stream)
-    _launch(load().pkv_paged_attention_decode_q8, "pkv_paged_attention_decode_q8", index, stream,
-            (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), key_scale.data_ptr(),
-             value_scale.data_ptr(), scale_stride, block_tables.data_ptr(), block_tables.shape[1],
-             context_lens.data_ptr(), _address(selected), _address(num_selected), keep, n, h, hkv, d, bs, nb, kind, float(scale),
-             int(num_ctas), ws, ws_bytes, _status_address(status, index)))
+    _launch_scratch(load().pkv_paged_attention_decode_q8, "pkv_paged_attention_decode_q8", index, stream,
+                    (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), key_scale.data_ptr(),
+                     value_scale.data_ptr(), scale_stride, block_tables.data_ptr(), block_tables.shape[1],
+                     context_lens.data_ptr(), _address(selected), _address(num_selected), keep, n, h, hkv, d, bs, nb,
+                     kind, float(scale), int(num_ctas)), workspace, size, status)
     return out
 
 
@@ -1037,11 +1042,10 @@ def paged_attention_decode_selected(out, query, key_cache, value_cache, block_ta
     if n == 0:
         return out
     size = _team_workspace(h, hkv, d, num_ctas, index) if workspace is None else 0
-    workspace, ws, ws_bytes = _scratch(workspace, size, index, query.device, stream)
-    _launch(load().pkv_paged_attention_decode_selected, "pkv_paged_attention_decode_selected", index, stream,
-            (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
-             block_tables.shape[1], context_lens.data_ptr(), selected.data_ptr(), num_selected.data_ptr(), keep, n, h,
-             hkv, d, bs, nb, float(scale), int(num_ctas), ws, ws_bytes, _status_address(status, index)))
+    _launch_scratch(load().pkv_paged_attention_decode_selected, "pkv_paged_attention_decode_selected", index, stream,
+                    (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
+                     block_tables.shape[1], context_lens.data_ptr(), selected.data_ptr(), num_selected.data_ptr(), keep, n, h,
+                     hkv, d, bs, nb, float(scale), int(num_ctas)), workspace, size, status)
     return out
 
 
@@ -1108,11 +1112,10 @@ def select_blocks(selected, num_selected, query, key_bounds, block_tables, conte
     if n == 0:
         return selected, num_selected
     size = _select_workspace(n, hkv, mb) if workspace is None else 0
-    workspace, ws, ws_bytes = _scratch(workspace, size, index, query.device, stream)
-    _launch(load().pkv_select_blocks, "pkv_select_blocks", index, stream,
-            (selected.data_ptr(), num_selected.data_ptr(), query.data_ptr(), key_bounds.data_ptr(),
-             block_tables.data_ptr(), mb, context_lens.data_ptr(), n, h, hkv, d, int(block_size), nb,
-             selected.shape[2], int(first_blocks), int(last_blocks), ws, ws_bytes, _status_address(status, index)))
+    _launch_scratch(load().pkv_select_blocks, "pkv_select_blocks", index, stream,
+                    (selected.data_ptr(), num_selected.data_ptr(), query.data_ptr(), key_bounds.data_ptr(),
+                     block_tables.data_ptr(), mb, context_lens.data_ptr(), n, h, hkv, d, int(block_size), nb,
+                     selected.shape[2], int(first_blocks), int(last_blocks)), workspace, size, status)
     return selected, num_selected
 
 

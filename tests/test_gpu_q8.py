@@ -402,6 +402,37 @@ def test_streams_graphs_and_workspaces(pkv):
     c.check(c.out)
 
 
+def test_captured_without_a_workspace(pkv):
+    """The captured calls' scratch stays theirs: eager calls and tensors of its
+    size, between and beside the replays, on the same stream and on another."""
+    c, d = Case(36, "int8", 8, 2, 128, 16, [3000, 40, 2000]).gpu(), Case(37, "fp16", 8, 1, 128, 32, [4000, 77]).pick(60).gpu()
+    expect, expect_d = c.oracle(), d.oracle()
+    c.call(pkv)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.call(pkv)
+        between = torch.full((pkv.decode_team_workspace_size(8, 2, 128),), 0x7f, dtype=torch.uint8, device="cuda")
+        d.call(pkv)
+    e = Case(38, "e4m3", 4, 4, 64, 16, [2500, 1, 900]).gpu()
+    expect_e = e.oracle()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        c.out.fill_(-77)
+        d.out.fill_(-77)
+        beside = [torch.full((1 << 18,), 0xff, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        e.call(pkv, stream=side)
+        graph.replay()
+        e.call(pkv, stream=side)
+        del beside
+    torch.cuda.synchronize()
+    c.check(c.out, expect)
+    d.check(d.out, expect_d)
+    e.check(e.out, expect_e)
+    assert bool((between == 0x7f).all())
+
+
 def test_two_streams_at_once(pkv):
     """Calls that run at the same time, each with a workspace of its own."""
     cases = [Case(31, "int8", 8, 2, 128, 16, [3000, 40, 2000]).gpu(), Case(32, "e4m3", 4, 4, 64, 16, [2500, 1, 900]).gpu(),
