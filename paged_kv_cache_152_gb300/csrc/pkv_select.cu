@@ -227,6 +227,8 @@ struct KeepScratch {
     double list64[kList];
     int keep[kList];
     int list_n;
+    int few_n;
+    uint32_t few[kList], found;
 };
 
 // Sums over the CTA of four counts, the same on all threads; `turn` alternates.
@@ -380,7 +382,7 @@ __device__ float keep_slowly(const SelectParams &p, KeepScratch &sh, int &turn, 
 
 // A CTA keeps the blocks of one (sequence, KV head) of more than max_selected.  score, reach: its blocks' scores and its
 // tiles' reach; thread t holds the scores t, t + 128, ... of up to VALUES * 128 blocks (VALUES 0: any number, in global
-// memory).  The need-th largest is found two bits of its key at a time.
+// memory).  The need-th largest is found two bits of its key at a time, until at most 128 keys have those bits.
 template <int D, int VALUES>
 __device__ __forceinline__ void keep_blocks(const SelectParams &p, KeepScratch &sh, int4 *places, int s, int kvh, int count,
                                             const float *score, const float *reach) {
@@ -395,7 +397,7 @@ __device__ __forceinline__ void keep_blocks(const SelectParams &p, KeepScratch &
     for (int i = tid; i < p.last_blocks; i += kKeepThreads) out[kept - p.last_blocks + i] = count - p.last_blocks + i;
     if (need == 0) return;
     int turn = 0;
-    if (tid == 0) sh.list_n = 0;
+    if (tid == 0) sh.list_n = sh.few_n = 0;
 
     float v[VALUES < 1 ? 1 : VALUES];
 #pragma unroll
@@ -436,7 +438,8 @@ __device__ __forceinline__ void keep_blocks(const SelectParams &p, KeepScratch &
         // ---- the need-th largest key ----
         const int same = __clz(high ^ low) & ~1;  // leading bits, an even number (32: all)
         uint32_t key = same == 0 ? 0 : high & ~(uint32_t)((1ull << (32 - same)) - 1);
-        for (int bit = 30 - same; bit >= 0; bit -= 2) {
+        int bit = 30 - same, above = 0, within = m;  // keys past key + 2^(bit + 2), and from key up to it
+        for (; bit >= 0 && within > kList; bit -= 2) {
             const uint32_t one = key + (1u << bit), two = key + (2u << bit), three = key + (3u << bit);
             int4 n = make_int4(0, 0, 0, 0);
 #pragma unroll
@@ -447,7 +450,31 @@ __device__ __forceinline__ void keep_blocks(const SelectParams &p, KeepScratch &
                 n.z += k >= three;
             }
             n = cta_sums(n, sh, turn);
+            const int all = above + within;
             key = n.z >= need ? three : n.y >= need ? two : n.x >= need ? one : key;
+            within = n.z >= need ? n.z - above : n.y >= need ? n.y - n.z : n.x >= need ? n.x - n.y : all - n.x;
+            above = n.z >= need ? above : n.y >= need ? n.z : n.x >= need ? n.y : n.x;
+        }
+        if (bit >= 0) {  // few are left: ranked
+            const uint32_t span = (uint32_t)((4ull << bit) - 1);
+#pragma unroll
+            for (int j = 0; j < VALUES; ++j) {
+                const uint32_t k = order32(v[j]);
+                if (j * kKeepThreads + tid < m && k >= key && k - key <= span) sh.few[atomicAdd(&sh.few_n, 1)] = k;
+            }
+            __syncthreads();
+            const int few = sh.few_n;
+            if (tid < few) {
+                const uint32_t mine = sh.few[tid];
+                int more = 0, alike = 0;
+                for (int j = 0; j < few; ++j) {
+                    more += sh.few[j] > mine;
+                    alike += sh.few[j] == mine;
+                }
+                if (above + more < need && above + more + alike >= need) sh.found = mine;
+            }
+            __syncthreads();
+            key = sh.found;
         }
         const float last = unorder32(key);
         // ---- the blocks about the border ----
