@@ -312,15 +312,18 @@ def _checked(specs):
     raise ValueError("the device tensors of one call must all be on the same CUDA device")
 
 
+def _stream_handle(torch, index, stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    return stream.cuda_stream
+
+
 def _launch(fn, what, index, stream, args):
     """fn(*args, stream handle) with device `index` current."""
     import torch
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
-    elif stream.device.index != index:
-        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
-    else:
-        handle = stream.cuda_stream
+    handle = _stream_handle(torch, index, stream)
     if torch._C._cuda_getDevice() == index:
         rc = fn(*args, handle)
     else:
@@ -877,22 +880,29 @@ def _launch_scratch(fn, what, index, stream, args, workspace, size, status):
     caller's workspace, or `size` bytes of torch's allocator.  Those belong to the
     stream that uses them: freed after the launch, they go to that stream's later
     work only.  (Raw bytes: beside a launch, a tensor costs 3 us more host time.)"""
+    import torch
     status = _status_address(status, index)
     if workspace is not None:
         if _checked(((workspace, workspace.dtype, "workspace", workspace.dim()),)) != index:
             raise ValueError("the device tensors of one call must all be on the same CUDA device")
         _launch(fn, what, index, stream, args + (workspace.data_ptr(), workspace.nbytes, status))
         return
-    raw = _torch()._C
+    handle = _stream_handle(torch, index, stream)
+    if torch._C._cuda_getDevice() == index:
+        rc = _call_with_bytes(torch._C, fn, args, size, status, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = _call_with_bytes(torch._C, fn, args, size, status, handle)
+    if rc != PKV_OK:
+        _check(rc, what)
 
-    def with_bytes(*args):
-        address = raw._cuda_cudaCachingAllocator_raw_alloc(size, args[-1])
-        try:
-            return fn(*args[:-1], address, size, status, args[-1])
-        finally:
-            raw._cuda_cudaCachingAllocator_raw_delete(address)
 
-    _launch(with_bytes, what, index, stream, args)
+def _call_with_bytes(raw, fn, args, size, status, handle):
+    address = raw._cuda_cudaCachingAllocator_raw_alloc(size, handle)
+    try:
+        return fn(*args, address, size, status, handle)
+    finally:
+        raw._cuda_cudaCachingAllocator_raw_delete(address)
 
 
 def _cache_type(t, name, f16=False):
@@ -908,31 +918,34 @@ def _cache_type(t, name, f16=False):
                     f"got {t.dtype}")
 
 
-def _scale_spec(t, name):
-    """The spec of an 8-bit cache's scales, fp32 [NB][Hkv], which may be the first
-    columns of wider rows."""
-    if t.dtype is not _torch().float32:
-        raise TypeError(f"{name}: expected torch.float32, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected 2 dims, got {tuple(t.shape)}")
+def _scale_spec(t, f32, name):
+    """_checked's spec of an 8-bit cache's scales, which leaves the layout to
+    _scale_stride."""
+    if t.is_contiguous():
+        return (t, f32, name, 2)
+    if t.dtype is not f32:
+        raise TypeError(f"{name}: expected {f32}, got {t.dtype}")
     return (t, None, name, 2)
 
 
-def _scale_stride(nb, hkv, *scales):
-    """Floats between the rows of one cache's scales."""
-    if all([t.shape == (nb, hkv) and t.is_contiguous() for t in scales]):
-        return hkv
-    for t in scales:
+def _scale_stride(nb, hkv, **scales):
+    """Floats between the rows of one cache's scales, fp32 [NB][Hkv], which may be
+    the first columns of wider rows."""
+    close = True
+    for name, t in scales.items():
         if t.shape != (nb, hkv):
-            raise ValueError("key_scale, value_scale: inconsistent shapes")
-        if hkv > 1 and t.stride(1) != 1:
-            raise ValueError("key_scale, value_scale: a block's scales must be contiguous")
+            raise ValueError(f"{name}: inconsistent shapes")
+        close = close and t.is_contiguous()
+    if close:
+        return hkv
+    strides = [t.stride(0) for t in scales.values()]
+    if hkv > 1 and any(t.stride(1) != 1 for t in scales.values()):
+        raise ValueError("key_scale, value_scale: a block's scales must be contiguous")
     if nb < 2:
         return hkv
-    stride = scales[0].stride(0)
-    if stride < hkv or stride > 0x7fffffff or scales[-1].stride(0) != stride:
+    if strides[0] < hkv or strides[0] > 0x7fffffff or strides[-1] != strides[0]:
         raise ValueError("key_scale, value_scale: rows must be equally far apart in both and must not overlap")
-    return stride
+    return strides[0]
 
 
 @_traced
@@ -952,8 +965,8 @@ def reshape_and_cache_q8(key, value, key_cache, value_cache, key_scale, value_sc
     sk, sv = _rows(key, "key", f16), _rows(value, "value", f16)
     kind = _cache_type(key_cache, "key_cache")
     specs = ((key, None, "key", 3), (value, None, "value", 3), (key_cache, key_cache.dtype, "key_cache", 4),
-             (value_cache, key_cache.dtype, "value_cache", 4), _scale_spec(key_scale, "key_scale"),
-             _scale_spec(value_scale, "value_scale"), (block_tables, i32, "block_tables", 2),
+             (value_cache, key_cache.dtype, "value_cache", 4), _scale_spec(key_scale, torch.float32, "key_scale"),
+             _scale_spec(value_scale, torch.float32, "value_scale"), (block_tables, i32, "block_tables", 2),
              (context_lens, i32, "context_lens", 1))
     if query_starts is not None:
         specs += ((query_starts, i32, "query_starts", 1),)
@@ -961,7 +974,7 @@ def reshape_and_cache_q8(key, value, key_cache, value_cache, key_scale, value_sc
     t, hkv, d = rows = key.shape
     nb, hkv2, bs, d2 = pool = key_cache.shape
     n, mb = block_tables.shape
-    scale_stride = _scale_stride(nb, hkv2, key_scale, value_scale)
+    scale_stride = _scale_stride(nb, hkv2, key_scale=key_scale, value_scale=value_scale)
     if value.shape != rows or hkv2 != hkv or d2 != d or value_cache.shape != pool or context_lens.shape != (n,) \
             or (t != n if query_starts is None else query_starts.shape != (n + 1,)):
         raise ValueError("inconsistent shapes")
@@ -987,8 +1000,8 @@ def paged_attention_decode_q8(out, query, key_cache, value_cache, key_scale, val
     f16, i32 = torch.float16, torch.int32
     kind = _cache_type(key_cache, "key_cache")
     specs = ((query, f16, "query", 3), (out, f16, "out", 3), (key_cache, key_cache.dtype, "key_cache", 4),
-             (value_cache, key_cache.dtype, "value_cache", 4), _scale_spec(key_scale, "key_scale"),
-             _scale_spec(value_scale, "value_scale"), (block_tables, i32, "block_tables", 2),
+             (value_cache, key_cache.dtype, "value_cache", 4), _scale_spec(key_scale, torch.float32, "key_scale"),
+             _scale_spec(value_scale, torch.float32, "value_scale"), (block_tables, i32, "block_tables", 2),
              (context_lens, i32, "context_lens", 1))
     if (selected is None) != (num_selected is None):
         raise ValueError("selected and num_selected go together")
@@ -997,7 +1010,7 @@ def paged_attention_decode_q8(out, query, key_cache, value_cache, key_scale, val
     index = _checked(specs)
     n, h, d = rows = query.shape
     nb, hkv, bs, d2 = pool = key_cache.shape
-    scale_stride = _scale_stride(nb, hkv, key_scale, value_scale)
+    scale_stride = _scale_stride(nb, hkv, key_scale=key_scale, value_scale=value_scale)
     if out.shape != rows or d2 != d or value_cache.shape != pool or block_tables.shape[0] != n \
             or context_lens.shape != (n,):
         raise ValueError("inconsistent shapes")
@@ -1072,14 +1085,14 @@ def block_key_bounds(key_bounds, key_cache, block_tables, context_lens, query_st
     if query_starts is not None:
         specs += ((query_starts, i32, "query_starts", 1),)
     if key_scale is not None:
-        specs += (_scale_spec(key_scale, "key_scale"),)
+        specs += (_scale_spec(key_scale, torch.float32, "key_scale"),)
     index = _checked(specs)
     nb, hkv, bs, d = key_cache.shape
     n, mb = block_tables.shape
     if key_bounds.shape != (nb, hkv, 2, d) or context_lens.shape != (n,) \
             or (query_starts is not None and query_starts.shape != (n + 1,)):
         raise ValueError("inconsistent shapes")
-    scale_stride = 0 if key_scale is None else _scale_stride(nb, hkv, key_scale)
+    scale_stride = 0 if key_scale is None else _scale_stride(nb, hkv, key_scale=key_scale)
     _launch(load().pkv_block_key_bounds, "pkv_block_key_bounds", index, stream,
             (key_bounds.data_ptr(), key_cache.data_ptr(), _address(key_scale), scale_stride, block_tables.data_ptr(),
              mb, context_lens.data_ptr(), _address(query_starts), n if num_tokens is None else int(num_tokens), n, hkv, d,

@@ -245,3 +245,35 @@ def test_team_schedule(tmp_path):
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout + r.stderr
     assert "team schedule ok" in r.stdout
+
+
+def test_scratch_is_given_back():
+    """A call's scratch goes back to the allocator, of the call's stream, whether
+    the library takes the call, refuses it or ctypes does."""
+    class Allocator:
+        def __init__(self):
+            self.out, self.asked = set(), []
+
+        def _cuda_cudaCachingAllocator_raw_alloc(self, size, stream):
+            self.asked.append((size, stream))
+            self.out.add(512 * len(self.asked))
+            return 512 * len(self.asked)
+
+        def _cuda_cudaCachingAllocator_raw_delete(self, address):
+            self.out.remove(address)
+
+    raw, seen = Allocator(), []
+
+    def call(*args):
+        assert raw.out == {args[2]}
+        seen.append(args)
+        if args[0] == "raise":
+            raise TypeError("argument 1")
+        return args[0]
+
+    assert pkv._call_with_bytes(raw, call, (0, 7), 4096, 99, 5) == 0
+    assert pkv._call_with_bytes(raw, call, (3, 7), 256, None, 6) == 3
+    with pytest.raises(TypeError):
+        pkv._call_with_bytes(raw, call, ("raise", 7), 256, None, 6)
+    assert seen == [(0, 7, 512, 4096, 99, 5), (3, 7, 1024, 256, None, 6), ("raise", 7, 1536, 256, None, 6)]
+    assert raw.asked == [(4096, 5), (256, 6), (256, 6)] and not raw.out
