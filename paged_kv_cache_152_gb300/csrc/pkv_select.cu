@@ -23,9 +23,10 @@
 //
 // Measured: 8 contexts of 8000 to 32768 tokens, blocks of 32, 8 KV heads 13.2 us (the
 // 23 MB of bounds need 3.4 of them; the rest is latency: look-ups, one round of
-// loads, the meeting in the first CTA, a few rounds of a sum over it for the border, the
-// list; 13.9 with as many rounds as the border's key has pairs of bits); 64 contexts of 4000 to 16384, blocks of 16, 42 us, 3900 GB/s, 0.58 of the
-// copy bandwidth (all CTAs run at once, so the longest contexts' end the call; choosing
+// loads, the meeting in the first CTA, a few rounds of a sum over it for the border,
+// the list; 13.9 with as many rounds as the border's key has pairs of bits); 64
+// contexts of 4000 to 16384, blocks of 16, 42 us, 3900 GB/s, 0.58 of the copy
+// bandwidth (all CTAs run at once, so the longest contexts' end the call; choosing
 // takes the last 6 us).  Scoring by persistent warps over all segments and choosing in
 // a second kernel took 48 there; queries in shared memory instead of registers, for
 // six CTAs an SM instead of four, 57.

@@ -309,3 +309,54 @@ def test_the_path_step_by_step(pkv, kind):
         got = out.double().cpu().numpy()
         more = G.biased(q, o_scales[0], tables, ln, bs, 0.125) if kind == "int8" else 0.0
         assert (np.abs(got - expect) <= G.bound(expect, spread, reach, seen, top, d, 4, more)).all()
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp16"])
+def test_the_path_past_32_bits(pkv, kind):
+    """Write, bounds, choice and decode in blocks whose codes and bounds lie past
+    2^32 bytes: the bits of the same blocks in a small pool."""
+    h, hkv, d, bs, keep = 8, 8, 128, 8, 9
+    rng = np.random.default_rng(32)
+    lens, dtype = [150, 33, 8], G.DTYPE[kind]
+    tables = np.full((3, 20), -1, np.int32)
+    order = rng.permutation(40)
+    at = 0
+    for s, n in enumerate(lens):
+        m = -(-n // bs)
+        tables[s, :m] = order[at:at + m]
+        at += m
+    rows = [torch.from_numpy(rng.standard_normal((sum(lens), hkv, d)).astype(np.float16)).cuda() for _ in range(2)]
+    q = torch.from_numpy(rng.standard_normal((3, h, d)).astype(np.float16)).cuda()
+    g_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, *np.cumsum(lens)], dtype=torch.int32, device="cuda")
+
+    def path(first):
+        nb = first + 40
+        kc, vc = (torch.empty(nb, hkv, bs, d, device="cuda", dtype=dtype) for _ in range(2))
+        kc[first:], vc[first:] = 0, 0
+        ks, vs = (torch.zeros(nb, hkv, device="cuda") for _ in range(2))
+        bounds = torch.empty(nb, hkv, 2, d, dtype=torch.float16, device="cuda")
+        bounds[first:] = 0
+        g_tables = torch.from_numpy(np.where(tables < 0, -1, tables + first).astype(np.int32)).cuda()
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        if kind == "fp16":
+            slots = [(int(tables[s][p // bs]) + first) * bs + p % bs for s in range(3) for p in range(lens[s])]
+            pkv.reshape_and_cache(*rows, kc, vc, torch.tensor(slots, device="cuda"), status=status)
+        else:
+            pkv.reshape_and_cache_q8(*rows, kc, vc, ks, vs, g_tables, g_lens, starts, status=status)
+        pkv.block_key_bounds(bounds, kc, g_tables, g_lens, starts, sum(lens), key_scale=None if kind == "fp16" else ks,
+                             status=status)
+        selected = torch.zeros(3, hkv, keep, dtype=torch.int32, device="cuda")
+        number = torch.zeros(3, hkv, dtype=torch.int32, device="cuda")
+        pkv.select_blocks(selected, number, q, bounds, g_tables, g_lens, bs, status=status)
+        out = torch.empty_like(q)
+        if kind == "fp16":
+            pkv.paged_attention_decode_selected(out, q, kc, vc, g_tables, g_lens, selected, number, 0.125, status=status)
+        else:
+            pkv.paged_attention_decode_q8(out, q, kc, vc, ks, vs, g_tables, g_lens, 0.125, selected=selected,
+                                          num_selected=number, status=status)
+        assert int(status.item()) == 0
+        return [x[first:].clone().view(torch.uint8) for x in (kc, vc, ks, vs, bounds)] + [selected, number, out]
+
+    for near, far in zip(path(0), path((1 << 20) + 24)):
+        assert torch.equal(near, far)
