@@ -62,7 +62,7 @@ struct SelectParams {
     const int32_t *block_tables;
     const int32_t *context_lens;
     float *score;                 // [N][Hkv][row]
-    double *score64;              // [N][Hkv][row]
+    uint64_t *score64;            // [N][Hkv][row]: exact_score's keys
     float *reach;                 // [N][Hkv][row / 16]: the largest finite |bound| of 16 blocks
     int32_t *status;
     int64_t row;                  // max_blocks_per_seq rounded up to 16
@@ -213,23 +213,18 @@ __device__ __forceinline__ uint32_t order32(float v) {
 __device__ __forceinline__ float unorder32(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
-__device__ __forceinline__ uint64_t order64(double v) {
-    const uint64_t b = (uint64_t)__double_as_longlong(v);
-    return b ^ ((b >> 63) ? ~0ull : 1ull << 63);
-}
-
 constexpr int kKeepThreads = 128;
 constexpr int kKeepWarps = kKeepThreads / 32;
-constexpr int kList = 128;  // candidates ranked in one step
+constexpr int kList = 128;  // candidates at the border ranked in one step
 
 struct KeepScratch {
     int sums[2][kKeepWarps][4];  // two sets in turn, so that a sum takes one barrier
     int list[kList];
-    double list64[kList];
+    uint64_t list64[kList];
     int keep[kList];
     int list_n;
     int few_n;
-    uint32_t few[kList], found;
+    uint32_t few[32], found;
 };
 
 // Sums over the CTA of four counts, the same on all threads; `turn` alternates.
@@ -256,14 +251,15 @@ __device__ __forceinline__ void add_exactly(float &sum, float &low, float x) {
     sum = to;
 }
 
-// The block's score as a sum of two fp32 values, off by 2^-44 of its terms' magnitudes at most, in 64 bits (the GPU has
-// few fp64 units); by a warp, lane 0's counts.
+// The block's score as a sum of two fp32 values, off by 2^-44 of its terms' magnitudes at most, as a key in the order of
+// the scores: the nearest fp32 value and what is left of it (a sum has one such pair).  (Not in fp64, of whose units the
+// GPU has few.)  By a warp.
 template <int D>
-__device__ double exact_score(const SelectParams &p, int s, int kvh, int64_t block, int lane) {
+__device__ uint64_t exact_score(const SelectParams &p, int s, int kvh, int64_t block, int lane) {
     int phys = __ldg(p.block_tables + (int64_t)s * p.max_blocks_per_seq + block);
     if (phys < 0 || phys >= p.num_blocks) phys = 0;
     const __half *hi = p.bounds + ((int64_t)phys * p.num_kv_heads + kvh) * 2 * D;
-    double best = -CUDART_INF;
+    uint64_t best = 0;
     float bounds[2][D / 32];
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) {
@@ -287,8 +283,10 @@ __device__ double exact_score(const SelectParams &p, int s, int kvh, int64_t blo
             add_exactly(sum, low, other);
             low += other_low;
         }
-        const double e = (double)sum + (double)low;
-        best = fmax(best, fabs(e) < CUDART_INF ? e : CUDART_INF);
+        float left = 0.f;
+        add_exactly(sum, left, low);
+        const uint64_t key = (uint64_t)order32(sum + 0.f) << 32 | order32(left + 0.f);  // (no -0)
+        best = max(best, fabsf(sum) < CUDART_INF_F ? key : ~(uint64_t)0);
     }
     return best;
 }
@@ -342,10 +340,10 @@ __device__ float keep_slowly(const SelectParams &p, KeepScratch &sh, int &turn, 
     const int want = need - sums.x;
     *all_near = want == sums.y;
     if (*all_near) return last - twice;
-    double *exact = p.score64 + seg * p.row;
+    uint64_t *exact = p.score64 + seg * p.row;
     for (int64_t i = warp; i < m; i += kKeepWarps)
         if (close(score[i])) {
-            const double e = exact_score<D>(p, s, kvh, m0 + i, lane);
+            const uint64_t e = exact_score<D>(p, s, kvh, m0 + i, lane);
             if (lane == 0) exact[i] = e;
         }
     __syncthreads();
@@ -354,17 +352,17 @@ __device__ float keep_slowly(const SelectParams &p, KeepScratch &sh, int &turn, 
         const uint64_t trial = key | 1ull << bit;
         int n = 0;
         for (int i = tid; i < m; i += kKeepThreads)
-            if (close(score[i])) n += order64(exact[i]) >= trial;
+            if (close(score[i])) n += exact[i] >= trial;
         if (cta_sums(make_int4(n, 0, 0, 0), sh, turn).x >= want) key = trial;
     }
     int more = 0;  // above the border's value; the first of its equals fill up
     for (int i = tid; i < m; i += kKeepThreads)
-        if (close(score[i])) more += order64(exact[i]) > key;
+        if (close(score[i])) more += exact[i] > key;
     int ties = want - cta_sums(make_int4(more, 0, 0, 0), sh, turn).x;
     for (int base = 0; base < m; base += kKeepThreads) {
         const int i = base + tid;
         const bool mine = i < m && close(score[i]);
-        const uint64_t e = mine ? order64(exact[i]) : 0;
+        const uint64_t e = mine ? exact[i] : 0;
         const unsigned mask = __ballot_sync(kFullMask, mine && e == key);
         if (lane == 0) sh.sums[turn][warp][0] = __popc(mask);
         __syncthreads();
@@ -383,7 +381,7 @@ __device__ float keep_slowly(const SelectParams &p, KeepScratch &sh, int &turn, 
 
 // A CTA keeps the blocks of one (sequence, KV head) of more than max_selected.  score, reach: its blocks' scores and its
 // tiles' reach; thread t holds the scores t, t + 128, ... of up to VALUES * 128 blocks (VALUES 0: any number, in global
-// memory).  The need-th largest is found two bits of its key at a time, until at most 128 keys have those bits.
+// memory).  The need-th largest is found two bits of its key at a time, until at most 32 keys have those bits.
 template <int D, int VALUES>
 __device__ __forceinline__ void keep_blocks(const SelectParams &p, KeepScratch &sh, int4 *places, int s, int kvh, int count,
                                             const float *score, const float *reach) {
@@ -440,7 +438,7 @@ __device__ __forceinline__ void keep_blocks(const SelectParams &p, KeepScratch &
         const int same = __clz(high ^ low) & ~1;  // leading bits, an even number (32: all)
         uint32_t key = same == 0 ? 0 : high & ~(uint32_t)((1ull << (32 - same)) - 1);
         int bit = 30 - same, above = 0, within = m;  // keys past key + 2^(bit + 2), and from key up to it
-        for (; bit >= 0 && within > kList; bit -= 2) {
+        for (; bit >= 0 && within > 32; bit -= 2) {
             const uint32_t one = key + (1u << bit), two = key + (2u << bit), three = key + (3u << bit);
             int4 n = make_int4(0, 0, 0, 0);
 #pragma unroll
@@ -458,21 +456,25 @@ __device__ __forceinline__ void keep_blocks(const SelectParams &p, KeepScratch &
         }
         if (bit >= 0) {  // few are left: ranked
             const uint32_t span = (uint32_t)((4ull << bit) - 1);
+            uint32_t mine = 0;
 #pragma unroll
-            for (int j = 0; j < VALUES; ++j) {
-                const uint32_t k = order32(v[j]);
-                if (j * kKeepThreads + tid < m && k >= key && k - key <= span) sh.few[atomicAdd(&sh.few_n, 1)] = k;
+            for (int j = 0; j < VALUES; ++j)
+                if (j * kKeepThreads + tid < m && order32(v[j]) - key <= span) mine |= 1u << j;
+            if (mine) {
+                int at = atomicAdd(&sh.few_n, __popc(mine));
+#pragma unroll
+                for (int j = 0; j < VALUES; ++j)
+                    if (mine >> j & 1) sh.few[at++] = order32(v[j]);
             }
             __syncthreads();
-            const int few = sh.few_n;
-            if (tid < few) {
-                const uint32_t mine = sh.few[tid];
-                int more = 0, alike = 0;
-                for (int j = 0; j < few; ++j) {
-                    more += sh.few[j] > mine;
-                    alike += sh.few[j] == mine;
+            if (warp == 0 && lane < sh.few_n) {
+                const uint32_t k = sh.few[lane];
+                int more = above, alike = 0;
+                for (int j = 0; j < sh.few_n; ++j) {
+                    more += sh.few[j] > k;
+                    alike += sh.few[j] == k;
                 }
-                if (above + more < need && above + more + alike >= need) sh.found = mine;
+                if (more < need && more + alike >= need) sh.found = k;
             }
             __syncthreads();
             key = sh.found;
@@ -500,13 +502,13 @@ __device__ __forceinline__ void keep_blocks(const SelectParams &p, KeepScratch &
                 if (close >> j & 1) sh.list[k++] = j * kKeepThreads + tid;
             __syncthreads();
             for (int i = warp; i < n.y; i += kKeepWarps) {
-                const double e = exact_score<D>(p, s, kvh, m0 + sh.list[i], lane);
+                const uint64_t e = exact_score<D>(p, s, kvh, m0 + sh.list[i], lane);
                 if (lane == 0) sh.list64[i] = e;
             }
             __syncthreads();
             if (tid < n.y) {
                 const int mine = sh.list[tid];
-                const double e = sh.list64[tid];
+                const uint64_t e = sh.list64[tid];
                 int before = 0;
                 for (int j = 0; j < n.y; ++j)
                     before += sh.list64[j] > e || (sh.list64[j] == e && sh.list[j] < mine);
@@ -774,7 +776,7 @@ extern "C" int pkv_select_blocks(int32_t *selected, int32_t *num_selected, const
     p.block_tables = block_tables;
     p.context_lens = context_lens;
     p.score = reinterpret_cast<float *>(wsb + ws.score);
-    p.score64 = reinterpret_cast<double *>(wsb + ws.score64);
+    p.score64 = reinterpret_cast<uint64_t *>(wsb + ws.score64);
     p.reach = reinterpret_cast<float *>(wsb + ws.reach);
     p.status = dev_status;
     p.row = ws.row;
