@@ -21,14 +21,15 @@
 // few between are scored again with twice the digits and ranked, ties to the lowest
 // index, so that the choice does not hang on the order of a sum.
 //
-// Measured: 8 contexts of 8000 to 32768 tokens, blocks of 32, 8 KV heads 13.2 us (the
-// 23 MB of bounds need 3.4 of them; the rest is latency: look-ups, one round of
-// loads, the meeting in the first CTA, a few rounds of a sum over it for the border,
-// the list; 13.9 with as many rounds as the border's key has pairs of bits); 64
-// contexts of 4000 to 16384, blocks of 16, 42 us, 3900 GB/s, 0.58 of the copy
-// bandwidth (all CTAs run at once, so the longest contexts' end the call; choosing
-// takes the last 6 us).  Scoring by persistent warps over all segments and choosing in
-// a second kernel took 48 there; queries in shared memory instead of registers, for
+// Measured: 8 contexts of 8000 to 32768 tokens, blocks of 32, 8 KV heads 11.9 us (the
+// 23 MB of bounds need 3.4 of them; all that comes before the choice, three look-ups
+// and two rounds of loads, takes 6.3; the choice is some ten steps of a CTA, each a
+// few hundred cycles of latency); 64 contexts of 4000 to 16384, blocks of 16, 40.4 us,
+// 4080 GB/s, 0.60 of the copy bandwidth (all CTAs run at once, so the longest contexts'
+// end the call; without the choice 34.2).  With the border's scores in fp64 and at most
+// 128 keys ranked instead of 32 13.2 and 42.2; with as many rounds as the keys have
+// pairs of bits 13.9.  Scoring by persistent warps over all segments and choosing in a
+// second kernel took 48 for the 64; queries in shared memory instead of registers, for
 // six CTAs an SM instead of four, 57.
 #include <cuda_runtime.h>
 #include <math_constants.h>
