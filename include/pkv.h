@@ -889,9 +889,8 @@ int pkv_block_key_bounds(void *key_bounds, const void *key_cache, const float *k
  * min(B, max_selected) are kept: the first first_blocks and the last
  * last_blocks, and of the others those with the largest scores, of equal ones
  * the lowest index.  A score that is not finite counts as the largest.  Scores
- * that fp32 sums cannot tell apart are summed again with twice the digits, off
- * by 2^-44 of their terms' magnitudes at most, before they are compared: what
- * is kept does not depend on the order of a sum.
+ * that fp32 sums may not tell apart are summed again as whole numbers of 2^-48,
+ * which all these scores are: what is kept is what the exact scores say.
  *
  *   selected      int32 [num_seqs][num_kv_heads][max_selected] (device, written):
  *                 the kept blocks' logical indices in ascending order, then -1

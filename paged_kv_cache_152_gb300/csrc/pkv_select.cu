@@ -18,17 +18,19 @@
 //
 // The choice: fp32 scores are off by E or less (below), so blocks more than 2 E
 // above the last kept score are kept and those more than 2 E below it are not; the
-// few between are scored again with twice the digits and ranked, ties to the lowest
-// index, so that the choice does not hang on the order of a sum.
+// few between are scored again as whole numbers, without any rounding, and ranked,
+// ties to the lowest index, so that the choice is that of the exact scores.
 //
-// Measured: 8 contexts of 8000 to 32768 tokens, blocks of 32, 8 KV heads 11.9 us (the
+// Measured: 8 contexts of 8000 to 32768 tokens, blocks of 32, 8 KV heads 12.1 us (the
 // 23 MB of bounds need 3.4 of them; all that comes before the choice, three look-ups
 // and two rounds of loads, takes 6.3; the choice is some ten steps of a CTA, each a
-// few hundred cycles of latency); 64 contexts of 4000 to 16384, blocks of 16, 40.4 us,
-// 4080 GB/s, 0.60 of the copy bandwidth (all CTAs run at once, so the longest contexts'
-// end the call; without the choice 34.2).  With the border's scores in fp64 and at most
-// 128 keys ranked instead of 32 13.2 and 42.2; with as many rounds as the keys have
-// pairs of bits 13.9.  Scoring by persistent warps over all segments and choosing in a
+// few hundred cycles of latency); 64 contexts of 4000 to 16384, blocks of 16, 40.6 us,
+// 4060 GB/s, 0.60 of the copy bandwidth (all CTAs run at once, so the longest contexts'
+// end the call; without the choice 34.2).  With the border's scores as pairs of fp32
+// values 11.9 and 40.4, but the second one is rounded, so that large terms that cancel
+// took the last digits with them and equal scores of other terms differed.  With them
+// in fp64 and at most 128 keys ranked instead of 32 13.2 and 42.2; with as many rounds
+// as the keys have pairs of bits 13.9.  Scoring by persistent warps over all segments and choosing in a
 // second kernel took 48 for the 64; queries in shared memory instead of registers, for
 // six CTAs an SM instead of four, 57.
 #include <cuda_runtime.h>
@@ -63,7 +65,7 @@ struct SelectParams {
     const int32_t *block_tables;
     const int32_t *context_lens;
     float *score;                 // [N][Hkv][row]
-    uint64_t *score64;            // [N][Hkv][row]: exact_score's keys
+    int64_t *score_hi;            // [N][Hkv][row]: exact_score's hi (its lo takes score's place)
     float *reach;                 // [N][Hkv][row / 16]: the largest finite |bound| of 16 blocks
     int32_t *status;
     int64_t row;                  // max_blocks_per_seq rounded up to 16
@@ -221,7 +223,8 @@ constexpr int kList = 128;  // candidates at the border ranked in one step
 struct KeepScratch {
     int sums[2][kKeepWarps][4];  // two sets in turn, so that a sum takes one barrier
     int list[kList];
-    uint64_t list64[kList];
+    int64_t list_hi[kList];
+    uint32_t list_lo[kList];
     int keep[kList];
     int list_n;
     int few_n;
@@ -245,50 +248,71 @@ __device__ __forceinline__ int4 cta_sums(int4 v, KeepScratch &sh, int &turn) {
     return sum;
 }
 
-// sum + low + x, with what rounding takes from the sum added to `low` (Knuth's two-sum).
-__device__ __forceinline__ void add_exactly(float &sum, float &low, float x) {
-    const float to = __fadd_rn(sum, x), part = __fsub_rn(to, sum);
-    low += __fadd_rn(__fsub_rn(sum, __fsub_rn(to, part)), __fsub_rn(x, part));
-    sum = to;
+// A score, exactly: an fp16 value is m 2^(e - 24) with m below 2^11 and 0 <= e <= 29, so a product of two is m 2^(e - 48)
+// with m below 2^22 and e up to 58, and a sum of 128 of them is a whole number of 2^-48 below 2^87 in size:
+// (hi 2^32 + lo) 2^-48.  No order of the sum and no rounding enters, so equal scores are equal here.
+struct ExactScore {
+    int64_t hi;
+    uint32_t lo;
+};
+constexpr int64_t kNoNumberHi = INT64_C(1) << 60;  // above every score: those that are not finite
+__device__ __forceinline__ bool exact_above(int64_t hi, uint32_t lo, int64_t hi2, uint32_t lo2) {
+    return hi > hi2 || (hi == hi2 && lo > lo2);
 }
 
-// The block's score as a sum of two fp32 values, off by 2^-44 of its terms' magnitudes at most, as a key in the order of
-// the scores: the nearest fp32 value and what is left of it (a sum has one such pair).  (Not in fp64, of whose units the
-// GPU has few.)  By a warp.
+// An fp16 value's m, with its sign, and e.
+__device__ __forceinline__ int2 half_parts(unsigned short h) {
+    const int e = h >> 10 & 31, m = (h & 0x3ff) | (e ? 0x400 : 0);
+    return make_int2(h >> 15 ? -m : m, e ? e - 1 : 0);
+}
+
+// The block's score, by a warp; the same on all lanes.
 template <int D>
-__device__ uint64_t exact_score(const SelectParams &p, int s, int kvh, int64_t block, int lane) {
+__device__ ExactScore exact_score(const SelectParams &p, int s, int kvh, int64_t block, int lane) {
     int phys = __ldg(p.block_tables + (int64_t)s * p.max_blocks_per_seq + block);
     if (phys < 0 || phys >= p.num_blocks) phys = 0;
-    const __half *hi = p.bounds + ((int64_t)phys * p.num_kv_heads + kvh) * 2 * D;
-    uint64_t best = 0;
-    float bounds[2][D / 32];
+    const unsigned short *hi = reinterpret_cast<const unsigned short *>(p.bounds) +
+                               ((int64_t)phys * p.num_kv_heads + kvh) * 2 * D;
+    unsigned short bounds[2][D / 32];
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) {
-        bounds[0][k] = __half2float(hi[k * 32 + lane]);
-        bounds[1][k] = __half2float(hi[D + k * 32 + lane]);
+        bounds[0][k] = hi[k * 32 + lane];
+        bounds[1][k] = hi[D + k * 32 + lane];
     }
+    bool finite = true;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) finite &= (bounds[0][k] & 0x7c00) != 0x7c00 && (bounds[1][k] & 0x7c00) != 0x7c00;
+    finite = __all_sync(kFullMask, finite);
+    ExactScore best = {-kNoNumberHi, 0};
 #pragma unroll 4
     for (int h = 0; h < p.group; ++h) {
-        const __half *q = p.query + ((int64_t)s * p.num_heads + (int64_t)kvh * p.group + h) * D;
-        float sum = 0.f, low = 0.f;
+        const unsigned short *q = reinterpret_cast<const unsigned short *>(p.query) +
+                                  ((int64_t)s * p.num_heads + (int64_t)kvh * p.group + h) * D;
+        int64_t low = 0, high = 0;  // low + high 2^32, each term below 2^53
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
-            const float v = __half2float(q[k * 32 + lane]);
-            // one of the two products is zero (or not a number, with a bound that is not finite); fp32 holds them exactly
-            const float a = fmaxf(v, 0.f) * bounds[0][k], b = fminf(v, 0.f) * bounds[1][k];
-            add_exactly(sum, low, v == v ? a + b : CUDART_NAN_F);
+            const unsigned short v = q[k * 32 + lane];
+            finite &= (v & 0x7c00) != 0x7c00;
+            const int2 a = half_parts(v), b = half_parts(v >> 15 ? bounds[1][k] : bounds[0][k]);
+            const int64_t x = (int64_t)(a.x * b.x) << (a.y + b.y & 31);
+            low += a.y + b.y < 32 ? x : 0;
+            high += a.y + b.y < 32 ? 0 : x;
         }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            const float other = __shfl_xor_sync(kFullMask, sum, d), other_low = __shfl_xor_sync(kFullMask, low, d);
-            add_exactly(sum, low, other);
-            low += other_low;
-        }
-        float left = 0.f;
-        add_exactly(sum, left, low);
-        const uint64_t key = (uint64_t)order32(sum + 0.f) << 32 | order32(left + 0.f);  // (no -0)
-        best = max(best, fabsf(sum) < CUDART_INF_F ? key : ~(uint64_t)0);
+        // this lane's sum, below 2^82 in size, in pieces of 26 bits that sum up over a warp in 32
+        high += low >> 32;
+        const uint32_t word = (uint32_t)low;
+        const int64_t rest = (int64_t)((uint64_t)high << 6 | word >> 26);
+        constexpr uint32_t kPiece = (1u << 26) - 1;
+        const uint32_t p0 = __reduce_add_sync(kFullMask, word & kPiece);
+        const uint32_t p1 = __reduce_add_sync(kFullMask, (uint32_t)rest & kPiece);
+        const uint32_t p2 = __reduce_add_sync(kFullMask, (uint32_t)(rest >> 26) & kPiece);
+        const int p3 = __reduce_add_sync(kFullMask, (int)(rest >> 52));
+        const uint64_t sum = p0 + ((uint64_t)p1 << 26);
+        ExactScore score = {(int64_t)(sum >> 32) + ((int64_t)p2 << 20) + (int64_t)p3 * (INT64_C(1) << 46), (uint32_t)sum};
+        if (exact_above(score.hi, score.lo, best.hi, best.lo)) best = score;
     }
+    // an infinite or missing bound or query times any other makes a sum that is not finite
+    if (!__all_sync(kFullMask, finite)) best.hi = kNoNumberHi, best.lo = 0;
     return best;
 }
 
@@ -341,30 +365,54 @@ __device__ float keep_slowly(const SelectParams &p, KeepScratch &sh, int &turn, 
     const int want = need - sums.x;
     *all_near = want == sums.y;
     if (*all_near) return last - twice;
-    uint64_t *exact = p.score64 + seg * p.row;
-    for (int64_t i = warp; i < m; i += kKeepWarps)
-        if (close(score[i])) {
-            const uint64_t e = exact_score<D>(p, s, kvh, m0 + i, lane);
-            if (lane == 0) exact[i] = e;
+    // The border's exact scores; what is surely kept or not is marked.
+    int64_t *hi = p.score_hi + seg * p.row;
+    constexpr int64_t kMarked = INT64_MIN;
+    for (int base = warp * 32; base < m; base += kKeepThreads) {
+        const int i = base + lane;
+        const float v = i < m ? score[i] : 0.f;
+        const bool mine = i < m && close(v);
+        if (i < m && !mine) {
+            hi[i] = kMarked;
+            score[i] = v > last ? CUDART_INF_F : -CUDART_INF_F;
         }
+        for (unsigned mask = __ballot_sync(kFullMask, mine); mask; mask &= mask - 1) {
+            const int b = __ffs(mask) - 1;
+            const ExactScore e = exact_score<D>(p, s, kvh, m0 + base + b, lane);
+            if (lane == b) {
+                hi[i] = e.hi;
+                score[i] = __uint_as_float(e.lo);
+            }
+        }
+    }
     __syncthreads();
+    // the want-th largest: hi's bits from an unsigned order, then lo's among its equals
+    auto key_hi = [&](int i) { return (uint64_t)hi[i] ^ (uint64_t)1 << 63; };  // (marked: 0, below every score)
     uint64_t key = 0;
     for (int bit = 63; bit >= 0; --bit) {
         const uint64_t trial = key | 1ull << bit;
         int n = 0;
-        for (int i = tid; i < m; i += kKeepThreads)
-            if (close(score[i])) n += exact[i] >= trial;
+        for (int i = tid; i < m; i += kKeepThreads) n += key_hi(i) >= trial;
         if (cta_sums(make_int4(n, 0, 0, 0), sh, turn).x >= want) key = trial;
     }
+    int past = 0;
+    for (int i = tid; i < m; i += kKeepThreads) past += key_hi(i) > key;
+    past = cta_sums(make_int4(past, 0, 0, 0), sh, turn).x;
+    uint32_t word = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t trial = word | 1u << bit;
+        int n = 0;
+        for (int i = tid; i < m; i += kKeepThreads) n += key_hi(i) == key && __float_as_uint(score[i]) >= trial;
+        if (past + cta_sums(make_int4(n, 0, 0, 0), sh, turn).x >= want) word = trial;
+    }
     int more = 0;  // above the border's value; the first of its equals fill up
-    for (int i = tid; i < m; i += kKeepThreads)
-        if (close(score[i])) more += exact[i] > key;
-    int ties = want - cta_sums(make_int4(more, 0, 0, 0), sh, turn).x;
+    for (int i = tid; i < m; i += kKeepThreads) more += key_hi(i) == key && __float_as_uint(score[i]) > word;
+    int ties = want - past - cta_sums(make_int4(more, 0, 0, 0), sh, turn).x;
     for (int base = 0; base < m; base += kKeepThreads) {
         const int i = base + tid;
-        const bool mine = i < m && close(score[i]);
-        const uint64_t e = mine ? exact[i] : 0;
-        const unsigned mask = __ballot_sync(kFullMask, mine && e == key);
+        const uint64_t k = i < m ? key_hi(i) : 0;
+        const uint32_t lo = k ? __float_as_uint(score[i]) : 0;
+        const unsigned mask = __ballot_sync(kFullMask, k == key && lo == word);
         if (lane == 0) sh.sums[turn][warp][0] = __popc(mask);
         __syncthreads();
         int place = __popc(mask & ((1u << lane) - 1)), total = 0;
@@ -373,11 +421,14 @@ __device__ float keep_slowly(const SelectParams &p, KeepScratch &sh, int &turn, 
             total += sh.sums[turn][w][0];
         }
         turn ^= 1;
-        if (mine) score[i] = e > key || (e == key && place < ties) ? CUDART_INF_F : -CUDART_INF_F;
+        if (k) {
+            const bool keep = k > key || (k == key && (lo > word || (lo == word && place < ties)));
+            score[i] = keep ? CUDART_INF_F : -CUDART_INF_F;
+        }
         ties -= min(ties, total);
     }
     __syncthreads();
-    return last + twice;
+    return 0.f;
 }
 
 // A CTA keeps the blocks of one (sequence, KV head) of more than max_selected.  score, reach: its blocks' scores and its
@@ -503,16 +554,18 @@ __device__ __forceinline__ void keep_blocks(const SelectParams &p, KeepScratch &
                 if (close >> j & 1) sh.list[k++] = j * kKeepThreads + tid;
             __syncthreads();
             for (int i = warp; i < n.y; i += kKeepWarps) {
-                const uint64_t e = exact_score<D>(p, s, kvh, m0 + sh.list[i], lane);
-                if (lane == 0) sh.list64[i] = e;
+                const ExactScore e = exact_score<D>(p, s, kvh, m0 + sh.list[i], lane);
+                if (lane == 0) sh.list_hi[i] = e.hi, sh.list_lo[i] = e.lo;
             }
             __syncthreads();
             if (tid < n.y) {
                 const int mine = sh.list[tid];
-                const uint64_t e = sh.list64[tid];
+                const int64_t hi = sh.list_hi[tid];
+                const uint32_t lo = sh.list_lo[tid];
                 int before = 0;
                 for (int j = 0; j < n.y; ++j)
-                    before += sh.list64[j] > e || (sh.list64[j] == e && sh.list[j] < mine);
+                    before += exact_above(sh.list_hi[j], sh.list_lo[j], hi, lo) ||
+                              (sh.list_hi[j] == hi && sh.list_lo[j] == lo && sh.list[j] < mine);
                 sh.keep[tid] = before < want;
             }
             __syncthreads();
@@ -715,7 +768,7 @@ cudaError_t launch_cluster(const void *fn, dim3 grid, int ctas, pkv_stream_t str
 
 // Workspace carve-up (byte offsets).  It carries nothing from call to call.
 struct SelectWorkspace {
-    size_t score, score64, reach, total;
+    size_t score, score_hi, reach, total;
     int64_t row;
     static SelectWorkspace plan(int num_seqs, int num_kv_heads, int max_blocks_per_seq) {
         auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -723,8 +776,8 @@ struct SelectWorkspace {
         w.row = ((int64_t)max_blocks_per_seq + kTileBlocks - 1) / kTileBlocks * kTileBlocks;
         const size_t n = (size_t)num_seqs * num_kv_heads * (size_t)w.row;
         w.score = 0;
-        w.score64 = up(4 * n);
-        w.reach = w.score64 + up(8 * n);
+        w.score_hi = up(4 * n);
+        w.reach = w.score_hi + up(8 * n);
         w.total = w.reach + up(4 * (n / kTileBlocks));
         return w;
     }
@@ -777,7 +830,7 @@ extern "C" int pkv_select_blocks(int32_t *selected, int32_t *num_selected, const
     p.block_tables = block_tables;
     p.context_lens = context_lens;
     p.score = reinterpret_cast<float *>(wsb + ws.score);
-    p.score64 = reinterpret_cast<uint64_t *>(wsb + ws.score64);
+    p.score_hi = reinterpret_cast<int64_t *>(wsb + ws.score_hi);
     p.reach = reinterpret_cast<float *>(wsb + ws.reach);
     p.status = dev_status;
     p.row = ws.row;
