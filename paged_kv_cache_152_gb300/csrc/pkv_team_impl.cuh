@@ -36,13 +36,11 @@
 //    from the scores' layout to the product's by movmatrix.  (One group's heads are
 //    16 rows at most: tcgen05's tiles of 64 or 128 would stay empty.  The tensor pipe
 //    is active 14% of the time, the integer pipe, which widens, most of all.)
-//  * int8 codes widen to fp16 below the normal range: the byte code ^ 0x80 is fp16's
-//    (code + 128) 2^-24, which the products take as it is.  The keys keep the 128
-//    (128 times the queries' sum is where the scores' sums begin, below zero, and the
-//    sums are of |code| + 256 instead of |code|, in fp32); off the values it is
-//    subtracted, exactly: their sums run over the whole context, and a mean of many
-//    values is small beside 128 (with a product for it instead, the outputs of
-//    contexts of 20000 had 2.5 times the error).
+//  * int8 codes widen to fp16 exactly: a byte with 0x64 above it is 1024 more than
+//    itself, off which one subtraction takes 1152 (the byte is code + 128).  Taking
+//    the 128 off the sums instead, 128 times the queries' sum at the scores' start,
+//    costs as much time (chats 49.8 us, 8 long contexts 62.9 and 63.0) and the digits
+//    of scores whose large queries meet codes near zero.
 //  * A weight goes into its product as two fp16 terms, after a factor of 2^15: 22
 //    significant bits down to 2^-18, 11 down to 2^-29, where 1 is a weight of the
 //    largest score and the largest scale.  (One term: 1.4 times the error of an output
@@ -110,24 +108,19 @@ __device__ __forceinline__ int team_swizzle(int r, int u) {
 }
 
 // Four codes in a register -> the fp16 pairs (b0, b1), (b2, b3), or with PAIRED
-// (b0, b2), (b1, b3).  An int8 code comes as (code + 128) 2^-24: the byte code ^
-// 0x80 in the low bits of an fp16 below the normal range, which the products take
-// as it is (PAIRED, the values: without the 128); team_unit undoes the 2^-24.
-constexpr uint32_t kTeamBias = 0x00800080u;  // two fp16 values 128 2^-24
+// (b0, b2), (b1, b3).  The byte code ^ 0x80 below 0x64 is fp16's 1024 + 128 + code,
+// off which 1152 is taken, exactly.
 template <int KIND, bool PAIRED>
 __device__ __forceinline__ void team_widen(uint32_t codes, uint32_t &lo, uint32_t &hi) {
     if (KIND == kTeamInt8) {
-        const uint32_t u = codes ^ 0x80808080u;
-        lo = __byte_perm(u, 0, PAIRED ? 0x4240 : 0x4140);
-        hi = __byte_perm(u, 0, PAIRED ? 0x4341 : 0x4342);
-        if (PAIRED) {
-            const uint32_t bias = kTeamBias;
-            const __half2 b = *reinterpret_cast<const __half2 *>(&bias);
-            const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&lo), b);
-            const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&hi), b);
-            lo = *reinterpret_cast<const uint32_t *>(&x);
-            hi = *reinterpret_cast<const uint32_t *>(&y);
-        }
+        const uint32_t u = codes ^ 0x80808080u, bias = 0x64806480u;
+        lo = __byte_perm(u, 0x64646464u, PAIRED ? 0x4240 : 0x4140);
+        hi = __byte_perm(u, 0x64646464u, PAIRED ? 0x4341 : 0x4342);
+        const __half2 b = *reinterpret_cast<const __half2 *>(&bias);
+        const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&lo), b);
+        const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&hi), b);
+        lo = *reinterpret_cast<const uint32_t *>(&x);
+        hi = *reinterpret_cast<const uint32_t *>(&y);
     } else {
         const uint32_t c = PAIRED ? __byte_perm(codes, 0, 0x3120) : codes;
         asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
@@ -136,8 +129,6 @@ __device__ __forceinline__ void team_widen(uint32_t codes, uint32_t &lo, uint32_
             : "r"(c));
     }
 }
-template <int KIND>
-__device__ __forceinline__ constexpr float team_unit() { return KIND == kTeamInt8 ? 16777216.f : 1.f; }
 
 __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -195,8 +186,7 @@ struct TeamState {
 template <int KIND, int D, int NT>
 __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt,
                                           const TeamMeta<TeamConfig<KIND, D, NT>::kGroups> &meta,
-                                          const uint32_t (&q)[NT][D / 16][2], const float (&bias)[NT][2],
-                                          float scale_log2, int group, TeamState<D, NT> &st, int lane) {
+                                          const uint32_t (&q)[NT][D / 16][2], float scale_log2, int group, TeamState<D, NT> &st, int lane) {
     using C = TeamConfig<KIND, D, NT>;
     constexpr int RB = C::kRowBytes;
     const int g = lane >> 2;
@@ -213,7 +203,7 @@ __device__ __forceinline__ void team_step(uint32_t kt, uint32_t vt,
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[r][n][e] = KIND == kTeamInt8 ? -bias[n][e & 1] : 0.f;
+            for (int e = 0; e < 4; ++e) s[r][n][e] = 0.f;
 #pragma unroll
     for (int u = 0; u < C::kUnits; u += 2)
 #pragma unroll
@@ -603,8 +593,6 @@ __global__ void __launch_bounds__(TeamConfig<KIND, D, NT>::kThreads, TeamConfig<
     const int g = lane >> 2, t = lane & 3;
     TeamState<D, NT> st;
     uint32_t q[NT][D / 16][2];
-    float bias[NT][2];
-    const float factor = p.scale_log2 * team_unit<KIND>();
     const int red_heads = min(8, p.group), hold = 8 / red_heads;
     auto load_q = [&](int seg) {
         const __half *rows_q = p.query + (int64_t)seg * p.group * D;
@@ -644,15 +632,12 @@ __global__ void __launch_bounds__(TeamConfig<KIND, D, NT>::kThreads, TeamConfig<
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) {
             if (((w - piece.y) & (C::kWarps - 1)) >= piece.z) continue;
-            const float f = team_exp2(x[w].x - ref), fo = f * x[w].z;
+            const float f = team_exp2(x[w].x - ref), fo = f * x[w].z * (1.f / (1 << kTeamPlace));
             const float2 y = *reinterpret_cast<const float2 *>(red + (w * 8 + row) * C::kPitch + d);
             l = fmaf(x[w].y, f, l);
             o.x = fmaf(y.x, fo, o.x);
             o.y = fmaf(y.y, fo, o.y);
         }
-        constexpr float unit = team_unit<KIND>() / (1 << kTeamPlace);
-        o.x *= unit;
-        o.y *= unit;
         if (piece.w == 2) {
             const float inv = l == 0.f ? 0.f : 1.f / l;  // no row: zeros
             *reinterpret_cast<__half2 *>(p.out + ((int64_t)piece.x * p.group + head) * D + d) =
@@ -677,22 +662,12 @@ __global__ void __launch_bounds__(TeamConfig<KIND, D, NT>::kThreads, TeamConfig<
             if (!whole) (lo > 0 ? cut.x : cut.y) = seg;
             if (tid == 0) held[j] = make_int4(seg, rot, live_warps, whole ? 2 : lo > 0 ? 0 : 1);
             if (mine < live_warps) {
-                if (KIND == kTeamInt8) {  // what the biases add to each head's scores
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i)
-                            mma_16816(x, kTeamBias, kTeamBias, kTeamBias, kTeamBias, q[n][i][0], q[n][i][1]);
-                        bias[n][0] = x[0], bias[n][1] = x[1];
-                    }
-                }
                 st.clear();
                 for (int c = lo + mine; c < end; c += C::kWarps) {
                     cp_async_wait<C::kStages - 1>();
                     __syncwarp();
                     const uint32_t kt = ring + stage * 2 * C::kTileBytes;
-                    team_step<KIND, D, NT>(kt, kt + C::kTileBytes, meta[stage], q, bias, factor, p.group, st, lane);
+                    team_step<KIND, D, NT>(kt, kt + C::kTileBytes, meta[stage], q, p.scale_log2, p.group, st, lane);
                     __syncwarp();
                     issue(stage);
                     if (++stage == C::kStages) stage = 0;
