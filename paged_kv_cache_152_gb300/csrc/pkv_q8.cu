@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kWriteThreads<TILE>) write_q8_kernel(const __g
     touched_ask(p.t);
     grid_dependency_wait();
     launch_dependents();
+    touched_check(p.t);
     const int in = threadIdx.x % TILE;
     const int64_t tile = (int64_t)blockIdx.x * kTiles + threadIdx.x / TILE;
     // tiles of one block side by side: its heads' keys, then its heads' values
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(kBoundsThreads) key_bounds_kernel(const __grid
     touched_ask(p.t);
     grid_dependency_wait();
     launch_dependents();
+    touched_check(p.t);
     const int lane = threadIdx.x % 32, row = lane / kPerRow, col = lane % kPerRow;
     const int64_t tile = (int64_t)blockIdx.x * (kBoundsThreads / 32) + threadIdx.x / 32;
     if (tile >= p.tiles) return;

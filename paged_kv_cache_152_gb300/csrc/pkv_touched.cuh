@@ -51,12 +51,20 @@ __device__ __forceinline__ void touched_ask(const TouchedParams &p) {
     ask(p.block_tables, (int64_t)p.num_seqs * p.max_blocks_per_seq * 4);
 }
 
+// Reports query_starts that decrease or leave the rows, of each sequence by a thread of its own: where they do, the
+// numbers may lead past a sequence.  For grids of at least num_seqs threads.
+__device__ __forceinline__ void touched_check(const TouchedParams &p) {
+    const int64_t s = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (!p.query_starts || s >= p.num_seqs) return;
+    const int start = __ldg(p.query_starts + s), end = __ldg(p.query_starts + s + 1);
+    if (start < 0 || end < start || end > p.num_tokens) report(p.status, PKV_ERR_OUT_OF_RANGE);
+}
+
 // Block number u.  `first`: one thread per number, which reports what is wrong.
 __device__ __forceinline__ TouchedBlock touched_block(const TouchedParams &p, int64_t u, bool first) {
     TouchedBlock t = {-1, 0, 0, 0};
     int s = (int)u, start = s, n = 1;
     int64_t j = 0;
-    bool bad = false;
     if (p.query_starts) {
         // the last s whose first number is not past u: seven of them looked at at a time
         int lo = 0, hi = p.num_seqs;
@@ -75,14 +83,12 @@ __device__ __forceinline__ TouchedBlock touched_block(const TouchedParams &p, in
         }
         s = lo;
         start = touched_start(p, s);
-        const int end = touched_start(p, s + 1);
-        n = max(end - start, 0);
+        n = max(touched_start(p, s + 1) - start, 0);
         j = u - ((start >> p.block_shift) + 2 * (int64_t)s);
-        bad = j == 0 && (end < start || start != __ldg(p.query_starts + s) || end != __ldg(p.query_starts + s + 1));
     }
     const int64_t reach = (int64_t)p.max_blocks_per_seq << p.block_shift;
     const int len = __ldg(p.context_lens + s);
-    bad |= j == 0 && (len < 0 || len > reach || (p.query_starts && n > max(len, 0)));
+    bool bad = j == 0 && (len < 0 || len > reach || (p.query_starts && n > max(len, 0)));
     const int64_t pos0 = (int64_t)max(len, 0) - n;              // the first new token's position
     const int64_t from = max(pos0, (int64_t)0), end = min((int64_t)max(len, 0), reach);
     const int64_t block = (from >> p.block_shift) + j;

@@ -1,0 +1,49 @@
+"""What the 8-bit cache's and the selected blocks' calls report, and what they
+leave alone."""
+
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_q8 as G
+
+pytestmark = pytest.mark.gpu
+pkv = G.pkv
+
+# of three sequences' rows, 140 in all
+DECREASING = ([0, 100, 10, 140], [0, 30, 29, 140], [90, 140, 0, 140], [0, 140, 140, 2], [140, 80, 20, 0], [0, 139, 0, 0],
+              [140, 140, 0, 0])
+
+
+@pytest.mark.parametrize("starts", DECREASING)
+def test_query_starts_that_decrease(pkv, starts):
+    """Reported by the write and by the bounds, and no block outside the tables is touched."""
+    for kind in G.EIGHT:
+        w = G.Write(28, kind, 2, 64, 16, [150, 145, 141], [50, 50, 40]).gpu()
+        w.t["starts"].copy_(torch.tensor(starts, dtype=torch.int32))
+        w.call(pkv)
+        torch.cuda.synchronize()
+        assert int(w.status.item()) == pkv.PKV_ERR_OUT_OF_RANGE
+        outside = np.setdiff1d(np.arange(w.codes[0].shape[0]), w.tables[w.tables >= 0])
+        assert len(outside)
+        for codes, scale, cache, gpu_scale in zip(w.codes, w.scales, (w.t["kc"], w.t["vc"]), (w.t["ks"], w.t["vs"])):
+            assert np.array_equal(G.from_gpu(cache)[outside], codes[outside])
+            assert np.array_equal(gpu_scale.cpu().numpy()[outside], scale[outside])
+        bounds = torch.full((w.codes[0].shape[0], 2, 2, 64), 7.0, dtype=torch.float16, device="cuda")
+        w.status.zero_()
+        pkv.block_key_bounds(bounds, w.t["kc"], w.t["tables"], w.t["lens"], w.t["starts"], 140, key_scale=w.t["ks"],
+                             status=w.status)
+        torch.cuda.synchronize()
+        assert int(w.status.item()) == pkv.PKV_ERR_OUT_OF_RANGE
+        assert bool((bounds[torch.from_numpy(outside).cuda()] == 7).all())
+
+
+def test_query_starts_in_order_are_not_reported(pkv):
+    """Rows before the first and behind the last, sequences without rows, many sequences."""
+    for n in (1, 3, 700, 4096):
+        rng = np.random.default_rng(n)
+        new = rng.integers(0, 4, n)
+        w = G.Write(29, "int8", 1, 64, 8, [int(x) + int(y) for x, y in zip(new, rng.integers(0, 9, n))],
+                    [int(x) for x in new], before=3, behind=2).gpu()
+        w.call(pkv)
+        w.check()
