@@ -584,9 +584,13 @@ __global__ void __launch_bounds__(TeamConfig<KIND, D, NT>::kThreads, TeamConfig<
     for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
         const int len = __ldg(p.context_lens + s);
         if ((len < 0 || len > reach) && tid == 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
-        if (cum[s + 1] == cum[s])  // no position: zeros
+        if (cum[s + 1] == cum[s]) {  // no position: zeros, and no entry of a list can count
             for (int i = tid; i < p.num_heads * D / 8; i += C::kThreads)
                 reinterpret_cast<uint4 *>(p.out + (int64_t)s * p.num_heads * D)[i] = make_uint4(0, 0, 0, 0);
+            if (p.selected)
+                for (int i = tid; i < heads; i += C::kThreads)
+                    if (__ldg(p.num_selected + (int64_t)s * heads + i) != 0) report(p.status, PKV_ERR_OUT_OF_RANGE);
+        }
     }
 
     // ---- pieces, some in hold: their outputs stay apart until a barrier for all ----

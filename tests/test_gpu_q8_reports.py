@@ -47,3 +47,23 @@ def test_query_starts_in_order_are_not_reported(pkv):
                     [int(x) for x in new], before=3, behind=2).gpu()
         w.call(pkv)
         w.check()
+
+
+@pytest.mark.parametrize("kind", G.ALL)
+@pytest.mark.parametrize("count", [1, -1, 9])
+@pytest.mark.parametrize("where", [(1, 0), (1, 2), (3, 1)])
+def test_lists_of_empty_contexts(pkv, kind, count, where):
+    """Entries that count where the context has no block are one too many; the
+    output is zeros."""
+    c = G.Case(9, kind, 6, 3, 64, 16, [100, 0, 50, 0]).pick(3).gpu()
+    c.check(c.call(pkv))
+    c.t["number"][where] = count
+    c.check(c.call(pkv), status=pkv.PKV_ERR_OUT_OF_RANGE)
+    assert bool((c.out[1] == 0).all()) and bool((c.out[3] == 0).all())
+    c.status.zero_()
+    c.t["number"][where] = 0
+    c.t["lens"][0] = -3
+    c.lens = np.array([0, 0, 50, 0], np.int32)
+    c.t["number"][0] = 0
+    c.lists[0] = [[], [], []]
+    c.check(c.call(pkv), status=pkv.PKV_ERR_OUT_OF_RANGE)
