@@ -630,8 +630,8 @@ __device__ __forceinline__ void keep_blocks(const SelectParams &p, KeepScratch &
 
 // A sequence of at most max_selected blocks keeps all of them.
 __device__ __forceinline__ void keep_all(const SelectParams &p, int64_t seg, int count) {
-    for (int i = threadIdx.x; i < p.max_selected; i += kKeepThreads)
-        p.selected[seg * p.max_selected + i] = i < count ? i : -1;
+    for (uint32_t i = threadIdx.x; i < (uint32_t)p.max_selected; i += kKeepThreads)  // (up to 2^31 - 1)
+        p.selected[seg * p.max_selected + i] = i < (uint32_t)count ? (int)i : -1;
     if (threadIdx.x == 0) p.num_selected[seg] = count;
 }
 

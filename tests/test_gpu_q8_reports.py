@@ -67,3 +67,20 @@ def test_lists_of_empty_contexts(pkv, kind, count, where):
     c.t["number"][0] = 0
     c.lists[0] = [[], [], []]
     c.check(c.call(pkv), status=pkv.PKV_ERR_OUT_OF_RANGE)
+
+
+def test_the_longest_list(pkv):
+    """max_selected 2^31 - 1, where an index that goes on by a CTA's threads passes 31 bits."""
+    keep = (1 << 31) - 1
+    c = G.Case(19, "fp16", 4, 1, 64, 16, [100]).pick(7).gpu()
+    selected = torch.full((1, 1, keep), 5, dtype=torch.int32, device="cuda")
+    number = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    bounds = torch.zeros(c.pools[0].shape[0], 1, 2, 64, dtype=torch.float16, device="cuda")
+    pkv.select_blocks(selected, number, c.t["q"], bounds, c.t["tables"], c.t["lens"], 16, status=c.status)
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0 and int(number.item()) == 7
+    assert selected[0, 0, :7].tolist() == list(range(7))
+    assert int(selected[0, 0, 7:].amax().item()) == -1 and int(selected[0, 0, 7:].amin().item()) == -1
+    c.t["selected"], c.t["number"] = selected, number
+    c.lists = [[list(range(7))]]
+    c.check(c.call(pkv))
