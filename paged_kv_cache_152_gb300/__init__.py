@@ -918,6 +918,14 @@ def _cache_type(t, name, f16=False):
                     f"got {t.dtype}")
 
 
+def _int32(x, name):
+    """x for a C int, which would take the low 32 bits of any number."""
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{name}: {x} does not fit 32 bits")
+    return x
+
+
 def _scale_spec(t, f32, name):
     """_checked's spec of an 8-bit cache's scales, which leaves the layout to
     _scale_stride."""
@@ -1016,17 +1024,18 @@ def paged_attention_decode_q8(out, query, key_cache, value_cache, key_scale, val
         raise ValueError("inconsistent shapes")
     keep = 0
     if selected is not None:
-        keep = selected.shape[2]
+        keep = _int32(selected.shape[2], "selected")
         if selected.shape != (n, hkv, keep) or num_selected.shape != (n, hkv):
             raise ValueError("inconsistent shapes")
     if n == 0:
         return out
+    num_ctas = _int32(num_ctas, "num_ctas")
     size = _team_workspace(h, hkv, d, num_ctas, index) if workspace is None else 0
     _launch_scratch(load().pkv_paged_attention_decode_q8, "pkv_paged_attention_decode_q8", index, stream,
                     (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), key_scale.data_ptr(),
                      value_scale.data_ptr(), scale_stride, block_tables.data_ptr(), block_tables.shape[1],
                      context_lens.data_ptr(), _address(selected), _address(num_selected), keep, n, h, hkv, d, bs, nb,
-                     kind, float(scale), int(num_ctas)), workspace, size, status)
+                     kind, float(scale), num_ctas), workspace, size, status)
     return out
 
 
@@ -1048,17 +1057,18 @@ def paged_attention_decode_selected(out, query, key_cache, value_cache, block_ta
                       (num_selected, i32, "num_selected", 2)))
     n, h, d = rows = query.shape
     nb, hkv, bs, d2 = pool = key_cache.shape
-    keep = selected.shape[2]
+    keep = _int32(selected.shape[2], "selected")
     if out.shape != rows or d2 != d or value_cache.shape != pool or block_tables.shape[0] != n \
             or context_lens.shape != (n,) or selected.shape != (n, hkv, keep) or num_selected.shape != (n, hkv):
         raise ValueError("inconsistent shapes")
     if n == 0:
         return out
+    num_ctas = _int32(num_ctas, "num_ctas")
     size = _team_workspace(h, hkv, d, num_ctas, index) if workspace is None else 0
     _launch_scratch(load().pkv_paged_attention_decode_selected, "pkv_paged_attention_decode_selected", index, stream,
                     (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
                      block_tables.shape[1], context_lens.data_ptr(), selected.data_ptr(), num_selected.data_ptr(), keep, n, h,
-                     hkv, d, bs, nb, float(scale), int(num_ctas)), workspace, size, status)
+                     hkv, d, bs, nb, float(scale), num_ctas), workspace, size, status)
     return out
 
 
@@ -1095,8 +1105,9 @@ def block_key_bounds(key_bounds, key_cache, block_tables, context_lens, query_st
     scale_stride = 0 if key_scale is None else _scale_stride(nb, hkv, key_scale=key_scale)
     _launch(load().pkv_block_key_bounds, "pkv_block_key_bounds", index, stream,
             (key_bounds.data_ptr(), key_cache.data_ptr(), _address(key_scale), scale_stride, block_tables.data_ptr(),
-             mb, context_lens.data_ptr(), _address(query_starts), n if num_tokens is None else int(num_tokens), n, hkv, d,
-             bs, nb, kind, _status_address(status, index)))
+             mb, context_lens.data_ptr(), _address(query_starts),
+             n if num_tokens is None else _int32(num_tokens, "num_tokens"), n, hkv, d, bs, nb, kind,
+             _status_address(status, index)))
     return key_bounds
 
 
@@ -1127,8 +1138,9 @@ def select_blocks(selected, num_selected, query, key_bounds, block_tables, conte
     size = _select_workspace(n, hkv, mb) if workspace is None else 0
     _launch_scratch(load().pkv_select_blocks, "pkv_select_blocks", index, stream,
                     (selected.data_ptr(), num_selected.data_ptr(), query.data_ptr(), key_bounds.data_ptr(),
-                     block_tables.data_ptr(), mb, context_lens.data_ptr(), n, h, hkv, d, int(block_size), nb,
-                     selected.shape[2], int(first_blocks), int(last_blocks)), workspace, size, status)
+                     block_tables.data_ptr(), mb, context_lens.data_ptr(), n, h, hkv, d, _int32(block_size, "block_size"),
+                     nb, _int32(selected.shape[2], "selected"), _int32(first_blocks, "first_blocks"),
+                     _int32(last_blocks, "last_blocks")), workspace, size, status)
     return selected, num_selected
 
 

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import test_gpu_q8 as G
+import test_gpu_select as S
 
 pytestmark = pytest.mark.gpu
 pkv = G.pkv
@@ -84,3 +85,29 @@ def test_the_longest_list(pkv):
     c.t["selected"], c.t["number"] = selected, number
     c.lists = [[list(range(7))]]
     c.check(c.call(pkv))
+
+
+def test_numbers_past_32_bits_are_refused(pkv):
+    """An argument that does not fit the library's 32 bits is not taken for the
+    part of it that does."""
+    far = 1 << 32
+    q, bounds, tables, lens = S.make(1, 2, 1, 64, 16, [16 * 30, 16 * 20])
+    t = [torch.from_numpy(x).cuda() for x in (q, bounds, tables, lens)]
+    selected = torch.full((2, 1, 6), -9, dtype=torch.int32, device="cuda")
+    number = torch.full((2, 1), -9, dtype=torch.int32, device="cuda")
+    for bad in (dict(first_blocks=far + 1), dict(last_blocks=far), dict(first_blocks=-far), dict(block_size=far + 16)):
+        kw = dict(block_size=16, first_blocks=1, last_blocks=2)
+        kw.update(bad)
+        with pytest.raises((ValueError, OverflowError, pkv.PkvError)):
+            pkv.select_blocks(selected, number, *t, **kw)
+    torch.cuda.synchronize()
+    assert bool((selected == -9).all())
+    w = G.Write(26, "int8", 2, 64, 16, [40, 20], [30, 20]).gpu()
+    out = torch.full((w.codes[0].shape[0], 2, 2, 64), 7.0, dtype=torch.float16, device="cuda")
+    with pytest.raises((ValueError, OverflowError, pkv.PkvError)):
+        pkv.block_key_bounds(out, w.t["kc"], w.t["tables"], w.t["lens"], w.t["starts"], far + 5, key_scale=w.t["ks"])
+    torch.cuda.synchronize()
+    assert bool((out == 7).all())
+    c = G.Case(9, "fp16", 4, 2, 64, 16, [100, 50]).pick(3).gpu()
+    with pytest.raises((ValueError, OverflowError, pkv.PkvError)):
+        c.call(pkv, num_ctas=far + 3)
