@@ -702,6 +702,10 @@ int pkv_validate_block_pairs(const int64_t *host_pairs, int num_pairs,
 /* ------------------------------------------------------------------------ */
 
 /*
+ * Writes of any number of tokens and decode of single ones.  Attention of several
+ * new tokens (a prompt, a chunk of one, drafts) and decode plans take fp16 caches
+ * only.
+ *
  * Element type of a cache.  An 8-bit cache has the layout of the fp16 one with
  * one byte per element, and for each of key_cache and value_cache an fp32 scale
  * per (block, KV head): num_blocks rows of num_kv_heads, scale_stride floats
@@ -791,6 +795,8 @@ int pkv_reshape_and_cache_q8(const void *key, int64_t key_stride,
  *                 the sequence, in any order.  A block listed twice counts twice.
  *   num_selected  int32 [num_seqs][num_kv_heads]: entries that count, at most
  *                 max_selected and the context's blocks.  No entry: zeros.
+ *                 (The work is shared out as if max_selected of them did, or all
+ *                 the context's blocks: entries that do not cost steps of zeros.)
  * selected and num_selected go together (both NULL: every block).
  *
  *   key_scale, value_scale, scale_stride  as for pkv_reshape_and_cache_q8; any
@@ -857,7 +863,11 @@ int pkv_paged_attention_decode_selected(void *out, const void *query,
  * holds new tokens, over the block's positions below the context length (all of
  * them are read from the cache again, so nothing depends on what the bounds held
  * before).  To be called after the write of the new tokens, with the same
- * tables, lengths and query_starts.  A channel with a NaN has NaN for both.
+ * tables, lengths and query_starts.  Blocks that are swapped in again need theirs
+ * at the new places: swapped along (pkv_swap_blocks, two layers' bounds as the two
+ * pools, block_bytes = 4 * num_kv_heads * head_dim), or made anew with query_starts
+ * over whole contexts.  A copy on write needs nothing, since the write that it is
+ * for is followed by this call.  A channel with a NaN has NaN for both.
  *
  *   key_bounds  fp16 [num_blocks][num_kv_heads][2][head_dim] (device, written):
  *               the largest, then the smallest; of an 8-bit cache the codes'
@@ -884,11 +894,13 @@ int pkv_block_key_bounds(void *key_bounds, const void *key_cache, const float *k
  *
  *     sum_i max(q[s][h][i], 0) * hi[b][i] + min(q[s][h][i], 0) * lo[b][i]
  *
- * with hi and lo the block's key bounds: no key of the block has a larger
- * product with the query.  Of the context's B = ceil(L / block_size) blocks,
- * min(B, max_selected) are kept: the first first_blocks and the last
- * last_blocks, and of the others those with the largest scores, of equal ones
- * the lowest index.  A score that is not finite counts as the largest.  Scores
+ * with hi and lo the block's key bounds: no key of an fp16 cache's block has a
+ * larger product with the query (of an 8-bit cache's, whose bounds are rounded to
+ * the nearest fp16, none by more than that rounding of its terms).  Of the
+ * context's B = ceil(L / block_size) blocks, min(B, max_selected) are kept: the
+ * first first_blocks and the last last_blocks, and of the others those with the
+ * largest scores, of equal ones the lowest index.  A score that is not finite
+ * counts as the largest.  Scores
  * that fp32 sums may not tell apart are summed again as whole numbers of 2^-48,
  * which all these scores are: what is kept is what the exact scores say.
  *
@@ -900,8 +912,12 @@ int pkv_block_key_bounds(void *key_bounds, const void *key_cache, const float *k
  *   max_selected >= 1, first_blocks >= 0, last_blocks >= 0 (host values),
  *                 first_blocks + last_blocks <= max_selected
  *   workspace     at least pkv_select_workspace_size(num_seqs, num_kv_heads,
- *                 max_blocks_per_seq) bytes; 256-byte aligned; as for
- *                 pkv_paged_attention_decode_q8
+ *                 max_blocks_per_seq) bytes, 12 per table entry and KV head;
+ *                 256-byte aligned; as for pkv_paged_attention_decode_q8
+ * The kernel goes by the table's width, since contexts are known on the device
+ * only: tables of more than 4096 columns take two kernels with the scores in the
+ * workspace, several times as slow, whatever the contexts are; up to there a table
+ * four times as wide as the contexts costs up to 7 us.
  * Supported: head_dim in {64, 128}; block_size in {8, 16, 32, 64, 128};
  * num_heads / num_kv_heads from 1 to 16; num_kv_heads <= 65535; num_seqs <= 4096;
  * sizes as for pkv_paged_attention_decode_q8.  A context that is negative (taken

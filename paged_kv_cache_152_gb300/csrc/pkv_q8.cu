@@ -18,9 +18,10 @@
 //
 // Measured: four prompts of 1000 to 4001 tokens, 8 heads of 128, 15.7 us, 3780 GB/s,
 // 0.56 of the copy bandwidth (with fp32 divisions for the codes and a search in
-// halves 25.1).  Not HBM but instructions bound it: 66% of the issue slots, of which
-// the conversions from fp16 and to the codes are the slowest.  64 single tokens of
-// 8 heads 4.4 us, three dependent look-ups behind a launch.
+// halves 25.1); in e4m3, with fewer steps to a code, 14.4.  No pipe is full (67% of the
+// issue slots, integer pipe 48%, HBM 29%): a warp goes through search, look-ups, loads,
+// maximum, conversion and stores of one tile, which only other warps overlap.  64 single
+// tokens of 8 heads 4.4 us, three dependent look-ups behind a launch.
 #include <cuda_runtime.h>
 
 #include "../../include/pkv.h"
@@ -253,8 +254,8 @@ struct BoundsParams {
 // rows at a time, eight loads ahead.  Nothing meets in shared memory: what the lanes
 // of one channel have is joined by shuffles.  Bound by HBM for prompts, whose blocks'
 // rows are read once, and its latency: those of two prompts of 8000 and 16384 tokens,
-// 8 heads of 128, fp16, 11.5 us, 4590 GB/s, 0.68 of the copy bandwidth; the last
-// blocks of 64 sequences 3.7 us.
+// 8 heads of 128, fp16, 11.5 us, 4590 GB/s, 0.68 of the copy bandwidth (int8 10.6, e4m3
+// 9.1); the last blocks of 64 sequences 3.8 us (4.8, 4.3).
 // Threads of a CTA, 32, 64, 128 and 256: prompts 11.4, 11.5, 11.9 and 12.1 us, single tokens 3.7, 3.7, 3.9 and 4.1.
 constexpr int kBoundsThreads = 64;
 

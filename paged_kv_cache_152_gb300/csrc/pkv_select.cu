@@ -1,7 +1,7 @@
 // pkv_select.cu -- the blocks of a context whose keys can score highest.
 //
 // With hi, lo a block's largest and smallest key channel by channel, no key k of
-// the block has q . k above
+// the block has q . k above (but for the rounding to fp16 of an 8-bit cache's bounds)
 //
 //     sum_i max(q_i hi_i, q_i lo_i) = sum_i max(q_i, 0) hi_i + min(q_i, 0) lo_i,
 //
@@ -13,8 +13,8 @@
 // once, straight into the fragments: the products' inner index is taken in the
 // order that 16-byte loads bring it) where there is much of them, and by latency
 // where there is little: so one kernel does both parts, a cluster of CTAs per
-// (sequence, KV head), and the scores never leave shared memory.  (Contexts of more
-// than 4096 blocks take two kernels, with the scores in global memory.)
+// (sequence, KV head), and the scores never leave shared memory.  (Tables of more
+// than 4096 columns take two kernels, with the scores in global memory.)
 //
 // The choice: fp32 scores are off by E or less (below), so blocks more than 2 E
 // above the last kept score are kept and those more than 2 E below it are not; the
@@ -30,9 +30,12 @@
 // values 11.9 and 40.4, but the second one is rounded, so that large terms that cancel
 // took the last digits with them and equal scores of other terms differed.  With them
 // in fp64 and at most 128 keys ranked instead of 32 13.2 and 42.2; with as many rounds
-// as the keys have pairs of bits 13.9.  Scoring by persistent warps over all segments and choosing in a
-// second kernel took 48 for the 64; queries in shared memory instead of registers, for
-// six CTAs an SM instead of four, 57.
+// as the keys have pairs of bits 13.9.  With tables of 4096 columns for the same contexts
+// 19.2 and 47.0 us (more scores a thread, larger clusters); of 8192, with the two kernels,
+// 70 and 150; 131072 tokens in blocks of 16 of one sequence 167 us, of eight 506.
+// Scoring by persistent warps over all segments and choosing in a second kernel took 48
+// for the 64; queries in shared memory instead of registers, for six CTAs an SM instead
+// of four, 57.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
@@ -182,7 +185,7 @@ __device__ __forceinline__ int select_phys(const SelectParams &p, int s, int64_t
     return phys;
 }
 
-// Contexts of more blocks than the fused kernel holds: scores to global memory.
+// Tables of more columns than the fused kernel holds blocks: scores to global memory.
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads) select_score_kernel(const __grid_constant__ SelectParams p) {
     grid_dependency_wait();

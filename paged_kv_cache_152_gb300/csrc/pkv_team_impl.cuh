@@ -18,10 +18,10 @@
 //    together, a step of 32 rows (16 of 256 bytes) each in turn, with a ring of
 //    their own (16 KB per warp, 128 KB per SM in flight) that runs on into the next
 //    pieces.  Their outputs meet in shared memory, those of up to eight short
-//    pieces between two barriers (64 sequences over 50 to 900, 32 heads, int8, "chats":
-//    48.3 us, 59.4 with barriers at every piece).  Four warps with steps of 32 rows,
-//    two CTAs per SM, took 48.8 us there, eight warps with steps of 16 rows 53.9; a
-//    grouped batch 176 and 180.
+//    pieces between two barriers (64 sequences over 50 to 900, 32 heads, int8, "chats",
+//    49.8 us now: 48.3 then, 59.4 with barriers at every piece).  Four warps with steps
+//    of 32 rows, two CTAs per SM, took 48.8 us there, eight warps with steps of 16 rows
+//    53.9; a grouped batch 176 and 180 (178 now).
 //  * Copies by cp.async: a lane copies the 16 bytes that its place in the swizzled
 //    tile wants, from the block that its row lies in, and rows past the end come
 //    as zeros; the block table's entries of 32 steps are looked up at once, a batch
@@ -35,7 +35,7 @@
 //    so that widening to fp16 is all that is done to them.  The weights turn
 //    from the scores' layout to the product's by movmatrix.  (One group's heads are
 //    16 rows at most: tcgen05's tiles of 64 or 128 would stay empty.  The tensor pipe
-//    is active 14% of the time, the integer pipe, which widens, most of all.)
+//    is active 22 to 25% of the time, the integer pipe, which widens, 36 to 41%.)
 //  * int8 codes widen to fp16 exactly: a byte with 0x64 above it is 1024 more than
 //    itself, off which one subtraction takes 1152 (the byte is code + 128).  Taking
 //    the 128 off the sums instead, 128 times the queries' sum at the scores' start,
@@ -51,9 +51,10 @@
 //
 // Measured (us, GB/s, of the copy bandwidth): 64 sequences over 50 to 900, 32 heads,
 // int8 49.8, 4890, 0.72; 256 over 256 to 4096, 32 heads and 8 KV heads, e4m3 178,
-// 6520, 0.96; 8 over 8000 to 32768, int8 62.9, 5830, 0.86; 64 blocks of 32 rows of
-// each of these, fp16 19.1, 3490, 0.51 (of a latency of three look-ups in a row);
-// 128 blocks of 16 for 64 sequences, fp16 90, 5960, 0.88.
+// 6520, 0.96; 8 over 8000 to 32768, int8 63.0, 5830, 0.86; 64 blocks of 32 rows of
+// each of these, fp16 19.2, 3480, 0.51 (of a latency of three look-ups in a row), int8
+// 14.8, e4m3 14.0; 128 blocks of 16 for 64 sequences, fp16 89 to 90, 6000, 0.88, int8
+// 53.3, 5060, 0.75, e4m3 52.5, 5140, 0.76.
 #ifndef PKV_TEAM_IMPL_CUH
 #define PKV_TEAM_IMPL_CUH
 
