@@ -21,18 +21,20 @@
 // few between are scored again as whole numbers, without any rounding, and ranked,
 // ties to the lowest index, so that the choice is that of the exact scores.
 //
-// Measured: 8 contexts of 8000 to 32768 tokens, blocks of 32, 8 KV heads 12.1 us (the
+// Measured: 8 contexts of 8000 to 32768 tokens, blocks of 32, 8 KV heads 11.7 us (the
 // 23 MB of bounds need 3.4 of them; all that comes before the choice, three look-ups
 // and two rounds of loads, takes 6.3; the choice is some ten steps of a CTA, each a
-// few hundred cycles of latency); 64 contexts of 4000 to 16384, blocks of 16, 40.6 us,
-// 4060 GB/s, 0.60 of the copy bandwidth (all CTAs run at once, so the longest contexts'
+// few hundred cycles of latency); 64 contexts of 4000 to 16384, blocks of 16, 40.2 us,
+// 4100 GB/s, 0.60 of the copy bandwidth (all CTAs run at once, so the longest contexts'
 // end the call; without the choice 34.2).  With the border's scores as pairs of fp32
 // values 11.9 and 40.4, but the second one is rounded, so that large terms that cancel
-// took the last digits with them and equal scores of other terms differed.  With them
-// in fp64 and at most 128 keys ranked instead of 32 13.2 and 42.2; with as many rounds
-// as the keys have pairs of bits 13.9.  With tables of 4096 columns for the same contexts
-// 19.2 and 47.0 us (more scores a thread, larger clusters); of 8192, with the two kernels,
-// 70 and 150; 131072 tokens in blocks of 16 of one sequence 167 us, of eight 506.
+// took the last digits with them and equal scores of other terms differed; as 96-bit
+// integers from shifts 12.1 and 40.7; in fp64 and at most 128 keys ranked instead of 32
+// 13.2 and 42.2; with as many rounds as the keys have pairs of bits 13.9.  Where one
+// channel is 30000 in every block, E is so wide that all are scored again: 317 and 375 us
+// (pairs of fp32 values 400 and 493, integers from shifts 575 and 665).  With tables of 4096 columns for the same contexts
+// 18.7 and 46.3 us (more scores a thread, larger clusters); of 8192, with the two kernels,
+// 36 and 106; 131072 tokens in blocks of 16 of one sequence 82 us, of eight 191.
 // Scoring by persistent warps over all segments and choosing in a second kernel took 48
 // for the 64; queries in shared memory instead of registers, for six CTAs an SM instead
 // of four, 57.
@@ -251,9 +253,9 @@ __device__ __forceinline__ int4 cta_sums(int4 v, KeepScratch &sh, int &turn) {
     return sum;
 }
 
-// A score, exactly: an fp16 value is m 2^(e - 24) with m below 2^11 and 0 <= e <= 29, so a product of two is m 2^(e - 48)
-// with m below 2^22 and e up to 58, and a sum of 128 of them is a whole number of 2^-48 below 2^87 in size:
-// (hi 2^32 + lo) 2^-48.  No order of the sum and no rounding enters, so equal scores are equal here.
+// A score, exactly: a product of two fp16 values is a whole number of 2^-48 of 22 bits, and below 2^32 in size, so a sum
+// of 128 of them is a whole number of 2^-48 below 2^87: (hi 2^32 + lo) 2^-48.  No order of the sum and no rounding enters,
+// so equal scores are equal here.
 struct ExactScore {
     int64_t hi;
     uint32_t lo;
@@ -263,56 +265,72 @@ __device__ __forceinline__ bool exact_above(int64_t hi, uint32_t lo, int64_t hi2
     return hi > hi2 || (hi == hi2 && lo > lo2);
 }
 
-// An fp16 value's m, with its sign, and e.
-__device__ __forceinline__ int2 half_parts(unsigned short h) {
-    const int e = h >> 10 & 31, m = (h & 0x3ff) | (e ? 0x400 : 0);
-    return make_int2(h >> 15 ? -m : m, e ? e - 1 : 0);
+// An exact product in four parts, whole numbers of 2^10, 2^-13, 2^-36 and 2^-48 up to 2^22 in size, added to a sum: the
+// product plus 1.5 2^23 of such a unit is rounded to a whole number of it, which the bits show; what is left of the
+// product, at most half a unit, is exact too.
+constexpr int kParts = 4;
+__device__ __forceinline__ float part_place(int i) {  // 1.5 2^23 units
+    return i == 0 ? 0x1.8p33f : i == 1 ? 0x1.8p10f : i == 2 ? 0x1.8p-13f : 0x1.8p-25f;
 }
+__device__ __forceinline__ void add_parts(uint32_t (&sum)[kParts], float x) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        const float y = __fadd_rn(x, part_place(i));
+        sum[i] += __float_as_uint(y);
+        if (i + 1 < kParts) x = __fsub_rn(x, __fsub_rn(y, part_place(i)));
+    }
+}
+
+// The physical block of a block that has been scored (a bad entry has been reported).
+__device__ __forceinline__ int border_phys(const SelectParams &p, int s, int64_t block) {
+    const int phys = __ldg(p.block_tables + (int64_t)s * p.max_blocks_per_seq + block);
+    return phys < 0 || phys >= p.num_blocks ? 0 : phys;
+}
+
+// A lane's channels of a block's bounds, lane + 32 k: loaded a block ahead of their use.
+template <int D>
+struct BorderBounds {
+    unsigned short hi[D / 32], lo[D / 32];
+    __device__ __forceinline__ void load(const SelectParams &p, int kvh, int phys, int lane) {
+        const unsigned short *at = reinterpret_cast<const unsigned short *>(p.bounds) +
+                                   ((int64_t)phys * p.num_kv_heads + kvh) * 2 * D + lane;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) hi[k] = __ldg(at + k * 32), lo[k] = __ldg(at + D + k * 32);
+    }
+};
 
 // The block's score, by a warp; the same on all lanes.
 template <int D>
-__device__ ExactScore exact_score(const SelectParams &p, int s, int kvh, int64_t block, int lane) {
-    int phys = __ldg(p.block_tables + (int64_t)s * p.max_blocks_per_seq + block);
-    if (phys < 0 || phys >= p.num_blocks) phys = 0;
-    const unsigned short *hi = reinterpret_cast<const unsigned short *>(p.bounds) +
-                               ((int64_t)phys * p.num_kv_heads + kvh) * 2 * D;
-    unsigned short bounds[2][D / 32];
+__device__ __forceinline__ ExactScore exact_score(const SelectParams &p, int s, int kvh, const BorderBounds<D> &bounds,
+                                                  int lane) {
+    bool finite = true;
+    float up[D / 32], down[D / 32];
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) {
-        bounds[0][k] = hi[k * 32 + lane];
-        bounds[1][k] = hi[D + k * 32 + lane];
+        finite &= (bounds.hi[k] & 0x7c00) != 0x7c00 && (bounds.lo[k] & 0x7c00) != 0x7c00;
+        up[k] = __half2float(__ushort_as_half(bounds.hi[k]));
+        down[k] = __half2float(__ushort_as_half(bounds.lo[k]));
     }
-    bool finite = true;
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) finite &= (bounds[0][k] & 0x7c00) != 0x7c00 && (bounds[1][k] & 0x7c00) != 0x7c00;
-    finite = __all_sync(kFullMask, finite);
     ExactScore best = {-kNoNumberHi, 0};
 #pragma unroll 4
     for (int h = 0; h < p.group; ++h) {
-        const unsigned short *q = reinterpret_cast<const unsigned short *>(p.query) +
-                                  ((int64_t)s * p.num_heads + (int64_t)kvh * p.group + h) * D;
-        int64_t low = 0, high = 0;  // low + high 2^32, each term below 2^53
+        const __half *row = p.query + ((int64_t)s * p.num_heads + (int64_t)kvh * p.group + h) * D;
+        uint32_t sum[kParts] = {};
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
-            const unsigned short v = q[k * 32 + lane];
-            finite &= (v & 0x7c00) != 0x7c00;
-            const int2 a = half_parts(v), b = half_parts(v >> 15 ? bounds[1][k] : bounds[0][k]);
-            const int64_t x = (int64_t)(a.x * b.x) << (a.y + b.y & 31);
-            low += a.y + b.y < 32 ? x : 0;
-            high += a.y + b.y < 32 ? 0 : x;
+            const float q = __half2float(row[k * 32 + lane]), x = q * (q < 0.f ? down[k] : up[k]);
+            finite &= fabsf(x) < CUDART_INF_F;
+            add_parts(sum, x);
         }
-        // this lane's sum, below 2^82 in size, in pieces of 26 bits that sum up over a warp in 32
-        high += low >> 32;
-        const uint32_t word = (uint32_t)low;
-        const int64_t rest = (int64_t)((uint64_t)high << 6 | word >> 26);
-        constexpr uint32_t kPiece = (1u << 26) - 1;
-        const uint32_t p0 = __reduce_add_sync(kFullMask, word & kPiece);
-        const uint32_t p1 = __reduce_add_sync(kFullMask, (uint32_t)rest & kPiece);
-        const uint32_t p2 = __reduce_add_sync(kFullMask, (uint32_t)(rest >> 26) & kPiece);
-        const int p3 = __reduce_add_sync(kFullMask, (int)(rest >> 52));
-        const uint64_t sum = p0 + ((uint64_t)p1 << 26);
-        ExactScore score = {(int64_t)(sum >> 32) + ((int64_t)p2 << 20) + (int64_t)p3 * (INT64_C(1) << 46), (uint32_t)sum};
-        if (exact_above(score.hi, score.lo, best.hi, best.lo)) best = score;
+        int part[kParts];
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+            part[i] = (int)__reduce_add_sync(kFullMask, sum[i] - D / 32 * __float_as_uint(part_place(i)));
+        // hi 2^32 + lo of the parts times 2^58, 2^35, 2^12 and 1
+        const int64_t low = ((int64_t)part[2] << 12) + part[3];
+        const int64_t hi = ((int64_t)part[0] << 26) + ((int64_t)part[1] << 3) + (low >> 32);
+        const uint32_t lo = (uint32_t)low;
+        if (exact_above(hi, lo, best.hi, best.lo)) best.hi = hi, best.lo = lo;
     }
     // an infinite or missing bound or query times any other makes a sum that is not finite
     if (!__all_sync(kFullMask, finite)) best.hi = kNoNumberHi, best.lo = 0;
@@ -371,6 +389,7 @@ __device__ float keep_slowly(const SelectParams &p, KeepScratch &sh, int &turn, 
     // The border's exact scores; what is surely kept or not is marked.
     int64_t *hi = p.score_hi + seg * p.row;
     constexpr int64_t kMarked = INT64_MIN;
+    int64_t highest = kMarked, lowest = INT64_MAX;
     for (int base = warp * 32; base < m; base += kKeepThreads) {
         const int i = base + lane;
         const float v = i < m ? score[i] : 0.f;
@@ -379,30 +398,51 @@ __device__ float keep_slowly(const SelectParams &p, KeepScratch &sh, int &turn, 
             hi[i] = kMarked;
             score[i] = v > last ? CUDART_INF_F : -CUDART_INF_F;
         }
-        for (unsigned mask = __ballot_sync(kFullMask, mine); mask; mask &= mask - 1) {
+        const int phys = mine ? border_phys(p, s, m0 + i) : 0;
+        unsigned mask = __ballot_sync(kFullMask, mine);
+        BorderBounds<D> next;
+        if (mask) next.load(p, kvh, __shfl_sync(kFullMask, phys, __ffs(mask) - 1), lane);
+        while (mask) {
             const int b = __ffs(mask) - 1;
-            const ExactScore e = exact_score<D>(p, s, kvh, m0 + base + b, lane);
+            const BorderBounds<D> now = next;
+            mask &= mask - 1;
+            if (mask) next.load(p, kvh, __shfl_sync(kFullMask, phys, __ffs(mask) - 1), lane);
+            const ExactScore e = exact_score<D>(p, s, kvh, now, lane);
+            highest = max(highest, e.hi);
+            lowest = min(lowest, e.hi);
             if (lane == b) {
                 hi[i] = e.hi;
                 score[i] = __uint_as_float(e.lo);
             }
         }
     }
+    if (lane == 0) sh.list_hi[warp] = highest, sh.list_hi[kKeepWarps + warp] = lowest;
     __syncthreads();
-    // the want-th largest: hi's bits from an unsigned order, then lo's among its equals
-    auto key_hi = [&](int i) { return (uint64_t)hi[i] ^ (uint64_t)1 << 63; };  // (marked: 0, below every score)
-    uint64_t key = 0;
-    for (int bit = 63; bit >= 0; --bit) {
+#pragma unroll
+    for (int w = 0; w < kKeepWarps; ++w) {
+        highest = max(highest, sh.list_hi[w]);
+        lowest = min(lowest, sh.list_hi[kKeepWarps + w]);
+    }
+    // the want-th largest: hi's bits in an unsigned order, past those that are all alike, then lo's among its equals
+    constexpr uint64_t kSign = (uint64_t)1 << 63;
+    auto key_hi = [&](int i) { return (uint64_t)hi[i] ^ kSign; };  // (marked: 0, below every score)
+    const int alike = __clzll(highest ^ lowest);
+    uint64_t key = ((uint64_t)highest ^ kSign) & ~(alike < 64 ? ~(uint64_t)0 >> alike : 0);
+    for (int bit = 63 - alike; bit >= 0; --bit) {
         const uint64_t trial = key | 1ull << bit;
         int n = 0;
         for (int i = tid; i < m; i += kKeepThreads) n += key_hi(i) >= trial;
         if (cta_sums(make_int4(n, 0, 0, 0), sh, turn).x >= want) key = trial;
     }
-    int past = 0;
-    for (int i = tid; i < m; i += kKeepThreads) past += key_hi(i) > key;
-    past = cta_sums(make_int4(past, 0, 0, 0), sh, turn).x;
-    uint32_t word = 0;
-    for (int bit = 31; bit >= 0; --bit) {
+    int past = 0, equal = 0;
+    for (int i = tid; i < m; i += kKeepThreads) {
+        past += key_hi(i) > key;
+        equal += key_hi(i) == key;
+    }
+    const int4 about = cta_sums(make_int4(past, equal, 0, 0), sh, turn);
+    past = about.x;
+    uint32_t word = 0;  // (all its equals are kept: any lo)
+    for (int bit = past + about.y == want ? -1 : 31; bit >= 0; --bit) {
         const uint32_t trial = word | 1u << bit;
         int n = 0;
         for (int i = tid; i < m; i += kKeepThreads) n += key_hi(i) == key && __float_as_uint(score[i]) >= trial;
@@ -556,8 +596,15 @@ __device__ __forceinline__ void keep_blocks(const SelectParams &p, KeepScratch &
             for (int j = 0; j < VALUES; ++j)
                 if (close >> j & 1) sh.list[k++] = j * kKeepThreads + tid;
             __syncthreads();
-            for (int i = warp; i < n.y; i += kKeepWarps) {
-                const ExactScore e = exact_score<D>(p, s, kvh, m0 + sh.list[i], lane);
+            // a lane looks up one of the warp's (at most 32)
+            const int ours = warp + lane * kKeepWarps;
+            const int phys = ours < n.y ? border_phys(p, s, m0 + sh.list[ours]) : 0;
+            BorderBounds<D> next;
+            if (warp < n.y) next.load(p, kvh, __shfl_sync(kFullMask, phys, 0), lane);
+            for (int i = warp, j = 1; i < n.y; i += kKeepWarps, ++j) {
+                const BorderBounds<D> now = next;
+                if (i + kKeepWarps < n.y) next.load(p, kvh, __shfl_sync(kFullMask, phys, j), lane);
+                const ExactScore e = exact_score<D>(p, s, kvh, now, lane);
                 if (lane == 0) sh.list_hi[i] = e.hi, sh.list_lo[i] = e.lo;
             }
             __syncthreads();

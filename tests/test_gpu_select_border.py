@@ -101,3 +101,27 @@ def test_the_smallest_and_the_largest_terms(pkv, blocks):
     steps = rng.integers(-3, 4, (len(bounds), 1, 1, 32))
     bounds[:, :, :, 32:] = steps * 2.0 ** -24
     check(pkv, q, bounds, tables, lens, 8, blocks // 2)
+
+
+@pytest.mark.parametrize("columns", [0, 5000])
+@pytest.mark.parametrize("blocks", [100, 900])
+@pytest.mark.parametrize("h,d", [(1, 64), (4, 128)])
+def test_fp16_values_of_every_size(pkv, h, d, blocks, columns):
+    """Queries and bounds of random bits, and the same with the large ones in pairs
+    that cancel."""
+    q, bounds, tables, lens = S.make(6, h, 1, d, 8, [8 * blocks])
+    rng = np.random.default_rng(blocks + d)
+
+    def bits(shape):
+        sign, size = rng.integers(0, 2, shape) << 15, rng.integers(0, 0x7c00, shape)
+        return (sign | size).astype(np.uint16).view(np.float16)
+
+    q, bounds = bits(q.shape), bits(bounds.shape)
+    bounds = np.stack([np.maximum(bounds[:, :, 0], bounds[:, :, 1]), np.minimum(bounds[:, :, 0], bounds[:, :, 1])], axis=2)
+    check(pkv, q, bounds, wider(tables, columns), lens, 8, blocks // 2)
+    bounds[...] = bounds[:, :, :1]  # hi = lo
+    q[:, :, 1::2] = q[:, :, ::2]
+    small = (np.abs(bounds[..., 1::2].astype(np.float64)) < 2.0 ** -8)
+    bounds[..., 1::2] = np.where(small, bounds[..., 1::2], -bounds[..., ::2])
+    bounds[..., ::2] = np.where(small, np.float16(2.0 ** -24), bounds[..., ::2])
+    check(pkv, q, bounds, wider(tables, columns), lens, 8, blocks // 2)
